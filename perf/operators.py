@@ -243,7 +243,7 @@ def _make_call(s):
                         kv_layout=s.kv_layout)
     if s.op == "append":
         return fia.KvAppendCall(cache, s.k_new, s.v_new, s.seqused_kv, cu_seqlens_q=s.cu_seqlens_q,
-                                max_seqlen_q=s.S_q, weights=s.weights, positions=s.positions,
+                                weights=s.weights, positions=s.positions,
                                 tokens_seen=s.tokens_seen)
     return fia.KvEvictCall(cache, s.seqused_kv, s.weights, budget=s.budget, first_tokens=s.first,
                            recent_tokens=s.recent, positions=s.positions,
