@@ -58,7 +58,7 @@ class FiaParams(ctypes.Structure):
         ("sinks", _P),
         ("num_sms", _I), ("kv_layout", _I),
         ("atten_mask", _P), ("mask_batch_stride", _L), ("mask_row_stride", _L),
-        ("reserved", _I * 8),
+        ("first_tokens", _I), ("reserved", _I * 7),
     ]
 
 
@@ -87,6 +87,45 @@ class CombineParams(ctypes.Structure):
     ]
 
 
+class KvCacheParams(ctypes.Structure):
+    _fields_ = [
+        ("batch", _I), ("num_kv_heads", _I), ("head_dim", _I), ("kv_dtype", _I),
+        ("quant_tile", _I), ("kv_layout", _I),
+        ("k_cache", _P), ("v_cache", _P), ("k_scale", _P), ("v_scale", _P),
+        ("block_table", _P),
+        ("max_blocks_per_seq", _I), ("block_size", _I), ("num_blocks", _I),
+        ("max_seqlen_kv", _I),
+    ]
+
+
+class AppendParams(ctypes.Structure):
+    _fields_ = [
+        ("cache", KvCacheParams),
+        ("layout", _I), ("seqlen_q", _I), ("total_q", _I), ("pad0_", _I),
+        ("k_new", _P), ("v_new", _P), ("k_token_stride", _L), ("v_token_stride", _L),
+        ("cu_seqlens_q", _P), ("seqused_kv", _P), ("tokens_seen", _P),
+        ("weights", _P), ("positions", _P), ("state_stride", _L),
+        ("status", _P), ("reserved", _I * 8),
+    ]
+
+
+class WeightsParams(ctypes.Structure):
+    _fields_ = [
+        ("weights_in", _P), ("weights_out", _P), ("state_stride", _L), ("reserved", _I * 8),
+    ]
+
+
+class EvictParams(ctypes.Structure):
+    _fields_ = [
+        ("cache", KvCacheParams),
+        ("seqused_kv", _P), ("seqused_out", _P), ("tokens_seen", _P),
+        ("weights_in", _P), ("weights_out", _P), ("positions_in", _P), ("positions_out", _P),
+        ("state_stride", _L),
+        ("budget", _I), ("first_tokens", _I), ("recent_tokens", _I), ("pad0_", _I),
+        ("status", _P), ("reserved", _I * 8),
+    ]
+
+
 class FiaPlanLayout(ctypes.Structure):
     _fields_ = [
         ("branch", _I), ("num_ctas", _I), ("num_units", _L), ("max_chunks", _L),
@@ -101,6 +140,9 @@ EXPORTS = (
     "fia_get_workspace_size", "fia_plan", "fia_execute", "fia_run", "fia_get_plan_layout",
     "sparse_attn_metadata", "sparse_attn_run", "fia_decode_run_noalloc",
     "fia_selftest_bounded_wait", "fia_lse_combine",
+    "fia_kv_append", "fia_get_weights_workspace_size", "fia_execute_weights", "fia_run_weights",
+    "fia_get_evict_workspace_size", "fia_kv_evict",
+    "fia_sizeof_append_params", "fia_sizeof_weights_params", "fia_sizeof_evict_params",
 )
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
@@ -139,6 +181,8 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
             L.fia_sizeof_params.restype = ctypes.c_size_t
             L.fia_sizeof_sparse_params.restype = ctypes.c_size_t
             L.fia_sizeof_combine_params.restype = ctypes.c_size_t
+            for f in ("append", "weights", "evict"):
+                getattr(L, f"fia_sizeof_{f}_params").restype = ctypes.c_size_t
             L.fia_get_workspace_size.argtypes = [ctypes.POINTER(FiaParams),
                                                  ctypes.POINTER(ctypes.c_size_t)]
             L.fia_get_plan_layout.argtypes = [ctypes.POINTER(FiaParams),
@@ -152,9 +196,18 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
             L.fia_decode_run_noalloc.argtypes = [ctypes.POINTER(FiaParams), _P, _P]
             L.fia_lse_combine.argtypes = [ctypes.POINTER(CombineParams), _P]
             L.fia_selftest_bounded_wait.argtypes = [_P, ctypes.c_uint64, _P]
+            L.fia_kv_append.argtypes = [ctypes.POINTER(AppendParams), _P]
+            L.fia_get_weights_workspace_size.argtypes = [
+                ctypes.POINTER(FiaParams), ctypes.POINTER(WeightsParams),
+                ctypes.POINTER(ctypes.c_size_t)]
+            for f in ("fia_execute_weights", "fia_run_weights"):
+                getattr(L, f).argtypes = [ctypes.POINTER(FiaParams), ctypes.POINTER(WeightsParams),
+                                          _P, ctypes.c_size_t, _P]
+            L.fia_get_evict_workspace_size.argtypes = [ctypes.POINTER(EvictParams),
+                                                       ctypes.POINTER(ctypes.c_size_t)]
+            L.fia_kv_evict.argtypes = [ctypes.POINTER(EvictParams), _P, ctypes.c_size_t, _P]
             for f in EXPORTS:
-                if f not in ("fia_status_string", "fia_abi_version", "fia_sizeof_params",
-                             "fia_sizeof_sparse_params", "fia_sizeof_combine_params"):
+                if f not in ("fia_status_string", "fia_abi_version") and "sizeof" not in f:
                     getattr(L, f).restype = ctypes.c_int
             if L.fia_abi_version() != ABI_VERSION:
                 raise RuntimeError("libfia ABI version differs from the binding's")
@@ -164,6 +217,10 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
                 raise RuntimeError("sparse_attn_params layout mismatch")
             if L.fia_sizeof_combine_params() != ctypes.sizeof(CombineParams):
                 raise RuntimeError("fia_combine_params layout mismatch")
+            for f, t in (("append", AppendParams), ("weights", WeightsParams),
+                         ("evict", EvictParams)):
+                if getattr(L, f"fia_sizeof_{f}_params")() != ctypes.sizeof(t):
+                    raise RuntimeError(f"fia_{f}_params layout mismatch")
             _lib = L
     return _lib
 
@@ -211,6 +268,38 @@ def fia_decode_run_noalloc(p: FiaParams, status: int = 0, stream: int = 0):
 
 def fia_lse_combine(p: CombineParams, stream: int = 0):
     _check(lib().fia_lse_combine(ctypes.byref(p), stream), "fia_lse_combine")
+
+
+def fia_kv_append(p: AppendParams, stream: int = 0):
+    _check(lib().fia_kv_append(ctypes.byref(p), stream), "fia_kv_append")
+
+
+def fia_get_weights_workspace_size(p: FiaParams, w: WeightsParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().fia_get_weights_workspace_size(ctypes.byref(p), ctypes.byref(w), ctypes.byref(n)),
+           "fia_get_weights_workspace_size")
+    return n.value
+
+
+def fia_execute_weights(p: FiaParams, w: WeightsParams, ws: int, nbytes: int, stream: int = 0):
+    _check(lib().fia_execute_weights(ctypes.byref(p), ctypes.byref(w), ws, nbytes, stream),
+           "fia_execute_weights")
+
+
+def fia_run_weights(p: FiaParams, w: WeightsParams, ws: int, nbytes: int, stream: int = 0):
+    _check(lib().fia_run_weights(ctypes.byref(p), ctypes.byref(w), ws, nbytes, stream),
+           "fia_run_weights")
+
+
+def fia_get_evict_workspace_size(p: EvictParams) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().fia_get_evict_workspace_size(ctypes.byref(p), ctypes.byref(n)),
+           "fia_get_evict_workspace_size")
+    return n.value
+
+
+def fia_kv_evict(p: EvictParams, ws: int, nbytes: int, stream: int = 0):
+    _check(lib().fia_kv_evict(ctypes.byref(p), ws, nbytes, stream), "fia_kv_evict")
 
 
 def sparse_attn_metadata(p: SparseParams, metadata: int, stream: int = 0) -> int:

@@ -46,10 +46,12 @@ def make_fia_params(*, q: torch.Tensor, out: torch.Tensor, k_cache: torch.Tensor
                     mask_mode: int = _abi.MASK_NONE, pre_tokens: int = 0, next_tokens: int = 0,
                     sinks: Optional[torch.Tensor] = None, num_sms: int = 0,
                     kv_layout: int = _abi.KV_LAYOUT_BNBSH,
-                    atten_mask: Optional[torch.Tensor] = None) -> FiaParams:
+                    atten_mask: Optional[torch.Tensor] = None,
+                    first_tokens: int = 0) -> FiaParams:
     """`atten_mask`: int8/uint8/bool [B or 1, rows, cols] (nonzero = masked
     out), rows >= the query length, cols a multiple of 16 >= the KV capacity;
-    a first dimension of 1 is shared by every batch."""
+    a first dimension of 1 is shared by every batch.  `first_tokens` (band
+    mask): keys below it stay visible beside the window."""
     for name, t in (("q", q), ("out", out), ("k_cache", k_cache), ("v_cache", v_cache)):
         _contig(t, name)
     p = FiaParams()
@@ -69,6 +71,7 @@ def make_fia_params(*, q: torch.Tensor, out: torch.Tensor, k_cache: torch.Tensor
     p.sinks = _ptr(sinks)
     p.num_sms = num_sms
     p.kv_layout = kv_layout
+    p.first_tokens = first_tokens
     if atten_mask is not None:
         _contig(atten_mask, "atten_mask")
         if atten_mask.dim() != 3 or atten_mask.element_size() != 1:
@@ -93,7 +96,8 @@ def params_from_problem(prob, out: torch.Tensor, lse: Optional[torch.Tensor],
         cu_seqlens_q=prob.cu_seqlens_q, seqused_kv=prob.seqused_kv, scale=prob.scale,
         mask_mode=prob.mask_mode, pre_tokens=prob.pre_tokens, next_tokens=prob.next_tokens,
         sinks=prob.sinks, num_sms=num_sms, kv_layout=getattr(prob, "kv_layout", 0),
-        atten_mask=getattr(prob, "atten_mask", None))
+        atten_mask=getattr(prob, "atten_mask", None),
+        first_tokens=getattr(prob, "first_tokens", 0))
 
 
 def lse_shape(prob):
@@ -135,6 +139,277 @@ def fused_infer_attention(prob, with_lse: bool = True, num_sms: int = 0, stream=
     """Run FIA on a problem object; returns (out, lse)."""
     c = FiaCall(prob, with_lse=with_lse, num_sms=num_sms)
     return c.run(stream)
+
+
+# ----------------------------------------------------------------------------
+# a bounded cache: append, attention with key weights, eviction
+# ----------------------------------------------------------------------------
+
+def _checked(t: Optional[torch.Tensor], name: str, dtype, shape, device):
+    """Device address of a contiguous tensor of that dtype, shape and device."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    return _ptr(t)
+
+
+def _state(t: Optional[torch.Tensor], name: str, dtype, batch: int, heads: int, capacity: int,
+           device):
+    """Address and row stride of a per-key state tensor [batch, heads, n], n >=
+    the cache's capacity, rows evenly spaced."""
+    if t is None:
+        return None, 0
+    if t.dtype != dtype or t.dim() != 3 or tuple(t.shape[:2]) != (batch, heads) \
+            or t.shape[2] < capacity:
+        raise ValueError(f"{name} must be a {dtype} tensor [{batch}, {heads}, >= {capacity}]")
+    row = int(t.stride(1)) if heads > 1 else int(t.stride(0))
+    if batch == 1 and heads == 1:
+        row = max(int(t.shape[2]), capacity)
+    if (t.shape[2] > 1 and t.stride(2) != 1) or (batch > 1 and t.stride(0) != heads * row):
+        raise ValueError(f"{name}: rows of unit stride, evenly spaced")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    return _ptr(t), row
+
+
+def _one_stride(strides, what: str) -> int:
+    found = {s for s in strides if s}
+    if len(found) > 1:
+        raise ValueError(f"{what} must share one row stride")
+    return found.pop() if found else 0
+
+
+class KvCache:
+    """A KV cache that calls write to: pools [pages, page rows, KV heads, D]
+    (KV_LAYOUT_BNBSH) or [pages, KV heads, page rows, D] (KV_LAYOUT_BNNBSD)
+    with an int32 block table [B, max pages], or contiguous tensors [B, S, KV
+    heads, D]; bf16, or E4M3 codes (uint8 or float8_e4m3fn) with fp32 scales
+    [pages or B, KV heads, rows, D/64]."""
+
+    def __init__(self, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                 block_table: Optional[torch.Tensor] = None, *,
+                 k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                 kv_layout: int = _abi.KV_LAYOUT_BNBSH):
+        if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+            raise ValueError("k_cache and v_cache must be 4-d and alike")
+        head_major = kv_layout == _abi.KV_LAYOUT_BNNBSD
+        n, rows, heads, dim = (int(x) for x in k_cache.shape)
+        if head_major:
+            rows, heads = heads, rows
+        fp8 = k_cache.dtype in (torch.uint8, torch.float8_e4m3fn)
+        if not fp8 and k_cache.dtype != torch.bfloat16:
+            raise ValueError("a cache is bfloat16, or E4M3 codes (uint8, float8_e4m3fn)")
+        if fp8 and (k_scale is None or v_scale is None):
+            raise ValueError("an FP8 cache needs k_scale and v_scale")
+        if not fp8 and (k_scale is not None or v_scale is not None):
+            raise ValueError("scales belong to an FP8 cache")
+        self.device = k_cache.device
+        self.num_kv_heads, self.head_dim = heads, dim
+        self.tensors = (k_cache, v_cache, block_table, k_scale, v_scale)  # kept alive
+        c = self.params = _abi.KvCacheParams()
+        c.num_kv_heads, c.head_dim, c.kv_layout = heads, dim, kv_layout
+        c.k_cache, c.v_cache = _ptr(_contig(k_cache, "k_cache")), _ptr(_contig(v_cache, "v_cache"))
+        if v_cache.device != self.device:
+            raise ValueError("k_cache and v_cache must be on one device")
+        c.kv_dtype = _abi.KV_FP8_E4M3 if fp8 else _abi.KV_BF16
+        if fp8:
+            c.quant_tile = 64
+            shape = (n, heads, rows, dim // 64)
+            c.k_scale = _checked(k_scale, "k_scale", torch.float32, shape, self.device)
+            c.v_scale = _checked(v_scale, "v_scale", torch.float32, shape, self.device)
+        if block_table is None:
+            self.batch, self.capacity = n, rows
+            c.max_seqlen_kv = rows
+        else:
+            if block_table.dim() != 2:
+                raise ValueError("block_table must be [B, max pages]")
+            self.batch, pages = (int(x) for x in block_table.shape)
+            self.capacity = pages * rows
+            c.block_table = _checked(block_table, "block_table", torch.int32, (self.batch, pages),
+                                     self.device)
+            c.max_blocks_per_seq, c.block_size, c.num_blocks = pages, rows, n
+        c.batch = self.batch
+
+    def _lens(self, t, name):
+        return _checked(t, name, torch.int32, (self.batch,), self.device)
+
+    def _state(self, t, name, dtype):
+        return _state(t, name, dtype, self.batch, self.num_kv_heads, self.capacity, self.device)
+
+    def _stream(self, stream) -> int:
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        return _stream(stream)
+
+
+class KvAppendCall:
+    """fia_kv_append with its buffers: the new rows k_new, v_new (bf16 [B, S, KV
+    heads, D], or [T, KV heads, D] with cu_seqlens_q) go behind the keys of their
+    sequences; `seqused_kv` holds the lengths with the new rows, as the attention
+    after it takes them.  Tokens may be strided (a slice of a fused projection).
+    `weights` (fp32) and `positions` (int32), [B, KV heads, >= capacity], get 0
+    and the tokens' places; `status` (int32 [1]) becomes 3 if a row had no place."""
+
+    def __init__(self, cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor,
+                 seqused_kv: torch.Tensor, *, cu_seqlens_q: Optional[torch.Tensor] = None,
+                 weights: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                 tokens_seen: Optional[torch.Tensor] = None,
+                 status: Optional[torch.Tensor] = None):
+        self.cache = cache
+        self.tensors = (k_new, v_new, seqused_kv, cu_seqlens_q, weights, positions, tokens_seen,
+                        status)
+        if k_new.shape != v_new.shape or k_new.dim() != (4 if cu_seqlens_q is None else 3):
+            raise ValueError("k_new and v_new must be alike: [B, S, heads, D], or [T, heads, D] "
+                             "with cu_seqlens_q")
+        if tuple(k_new.shape[-2:]) != (cache.num_kv_heads, cache.head_dim):
+            raise ValueError("k_new does not have the cache's heads")
+        p = self.params = _abi.AppendParams()
+        p.cache = cache.params
+        if cu_seqlens_q is None:
+            if k_new.shape[0] != cache.batch:
+                raise ValueError("k_new does not have the cache's batch")
+            p.layout, p.seqlen_q = _abi.LAYOUT_BSND, int(k_new.shape[1])
+        else:
+            p.layout, p.total_q = _abi.LAYOUT_TND, int(k_new.shape[0])
+            p.cu_seqlens_q = _checked(cu_seqlens_q, "cu_seqlens_q", torch.int32,
+                                      (cache.batch + 1,), cache.device)
+        for name, t in (("k", k_new), ("v", v_new)):
+            if t.dtype != torch.bfloat16 or t.device != cache.device:
+                raise ValueError(f"{name}_new must be bfloat16 on the cache's device")
+            setattr(p, name + "_new", _ptr(t))
+            setattr(p, name + "_token_stride", self._token_stride(t, name + "_new"))
+        p.seqused_kv = cache._lens(seqused_kv, "seqused_kv")
+        p.tokens_seen = cache._lens(tokens_seen, "tokens_seen")
+        if seqused_kv is None:
+            raise ValueError("seqused_kv is required")
+        p.weights, s1 = cache._state(weights, "weights", torch.float32)
+        p.positions, s2 = cache._state(positions, "positions", torch.int32)
+        p.state_stride = _one_stride((s1, s2), "weights and positions")
+        p.status = _checked(status, "status", torch.int32, (1,), cache.device)
+
+    @staticmethod
+    def _token_stride(t: torch.Tensor, name: str) -> int:
+        """Elements between tokens: rows of heads are whole, tokens evenly spaced."""
+        heads, dim = int(t.shape[-2]), int(t.shape[-1])
+        tok = t.dim() - 3
+        n = int(t.shape[tok])
+        if t.numel() == 0:
+            return 0
+        if (dim > 1 and t.stride(-1) != 1) or (heads > 1 and t.stride(-2) != dim):
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+        step = int(t.stride(tok)) if n > 1 else heads * dim
+        if t.dim() == 4 and t.shape[0] > 1:
+            if n == 1:
+                step = int(t.stride(0))
+            elif t.stride(0) != n * step:
+                raise ValueError(f"{name}: tokens must be evenly spaced")
+        return step
+
+    def run(self, stream=None):
+        _abi.fia_kv_append(self.params, self.cache._stream(stream))
+
+
+def kv_append(cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, seqused_kv: torch.Tensor,
+              *, stream=None, **kw):
+    """Write the K and V rows of new tokens to the cache (KvAppendCall's
+    arguments)."""
+    KvAppendCall(cache, k_new, v_new, seqused_kv, **kw).run(stream)
+
+
+class KeyWeightsCall(FiaCall):
+    """An FIA call that also adds up the attention weight of every cached key:
+    weights_out = weights + this call's probabilities summed over the query rows
+    and the heads of a KV head (fp32 [B, KV heads, >= capacity]).  `weights` None
+    starts from zero; `weights_out` defaults to a new tensor of zeros, and may be
+    `weights` itself.  run() returns (out, lse, weights_out)."""
+
+    def __init__(self, prob, weights: Optional[torch.Tensor] = None,
+                 weights_out: Optional[torch.Tensor] = None, num_sms: int = 0, out=None, lse=None):
+        dev = prob.q.device
+        self.prob = prob
+        self.out = torch.empty_like(prob.q) if out is None else out
+        self.lse = (torch.empty(lse_shape(prob), dtype=torch.float32, device=dev)
+                    if lse is None else lse)
+        self.params = params_from_problem(prob, self.out, self.lse, num_sms)
+        capacity = int(prob.S_kv if prob.block_table is None
+                       else prob.block_table.shape[1] * prob.block_size)
+        self.weights = weights
+        self.weights_out = (torch.zeros((prob.B, prob.KVN, capacity), dtype=torch.float32,
+                                        device=dev) if weights_out is None else weights_out)
+        w = self.weights_params = _abi.WeightsParams()
+        w.weights_in, s1 = _state(weights, "weights", torch.float32, prob.B, prob.KVN, capacity,
+                                  dev)
+        w.weights_out, s2 = _state(self.weights_out, "weights_out", torch.float32, prob.B,
+                                   prob.KVN, capacity, dev)
+        w.state_stride = _one_stride((s1, s2), "weights and weights_out")
+        self.ws_bytes = _abi.fia_get_weights_workspace_size(self.params, w)
+        self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=dev)
+
+    def execute(self, stream=None):
+        _abi.fia_execute_weights(self.params, self.weights_params, self.ws.data_ptr(),
+                                 self.ws_bytes, _stream(stream))
+
+    def run(self, stream=None):
+        _abi.fia_run_weights(self.params, self.weights_params, self.ws.data_ptr(), self.ws_bytes,
+                             _stream(stream))
+        return self.out, self.lse, self.weights_out
+
+
+class KvEvictCall:
+    """fia_kv_evict with its buffers and workspace: every KV head of a sequence
+    with more than `budget` keys keeps `budget` of them -- positions below
+    `first_tokens`, the newest `recent_tokens`, then the largest `weights` (ties
+    to the lowest slot) -- and the kept keys past the budget move into the evicted
+    slots below it.  run() returns (seqused_out, weights_out, positions_out); the
+    outputs default to new tensors, and weights_out / positions_out may be the
+    inputs themselves."""
+
+    def __init__(self, cache: KvCache, seqused_kv: torch.Tensor, weights: torch.Tensor, *,
+                 budget: int, first_tokens: int = 0, recent_tokens: int = 0,
+                 positions: Optional[torch.Tensor] = None,
+                 tokens_seen: Optional[torch.Tensor] = None,
+                 weights_out: Optional[torch.Tensor] = None,
+                 positions_out: Optional[torch.Tensor] = None,
+                 seqused_out: Optional[torch.Tensor] = None,
+                 status: Optional[torch.Tensor] = None):
+        self.cache = cache
+        if seqused_kv is None or weights is None:
+            raise ValueError("seqused_kv and weights are required")
+        self.seqused_out = torch.empty_like(seqused_kv) if seqused_out is None else seqused_out
+        self.weights_out = torch.zeros_like(weights) if weights_out is None else weights_out
+        if positions_out is None:
+            positions_out = torch.zeros_like(weights, dtype=torch.int32)
+        self.positions_out = positions_out
+        self.tensors = (seqused_kv, weights, positions, tokens_seen, status)
+        p = self.params = _abi.EvictParams()
+        p.cache = cache.params
+        p.seqused_kv = cache._lens(seqused_kv, "seqused_kv")
+        p.seqused_out = cache._lens(self.seqused_out, "seqused_out")
+        p.tokens_seen = cache._lens(tokens_seen, "tokens_seen")
+        p.weights_in, s1 = cache._state(weights, "weights", torch.float32)
+        p.weights_out, s2 = cache._state(self.weights_out, "weights_out", torch.float32)
+        p.positions_in, s3 = cache._state(positions, "positions", torch.int32)
+        p.positions_out, s4 = cache._state(positions_out, "positions_out", torch.int32)
+        p.state_stride = _one_stride((s1, s2, s3, s4), "weights and positions")
+        p.budget, p.first_tokens, p.recent_tokens = budget, first_tokens, recent_tokens
+        p.status = _checked(status, "status", torch.int32, (1,), cache.device)
+        self.ws_bytes = _abi.fia_get_evict_workspace_size(p)
+        self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=cache.device)
+
+    def run(self, stream=None):
+        _abi.fia_kv_evict(self.params, self.ws.data_ptr(), self.ws_bytes,
+                          self.cache._stream(stream))
+        return self.seqused_out, self.weights_out, self.positions_out
+
+
+def kv_evict(cache: KvCache, seqused_kv: torch.Tensor, weights: torch.Tensor, *, stream=None,
+             **kw):
+    """Cut the cache down to a budget (KvEvictCall's arguments); returns
+    (seqused_out, weights_out, positions_out)."""
+    return KvEvictCall(cache, seqused_kv, weights, **kw).run(stream)
 
 
 # ----------------------------------------------------------------------------

@@ -101,14 +101,25 @@ struct UnitInfo {
   int qrow0, q_len, kv_len;  // the batch's first token row; lengths (q_len <= S_max)
   int lo, hi;                // keys the batch's rows see together
   int lo_last, hi_first;     // the last row's lower bound, the first row's upper
-  int tile0, ntiles;
+  // the unit's KV tiles in the order they run: nwin tiles from tile0 on (the
+  // window), then tiles 0 .. ntiles - nwin - 1 (a band's first tokens, where
+  // tiles that no row sees lie between; otherwise nwin = ntiles)
+  int tile0, nwin, ntiles;
 };
+
+// KV tile of the unit's t-th place (X: the kernel variant that knows a band's
+// first tokens).
+template <bool X>
+__device__ __forceinline__ int tile_at(const UnitInfo& r, int t) {
+  return !X || t < r.nwin ? r.tile0 + t : t - r.nwin;
+}
 
 // Keys [lo, hi] that query row i of a sequence sees, per the mask mode: modes
 // 0 and 1 every key (an explicit mask then hides single keys), 2 the causal
 // mask from the top-left corner (p = i), 3 from the bottom-right corner
 // (p = kv_len - q_len + i), 4 the band p - pre .. p + next.  Clipped to
-// [0, kv_len); hi < lo when the row sees nothing.
+// [0, kv_len); hi < lo when the row sees nothing.  A band's first tokens, the
+// keys below first_tokens up to hi, are seen beside [lo, hi].
 __device__ __forceinline__ void row_bounds(const DecodeArgs& a, int q_len, int kv_len, int i,
                                            int* lo, int* hi) {
   const int64_t p = (int64_t)(a.mask_mode == 2 ? 0 : kv_len - q_len) + i;
@@ -147,16 +158,26 @@ __device__ __forceinline__ UnitInfo unit_from(const DecodeArgs& a, int b, int w,
   r.kv_len = kv_len;
   r.lo = r.lo_last = 0;
   r.hi = r.hi_first = -1;
-  r.tile0 = r.ntiles = 0;
+  r.tile0 = r.nwin = r.ntiles = 0;
   if (r.q_len > 0 && kv_len > 0) {
     int lo1, hi0;
     row_bounds(a, r.q_len, kv_len, 0, &r.lo, &hi0);
     row_bounds(a, r.q_len, kv_len, r.q_len - 1, &lo1, &r.hi);
     r.lo_last = lo1;
     r.hi_first = hi0;
+    // tiles of the first tokens that the last row (which sees furthest) sees
+    const int nf = (min(a.first_tokens, r.hi + 1) + kKvTile - 1) / kKvTile;
     if (r.hi >= r.lo) {
       r.tile0 = r.lo / kKvTile;
-      r.ntiles = r.hi / kKvTile - r.lo / kKvTile + 1;
+      if (nf >= r.tile0) {  // (with nf = 0: the window starts in tile 0)
+        r.tile0 = 0;
+        r.nwin = r.ntiles = r.hi / kKvTile + 1;
+      } else {
+        r.nwin = r.hi / kKvTile - r.tile0 + 1;
+        r.ntiles = r.nwin + nf;
+      }
+    } else {
+      r.nwin = r.ntiles = nf;
     }
   }
   return r;
@@ -557,7 +578,10 @@ __device__ __forceinline__ void combine_store(const DecodeArgs& a, int b, int64_
 // several query rows per sequence (each column masked with its own row's
 // bounds) or an explicit mask; without it every column of a unit is row 0 of
 // its sequence, shares that row's bounds, and the per-column work drops out.
-template <int D, bool FP8, int NG, bool MR>
+// X: a band whose first tokens stay visible; a variant of its own, so that the
+// others keep their registers (with the extra tile order in every variant the
+// FP8 one-row kernel spilled, 0 -> 12 bytes).
+template <int D, bool FP8, int NG, bool MR, bool X>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv) {
@@ -631,19 +655,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The chunk's page ids, one per lane, with one coalesced load when the
     // chunk spans at most 32 pages: each tile then finds its pages by a
     // shuffle instead of a dependent global load.
+    // (the pages of a band's first tokens follow the window's in the lanes)
     struct Pages {
-      int64_t pg0;
-      int npg, mypage;
+      int64_t pg0, fg0;       // first page of the chunk's window tiles, of its first-token tiles
+      int npg, nfg, mypage;   // how many of each
     };
     auto chunk_pages = [&](const UnitInfo& r, int t_begin, int t_end) -> Pages {
-      Pages pp{0, 0, 0};
+      Pages pp{0, 0, 0, 0, 0};
       if (a.block_table && r.ntiles > 0 && t_begin < t_end) {
-        const int64_t jlo = (int64_t)(r.tile0 + t_begin) * kKvTile;
-        const int64_t jhi = min((int64_t)(r.tile0 + t_end) * kKvTile, (int64_t)r.kv_len);
-        pp.pg0 = page_index(a, jlo);
-        pp.npg = (int)(page_index(a, jhi - 1) - pp.pg0 + 1);
-        if (pp.npg <= 32 && lane < pp.npg)
-          pp.mypage = a.block_table[(int64_t)r.b * a.max_blocks + pp.pg0 + lane];
+        const int we = X ? min(t_end, r.nwin) : t_end;
+        if (t_begin < we) {
+          const int64_t jlo = (int64_t)(r.tile0 + t_begin) * kKvTile;
+          const int64_t jhi = min((int64_t)(r.tile0 + we) * kKvTile, (int64_t)r.kv_len);
+          pp.pg0 = page_index(a, jlo);
+          pp.npg = (int)(page_index(a, jhi - 1) - pp.pg0 + 1);
+        }
+        if (X && t_end > r.nwin) {
+          pp.fg0 = page_index(a, (int64_t)max(t_begin - r.nwin, 0) * kKvTile);
+          pp.nfg = (int)(page_index(a, min((int64_t)(t_end - r.nwin) * kKvTile, (int64_t)r.kv_len) - 1) -
+                         pp.fg0 + 1);
+        }
+        if (pp.npg + pp.nfg <= 32 && lane < pp.npg + pp.nfg)
+          pp.mypage = a.block_table[(int64_t)r.b * a.max_blocks +
+                                    (lane < pp.npg ? pp.pg0 + lane : pp.fg0 + lane - pp.npg)];
       }
       return pp;
     };
@@ -658,15 +692,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int s = it % S;
       const uint32_t par = ((it / S) & 1) ^ 1;
-      const int64_t j0 = (int64_t)(r.tile0 + t) * kKvTile;
+      const int64_t j0 = (int64_t)tile_at<X>(r, t) * kKvTile;
       const int64_t jb = j0 + (int64_t)rb * a.box_rows;
       const bool mine = lane < nbox && jb < r.kv_len;
       int64_t blk, jp = 0;
       if (a.block_table) {
         const int64_t pj = mine ? page_index(a, jb) : 0;
         jp = jb - pj * a.block_size;
-        if (pp.npg > 0 && pp.npg <= 32) {
-          blk = __shfl_sync(0xffffffffu, pp.mypage, (int)(pj - pp.pg0));
+        if (pp.npg + pp.nfg > 0 && pp.npg + pp.nfg <= 32) {
+          blk = __shfl_sync(0xffffffffu, pp.mypage,
+                            !X || t < r.nwin ? (int)(pj - pp.pg0) : pp.npg + (int)(pj - pp.fg0));
         } else {
           blk = mine ? (int64_t)a.block_table[(int64_t)r.b * a.max_blocks + pj] : 0;
         }
@@ -1130,7 +1165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint8_t* stp = smem + s * Cfg::kStageBytes;
       // KV positions in 32 bits: lengths are int32, so every position and
       // bound here is below 2^31
-      const int jw = (r.tile0 + t) * kKvTile + R0;  // first KV row of this warp
+      const int jw = tile_at<X>(r, t) * kKvTile + R0;  // first KV row of this warp
       // rows of this warp some column may not see (every column sees keys
       // lo_last .. hi_first, and hi_first < kv_len, so a tail is an edge)
       const bool edge =
@@ -1222,8 +1257,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            bool okA = jg0 >= loc[ng][e] && jg0 <= hic[ng][e];
-            bool okB = jg1 >= loc[ng][e] && jg1 <= hic[ng][e];
+            bool okA = jg0 >= loc[ng][e], okB = jg1 >= loc[ng][e];
+            if (X) {
+              okA = okA || jg0 < a.first_tokens;
+              okB = okB || jg1 < a.first_tokens;
+            }
+            okA = okA && jg0 <= hic[ng][e];
+            okB = okB && jg1 <= hic[ng][e];
             if (MR && a.mask) {
               okA = okA && mk[mrow[ng][e] + ta] == 0;
               okB = okB && mk[mrow[ng][e] + tb] == 0;
@@ -1669,11 +1709,11 @@ cudaError_t launch_decode_schedule(const DecodeArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <int D, bool FP8, int NG, bool MR>
+template <int D, bool FP8, int NG, bool MR, bool X>
 static cudaError_t launch_decode_t(const DecodeArgs& a, const CUtensorMap& tk,
                                    const CUtensorMap& tv, cudaStream_t s) {
   using Cfg = DecodeCfg<D, FP8>;
-  auto kern = decode_kernel<D, FP8, NG, MR>;
+  auto kern = decode_kernel<D, FP8, NG, MR, X>;
   // the shared-memory opt-in is per device and function: set it once for each
   static std::atomic<uint64_t> done_mask[4];
   int dev = 0;
@@ -1692,8 +1732,11 @@ template <int D, bool FP8, int NG>
 static cudaError_t launch_decode_mr(const DecodeArgs& a, const CUtensorMap& tk,
                                     const CUtensorMap& tv, cudaStream_t s) {
   const bool mr = a.S_max > 1 || a.mask != nullptr;
-  return mr ? launch_decode_t<D, FP8, NG, true>(a, tk, tv, s)
-            : launch_decode_t<D, FP8, NG, false>(a, tk, tv, s);
+  if (a.first_tokens > 0)
+    return mr ? launch_decode_t<D, FP8, NG, true, true>(a, tk, tv, s)
+              : launch_decode_t<D, FP8, NG, false, true>(a, tk, tv, s);
+  return mr ? launch_decode_t<D, FP8, NG, true, false>(a, tk, tv, s)
+            : launch_decode_t<D, FP8, NG, false, false>(a, tk, tv, s);
 }
 
 static cudaError_t launch_decode_main(const DecodeArgs& a, const CUtensorMap& tk,

@@ -112,7 +112,7 @@ int64_t kv_capacity_of(const fia_params* p) {
 
 fia_status validate(const fia_params* p) {
   if (!p) return FIA_ERR_NULL_ARG;
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < 7; ++i)
     if (p->reserved[i] != 0) return FIA_ERR_BAD_SHAPE;
   if (p->batch < 1 || p->batch > 65536) return FIA_ERR_BAD_SHAPE;
   if (p->num_q_heads < 1 || p->num_q_heads > 256) return FIA_ERR_BAD_SHAPE;
@@ -141,6 +141,8 @@ fia_status validate(const fia_params* p) {
     return FIA_ERR_BAD_SHAPE;
   if (p->kv_layout == FIA_KV_LAYOUT_BNNBSD && !p->block_table) return FIA_ERR_BAD_SHAPE;
   if (p->mask_mode == FIA_MASK_BAND && (int64_t)p->pre_tokens + p->next_tokens < 0)
+    return FIA_ERR_BAD_SHAPE;
+  if (p->first_tokens < 0 || (p->first_tokens && p->mask_mode != FIA_MASK_BAND))
     return FIA_ERR_BAD_SHAPE;
   if (!std::isfinite(p->scale)) return FIA_ERR_BAD_SHAPE;
   if (p->num_sms < 0 || p->num_sms > 4096) return FIA_ERR_BAD_SHAPE;
@@ -283,6 +285,7 @@ DecodeArgs decode_args(const fia_params* p, const DecodePlan& pl, void* ws) {
   a.mask_mode = p->mask_mode;
   a.pre_tokens = p->pre_tokens;
   a.next_tokens = p->next_tokens;
+  a.first_tokens = p->first_tokens;
   a.sinks = p->sinks;
   a.num_ctas = pl.n;
   a.num_units = pl.U;
@@ -418,6 +421,10 @@ DequantArgs dequant_args(const fia_params* p, const PrefillPlan& pl, void* ws) {
   d.kvfac = reinterpret_cast<float*>(w + pl.off_kvfac);
   d.err = reinterpret_cast<int*>(w);
   d.debug = debug_checks();
+  d.first_tokens = p->first_tokens;
+  d.pre_tokens = p->pre_tokens;
+  d.S_q = p->max_seqlen_q;
+  d.cu_seqlens_q = p->layout == FIA_LAYOUT_TND ? p->cu_seqlens_q : nullptr;
   return d;
 }
 
@@ -451,6 +458,7 @@ PrefillArgs prefill_args(const fia_params* p, const PrefillPlan& pl, void* ws) {
   a.mask_mode = p->mask_mode;
   a.pre_tokens = p->pre_tokens;
   a.next_tokens = p->next_tokens;
+  a.first_tokens = p->first_tokens;
   a.sinks = p->sinks;
   a.num_ctas = pl.n;
   a.max_cost = pl.max_cost;
@@ -600,6 +608,73 @@ bool q_empty(const fia_params* p) {
   return p->layout == FIA_LAYOUT_TND ? p->total_q == 0 : p->max_seqlen_q == 0;
 }
 
+// ---------------------------------------------------------------------------
+// key weights
+// ---------------------------------------------------------------------------
+fia_status weights_validate(const fia_params* p, const fia_weights_params* w) {
+  const fia_status st = validate(p);
+  if (st != FIA_OK) return st;
+  if (!w) return FIA_ERR_NULL_ARG;
+  for (int i = 0; i < 8; ++i)
+    if (w->reserved[i] != 0) return FIA_ERR_BAD_SHAPE;
+  if (!w->weights_out || !p->lse) return FIA_ERR_NULL_ARG;
+  if ((reinterpret_cast<uintptr_t>(w->weights_in) | reinterpret_cast<uintptr_t>(w->weights_out)) & 3u)
+    return FIA_ERR_BAD_SHAPE;
+  if (w->state_stride < kv_capacity_of(p)) return FIA_ERR_BAD_SHAPE;
+  return FIA_OK;
+}
+
+WeightsArgs weights_args(const fia_params* p, const fia_weights_params* w, void* ws) {
+  WeightsArgs a;
+  memset(&a, 0, sizeof a);
+  a.B = p->batch;
+  a.QN = p->num_q_heads;
+  a.KVN = p->num_kv_heads;
+  a.D = p->head_dim;
+  a.G = p->num_q_heads / p->num_kv_heads;
+  a.S_q = p->max_seqlen_q;
+  a.S_kv = (int)kv_capacity_of(p);
+  a.q = static_cast<const uint16_t*>(p->q);
+  a.q_stride = p->q_token_stride ? p->q_token_stride : (int64_t)p->num_q_heads * p->head_dim;
+  a.lse = p->lse;
+  a.cu_seqlens_q = p->layout == FIA_LAYOUT_TND ? p->cu_seqlens_q : nullptr;
+  a.seqused_kv = p->seqused_kv;
+  a.mask = p->atten_mask;
+  a.mask_bstride = p->mask_batch_stride;
+  a.mask_rstride = p->mask_row_stride;
+  a.scale = p->scale;
+  a.mask_mode = p->mask_mode;
+  a.pre_tokens = p->pre_tokens;
+  a.next_tokens = p->next_tokens;
+  a.first_tokens = p->first_tokens;
+  a.w_in = w->weights_in;
+  a.w_out = w->weights_out;
+  a.stride = w->state_stride;
+  a.err = q_empty(p) ? nullptr : static_cast<int*>(ws);  // (nothing else ran: no word to read)
+  return a;
+}
+
+fia_kv_cache cache_of(const fia_params* p) {
+  fia_kv_cache c;
+  memset(&c, 0, sizeof c);
+  c.batch = p->batch;
+  c.num_kv_heads = p->num_kv_heads;
+  c.head_dim = p->head_dim;
+  c.kv_dtype = p->kv_dtype;
+  c.quant_tile = p->quant_tile;
+  c.kv_layout = p->kv_layout;
+  c.k_cache = const_cast<void*>(p->k_cache);
+  c.v_cache = const_cast<void*>(p->v_cache);
+  c.k_scale = const_cast<float*>(p->k_scale);
+  c.v_scale = const_cast<float*>(p->v_scale);
+  c.block_table = p->block_table;
+  c.max_blocks_per_seq = p->max_blocks_per_seq;
+  c.block_size = p->block_size;
+  c.num_blocks = p->num_blocks;
+  c.max_seqlen_kv = p->max_seqlen_kv;
+  return c;
+}
+
 }  // namespace
 
 // ===========================================================================
@@ -740,6 +815,44 @@ fia_status fia_run(const fia_params* p, void* ws, size_t ws_bytes, void* stream)
   fia_status st = fia_plan(p, ws, ws_bytes, stream);
   if (st != FIA_OK) return st;
   return fia_execute(p, ws, ws_bytes, stream);
+}
+
+size_t fia_sizeof_weights_params(void) { return sizeof(fia_weights_params); }
+
+fia_status fia_get_weights_workspace_size(const fia_params* p, const fia_weights_params* w,
+                                          size_t* bytes) {
+  if (!bytes) return FIA_ERR_NULL_ARG;
+  const fia_status st = weights_validate(p, w);
+  if (st != FIA_OK) return st;
+  return fia_get_workspace_size(p, bytes);
+}
+
+fia_status fia_execute_weights(const fia_params* p, const fia_weights_params* w, void* ws,
+                               size_t ws_bytes, void* stream) {
+  NvtxRange range("fia_execute_weights");
+  size_t need;
+  fia_status st = fia_get_weights_workspace_size(p, w, &need);
+  if (st != FIA_OK) return st;
+  if (!ws || ws_bytes < need) return FIA_ERR_WORKSPACE_TOO_SMALL;
+  st = fia_execute(p, ws, ws_bytes, stream);
+  if (st != FIA_OK) return st;
+  const fia_kv_cache cache = cache_of(p);
+  return launch_key_weights(weights_args(p, w, ws), cache, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? FIA_OK
+             : FIA_ERR_CUDA;
+}
+
+fia_status fia_run_weights(const fia_params* p, const fia_weights_params* w, void* ws,
+                           size_t ws_bytes, void* stream) {
+  NvtxRange range("fia_run_weights");
+  size_t need;
+  fia_status st = fia_get_weights_workspace_size(p, w, &need);
+  if (st != FIA_OK) return st;
+  if (!ws || ws_bytes < need) return FIA_ERR_WORKSPACE_TOO_SMALL;
+  st = fia_plan(p, ws, ws_bytes, stream);
+  if (st != FIA_OK) return st;
+  return fia_execute_weights(p, w, ws, ws_bytes, stream);
 }
 
 fia_status sparse_attn_metadata(const sparse_attn_params* p, int32_t* metadata,

@@ -7,6 +7,8 @@
 #include <nvtx3/nvToolsExt.h>
 #include <stdint.h>
 
+#include "../../include/fia.h"
+
 namespace fia {
 
 // An NVTX range over one C-ABI call (plan, execute, run, the sparse calls,
@@ -62,6 +64,7 @@ struct DecodeArgs {
   const float* v_scale;
   float scale_log2;      // scale * log2(e)
   int mask_mode, pre_tokens, next_tokens;
+  int first_tokens;            // band: keys below it stay visible
   const float* sinks;
   // plan (workspace)
   int num_ctas;
@@ -119,6 +122,7 @@ struct PrefillArgs {
   int max_blocks, block_size, box_rows;
   float scale_log2;
   int mask_mode, pre_tokens, next_tokens;
+  int first_tokens;          // band: keys below it stay visible
   const float* sinks;
   // plan (workspace)
   int num_ctas;
@@ -194,10 +198,35 @@ struct DequantArgs {
   float* kvfac;                // [B * KVN * 2] the power of two taken out of K and V
   int* err;                    // the workspace's error word
   int debug;                   // FIA_DEBUG: report page ids outside the pool (error word 3)
+  // a band with first tokens: only the KV tiles that some row sees
+  int first_tokens, pre_tokens, S_q;
+  const int32_t* cu_seqlens_q; // null: S_q rows per sequence
 };
 cudaError_t launch_kv_dequant(const DequantArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
                            const CUtensorMap& tv, cudaStream_t s);
+
+// Key weights: the probabilities of an attention call summed per cached key
+// (key_weights.cu).
+struct WeightsArgs {
+  int B, QN, KVN, D, G;
+  int S_q;                     // BSND query length
+  int S_kv;                    // KV capacity
+  const uint16_t* q;
+  int64_t q_stride;
+  const float* lse;
+  const int32_t* cu_seqlens_q; // null: BSND
+  const int32_t* seqused_kv;   // null: S_kv for every batch
+  const uint8_t* mask;
+  int64_t mask_bstride, mask_rstride;
+  float scale;
+  int mask_mode, pre_tokens, next_tokens, first_tokens;
+  const float* w_in;           // null: zeros
+  float* w_out;
+  int64_t stride;
+  int* err;                    // the workspace's error word
+};
+cudaError_t launch_key_weights(const WeightsArgs& a, const fia_kv_cache& cache, cudaStream_t s);
 
 cudaError_t launch_sparse_metadata(const SparseArgs& a, int32_t* md, cudaStream_t s);
 cudaError_t launch_sparse(const SparseArgs& a, const int32_t* md, cudaStream_t s);

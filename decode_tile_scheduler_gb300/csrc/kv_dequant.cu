@@ -55,6 +55,18 @@ __device__ __forceinline__ bool locate(const DequantArgs& a, int b, int j, int h
   return true;
 }
 
+// Whether some query row of sequence b sees a key of j's KV tile; the tiles
+// between a band's first tokens and its window are left out (a short query
+// behind a long cache would otherwise convert all of it).
+__device__ __forceinline__ bool tile_needed(const DequantArgs& a, int b, int kv_len, int j) {
+  if (a.first_tokens == 0) return true;
+  const int ql = a.cu_seqlens_q ? a.cu_seqlens_q[b + 1] - a.cu_seqlens_q[b] : a.S_q;
+  const int64_t p0 = (int64_t)kv_len - ql;
+  const int64_t lo = max(p0 - a.pre_tokens, (int64_t)0) / kKvTile;
+  const int tile = j / kKvTile;
+  return tile >= lo || tile * kKvTile < a.first_tokens;
+}
+
 // Largest K and V scale of every (batch, KV head) over its visible rows: a
 // warp per (batch, KV head, run of 128 rows), a warp maximum, then one
 // atomic per warp (an atomic per row serialised on the few addresses).  Each
@@ -77,6 +89,7 @@ __global__ void __launch_bounds__(256) scale_max_kernel(const DequantArgs a) {
     uint32_t mk = 0, mv = 0;
     for (int j = run * kScaleRun + lane; j < j_end; j += 32) {
       int64_t off, srow;
+      if (!tile_needed(a, b, kv_len, j)) continue;
       if (!locate(a, b, j, hk, 0, &off, &srow)) continue;
       for (int k = 0; k < NT; ++k) {
         mk = max(mk, __float_as_uint(fabsf(__ldg(a.k_scale + srow * NT + k))));
@@ -116,7 +129,7 @@ __global__ void __launch_bounds__(256) kv_dequant_kernel(const DequantArgs a) {
     const int b = (int)(bj / a.cap);
     const int j = (int)(bj - (int64_t)b * a.cap);
     const int kv_len = a.seqused_kv ? a.seqused_kv[b] : a.cap;
-    if (j >= kv_len) continue;
+    if (j >= kv_len || !tile_needed(a, b, kv_len, j)) continue;
     const int hk = rest / (a.D / 16), d0 = (rest % (a.D / 16)) * 16;
     int64_t code_off, scale_row;
     if (!locate(a, b, j, hk, d0, &code_off, &scale_row)) continue;

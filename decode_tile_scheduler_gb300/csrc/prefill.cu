@@ -63,7 +63,7 @@ struct PrefillCfg {
 
 struct PMsg {
   int b, t, hk, nslots, h0, h1;
-  int q_len, kv_len, tile0, ntiles, done, pad;
+  int q_len, kv_len, tile0, nwin, ntiles, done;  // (tiles: see tile_span)
   int64_t q_row0;  // token row of the tile's first query row
 };
 static_assert(sizeof(PMsg) <= 64, "message slot");
@@ -103,6 +103,13 @@ __device__ __forceinline__ float fmin3(float a, float b, float c) {
   return d;
 }
 
+// First key of the unit's j-th KV tile (X: the kernel variant that knows a
+// band's first tokens).
+template <bool X>
+__device__ __forceinline__ int64_t tile_key(const PMsg& m, int j) {
+  return (int64_t)(!X || j < m.nwin ? m.tile0 + j : j - m.nwin) * kKvTile;
+}
+
 __device__ __forceinline__ void pwait(uint64_t* bar, uint32_t parity, int* err, int* abort_flag) {
   if (*reinterpret_cast<volatile int*>(abort_flag)) return;
   if (!mbar_wait(bar, parity, err)) *reinterpret_cast<volatile int*>(abort_flag) = 1;
@@ -128,11 +135,13 @@ __device__ __forceinline__ int64_t row_pos(const PrefillArgs& a, int64_t q_len, 
   return (a.mask_mode == 2 ? 0 : kv_len - q_len) + i;
 }
 
-// KV interval [lo, hi] (clipped) seen by query rows i0..i1 of a sequence, as a
-// tile range; returns the number of 128-wide KV tiles (0 if none).  An
-// explicit mask narrows nothing here: its bytes are read per row.
+// KV tiles (128 keys) seen by query rows i0..i1 of a sequence; returns their
+// number (0 if none).  They run in this order: *nwin tiles from *tile0 on (the
+// interval [lo, hi] of the rows), then tiles 0, 1, ... (a band's first tokens,
+// where tiles that no row sees lie between; otherwise *nwin is all of them).
+// An explicit mask narrows nothing here: its bytes are read per row.
 __device__ __forceinline__ int tile_span(const PrefillArgs& a, int64_t q_len, int64_t kv_len,
-                                         int64_t i0, int64_t i1, int* tile0) {
+                                         int64_t i0, int64_t i1, int* tile0, int* nwin) {
   const int64_t p0 = row_pos(a, q_len, kv_len, i0), p1 = row_pos(a, q_len, kv_len, i1);
   int64_t lo = a.mask_mode == 4 ? p0 - a.pre_tokens : 0;
   int64_t hi = (a.mask_mode == 2 || a.mask_mode == 3)
@@ -140,10 +149,17 @@ __device__ __forceinline__ int tile_span(const PrefillArgs& a, int64_t q_len, in
                    : (a.mask_mode == 4 ? p1 + a.next_tokens : kv_len - 1);
   lo = max(lo, (int64_t)0);
   hi = min(hi, kv_len - 1);
-  *tile0 = 0;
-  if (kv_len <= 0 || hi < lo) return 0;
+  *tile0 = *nwin = 0;
+  if (kv_len <= 0 || hi < 0) return 0;
+  const int nf = (int)((min((int64_t)a.first_tokens, hi + 1) + kKvTile - 1) / kKvTile);
+  if (hi < lo) return *nwin = nf;
   *tile0 = (int)(lo / kKvTile);
-  return (int)(hi / kKvTile - lo / kKvTile + 1);
+  if (nf >= *tile0) {  // (with nf = 0: the window starts in tile 0)
+    *tile0 = 0;
+    return *nwin = (int)(hi / kKvTile + 1);
+  }
+  *nwin = (int)(hi / kKvTile) - *tile0 + 1;
+  return *nwin + nf;
 }
 
 // Tensor-map row of logical KV row j of batch b, KV head hk: token-major
@@ -237,8 +253,8 @@ __global__ void __launch_bounds__(1024) prefill_schedule_kernel(const PrefillArg
     int64_t qs, ql, kl;
     seq_lengths(a, b, &qs, &ql, &kl);
     const int64_t i0 = (int64_t)t * kQTile, i1 = min(i0 + kQTile, ql) - 1;
-    int tile0;
-    const int n = tile_span(a, ql, kl, i0, i1, &tile0);
+    int tile0, nwin;
+    const int n = tile_span(a, ql, kl, i0, i1, &tile0, &nwin);
     *cost = min(1 + n, a.max_cost + 1);
   };
   for (int64_t k = tid; k < U; k += nthr) {
@@ -282,8 +298,9 @@ __global__ void __launch_bounds__(1024) prefill_schedule_kernel(const PrefillArg
 // NEG: the softmax scale is negative.  F16: fp16 operands (FP8 caches after
 // their conversion): Q' = Q * 2^sh per (token, head), K' and V' divided by a
 // power of two per (batch, KV head); every row takes the factors back in its
-// score scale and its output.
-template <int D, bool NEG, bool F16>
+// score scale and its output.  X: a band whose first tokens stay visible (a
+// variant of its own: the others keep their registers).
+template <int D, bool NEG, bool F16, bool X>
 __global__ void __launch_bounds__(kPThreads, 1)
     prefill_kernel(const PrefillArgs a, const __grid_constant__ CUtensorMap tq,
                    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
@@ -422,11 +439,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if (!ent_ok || i0 >= ql) ql = 0;  // no query row of the tile exists
       m.q_len = (int)ql;
       m.kv_len = (int)kl;
-      m.ntiles = ql > 0 ? tile_span(a, ql, kl, i0, i1, &m.tile0) : 0;
-      if (ql <= 0) m.tile0 = 0;
+      m.ntiles = ql > 0 ? tile_span(a, ql, kl, i0, i1, &m.tile0, &m.nwin) : 0;
+      if (ql <= 0) m.tile0 = m.nwin = 0;
       m.q_row0 = qs + i0;
       m.done = 0;
-      m.pad = 0;
       if (lane == 0) {
         msg[ms] = m;
         mbar_arrive(&mfull[ms]);
@@ -446,7 +462,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       // K and V tiles
       const int nrb = kKvTile / a.box_rows;
       for (int j = 0; j < m.ntiles; ++j, ++kv_it) {
-        const int64_t j0 = (int64_t)(m.tile0 + j) * kKvTile;
+        const int64_t j0 = tile_key<X>(m, j);
         const int rb = lane / NSUB, sub = lane % NSUB;
         const int64_t jb = j0 + (int64_t)rb * a.box_rows;
         const bool mine = lane < nrb * NSUB && jb < kl;
@@ -628,7 +644,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       for (int j = 0; j < m.ntiles; ++j, ++kv_it) {
         const int vs = kv_it % VS;
         pwait(&vfull[vs], (kv_it / VS) & 1, a.err, misc);
-        const int64_t j0 = (int64_t)(m.tile0 + j) * kKvTile;
+        const int64_t j0 = tile_key<X>(m, j);
         const int nv = (int)min((int64_t)kKvTile, (int64_t)m.kv_len - j0);
         if (nv < kKvTile) {
           uint8_t* vt = smem + Cfg::kOffV + vs * Cfg::kTileBytes;
@@ -730,7 +746,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       float m_used = -INFINITY, l = 0.f;
       for (int j = 0; j < m.ntiles; ++j) {
         // visible columns of this row in the tile: [c0, c1) (tile-local)
-        const int64_t j0 = (int64_t)(m.tile0 + j) * kKvTile;
+        const int64_t j0 = tile_key<X>(m, j);
         const int c0 = (int)min(max(lo - j0, (int64_t)0), (int64_t)kKvTile);
         const int c1 = (int)min(max(hi - j0 + 1, (int64_t)0), (int64_t)kKvTile);
         // explicit mask: the tile's bytes of this row, 16 at a time up to the
@@ -760,6 +776,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const bool all_full =
             __all_sync(0xffffffffu, c0 == 0 && c1 == kKvTile &&
                                         (hidden[0] | hidden[1] | hidden[2] | hidden[3]) == 0u);
+        // a band's first tokens: columns [0, f0) are seen besides [c0, c1)
+        const int f0 = !X ? 0 : (int)min(max((int64_t)a.first_tokens - j0, (int64_t)0), (int64_t)kKvTile);
         // masked score: -inf after the scaling for either sign of the scale
         const uint32_t hole = __float_as_uint(NEG ? INFINITY : -INFINITY);
         // the row's 128 scores: four TMEM loads, one wait; they stay in
@@ -770,9 +788,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
           tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
         tmem_wait_ld();
         if (!all_full) {
+          if constexpr (!X) {
 #pragma unroll
-          for (int e = 0; e < kKvTile; ++e)
-            if (e < c0 || e >= c1 || ((hidden[e >> 5] >> (e & 31)) & 1u)) v[e] = hole;
+            for (int e = 0; e < kKvTile; ++e)
+              if (e < c0 || e >= c1 || ((hidden[e >> 5] >> (e & 31)) & 1u)) v[e] = hole;
+          } else {
+#pragma unroll
+            for (int e = 0; e < kKvTile; ++e)
+              if ((e < c0 && e >= f0) || e >= c1) v[e] = hole;
+          }
         }
         // row maximum of the raw scores (minimum for a negative scale), four
         // three-input chains
@@ -919,12 +943,12 @@ cudaError_t launch_prefill_schedule(const PrefillArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <int D, bool NEG, bool F16>
-static cudaError_t launch_prefill_t(const PrefillArgs& a, const CUtensorMap& tq,
+template <int D, bool NEG, bool F16, bool X>
+static cudaError_t launch_prefill_x(const PrefillArgs& a, const CUtensorMap& tq,
                                     const CUtensorMap& tk, const CUtensorMap& tv,
                                     cudaStream_t s) {
   using Cfg = PrefillCfg<D>;
-  auto kern = prefill_kernel<D, NEG, F16>;
+  auto kern = prefill_kernel<D, NEG, F16, X>;
   static std::atomic<uint64_t> done_mask[4];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -936,6 +960,14 @@ static cudaError_t launch_prefill_t(const PrefillArgs& a, const CUtensorMap& tq,
     done_mask[(dev >> 6) & 3].fetch_or(bit);
   }
   return launch_pdl(kern, dim3(a.num_ctas), dim3(kPThreads), Cfg::kSmem, s, a, tq, tk, tv);
+}
+
+template <int D, bool NEG, bool F16>
+static cudaError_t launch_prefill_t(const PrefillArgs& a, const CUtensorMap& tq,
+                                    const CUtensorMap& tk, const CUtensorMap& tv,
+                                    cudaStream_t s) {
+  return a.first_tokens > 0 ? launch_prefill_x<D, NEG, F16, true>(a, tq, tk, tv, s)
+                            : launch_prefill_x<D, NEG, F16, false>(a, tq, tk, tv, s);
 }
 
 cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,

@@ -76,6 +76,7 @@ class FiaProblem:
     kv_lens: Optional[list] = None         # host copy of KV lengths
     kv_layout: int = KV_LAYOUT_BNBSH       # paged pools: [nb,bs,KVN,D] or [nb,KVN,bs,D]
     atten_mask: Optional[torch.Tensor] = None  # uint8 [B or 1, rows, cols], 1 = hidden
+    first_tokens: int = 0         # band mask: keys below it stay visible
 
     @property
     def max_blocks(self) -> int:
@@ -114,7 +115,7 @@ class FiaProblem:
             hi = (p1 if self.mask_mode in (MASK_RIGHT_DOWN_CAUSAL, MASK_LEFT_UP_CAUSAL) else
                   p1 + self.next_tokens if self.mask_mode == MASK_BAND else kl - 1)
             lo, hi = max(lo, 0), min(hi, kl - 1)
-            out.append(max(0, hi - lo + 1))
+            out.append(max(0, hi - lo + 1) + min(self.first_tokens, max(lo, 0), hi + 1))
         return out
 
 
@@ -265,7 +266,8 @@ def make_fia(*, B, QN, KVN, D, q_lens, kv_lens, layout=LAYOUT_BSND, paged=True,
              block_size=128, kv_dtype=KV_BF16, mask_mode=MASK_NONE, pre_tokens=0,
              next_tokens=0, with_sinks=False, scale=None, seed=0, device="cpu",
              poison=True, max_blocks=None, S_kv=None, q_mult=None, kv_layout=KV_LAYOUT_BNBSH,
-             mask_density=None, mask_shared=False, mask_full_rows=0) -> FiaProblem:
+             mask_density=None, mask_shared=False, mask_full_rows=0,
+             first_tokens=0) -> FiaProblem:
     """Build one FIA problem.  `q_lens`/`kv_lens` are host lists of length B
     (for BSND all q_lens must be equal).  `paged=False` gives a contiguous
     BSND KV cache [B, S_kv, KVN, D].  `q_mult` (a power of two, or one per
@@ -362,7 +364,7 @@ def make_fia(*, B, QN, KVN, D, q_lens, kv_lens, layout=LAYOUT_BSND, paged=True,
                       pre_tokens=pre_tokens, next_tokens=next_tokens,
                       sinks=None if sinks is None else sinks.to(device),
                       q_lens=q_lens, kv_lens=kv_lens, kv_layout=kv_layout,
-                      atten_mask=atten_mask)
+                      atten_mask=atten_mask, first_tokens=first_tokens)
 
 
 def make_sparse(*, B, N1, D, q_lens, kv_lens, layout=LAYOUT_BSND, mode="csa", K2=512,

@@ -12,6 +12,14 @@
  *   COMBINE the log-sum-exp join of partial results computed over disjoint
  *           key sets (fia_lse_combine; the softmax_lse use of "...V2" and the
  *           context-parallel example of "sparse_flash_mla").
+ *   WEIGHTS the same attention, and with it how much weight every cached key
+ *           received (fia_run_weights): what an eviction by accumulated
+ *           attention weight goes by.
+ *   APPEND  new K and V rows written to their pages, quantised where the cache
+ *           is FP8 (fia_kv_append).
+ *   EVICT   a cache cut down to a budget of keys per KV head: the first and the
+ *           newest tokens stay, and of the others those with the largest
+ *           weights (fia_kv_evict).
  *   SPARSE  O = softmax(Q K~^T * softmax_scale) V~ with K~ = V~ gathered from a
  *           band window of the original KV and from compressed KV rows
  *           ("kv_quant_sparse_attn_sharedkv", formula and parameter table;
@@ -33,7 +41,8 @@
  *    row i of a sequence sits at KV position p = kv_len - q_len + i;
  *  - mask modes: 0 none (or an explicit mask); 1 the explicit mask; 2
  *    left-up causal (j <= i); 3 right-down causal (j <= p); 4 band
- *    (p - pre_tokens <= j <= p + next_tokens);
+ *    (p - pre_tokens <= j <= p + next_tokens, and with first_tokens the keys
+ *    j < first_tokens up to p + next_tokens);
  *  - a sink is one extra logit per query head that enters the softmax
  *    denominator only (not multiplied by scale, carries no value); lse
  *    includes it;
@@ -80,7 +89,9 @@ typedef int fia_status;
  *   1 ALL_MASK           where the mask byte is 0 (atten_mask required)
  *   2 LEFT_UP_CAUSAL     j <= i            (the diagonal from the top-left)
  *   3 RIGHT_DOWN_CAUSAL  j <= p, p = kv_len - q_len + i
- *   4 BAND               p - pre_tokens <= j <= p + next_tokens
+ *   4 BAND               p - pre_tokens <= j <= p + next_tokens; also, with
+ *                        first_tokens = f > 0, j < f where j <= p + next_tokens
+ *                        (a sliding window whose first f tokens stay visible)
  * Modes 2-4 are computed from positions; the pages pass them a fixed
  * 2048 x 2048 mask that encodes the same rule, which this library neither
  * needs nor reads (atten_mask must be NULL there). */
@@ -158,7 +169,12 @@ typedef struct fia_params {
     int64_t mask_batch_stride;    /* bytes; 0 = one [S_q, S_kv] mask for all B  */
     int64_t mask_row_stride;      /* bytes, a multiple of 16, >= the KV capacity */
                               /* (paged: max_blocks_per_seq * block_size)        */
-    int32_t reserved[8];      /* must be 0                                     */
+    int32_t first_tokens;     /* band: keys j < first_tokens stay visible       */
+                              /* (>= 0; 0 in every other mode).  The table      */
+                              /* entries of pages that no row of a sequence     */
+                              /* sees -- whole 128-key tiles between the first   */
+                              /* tokens and the window -- are never read        */
+    int32_t reserved[7];      /* must be 0                                     */
 } fia_params;
 
 /* Returns a static string naming a status code. */
@@ -282,6 +298,157 @@ typedef struct fia_combine_params {
     int32_t reserved[8];      /* must be 0                                     */
 } fia_combine_params;
 fia_status fia_lse_combine(const fia_combine_params *p, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* a bounded cache: append, attention with key weights, eviction            */
+/* ------------------------------------------------------------------------ */
+
+/* A KV cache as fia_params describes it (same layouts, limits, alignment and
+ * dtypes; K and V are written here). */
+typedef struct fia_kv_cache {
+    int32_t batch;            /* B                                             */
+    int32_t num_kv_heads;     /* KV_N                                          */
+    int32_t head_dim;         /* D                                             */
+    int32_t kv_dtype;         /* FIA_KV_*                                      */
+    int32_t quant_tile;       /* FP8: 64                                       */
+    int32_t kv_layout;        /* FIA_KV_LAYOUT_* (paged caches)                */
+    void *k_cache;
+    void *v_cache;
+    float *k_scale;           /* FP8 only                                      */
+    float *v_scale;           /* FP8 only                                      */
+    const int32_t *block_table;   /* int32 [B, max_blocks_per_seq] or NULL     */
+    int32_t max_blocks_per_seq;
+    int32_t block_size;
+    int32_t num_blocks;
+    int32_t max_seqlen_kv;    /* contiguous KV: S_kv; paged: ignored           */
+} fia_kv_cache;
+
+/* Per-key state of a bounded cache: for slot j of KV head g of sequence b,
+ * element (b * KV_N + g) * stride + j.
+ *   weights    fp32, how much attention weight the key received so far
+ *   positions  int32, the key's place in its sequence as it was written (slots
+ *              stop being positions once an eviction has moved keys) */
+
+/* APPEND.  Row i of a sequence's q_len new rows goes to slot
+ * kv_len - q_len + i, kv_len = seqused_kv[b] its length WITH the new rows: the
+ * same lengths, and the same right-down alignment, that the attention call
+ * after it takes.
+ *  - bf16 caches: copied.  FP8: per 64 elements scale = amax / 448 (1 where
+ *    amax is 0) and code = x / scale rounded to nearest even, saturated at
+ *    448, both in fp32 with correctly rounded divisions.  A NaN element gets
+ *    the NaN code and does not count in amax; an infinite one counts as the
+ *    largest finite bf16 value.
+ *  - weights (nullable): 0 for the new slots.  positions (nullable):
+ *    tokens_seen[b] - q_len + i with tokens_seen (int32 [B], the tokens of the
+ *    sequence so far, the new ones among them), else the slot.
+ *  - A row whose slot lies outside the cache (negative, or past its capacity)
+ *    or whose page id lies outside [0, num_blocks) is left out, and *status
+ *    (nullable, a device int32 that the caller has cleared) becomes 3.
+ *  - Nothing else is written.  Two rows with the same place (a page listed
+ *    twice) leave either's values.  One launch, no workspace.
+ * cu_seqlens_q must be non-decreasing from 0 to total_q (TND). */
+typedef struct fia_append_params {
+    fia_kv_cache cache;
+    int32_t layout;           /* FIA_LAYOUT_*: k_new, v_new [B,S,KV_N,D] or     */
+                              /* [T,KV_N,D]                                    */
+    int32_t seqlen_q;         /* BSND: S; TND: ignored                         */
+    int32_t total_q;          /* TND: T; BSND: ignored                         */
+    int32_t pad0_;
+    const void *k_new;        /* bf16, 16-byte aligned                         */
+    const void *v_new;        /* bf16, 16-byte aligned                         */
+    int64_t k_token_stride;   /* elements between tokens (0: KV_N*D), a         */
+    int64_t v_token_stride;   /* multiple of 8                                 */
+    const int32_t *cu_seqlens_q;  /* TND: int32 [B+1]                          */
+    const int32_t *seqused_kv;    /* int32 [B], the new rows counted           */
+    const int32_t *tokens_seen;   /* int32 [B] or NULL                         */
+    float *weights;           /* or NULL                                       */
+    int32_t *positions;       /* or NULL                                       */
+    int64_t state_stride;     /* elements between the rows of weights and       */
+                              /* positions, >= the cache's capacity            */
+    int32_t *status;          /* device int32 or NULL                          */
+    int32_t reserved[8];      /* must be 0                                     */
+} fia_append_params;
+fia_status fia_kv_append(const fia_append_params *p, void *stream);
+
+/* WEIGHTS.  fia_run, and for every slot j < kv_len of every KV head g
+ *   weights_out[b,g,j] = weights_in[b,g,j]
+ *                      + sum over rows i and heads h of g's group of
+ *                        exp(scale * q_ih . k_j - lse_ih)  (visible pairs)
+ * i.e. the attention probabilities of this call, summed over its rows and the
+ * group's heads, in fp32 in a fixed order (deterministic).  Rows that see no
+ * key add nothing; a sink takes its share of a row's probability.  Slots at
+ * or past kv_len are left as they were.  weights_in may be NULL (zeros) or
+ * weights_out itself; other overlaps are not allowed.  p->lse is required.
+ * The workspace is fia_get_weights_workspace_size's, larger than
+ * fia_get_workspace_size's; fia_plan on it, then fia_execute_weights any
+ * number of times, or fia_run_weights for both.  Error word as for
+ * fia_execute; with 2 in it weights_out is not written. */
+typedef struct fia_weights_params {
+    const float *weights_in;  /* fp32 [B, KV_N, stride] or NULL                */
+    float *weights_out;       /* fp32 [B, KV_N, stride]                        */
+    int64_t state_stride;     /* >= the cache's capacity                       */
+    int32_t reserved[8];      /* must be 0                                     */
+} fia_weights_params;
+fia_status fia_get_weights_workspace_size(const fia_params *p, const fia_weights_params *w,
+                                          size_t *bytes);
+fia_status fia_execute_weights(const fia_params *p, const fia_weights_params *w, void *workspace,
+                               size_t workspace_bytes, void *stream);
+fia_status fia_run_weights(const fia_params *p, const fia_weights_params *w, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/* EVICT.  Every (sequence, KV head) with n = seqused_kv[b] > budget slots keeps
+ * exactly `budget` of them; with n <= budget it keeps all.  Kept first: keys
+ * whose position is below first_tokens or among the newest recent_tokens
+ * (position >= tokens_seen[b] - recent_tokens); then larger weights (a NaN
+ * ranks below every number, -0 equals 0); ties go to the lowest slot.
+ * Each KV head keeps its own keys.  first + recent <= budget.
+ *
+ * Compaction moves as few rows as possible: with holes the evicted slots below
+ * budget and tails the kept slots at or past it, both ascending (there are
+ * equally many), the k-th tail's K and V rows (and FP8 scales, weight and
+ * position) move into the k-th hole.  Every other kept key stays in its slot,
+ * and rows at or past the new length keep their contents.  Slots are then no
+ * longer in the order of their tokens: attend with a mask that sees all of
+ * the older keys (mode 0, or mode 3, whose last rows are the newest tokens).
+ *
+ *  - seqused_out[b] = min(n, budget); must not be seqused_kv itself.
+ *  - positions_in NULL: slot j is position j (before any eviction).
+ *    tokens_seen NULL: seqused_kv[b].  positions_out is required with
+ *    positions_in, else nullable.
+ *  - weights_out and positions_out receive the kept slots' values (slots below
+ *    the new length); they may be the inputs themselves or be distinct.
+ *  - A length below 0 counts as 0, one past the capacity as the capacity.  A
+ *    move whose page id lies outside [0, num_blocks) is left out (its weight
+ *    and position still move) and *status (nullable, cleared by the caller)
+ *    becomes 3.  Sequences must not share pages that hold moved rows.
+ *  - The workspace size depends on scalars only; its contents do not outlive
+ *    the call.  Deterministic. */
+typedef struct fia_evict_params {
+    fia_kv_cache cache;
+    const int32_t *seqused_kv;    /* int32 [B]                                 */
+    int32_t *seqused_out;         /* int32 [B]                                 */
+    const int32_t *tokens_seen;   /* int32 [B] or NULL                         */
+    const float *weights_in;      /* fp32 [B, KV_N, stride]                    */
+    float *weights_out;
+    const int32_t *positions_in;  /* int32 [B, KV_N, stride] or NULL           */
+    int32_t *positions_out;
+    int64_t state_stride;         /* >= the cache's capacity                   */
+    int32_t budget;               /* 1 .. the cache's capacity                 */
+    int32_t first_tokens;         /* >= 0                                      */
+    int32_t recent_tokens;        /* >= 0                                      */
+    int32_t pad0_;
+    int32_t *status;              /* device int32 or NULL                      */
+    int32_t reserved[8];          /* must be 0                                 */
+} fia_evict_params;
+fia_status fia_get_evict_workspace_size(const fia_evict_params *p, size_t *bytes);
+fia_status fia_kv_evict(const fia_evict_params *p, void *workspace, size_t workspace_bytes,
+                        void *stream);
+
+/* sizeof(fia_append_params), sizeof(fia_weights_params) and
+ * sizeof(fia_evict_params) as compiled into the library. */
+size_t fia_sizeof_append_params(void);
+size_t fia_sizeof_weights_params(void);
+size_t fia_sizeof_evict_params(void);
 
 /* Self-test of the bounded wait that every pipeline barrier of this library
  * uses (failure detection without a GPU fault): launches, on `stream`, one
