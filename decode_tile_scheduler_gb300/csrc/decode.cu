@@ -578,9 +578,10 @@ __device__ __forceinline__ void combine_store(const DecodeArgs& a, int b, int64_
 // several query rows per sequence (each column masked with its own row's
 // bounds) or an explicit mask; without it every column of a unit is row 0 of
 // its sequence, shares that row's bounds, and the per-column work drops out.
-// X: a band whose first tokens stay visible; a variant of its own, so that the
-// others keep their registers (with the extra tile order in every variant the
-// FP8 one-row kernel spilled, 0 -> 12 bytes).
+// X: a band whose first tokens stay visible, or a call that keeps its scores
+// for the key weights; a variant of its own, so that the others keep their
+// registers (with the extra tile order in every variant the FP8 one-row kernel
+// spilled, 0 -> 12 bytes).
 template <int D, bool FP8, int NG, bool MR, bool X>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tk,
@@ -1272,6 +1273,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             xs[ng][2 + e] = okB ? sc[ng][2 + e] * slc : -INFINITY;
           }
       }
+      if (X && a.scores) {
+        // keys jg0 and jg1, columns c0 + 8 ng + 2 q4 and the next (c0 and the
+        // row length are even: 8-byte stores); eight lanes' rows of a quad
+        // column are neighbours, so a warp writes whole sectors
+        const int64_t base = ((int64_t)r.b * a.KVN + r.hk) * a.S_kv;
+#pragma unroll
+        for (int ng = 0; ng < NG; ++ng) {
+          const int cl = ng * 8 + 2 * q4;
+          if (cl < r.ncols) {
+            if (jg0 < kvl)
+              *reinterpret_cast<float2*>(a.scores + (base + jg0) * a.score_cols + r.c0 + cl) =
+                  make_float2(xs[ng][0], xs[ng][1]);
+            if (jg1 < kvl)
+              *reinterpret_cast<float2*>(a.scores + (base + jg1) * a.score_cols + r.c0 + cl) =
+                  make_float2(xs[ng][2], xs[ng][3]);
+          }
+        }
+      }
 #pragma unroll
       for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
@@ -1697,8 +1716,78 @@ __global__ void __launch_bounds__(256, 4) decode_combine_grouped(const DecodeArg
 }
 
 // ---------------------------------------------------------------------------
+// key weights of a decode call: w_j = sum over its columns (query row, head) of
+// 2^(score - lse), from the scores the decode kernel kept and the lse the
+// combine finished.  Keeping 4 bytes per (key, column) costs far less than
+// forming K Q^T again would (a key is 256 bytes of K per KV head, and a GQA-4
+// step has four columns).
+// ---------------------------------------------------------------------------
+constexpr int kMaxCols = kDecodeMaxRows * 64;  // query rows x heads per KV head
+
+// L threads per key, each every L-th pair of its columns.
+template <int L>
+__global__ void __launch_bounds__(256) decode_weights_kernel(const DecodeArgs a, const float* w_in,
+                                                             float* w_out, int64_t stride,
+                                                             int per_pair) {
+  __shared__ float nl[kMaxCols];
+  const int pair = blockIdx.x / per_pair, b = pair / a.KVN, hk = pair - b * a.KVN;
+  pdl_wait();
+  if (a.sched[5] != kDecodePlanMark || a.sched[6] != a.B || a.sched[7] != a.num_ctas ||
+      *a.prefill_mark == kPrefillPlanMark)
+    return;  // no plan of these arguments: the decode kernel has reported it
+  int64_t qrow, ql, kl64;
+  batch_lengths(a, b, &qrow, &ql, &kl64);
+  const int kl = (int)min(max(kl64, (int64_t)0), (int64_t)a.S_kv);
+  const UnitInfo r = unit_from(a, b, hk * a.HG, (int)qrow, ql, kl);
+  const int ncols = r.q_len * a.G;
+  for (int c = threadIdx.x; c < ncols; c += 256) {
+    const int i = c / a.G, h = hk * a.G + c - i * a.G;
+    const int64_t li = a.layout == 1 ? (qrow + i) * a.QN + h : ((int64_t)b * a.QN + h) * a.S_q + i;
+    nl[c] = -1.4426950408889634f * __ldcg(a.lse + li);
+  }
+  __syncthreads();
+  const int sub = threadIdx.x % L;
+  for (int j0 = (blockIdx.x % per_pair) * (256 / L); j0 < kl; j0 += per_pair * (256 / L)) {
+    const int j = j0 + threadIdx.x / L;
+    float w = 0.f;
+    // (the tiles that ran: the others hold no scores, and no row sees them)
+    const int t = j / kKvTile;
+    const bool ran = j < kl && ((t >= r.tile0 && t < r.tile0 + r.nwin) || t < r.ntiles - r.nwin);
+    if (ran) {
+      const float2* s = reinterpret_cast<const float2*>(
+          a.scores + (((int64_t)b * a.KVN + hk) * a.S_kv + j) * a.score_cols);
+      for (int c = 2 * sub; c < ncols; c += 2 * L) {
+        const float2 x = __ldcg(s + c / 2);
+        w += fast_exp2(x.x + nl[c]);
+        if (c + 1 < ncols) w += fast_exp2(x.y + nl[c + 1]);
+      }
+    }
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+    if (j < kl && sub == 0) {
+      const int64_t at = (int64_t)pair * stride + j;
+      w_out[at] = (w_in ? w_in[at] : 0.f) + w;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
 // host launchers
 // ---------------------------------------------------------------------------
+cudaError_t launch_decode_weights(const DecodeArgs& a, const float* w_in, float* w_out,
+                                  int64_t stride, cudaStream_t s) {
+  const int pairs = a.B * a.KVN;
+  if (a.S_kv == 0) return cudaSuccess;
+  const int L = a.score_cols <= 4 ? 1 : a.score_cols <= 16 ? 4 : 16;
+  const int64_t keys = 256 / L;  // per block and pass
+  const int per_pair = (int)std::max<int64_t>(
+      1, std::min<int64_t>((a.S_kv + keys - 1) / keys, (int64_t)a.num_ctas * 8 / pairs));
+  auto kern = L == 1 ? decode_weights_kernel<1> : L == 4 ? decode_weights_kernel<4>
+                                                         : decode_weights_kernel<16>;
+  return launch_pdl(kern, dim3(pairs * per_pair), dim3(256), 0, s, a, w_in, w_out, stride,
+                    per_pair);
+}
+
 size_t decode_smem_bytes(int D, int fp8) {
   if (fp8) return DecodeCfg<128, true>::kSmem;
   return D == 64 ? DecodeCfg<64, false>::kSmem : DecodeCfg<128, false>::kSmem;
@@ -1732,7 +1821,7 @@ template <int D, bool FP8, int NG>
 static cudaError_t launch_decode_mr(const DecodeArgs& a, const CUtensorMap& tk,
                                     const CUtensorMap& tv, cudaStream_t s) {
   const bool mr = a.S_max > 1 || a.mask != nullptr;
-  if (a.first_tokens > 0)
+  if (a.first_tokens > 0 || a.scores)
     return mr ? launch_decode_t<D, FP8, NG, true, true>(a, tk, tv, s)
               : launch_decode_t<D, FP8, NG, false, true>(a, tk, tv, s);
   return mr ? launch_decode_t<D, FP8, NG, true, false>(a, tk, tv, s)

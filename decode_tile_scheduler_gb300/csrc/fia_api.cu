@@ -467,6 +467,7 @@ PrefillArgs prefill_args(const fia_params* p, const PrefillPlan& pl, void* ws) {
   char* w = static_cast<char*>(ws);
   a.err = reinterpret_cast<int*>(w);
   a.claim = reinterpret_cast<int*>(w + 16);
+  a.wclaim = reinterpret_cast<int*>(w + kWsWeightsClaimOff);
   a.num_units = reinterpret_cast<int64_t*>(w + 8);
   a.seq_prefix = reinterpret_cast<int64_t*>(w + pl.off_seq);
   a.hist = reinterpret_cast<int*>(w + pl.off_hist);
@@ -624,7 +625,32 @@ fia_status weights_validate(const fia_params* p, const fia_weights_params* w) {
   return FIA_OK;
 }
 
-WeightsArgs weights_args(const fia_params* p, const fia_weights_params* w, void* ws) {
+// Behind the attention's own workspace: decode keeps the scores of the call
+// ([B, KV_N, capacity, columns] fp32), a prompt the partial sums of its parts
+// ([parts, B, KV_N, capacity] fp32).
+struct WeightsPlan {
+  fia_plan_layout lay;
+  int cols, chunk, parts;
+  int64_t off, total;
+};
+
+fia_status weights_plan(const fia_params* p, const fia_weights_params* w, WeightsPlan* pl) {
+  fia_status st = weights_validate(p, w);
+  if (st != FIA_OK) return st;
+  st = fia_get_plan_layout(p, &pl->lay);
+  if (st != FIA_OK) return st;
+  const int G = p->num_q_heads / p->num_kv_heads;
+  pl->cols = (p->max_seqlen_q * G + 1) & ~1;
+  pl->chunk = weights_chunk(G, p->max_seqlen_q, &pl->parts);
+  pl->off = align_up(pl->lay.total_bytes);
+  const int64_t keys = (int64_t)p->batch * p->num_kv_heads * kv_capacity_of(p);
+  const int64_t per_key = pl->lay.branch == 0 ? 0 : pl->lay.branch == 1 ? pl->cols : pl->parts;
+  pl->total = pl->off + align_up(4 * keys * per_key);
+  return FIA_OK;
+}
+
+WeightsArgs weights_args(const fia_params* p, const fia_weights_params* w, const WeightsPlan& pl,
+                         void* ws) {
   WeightsArgs a;
   memset(&a, 0, sizeof a);
   a.B = p->batch;
@@ -634,15 +660,15 @@ WeightsArgs weights_args(const fia_params* p, const fia_weights_params* w, void*
   a.G = p->num_q_heads / p->num_kv_heads;
   a.S_q = p->max_seqlen_q;
   a.S_kv = (int)kv_capacity_of(p);
-  a.q = static_cast<const uint16_t*>(p->q);
-  a.q_stride = p->q_token_stride ? p->q_token_stride : (int64_t)p->num_q_heads * p->head_dim;
+  a.q_rows = q_rows_of(p);
   a.lse = p->lse;
   a.cu_seqlens_q = p->layout == FIA_LAYOUT_TND ? p->cu_seqlens_q : nullptr;
   a.seqused_kv = p->seqused_kv;
+  a.box_rows = p->block_table ? gcd_i(p->block_size, kKvTile) : kKvTile;
   a.mask = p->atten_mask;
   a.mask_bstride = p->mask_batch_stride;
   a.mask_rstride = p->mask_row_stride;
-  a.scale = p->scale;
+  a.scale_log2 = p->scale * 1.4426950408889634f;
   a.mask_mode = p->mask_mode;
   a.pre_tokens = p->pre_tokens;
   a.next_tokens = p->next_tokens;
@@ -650,7 +676,13 @@ WeightsArgs weights_args(const fia_params* p, const fia_weights_params* w, void*
   a.w_in = w->weights_in;
   a.w_out = w->weights_out;
   a.stride = w->state_stride;
-  a.err = q_empty(p) ? nullptr : static_cast<int*>(ws);  // (nothing else ran: no word to read)
+  a.num_ctas = pl.lay.num_ctas;
+  a.chunk = pl.chunk;
+  char* b = static_cast<char*>(ws);
+  if (pl.lay.branch == 2) a.plan = reinterpret_cast<const int64_t*>(b + kWsPrefillMarkOff);
+  a.claim = reinterpret_cast<int*>(b + kWsWeightsClaimOff);
+  a.partials = reinterpret_cast<float*>(b + pl.off);
+  a.err = reinterpret_cast<int*>(b);
   return a;
 }
 
@@ -673,6 +705,27 @@ fia_kv_cache cache_of(const fia_params* p) {
   c.num_blocks = p->num_blocks;
   c.max_seqlen_kv = p->max_seqlen_kv;
   return c;
+}
+
+}  // namespace
+
+namespace {
+
+// The decode branch of an execute; with `scores`, every score is kept there.
+fia_status execute_decode(const fia_params* p, void* ws, float* scores, int cols, cudaStream_t s,
+                          DecodeArgs* a) {
+  DecodePlan pl;
+  fia_status st = decode_plan(p, &pl);
+  if (st != FIA_OK) return st;
+  *a = decode_args(p, pl, ws);
+  a->scores = scores;
+  a->score_cols = cols;
+  CUtensorMap tk, tv;
+  st = kv_maps(p, a->box_rows, &tk, &tv);
+  if (st != FIA_OK) return st;
+  return launch_decode(*a, tk, tv, p->kv_dtype == FIA_KV_FP8_E4M3, s) == cudaSuccess
+             ? FIA_OK
+             : FIA_ERR_CUDA;
 }
 
 }  // namespace
@@ -799,15 +852,8 @@ fia_status fia_execute(const fia_params* p, void* ws, size_t ws_bytes, void* str
     }
     return launch_prefill(a, tq, tk, tv, s) == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
   }
-  DecodePlan pl;
-  st = decode_plan(p, &pl);
-  if (st != FIA_OK) return st;
-  DecodeArgs a = decode_args(p, pl, ws);
-  CUtensorMap tk, tv;
-  st = kv_maps(p, a.box_rows, &tk, &tv);
-  if (st != FIA_OK) return st;
-  return launch_decode(a, tk, tv, p->kv_dtype == FIA_KV_FP8_E4M3, s) == cudaSuccess ? FIA_OK
-                                                                                     : FIA_ERR_CUDA;
+  DecodeArgs a;
+  return execute_decode(p, ws, nullptr, 0, s, &a);
 }
 
 fia_status fia_run(const fia_params* p, void* ws, size_t ws_bytes, void* stream) {
@@ -822,25 +868,41 @@ size_t fia_sizeof_weights_params(void) { return sizeof(fia_weights_params); }
 fia_status fia_get_weights_workspace_size(const fia_params* p, const fia_weights_params* w,
                                           size_t* bytes) {
   if (!bytes) return FIA_ERR_NULL_ARG;
-  const fia_status st = weights_validate(p, w);
+  WeightsPlan pl;
+  const fia_status st = weights_plan(p, w, &pl);
   if (st != FIA_OK) return st;
-  return fia_get_workspace_size(p, bytes);
+  *bytes = (size_t)pl.total;
+  return FIA_OK;
 }
 
 fia_status fia_execute_weights(const fia_params* p, const fia_weights_params* w, void* ws,
                                size_t ws_bytes, void* stream) {
   NvtxRange range("fia_execute_weights");
-  size_t need;
-  fia_status st = fia_get_weights_workspace_size(p, w, &need);
+  WeightsPlan pl;
+  fia_status st = weights_plan(p, w, &pl);
   if (st != FIA_OK) return st;
-  if (!ws || ws_bytes < need) return FIA_ERR_WORKSPACE_TOO_SMALL;
+  if (!ws || ws_bytes < (size_t)pl.total) return FIA_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (pl.lay.branch == 1) {
+    float* scores = reinterpret_cast<float*>(static_cast<char*>(ws) + pl.off);
+    DecodeArgs a;
+    st = execute_decode(p, ws, scores, pl.cols, s, &a);
+    if (st != FIA_OK) return st;
+    return launch_decode_weights(a, w->weights_in, w->weights_out, w->state_stride, s) == cudaSuccess
+               ? FIA_OK
+               : FIA_ERR_CUDA;
+  }
   st = fia_execute(p, ws, ws_bytes, stream);
   if (st != FIA_OK) return st;
-  const fia_kv_cache cache = cache_of(p);
-  return launch_key_weights(weights_args(p, w, ws), cache, static_cast<cudaStream_t>(stream)) ==
-                 cudaSuccess
-             ? FIA_OK
-             : FIA_ERR_CUDA;
+  const WeightsArgs a = weights_args(p, w, pl, ws);
+  if (pl.lay.branch == 0)  // no query row
+    return launch_key_weights_fold(a, s) == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
+  CUtensorMap tq, tk, tv;
+  st = q_map(p, &tq);
+  if (st != FIA_OK) return st;
+  st = kv_maps(p, a.box_rows, &tk, &tv);
+  if (st != FIA_OK) return st;
+  return launch_key_weights(a, cache_of(p), tq, tk, s) == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
 }
 
 fia_status fia_run_weights(const fia_params* p, const fia_weights_params* w, void* ws,

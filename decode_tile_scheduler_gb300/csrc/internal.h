@@ -82,6 +82,10 @@ struct DecodeArgs {
   float* partials;             // [max_chunks][GH][D + 2]: acc, then m and l
   int* err;
   int debug;                   // FIA_DEBUG: report page ids outside the pool (error word 3)
+  // key weights: every score (times log2 e, -inf where masked) is kept, the
+  // columns (query row, head) of a key next to each other
+  float* scores;               // [B * KVN][S_kv][score_cols], or null
+  int score_cols;              // S_max * G, rounded up to even
 };
 
 // Target number of big chunks per persistent CTA in the decode schedule.
@@ -94,11 +98,13 @@ constexpr int64_t kDecodePlanMark = 0x4649414445434F44LL;
 constexpr int64_t kPrefillPlanMark = 0x4649415052454649LL;
 // The first 256 bytes of a workspace are a header that both branches share:
 // [0, 4) error word, [8, 16) prefill unit count, [16, 24) claim counters,
-// [24, 48) prefill plan mark, B and CTA count.  A decode plan clears the
+// [24, 48) prefill plan mark, B and CTA count, [48, 56) claim counters of the
+// key weights pass behind a prefill.  A decode plan clears the
 // prefill mark, and a decode execute runs nothing while that mark is set, so
 // one workspace can serve both branches: an execute after the other branch's
 // plan reports 2 in the error word instead of reading a plan that is gone.
 constexpr int kWsPrefillMarkOff = 24;
+constexpr int kWsWeightsClaimOff = 48;
 
 struct PrefillArgs {
   int B, QN, KVN, D, G, npairs, per_pair;  // per_pair query heads per unit (2, or 1 if G odd)
@@ -132,6 +138,7 @@ struct PrefillArgs {
   int* hist;              // [max_cost + 2] cost histogram, then offsets
   int2* unit_list;        // [units] (b, q_tile | hk << 18 | pair << 26), cost-descending
   int* claim;             // [2]: next unit to claim, CTAs done claiming
+  int* wclaim;            // [2]: the same of the key weights pass, cleared with a plan
   int* err;
   int64_t max_units;      // bound on the plan's unit count (the unit list's length)
   int64_t num_blocks;     // pages in the pool (paged caches)
@@ -206,27 +213,41 @@ cudaError_t launch_kv_dequant(const DequantArgs& a, int num_sms, cudaStream_t s)
 cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
                            const CUtensorMap& tv, cudaStream_t s);
 
-// Key weights: the probabilities of an attention call summed per cached key
+// Key weights of a prompt: its attention's probabilities summed per cached key
 // (key_weights.cu).
 struct WeightsArgs {
   int B, QN, KVN, D, G;
-  int S_q;                     // BSND query length
+  int S_q;                     // BSND query length; TND: its upper bound
   int S_kv;                    // KV capacity
-  const uint16_t* q;
-  int64_t q_stride;
+  int64_t q_rows;              // rows of q
   const float* lse;
   const int32_t* cu_seqlens_q; // null: BSND
   const int32_t* seqused_kv;   // null: S_kv for every batch
+  int box_rows;
   const uint8_t* mask;
   int64_t mask_bstride, mask_rstride;
-  float scale;
+  float scale_log2;
   int mask_mode, pre_tokens, next_tokens, first_tokens;
   const float* w_in;           // null: zeros
   float* w_out;
   int64_t stride;
-  int* err;                    // the workspace's error word
+  // workspace
+  int num_ctas;
+  int chunk;                   // steps (query tile, head) per part of a unit
+  const int64_t* plan;         // mark, B, CTA count of the prefill plan; null: nothing to add
+  int* claim;                  // [2]: next item, CTAs done
+  float* partials;             // [parts][B * KVN][S_kv]
+  int* err;
 };
-cudaError_t launch_key_weights(const WeightsArgs& a, const fia_kv_cache& cache, cudaStream_t s);
+// Steps per part and the most parts of a unit, for queries of at most max_q rows.
+int weights_chunk(int G, int64_t max_q, int* parts);
+cudaError_t launch_key_weights(const WeightsArgs& a, const fia_kv_cache& cache,
+                               const CUtensorMap& tq, const CUtensorMap& tk, cudaStream_t s);
+// w_out = w_in plus the parts (none without a plan).
+cudaError_t launch_key_weights_fold(const WeightsArgs& a, cudaStream_t s);
+// The same for a decode call whose scores were kept (decode.cu).
+cudaError_t launch_decode_weights(const DecodeArgs& a, const float* w_in, float* w_out,
+                                  int64_t stride, cudaStream_t s);
 
 cudaError_t launch_sparse_metadata(const SparseArgs& a, int32_t* md, cudaStream_t s);
 cudaError_t launch_sparse(const SparseArgs& a, const int32_t* md, cudaStream_t s);
