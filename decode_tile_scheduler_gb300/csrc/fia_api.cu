@@ -467,7 +467,6 @@ PrefillArgs prefill_args(const fia_params* p, const PrefillPlan& pl, void* ws) {
   char* w = static_cast<char*>(ws);
   a.err = reinterpret_cast<int*>(w);
   a.claim = reinterpret_cast<int*>(w + 16);
-  a.wclaim = reinterpret_cast<int*>(w + kWsWeightsClaimOff);
   a.num_units = reinterpret_cast<int64_t*>(w + 8);
   a.seq_prefix = reinterpret_cast<int64_t*>(w + pl.off_seq);
   a.hist = reinterpret_cast<int*>(w + pl.off_hist);
@@ -626,12 +625,12 @@ fia_status weights_validate(const fia_params* p, const fia_weights_params* w) {
 }
 
 // Behind the attention's own workspace: decode keeps the scores of the call
-// ([B, KV_N, capacity, columns] fp32), a prompt the partial sums of its parts
-// ([parts, B, KV_N, capacity] fp32).
+// ([B, KV_N, capacity, columns] fp32), a prompt its units' part counts ([B, KV_N,
+// units] int32) and the partial sums ([parts, B, KV_N, capacity] fp32).
 struct WeightsPlan {
   fia_plan_layout lay;
-  int cols, chunk, parts;
-  int64_t off, total;
+  int cols;
+  int64_t off, off_part, total;
 };
 
 fia_status weights_plan(const fia_params* p, const fia_weights_params* w, WeightsPlan* pl) {
@@ -641,11 +640,14 @@ fia_status weights_plan(const fia_params* p, const fia_weights_params* w, Weight
   if (st != FIA_OK) return st;
   const int G = p->num_q_heads / p->num_kv_heads;
   pl->cols = (p->max_seqlen_q * G + 1) & ~1;
-  pl->chunk = weights_chunk(G, p->max_seqlen_q, &pl->parts);
-  pl->off = align_up(pl->lay.total_bytes);
-  const int64_t keys = (int64_t)p->batch * p->num_kv_heads * kv_capacity_of(p);
-  const int64_t per_key = pl->lay.branch == 0 ? 0 : pl->lay.branch == 1 ? pl->cols : pl->parts;
-  pl->total = pl->off + align_up(4 * keys * per_key);
+  pl->off = pl->off_part = pl->total = align_up(pl->lay.total_bytes);
+  const int64_t pairs = (int64_t)p->batch * p->num_kv_heads;
+  if (pl->lay.branch == 2) {
+    pl->off_part = align_up(pl->off + 4 * pairs * weights_units(kv_capacity_of(p)));
+    pl->total = align_up(pl->off_part + 4 * pairs * kv_capacity_of(p) * weights_parts());
+  } else if (pl->lay.branch == 1) {
+    pl->total = align_up(pl->off + 4 * pairs * kv_capacity_of(p) * pl->cols);
+  }
   return FIA_OK;
 }
 
@@ -677,11 +679,12 @@ WeightsArgs weights_args(const fia_params* p, const fia_weights_params* w, const
   a.w_out = w->weights_out;
   a.stride = w->state_stride;
   a.num_ctas = pl.lay.num_ctas;
-  a.chunk = pl.chunk;
+  a.chunk = weights_chunk(a.G, p->max_seqlen_q);
   char* b = static_cast<char*>(ws);
   if (pl.lay.branch == 2) a.plan = reinterpret_cast<const int64_t*>(b + kWsPrefillMarkOff);
-  a.claim = reinterpret_cast<int*>(b + kWsWeightsClaimOff);
-  a.partials = reinterpret_cast<float*>(b + pl.off);
+  a.units_max = weights_units(a.S_kv);
+  a.nparts = reinterpret_cast<int*>(b + pl.off);
+  a.partials = reinterpret_cast<float*>(b + pl.off_part);
   a.err = reinterpret_cast<int*>(b);
   return a;
 }

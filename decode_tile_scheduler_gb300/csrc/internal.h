@@ -98,13 +98,11 @@ constexpr int64_t kDecodePlanMark = 0x4649414445434F44LL;
 constexpr int64_t kPrefillPlanMark = 0x4649415052454649LL;
 // The first 256 bytes of a workspace are a header that both branches share:
 // [0, 4) error word, [8, 16) prefill unit count, [16, 24) claim counters,
-// [24, 48) prefill plan mark, B and CTA count, [48, 56) claim counters of the
-// key weights pass behind a prefill.  A decode plan clears the
+// [24, 48) prefill plan mark, B and CTA count.  A decode plan clears the
 // prefill mark, and a decode execute runs nothing while that mark is set, so
 // one workspace can serve both branches: an execute after the other branch's
 // plan reports 2 in the error word instead of reading a plan that is gone.
 constexpr int kWsPrefillMarkOff = 24;
-constexpr int kWsWeightsClaimOff = 48;
 
 struct PrefillArgs {
   int B, QN, KVN, D, G, npairs, per_pair;  // per_pair query heads per unit (2, or 1 if G odd)
@@ -138,7 +136,6 @@ struct PrefillArgs {
   int* hist;              // [max_cost + 2] cost histogram, then offsets
   int2* unit_list;        // [units] (b, q_tile | hk << 18 | pair << 26), cost-descending
   int* claim;             // [2]: next unit to claim, CTAs done claiming
-  int* wclaim;            // [2]: the same of the key weights pass, cleared with a plan
   int* err;
   int64_t max_units;      // bound on the plan's unit count (the unit list's length)
   int64_t num_blocks;     // pages in the pool (paged caches)
@@ -233,14 +230,16 @@ struct WeightsArgs {
   int64_t stride;
   // workspace
   int num_ctas;
-  int chunk;                   // steps (query tile, head) per part of a unit
+  int chunk;                   // the fewest steps (query tile, head) per part of a unit
   const int64_t* plan;         // mark, B, CTA count of the prefill plan; null: nothing to add
-  int* claim;                  // [2]: next item, CTAs done
-  float* partials;             // [parts][B * KVN][S_kv]
+  int64_t units_max;           // units of a (sequence, KV head), at most
+  int* nparts;                 // [B * KVN][units_max] parts of a unit
+  float* partials;             // [weights_parts()][B * KVN][S_kv]
   int* err;
 };
-// Steps per part and the most parts of a unit, for queries of at most max_q rows.
-int weights_chunk(int G, int64_t max_q, int* parts);
+int weights_chunk(int G, int64_t max_q);
+int64_t weights_units(int64_t capacity);
+int weights_parts();  // parts of a unit, at most
 cudaError_t launch_key_weights(const WeightsArgs& a, const fia_kv_cache& cache,
                                const CUtensorMap& tq, const CUtensorMap& tk, cudaStream_t s);
 // w_out = w_in plus the parts (none without a plan).

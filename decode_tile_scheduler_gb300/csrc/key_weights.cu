@@ -11,14 +11,17 @@
 // and heads in a register, with no reduction across threads and no atomics.
 //
 // Work: a unit is (sequence, KV head, 256 keys), its steps the (query tile,
-// head) pairs that see some of its keys, cut into parts of at most `chunk`
-// steps so that short calls still fill the GPU.  A part keeps its two K tiles in
-// shared memory and streams the Q tiles past them; each K tile belongs to one
-// epilogue warpgroup, so a Q tile in shared memory serves 2 x 128 keys (with one
-// K tile per part the Q reads from L2 alone would be 32 KB per 1024 cycles of
-// exponentials, on 152 SMs about the L2's rate).  A part's sums go to its own
-// row of the workspace, and key_weights_fold_kernel adds the parts of a key in
-// order, so the result does not depend on which CTA ran what.
+// head) pairs that see some of its keys.  All steps of the call form one list, of
+// which every CTA takes an equal range; a unit that ranges cut has several parts.
+// (With units cut in parts of 4 or 8 steps that CTAs claimed one by one, each CTA
+// held one or two claims ahead for its loads, and on four prompts of up to 2048
+// rows the slowest had 20 steps where the mean was 16.)  A unit's two K tiles stay
+// in shared memory while the Q tiles stream past them; each K tile belongs to one
+// epilogue warpgroup, so a Q tile in shared memory serves 2 x 128 keys (with one K
+// tile the Q reads from L2 alone would be 32 KB per 1024 cycles of exponentials,
+// on 152 SMs about the L2's rate).  The sums of a unit's parts go to rows of the
+// workspace, and key_weights_fold_kernel adds them in order: no atomics, the same
+// bits every time.
 //
 // FP8 keys: E4M3 codes are bf16 values as they are, so the K tiles are widened
 // to bf16 without their scales, the two 64-element halves of D accumulate apart,
@@ -38,6 +41,7 @@ namespace {
 
 constexpr int kWThreads = 384;
 constexpr int kUnitKeys = 2 * kKvTile;
+constexpr int kMaxParts = 16;  // parts of a unit, at most
 
 template <int D, bool FP8>
 struct WeightsCfg {
@@ -66,10 +70,14 @@ struct WeightsCfg {
 
 struct WMsg {
   int b, hk, j0, kl, ql, qt0, s0, s1;  // steps s0 .. s1 - 1 of the unit
-  int part, done;
+  int part, parts, done;               // this part of the unit, parts of the unit
   int64_t qrow;                        // first token row of the sequence
 };
 static_assert(sizeof(WMsg) <= 64, "message slot");
+
+// Sequences whose steps are summed at a time, and how many such windows there
+// can be (fia.h: at most 65536 sequences).
+constexpr int kSeqWindow = 4096, kSeqWindows = 16;
 
 // First token row, query length and KV length of sequence b.
 __device__ __forceinline__ void w_lengths(const WeightsArgs& a, int b, int64_t* qrow, int* ql,
@@ -118,10 +126,6 @@ __device__ __forceinline__ int unit_steps(const WeightsArgs& a, int ql, int kl, 
   *qt0 = lo / kQTile;
   return (hi1 / kQTile - lo / kQTile + 1) * a.G;
 }
-__device__ __forceinline__ int unit_parts(const WeightsArgs& a, int steps) {
-  return (steps + a.chunk - 1) / a.chunk;
-}
-
 __device__ __forceinline__ bool plan_ok(const WeightsArgs& a) {
   return a.plan[0] == kPrefillPlanMark && a.plan[1] == a.B && a.plan[2] == a.num_ctas;
 }
@@ -132,6 +136,14 @@ __device__ __forceinline__ float2 w_ffma2(float2 a, float2 b, float2 c) {
       "mov.b64 rc, {%6, %7};\n\tfma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 w_fadd2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\tmov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
 __device__ __forceinline__ float w_ex2(float x) {
@@ -205,90 +217,163 @@ __global__ void __launch_bounds__(kWThreads, 1)
   pdl_wait();  // the attention is done: its lse, and the plan before it
   const bool ok = plan_ok(a);
   volatile int* abort_flag = misc;
+
+  // Every CTA takes an equal range of the list of all steps (sequence, 256 keys,
+  // KV head, step).  The sums over a sequence, for finding a range's start, are
+  // formed by all CTAs alike, a warp per sequence and a lane per 256 keys.
+  int64_t* win_sum = reinterpret_cast<int64_t*>(smem + Cfg::kOffQ);
+  int64_t* seq_sum = win_sum + kSeqWindows;
+  const int nwin = (a.B + kSeqWindow - 1) / kSeqWindow;
+  auto sum_window = [&](int w0) {
+    const int nb = min(kSeqWindow, a.B - w0 * kSeqWindow);
+    for (int i = warp; i < nb; i += kWThreads / 32) {
+      int64_t qrow, n = 0;
+      int ql, kl, t0;
+      w_lengths(a, w0 * kSeqWindow + i, &qrow, &ql, &kl);
+      for (int j0 = lane * kUnitKeys; j0 < kl; j0 += 32 * kUnitKeys)
+        n += unit_steps(a, ql, kl, j0, &t0);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      if (lane == 0) seq_sum[i] = n * a.KVN;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      int64_t n = 0;
+      for (int i = lane; i < nb; i += 32) n += seq_sum[i];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      if (lane == 0) win_sum[w0] = n;
+    }
+    __syncthreads();
+  };
+  int64_t all_steps = 0, range = 1;
+  if (ok) {
+    for (int w0 = 0; w0 < nwin; ++w0) {
+      sum_window(w0);
+      all_steps += win_sum[w0];
+    }
+    // no shorter than a.chunk (a part has its K tiles to load, and a unit's
+    // longest has to fit kMaxParts parts)
+    range = max((int64_t)a.chunk, (all_steps + gridDim.x - 1) / gridDim.x);
+    if (nwin > 1) {  // back to the window of this CTA's start
+      int64_t before = 0;
+      int w0 = 0;
+      while (w0 < nwin - 1 && before + win_sum[w0] <= range * (int64_t)blockIdx.x)
+        before += win_sum[w0++];
+      sum_window(w0);
+    }
+  }
   // (the same answer for a whole warp)
   auto stopped = [&]() { return __any_sync(0xffffffffu, *abort_flag != 0); };
 
+  // (the other warps only meet the producer: it reads the sums, then fills the
+  // Q stages they lie in)
+  if (warp != 0) named_bar_sync(4, kWThreads);
+
   if (warp == 0) {
     // ============================ producer ============================
-    // Items in order: sequence, then 256 keys, then KV head, then part (each
-    // unit of a sequence with as many parts as its longest has; those past a
-    // unit's own are skipped).  A CTA's claims only grow, so the sequence of an
-    // item is found by walking on from the last one's, 32 lengths at a time.
+    // The CTA's range of the list of all steps, unit by unit.
     int ucnt = 0, qn = 0;
-    int win = 0;                 // first sequence of the lanes' window
-    int64_t base = 0;            // items before it
-    int64_t qrow = 0, items = 0, before = 0, total = 0;
-    int ql = 0, kl = 0, parts = 0;
-    auto load_window = [&]() {
-      const int b = win + lane;
-      ql = kl = parts = 0;
-      items = 0;
-      if (ok && b < a.B) {
-        w_lengths(a, b, &qrow, &ql, &kl);
-        parts = unit_parts(a, (ql + kQTile - 1) / kQTile * a.G);
-        items = (int64_t)((kl + kUnitKeys - 1) / kUnitKeys) * a.KVN * parts;
+    int b = 0, kt = 0, hk = 0, ql = 0, kl = 0, nkt = 0, steps = 0, qt0 = 0;
+    int64_t qrow = 0, at = range * (int64_t)blockIdx.x, s = 0;  // place in the list, in the unit
+    const int64_t end = min(at + range, all_steps);
+    // the first unit with steps at or behind tile pair `from` of the sequence
+    auto next_kt = [&](int from) {
+      for (int base = from; base < nkt; base += 32) {
+        int t0 = 0;
+        const int n = base + lane < nkt ? unit_steps(a, ql, kl, (base + lane) * kUnitKeys, &t0) : 0;
+        const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
+        if (some) {
+          const int src = __ffs(some) - 1;
+          kt = base + src;
+          steps = __shfl_sync(0xffffffffu, n, src);
+          qt0 = __shfl_sync(0xffffffffu, t0, src);
+          return true;
+        }
       }
-      int64_t x = items;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      before = x - items;
-      total = __shfl_sync(0xffffffffu, x, 31);
+      return false;
     };
-    load_window();
-    int claim = 0;
-    if (lane == 0 && ok) claim = atomicAdd(a.claim, 1);
+    // the first sequence with steps at or behind `from`
+    auto next_seq = [&](int from) {
+      for (int base = from; base < a.B; base += 32) {
+        int l = 0, k = 0;
+        int64_t r = 0;
+        if (base + lane < a.B) w_lengths(a, base + lane, &r, &l, &k);
+        uint32_t some = __ballot_sync(0xffffffffu, l > 0 && k > 0);
+        while (some) {
+          const int src = __ffs(some) - 1;
+          some &= some - 1;
+          b = base + src;
+          ql = __shfl_sync(0xffffffffu, l, src);
+          kl = __shfl_sync(0xffffffffu, k, src);
+          qrow = __shfl_sync(0xffffffffu, r, src);
+          nkt = (kl + kUnitKeys - 1) / kUnitKeys;
+          if (next_kt(0)) return true;
+        }
+      }
+      return false;
+    };
+    bool more = at < end;
+    if (more) {
+      // sequence of the range's first step: window, then the prefix inside it
+      int64_t before = 0;
+      int w0 = 0;
+      while (before + win_sum[w0] <= at) before += win_sum[w0++];
+      const int nb = min(kSeqWindow, a.B - w0 * kSeqWindow);
+      for (int base = 0; base < nb; base += 32) {
+        const int64_t n = base + lane < nb ? seq_sum[base + lane] : 0;
+        int64_t x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        const uint32_t here = __ballot_sync(0xffffffffu, before + x > at);
+        if (here) {
+          const int src = __ffs(here) - 1;
+          b = w0 * kSeqWindow + base + src;
+          before += __shfl_sync(0xffffffffu, x - n, src);
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, x, 31);
+      }
+      more = next_seq(b);
+      // then its units
+      while (more && before + (int64_t)steps * a.KVN <= at) {
+        before += (int64_t)steps * a.KVN;
+        more = next_kt(kt + 1);
+      }
+      if (more) {
+        hk = (int)((at - before) / steps);
+        s = at - before - (int64_t)hk * steps;
+      }
+    }
+    named_bar_sync(4, kWThreads);  // the sums, in the Q stages' place, have been read
+    fence_proxy_async_smem();      // (before the copies that overwrite them)
     while (true) {
-      const int64_t idx = __shfl_sync(0xffffffffu, claim, 0);
-      while (ok && win < a.B && base + total <= idx) {
-        base += total;
-        win += 32;
-        load_window();
-      }
-      const bool done = stopped() || !ok || win >= a.B;
-      if (!done && lane == 0) claim = atomicAdd(a.claim, 1);  // the next one, ahead
+      const bool done = stopped() || !more || at >= end;
       WMsg m;
-      int nsteps = 0;
-      if (!done) {
-        const int64_t r = idx - base;
-        const uint32_t at = __ballot_sync(0xffffffffu, items > 0 && before <= r && r < before + items);
-        const int src = __ffs(at) - 1;
-        m.b = win + src;
-        m.ql = __shfl_sync(0xffffffffu, ql, src);
-        m.kl = __shfl_sync(0xffffffffu, kl, src);
-        m.qrow = __shfl_sync(0xffffffffu, qrow, src);
-        const int np = __shfl_sync(0xffffffffu, parts, src);
-        const int64_t local = r - __shfl_sync(0xffffffffu, before, src);
-        m.part = (int)(local % np);
-        const int64_t u = local / np;
-        m.hk = (int)(u % a.KVN);
-        m.j0 = (int)(u / a.KVN) * kUnitKeys;
-        const int steps = unit_steps(a, m.ql, m.kl, m.j0, &m.qt0);
-        m.s0 = m.part * a.chunk;
-        m.s1 = min(steps, m.s0 + a.chunk);
-        nsteps = m.s1 - m.s0;
-        m.done = 0;
-        if (nsteps <= 0) continue;  // past the unit's parts
-      }
       const int ms = ucnt & 1;
       wait_or_abort(&mempty[ms], ((ucnt >> 1) & 1) ^ 1, a.err, misc);
       if (done) {
         if (lane == 0) {
-          if (ok) {
-            // the last CTA out re-arms the counter for the next execute
-            __threadfence();
-            if (atomicAdd(a.claim + 1, 1) == (int)gridDim.x - 1) {
-              a.claim[0] = 0;
-              a.claim[1] = 0;
-            }
-          }
           msg[ms].done = 1;
           mbar_arrive(&mfull[ms]);
         }
         break;
       }
+      m.b = b;
+      m.hk = hk;
+      m.j0 = kt * kUnitKeys;
+      m.kl = kl;
+      m.ql = ql;
+      m.qt0 = qt0;
+      m.qrow = qrow;
+      m.s0 = (int)s;
+      m.s1 = (int)min((int64_t)steps, s + (end - at));
+      m.part = (int)(blockIdx.x - (at - s) / range);
+      m.parts = (int)((at - s + steps - 1) / range - (at - s) / range + 1);
+      m.done = 0;
       if (lane == 0) {
         msg[ms] = m;
         mbar_arrive(&mfull[ms]);
@@ -326,17 +411,24 @@ __global__ void __launch_bounds__(kWThreads, 1)
         }
       }
       ++ucnt;
-      for (int s = m.s0; s < m.s1; ++s, ++qn) {
+      for (int st = m.s0; st < m.s1; ++st, ++qn) {
         const int qs = qn % QS;
         wait_or_abort(&qempty[qs], ((qn / QS) & 1) ^ 1, a.err, misc);
         if (stopped()) break;
         if (lane == 0) mbar_arrive_expect_tx(&qfull[qs], (uint32_t)Cfg::kTile);
         __syncwarp();
-        const int h = m.hk * a.G + s % a.G;
-        const int64_t row = m.qrow + (int64_t)(m.qt0 + s / a.G) * kQTile;
+        const int h = m.hk * a.G + st % a.G;
+        const int64_t row = m.qrow + (int64_t)(m.qt0 + st / a.G) * kQTile;
         if (lane < NSUB)
           tma_load_2d(smem + Cfg::kOffQ + qs * Cfg::kTile + lane * 16384, &tq, &qfull[qs],
                       h * D + lane * 64, (int)row);
+      }
+      // on to the next unit: the next KV head, 256 keys, sequence
+      at += m.s1 - m.s0;
+      s = 0;
+      if (at < end && ++hk == a.KVN) {
+        hk = 0;
+        more = next_kt(kt + 1) || next_seq(b + 1);
       }
     }
     // after a time-out: the copies in flight land before the CTA ends
@@ -408,24 +500,30 @@ __global__ void __launch_bounds__(kWThreads, 1)
       if (lane == 0) mbar_arrive(&mempty[ms]);
       ++ucnt;
       if (stopped() || m.done) break;
-      for (int s = m.s0; s < m.s1; ++s, ++n) {
-        const int ls = n % LS;
+      auto fetch = [&](int s, float (&v)[4]) {
         const int h = m.hk * a.G + s % a.G;
         const int i0 = (m.qt0 + s / a.G) * kQTile;
-        float v[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int i = i0 + lane + 32 * k;
-          v[k] = -INFINITY;
-          if (i < m.ql)
-            v[k] = -1.4426950408889634f *
-                   __ldcg(a.lse + (a.cu_seqlens_q ? (m.qrow + i) * a.QN + h
+          v[k] = INFINITY;
+          if (s < m.s1 && i < m.ql)
+            v[k] = __ldcg(a.lse + (a.cu_seqlens_q ? (m.qrow + i) * a.QN + h
                                                   : ((int64_t)m.b * a.QN + h) * a.S_q + i));
         }
+      };
+      float v[4], next[4];
+      fetch(m.s0, v);
+      for (int s = m.s0; s < m.s1; ++s, ++n) {
+        const int ls = n % LS;
+        fetch(s + 1, next);  // in flight while this step's values are stored
         wait_or_abort(&lempty[ls], ((n / LS) & 1) ^ 1, a.err, misc);
         if (stopped()) break;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) lse_s[ls * 128 + lane + 32 * k] = v[k];
+        for (int k = 0; k < 4; ++k) {
+          lse_s[ls * 128 + lane + 32 * k] = -1.4426950408889634f * v[k];
+          v[k] = next[k];
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&lfull[ls]);
       }
@@ -504,30 +602,58 @@ __global__ void __launch_bounds__(kWThreads, 1)
           tc_fence_after();
           const int i0 = (m.qt0 + s / a.G) * kQTile;
           const int c0 = lo - i0, c1 = hi - i0;  // columns c0 .. c1 are seen
-          const bool full = __all_sync(0xffffffffu, c0 <= 0 && c1 >= 127) && !a.mask;
-          const bool none = __all_sync(0xffffffffu, c1 < c0 || c1 < 0 || c0 > 127);
           const float* ls4 = lse_s + ls * 128;
           const uint32_t tS = tS0 + 128 * sb;
           float2 acc[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) acc[k] = make_float2(0.f, 0.f);
-          if (!none) {
+          const float2 f0v = make_float2(f0, f0), f1v = make_float2(f1, f1);
+          auto release = [&]() {  // the S buffer, once its values are in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sempty[2 * w + sb]);
+          };
+          const bool full = __all_sync(0xffffffffu, c0 <= 0 && c1 >= 127) && !a.mask;
+          if (!FP8 && full) {
+            // every pair is seen: the row's 128 scores in registers with one
+            // wait, the buffer free for the next product at once
+            uint32_t v[128];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t v[64], u[FP8 ? 64 : 1];
+            for (int q = 0; q < 4; ++q)
+              tmem_ld32(tS + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * q]));
+            tmem_wait_ld();
+            release();
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                tmem_ld32(tS + 64 * half + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * k]));
-                if constexpr (FP8)
-                  tmem_ld32(tS + 128 + 64 * half + 32 * k,
-                            *reinterpret_cast<uint32_t(*)[32]>(&u[32 * k]));
-              }
+            for (int e = 0; e < 128; e += 4) {
+              const float4 nl = *reinterpret_cast<const float4*>(ls4 + e);
+              const float2 t0 = w_ffma2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])),
+                                        f0v, make_float2(nl.x, nl.y));
+              const float2 t1 = w_ffma2(make_float2(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])),
+                                        f0v, make_float2(nl.z, nl.w));
+              acc[(e >> 1) & 3] = w_fadd2(acc[(e >> 1) & 3], make_float2(w_ex2(t0.x), w_ex2(t0.y)));
+              acc[((e >> 1) + 1) & 3] =
+                  w_fadd2(acc[((e >> 1) + 1) & 3], make_float2(w_ex2(t1.x), w_ex2(t1.y)));
+            }
+          } else {
+            // 32 columns at a time (a rolled loop: unrolled over all 128, the
+            // instructions no longer fit their cache)
+            const uint32_t span = (uint32_t)(c1 - c0);
+            const bool any = c1 >= c0;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              // on a diagonal most of a warp's 32 x 32 squares are seen whole or
+              // not at all
+              if (!__any_sync(0xffffffffu, any && c0 <= 32 * q + 31 && c1 >= 32 * q)) continue;
+              const bool whole = __all_sync(0xffffffffu, c0 <= 32 * q && c1 >= 32 * q + 31) && !a.mask;
+              uint32_t v[32], u[FP8 ? 32 : 1];
+              tmem_ld32(tS + 32 * q, v);
+              if constexpr (FP8) tmem_ld32(tS + 128 + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&u));
               tmem_wait_ld();
-              const float2 f0v = make_float2(f0, f0), f1v = make_float2(f1, f1);
+              const float4* nl4 = reinterpret_cast<const float4*>(ls4 + 32 * q);
+              float x[32];  // exponents, log2 units
 #pragma unroll
-              for (int e = 0; e < 64; e += 4) {
-                const float4 nl = *reinterpret_cast<const float4*>(ls4 + 64 * half + e);
-                float2 x[2];
+              for (int e = 0; e < 32; e += 4) {
+                const float4 nl = nl4[e / 4];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                   float2 t = k ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y);
@@ -536,32 +662,34 @@ __global__ void __launch_bounds__(kWThreads, 1)
                                             __uint_as_float(u[e + 2 * k + 1])), f1v, t);
                   t = w_ffma2(make_float2(__uint_as_float(v[e + 2 * k]),
                                           __uint_as_float(v[e + 2 * k + 1])), f0v, t);
-                  x[k] = make_float2(w_ex2(t.x), w_ex2(t.y));
-                }
-                if (!full) {
-                  float p[4] = {x[0].x, x[0].y, x[1].x, x[1].y};
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const int col = 64 * half + e + k;
-                    bool see = col >= c0 && col <= c1;
-                    if (see && mrow) see = __ldg(mrow + (int64_t)(i0 + col) * a.mask_rstride) == 0;
-                    if (!see) p[k] = 0.f;
-                  }
-                  x[0] = make_float2(p[0], p[1]);
-                  x[1] = make_float2(p[2], p[3]);
-                }
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  float2& s2 = acc[(e / 2 + k) & 3];
-                  s2.x += x[k].x;
-                  s2.y += x[k].y;
+                  x[e + 2 * k] = t.x;
+                  x[e + 2 * k + 1] = t.y;
                 }
               }
+              if (!whole) {  // pairs outside the row interval, or hidden by the mask
+                uint32_t hid = 0;
+                if (a.mask) {
+#pragma unroll 4
+                  for (int e = 0; e < 32; ++e) {
+                    const int col = 32 * q + e;
+                    if (any && (uint32_t)(col - c0) <= span &&
+                        __ldg(mrow + (int64_t)(i0 + col) * a.mask_rstride) != 0)
+                      hid |= 1u << e;
+                  }
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!any || (uint32_t)(32 * q + e - c0) > span || ((hid >> e) & 1u))
+                    x[e] = -INFINITY;
+              }
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float2& s2 = acc[(e / 2) & 3];
+                s2 = w_fadd2(s2, make_float2(w_ex2(x[e]), w_ex2(x[e + 1])));
+              }
             }
+            release();
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sempty[2 * w + sb]);
           sum += ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) +
                  ((acc[2].x + acc[2].y) + (acc[3].x + acc[3].y));
         }
@@ -569,8 +697,17 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (lane == 0) mbar_arrive(&lempty[ls]);
       }
       ++ucnt;
-      if (active && j < m.kl && !*abort_flag)
-        a.partials[((int64_t)m.part * a.B * a.KVN + (int64_t)m.b * a.KVN + m.hk) * a.S_kv + j] = sum;
+      if (active && j < m.kl && !*abort_flag) {
+        const int64_t pair = (int64_t)m.b * a.KVN + m.hk;
+        if (m.parts == 1) {  // the whole unit: nothing to fold
+          const int64_t o = pair * a.stride + j;
+          a.w_out[o] = (a.w_in ? a.w_in[o] : 0.f) + sum;
+        } else {
+          a.partials[((int64_t)m.part * a.B * a.KVN + pair) * a.S_kv + j] = sum;
+        }
+        if (m.part == 0 && w == 0 && row == 0)
+          a.nparts[pair * a.units_max + m.j0 / kUnitKeys] = m.parts;
+      }
     }
   }
   tc_fence_before();
@@ -579,7 +716,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// w_out = w_in + the parts of each key, in order.
+// w_out = w_in + the parts of each key, in order, where a unit had several; and
+// w_in where no row sees any of a unit's keys.
 __global__ void __launch_bounds__(256) key_weights_fold_kernel(const WeightsArgs a, int per_pair) {
   pdl_wait();
   if (a.plan && !plan_ok(a)) return;
@@ -589,12 +727,17 @@ __global__ void __launch_bounds__(256) key_weights_fold_kernel(const WeightsArgs
   w_lengths(a, b, &qrow, &ql, &kl);
   const int64_t stride = (int64_t)a.B * a.KVN * a.S_kv;
   for (int j = (blockIdx.x % per_pair) * 256 + threadIdx.x; j < kl; j += per_pair * 256) {
-    int qt0;
-    const int parts = a.plan ? unit_parts(a, unit_steps(a, ql, kl, j / kUnitKeys * kUnitKeys, &qt0)) : 0;
+    int qt0, parts = 0;
+    if (a.plan && unit_steps(a, ql, kl, j / kUnitKeys * kUnitKeys, &qt0) > 0)
+      parts = min(__ldcg(a.nparts + (int64_t)pair * a.units_max + j / kUnitKeys), kMaxParts);
+    if (parts == 1) continue;  // written by its part
     const int64_t at = (int64_t)pair * a.stride + j;
-    float w = 0.f;
+    float w = 0.f, x[kMaxParts];
     const float* p = a.partials + (int64_t)pair * a.S_kv + j;
-    for (int k = 0; k < parts; ++k) w += __ldcg(p + k * stride);
+#pragma unroll
+    for (int k = 0; k < kMaxParts; ++k) x[k] = k < parts ? __ldcg(p + k * stride) : 0.f;
+#pragma unroll
+    for (int k = 0; k < kMaxParts; ++k) w += x[k];
     a.w_out[at] = (a.w_in ? a.w_in[at] : 0.f) + w;
   }
 }
@@ -619,14 +762,15 @@ cudaError_t launch_t(const WeightsArgs& a, const CacheView& c, const CUtensorMap
 
 }  // namespace
 
-// Steps per part: at least 8 (a part loads 64 KB of K; a step takes about 1 us),
-// and few enough parts that the partial sums stay below 16 times the weights.
-int weights_chunk(int G, int64_t max_q, int* parts) {
+// The fewest steps per part: 4 (a part loads 64 KB of K; a step takes about
+// 1 us), and enough that a unit of queries of max_q rows, cut anywhere, has at
+// most kMaxParts parts.
+int weights_chunk(int G, int64_t max_q) {
   const int64_t steps = (max_q + kQTile - 1) / kQTile * G;
-  const int chunk = (int)std::max<int64_t>(8, (steps + 15) / 16);
-  *parts = (int)std::max<int64_t>(1, (steps + chunk - 1) / chunk);
-  return chunk;
+  return (int)std::max<int64_t>(4, (steps + kMaxParts - 2) / (kMaxParts - 1));
 }
+int64_t weights_units(int64_t capacity) { return (capacity + kUnitKeys - 1) / kUnitKeys; }
+int weights_parts() { return kMaxParts; }
 
 cudaError_t launch_key_weights_fold(const WeightsArgs& a, cudaStream_t s) {
   const int pairs = a.B * a.KVN;

@@ -288,7 +288,6 @@ __global__ void __launch_bounds__(1024) prefill_schedule_kernel(const PrefillArg
     a.num_units[4] = a.num_ctas;
     a.claim[0] = 0;
     a.claim[1] = 0;
-    a.wclaim[0] = a.wclaim[1] = 0;
     *a.err = 0;
   }
 }
