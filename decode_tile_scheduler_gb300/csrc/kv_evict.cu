@@ -5,14 +5,23 @@
 // that orders the same way (floats order like their bits once negative ones
 // are complemented and the others have their top bit set; a protected key is
 // the largest value, a NaN weight 0), and the budget-th largest key T is found
-// by radix selection, a histogram of the next digit over the keys that share
-// the digits found so far.  Keys above T stay, and of those equal to T the
-// lowest slots, as many as the budget has left.
+// by radix selection: three histograms of 11, 11 and 10 bits, each over the keys
+// that share the digits found so far, ending early where a digit's keys all
+// stay.  Keys above T stay, and of those equal to T the lowest slots, as many as
+// the budget has left.
 //
 // Compaction moves what has to move and nothing else: the k-th kept slot at or
 // past the budget into the k-th evicted slot below it.  Sources and targets
 // are disjoint, so the moves are independent of each other.
+//
+// One cluster of 1 to 8 CTAs per (sequence, KV head), each a contiguous slice of
+// its slots.  A slice's keys are read once into shared memory; the CTAs join
+// their histograms and counts by reading each other's shared memory, so the
+// weights travel once and nothing but the list of moves passes through global
+// memory.  Bound by latency: a short chain of passes over shared memory between
+// one read of the weights and positions and one copy of the moved rows.
 #include <algorithm>
+#include <atomic>
 
 #include "kv_cache.cuh"
 
@@ -43,111 +52,339 @@ __device__ __forceinline__ uint32_t order_key(float w, int pos, int first, int64
   return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kStagedMax = 40 * 1024;  // keys of a slice kept in shared memory, at most
 
-__global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t s_digit, s_left;
-  __shared__ int s_sum[3][32];
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Every thread of the cluster; writes before it (shared and global memory) are
+// seen by its threads after it.
+template <int CS>
+__device__ __forceinline__ void cluster_sync() {
+  if constexpr (CS == 1) {
+    __syncthreads();
+  } else {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+}
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ uint4 peer_load4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ int peer_load(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Sum of x over the block's threads before this one (exclusive), `total` over
+// all; two barriers.
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_sums, uint32_t* total) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  uint32_t incl = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) warp_sums[wid] = incl;
+  __syncthreads();
+  uint32_t v = lane < kWarps ? warp_sums[lane] : 0u;
+  uint32_t before = lane < wid ? v : 0u;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    v += __shfl_xor_sync(0xffffffffu, v, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  __syncthreads();
+  *total = v;
+  return before + incl - x;
+}
+
+template <int CS>
+__global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a, int staged) {
+  extern __shared__ uint32_t skey[];  // the slice's keys, with `staged` places
+  __shared__ __align__(16) uint32_t hist[3][kBins];
+  __shared__ uint32_t warp_sums[kWarps], found[3];
+  __shared__ int totals[3];   // of this CTA: keys at the threshold, kept keys, kept below the budget
+  __shared__ int warp_cnt[3][kWarps];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int pair = blockIdx.x, b = pair / a.c.KVN, hk = pair - b * a.c.KVN;
+  const uint32_t rank = CS == 1 ? 0u : cluster_rank();
+  const int pair = blockIdx.x / CS, b = pair / a.c.KVN, hk = pair - b * a.c.KVN;
   const int n = min(max(__ldg(a.seqused + b), 0), a.c.cap);
   const int m = min(n, a.budget);
-  if (hk == 0 && tid == 0) a.seqused_out[b] = m;
+  if (hk == 0 && rank == 0 && tid == 0) a.seqused_out[b] = m;
   const float* w = a.w_in + pair * a.stride;
   const int32_t* pin = a.p_in ? a.p_in + pair * a.stride : nullptr;
   float* wo = a.w_out + pair * a.stride;
   int32_t* po = a.p_out ? a.p_out + pair * a.stride : nullptr;
-  if (n <= a.budget) {
-    for (int j = tid; j < n; j += kThreads) {
+  const int slice = ((n + CS - 1) / CS + 31) & ~31;  // n <= 20M: no overflow
+  const int lo = min(n, (int)rank * slice), hi = min(n, lo + slice);
+  if (n <= a.budget) {  // (the whole cluster leaves)
+    for (int j = lo + tid; j < hi; j += kThreads) {
       if (wo != w) wo[j] = w[j];
       if (po && po != pin) po[j] = pin ? pin[j] : j;
     }
     return;
   }
   const int64_t newest = (int64_t)(a.seen ? __ldg(a.seen + b) : n) - a.recent;
-  auto key_of = [&](int j) { return order_key(w[j], pin ? pin[j] : j, a.first, newest); };
-  // the budget-th largest key
-  uint32_t prefix = 0, left = (uint32_t)a.budget;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    if (tid < 256) hist[tid] = 0;
-    __syncthreads();
-    const uint32_t known = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-    for (int j = tid; j < n; j += kThreads) {
-      const uint32_t k = key_of(j);
-      if ((k & known) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1u);
+  auto key_at = [&](int j) { return order_key(w[j], pin ? pin[j] : j, a.first, newest); };
+  const bool in_smem = slice <= staged;
+  auto key_of = [&](int j) { return in_smem ? skey[j - lo] : key_at(j); };
+
+  // ---- the budget-th largest key ----
+  for (int i = tid; i < 3 * kBins; i += kThreads) (&hist[0][0])[i] = 0u;
+  __syncthreads();
+  uint32_t prefix = 0, known = 0, left = (uint32_t)a.budget;
+  bool ties = true;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t digits = pass == 2 ? 1023u : 2047u;
+    const int end = lo + ((hi - lo + 31) & ~31);
+    for (int j = lo + tid; j < end; j += kThreads) {
+      uint32_t k = 0;
+      bool mine = false;
+      if (j < hi) {
+        if (pass == 0) {
+          k = key_at(j);
+          if (in_smem) skey[j - lo] = k;
+        } else {
+          k = key_of(j);
+        }
+        mine = (k & known) == prefix;
+      }
+      // protected keys fall into one bin: one count per warp
+      const uint32_t safe = __ballot_sync(0xffffffffu, mine && k == 0xffffffffu);
+      if (mine && k != 0xffffffffu) atomicAdd(&hist[pass][(k >> shift) & digits], 1u);
+      if (safe && lane == 0) atomicAdd(&hist[pass][digits], (uint32_t)__popc(safe));
+    }
+    cluster_sync<CS>();
+    // bins in falling order, four to a thread, summed over the cluster
+    const int top = kBins - 4 - 4 * tid;
+    uint4 h = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (CS == 1) {
+      h = *reinterpret_cast<const uint4*>(&hist[pass][top]);
+    } else {
+      uint4 x[CS];
+#pragma unroll
+      for (int r = 0; r < CS; ++r) x[r] = peer_load4(peer_addr(&hist[pass][top], r));
+#pragma unroll
+      for (int r = 0; r < CS; ++r) {
+        h.x += x[r].x;
+        h.y += x[r].y;
+        h.z += x[r].z;
+        h.w += x[r].w;
+      }
+    }
+    uint32_t total;
+    uint32_t above = block_scan(h.x + h.y + h.z + h.w, warp_sums, &total);
+    const uint32_t c[4] = {h.w, h.z, h.y, h.x};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (above < left && left <= above + c[i]) {
+        found[0] = (uint32_t)(top + 3 - i);
+        found[1] = left - above;
+        found[2] = c[i];
+      }
+      above += c[i];
     }
     __syncthreads();
-    if (tid == 0) {
-      uint32_t l = left;
-      int d = 255;
-      for (; d > 0 && hist[d] < l; --d) l -= hist[d];
-      s_digit = (uint32_t)d;
-      s_left = l;
-    }
-    __syncthreads();
-    prefix |= s_digit << shift;
-    left = s_left;
+    prefix |= found[0] << shift;
+    known |= digits << shift;
+    left = found[1];
+    ties = left != found[2];
+    if (!ties) break;  // every key with these digits stays
   }
-  // in slot order: which keys equal to the threshold stay, then the holes and
-  // tails and their ranks
+  // (with ties the threshold is a whole key, and `left` of its keys stay)
+
+  // ---- ranks in slot order: each warp a contiguous part of the slice ----
+  const int part = (((hi - lo) + kWarps - 1) / kWarps + 31) & ~31;
+  const int w0 = min(hi, lo + wid * part), w1 = min(hi, w0 + part);
+  int eq_base = 0;
+  if (ties) {
+    int c = 0;
+    for (int j0 = w0; j0 < w1; j0 += 32) {
+      const int j = j0 + lane;
+      c += __popc(__ballot_sync(0xffffffffu, j < w1 && key_of(j) == prefix));
+    }
+    if (lane == 0) warp_cnt[0][wid] = c;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      const int x = warp_cnt[0][i];
+      before += i < wid ? x : 0;
+      all += x;
+    }
+    if (CS > 1) {
+      if (tid == 0) totals[0] = all;
+      cluster_sync<CS>();
+      for (int r = 0; r < (int)rank; ++r) before += peer_load(peer_addr(&totals[0], r));
+    }
+    eq_base = before;
+  }
+  // whether the key of lane's slot stays; `eq` runs over the warp's part
+  auto keeps = [&](int j, int& eq) {
+    const uint32_t k = j < w1 ? key_of(j) : 0u;
+    const uint32_t d = k & known;
+    if (!ties) return j < w1 && d >= prefix;
+    const bool is = j < w1 && d == prefix;
+    const uint32_t me = __ballot_sync(0xffffffffu, is);
+    const bool stay = j < w1 && (d > prefix || (is && eq + __popc(me & ((1u << lane) - 1)) < (int)left));
+    eq += __popc(me);
+    return stay;
+  };
+  {
+    int kept = 0, low = 0, eq = eq_base;
+    for (int j0 = w0; j0 < w1; j0 += 32) {
+      const int j = j0 + lane;
+      const bool stay = keeps(j, eq);
+      kept += __popc(__ballot_sync(0xffffffffu, stay));
+      low += __popc(__ballot_sync(0xffffffffu, stay && j < m));
+    }
+    if (lane == 0) warp_cnt[1][wid] = kept, warp_cnt[2][wid] = low;
+    __syncthreads();
+  }
+  int kept = 0, low = 0;  // kept before this warp's part; kept below the budget, in all
+  {
+    int all = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      const int x = warp_cnt[1][i];
+      kept += i < wid ? x : 0;
+      all += x;
+      low += warp_cnt[2][i];
+    }
+    if (CS > 1) {
+      if (tid == 0) totals[1] = all, totals[2] = low;
+      cluster_sync<CS>();
+      low = 0;
+      for (int r = 0; r < CS; ++r) {
+        if (r < (int)rank) kept += peer_load(peer_addr(&totals[1], r));
+        low += peer_load(peer_addr(&totals[2], r));
+      }
+    }
+  }
+  const int moves = min(m - low, a.max_moves);
+  // a hole's rank is its slot less the kept slots before it, a tail's the kept
+  // slots before it less those below the budget
   int2* mv = a.moves + (int64_t)pair * a.max_moves;
-  int eq_before = 0, holes = 0, tails = 0;
-  for (int base = 0; base < n; base += kThreads) {
-    const int j = base + tid;
-    const uint32_t k = j < n ? key_of(j) : 0u;
-    const bool eq = j < n && k == prefix;
-    const uint32_t me = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) s_sum[0][wid] = __popc(me);
-    __syncthreads();
-    int eq_rank = eq_before + __popc(me & ((1u << lane) - 1));
-    for (int i = 0; i < 32; ++i) {
-      if (i < wid) eq_rank += s_sum[0][i];
-      eq_before += s_sum[0][i];
+  {
+    int eq = eq_base;
+    for (int j0 = w0; j0 < w1; j0 += 32) {
+      const int j = j0 + lane;
+      const bool stay = keeps(j, eq);
+      const uint32_t mk = __ballot_sync(0xffffffffu, stay);
+      const int before = kept + __popc(mk & ((1u << lane) - 1));
+      if (j < w1) {
+        if (j < m && !stay && j - before < a.max_moves) mv[j - before].x = j;
+        if (j >= m && stay && before - low < a.max_moves) mv[before - low].y = j;
+        if (j < m && stay) {
+          if (wo != w) wo[j] = w[j];
+          if (po && po != pin) po[j] = pin ? pin[j] : j;
+        }
+      }
+      kept += __popc(mk);
     }
-    const bool keep = j < n && (k > prefix || (eq && eq_rank < (int)left));
-    const bool hole = j < m && !keep, tail = j >= m && keep;
-    const uint32_t mh = __ballot_sync(0xffffffffu, hole), mt = __ballot_sync(0xffffffffu, tail);
-    if (lane == 0) s_sum[1][wid] = __popc(mh), s_sum[2][wid] = __popc(mt);
-    __syncthreads();
-    int rh = holes + __popc(mh & ((1u << lane) - 1)), rt = tails + __popc(mt & ((1u << lane) - 1));
-    for (int i = 0; i < 32; ++i) {
-      if (i < wid) rh += s_sum[1][i], rt += s_sum[2][i];
-      holes += s_sum[1][i];
-      tails += s_sum[2][i];
-    }
-    if (hole && rh < a.max_moves) mv[rh].x = j;
-    if (tail && rt < a.max_moves) mv[rt].y = j;
-    if (keep && j < m) {
-      if (wo != w) wo[j] = w[j];
-      if (po && po != pin) po[j] = pin ? pin[j] : j;
-    }
-    __syncthreads();
   }
-  // the moves (holes == tails)
+  cluster_sync<CS>();
+
+  // ---- the moves: 16 bytes of K or V per lane, four moves of a group in flight ----
   const int es = a.c.fp8 ? 1 : 2;
-  const int pieces = a.c.D * es / 16;
-  for (int64_t x = tid; x < (int64_t)holes * pieces; x += kThreads) {
-    const int i = (int)(x / pieces), pc = (int)(x % pieces);
-    const int2 ht = mv[i];
-    const RowAt to = cache_row(a.c, b, hk, ht.x), of = cache_row(a.c, b, hk, ht.y);
-    if (pc == 0) {
-      wo[ht.x] = w[ht.y];
-      if (po) po[ht.x] = pin ? pin[ht.y] : ht.y;
+  const int pieces = a.c.D * es / 16;        // of a K row: 8 or 16
+  const int per = 32 / (2 * pieces);         // moves a warp makes side by side: 2 or 1
+  const int grp = lane / (2 * pieces), x = lane % (2 * pieces);
+  const int isv = x >= pieces, pc = x % pieces;
+  uint8_t* pool = isv ? a.c.v : a.c.k;
+  const int step = CS * kWarps * per;
+  constexpr int U = 4;
+  for (int i0 = ((int)rank * kWarps + wid) * per + grp; i0 < moves; i0 += U * step) {
+    int2 ht[U];
+    RowAt to[U], of[U];
+    uint4 v[U];
+    float sc[U], wt[U];
+    int pos[U];
+    bool ok[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      ht[u] = make_int2(0, 0);
+      if (i0 + u * step < moves) ht[u] = __ldcg(mv + i0 + u * step);
     }
-    if (!to.ok || !of.ok) {
-      if (a.status) atomicExch(a.status, 3);
-      continue;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      to[u] = cache_row(a.c, b, hk, ht[u].x);
+      of[u] = cache_row(a.c, b, hk, ht[u].y);
+      ok[u] = i0 + u * step < moves && to[u].ok && of[u].ok;
+      if (i0 + u * step < moves && !ok[u] && x == 0 && a.status) atomicExch(a.status, 3);
     }
-    const int64_t t0 = to.row * a.c.D * es + pc * 16, f0 = of.row * a.c.D * es + pc * 16;
-    *reinterpret_cast<uint4*>(a.c.k + t0) = *reinterpret_cast<const uint4*>(a.c.k + f0);
-    *reinterpret_cast<uint4*>(a.c.v + t0) = *reinterpret_cast<const uint4*>(a.c.v + f0);
-    if (a.c.fp8 && pc < a.c.D / 64) {
-      const int nt = a.c.D / 64;
-      a.c.ks[to.srow * nt + pc] = a.c.ks[of.srow * nt + pc];
-      a.c.vs[to.srow * nt + pc] = a.c.vs[of.srow * nt + pc];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (ok[u]) {
+        v[u] = *reinterpret_cast<const uint4*>(pool + of[u].row * a.c.D * es + pc * 16);
+        if (a.c.fp8 && pc < 2)
+          sc[u] = (isv ? a.c.vs : a.c.ks)[of[u].srow * 2 + pc];  // (FP8 caches: D = 128)
+      }
+      if (i0 + u * step < moves && x == 0) {
+        wt[u] = w[ht[u].y];
+        pos[u] = pin ? pin[ht[u].y] : ht[u].y;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (ok[u]) {
+        *reinterpret_cast<uint4*>(pool + to[u].row * a.c.D * es + pc * 16) = v[u];
+        if (a.c.fp8 && pc < 2) (isv ? a.c.vs : a.c.ks)[to[u].srow * 2 + pc] = sc[u];
+      }
+      if (i0 + u * step < moves && x == 0) {
+        wo[ht[u].x] = wt[u];
+        if (po) po[ht[u].x] = pos[u];
+      }
     }
   }
+}
+
+template <int CS>
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
+  auto kern = kv_evict_kernel<CS>;
+  const int slice = (((a.c.cap + CS - 1) / CS) + 31) & ~31;
+  const int staged = slice <= kStagedMax ? slice : 0;
+  static std::atomic<uint64_t> done_mask[4];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(done_mask[(dev >> 6) & 3].load() & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kStagedMax);
+    if (e != cudaSuccess) return e;
+    done_mask[(dev >> 6) & 3].fetch_or(bit);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.c.B * a.c.KVN * CS);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = 4 * (size_t)staged;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CS;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = CS > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, a, staged);
 }
 
 // At most min(budget, capacity - budget) keys of a head move.
@@ -221,6 +458,18 @@ extern "C" fia_status fia_kv_evict(const fia_evict_params* p, void* ws, size_t w
   a.moves = static_cast<int2*>(ws);
   a.max_moves = (int)max_moves_of(p);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  kv_evict_kernel<<<a.c.B * a.c.KVN, kThreads, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return FIA_ERR_CUDA;
+  // CTAs per head: while they have a few thousand slots each, as many as there
+  // is room for (four CTAs of an SM at once)
+  const int64_t pairs = (int64_t)a.c.B * a.c.KVN;
+  int cs = 8;
+  while (cs > 1 && (pairs * cs > 4 * sms || a.c.cap < 2048 * cs)) cs /= 2;
+  const cudaError_t e = cs == 8   ? launch_evict<8>(a, s)
+                        : cs == 4 ? launch_evict<4>(a, s)
+                        : cs == 2 ? launch_evict<2>(a, s)
+                                  : launch_evict<1>(a, s);
+  return e == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
 }
