@@ -15,10 +15,10 @@
 // are disjoint, so the moves are independent of each other.
 //
 // One cluster of 1 to 8 CTAs per (sequence, KV head), each a contiguous slice of
-// its slots.  A slice's keys are read once into shared memory; the CTAs join
-// their histograms and counts by reading each other's shared memory, so the
-// weights travel once and nothing but the list of moves passes through global
-// memory.  Bound by latency: a short chain of passes over shared memory between
+// its slots.  A slice's keys are read once into shared memory; a CTA adds the few
+// bins of its histogram that are not empty to every peer's joined one, and reads
+// the peers' counts, in their shared memory, so the weights travel once and
+// nothing but the list of moves passes through global memory.  Bound by latency: a short chain of passes over shared memory between
 // one read of the weights and positions and one copy of the moved rows.
 #include <algorithm>
 #include <atomic>
@@ -61,29 +61,32 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-// Every thread of the cluster; writes before it (shared and global memory) are
-// seen by its threads after it.
+// A barrier over every thread of the cluster; writes before its first half
+// (shared and global memory) are seen by its threads after the second.
+template <int CS>
+__device__ __forceinline__ void cluster_arrive() {
+  if constexpr (CS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+template <int CS>
+__device__ __forceinline__ void cluster_wait() {
+  if constexpr (CS == 1)
+    __syncthreads();
+  else
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 template <int CS>
 __device__ __forceinline__ void cluster_sync() {
-  if constexpr (CS == 1) {
-    __syncthreads();
-  } else {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  }
+  cluster_arrive<CS>();
+  cluster_wait<CS>();
 }
 __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
-__device__ __forceinline__ uint4 peer_load4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
+__device__ __forceinline__ void peer_add(uint32_t addr, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v)
                : "memory");
-  return v;
 }
 __device__ __forceinline__ int peer_load(uint32_t addr) {
   int v;
@@ -116,8 +119,10 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_sums, 
 }
 
 template <int CS>
-__global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a, int staged) {
+__global__ void __launch_bounds__(kThreads, 2) kv_evict_kernel(const EvictArgs a, int staged) {
   extern __shared__ uint32_t skey[];  // the slice's keys, with `staged` places
+  // this CTA's histogram of a pass, and each pass's over the cluster (alone: its own)
+  __shared__ __align__(16) uint32_t mine_h[CS > 1 ? kBins : 4];
   __shared__ __align__(16) uint32_t hist[3][kBins];
   __shared__ uint32_t warp_sums[kWarps], found[3];
   __shared__ int totals[3];   // of this CTA: keys at the threshold, kept keys, kept below the budget
@@ -148,49 +153,72 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a, i
 
   // ---- the budget-th largest key ----
   for (int i = tid; i < 3 * kBins; i += kThreads) (&hist[0][0])[i] = 0u;
+  if (CS > 1)
+    for (int i = tid; i < kBins; i += kThreads) mine_h[i] = 0u;
   __syncthreads();
+  cluster_arrive<CS>();  // (peers may add to the joined histograms once all are clear)
   uint32_t prefix = 0, known = 0, left = (uint32_t)a.budget;
   bool ties = true;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const uint32_t digits = pass == 2 ? 1023u : 2047u;
-    const int end = lo + ((hi - lo + 31) & ~31);
-    for (int j = lo + tid; j < end; j += kThreads) {
-      uint32_t k = 0;
-      bool mine = false;
-      if (j < hi) {
-        if (pass == 0) {
-          k = key_at(j);
-          if (in_smem) skey[j - lo] = k;
-        } else {
-          k = key_of(j);
-        }
-        mine = (k & known) == prefix;
-      }
+    uint32_t* h0 = CS > 1 ? mine_h : hist[pass];
+    auto count = [&](uint32_t k, bool mine) {
       // protected keys fall into one bin: one count per warp
       const uint32_t safe = __ballot_sync(0xffffffffu, mine && k == 0xffffffffu);
-      if (mine && k != 0xffffffffu) atomicAdd(&hist[pass][(k >> shift) & digits], 1u);
-      if (safe && lane == 0) atomicAdd(&hist[pass][digits], (uint32_t)__popc(safe));
-    }
-    cluster_sync<CS>();
-    // bins in falling order, four to a thread, summed over the cluster
-    const int top = kBins - 4 - 4 * tid;
-    uint4 h = make_uint4(0u, 0u, 0u, 0u);
-    if constexpr (CS == 1) {
-      h = *reinterpret_cast<const uint4*>(&hist[pass][top]);
+      if (mine && k != 0xffffffffu) atomicAdd(&h0[(k >> shift) & digits], 1u);
+      if (safe && lane == 0) atomicAdd(&h0[digits], (uint32_t)__popc(safe));
+    };
+    const int end = lo + ((hi - lo + 31) & ~31);  // (whole warps)
+    if (pass == 0) {
+      constexpr int U = 4;  // loads in flight
+      for (int j0 = lo + tid; j0 < end; j0 += U * kThreads) {
+        float wv[U];
+        int pv[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int j = j0 + u * kThreads;
+          wv[u] = j < hi ? w[j] : 0.f;
+          pv[u] = j < hi && pin ? pin[j] : j;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int j = j0 + u * kThreads;
+          const uint32_t k = order_key(wv[u], pv[u], a.first, newest);
+          if (j < hi && in_smem) skey[j - lo] = k;
+          // every slot below the new length starts with its own values; those
+          // of the holes are overwritten by the moves, after the last barrier
+          if (j < min(hi, m)) {
+            if (wo != w) wo[j] = wv[u];
+            if (po && po != pin) po[j] = pv[u];
+          }
+          count(k, j < hi);  // (past `end` for a whole warp: nothing)
+        }
+      }
     } else {
-      uint4 x[CS];
-#pragma unroll
-      for (int r = 0; r < CS; ++r) x[r] = peer_load4(peer_addr(&hist[pass][top], r));
-#pragma unroll
-      for (int r = 0; r < CS; ++r) {
-        h.x += x[r].x;
-        h.y += x[r].y;
-        h.z += x[r].z;
-        h.w += x[r].w;
+      for (int j = lo + tid; j < end; j += kThreads) {
+        const uint32_t k = j < hi ? key_of(j) : 0u;
+        count(k, j < hi && (k & known) == prefix);
       }
     }
+    __syncthreads();
+    // bins in falling order, four to a thread
+    const int top = kBins - 4 - 4 * tid;
+    if constexpr (CS > 1) {
+      const uint4 x = *reinterpret_cast<const uint4*>(&mine_h[top]);
+      *reinterpret_cast<uint4*>(&mine_h[top]) = make_uint4(0u, 0u, 0u, 0u);
+      if (pass == 0) cluster_wait<CS>();
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (xs[i]) {
+#pragma unroll
+          for (int r = 0; r < CS; ++r) peer_add(peer_addr(&hist[pass][top + i], r), xs[i]);
+        }
+      cluster_sync<CS>();
+    }
+    const uint4 h = *reinterpret_cast<const uint4*>(&hist[pass][top]);
     uint32_t total;
     uint32_t above = block_scan(h.x + h.y + h.z + h.w, warp_sums, &total);
     const uint32_t c[4] = {h.w, h.z, h.y, h.x};
@@ -294,10 +322,6 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a, i
       if (j < w1) {
         if (j < m && !stay && j - before < a.max_moves) mv[j - before].x = j;
         if (j >= m && stay && before - low < a.max_moves) mv[before - low].y = j;
-        if (j < m && stay) {
-          if (wo != w) wo[j] = w[j];
-          if (po && po != pin) po[j] = pin ? pin[j] : j;
-        }
       }
       kept += __popc(mk);
     }
@@ -310,50 +334,49 @@ __global__ void __launch_bounds__(kThreads) kv_evict_kernel(const EvictArgs a, i
   const int per = 32 / (2 * pieces);         // moves a warp makes side by side: 2 or 1
   const int grp = lane / (2 * pieces), x = lane % (2 * pieces);
   const int isv = x >= pieces, pc = x % pieces;
-  uint8_t* pool = isv ? a.c.v : a.c.k;
+  uint8_t* pool = (isv ? a.c.v : a.c.k) + pc * 16;
+  const int64_t row_bytes = a.c.D * es;
+  // the four-byte words of a move, a lane each: the scales (FP8: D = 128, two of
+  // K and of V), the weight, the position
+  enum { kNone, kScale, kWeight, kPosition };
+  const int role = x == 2 ? kWeight : x == 3 ? (po ? kPosition : kNone)
+                   : a.c.fp8 && pc < 2 ? kScale : kNone;
+  uint32_t* scales = reinterpret_cast<uint32_t*>(isv ? a.c.vs : a.c.ks) + pc;
   const int step = CS * kWarps * per;
   constexpr int U = 4;
   for (int i0 = ((int)rank * kWarps + wid) * per + grp; i0 < moves; i0 += U * step) {
     int2 ht[U];
-    RowAt to[U], of[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      ht[u] = i0 + u * step < moves ? __ldcg(mv + i0 + u * step) : make_int2(-1, 0);
+    // (no branches around the loads, so that all of a kind are in flight at
+    // once: a move without a place reads row 0 and slot 0, which exist)
     uint4 v[U];
-    float sc[U], wt[U];
-    int pos[U];
-    bool ok[U];
+    uint32_t word[U];
+    uint32_t fine = 0;  // moves whose pages lie in the pool
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      ht[u] = make_int2(0, 0);
-      if (i0 + u * step < moves) ht[u] = __ldcg(mv + i0 + u * step);
+      const RowAt t = cache_row(a.c, b, hk, max(ht[u].x, 0)), f = cache_row(a.c, b, hk, ht[u].y);
+      const bool ok = ht[u].x >= 0 && t.ok && f.ok;
+      fine |= (uint32_t)ok << u;
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(w) + ht[u].y;
+      if (role == kScale) src = scales + (ok ? f.srow * 2 : 0);
+      if (role == kPosition && pin) src = reinterpret_cast<const uint32_t*>(pin) + ht[u].y;
+      v[u] = *reinterpret_cast<const uint4*>(pool + (ok ? f.row : 0) * row_bytes);
+      word[u] = *src;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      to[u] = cache_row(a.c, b, hk, ht[u].x);
-      of[u] = cache_row(a.c, b, hk, ht[u].y);
-      ok[u] = i0 + u * step < moves && to[u].ok && of[u].ok;
-      if (i0 + u * step < moves && !ok[u] && x == 0 && a.status) atomicExch(a.status, 3);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (ok[u]) {
-        v[u] = *reinterpret_cast<const uint4*>(pool + of[u].row * a.c.D * es + pc * 16);
-        if (a.c.fp8 && pc < 2)
-          sc[u] = (isv ? a.c.vs : a.c.ks)[of[u].srow * 2 + pc];  // (FP8 caches: D = 128)
+      if (ht[u].x < 0) break;
+      if ((fine >> u) & 1u) {  // (the target's row again: cheaper than the registers)
+        const RowAt t = cache_row(a.c, b, hk, ht[u].x);
+        *reinterpret_cast<uint4*>(pool + t.row * row_bytes) = v[u];
+        if (role == kScale) scales[t.srow * 2] = word[u];
+      } else if (x == 0 && a.status) {
+        atomicExch(a.status, 3);
       }
-      if (i0 + u * step < moves && x == 0) {
-        wt[u] = w[ht[u].y];
-        pos[u] = pin ? pin[ht[u].y] : ht[u].y;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (ok[u]) {
-        *reinterpret_cast<uint4*>(pool + to[u].row * a.c.D * es + pc * 16) = v[u];
-        if (a.c.fp8 && pc < 2) (isv ? a.c.vs : a.c.ks)[to[u].srow * 2 + pc] = sc[u];
-      }
-      if (i0 + u * step < moves && x == 0) {
-        wo[ht[u].x] = wt[u];
-        if (po) po[ht[u].x] = pos[u];
-      }
+      if (role == kWeight) wo[ht[u].x] = __uint_as_float(word[u]);
+      if (role == kPosition) po[ht[u].x] = pin ? (int32_t)word[u] : ht[u].y;
     }
   }
 }
@@ -462,11 +485,11 @@ extern "C" fia_status fia_kv_evict(const fia_evict_params* p, void* ws, size_t w
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return FIA_ERR_CUDA;
-  // CTAs per head: while they have a few thousand slots each, as many as there
-  // is room for (four CTAs of an SM at once)
+  // CTAs per head: while they have a few thousand slots each, as many as run at
+  // once (two to an SM)
   const int64_t pairs = (int64_t)a.c.B * a.c.KVN;
   int cs = 8;
-  while (cs > 1 && (pairs * cs > 4 * sms || a.c.cap < 2048 * cs)) cs /= 2;
+  while (cs > 1 && (pairs * cs > 2 * sms || a.c.cap < 2048 * cs)) cs /= 2;
   const cudaError_t e = cs == 8   ? launch_evict<8>(a, s)
                         : cs == 4 ? launch_evict<4>(a, s)
                         : cs == 2 ? launch_evict<2>(a, s)
