@@ -1724,12 +1724,15 @@ __global__ void __launch_bounds__(256, 4) decode_combine_grouped(const DecodeArg
 // ---------------------------------------------------------------------------
 constexpr int kMaxCols = kDecodeMaxRows * 64;  // query rows x heads per KV head
 
-// L threads per key, each every L-th pair of its columns.
+// L threads per key, each 16 bytes of its columns at a time; four keys of a
+// thread in flight (with one, a long FP8 cache took 31 us for scores that lie
+// in L2).
 template <int L>
 __global__ void __launch_bounds__(256) decode_weights_kernel(const DecodeArgs a, const float* w_in,
                                                              float* w_out, int64_t stride,
                                                              int per_pair) {
-  __shared__ float nl[kMaxCols];
+  __shared__ __align__(16) float nl[kMaxCols];
+  constexpr int U = 4, KEYS = 256 / L;
   const int pair = blockIdx.x / per_pair, b = pair / a.KVN, hk = pair - b * a.KVN;
   pdl_wait();
   if (a.sched[5] != kDecodePlanMark || a.sched[6] != a.B || a.sched[7] != a.num_ctas ||
@@ -1747,26 +1750,42 @@ __global__ void __launch_bounds__(256) decode_weights_kernel(const DecodeArgs a,
   }
   __syncthreads();
   const int sub = threadIdx.x % L;
-  for (int j0 = (blockIdx.x % per_pair) * (256 / L); j0 < kl; j0 += per_pair * (256 / L)) {
-    const int j = j0 + threadIdx.x / L;
-    float w = 0.f;
-    // (the tiles that ran: the others hold no scores, and no row sees them)
-    const int t = j / kKvTile;
-    const bool ran = j < kl && ((t >= r.tile0 && t < r.tile0 + r.nwin) || t < r.ntiles - r.nwin);
-    if (ran) {
-      const float2* s = reinterpret_cast<const float2*>(
-          a.scores + (((int64_t)b * a.KVN + hk) * a.S_kv + j) * a.score_cols);
-      for (int c = 2 * sub; c < ncols; c += 2 * L) {
-        const float2 x = __ldcg(s + c / 2);
-        w += fast_exp2(x.x + nl[c]);
-        if (c + 1 < ncols) w += fast_exp2(x.y + nl[c + 1]);
-      }
+  const float* scores = a.scores + ((int64_t)b * a.KVN + hk) * a.S_kv * a.score_cols;
+  const int step = per_pair * KEYS;
+  for (int j0 = (blockIdx.x % per_pair) * KEYS + threadIdx.x / L; j0 - (int)threadIdx.x / L < kl;
+       j0 += U * step) {
+    float w[U], old[U];
+    bool ran[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u * step, t = j / kKvTile;
+      // (the tiles that ran: the others hold no scores, and no row sees them)
+      ran[u] = j < kl && ((t >= r.tile0 && t < r.tile0 + r.nwin) || t < r.ntiles - r.nwin);
+      old[u] = w_in && j < kl && sub == 0 ? w_in[(int64_t)pair * stride + j] : 0.f;
+      w[u] = 0.f;
+    }
+    for (int c = 4 * sub; c < ncols; c += 4 * L) {
+      float4 x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (ran[u])
+          x[u] = __ldcg(reinterpret_cast<const float4*>(scores + (int64_t)(j0 + u * step) * a.score_cols + c));
+      const float4 n4 = *reinterpret_cast<const float4*>(nl + c);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (ran[u]) {  // (columns past the batch's own hold nothing)
+          w[u] += fast_exp2(x[u].x + n4.x);
+          if (c + 1 < ncols) w[u] += fast_exp2(x[u].y + n4.y);
+          if (c + 2 < ncols) w[u] += fast_exp2(x[u].z + n4.z);
+          if (c + 3 < ncols) w[u] += fast_exp2(x[u].w + n4.w);
+        }
     }
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-    if (j < kl && sub == 0) {
-      const int64_t at = (int64_t)pair * stride + j;
-      w_out[at] = (w_in ? w_in[at] : 0.f) + w;
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) w[u] += __shfl_xor_sync(0xffffffffu, w[u], o);
+      const int j = j0 + u * step;
+      if (j < kl && sub == 0) w_out[(int64_t)pair * stride + j] = old[u] + w[u];
     }
   }
 }
@@ -1778,12 +1797,17 @@ cudaError_t launch_decode_weights(const DecodeArgs& a, const float* w_in, float*
                                   int64_t stride, cudaStream_t s) {
   const int pairs = a.B * a.KVN;
   if (a.S_kv == 0) return cudaSuccess;
-  const int L = a.score_cols <= 4 ? 1 : a.score_cols <= 16 ? 4 : 16;
-  const int64_t keys = 256 / L;  // per block and pass
+  int L = 1;
+  while (L < 32 && 4 * L < a.score_cols) L *= 2;
+  const int64_t keys = 4 * 256 / L;  // per block and pass
   const int per_pair = (int)std::max<int64_t>(
       1, std::min<int64_t>((a.S_kv + keys - 1) / keys, (int64_t)a.num_ctas * 8 / pairs));
-  auto kern = L == 1 ? decode_weights_kernel<1> : L == 4 ? decode_weights_kernel<4>
-                                                         : decode_weights_kernel<16>;
+  auto kern = L == 1   ? decode_weights_kernel<1>
+              : L == 2 ? decode_weights_kernel<2>
+              : L == 4 ? decode_weights_kernel<4>
+              : L == 8 ? decode_weights_kernel<8>
+              : L == 16 ? decode_weights_kernel<16>
+                        : decode_weights_kernel<32>;
   return launch_pdl(kern, dim3(pairs * per_pair), dim3(256), 0, s, a, w_in, w_out, stride,
                     per_pair);
 }

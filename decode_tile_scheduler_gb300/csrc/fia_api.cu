@@ -639,7 +639,7 @@ fia_status weights_plan(const fia_params* p, const fia_weights_params* w, Weight
   st = fia_get_plan_layout(p, &pl->lay);
   if (st != FIA_OK) return st;
   const int G = p->num_q_heads / p->num_kv_heads;
-  pl->cols = (p->max_seqlen_q * G + 1) & ~1;
+  pl->cols = (p->max_seqlen_q * G + 3) & ~3;
   pl->off = pl->off_part = pl->total = align_up(pl->lay.total_bytes);
   const int64_t pairs = (int64_t)p->batch * p->num_kv_heads;
   if (pl->lay.branch == 2) {

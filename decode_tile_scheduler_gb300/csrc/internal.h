@@ -85,7 +85,7 @@ struct DecodeArgs {
   // key weights: every score (times log2 e, -inf where masked) is kept, the
   // columns (query row, head) of a key next to each other
   float* scores;               // [B * KVN][S_kv][score_cols], or null
-  int score_cols;              // S_max * G, rounded up to even
+  int score_cols;              // S_max * G, rounded up to a multiple of 4
 };
 
 // Target number of big chunks per persistent CTA in the decode schedule.
