@@ -110,6 +110,14 @@ __device__ __forceinline__ int64_t tile_key(const PMsg& m, int j) {
   return (int64_t)(!X || j < m.nwin ? m.tile0 + j : j - m.nwin) * kKvTile;
 }
 
+// Whether the unit's j-th tile holds first tokens alone, and at most 64 of them:
+// only its first 64 keys are multiplied then (it is one tile in ten of a window
+// of 1024).
+template <bool X>
+__device__ __forceinline__ bool half_tile(const PrefillArgs& a, const PMsg& m, int j) {
+  return X && j >= m.nwin && a.first_tokens - (j - m.nwin) * kKvTile <= 64;
+}
+
 __device__ __forceinline__ void pwait(uint64_t* bar, uint32_t parity, int* err, int* abort_flag) {
   if (*reinterpret_cast<volatile int*>(abort_flag)) return;
   if (!mbar_wait(bar, parity, err)) *reinterpret_cast<volatile int*>(abort_flag) = 1;
@@ -531,18 +539,21 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const uint64_t vd0 = smem_desc_sw128(sv, 16384, 1024);
       constexpr uint64_t kTileUnits = Cfg::kTileBytes >> 4;
       const uint32_t tS = tmem + 256 * s, tO = tmem + 256 * s + 128;
-      auto issue_qk = [&](int ks) {
+      constexpr uint32_t kIdS64 = F16 ? idesc_f16(128, 64, false) : idesc_bf16(128, 64, false);
+      auto issue_qk = [&](int ks, bool half) {
         const uint64_t kd = kd0 + (uint64_t)ks * kTileUnits;
+        const uint32_t id = X && half ? kIdS64 : kIdS;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint64_t off = (uint64_t)(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
-          mma_ss(tS, qd + off, kd + off, kIdS, kk > 0);
+          mma_ss(tS, qd + off, kd + off, id, kk > 0);
         }
       };
-      auto issue_pv = [&](int vs, bool first_tile) {
+      auto issue_pv = [&](int vs, bool first_tile, bool half) {
         const uint64_t vd = vd0 + (uint64_t)vs * kTileUnits;
 #pragma unroll
         for (int kk = 0; kk < kKvTile / 16; ++kk) {
+          if (X && half && kk >= 4) break;
           const uint64_t off = (uint64_t)((kk * 2048) >> 4);
           mma_ts(tO, tS + kk * 8, vd + off, kIdO, (!first_tile || kk > 0) ? 1u : 0u);
         }
@@ -587,7 +598,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           pwait(&kfull[ks0], (kv_it / KS) & 1, a.err, misc);
           take_turn(paired);
           tc_fence_after();
-          issue_qk(ks0);
+          issue_qk(ks0, half_tile<X>(a, m, 0));
           pass_turn(paired);
           tc_commit(&sfull[s]);
           tc_commit(&kempty[ks0]);
@@ -611,8 +622,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
           take_turn(paired);
           tc_fence_after();
-          issue_pv(vs, j == 0);
-          if (j + 1 < n) issue_qk(ksn);
+          issue_pv(vs, j == 0, half_tile<X>(a, m, j));
+          if (j + 1 < n) issue_qk(ksn, half_tile<X>(a, m, j + 1));
           pass_turn(paired);
           if (j == n - 1) tc_commit(&ofull[s]);
           tc_commit(&vempty[vs]);
@@ -782,6 +793,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const uint32_t hole = __float_as_uint(NEG ? INFINITY : -INFINITY);
         // the row's 128 scores: four TMEM loads, one wait; they stay in
         // registers for the maximum and the exponentials
+        const bool half = half_tile<X>(a, m, j);
         uint32_t v[kKvTile];
 #pragma unroll
         for (int c = 0; c < kKvTile / 32; ++c)
@@ -793,9 +805,18 @@ __global__ void __launch_bounds__(kPThreads, 1)
             for (int e = 0; e < kKvTile; ++e)
               if (e < c0 || e >= c1 || ((hidden[e >> 5] >> (e & 31)) & 1u)) v[e] = hole;
           } else {
+            // hidden: [f0, c0) and [c1, 128), as bits, one test per element
 #pragma unroll
-            for (int e = 0; e < kKvTile; ++e)
-              if ((e < c0 && e >= f0) || e >= c1) v[e] = hole;
+            for (int c = 0; c < kKvTile / 32; ++c) {
+              const auto below = [&](int x) {  // bits of the columns below x
+                const int k = min(max(x - 32 * c, 0), 32);
+                return k == 32 ? 0xffffffffu : (1u << k) - 1u;
+              };
+              const uint32_t hid = (below(c0) & ~below(f0)) | ~below(c1);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (hid & (1u << e)) v[32 * c + e] = hole;
+            }
           }
         }
         // row maximum of the raw scores (minimum for a negative scale), four
@@ -849,6 +870,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const float2 sl2 = make_float2(sl, sl), nb2 = make_float2(nbase, nbase);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
+          if (X && c == 1 && half) continue;  // (no product reads the second half of P)
           uint32_t pv[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
