@@ -164,6 +164,8 @@ def lib_path() -> str:
 def lib(build_if_missing: bool = True) -> ctypes.CDLL:
     """Load libfia.so (building it first when absent and nvcc is available)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.LIB

@@ -21,9 +21,20 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it (2 us of a call
+# that takes 6), where this PyTorch has the accessor.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current_stream(device_index: int) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(device_index)
+    return torch.cuda.current_stream(device_index).cuda_stream
+
+
 def _stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return _current_stream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -240,9 +251,7 @@ class KvCache:
         return _state(t, name, dtype, self.batch, self.num_kv_heads, self.capacity, self.device)
 
     def _stream(self, stream) -> int:
-        if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        return _stream(stream)
+        return _current_stream(self.device.index) if stream is None else _stream(stream)
 
 
 class KvAppendCall:
