@@ -1650,8 +1650,9 @@ __device__ __forceinline__ bool combine_item(const DecodeArgs& a, int64_t pr, in
 }
 
 // Few chunks per unit: one thread per (item, d-pair), chunks folded in order.
+// (Block `bid` of `nb` combine blocks.)
 template <int D>
-__global__ void __launch_bounds__(256, 4) decode_combine_flat(const DecodeArgs a) {
+__device__ __forceinline__ void combine_flat(const DecodeArgs& a, int bid, int nb) {
   if (a.sched[5] != kDecodePlanMark || a.sched[6] != a.B || a.sched[7] != a.num_ctas ||
       a.sched[4] < 0 || a.sched[4] > a.B || *a.prefill_mark == kPrefillPlanMark)
     return;  // no plan of these arguments: the decode kernel has reported it
@@ -1661,7 +1662,7 @@ __global__ void __launch_bounds__(256, 4) decode_combine_flat(const DecodeArgs a
   // partials need its completion.
   const int64_t items = a.sched[4] * a.KVN * a.HG * combine_cols(a);
   const int d = 2 * (threadIdx.x % TPP);
-  int64_t pr = (int64_t)blockIdx.x * PPB + threadIdx.x / TPP;
+  int64_t pr = (int64_t)bid * PPB + threadIdx.x / TPP;
   CombineItem it;
   bool have = pr < items && combine_item(a, pr, D, &it);
   pdl_wait();  // every partial of the decode kernel is written
@@ -1671,15 +1672,19 @@ __global__ void __launch_bounds__(256, 4) decode_combine_flat(const DecodeArgs a
       fold_chunks<D>(it.base, it.kstride, d, 0, 1, it.nch, M, L, o0, o1);
       combine_store(a, it.b, it.tok, it.i, it.h, D, d, M, L, o0, o1);
     }
-    pr += (int64_t)gridDim.x * PPB;
+    pr += (int64_t)nb * PPB;
     have = pr < items && combine_item(a, pr, D, &it);
   }
+}
+template <int D>
+__global__ void __launch_bounds__(256, 4) decode_combine_flat(const DecodeArgs a) {
+  combine_flat<D>(a, blockIdx.x, gridDim.x);
 }
 
 // Many chunks per unit: one CTA per item; NGRP thread groups fold every
 // NGRP-th chunk, then group 0 folds the groups in order.
 template <int D>
-__global__ void __launch_bounds__(256, 4) decode_combine_grouped(const DecodeArgs a) {
+__device__ __forceinline__ void combine_grouped(const DecodeArgs& a, int bid, int nb) {
   if (a.sched[5] != kDecodePlanMark || a.sched[6] != a.B || a.sched[7] != a.num_ctas ||
       a.sched[4] < 0 || a.sched[4] > a.B || *a.prefill_mark == kPrefillPlanMark)
     return;  // no plan of these arguments: the decode kernel has reported it
@@ -1687,11 +1692,11 @@ __global__ void __launch_bounds__(256, 4) decode_combine_grouped(const DecodeArg
   __shared__ float4 st[NGRP][TPP];
   const int64_t items = a.sched[4] * a.KVN * a.HG * combine_cols(a);
   const int grp = threadIdx.x / TPP, t = threadIdx.x % TPP, d = 2 * t;
-  int64_t pr = blockIdx.x;
+  int64_t pr = bid;
   CombineItem it;
   bool have = pr < items && combine_item(a, pr, D, &it);  // the schedule is complete
   pdl_wait();  // every partial of the decode kernel is written
-  for (; pr < items; pr += gridDim.x, have = pr < items && combine_item(a, pr, D, &it)) {
+  for (; pr < items; pr += nb, have = pr < items && combine_item(a, pr, D, &it)) {
     if (!have) continue;  // uniform over the CTA
     float M = -INFINITY, L = 0.f, o0 = 0.f, o1 = 0.f;
     fold_chunks<D>(it.base, it.kstride, d, grp, NGRP, it.nch, M, L, o0, o1);
@@ -1714,62 +1719,135 @@ __global__ void __launch_bounds__(256, 4) decode_combine_grouped(const DecodeArg
     __syncthreads();
   }
 }
+template <int D>
+__global__ void __launch_bounds__(256, 4) decode_combine_grouped(const DecodeArgs a) {
+  combine_grouped<D>(a, blockIdx.x, gridDim.x);
+}
 
 // ---------------------------------------------------------------------------
 // key weights of a decode call: w_j = sum over its columns (query row, head) of
-// 2^(score - lse), from the scores the decode kernel kept and the lse the
-// combine finished.  Keeping 4 bytes per (key, column) costs far less than
-// forming K Q^T again would (a key is 256 bytes of K per KV head, and a GQA-4
-// step has four columns).
+// 2^(score - lse), from the scores the decode kernel kept.  Keeping 4 bytes per
+// (key, column) costs far less than forming K Q^T again would (a key is 256 bytes
+// of K per KV head, and a GQA-4 step has four columns).
+//
+// They run in the combine's launch, behind its blocks (a launch of their own
+// after it cost 4 to 6 us a step): a column's lse comes from the same partials
+// (m, l) the combine folds.
 // ---------------------------------------------------------------------------
 constexpr int kMaxCols = kDecodeMaxRows * 64;  // query rows x heads per KV head
 
-// L threads per key, each 16 bytes of its columns at a time; four keys of a
-// thread in flight (with one, a long FP8 cache took 31 us for scores that lie
-// in L2).
-template <int L>
-__global__ void __launch_bounds__(256) decode_weights_kernel(const DecodeArgs a, const float* w_in,
-                                                             float* w_out, int64_t stride,
-                                                             int per_pair) {
+// -lse (log2 units) of column c of KV head hk of batch b, for the eight lanes
+// around a lane (`sub` its place among them): the lse the decode kernel wrote
+// where the unit has one chunk, else the chunks' (m, l) folded, every eighth
+// chunk by a lane.  c = -1: no column (the lanes take part in the shuffles).
+__device__ __forceinline__ float column_nlse(const DecodeArgs& a, int b, int hk, int64_t qrow,
+                                             int qlen, int c, int sub, int D) {
+  const int cc = max(c, 0), i = cc / a.G, h = hk * a.G + cc - i * a.G;
+  const int64_t* Q = a.sched + kSchedHeader;
+  const int ha = active_groups(a, qlen), A = max(a.KVN * ha, 1);
+  const int64_t q0 = Q[b], n = Q[b + 1] - q0;
+  const bool ok = c >= 0 && q0 >= 0 && n >= A && q0 + n <= a.max_chunks && n % A == 0;
+  const int nch = ok ? (int)(n / A) : 0;  // (0: a plan of other lengths)
+  float M = -INFINITY, L = 0.f;
+  if (nch == 1) {
+    const int64_t li = a.layout == 1 ? (qrow + i) * a.QN + h : ((int64_t)b * a.QN + h) * a.S_q + i;
+    return -1.4426950408889634f * __ldcg(a.lse + li);
+  }
+  const int64_t kstride = (int64_t)A * a.GH * (D + 2);
+  const float* base = a.partials + (q0 + hk * ha + cc / a.GH) * (int64_t)a.GH * (D + 2) +
+                      (int64_t)(cc % a.GH) * (D + 2) + D;
+  for (int k0 = sub; k0 < nch; k0 += 32) {
+    float2 ml[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      ml[k] = k0 + 8 * k < nch ? __ldcg(reinterpret_cast<const float2*>(base + (k0 + 8 * k) * kstride))
+                               : make_float2(-INFINITY, 0.f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (ml[k].x == -INFINITY) continue;
+      const float Mn = fmaxf(M, ml[k].x);
+      L = L * (M == -INFINITY ? 0.f : exp2f(M - Mn)) + ml[k].y * exp2f(ml[k].x - Mn);
+      M = Mn;
+    }
+  }
+  const uint32_t lanes = 0xffu << (threadIdx.x & 24);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) {
+    const float m2 = __shfl_xor_sync(lanes, M, o), l2 = __shfl_xor_sync(lanes, L, o);
+    const float Mn = fmaxf(M, m2);
+    if (Mn != -INFINITY)
+      L = (M == -INFINITY ? 0.f : L * exp2f(M - Mn)) + (m2 == -INFINITY ? 0.f : l2 * exp2f(m2 - Mn));
+    M = Mn;
+  }
+  if (M == -INFINITY) return -INFINITY;
+  if (a.sinks) {
+    const float sk = a.sinks[h] * 1.4426950408889634f;
+    const float Mp = fmaxf(M, sk);
+    L = L * exp2f(M - Mp) + exp2f(sk - Mp);
+    M = Mp;
+  }
+  return -(M + log2f(L));
+}
+
+// 2^lg threads per key, each 16 bytes of its columns at a time; four keys of a
+// thread in flight (with one, a long FP8 cache took 31 us for scores that lie in
+// L2, against 16).
+__device__ __forceinline__ void weights_block(const DecodeArgs& a, const KeyWeightsOut& o, int bid,
+                                              int D) {
   __shared__ __align__(16) float nl[kMaxCols];
-  constexpr int U = 4, KEYS = 256 / L;
-  const int pair = blockIdx.x / per_pair, b = pair / a.KVN, hk = pair - b * a.KVN;
-  pdl_wait();
-  if (a.sched[5] != kDecodePlanMark || a.sched[6] != a.B || a.sched[7] != a.num_ctas ||
-      *a.prefill_mark == kPrefillPlanMark)
-    return;  // no plan of these arguments: the decode kernel has reported it
+  constexpr int U = 4;
+  const int L = 1 << o.lg, keys = 256 >> o.lg;
+  const int pair = bid / o.per_pair, b = pair / a.KVN, hk = pair - b * a.KVN;
   int64_t qrow, ql, kl64;
   batch_lengths(a, b, &qrow, &ql, &kl64);
   const int kl = (int)min(max(kl64, (int64_t)0), (int64_t)a.S_kv);
   const UnitInfo r = unit_from(a, b, hk * a.HG, (int)qrow, ql, kl);
   const int ncols = r.q_len * a.G;
-  for (int c = threadIdx.x; c < ncols; c += 256) {
-    const int i = c / a.G, h = hk * a.G + c - i * a.G;
-    const int64_t li = a.layout == 1 ? (qrow + i) * a.QN + h : ((int64_t)b * a.QN + h) * a.S_q + i;
-    nl[c] = -1.4426950408889634f * __ldcg(a.lse + li);
-  }
-  __syncthreads();
-  const int sub = threadIdx.x % L;
+  pdl_wait();  // the decode kernel is done
+  if (a.sched[5] != kDecodePlanMark || a.sched[6] != a.B || a.sched[7] != a.num_ctas ||
+      *a.prefill_mark == kPrefillPlanMark)
+    return;  // no plan of these arguments: the decode kernel has reported it
+  const int sub = threadIdx.x & (L - 1);
   const float* scores = a.scores + ((int64_t)b * a.KVN + hk) * a.S_kv * a.score_cols;
-  const int step = per_pair * KEYS;
-  for (int j0 = (blockIdx.x % per_pair) * KEYS + threadIdx.x / L; j0 - (int)threadIdx.x / L < kl;
-       j0 += U * step) {
-    float w[U], old[U];
-    bool ran[U];
+  const float* w_in = o.w_in ? o.w_in + (int64_t)pair * o.stride : nullptr;
+  float* w_out = o.w_out + (int64_t)pair * o.stride;
+  const int step = o.per_pair * keys, mine = threadIdx.x >> o.lg;
+  // a round's U keys: what they had, and their first 16 bytes of scores
+  float old[U];
+  float4 x[U];
+  bool ran[U];
+  auto fetch = [&](int j0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * step, t = j / kKvTile;
+      const int j = j0 + mine + u * step, t = j / kKvTile;
       // (the tiles that ran: the others hold no scores, and no row sees them)
       ran[u] = j < kl && ((t >= r.tile0 && t < r.tile0 + r.nwin) || t < r.ntiles - r.nwin);
-      old[u] = w_in && j < kl && sub == 0 ? w_in[(int64_t)pair * stride + j] : 0.f;
-      w[u] = 0.f;
+      old[u] = w_in && j < kl && sub == 0 ? w_in[j] : 0.f;
+      x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (ran[u] && 4 * sub < ncols)
+        x[u] = __ldcg(reinterpret_cast<const float4*>(scores + (int64_t)j * a.score_cols + 4 * sub));
     }
-    for (int c = 4 * sub; c < ncols; c += 4 * L) {
-      float4 x[U];
+  };
+  int j0 = (bid % o.per_pair) * keys;
+  fetch(j0);  // in flight while the columns' lse are folded
+  for (int c0 = 0; c0 < ncols; c0 += 32) {
+    const int c = c0 + (int)threadIdx.x / 8;
+    const float v = column_nlse(a, b, hk, qrow, r.q_len, c < ncols ? c : -1, threadIdx.x & 7, D);
+    if (c < ncols && (threadIdx.x & 7) == 0) nl[c] = v;
+  }
+  __syncthreads();
+  for (; j0 < kl; j0 += U * step) {
+    float w[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (ran[u])
-          x[u] = __ldcg(reinterpret_cast<const float4*>(scores + (int64_t)(j0 + u * step) * a.score_cols + c));
+    for (int u = 0; u < U; ++u) w[u] = 0.f;
+    for (int c = 4 * sub; c < ncols; c += 4 * L) {
+      if (c != 4 * sub) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (ran[u])
+            x[u] = __ldcg(reinterpret_cast<const float4*>(
+                scores + (int64_t)(j0 + mine + u * step) * a.score_cols + c));
+      }
       const float4 n4 = *reinterpret_cast<const float4*>(nl + c);
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -1781,37 +1859,34 @@ __global__ void __launch_bounds__(256) decode_weights_kernel(const DecodeArgs a,
         }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < U; ++u) w[u] += old[u];  // (lanes past the first: 0)
+    const int jn = j0 + U * step;
+    if (jn < kl) fetch(jn);
 #pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) w[u] += __shfl_xor_sync(0xffffffffu, w[u], o);
-      const int j = j0 + u * step;
-      if (j < kl && sub == 0) w_out[(int64_t)pair * stride + j] = old[u] + w[u];
+    for (int u = 0; u < U; ++u) {
+      for (int y = L >> 1; y > 0; y >>= 1) w[u] += __shfl_xor_sync(0xffffffffu, w[u], y);
+      const int j = j0 + mine + u * step;
+      if (j < kl && sub == 0) w_out[j] = w[u];
     }
+  }
+}
+
+// The first nb blocks combine, the others count weights.
+template <int D, bool GROUPED>
+__global__ void __launch_bounds__(256, 4)
+    decode_finish_kernel(const DecodeArgs a, const KeyWeightsOut o, int nb) {
+  if ((int)blockIdx.x >= nb) {
+    weights_block(a, o, (int)blockIdx.x - nb, D);
+  } else if constexpr (GROUPED) {
+    combine_grouped<D>(a, blockIdx.x, nb);
+  } else {
+    combine_flat<D>(a, blockIdx.x, nb);
   }
 }
 
 // ---------------------------------------------------------------------------
 // host launchers
 // ---------------------------------------------------------------------------
-cudaError_t launch_decode_weights(const DecodeArgs& a, const float* w_in, float* w_out,
-                                  int64_t stride, cudaStream_t s) {
-  const int pairs = a.B * a.KVN;
-  if (a.S_kv == 0) return cudaSuccess;
-  int L = 1;
-  while (L < 32 && 4 * L < a.score_cols) L *= 2;
-  const int64_t keys = 4 * 256 / L;  // per block and pass
-  const int per_pair = (int)std::max<int64_t>(
-      1, std::min<int64_t>((a.S_kv + keys - 1) / keys, (int64_t)a.num_ctas * 8 / pairs));
-  auto kern = L == 1   ? decode_weights_kernel<1>
-              : L == 2 ? decode_weights_kernel<2>
-              : L == 4 ? decode_weights_kernel<4>
-              : L == 8 ? decode_weights_kernel<8>
-              : L == 16 ? decode_weights_kernel<16>
-                        : decode_weights_kernel<32>;
-  return launch_pdl(kern, dim3(pairs * per_pair), dim3(256), 0, s, a, w_in, w_out, stride,
-                    per_pair);
-}
-
 size_t decode_smem_bytes(int D, int fp8) {
   if (fp8) return DecodeCfg<128, true>::kSmem;
   return D == 64 ? DecodeCfg<64, false>::kSmem : DecodeCfg<128, false>::kSmem;
@@ -1863,8 +1938,25 @@ static cudaError_t launch_decode_main(const DecodeArgs& a, const CUtensorMap& tk
              : launch_decode_mr<128, false, 1>(a, tk, tv, s);
 }
 
+template <int D>
+static cudaError_t launch_finish(const DecodeArgs& a, const KeyWeightsOut* w, bool grouped, int nb,
+                                 cudaStream_t s) {
+  if (!w)
+    return launch_pdl(grouped ? decode_combine_grouped<D> : decode_combine_flat<D>, dim3(nb),
+                      dim3(256), 0, s, a);
+  KeyWeightsOut o = *w;
+  const int pairs = a.B * a.KVN;
+  o.lg = 0;
+  while (o.lg < 5 && (4 << o.lg) < a.score_cols) ++o.lg;
+  const int64_t keys = 4 * (256 >> o.lg);  // per block and pass
+  o.per_pair = (int)std::max<int64_t>(
+      1, std::min<int64_t>((a.S_kv + keys - 1) / keys, (int64_t)a.num_ctas * 4 / pairs));
+  return launch_pdl(grouped ? decode_finish_kernel<D, true> : decode_finish_kernel<D, false>,
+                    dim3(nb + pairs * o.per_pair), dim3(256), 0, s, a, o, nb);
+}
+
 cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
-                          int fp8, cudaStream_t s) {
+                          int fp8, const KeyWeightsOut* w, cudaStream_t s) {
   cudaError_t e = launch_decode_main(a, tk, tv, fp8, s);
   if (e != cudaSuccess) return e;
   // The plan bounds the chunks by n*W + 6*U, so a unit has about n*W/U + 6;
@@ -1872,15 +1964,10 @@ cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& tk, const CUte
   // only, so results stay deterministic.
   const int64_t items = a.num_units * combine_cols(a);  // bound: every batch split
   const int64_t est = (int64_t)a.num_ctas * a.chunks_per_cta / a.num_units + 2 * a.small_div;
-  if (est > 16) {
-    const int grid = (int)std::min<int64_t>(items, (int64_t)a.num_ctas * 8);
-    if (a.D == 64) return launch_pdl(decode_combine_grouped<64>, dim3(grid), dim3(256), 0, s, a);
-    return launch_pdl(decode_combine_grouped<128>, dim3(grid), dim3(256), 0, s, a);
-  }
-  const int ppb = 256 / (a.D / 2);
-  const int grid = (int)std::min<int64_t>((items + ppb - 1) / ppb, (int64_t)a.num_ctas * 8);
-  if (a.D == 64) return launch_pdl(decode_combine_flat<64>, dim3(grid), dim3(256), 0, s, a);
-  return launch_pdl(decode_combine_flat<128>, dim3(grid), dim3(256), 0, s, a);
+  const bool grouped = est > 16;
+  const int ppb = grouped ? 1 : 256 / (a.D / 2);
+  const int nb = (int)std::min<int64_t>((items + ppb - 1) / ppb, (int64_t)a.num_ctas * 8);
+  return a.D == 64 ? launch_finish<64>(a, w, grouped, nb, s) : launch_finish<128>(a, w, grouped, nb, s);
 }
 
 }  // namespace fia

@@ -714,19 +714,20 @@ fia_kv_cache cache_of(const fia_params* p) {
 
 namespace {
 
-// The decode branch of an execute; with `scores`, every score is kept there.
-fia_status execute_decode(const fia_params* p, void* ws, float* scores, int cols, cudaStream_t s,
-                          DecodeArgs* a) {
+// The decode branch of an execute; with `w` also the key weights, every score
+// kept at `scores` (rows of `cols`).
+fia_status execute_decode(const fia_params* p, void* ws, cudaStream_t s,
+                          const KeyWeightsOut* w = nullptr, float* scores = nullptr, int cols = 0) {
   DecodePlan pl;
   fia_status st = decode_plan(p, &pl);
   if (st != FIA_OK) return st;
-  *a = decode_args(p, pl, ws);
-  a->scores = scores;
-  a->score_cols = cols;
+  DecodeArgs a = decode_args(p, pl, ws);
+  a.scores = scores;
+  a.score_cols = cols;
   CUtensorMap tk, tv;
-  st = kv_maps(p, a->box_rows, &tk, &tv);
+  st = kv_maps(p, a.box_rows, &tk, &tv);
   if (st != FIA_OK) return st;
-  return launch_decode(*a, tk, tv, p->kv_dtype == FIA_KV_FP8_E4M3, s) == cudaSuccess
+  return launch_decode(a, tk, tv, p->kv_dtype == FIA_KV_FP8_E4M3, w, s) == cudaSuccess
              ? FIA_OK
              : FIA_ERR_CUDA;
 }
@@ -855,8 +856,7 @@ fia_status fia_execute(const fia_params* p, void* ws, size_t ws_bytes, void* str
     }
     return launch_prefill(a, tq, tk, tv, s) == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
   }
-  DecodeArgs a;
-  return execute_decode(p, ws, nullptr, 0, s, &a);
+  return execute_decode(p, ws, s);
 }
 
 fia_status fia_run(const fia_params* p, void* ws, size_t ws_bytes, void* stream) {
@@ -888,12 +888,8 @@ fia_status fia_execute_weights(const fia_params* p, const fia_weights_params* w,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (pl.lay.branch == 1) {
     float* scores = reinterpret_cast<float*>(static_cast<char*>(ws) + pl.off);
-    DecodeArgs a;
-    st = execute_decode(p, ws, scores, pl.cols, s, &a);
-    if (st != FIA_OK) return st;
-    return launch_decode_weights(a, w->weights_in, w->weights_out, w->state_stride, s) == cudaSuccess
-               ? FIA_OK
-               : FIA_ERR_CUDA;
+    const KeyWeightsOut o = {w->weights_in, w->weights_out, w->state_stride, 0, 0};
+    return execute_decode(p, ws, s, &o, scores, pl.cols);
   }
   st = fia_execute(p, ws, ws_bytes, stream);
   if (st != FIA_OK) return st;

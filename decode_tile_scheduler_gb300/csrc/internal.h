@@ -175,8 +175,17 @@ struct SparseArgs {
 
 // host launchers (return cudaSuccess or the launch error)
 cudaError_t launch_decode_schedule(const DecodeArgs& a, cudaStream_t s);
+// Where a decode call's key weights come from and go to (lg and per_pair: the
+// launch's own).
+struct KeyWeightsOut {
+  const float* w_in;  // null: zeros
+  float* w_out;
+  int64_t stride;
+  int lg, per_pair;   // 2^lg threads per key, blocks per (sequence, KV head)
+};
+// The decode kernel and its combine; with `w` (and a.scores) the key weights too.
 cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
-                          int fp8, cudaStream_t s);
+                          int fp8, const KeyWeightsOut* w, cudaStream_t s);
 size_t decode_smem_bytes(int D, int fp8);
 
 cudaError_t launch_prefill_schedule(const PrefillArgs& a, cudaStream_t s);
@@ -244,9 +253,6 @@ cudaError_t launch_key_weights(const WeightsArgs& a, const fia_kv_cache& cache,
                                const CUtensorMap& tq, const CUtensorMap& tk, cudaStream_t s);
 // w_out = w_in plus the parts (none without a plan).
 cudaError_t launch_key_weights_fold(const WeightsArgs& a, cudaStream_t s);
-// The same for a decode call whose scores were kept (decode.cu).
-cudaError_t launch_decode_weights(const DecodeArgs& a, const float* w_in, float* w_out,
-                                  int64_t stride, cudaStream_t s);
 
 cudaError_t launch_sparse_metadata(const SparseArgs& a, int32_t* md, cudaStream_t s);
 cudaError_t launch_sparse(const SparseArgs& a, const int32_t* md, cudaStream_t s);
