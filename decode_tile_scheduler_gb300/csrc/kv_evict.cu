@@ -54,6 +54,8 @@ __device__ __forceinline__ uint32_t order_key(float w, int pos, int first, int64
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kRanked = kThreads;  // keys with one first digit ranked directly, at most
+constexpr int kListedMax = 2048;   // moves listed in shared memory, at most
 constexpr int kStagedMax = 40 * 1024;  // keys of a slice kept in shared memory, at most
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -119,8 +121,10 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_sums, 
 }
 
 template <int CS>
-__global__ void __launch_bounds__(kThreads, 2) kv_evict_kernel(const EvictArgs a, int staged) {
+__global__ void __launch_bounds__(kThreads, 2) kv_evict_kernel(const EvictArgs a, int staged,
+                                                                int listed) {
   extern __shared__ uint32_t skey[];  // the slice's keys, with `staged` places
+  int2* slist = reinterpret_cast<int2*>(skey + staged);  // CS = 1: the moves, with `listed` places
   // this CTA's histogram of a pass, and each pass's over the cluster (alone: its own)
   __shared__ __align__(16) uint32_t mine_h[CS > 1 ? kBins : 4];
   __shared__ __align__(16) uint32_t hist[3][kBins];
@@ -155,6 +159,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_evict_kernel(const EvictArgs a
   for (int i = tid; i < 3 * kBins; i += kThreads) (&hist[0][0])[i] = 0u;
   if (CS > 1)
     for (int i = tid; i < kBins; i += kThreads) mine_h[i] = 0u;
+  if (tid == 0) totals[0] = 0;
   __syncthreads();
   cluster_arrive<CS>();  // (peers may add to the joined histograms once all are clear)
   uint32_t prefix = 0, known = 0, left = (uint32_t)a.budget;
@@ -237,6 +242,33 @@ __global__ void __launch_bounds__(kThreads, 2) kv_evict_kernel(const EvictArgs a
     left = found[1];
     ties = left != found[2];
     if (!ties) break;  // every key with these digits stays
+    if (CS == 1 && pass == 0 && in_smem && found[2] <= kRanked && found[0] != digits) {
+      // few keys share the first digit: rank them among themselves, each by a
+      // thread, instead of two more passes and a count of ties (the newest keys
+      // often have equal weights, of no query yet).  Those that stay become the
+      // largest key, the others the smallest.
+      const int few = (int)found[2];
+      uint2* cand = reinterpret_cast<uint2*>(&hist[1][0]);
+      for (int j = lo + tid; j < hi; j += kThreads) {
+        const uint32_t k = skey[j - lo];
+        if ((k & known) == prefix) cand[atomicAdd(&totals[0], 1)] = make_uint2(k, (uint32_t)j);
+      }
+      __syncthreads();
+      if (tid < few) {
+        const uint2 mine = cand[tid];
+        uint32_t better = 0;
+#pragma unroll 8
+        for (int i = 0; i < few; ++i) {
+          const uint2 o = cand[i];
+          better += o.x > mine.x || (o.x == mine.x && o.y < mine.y);
+        }
+        skey[(int)mine.y - lo] = better < left ? 0xffffffffu : 0u;
+      }
+      __syncthreads();
+      prefix += 1u << shift;
+      ties = false;
+      break;
+    }
   }
   // (with ties the threshold is a whole key, and `left` of its keys stay)
 
@@ -311,7 +343,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv_evict_kernel(const EvictArgs a
   const int moves = min(m - low, a.max_moves);
   // a hole's rank is its slot less the kept slots before it, a tail's the kept
   // slots before it less those below the budget
-  int2* mv = a.moves + (int64_t)pair * a.max_moves;
+  const bool in_list = CS == 1 && listed > 0;
+  int2* mv = in_list ? slist : a.moves + (int64_t)pair * a.max_moves;
   {
     int eq = eq_base;
     for (int j0 = w0; j0 < w1; j0 += 32) {
@@ -348,7 +381,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv_evict_kernel(const EvictArgs a
     int2 ht[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      ht[u] = i0 + u * step < moves ? __ldcg(mv + i0 + u * step) : make_int2(-1, 0);
+      ht[u] = i0 + u * step >= moves ? make_int2(-1, 0)
+              : in_list              ? slist[i0 + u * step]
+                                     : __ldcg(mv + i0 + u * step);
     // (no branches around the loads, so that all of a kind are in flight at
     // once: a move without a place reads row 0 and slot 0, which exist)
     uint4 v[U];
@@ -386,20 +421,22 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
   auto kern = kv_evict_kernel<CS>;
   const int slice = (((a.c.cap + CS - 1) / CS) + 31) & ~31;
   const int staged = slice <= kStagedMax ? slice : 0;
+  const int listed = CS == 1 && a.max_moves <= kListedMax ? a.max_moves : 0;
   static std::atomic<uint64_t> done_mask[4];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (!(done_mask[(dev >> 6) & 3].load() & bit)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * kStagedMax);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             4 * kStagedMax + 8 * kListedMax);
     if (e != cudaSuccess) return e;
     done_mask[(dev >> 6) & 3].fetch_or(bit);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.c.B * a.c.KVN * CS);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = 4 * (size_t)staged;
+  cfg.dynamicSmemBytes = 4 * (size_t)staged + 8 * (size_t)listed;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -407,7 +444,7 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CS > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, a, staged);
+  return cudaLaunchKernelEx(&cfg, kern, a, staged, listed);
 }
 
 // At most min(budget, capacity - budget) keys of a head move.
