@@ -181,6 +181,8 @@ def _state(t: Optional[torch.Tensor], name: str, dtype, batch: int, heads: int, 
         row = max(int(t.shape[2]), capacity)
     if (t.shape[2] > 1 and t.stride(2) != 1) or (batch > 1 and t.stride(0) != heads * row):
         raise ValueError(f"{name}: rows of unit stride, evenly spaced")
+    if row < capacity:
+        raise ValueError(f"{name}: its rows overlap")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the cache on {device}")
     return _ptr(t), row
@@ -315,6 +317,8 @@ class KvAppendCall:
                 step = int(t.stride(0))
             elif t.stride(0) != n * step:
                 raise ValueError(f"{name}: tokens must be evenly spaced")
+        if step < heads * dim:
+            raise ValueError(f"{name}: its tokens overlap")
         return step
 
     def run(self, stream=None):

@@ -1851,11 +1851,13 @@ __device__ __forceinline__ void weights_block(const DecodeArgs& a, const KeyWeig
       const float4 n4 = *reinterpret_cast<const float4*>(nl + c);
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        if (ran[u]) {  // (columns past the batch's own hold nothing)
-          w[u] += fast_exp2(x[u].x + n4.x);
-          if (c + 1 < ncols) w[u] += fast_exp2(x[u].y + n4.y);
-          if (c + 2 < ncols) w[u] += fast_exp2(x[u].z + n4.z);
-          if (c + 3 < ncols) w[u] += fast_exp2(x[u].w + n4.w);
+        if (ran[u]) {
+          // columns past the batch's own hold nothing; a hidden pair (-inf) adds
+          // nothing, whatever its row's lse (a NaN query has a NaN one)
+          const float xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w}, ns[4] = {n4.x, n4.y, n4.z, n4.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (c + k < ncols && xs[k] != -INFINITY) w[u] += fast_exp2(xs[k] + ns[k]);
         }
     }
 #pragma unroll

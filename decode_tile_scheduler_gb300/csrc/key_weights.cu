@@ -59,9 +59,9 @@ struct WeightsCfg {
   static constexpr int kOffLse = kOffQ + kQStages * kTile;
   static constexpr int kLseStages = 3;
   static constexpr int kOffBar = kOffLse + kLseStages * 128 * 4;
-  // mfull[2] mempty[2] kfull[2] kempty[2] kconv qfull[QS] qempty[QS] lfull[LS]
+  // mfull[2] mempty[2] kfull[2] kempty[2] kconv[2] qfull[QS] qempty[QS] lfull[LS]
   // lempty[LS] sfull[2][2] sempty[2][2] drain
-  static constexpr int kBars = 9 + 2 * kQStages + 2 * kLseStages + 8 + 1;
+  static constexpr int kBars = 10 + 2 * kQStages + 2 * kLseStages + 8 + 1;
   static constexpr int kOffMsg = kOffBar + 8 * kBars;
   static constexpr int kOffMisc = kOffMsg + 2 * 64;
   static constexpr int kSmem = kOffMisc + 16 + 1024;
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
   uint64_t* kfull = mempty + 2;
   uint64_t* kempty = kfull + 2;
   uint64_t* kconv = kempty + 2;
-  uint64_t* qfull = kconv + 1;
+  uint64_t* qfull = kconv + 2;
   uint64_t* qempty = qfull + QS;
   uint64_t* lfull = qempty + QS;
   uint64_t* lempty = lfull + LS;
@@ -187,7 +187,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
       mbar_init(&kfull[s], 1);
       mbar_init(&kempty[s], FP8 ? 2 : 1);  // codes: the warpgroups; bf16: the MMA's commit
     }
-    mbar_init(kconv, 2);
+    // (a barrier per warpgroup, and only units with keys of its own count: a
+    // warpgroup without keys runs ahead of the other)
+    mbar_init(&kconv[0], 1);
+    mbar_init(&kconv[1], 1);
     for (int s = 0; s < QS; ++s) {
       mbar_init(&qfull[s], 1);
       mbar_init(&qempty[s], 1);
@@ -318,7 +321,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
       // sequence of the range's first step: window, then the prefix inside it
       int64_t before = 0;
       int w0 = 0;
-      while (before + win_sum[w0] <= at) before += win_sum[w0++];
+      while (w0 < nwin - 1 && before + win_sum[w0] <= at) before += win_sum[w0++];
       const int nb = min(kSeqWindow, a.B - w0 * kSeqWindow);
       for (int base = 0; base < nb; base += 32) {
         const int64_t n = base + lane < nb ? seq_sum[base + lane] : 0;
@@ -445,6 +448,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
       constexpr uint64_t kUnits = Cfg::kTile >> 4;
       int ucnt = 0, n = 0;
       int sn[2] = {0, 0};  // S buffers filled per warpgroup
+      int kc[2] = {0, 0};  // (FP8) K tiles taken per warpgroup
       while (true) {
         const int ms = ucnt & 1;
         wait_or_abort(&mfull[ms], (ucnt >> 1) & 1, a.err, misc);
@@ -452,9 +456,15 @@ __global__ void __launch_bounds__(kWThreads, 1)
         mbar_arrive(&mempty[ms]);
         if (*abort_flag || m.done) break;
         const int ks = FP8 ? 0 : ucnt % Cfg::kKStages;
-        if constexpr (FP8) wait_or_abort(kconv, ucnt & 1, a.err, misc);
-        else wait_or_abort(&kfull[ks], (ucnt / Cfg::kKStages) & 1, a.err, misc);
         const int nwg = m.j0 + kKvTile < m.kl ? 2 : 1;
+        if constexpr (FP8) {
+          for (int w = 0; w < nwg; ++w) {
+            wait_or_abort(&kconv[w], kc[w] & 1, a.err, misc);
+            ++kc[w];
+          }
+        } else {
+          wait_or_abort(&kfull[ks], (ucnt / Cfg::kKStages) & 1, a.err, misc);
+        }
         for (int s = m.s0; s < m.s1; ++s, ++n) {
           const int qs = n % QS;
           wait_or_abort(&qfull[qs], (n / QS) & 1, a.err, misc);
@@ -585,7 +595,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
         named_bar_sync(2 + w, 128);
         if (row == 0) {
           mbar_arrive(&kempty[ks]);
-          mbar_arrive(kconv);
+          if (active) mbar_arrive(&kconv[w]);
         }
       }
       int lo, hi;

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
       if (__ldg(a.cu + mid) <= t) lo = mid; else hi = mid;
     }
     b = lo;
-    back = (int)(t - __ldg(a.cu + b + 1));
+    back = t >= __ldg(a.cu + b) ? (int)(t - __ldg(a.cu + b + 1)) : 0;  // (0: no row's place)
   } else {
     b = (int)(t / a.S);
     back = (int)(t - (int64_t)(b + 1) * a.S);

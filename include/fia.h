@@ -381,8 +381,11 @@ fia_status fia_kv_append(const fia_append_params *p, void *stream);
  * weights_out itself; other overlaps are not allowed.  p->lse is required.
  * The workspace is fia_get_weights_workspace_size's, larger than
  * fia_get_workspace_size's; fia_plan on it, then fia_execute_weights any
- * number of times, or fia_run_weights for both.  Error word as for
- * fia_execute; with 2 in it weights_out is not written. */
+ * number of times, or fia_run_weights for both.  It grows with the cache's
+ * capacity: up to 16 query rows, 4 bytes per (slot, KV head, query row, head of
+ * the group), otherwise 64 bytes per (slot, KV head).  Calls that may run at the
+ * same time (other streams, captured graphs) need workspaces of their own.
+ * Error word as for fia_execute; with 2 in it weights_out is not written. */
 typedef struct fia_weights_params {
     const float *weights_in;  /* fp32 [B, KV_N, stride] or NULL                */
     float *weights_out;       /* fp32 [B, KV_N, stride]                        */
@@ -421,8 +424,9 @@ fia_status fia_run_weights(const fia_params *p, const fia_weights_params *w, voi
  *    move whose page id lies outside [0, num_blocks) is left out (its weight
  *    and position still move) and *status (nullable, cleared by the caller)
  *    becomes 3.  Sequences must not share pages that hold moved rows.
- *  - The workspace size depends on scalars only; its contents do not outlive
- *    the call.  Deterministic. */
+ *  - The workspace (8-byte aligned) has a size that depends on scalars only;
+ *    its contents do not outlive the call, and calls that may run at the same
+ *    time need workspaces of their own.  Deterministic. */
 typedef struct fia_evict_params {
     fia_kv_cache cache;
     const int32_t *seqused_kv;    /* int32 [B]                                 */

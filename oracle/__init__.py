@@ -172,6 +172,8 @@ def _fia_struct(p):
         "sinks": _np(p.sinks, np.float32),
         "mask": _np(getattr(p, "atten_mask", None)),
     }
+    if getattr(p, "first_tokens", 0):
+        raise NotImplementedError("the oracle's band has no first tokens (tests/bounded.py has)")
     mask = getattr(p, "atten_mask", None)
     if mask is not None:
         mrs, mbs = int(mask.shape[2]), (0 if mask.shape[0] == 1 else int(mask.shape[1] * mask.shape[2]))

@@ -84,7 +84,8 @@ def fia(p):
         if p.mask_mode in (2, 3):
             vis = j <= pos
         elif p.mask_mode == 4:
-            vis = (j >= pos - p.pre_tokens) & (j <= pos + p.next_tokens)
+            vis = ((j >= pos - p.pre_tokens) | (j < getattr(p, "first_tokens", 0))) \
+                & (j <= pos + p.next_tokens)
         else:
             vis = np.ones((ql, kl), dtype=bool)
         mask = getattr(p, "atten_mask", None)

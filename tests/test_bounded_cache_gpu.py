@@ -707,3 +707,156 @@ def test_a_captured_step_replays():
         torch.cuda.synchronize()
         for x, y in zip(state + [att.out, att.lse], want):
             assert torch.equal(x, y)
+
+
+# ----------------------------------------------------------------------------
+# large offsets, many sequences, other streams, hidden NaNs
+# ----------------------------------------------------------------------------
+
+def test_pages_past_two_to_the_31_elements():
+    """append and evict on pages whose elements lie past 2^31 in the pool."""
+    KVN, D, block = 8, 128, 128
+    nb = (1 << 31) // (block * KVN * D) + 20
+    k, v = (torch.empty(nb, block, KVN, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    table = torch.tensor([[nb - 1, nb - 3]], dtype=torch.int32, device=DEV)
+    cache = fia.KvCache(k, v, table)
+    n = 200
+    new = [torch.randn(1, n, KVN, D, device=DEV).to(torch.bfloat16) for _ in range(2)]
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    fia.kv_append(cache, *new, lens)
+    for x, y in ((k, new[0]), (v, new[1])):
+        got = torch.cat([x[nb - 1], x[nb - 3]])[:n]
+        assert torch.equal(got, y[0])
+    w = torch.arange(256, device=DEV).float().expand(1, KVN, 256).contiguous()
+    n_out, _, pos = fia.kv_evict(cache, lens, w, budget=150)
+    assert int(n_out) == 150
+    for x, y in ((k, new[0]), (v, new[1])):
+        got = torch.cat([x[nb - 1], x[nb - 3]])[:150]
+        for h in (0, KVN - 1):
+            assert torch.equal(got[:, h], y[0, pos[0, h, :150].long(), h])
+    p = fi.make_fia(B=1, QN=8, KVN=KVN, D=D, q_lens=[1], kv_lens=[n], device=DEV, seed=31,
+                    mask_mode=3)
+    p.k_cache, p.v_cache, p.block_table, p.num_blocks = k, v, table, nb
+    p.seqused_kv, p.kv_lens = torch.tensor([150], dtype=torch.int32, device=DEV), [150]
+    out, lse, wt = fia.KeyWeightsCall(p).run()
+    small = fi.make_fia(B=1, QN=8, KVN=KVN, D=D, q_lens=[1], kv_lens=[150], device=DEV, seed=31,
+                        mask_mode=3)
+    small.q = p.q
+    for i, page in enumerate((nb - 1, nb - 3)):
+        small.k_cache[int(small.block_table[0, i])] = k[page]
+        small.v_cache[int(small.block_table[0, i])] = v[page]
+    bounded.check_attention(small, out, lse, wt)
+
+
+def test_weights_workspace_past_two_to_the_31_elements():
+    """Scores of the last (sequence, KV head) of a batch with a wide table lie past
+    2^31 elements of the workspace."""
+    B, KVN, rows, G = 17, 8, 16, 8
+    p = fi.make_fia(B=B, QN=KVN * G, KVN=KVN, D=128, q_lens=[rows] * B, kv_lens=[40] * (B - 1) + [150],
+                    block_size=128, max_blocks=1000, device=DEV, seed=32, mask_mode=3)
+    assert B * KVN * 128000 * rows * G > 1 << 31
+    call = fia.KeyWeightsCall(p)
+    out, lse, w = call.run()
+    bounded.check_attention(p, out, lse, w)
+
+
+@pytest.mark.parametrize("kv_dtype,D", [(fi.KV_BF16, 64), (fi.KV_FP8_E4M3, 128)])
+def test_weights_prefill_of_many_sequences(kv_dtype, D):
+    """More sequences than one window of the step list holds, some without rows or
+    keys."""
+    g = torch.Generator().manual_seed(33)
+    B = 4300
+    q = torch.randint(0, 20, (B,), generator=g)
+    q[5:4100] *= (torch.rand(4095, generator=g) < 0.2).long()
+    q[-1], q[7] = 200, 17
+    kv = q + torch.randint(0, 30, (B,), generator=g) * (q > 0)
+    kv[100:120] = 0
+    p = fi.make_fia(B=B, QN=2, KVN=1, D=D, q_lens=q.tolist(), kv_lens=kv.tolist(), block_size=32,
+                    layout=fi.LAYOUT_TND, kv_dtype=kv_dtype, device=DEV, seed=34, mask_mode=3)
+    _check_weights(p)
+
+
+def test_weights_prefill_of_long_prompts_cut_over_many_ctas():
+    _check_weights(fi.make_fia(B=1, QN=4, KVN=1, D=128, q_lens=[3000], kv_lens=[4100],
+                               layout=fi.LAYOUT_TND, block_size=128, device=DEV, seed=35, mask_mode=3))
+    p = fi.make_fia(B=2, QN=16, KVN=2, D=64, q_lens=[1500, 130], kv_lens=[1500, 2600],
+                    layout=fi.LAYOUT_TND, block_size=64, device=DEV, seed=36,
+                    mask_mode=fi.MASK_BAND, pre_tokens=400, first_tokens=3)
+    _check_weights(p)
+
+
+@pytest.mark.parametrize("rows", [3, 40])
+def test_a_nan_row_reaches_only_the_keys_it_sees(rows):
+    """A query row of NaN (and a key of NaN) leave every other key's weight alone."""
+    p = fi.make_fia(B=1, QN=4, KVN=2, D=128, q_lens=[rows], kv_lens=[300], layout=fi.LAYOUT_TND,
+                    device=DEV, seed=37, mask_mode=fi.MASK_BAND, pre_tokens=20, next_tokens=0)
+    clean = fia.KeyWeightsCall(p).run()[2].clone()
+    p.q[0] = float("nan")  # row 0 sees keys 300 - rows - 20 .. 300 - rows
+    got = fia.KeyWeightsCall(p).run()[2]
+    first = 300 - rows
+    seen = torch.zeros(300, dtype=torch.bool, device=DEV)
+    seen[first - 20:first + 1] = True
+    assert torch.isnan(got[0, :, :300][:, seen]).all()
+    assert torch.equal(got[0, :, :300][:, ~seen], clean[0, :, :300][:, ~seen])
+
+
+def test_calls_on_another_stream_with_slow_producers():
+    """Inputs written on a side stream just before the calls there."""
+    B, KVN, D = 2, 2, 128
+    cache, t = _empty_cache(B, KVN, D, 4, 32, False, 0)
+    side = torch.cuda.Stream()
+    k, v = (torch.zeros(B, 3, KVN, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    lens = torch.zeros(B, dtype=torch.int32, device=DEV)
+    w = torch.zeros(B, KVN, cache.capacity, device=DEV)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+        k.normal_(), v.normal_()
+        lens.fill_(100)
+        w.uniform_()
+        fia.kv_append(cache, k, v, lens, weights=w)
+        n, wo, po = fia.kv_evict(cache, lens, w, budget=64, recent_tokens=10)
+    side.synchronize()
+    assert n.tolist() == [64, 64]
+    for b in range(B):
+        for h in range(KVN):
+            kept = bounded.keep_of(w[b, h].cpu().numpy(), None, 100, 64, 0, 10, 100)
+            assert sorted(po[b, h, :64].tolist()) == list(np.nonzero(kept)[0])
+            j = 97 + int(torch.tensor(0))  # a new row, newest: kept, moved into a hole
+            slot = po[b, h, :64].tolist().index(j)
+            page, row = int(t[4][b, slot // 32]), slot % 32
+            assert torch.equal(t[0][page, row, h], k[b, 0, h])
+
+
+def test_python_calls_refuse_tensors_that_do_not_fit():
+    cache, t = _empty_cache(2, 2, 128, 2, 32, False, 0)
+    lens = torch.tensor([3, 4], dtype=torch.int32, device=DEV)
+    k = torch.zeros(2, 1, 2, 128, dtype=torch.bfloat16, device=DEV)
+    w = torch.zeros(2, 2, 64, device=DEV)
+    bad = [
+        lambda: fia.KvAppendCall(cache, k.float(), k.float(), lens),
+        lambda: fia.KvAppendCall(cache, k[:1], k[:1], lens),
+        lambda: fia.KvAppendCall(cache, k, k, lens.long()),
+        lambda: fia.KvAppendCall(cache, k, k, lens[:1]),
+        lambda: fia.KvAppendCall(cache, k, k, lens, weights=w[:, :, :63]),
+        lambda: fia.KvAppendCall(cache, k, k, lens, weights=w[:, :, :1].expand(2, 2, 64)),
+        lambda: fia.KvAppendCall(cache, k, k, lens, weights=w[:1, :1].expand(2, 2, 64)),
+        lambda: fia.KvAppendCall(cache, k[:, :, :, ::2], k[:, :, :, ::2], lens),
+        lambda: fia.KvAppendCall(cache, k[:, :1].expand(2, 5, 2, 128), k[:, :1].expand(2, 5, 2, 128),
+                                 lens),
+        lambda: fia.KvAppendCall(cache, k, k, lens, status=torch.zeros(1, device=DEV)),
+        lambda: fia.KvEvictCall(cache, lens, w.double(), budget=8),
+        lambda: fia.KvEvictCall(cache, lens, w, budget=8, positions=w),
+        lambda: fia.KvEvictCall(cache, lens, w, budget=8, weights_out=torch.zeros(2, 2, 70, device=DEV)),
+        lambda: fia.KvEvictCall(cache, None, w, budget=8),
+        lambda: fia.KvCache(t[0], t[1], t[4].long()),
+        lambda: fia.KvCache(t[0], t[1], t[4], k_scale=w),
+    ]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+    for f in (lambda: fia.KvEvictCall(cache, lens, w, budget=65),
+              lambda: fia.KvEvictCall(cache, lens, w, budget=8, recent_tokens=9),
+              lambda: fia.KvEvictCall(cache, lens, w, budget=8, seqused_out=lens)):
+        with pytest.raises(fia.FiaError):
+            f()
