@@ -18,8 +18,8 @@
 // rows the slowest had 20 steps where the mean was 16.)  A unit's two K tiles stay
 // in shared memory while the Q tiles stream past them; each K tile belongs to one
 // epilogue warpgroup, so a Q tile in shared memory serves 2 x 128 keys (with one K
-// tile the Q reads from L2 alone would be 32 KB per 1024 cycles of exponentials,
-// on 152 SMs about the L2's rate).  The sums of a unit's parts go to rows of the
+// tile the reads of Q from L2 alone would be 32 KB per 512 cycles of products, on
+// 152 SMs above the L2's rate).  The sums of a unit's parts go to rows of the
 // workspace, and key_weights_fold_kernel adds them in order: no atomics, the same
 // bits every time.
 //
@@ -27,8 +27,16 @@
 // to bf16 without their scales, the two 64-element halves of D accumulate apart,
 // and a key's two scales multiply the two sums of its lane: no rounding of K.
 //
-// Bound: one ex2 per (key, row, head) on the MUFU, 16 a clock per SM, i.e. 1024
-// cycles per 128 x 128 tile, against 512 on the tensor core (D = 128).
+// Bound: a step of 256 keys x 128 rows is 1024 cycles on the tensor core (D = 128)
+// and as many on the MUFU (an ex2 per key, row and head), and takes 1.2 to 1.4 us,
+// 2300 to 2700 cycles: one prompt of 8192 rows with 32 heads 312 us for 222 steps
+// a CTA, 44 % of the tensor core's and of the MUFU's cycles.  The issue of a step's
+// products alone then takes 0.88 us, where they run in 0.53 us by themselves:
+// products and reads of their results share TMEM and shared memory.  Not kept, of
+// the same time or slower (312 us here): both K tiles to each of two warpgroups,
+// 64 rows each, so that an lse is read once for two keys (309 us; FP8 433 -> 478);
+// four warpgroups of a tile and 64 rows each (360 us), or of both tiles and 32
+// rows each (323 us).
 #include <algorithm>
 #include <atomic>
 
