@@ -95,7 +95,9 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
   const int t = inside ? (int)row : 0;
   const int hk = (int)(in_row >> two);
   const int part = (int)(((in_row & two) << 3) | (threadIdx.x & 7));
-  int b, back;  // sequence, and the row's place counted from the sequence's end (negative)
+  // sequence, and the row's place counted from the sequence's end (negative; else
+  // the row is no sequence's, and nothing is done with it)
+  int b, back;
   if (a.cu) {
     int lo = 0, hi = a.c.B;  // largest b with cu[b] <= t
     while (hi - lo > 1) {
@@ -103,7 +105,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
       if (__ldg(a.cu + mid) <= t) lo = mid; else hi = mid;
     }
     b = lo;
-    back = t >= __ldg(a.cu + b) ? t - __ldg(a.cu + b + 1) : 0;  // (0: no row's place)
+    back = t >= __ldg(a.cu + b) ? t - __ldg(a.cu + b + 1) : 0;
   } else {
     b = t / a.S;
     back = t - (b + 1) * a.S;
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
   RowAt r = {0, 0, false};
   if (ok) r = cache_row(a.c, b, hk, (int)slot);
   ok = ok && r.ok;
-  if (inside && !ok && part == 0 && a.status) atomicExch(a.status, 3);
+  if (inside && back < 0 && !ok && part == 0 && a.status) atomicExch(a.status, 3);
   const int64_t src = (int64_t)hk * a.c.D + part * E;
   const uint4* ks = reinterpret_cast<const uint4*>(a.k_new + (int64_t)t * a.k_stride + src);
   const uint4* vs = reinterpret_cast<const uint4*>(a.v_new + (int64_t)t * a.v_stride + src);

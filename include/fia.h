@@ -346,7 +346,9 @@ typedef struct fia_kv_cache {
  *    (nullable, a device int32 that the caller has cleared) becomes 3.
  *  - Nothing else is written.  Two rows with the same place (a page listed
  *    twice) leave either's values.  One launch, no workspace.
- * cu_seqlens_q must be non-decreasing from 0 to total_q (TND). */
+ *  - cu_seqlens_q (TND) is non-decreasing.  Rows below cu_seqlens_q[0] or at and
+ *    past cu_seqlens_q[B] (a padded batch) belong to no sequence: they are left
+ *    out, and do not count as errors. */
 typedef struct fia_append_params {
     fia_kv_cache cache;
     int32_t layout;           /* FIA_LAYOUT_*: k_new, v_new [B,S,KV_N,D] or     */
@@ -385,7 +387,8 @@ fia_status fia_kv_append(const fia_append_params *p, void *stream);
  * capacity: up to 16 query rows, 4 bytes per (slot, KV head, query row, head of
  * the group), otherwise 64 bytes per (slot, KV head).  Calls that may run at the
  * same time (other streams, captured graphs) need workspaces of their own.
- * Error word as for fia_execute; with 2 in it weights_out is not written. */
+ * Error word as for fia_execute: weights_out is not written where nothing ran,
+ * and undefined for the sequences of a plan entry that ran as empty. */
 typedef struct fia_weights_params {
     const float *weights_in;  /* fp32 [B, KV_N, stride] or NULL                */
     float *weights_out;       /* fp32 [B, KV_N, stride]                        */

@@ -149,6 +149,27 @@ def test_append_leaves_out_rows_without_a_place():
     assert int((pos != 0).sum()) == KVN  # slot 31's; slot 0 is position 0
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_append_of_a_padded_batch_is_no_error(fp8):
+    """Rows before the first sequence and behind the last are nobody's."""
+    B, KVN, D, block = 2, 2, 128, 32
+    cache, t = _empty_cache(B, KVN, D, 2, block, fp8, 0)
+    clean, t2 = _empty_cache(B, KVN, D, 2, block, fp8, 0)
+    new = torch.randn(40, KVN, D, device=DEV).to(torch.bfloat16)
+    lens = torch.tensor([5, 40], dtype=torch.int32, device=DEV)
+    cu = torch.tensor([2, 7, 11], dtype=torch.int32, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    w = torch.full((B, KVN, 64), 3.0, device=DEV)
+    fia.kv_append(cache, new, new, lens, cu_seqlens_q=cu, status=status, weights=w)
+    fia.kv_append(clean, new[2:11].contiguous(), new[2:11].contiguous(), lens, cu_seqlens_q=cu - 2)
+    assert int(status) == 0
+    for x, y in zip(t, t2):
+        assert x is None or torch.equal(x, y)
+    want = torch.full((B, KVN, 64), 3.0)
+    want[0, :, :5], want[1, :, 36:40] = 0, 0
+    assert torch.equal(w.cpu(), want)
+
+
 # ----------------------------------------------------------------------------
 # window attention with first tokens
 # ----------------------------------------------------------------------------
