@@ -1315,14 +1315,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // row length are even: 8-byte stores); eight lanes' rows of a quad
         // column are neighbours, so a warp writes whole sectors
         const int64_t base = ((int64_t)r.b * a.KVN + r.hk) * a.S_kv;
+        const int end = min(kvl, a.S_kv);  // (the scores have no room past the capacity)
 #pragma unroll
         for (int ng = 0; ng < NG; ++ng) {
           const int cl = ng * 8 + 2 * q4;
           if (cl < r.ncols) {
-            if (jg0 < kvl)
+            if (jg0 < end)
               *reinterpret_cast<float2*>(a.scores + (base + jg0) * a.score_cols + r.c0 + cl) =
                   make_float2(xs[ng][0], xs[ng][1]);
-            if (jg1 < kvl)
+            if (jg1 < end)
               *reinterpret_cast<float2*>(a.scores + (base + jg1) * a.score_cols + r.c0 + cl) =
                   make_float2(xs[ng][2], xs[ng][3]);
           }
