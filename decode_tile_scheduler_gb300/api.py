@@ -82,7 +82,7 @@ def make_fia_params(*, q: torch.Tensor, out: torch.Tensor, k_cache: torch.Tensor
     p.sinks = _ptr(sinks)
     p.num_sms = num_sms
     p.kv_layout = kv_layout
-    p.first_tokens = first_tokens
+    p.first_tokens = _int32(first_tokens, "first_tokens")
     if atten_mask is not None:
         _contig(atten_mask, "atten_mask")
         if atten_mask.dim() != 3 or atten_mask.element_size() != 1:
@@ -178,7 +178,7 @@ def _state(t: Optional[torch.Tensor], name: str, dtype, batch: int, heads: int, 
         raise ValueError(f"{name} must be a {dtype} tensor [{batch}, {heads}, >= {capacity}]")
     row = int(t.stride(1)) if heads > 1 else int(t.stride(0))
     if batch == 1 and heads == 1:
-        row = max(int(t.shape[2]), capacity)
+        row = max(capacity, 1)  # (one row: any stride)
     if (t.shape[2] > 1 and t.stride(2) != 1) or (batch > 1 and t.stride(0) != heads * row):
         raise ValueError(f"{name}: rows of unit stride, evenly spaced")
     if row < capacity:
@@ -186,6 +186,22 @@ def _state(t: Optional[torch.Tensor], name: str, dtype, batch: int, heads: int, 
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the cache on {device}")
     return _ptr(t), row
+
+
+def _new_state(like: Optional[torch.Tensor], dtype, batch: int, heads: int, capacity: int, device):
+    """A state tensor of zeros with the row stride (and shape) of `like`."""
+    if like is None or like.dim() != 3:
+        return torch.zeros((batch, heads, capacity), dtype=dtype, device=device)
+    row = int(like.stride(1)) if heads > 1 else int(like.stride(0)) if batch > 1 else 0
+    row = max(row, int(like.shape[2]))
+    return torch.zeros((batch, heads, row), dtype=dtype, device=device)[:, :, :like.shape[2]]
+
+
+def _int32(x: int, name: str) -> int:
+    """An int32 field's value (ctypes would drop the upper bits of a larger one)."""
+    if not -(1 << 31) <= int(x) < 1 << 31:
+        raise ValueError(f"{name} must fit 32 bits")
+    return int(x)
 
 
 def _one_stride(strides, what: str) -> int:
@@ -350,8 +366,8 @@ class KeyWeightsCall(FiaCall):
         capacity = int(prob.S_kv if prob.block_table is None
                        else prob.block_table.shape[1] * prob.block_size)
         self.weights = weights
-        self.weights_out = (torch.zeros((prob.B, prob.KVN, capacity), dtype=torch.float32,
-                                        device=dev) if weights_out is None else weights_out)
+        self.weights_out = (_new_state(weights, torch.float32, prob.B, prob.KVN, capacity, dev)
+                            if weights_out is None else weights_out)
         w = self.weights_params = _abi.WeightsParams()
         w.weights_in, s1 = _state(weights, "weights", torch.float32, prob.B, prob.KVN, capacity,
                                   dev)
@@ -392,9 +408,13 @@ class KvEvictCall:
         if seqused_kv is None or weights is None:
             raise ValueError("seqused_kv and weights are required")
         self.seqused_out = torch.empty_like(seqused_kv) if seqused_out is None else seqused_out
-        self.weights_out = torch.zeros_like(weights) if weights_out is None else weights_out
+        def new(dtype):
+            return _new_state(weights, dtype, cache.batch, cache.num_kv_heads, cache.capacity,
+                              cache.device)
+
+        self.weights_out = new(torch.float32) if weights_out is None else weights_out
         if positions_out is None:
-            positions_out = torch.zeros_like(weights, dtype=torch.int32)
+            positions_out = new(torch.int32)
         self.positions_out = positions_out
         self.tensors = (seqused_kv, weights, positions, tokens_seen, status)
         p = self.params = _abi.EvictParams()
@@ -407,7 +427,9 @@ class KvEvictCall:
         p.positions_in, s3 = cache._state(positions, "positions", torch.int32)
         p.positions_out, s4 = cache._state(positions_out, "positions_out", torch.int32)
         p.state_stride = _one_stride((s1, s2, s3, s4), "weights and positions")
-        p.budget, p.first_tokens, p.recent_tokens = budget, first_tokens, recent_tokens
+        p.budget = _int32(budget, "budget")
+        p.first_tokens = _int32(first_tokens, "first_tokens")
+        p.recent_tokens = _int32(recent_tokens, "recent_tokens")
         p.status = _checked(status, "status", torch.int32, (1,), cache.device)
         self.ws_bytes = _abi.fia_get_evict_workspace_size(p)
         self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=cache.device)

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import decode_tile_scheduler_gb300 as fia
-from decode_tile_scheduler_gb300 import _abi
+from decode_tile_scheduler_gb300 import _abi, api
 from tests import bounded
 
 FAKE = 0x10000  # aligned, never dereferenced by a refused call
@@ -175,6 +175,27 @@ def test_python_calls_check_their_tensors():
         fia.KvCache(k.float(), k.float())
     with pytest.raises(ValueError, match="k_scale"):
         fia.KvCache(k.to(torch.uint8), k.to(torch.uint8))
+
+
+@pytest.mark.parametrize("shape,cut", [((2, 3, 80), 80), ((2, 3, 80), 64), ((2, 1, 80), 70),
+                                       ((1, 4, 80), 64), ((1, 1, 80), 64)])
+def test_new_state_has_the_row_stride_of_the_old(shape, cut):
+    w = torch.zeros(shape)[:, :, :cut]
+    B, heads, _ = shape
+    new = api._new_state(w, torch.int32, B, heads, 64, w.device)
+    assert new.shape == w.shape and new.dtype == torch.int32
+    if heads > 1:
+        assert new.stride(1) == w.stride(1)
+    if B > 1:
+        assert new.stride(0) == w.stride(0)
+    assert api._new_state(None, torch.float32, B, heads, 64, w.device).shape == (B, heads, 64)
+
+
+def test_numbers_past_32_bits_are_refused():
+    assert api._int32(-(1 << 31), "x") == -(1 << 31)
+    for x in (1 << 31, (1 << 32) + 4, -(1 << 31) - 1):
+        with pytest.raises(ValueError, match="32 bits"):
+            api._int32(x, "budget")
 
 
 # ---- the suite's own definitions ----

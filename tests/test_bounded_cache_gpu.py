@@ -881,3 +881,27 @@ def test_python_calls_refuse_tensors_that_do_not_fit():
               lambda: fia.KvEvictCall(cache, lens, w, budget=8, seqused_out=lens)):
         with pytest.raises(fia.FiaError):
             f()
+
+
+@pytest.mark.parametrize("B,KVN", [(2, 2), (2, 1), (1, 3), (1, 1)])
+@pytest.mark.parametrize("wide", ["longer", "slice", "head"])
+def test_default_outputs_follow_the_row_stride_of_the_state(B, KVN, wide):
+    """State tensors longer than the cache, or slices of such: the outputs that a
+    call makes itself have their row stride."""
+    cache, t = _empty_cache(B, KVN, 128, 2, 32, False, 0)
+    whole = torch.rand(B, KVN, 80, device=DEV)
+    w = whole if wide == "longer" else whole[:, :, :64] if wide == "slice" else whole[:, :, :70]
+    lens = torch.tensor([50, 64][:B], dtype=torch.int32, device=DEV)
+    n, wo, po = fia.kv_evict(cache, lens, w, budget=40)
+    assert wo.shape == w.shape and po.shape == w.shape and n.tolist() == [40] * B
+    for b in range(B):
+        for h in range(KVN):
+            kept = bounded.keep_of(w[b, h].cpu().numpy(), None, int(lens[b]), 40, 0, 0, int(lens[b]))
+            assert sorted(po[b, h, :40].tolist()) == list(np.nonzero(kept)[0])
+            assert torch.equal(wo[b, h, :40], w[b, h][po[b, h, :40].long()])
+    p = fi.make_fia(B=B, QN=2 * KVN, KVN=KVN, D=128, q_lens=[1] * B, kv_lens=lens.tolist(),
+                    block_size=32, device=DEV, seed=41, mask_mode=3)
+    w_in = w.clone()
+    out, lse, w2 = fia.KeyWeightsCall(p, weights=w).run()
+    assert w2.shape == w.shape
+    bounded.check_attention(p, out, lse, w2, w_in)
