@@ -31,22 +31,30 @@ struct RowAt {
   bool ok;        // the page lies inside the pool
 };
 
+// Page of key j of a paged cache, and the row of a key in it whose table entry is blk.
+__device__ __forceinline__ int cache_page(const CacheView& c, int j) {
+  return (int)(((uint64_t)(uint32_t)j * c.magic) >> c.shift);
+}
+__device__ __forceinline__ RowAt page_row(const CacheView& c, int hk, int j, int pg, int64_t blk) {
+  RowAt r;
+  const int jp = j - pg * c.bs;
+  r.ok = blk >= 0 && blk < c.num_blocks;
+  r.srow = (blk * c.KVN + hk) * c.bs + jp;
+  r.row = c.head_major ? r.srow : (blk * c.bs + jp) * c.KVN + hk;
+  return r;
+}
+
 // Row of key j (0 <= j < cap) of sequence b, KV head hk.
 __device__ __forceinline__ RowAt cache_row(const CacheView& c, int b, int hk, int j) {
-  RowAt r;
   if (!c.bt) {
+    RowAt r;
     r.row = ((int64_t)b * c.cap + j) * c.KVN + hk;
     r.srow = ((int64_t)b * c.KVN + hk) * c.cap + j;
     r.ok = true;
     return r;
   }
-  const int pg = (int)(((uint64_t)(uint32_t)j * c.magic) >> c.shift);
-  const int jp = j - pg * c.bs;
-  const int64_t blk = __ldg(c.bt + (int64_t)b * c.max_blocks + pg);
-  r.ok = blk >= 0 && blk < c.num_blocks;
-  r.srow = (blk * c.KVN + hk) * c.bs + jp;
-  r.row = c.head_major ? r.srow : (blk * c.bs + jp) * c.KVN + hk;
-  return r;
+  const int pg = cache_page(c, j);
+  return page_row(c, hk, j, pg, __ldg(c.bt + (int64_t)b * c.max_blocks + pg));
 }
 
 inline int64_t cache_capacity(const fia_kv_cache& c) {

@@ -57,6 +57,8 @@ constexpr int kBins = 2048;
 constexpr int kRanked = kThreads;  // keys with one first digit ranked directly, at most
 constexpr int kListedMax = 2048;   // moves listed in shared memory, at most
 constexpr int kStagedMax = 40 * 1024;  // keys of a slice kept in shared memory, at most
+constexpr int kPages = 2 * kThreads;   // table entries kept in shared memory, at most
+constexpr int kInFlight = 4;           // rows of a lane in flight
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -125,6 +127,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_evict_kernel(const EvictArgs a
                                                                 int listed) {
   extern __shared__ uint32_t skey[];  // the slice's keys, with `staged` places
   int2* slist = reinterpret_cast<int2*>(skey + staged);  // CS = 1: the moves, with `listed` places
+  __shared__ int32_t pages[kPages];  // the sequence's first table entries
   // this CTA's histogram of a pass, and each pass's over the cluster (alone: its own)
   __shared__ __align__(16) uint32_t mine_h[CS > 1 ? kBins : 4];
   __shared__ __align__(16) uint32_t hist[3][kBins];
@@ -134,11 +137,32 @@ __global__ void __launch_bounds__(kThreads, 2) kv_evict_kernel(const EvictArgs a
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const uint32_t rank = CS == 1 ? 0u : cluster_rank();
   const int pair = blockIdx.x / CS, b = pair / a.c.KVN, hk = pair - b * a.c.KVN;
-  const int n = min(max(__ldg(a.seqused + b), 0), a.c.cap);
-  const int m = min(n, a.budget);
-  if (hk == 0 && rank == 0 && tid == 0) a.seqused_out[b] = m;
   const float* w = a.w_in + pair * a.stride;
   const int32_t* pin = a.p_in ? a.p_in + pair * a.stride : nullptr;
+  // everything whose place does not depend on the length is fetched beside it (the
+  // weights of slots behind the length among them: rows have the capacity's places)
+  const int n_raw = __ldg(a.seqused + b), seen_raw = a.seen ? __ldg(a.seen + b) : 0;
+  const int32_t* table = a.c.bt ? a.c.bt + (int64_t)b * a.c.max_blocks : nullptr;
+  const int npages = table ? min(a.c.max_blocks, kPages) : 0;
+  int32_t page[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    page[i] = tid + i * kThreads < npages ? __ldg(table + tid + i * kThreads) : 0;
+  constexpr int U = 4;  // loads in flight
+  float wv[U];
+  int pv[U];
+  auto fetch = [&](int j0, int end) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u * kThreads;
+      wv[u] = j < end ? w[j] : 0.f;
+      pv[u] = j < end && pin ? pin[j] : j;
+    }
+  };
+  if (CS == 1) fetch(tid, a.c.cap);
+  const int n = min(max(n_raw, 0), a.c.cap);
+  const int m = min(n, a.budget);
+  if (hk == 0 && rank == 0 && tid == 0) a.seqused_out[b] = m;
   float* wo = a.w_out + pair * a.stride;
   int32_t* po = a.p_out ? a.p_out + pair * a.stride : nullptr;
   const int slice = ((n + CS - 1) / CS + 31) & ~31;  // n <= 20M: no overflow
@@ -150,7 +174,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv_evict_kernel(const EvictArgs a
     }
     return;
   }
-  const int64_t newest = (int64_t)(a.seen ? __ldg(a.seen + b) : n) - a.recent;
+  if (CS > 1) fetch(lo + tid, hi);
+  const int64_t newest = (int64_t)(a.seen ? seen_raw : n) - a.recent;
   auto key_at = [&](int j) { return order_key(w[j], pin ? pin[j] : j, a.first, newest); };
   const bool in_smem = slice <= staged;
   auto key_of = [&](int j) { return in_smem ? skey[j - lo] : key_at(j); };
@@ -160,6 +185,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv_evict_kernel(const EvictArgs a
   if (CS > 1)
     for (int i = tid; i < kBins; i += kThreads) mine_h[i] = 0u;
   if (tid == 0) totals[0] = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (tid + i * kThreads < npages) pages[tid + i * kThreads] = page[i];
   __syncthreads();
   cluster_arrive<CS>();  // (peers may add to the joined histograms once all are clear)
   uint32_t prefix = 0, known = 0, left = (uint32_t)a.budget;
@@ -177,16 +205,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv_evict_kernel(const EvictArgs a
     };
     const int end = lo + ((hi - lo + 31) & ~31);  // (whole warps)
     if (pass == 0) {
-      constexpr int U = 4;  // loads in flight
       for (int j0 = lo + tid; j0 < end; j0 += U * kThreads) {
-        float wv[U];
-        int pv[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int j = j0 + u * kThreads;
-          wv[u] = j < hi ? w[j] : 0.f;
-          pv[u] = j < hi && pin ? pin[j] : j;
-        }
+        if (j0 != lo + tid) fetch(j0, hi);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           const int j = j0 + u * kThreads;
@@ -361,57 +381,68 @@ __global__ void __launch_bounds__(kThreads, 2) kv_evict_kernel(const EvictArgs a
   }
   cluster_sync<CS>();
 
-  // ---- the moves: 16 bytes of K or V per lane, four moves of a group in flight ----
-  const int es = a.c.fp8 ? 1 : 2;
-  const int pieces = a.c.D * es / 16;        // of a K row: 8 or 16
-  const int per = 32 / (2 * pieces);         // moves a warp makes side by side: 2 or 1
-  const int grp = lane / (2 * pieces), x = lane % (2 * pieces);
-  const int isv = x >= pieces, pc = x % pieces;
-  uint8_t* pool = (isv ? a.c.v : a.c.k) + pc * 16;
-  const int64_t row_bytes = a.c.D * es;
-  // the four-byte words of a move, a lane each: the scales (FP8: D = 128, two of
-  // K and of V), the weight, the position
-  enum { kNone, kScale, kWeight, kPosition };
-  const int role = x == 2 ? kWeight : x == 3 ? (po ? kPosition : kNone)
-                   : a.c.fp8 && pc < 2 ? kScale : kNone;
-  uint32_t* scales = reinterpret_cast<uint32_t*>(isv ? a.c.vs : a.c.ks) + pc;
-  const int step = CS * kWarps * per;
-  constexpr int U = 4;
-  for (int i0 = ((int)rank * kWarps + wid) * per + grp; i0 < moves; i0 += U * step) {
-    int2 ht[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      ht[u] = i0 + u * step >= moves ? make_int2(-1, 0)
-              : in_list              ? slist[i0 + u * step]
-                                     : __ldcg(mv + i0 + u * step);
-    // (no branches around the loads, so that all of a kind are in flight at
-    // once: a move without a place reads row 0 and slot 0, which exist)
-    uint4 v[U];
-    uint32_t word[U];
-    uint32_t fine = 0;  // moves whose pages lie in the pool
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const RowAt t = cache_row(a.c, b, hk, max(ht[u].x, 0)), f = cache_row(a.c, b, hk, ht[u].y);
-      const bool ok = ht[u].x >= 0 && t.ok && f.ok;
-      fine |= (uint32_t)ok << u;
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(w) + ht[u].y;
-      if (role == kScale) src = scales + (ok ? f.srow * 2 : 0);
-      if (role == kPosition && pin) src = reinterpret_cast<const uint32_t*>(pin) + ht[u].y;
-      v[u] = *reinterpret_cast<const uint4*>(pool + (ok ? f.row : 0) * row_bytes);
-      word[u] = *src;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (ht[u].x < 0) break;
-      if ((fine >> u) & 1u) {  // (the target's row again: cheaper than the registers)
-        const RowAt t = cache_row(a.c, b, hk, ht[u].x);
-        *reinterpret_cast<uint4*>(pool + t.row * row_bytes) = v[u];
-        if (role == kScale) scales[t.srow * 2] = word[u];
-      } else if (x == 0 && a.status) {
-        atomicExch(a.status, 3);
+  // ---- the moves ----
+  // A warp takes up to 32 at a time.  Each lane finds the rows of one move and
+  // makes its small copies (weight, position, scales); then the warp copies the
+  // rows, 16 bytes of K or V per lane, kInFlight moves in flight.  (With every lane
+  // finding the rows of every move the address arithmetic bound the phase.)
+  const int row_pieces = a.c.D * (a.c.fp8 ? 1 : 2) / 16;  // 16-byte pieces of a K row: 8 or 16
+  const int per = 16 / row_pieces;           // moves a warp makes side by side: 2 or 1
+  const int grp = lane / (2 * row_pieces), x = lane % (2 * row_pieces);
+  uint4* pool = reinterpret_cast<uint4*>(x >= row_pieces ? a.c.v : a.c.k) + x % row_pieces;
+  auto row_of = [&](int j) {
+    if (!table) return cache_row(a.c, b, hk, j);
+    const int pg = cache_page(a.c, j);
+    return page_row(a.c, hk, j, pg, pg < kPages ? pages[pg] : __ldg(table + pg));
+  };
+  constexpr int kAll = CS * kWarps;  // warps of the cluster
+  for (int i0 = (int)rank * kWarps + wid; i0 < moves; i0 += 32 * kAll) {
+    const int i = i0 + lane * kAll;
+    int2 ht = make_int2(0, 0);
+    if (i < moves) ht = in_list ? slist[i] : __ldcg(mv + i);
+    int64_t to = 0, from = 0;  // rows, in pieces
+    bool ok = false;
+    float weight = 0.f;
+    int position = 0;
+    float2 ks = make_float2(0.f, 0.f), vs = ks;
+    int64_t scale_to = 0;
+    if (i < moves) {
+      const RowAt t = row_of(ht.x), f = row_of(ht.y);
+      ok = t.ok && f.ok;
+      to = t.row * row_pieces;
+      from = f.row * row_pieces;
+      weight = w[ht.y];
+      if (po) position = pin ? pin[ht.y] : ht.y;
+      scale_to = t.srow;
+      if (a.c.fp8 && ok) {  // (D = 128: two scales a row)
+        ks = reinterpret_cast<const float2*>(a.c.ks)[f.srow];
+        vs = reinterpret_cast<const float2*>(a.c.vs)[f.srow];
       }
-      if (role == kWeight) wo[ht[u].x] = __uint_as_float(word[u]);
-      if (role == kPosition) po[ht[u].x] = pin ? (int32_t)word[u] : ht[u].y;
+    }
+    const uint32_t fine = __ballot_sync(0xffffffffu, ok);
+    for (int c0 = 0; c0 < 32 && i0 + c0 * kAll < moves; c0 += kInFlight * per) {
+      uint4 v[kInFlight];
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u) {
+        const int c = c0 + u * per + grp;
+        const int64_t at = __shfl_sync(0xffffffffu, from, c);
+        if ((fine >> c) & 1u) v[u] = pool[at];
+      }
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u) {
+        const int c = c0 + u * per + grp;
+        const int64_t at = __shfl_sync(0xffffffffu, to, c);
+        if ((fine >> c) & 1u) pool[at] = v[u];
+      }
+    }
+    if (i < moves) {
+      wo[ht.x] = weight;
+      if (po) po[ht.x] = position;
+      if (a.c.fp8 && ok) {
+        reinterpret_cast<float2*>(a.c.ks)[scale_to] = ks;
+        reinterpret_cast<float2*>(a.c.vs)[scale_to] = vs;
+      }
+      if (!ok && a.status) atomicExch(a.status, 3);
     }
   }
 }
