@@ -185,9 +185,6 @@ __global__ void __launch_bounds__(kThreads, 2) kv_evict_kernel(const EvictArgs a
   if (CS > 1)
     for (int i = tid; i < kBins; i += kThreads) mine_h[i] = 0u;
   if (tid == 0) totals[0] = 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (tid + i * kThreads < npages) pages[tid + i * kThreads] = page[i];
   __syncthreads();
   cluster_arrive<CS>();  // (peers may add to the joined histograms once all are clear)
   uint32_t prefix = 0, known = 0, left = (uint32_t)a.budget;
@@ -221,6 +218,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv_evict_kernel(const EvictArgs a
           count(k, j < hi);  // (past `end` for a whole warp: nothing)
         }
       }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (tid + i * kThreads < npages) pages[tid + i * kThreads] = page[i];
     } else {
       for (int j = lo + tid; j < end; j += kThreads) {
         const uint32_t k = j < hi ? key_of(j) : 0u;
