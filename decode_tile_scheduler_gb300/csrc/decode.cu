@@ -1924,6 +1924,12 @@ __global__ void __launch_bounds__(256, 4)
   }
 }
 
+}  // namespace fia
+
+#include "decode_cluster.cuh"
+
+namespace fia {
+
 // ---------------------------------------------------------------------------
 // host launchers
 // ---------------------------------------------------------------------------

@@ -715,13 +715,16 @@ fia_kv_cache cache_of(const fia_params* p) {
 namespace {
 
 // The decode branch of an execute; with `w` also the key weights, every score
-// kept at `scores` (rows of `cols`).
-fia_status execute_decode(const fia_params* p, void* ws, cudaStream_t s,
+// kept at `scores` (rows of `cols`).  `planned`: the plan was made before, else
+// its launch is the one before this on the stream.
+fia_status execute_decode(const fia_params* p, void* ws, cudaStream_t s, bool planned,
                           const KeyWeightsOut* w = nullptr, float* scores = nullptr, int cols = 0) {
   DecodePlan pl;
   fia_status st = decode_plan(p, &pl);
   if (st != FIA_OK) return st;
   DecodeArgs a = decode_args(p, pl, ws);
+  if (decode_is_few(a, w != nullptr))
+    return launch_decode_few(a, cache_of(p), w, planned, s) == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
   a.scores = scores;
   a.score_cols = cols;
   CUtensorMap tk, tv;
@@ -730,6 +733,67 @@ fia_status execute_decode(const fia_params* p, void* ws, cudaStream_t s,
   return launch_decode(a, tk, tv, p->kv_dtype == FIA_KV_FP8_E4M3, w, s) == cudaSuccess
              ? FIA_OK
              : FIA_ERR_CUDA;
+}
+
+fia_status execute(const fia_params* p, void* ws, size_t ws_bytes, void* stream, bool planned) {
+  fia_plan_layout l;
+  fia_status st = fia_get_plan_layout(p, &l);
+  if (st != FIA_OK) return st;
+  if (!ws || ws_bytes < (size_t)l.total_bytes) return FIA_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (q_empty(p)) return FIA_OK;
+  if (l.branch == 2) {
+    PrefillPlan pp;
+    st = prefill_plan(p, &pp);
+    if (st != FIA_OK) return st;
+    const fia_params v = prefill_view(p, pp, ws);
+    PrefillArgs a = prefill_args(&v, pp, ws);
+    if (p->kv_dtype == FIA_KV_FP8_E4M3) {
+      char* w = static_cast<char*>(ws);
+      a.f16 = 1;
+      a.kvfac = reinterpret_cast<const float*>(w + pp.off_kvfac);
+    }
+    // (FP8 caches: the prefill kernel converts each bf16 query tile to fp16
+    // itself; the conversion pass covers K and V)
+    CUtensorMap tq, tk, tv;
+    st = q_map(&v, &tq);
+    if (st != FIA_OK) return st;
+    st = kv_maps(&v, a.box_rows, &tk, &tv);
+    if (st != FIA_OK) return st;
+    if (p->kv_dtype == FIA_KV_FP8_E4M3) {
+      int n;
+      st = sm_count(p->num_sms, &n);
+      if (st != FIA_OK) return st;
+      if (launch_kv_dequant(dequant_args(p, pp, ws), n, s) != cudaSuccess) return FIA_ERR_CUDA;
+    }
+    return launch_prefill(a, tq, tk, tv, s) == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
+  }
+  return execute_decode(p, ws, s, planned);
+}
+
+fia_status execute_weights(const fia_params* p, const fia_weights_params* w, void* ws,
+                           size_t ws_bytes, void* stream, bool planned) {
+  WeightsPlan pl;
+  fia_status st = weights_plan(p, w, &pl);
+  if (st != FIA_OK) return st;
+  if (!ws || ws_bytes < (size_t)pl.total) return FIA_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (pl.lay.branch == 1) {
+    float* scores = reinterpret_cast<float*>(static_cast<char*>(ws) + pl.off);
+    const KeyWeightsOut o = {w->weights_in, w->weights_out, w->state_stride, 0, 0};
+    return execute_decode(p, ws, s, planned, &o, scores, pl.cols);
+  }
+  st = execute(p, ws, ws_bytes, stream, planned);
+  if (st != FIA_OK) return st;
+  const WeightsArgs a = weights_args(p, w, pl, ws);
+  if (pl.lay.branch == 0)  // no query row
+    return launch_key_weights_fold(a, s) == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
+  CUtensorMap tq, tk, tv;
+  st = q_map(p, &tq);
+  if (st != FIA_OK) return st;
+  st = kv_maps(p, a.box_rows, &tk, &tv);
+  if (st != FIA_OK) return st;
+  return launch_key_weights(a, cache_of(p), tq, tk, s) == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
 }
 
 }  // namespace
@@ -824,46 +888,14 @@ fia_status fia_plan(const fia_params* p, void* ws, size_t ws_bytes, void* stream
 
 fia_status fia_execute(const fia_params* p, void* ws, size_t ws_bytes, void* stream) {
   NvtxRange range("fia_execute");
-  fia_plan_layout l;
-  fia_status st = fia_get_plan_layout(p, &l);
-  if (st != FIA_OK) return st;
-  if (!ws || ws_bytes < (size_t)l.total_bytes) return FIA_ERR_WORKSPACE_TOO_SMALL;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (q_empty(p)) return FIA_OK;
-  if (l.branch == 2) {
-    PrefillPlan pp;
-    st = prefill_plan(p, &pp);
-    if (st != FIA_OK) return st;
-    const fia_params v = prefill_view(p, pp, ws);
-    PrefillArgs a = prefill_args(&v, pp, ws);
-    if (p->kv_dtype == FIA_KV_FP8_E4M3) {
-      char* w = static_cast<char*>(ws);
-      a.f16 = 1;
-      a.kvfac = reinterpret_cast<const float*>(w + pp.off_kvfac);
-    }
-    // (FP8 caches: the prefill kernel converts each bf16 query tile to fp16
-    // itself; the conversion pass covers K and V)
-    CUtensorMap tq, tk, tv;
-    st = q_map(&v, &tq);
-    if (st != FIA_OK) return st;
-    st = kv_maps(&v, a.box_rows, &tk, &tv);
-    if (st != FIA_OK) return st;
-    if (p->kv_dtype == FIA_KV_FP8_E4M3) {
-      int n;
-      st = sm_count(p->num_sms, &n);
-      if (st != FIA_OK) return st;
-      if (launch_kv_dequant(dequant_args(p, pp, ws), n, s) != cudaSuccess) return FIA_ERR_CUDA;
-    }
-    return launch_prefill(a, tq, tk, tv, s) == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
-  }
-  return execute_decode(p, ws, s);
+  return execute(p, ws, ws_bytes, stream, true);
 }
 
 fia_status fia_run(const fia_params* p, void* ws, size_t ws_bytes, void* stream) {
   NvtxRange range("fia_run");
   fia_status st = fia_plan(p, ws, ws_bytes, stream);
   if (st != FIA_OK) return st;
-  return fia_execute(p, ws, ws_bytes, stream);
+  return execute(p, ws, ws_bytes, stream, false);
 }
 
 size_t fia_sizeof_weights_params(void) { return sizeof(fia_weights_params); }
@@ -881,27 +913,7 @@ fia_status fia_get_weights_workspace_size(const fia_params* p, const fia_weights
 fia_status fia_execute_weights(const fia_params* p, const fia_weights_params* w, void* ws,
                                size_t ws_bytes, void* stream) {
   NvtxRange range("fia_execute_weights");
-  WeightsPlan pl;
-  fia_status st = weights_plan(p, w, &pl);
-  if (st != FIA_OK) return st;
-  if (!ws || ws_bytes < (size_t)pl.total) return FIA_ERR_WORKSPACE_TOO_SMALL;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (pl.lay.branch == 1) {
-    float* scores = reinterpret_cast<float*>(static_cast<char*>(ws) + pl.off);
-    const KeyWeightsOut o = {w->weights_in, w->weights_out, w->state_stride, 0, 0};
-    return execute_decode(p, ws, s, &o, scores, pl.cols);
-  }
-  st = fia_execute(p, ws, ws_bytes, stream);
-  if (st != FIA_OK) return st;
-  const WeightsArgs a = weights_args(p, w, pl, ws);
-  if (pl.lay.branch == 0)  // no query row
-    return launch_key_weights_fold(a, s) == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
-  CUtensorMap tq, tk, tv;
-  st = q_map(p, &tq);
-  if (st != FIA_OK) return st;
-  st = kv_maps(p, a.box_rows, &tk, &tv);
-  if (st != FIA_OK) return st;
-  return launch_key_weights(a, cache_of(p), tq, tk, s) == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
+  return execute_weights(p, w, ws, ws_bytes, stream, true);
 }
 
 fia_status fia_run_weights(const fia_params* p, const fia_weights_params* w, void* ws,
@@ -913,7 +925,7 @@ fia_status fia_run_weights(const fia_params* p, const fia_weights_params* w, voi
   if (!ws || ws_bytes < need) return FIA_ERR_WORKSPACE_TOO_SMALL;
   st = fia_plan(p, ws, ws_bytes, stream);
   if (st != FIA_OK) return st;
-  return fia_execute_weights(p, w, ws, ws_bytes, stream);
+  return execute_weights(p, w, ws, ws_bytes, stream, false);
 }
 
 fia_status sparse_attn_metadata(const sparse_attn_params* p, int32_t* metadata,

@@ -186,6 +186,12 @@ struct KeyWeightsOut {
 // The decode kernel and its combine; with `w` (and a.scores) the key weights too.
 cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
                           int fp8, const KeyWeightsOut* w, cudaStream_t s);
+// Whether a call has few units and few keys (a rule on sizes), and its one kernel:
+// `planned` if it has to find a plan in the workspace, else the plan's launch goes
+// before it and need not be done.
+bool decode_is_few(const DecodeArgs& a, bool weights);
+cudaError_t launch_decode_few(const DecodeArgs& a, const fia_kv_cache& cache, const KeyWeightsOut* w,
+                              bool planned, cudaStream_t s);
 size_t decode_smem_bytes(int D, int fp8);
 
 cudaError_t launch_prefill_schedule(const PrefillArgs& a, cudaStream_t s);

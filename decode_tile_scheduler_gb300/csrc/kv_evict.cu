@@ -23,6 +23,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "cluster.cuh"
 #include "kv_cache.cuh"
 
 namespace fia {
@@ -60,44 +61,27 @@ constexpr int kStagedMax = 40 * 1024;  // keys of a slice kept in shared memory,
 constexpr int kPages = 2 * kThreads;   // table entries kept in shared memory, at most
 constexpr int kInFlight = 4;           // rows of a lane in flight
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// A barrier over every thread of the cluster; writes before its first half
-// (shared and global memory) are seen by its threads after the second.
+// The cluster's barrier in two halves; alone, the CTA's.
 template <int CS>
 __device__ __forceinline__ void cluster_arrive() {
-  if constexpr (CS > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if constexpr (CS > 1) cluster_bar_arrive();
 }
 template <int CS>
 __device__ __forceinline__ void cluster_wait() {
   if constexpr (CS == 1)
     __syncthreads();
   else
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_bar_wait();
 }
 template <int CS>
 __device__ __forceinline__ void cluster_sync() {
   cluster_arrive<CS>();
   cluster_wait<CS>();
 }
-__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  return a;
-}
 __device__ __forceinline__ void peer_add(uint32_t addr, uint32_t v) {
   asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(addr), "r"(v)
                : "memory");
 }
-__device__ __forceinline__ int peer_load(uint32_t addr) {
-  int v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-
 // Sum of x over the block's threads before this one (exclusive), `total` over
 // all; two barriers.
 __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_sums, uint32_t* total) {

@@ -206,8 +206,18 @@ def _window(**kw):
     return p
 
 
+# CTAs too few for a cluster: a call of few units that runs in one kernel
+# otherwise takes the kernels of the larger ones
+NO_CLUSTER = 7
+
+
 def _check(p):
-    call = fia.FiaCall(p)
+    for num_sms in (0, NO_CLUSTER):
+        _check_on(p, num_sms)
+
+
+def _check_on(p, num_sms):
+    call = fia.FiaCall(p, num_sms=num_sms)
     out, lse = call.run()
     torch.cuda.synchronize()
     bounded.check_attention(p, out, lse)
@@ -302,7 +312,8 @@ def test_first_tokens_zero_is_the_band():
 
 def test_window_wider_than_the_cache_is_causal():
     for ql in (1, 3, 70):
-        kw = dict(B=2, q_lens=[ql, ql], kv_lens=[700, 200], seed=15)
+        # (a table for long caches, so that the same kernel runs for both)
+        kw = dict(B=2, q_lens=[ql, ql], kv_lens=[700, 200], seed=15, max_blocks=200)
         a = _window(pre_tokens=1 << 20, first_tokens=4, **kw)
         b = fi.make_fia(QN=8, KVN=2, D=128, block_size=32, layout=fi.LAYOUT_TND, device=DEV,
                         mask_mode=fi.MASK_RIGHT_DOWN_CAUSAL, **kw)
@@ -315,24 +326,31 @@ def test_window_wider_than_the_cache_is_causal():
 # ----------------------------------------------------------------------------
 
 def _check_weights(p, with_in=True, seed=1):
+    for num_sms in (0, NO_CLUSTER):
+        _check_weights_on(p, num_sms, with_in, seed)
+
+
+def _check_weights_on(p, num_sms, with_in, seed):
     g = torch.Generator().manual_seed(seed)
     cap = p.S_kv if p.block_table is None else p.block_table.shape[1] * p.block_size
     w_in = (torch.rand(p.B, p.KVN, cap, generator=g).to(DEV) if with_in else None)
     mark = torch.full((p.B, p.KVN, cap), -3.0, device=DEV)
-    call = fia.KeyWeightsCall(p, weights=w_in, weights_out=mark.clone())
+    call = fia.KeyWeightsCall(p, weights=w_in, weights_out=mark.clone(), num_sms=num_sms)
     out, lse, w = call.run()
     torch.cuda.synchronize()
     assert call.error_word() == 0
     bounded.check_attention(p, out, lse, w, w_in)
     for b in range(p.B):
         assert torch.all(w[b, :, p.kv_lens[b]:] == -3.0), "slots past the keys were written"
-    plain, plain_lse = fia.FiaCall(p).run()
-    assert torch.equal(out, plain) and torch.equal(lse, plain_lse)
+    plain, plain_lse = fia.FiaCall(p, num_sms=num_sms).run()
+    if num_sms == NO_CLUSTER or 8 * p.B * p.KVN > 152:  # (one kernel runs in both)
+        assert torch.equal(out, plain) and torch.equal(lse, plain_lse)
+    bounded.check_attention(p, plain, plain_lse)
     first = w.clone()
     call.weights_out.copy_(mark)
     assert torch.equal(call.run()[2], first), "the same bits again"
     if with_in:  # in place
-        again = fia.KeyWeightsCall(p, weights=w_in, weights_out=w_in)
+        again = fia.KeyWeightsCall(p, weights=w_in, weights_out=w_in, num_sms=num_sms)
         again.run()
         for b in range(p.B):
             assert torch.equal(w_in[b, :, :p.kv_lens[b]], first[b, :, :p.kv_lens[b]])
@@ -905,3 +923,88 @@ def test_default_outputs_follow_the_row_stride_of_the_state(B, KVN, wide):
     out, lse, w2 = fia.KeyWeightsCall(p, weights=w).run()
     assert w2.shape == w.shape
     bounded.check_attention(p, out, lse, w2, w_in)
+
+
+# ----------------------------------------------------------------------------
+# few units: one kernel beside the plan
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "d64"])
+@pytest.mark.parametrize("kv_layout,paged", [(0, True), (1, True), (0, False)])
+def test_few_units(kind, kv_layout, paged, weights):
+    """Several steps a warp, a first token's step beside the window's, rows of a
+    batch that has none, tables past the entries kept in shared memory."""
+    kw = dict(block_size=32, kv_layout=kv_layout) if paged else dict(paged=False, S_kv=3600)
+    if paged and not weights:
+        kw["max_blocks"] = 2000
+    p = _window(B=3, QN=8, KVN=2, D=64 if kind == "d64" else 128, q_lens=[2, 0, 1],
+                kv_lens=[3500, 70, 1111], seed=51, pre_tokens=2000, first_tokens=37,
+                with_sinks=True, kv_dtype=fi.KV_FP8_E4M3 if kind == "fp8" else fi.KV_BF16, **kw)
+    if weights:
+        _check_weights(p)
+    else:
+        _check(p)
+
+
+def test_few_units_after_a_plan_and_without_one():
+    """fia_plan then executes of both kinds on one workspace, and a run before them."""
+    p = _window(B=2, QN=8, KVN=2, q_lens=[1, 1], kv_lens=[400, 90], seed=52, pre_tokens=100,
+                first_tokens=4)
+    call = fia.KeyWeightsCall(p)
+    want = [x.clone() for x in call.run()]
+    call.out.zero_(), call.lse.zero_(), call.weights_out.zero_()
+    call.plan()
+    for _ in range(2):
+        call.execute()
+    torch.cuda.synchronize()
+    assert call.error_word() == 0
+    for x, y in zip((call.out, call.lse, call.weights_out), want):
+        assert torch.equal(x, y)
+    call.run()
+    call.out.zero_()
+    fia.FiaCall.execute(call)  # the attention alone, on the run's plan
+    assert torch.equal(call.out, want[0]) and call.error_word() == 0
+    call.ws.zero_()
+    call.out.fill_(3.0)
+    fia.FiaCall.execute(call)
+    assert call.error_word() == 2 and torch.all(call.out == 3.0)
+
+
+def test_few_units_wait_for_their_inputs():
+    """Inputs written by slow kernels before the call, outputs read after it, on a
+    side stream, eager and in a graph."""
+    p = _window(B=2, QN=8, KVN=2, q_lens=[1, 1], kv_lens=[400, 90], seed=53, pre_tokens=100,
+                first_tokens=4)
+    call = fia.KeyWeightsCall(p)
+    want = [x.clone() for x in call.run()]
+    keep = {n: getattr(p, n).clone() for n in ("q", "k_cache", "v_cache", "seqused_kv")}
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+
+    def late():
+        for n in keep:
+            getattr(p, n).zero_()
+        torch.cuda._sleep(5_000_000)
+        for n, x in keep.items():
+            getattr(p, n).copy_(x)
+        call.weights_out.zero_()
+        call.run()
+        got = [x.clone() for x in (call.out, call.lse, call.weights_out)]
+        for n in keep:  # (and nothing of the call is left behind these)
+            getattr(p, n).zero_()
+        return got
+
+    with torch.cuda.stream(side):
+        got = late()
+    side.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = late()
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
