@@ -26,7 +26,8 @@ constexpr int kFewCtas = 8, kFewWarps = 8, kFewThreads = 32 * kFewWarps;
 constexpr int kFewKeys = 16;                               // keys of a warp's step
 constexpr int kFewSpan = kFewCtas * kFewWarps;             // steps side by side
 constexpr int kFewKept = kFewKeys * 8 + kFewKeys;          // floats kept per step (weights)
-constexpr int kFewMaxRounds = 4;                           // steps of a warp, at most
+constexpr int kFewMaxRounds = 8;                           // steps of a warp, at most
+constexpr int kFewMaxKept = 4;                             // the same with key weights
 constexpr int kFewPages = 4 * kFewThreads;                 // table entries in shared memory
 
 // The pairs (a.e, b.e) and (a.e+1, b.e+1) of four codes' bytes as two bf16 pairs.
@@ -40,7 +41,7 @@ __device__ __forceinline__ void codes_bf16(uint32_t codes, uint32_t& lo, uint32_
 }
 
 template <int D, bool FP8, bool WT>
-__global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 1)
+__global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 2)
     decode_few_kernel(const DecodeArgs a, const CacheView c, const KeyWeightsOut o, int groups,
                       int planned) {
   constexpr int NK = FP8 ? 4 : D / 32;   // 16-byte pieces of a lane's Q row
@@ -411,10 +412,11 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
 
 // Steps of 16 keys that a row of the call can see, at most.
 int64_t few_steps(const DecodeArgs& a) {
-  int64_t keys = a.S_kv;
-  if (a.mask_mode == 4)
-    keys = std::min<int64_t>(keys, (int64_t)a.pre_tokens + a.next_tokens + a.S_max + a.first_tokens);
-  return keys / kFewKeys + 3;  // (two intervals, each cut at both ends)
+  const int64_t all = ((int64_t)a.S_kv + kFewKeys - 1) / kFewKeys;
+  if (a.mask_mode != 4) return all;
+  // (a window and the first tokens, each cut at both ends)
+  const int64_t keys = (int64_t)a.pre_tokens + a.next_tokens + a.S_max + a.first_tokens;
+  return std::min(all, keys / kFewKeys + 3);
 }
 
 template <int D, bool FP8, bool WT>
@@ -431,7 +433,7 @@ cudaError_t launch_few_t(const DecodeArgs& a, const CacheView& c, const KeyWeigh
   const uint64_t bit = 1ull << (dev & 63);
   if (!(done_mask[(dev >> 6) & 3].load() & bit)) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             4 * kFewKept * kFewWarps * kFewMaxRounds);
+                             4 * kFewKept * kFewWarps * kFewMaxKept);
     if (e != cudaSuccess) return e;
     done_mask[(dev >> 6) & 3].fetch_or(bit);
   }
@@ -441,12 +443,20 @@ cudaError_t launch_few_t(const DecodeArgs& a, const CacheView& c, const KeyWeigh
 
 }  // namespace
 
+// The rule: clusters that run at once (two CTAs to an SM; 16 clusters of 8 fit with
+// one to an SM), and rounds up to which this kernel was the faster.  Measured (us a
+// call, here / plan, decode and combine; 4 query heads per KV head, bf16): 4 units,
+// window 1000 7.3 / 12.4, 8000 14.4 / 16.8; 32 units, 1000 9.5 / 15.7, 8000 27.0 /
+// 32.4; 48 units, 1000 16.8 / 16.8.  With key weights 4 units of 1000 keys 8.3 / 13.9,
+// of 4000 14.1 / 14.5, of 8000 22.3 / 17.5; 32 units 10.8 / 17.6, 18.8 / 26.3, 37.3 /
+// 36.1; 48 units of 2000 keys 24.1 / 23.3.  FP8 gains more.  (With FIA_DEBUG the other
+// kernels run: they report pages outside the pool.)
 bool decode_is_few(const DecodeArgs& a, bool weights) {
-  if ((a.first_tokens == 0 && !weights) || a.mask || a.debug) return false;
+  if ((a.first_tokens == 0 && !weights) || a.mask || a.debug || a.num_ctas < kFewCtas) return false;
   const int64_t groups = (a.S_max * a.G + 7) / 8;
   if (weights && groups > 1) return false;  // (a key's weight is a sum within one unit)
-  return (int64_t)a.B * a.KVN * groups * kFewCtas <= a.num_ctas &&
-         few_steps(a) <= kFewSpan * kFewMaxRounds;
+  return (int64_t)a.B * a.KVN * groups * 9 <= 2 * a.num_ctas &&
+         few_steps(a) <= kFewSpan * (weights ? kFewMaxKept : kFewMaxRounds);
 }
 
 cudaError_t launch_decode_few(const DecodeArgs& a, const fia_kv_cache& cache, const KeyWeightsOut* w,

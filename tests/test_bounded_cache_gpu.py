@@ -313,7 +313,7 @@ def test_first_tokens_zero_is_the_band():
 def test_window_wider_than_the_cache_is_causal():
     for ql in (1, 3, 70):
         # (a table for long caches, so that the same kernel runs for both)
-        kw = dict(B=2, q_lens=[ql, ql], kv_lens=[700, 200], seed=15, max_blocks=200)
+        kw = dict(B=2, q_lens=[ql, ql], kv_lens=[700, 200], seed=15, max_blocks=300)
         a = _window(pre_tokens=1 << 20, first_tokens=4, **kw)
         b = fi.make_fia(QN=8, KVN=2, D=128, block_size=32, layout=fi.LAYOUT_TND, device=DEV,
                         mask_mode=fi.MASK_RIGHT_DOWN_CAUSAL, **kw)
@@ -343,7 +343,7 @@ def _check_weights_on(p, num_sms, with_in, seed):
     for b in range(p.B):
         assert torch.all(w[b, :, p.kv_lens[b]:] == -3.0), "slots past the keys were written"
     plain, plain_lse = fia.FiaCall(p, num_sms=num_sms).run()
-    if num_sms == NO_CLUSTER or 8 * p.B * p.KVN > 152:  # (one kernel runs in both)
+    if num_sms == NO_CLUSTER or 9 * p.B * p.KVN > 2 * 152:  # (one kernel runs in both)
         assert torch.equal(out, plain) and torch.equal(lse, plain_lse)
     bounded.check_attention(p, plain, plain_lse)
     first = w.clone()
