@@ -160,6 +160,13 @@ __device__ __forceinline__ float w_ex2(float x) {
   return y;
 }
 
+// n / d for n >= 0, d > 0, in 32 bits where they allow (a 64-bit division takes
+// ten times as long, and a CTA's first loads wait for some).
+__device__ __forceinline__ int64_t div_int(int64_t n, int64_t d) {
+  return ((uint64_t)(n | d) >> 32) == 0 ? (int64_t)((uint32_t)n / (uint32_t)d) : n / d;
+}
+__device__ __forceinline__ int64_t div_up(int64_t n, int64_t d) { return div_int(n + d - 1, d); }
+
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kWThreads, 1)
     key_weights_kernel(const WeightsArgs a, const CacheView c,
@@ -225,7 +232,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(misc[1]);
-  pdl_wait();  // the attention is done: its lse, and the plan before it
+  // the attention is done: its lse, and the plan before it.  (Waiting for the lse alone,
+  // with the attention letting this kernel start on SMs that have finished, made four
+  // prompts slower, 103 -> 105 us a call.)
+  pdl_wait();
   const bool ok = plan_ok(a);
   volatile int* abort_flag = misc;
 
@@ -265,7 +275,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     }
     // no shorter than a.chunk (a part has its K tiles to load, and a unit's
     // longest has to fit kMaxParts parts)
-    range = max((int64_t)a.chunk, (all_steps + gridDim.x - 1) / gridDim.x);
+    range = max((int64_t)a.chunk, div_up(all_steps, gridDim.x));
     if (nwin > 1) {  // back to the window of this CTA's start
       int64_t before = 0;
       int w0 = 0;
@@ -349,14 +359,29 @@ __global__ void __launch_bounds__(kWThreads, 1)
         before += __shfl_sync(0xffffffffu, x, 31);
       }
       more = next_seq(b);
-      // then its units
-      while (more && before + (int64_t)steps * a.KVN <= at) {
-        before += (int64_t)steps * a.KVN;
-        more = next_kt(kt + 1);
-      }
-      if (more) {
-        hk = (int)((at - before) / steps);
-        s = at - before - (int64_t)hk * steps;
+      // then its unit: a lane per 256 keys, 32 units at a time
+      for (int base = 0; more; base += 32) {
+        int t0 = 0;
+        const int n = base + lane < nkt ? unit_steps(a, ql, kl, (base + lane) * kUnitKeys, &t0) : 0;
+        int64_t x = (int64_t)n * a.KVN;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        const uint32_t here = __ballot_sync(0xffffffffu, before + x > at);
+        if (here) {
+          const int src = __ffs(here) - 1;
+          kt = base + src;
+          steps = __shfl_sync(0xffffffffu, n, src);
+          qt0 = __shfl_sync(0xffffffffu, t0, src);
+          before += __shfl_sync(0xffffffffu, x, src) - (int64_t)steps * a.KVN;
+          hk = (int)div_int(at - before, steps);
+          s = at - before - (int64_t)hk * steps;
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, x, 31);
+        more = base + 32 < nkt;
       }
     }
     named_bar_sync(4, kWThreads);  // the sums, in the Q stages' place, have been read
@@ -382,8 +407,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
       m.qrow = qrow;
       m.s0 = (int)s;
       m.s1 = (int)min((int64_t)steps, s + (end - at));
-      m.part = (int)(blockIdx.x - (at - s) / range);
-      m.parts = (int)((at - s + steps - 1) / range - (at - s) / range + 1);
+      const int64_t first = div_int(at - s, range);  // the CTA of the unit's first part
+      m.part = (int)(blockIdx.x - first);
+      m.parts = (int)(div_int(at - s + steps - 1, range) - first + 1);
       m.done = 0;
       if (lane == 0) {
         msg[ms] = m;
@@ -780,12 +806,12 @@ cudaError_t launch_t(const WeightsArgs& a, const CacheView& c, const CUtensorMap
 
 }  // namespace
 
-// The fewest steps per part: 4 (a part loads 64 KB of K; a step takes about
-// 1 us), and enough that a unit of queries of max_q rows, cut anywhere, has at
-// most kMaxParts parts.
+// The fewest steps per part: 2 (a part loads 64 KB of K, and a step takes about
+// 1.2 us: one prompt of 34 rows over 6 keys 30.5 us with 4, 28.1 us with 2), and enough
+// that a unit of queries of max_q rows, cut anywhere, has at most kMaxParts parts.
 int weights_chunk(int G, int64_t max_q) {
   const int64_t steps = (max_q + kQTile - 1) / kQTile * G;
-  return (int)std::max<int64_t>(4, (steps + kMaxParts - 2) / (kMaxParts - 1));
+  return (int)std::max<int64_t>(2, (steps + kMaxParts - 2) / (kMaxParts - 1));
 }
 int64_t weights_units(int64_t capacity) { return (capacity + kUnitKeys - 1) / kUnitKeys; }
 int weights_parts() { return kMaxParts; }

@@ -824,6 +824,14 @@ def test_weights_prefill_of_long_prompts_cut_over_many_ctas():
     _check_weights(p)
 
 
+@pytest.mark.parametrize("kv_dtype", [fi.KV_BF16, fi.KV_FP8_E4M3])
+def test_weights_of_short_prompts_behind_long_caches(kv_dtype):
+    """More than 32 units of 256 keys in a sequence, ranges that start in any of them."""
+    _check_weights(fi.make_fia(B=3, QN=8, KVN=2, D=128, q_lens=[40, 300, 20],
+                               kv_lens=[20001, 9000, 8449], layout=fi.LAYOUT_TND, block_size=128,
+                               kv_dtype=kv_dtype, device=DEV, seed=35, mask_mode=3))
+
+
 @pytest.mark.parametrize("rows", [3, 40])
 def test_a_nan_row_reaches_only_the_keys_it_sees(rows):
     """A query row of NaN (and a key of NaN) leave every other key's weight alone."""
