@@ -13,7 +13,10 @@
 // of D.  Key weights need no second look at K: a warp keeps its scores in shared
 // memory until the columns' lse is known.
 //
-// Bound by latency: lengths and page table, then K and V, then two folds.
+// Bound by latency: lengths and page table, then K and V, then two folds.  One sequence,
+// 8 KV heads, a window of 1024 and 4 first tokens: 7.7 us a call in a graph (plan, decode
+// and combine 12.4); two contexts of up to 777 keys with key weights 8.7 us (14.3).  At
+// 188 registers, one CTA to an SM, 16 clusters of eight did not fit at once: 12.7 us.
 #pragma once
 
 #include "cluster.cuh"

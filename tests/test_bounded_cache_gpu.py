@@ -955,6 +955,27 @@ def test_few_units(kind, kv_layout, paged, weights):
         _check(p)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("mode,scale", [(fi.MASK_NONE, None), (fi.MASK_LEFT_UP_CAUSAL, None),
+                                        (fi.MASK_RIGHT_DOWN_CAUSAL, -0.07)])
+def test_few_units_masks(mode, scale, fp8):
+    """Key weights of several rows in the eight columns of a unit."""
+    _check_weights(fi.make_fia(B=4, QN=4, KVN=4, D=128, q_lens=[3, 8, 0, 5], kv_lens=[1, 700, 40, 2],
+                               layout=fi.LAYOUT_TND, block_size=32, device=DEV, seed=54,
+                               mask_mode=mode, scale=scale,
+                               kv_dtype=fi.KV_FP8_E4M3 if fp8 else fi.KV_BF16))
+    _check_weights(fi.make_fia(B=2, QN=7, KVN=1, D=128, q_lens=[1, 1], kv_lens=[300, 0],
+                               block_size=96, device=DEV, seed=55, mask_mode=mode, scale=scale,
+                               kv_dtype=fi.KV_FP8_E4M3 if fp8 else fi.KV_BF16))
+
+
+def test_pages_behind_those_kept_in_shared_memory():
+    """Table entries past the first 1024, in a window call of few units and an eviction."""
+    _check(_window(B=1, QN=8, KVN=2, q_lens=[2], kv_lens=[20000], block_size=16, seed=56,
+                   pre_tokens=500, first_tokens=20))
+    _evict_case([20000, 17000], 16500, first=4, recent=300, KVN=2, D=64, block=16, seed=7)
+
+
 def test_few_units_after_a_plan_and_without_one():
     """fia_plan then executes of both kinds on one workspace, and a run before them."""
     p = _window(B=2, QN=8, KVN=2, q_lens=[1, 1], kv_lens=[400, 90], seed=52, pre_tokens=100,
