@@ -378,7 +378,9 @@ fia_status fia_kv_append(const fia_append_params *p, void *stream);
  *                        exp(scale * q_ih . k_j - lse_ih)  (visible pairs)
  * i.e. the attention probabilities of this call, summed over its rows and the
  * group's heads, in fp32 in a fixed order (deterministic).  Rows that see no
- * key add nothing; a sink takes its share of a row's probability.  Slots at
+ * key add nothing; a sink takes its share of a row's probability.  (out and lse
+ * may differ from fia_run's in their last bits: few units take a kernel of
+ * their own.)  Slots at
  * or past kv_len are left as they were.  weights_in may be NULL (zeros) or
  * weights_out itself; other overlaps are not allowed.  p->lse is required.
  * The workspace is fia_get_weights_workspace_size's, larger than
