@@ -256,6 +256,13 @@ __device__ __forceinline__ int find_batch(const T* prefix, int B, int64_t g) {
 __device__ __forceinline__ int64_t page_index(const DecodeArgs& a, int64_t j) {
   return (int64_t)(((uint64_t)(uint32_t)j * a.bs_magic) >> a.bs_shift);
 }
+// A table entry as the producers take it: -1 for a page outside the pool.  Page
+// -1 lies wholly before the tensor map's first row, so its boxes fill with zeros
+// (the row of the id itself, cut to the map's 32 bits, may be one of another
+// page: id 2^25 with 128-row pages is row 0).
+__device__ __forceinline__ int pool_page(const DecodeArgs& a, int id) {
+  return (uint32_t)id < (uint32_t)a.num_blocks ? id : -1;
+}
 // Pool row and FP8 scale row of logical KV row j of batch b, KV head hk, in
 // page blk, with jp = j - block_size * page_index(j) (j's row in its page).
 // Token-major pages [pages, page rows, KV_N, D] are a matrix of KV_N * D
@@ -270,6 +277,8 @@ __device__ __forceinline__ int64_t pool_row(const DecodeArgs& a, int b, int hk, 
   if (!a.block_table) return (int64_t)b * a.S_kv + j;
   return a.kv_layout == 1 ? (blk * a.KVN + hk) * a.block_size + jp : blk * a.block_size + jp;
 }
+// The FP8 scales of a page outside the pool: a box of rows.
+__device__ __align__(16) const float zero_scales[kKvTile * 2] = {};
 __device__ __forceinline__ int64_t scale_row_in(const DecodeArgs& a, int b, int hk, int64_t blk,
                                                 int64_t j, int64_t jp) {
   return a.block_table ? (blk * a.KVN + hk) * a.block_size + jp
@@ -714,8 +723,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                          pp.fg0 + 1);
         }
         if (pp.npg + pp.nfg <= 32 && lane < pp.npg + pp.nfg)
-          pp.mypage = a.block_table[(int64_t)r.b * a.max_blocks +
-                                    (lane < pp.npg ? pp.pg0 + lane : pp.fg0 + lane - pp.npg)];
+          pp.mypage = pool_page(a, a.block_table[(int64_t)r.b * a.max_blocks +
+                                                 (lane < pp.npg ? pp.pg0 + lane
+                                                                : pp.fg0 + lane - pp.npg)]);
       }
       return pp;
     };
@@ -741,12 +751,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           blk = __shfl_sync(0xffffffffu, pp.mypage,
                             !X || t < r.nwin ? (int)(pj - pp.pg0) : pp.npg + (int)(pj - pp.fg0));
         } else {
-          blk = mine ? (int64_t)a.block_table[(int64_t)r.b * a.max_blocks + pj] : 0;
+          blk = mine ? pool_page(a, a.block_table[(int64_t)r.b * a.max_blocks + pj]) : 0;
         }
       } else {
         blk = 0;
       }
-      if (a.debug && mine && a.block_table && (blk < 0 || blk >= a.num_blocks))
+      if (a.debug && mine && blk < 0)
         atomicExch(a.err, 3);  // (read as zeros by the TMA box all the same)
       const int64_t prow = mine ? pool_row(a, r.b, r.hk, blk, jb, jp) : 0;
       constexpr int NT = D / 64;
@@ -756,13 +766,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // multiples of 32; contiguous caches have an even length), hence
       // 16-byte aligned.
       // (a page id outside the pool reads zeros through TMA; its FP8
-      // scales, which come by plain bulk copy, are not read at all)
-      int64_t srow = 0;
+      // scales, which come by plain bulk copy, are zeros from zero_scales:
+      // what the stage held before may be no number)
+      const float* ssrc = zero_scales;
       int srows = a.box_rows;
-      bool scale_ok = false;
       if constexpr (FP8) {
-        scale_ok = mine && (!a.block_table || (blk >= 0 && blk < a.num_blocks));
-        if (scale_ok) srow = scale_row_in(a, r.b, r.hk, blk, jb, jp);
+        if (mine && blk >= 0)
+          ssrc = (isv ? a.v_scale : a.k_scale) + scale_row_in(a, r.b, r.hk, blk, jb, jp) * NT;
         if (!a.block_table) srows = (int)min((int64_t)a.box_rows, (int64_t)a.S_kv - jb);
       }
       int nvalid = 0;
@@ -770,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j0 + (int64_t)q * a.box_rows < r.kv_len) ++nvalid;
       uint32_t scale_bytes = 0;
       if constexpr (FP8)
-        scale_bytes = __reduce_add_sync(0xffffffffu, scale_ok ? (uint32_t)(srows * NT * 4) : 0u);
+        scale_bytes = __reduce_add_sync(0xffffffffu, mine ? (uint32_t)(srows * NT * 4) : 0u);
       // explicit mask (K warp): the tile's slice of each of the unit's query
       // rows, 16-byte pieces up to kv_len (row strides are multiples of 16
       // that cover the KV capacity, so the copy stays inside the row)
@@ -803,9 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (FP8) {
           float* sdst = reinterpret_cast<float*>(st + 2 * Cfg::kTileBytes) + isv * (kKvTile * NT) +
                         rb * a.box_rows * NT;
-          if (scale_ok)
-            bulk_load(sdst, (isv ? a.v_scale : a.k_scale) + srow * NT, (uint32_t)(srows * NT * 4),
-                      &full[s]);
+          bulk_load(sdst, ssrc, (uint32_t)(srows * NT * 4), &full[s]);
         }
       }
       ++it;

@@ -436,7 +436,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
             if (c.bt) {
               const int pg = (int)(((uint64_t)(uint32_t)j * c.magic) >> c.shift);
               const int64_t blk = __ldg(c.bt + (int64_t)m.b * c.max_blocks + pg);
-              row = (c.head_major ? blk * c.KVN + m.hk : blk) * c.bs + (j - pg * c.bs);
+              // (a page outside the pool: a box before the map's rows, zeros)
+              row = blk < 0 || blk >= c.num_blocks
+                        ? -kKvTile
+                        : (c.head_major ? blk * c.KVN + m.hk : blk) * c.bs + (j - pg * c.bs);
             } else {
               row = (int64_t)m.b * c.cap + j;
             }

@@ -132,10 +132,15 @@ __global__ void __launch_bounds__(256) kv_dequant_kernel(const DequantArgs a) {
     if (j >= kv_len || !tile_needed(a, b, kv_len, j)) continue;
     const int hk = rest / (a.D / 16), d0 = (rest % (a.D / 16)) * 16;
     int64_t code_off, scale_row;
-    if (!locate(a, b, j, hk, d0, &code_off, &scale_row)) continue;
+    const bool in_pool = locate(a, b, j, hk, d0, &code_off, &scale_row);
     const int64_t out_off = (((int64_t)b * a.cap + j) * a.KVN + hk) * a.D + d0;
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
+      uint16_t* dst = (kv ? a.v_out : a.k_out) + out_off;
+      if (!in_pool) {  // zeros, not what an earlier call left there
+        reinterpret_cast<uint4*>(dst)[0] = reinterpret_cast<uint4*>(dst)[1] = make_uint4(0u, 0u, 0u, 0u);
+        continue;
+      }
       const uint8_t* src = kv ? a.v : a.k;
       const float f = inv_pow2_of(__ldg(a.smax + ((int64_t)b * a.KVN + hk) * 2 + kv));
       const float sc = __ldg((kv ? a.v_scale : a.k_scale) + scale_row * NT + d0 / 64) * f;
@@ -151,7 +156,6 @@ __global__ void __launch_bounds__(256) kv_dequant_kernel(const DequantArgs a) {
         o[2 * w] = pack_f16(fl.x * sc, fl.y * sc);
         o[2 * w + 1] = pack_f16(fh.x * sc, fh.y * sc);
       }
-      uint16_t* dst = (kv ? a.v_out : a.k_out) + out_off;
       reinterpret_cast<uint4*>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
       reinterpret_cast<uint4*>(dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }

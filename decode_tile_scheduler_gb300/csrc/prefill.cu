@@ -176,8 +176,10 @@ __device__ __forceinline__ int tile_span(const PrefillArgs& a, int64_t q_len, in
 __device__ __forceinline__ int64_t kv_phys_row(const PrefillArgs& a, int b, int hk, int64_t j) {
   if (a.block_table) {
     const int64_t blk = a.block_table[(int64_t)b * a.max_blocks + j / a.block_size];
-    if (a.debug && (blk < 0 || blk >= a.num_blocks))
-      atomicExch(a.err, 3);  // (read as zeros by the TMA box all the same)
+    if (blk < 0 || blk >= a.num_blocks) {
+      if (a.debug) atomicExch(a.err, 3);
+      return -kKvTile;  // the box lies before the map's rows: zeros
+    }
     if (a.kv_layout == 1) return (blk * a.KVN + hk) * a.block_size + j % a.block_size;
     return blk * a.block_size + j % a.block_size;
   }
