@@ -197,6 +197,14 @@ __device__ __forceinline__ void batch_lengths(const DecodeArgs& a, int b, int64_
   *kv_len = a.seqused_kv ? a.seqused_kv[b] : a.S_kv;
 }
 
+// Whether a batch's query rows lie inside q and its length inside the cache.  One
+// that does not runs as empty, with 2 in the error word: the decode kernel checks
+// each queue entry so, the kernels that read the lengths themselves check them.
+__device__ __forceinline__ bool lengths_fit(const DecodeArgs& a, int64_t qrow, int q_len,
+                                            int64_t kv_len) {
+  return qrow >= 0 && qrow + q_len <= a.q_rows && kv_len >= 0 && kv_len <= a.S_kv;
+}
+
 // What the producer hands the consumers with each chunk's query rows (one per
 // query buffer), so that consumers never wait on global loads between chunks.
 struct UnitMsg {
@@ -1678,6 +1686,7 @@ __device__ __forceinline__ bool combine_item(const DecodeArgs& a, int64_t pr, in
   const int ha = active_groups(a, qlen);
   const int A = a.KVN * ha;
   if (act >= A) return false;  // past the batch's active units
+  if (!lengths_fit(a, qrow, qlen, kv_len)) return false;  // (the decode kernel has reported it)
   const int hk = act / ha, hg = act % ha;
   const int c = hg * a.GH + col;
   if (c >= qlen * a.G || col >= GC) return false;  // past the unit's columns
@@ -1848,7 +1857,7 @@ __device__ __forceinline__ void weights_block(const DecodeArgs& a, const KeyWeig
   batch_lengths(a, b, &qrow, &ql, &kl64);
   const int kl = (int)min(max(kl64, (int64_t)0), (int64_t)a.S_kv);
   const UnitInfo r = unit_from(a, b, hk * a.HG, (int)qrow, ql, kl);
-  const int ncols = r.q_len * a.G;
+  const int ncols = lengths_fit(a, qrow, r.q_len, kl64) ? r.q_len * a.G : 0;
   pdl_wait();  // the decode kernel is done
   if (a.sched[5] != kDecodePlanMark || a.sched[6] != a.B || a.sched[7] != a.num_ctas ||
       *a.prefill_mark == kPrefillPlanMark)

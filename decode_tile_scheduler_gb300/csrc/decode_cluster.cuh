@@ -79,7 +79,8 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
   batch_lengths(a, b, &qrow, &ql, &kl64);
   const int kl = (int)min(max(kl64, (int64_t)0), (int64_t)a.S_kv);
   const UnitInfo r = unit_from(a, b, hk * a.HG, (int)qrow, ql, kl);
-  const int c0 = 8 * grp, ncols = min(8, r.q_len * a.G - c0);
+  const bool fits = r.q_len == 0 || lengths_fit(a, qrow, r.q_len, kl64);
+  const int c0 = 8 * grp, ncols = fits ? min(8, r.q_len * a.G - c0) : 0;
   float* w_out = WT ? o.w_out + (int64_t)pair * o.stride : nullptr;
   const float* w_in = WT && o.w_in ? o.w_in + (int64_t)pair * o.stride : nullptr;
 
@@ -411,6 +412,7 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
   }
   cluster_bar_wait();
   pdl_wait();  // (without a wait for the plan above: nothing behind this kernel overtakes it)
+  if (!fits && rank == 0 && tid == 0) atomicExch(a.err, 2);  // (behind the plan, which clears it)
 }
 
 // Steps of 16 keys that a row of the call can see, at most.

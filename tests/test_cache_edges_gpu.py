@@ -1,5 +1,7 @@
 """Edges of the attention and bounded-cache calls on the GPU: tables, lengths and
 tensors that lie outside what a call was given."""
+import copy
+
 import pytest
 import torch
 
@@ -56,3 +58,70 @@ def test_pages_outside_the_pool_read_as_zeros(kind, fp8, page, kv_layout):
             assert call.error_word() == 0
         for a, b in zip(*got):
             assert torch.isfinite(a.float()).all() and torch.equal(a, b)
+
+
+# ----------------------------------------------------------------------------
+# lengths outside a decode call's tensors
+# ----------------------------------------------------------------------------
+
+def _alone(p, b):
+    """Sequence b of a TND problem, for the 64-bit check."""
+    one, t0 = copy.copy(p), sum(p.q_lens[:b])
+    one.B, one.T, one.q_lens, one.kv_lens = 1, p.q_lens[b], p.q_lens[b:b + 1], p.kv_lens[b:b + 1]
+    one.q, one.block_table = p.q[t0:t0 + one.T], p.block_table[b:b + 1]
+    return one
+
+
+@pytest.mark.parametrize("bad", ["rows", "negative_row", "keys", "negative_keys"])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("num_sms", [0, NO_CLUSTER])
+def test_decode_lengths_outside_the_tensors(num_sms, weights, fp8, bad):
+    """A sequence whose rows lie outside q, or whose length is past the capacity:
+    it runs as empty, the error word says 2, the others get their results (not the
+    same bits: the plan cuts by the lengths of all), and nothing is written outside
+    the outputs (which lie inside larger ones here)."""
+    T, slack = 6, 40
+    p = fi.make_fia(B=3, QN=8, KVN=2, D=128, q_lens=[2, 2, 2], kv_lens=[1500, 700, 300],
+                    layout=fi.LAYOUT_TND, block_size=32, seed=33, mask_mode=fi.MASK_BAND,
+                    pre_tokens=900, first_tokens=4, device=DEV,
+                    kv_dtype=fi.KV_FP8_E4M3 if fp8 else fi.KV_BF16)
+    p.q = torch.cat([p.q.new_zeros(slack, 8, 128), p.q, p.q.new_zeros(slack, 8, 128)])[slack:-slack]
+    cap = p.block_table.shape[1] * 32
+    big = {"out": torch.full((T + 2 * slack, 8, 128), 3.0, dtype=torch.bfloat16, device=DEV),
+           "lse": torch.full((T + 2 * slack, 8, 1), 3.0, device=DEV),
+           "w": torch.full((5, 2, cap), 3.0, device=DEV)}
+
+    def run():
+        for x in big.values():
+            x.fill_(3.0)
+        kw = dict(num_sms=num_sms, out=big["out"][slack:-slack], lse=big["lse"][slack:-slack])
+        call = fia.KeyWeightsCall(p, weights_out=big["w"][1:4], **kw) if weights \
+            else fia.FiaCall(p, **kw)
+        call.run()
+        torch.cuda.synchronize()
+        return call.error_word(), {n: x.clone() for n, x in big.items()}
+
+    assert run()[0] == 0
+    if bad == "rows":
+        p.cu_seqlens_q[3] += 7   # sequence 2: rows 4 and on; two of them at most are taken
+        p.cu_seqlens_q[2] += 1   # and it starts a row later, so that they pass the last one
+        hit, fine = [2], [0]
+    elif bad == "negative_row":
+        p.cu_seqlens_q[0] = -1
+        hit, fine = [0], [1, 2]
+    else:
+        p.seqused_kv[1] = cap + 1 if bad == "keys" else -3
+        hit, fine = [1], [0, 2]
+    word, got = run()
+    assert word == 2
+    rows = {0: slice(slack, slack + 2), 1: slice(slack + 2, slack + 4), 2: slice(slack + 4, slack + 6)}
+    for name in ("out", "lse"):
+        assert torch.all(got[name][:slack] == 3.0) and torch.all(got[name][slack + T:] == 3.0)
+    if bad != "negative_row":  # (the rows before the first belong to nobody)
+        last = rows[hit[0]]
+        assert torch.all(got["out"][last.stop - 1] == 3.0)
+    assert torch.all(got["w"][0] == 3.0) and torch.all(got["w"][4] == 3.0)
+    for b in fine:
+        bounded.check_attention(_alone(p, b), got["out"][rows[b]], got["lse"][rows[b]],
+                                got["w"][1 + b:2 + b] if weights else None)
