@@ -4,6 +4,7 @@ CUDA stream.  Memory and streams only -- the computation is libfia's.
 """
 from __future__ import annotations
 
+import contextlib
 import math
 from typing import Optional
 
@@ -36,6 +37,20 @@ def _stream(stream) -> int:
     if stream is None:
         return _current_stream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _made_on(stream, device: torch.device):
+    """Context in which torch allocates and fills on `stream` (None: the current
+    one).  A call that makes its own outputs and workspace and returns enters it:
+    made on the current stream, a fill could run behind the call's kernels, and
+    the workspace could go to the current stream's next tensor while they run."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = (torch.cuda.ExternalStream(handle, device=device) if handle
+                  else torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)
 
 
 def _contig(t: Optional[torch.Tensor], name: str):
@@ -117,7 +132,9 @@ def lse_shape(prob):
 
 class FiaCall:
     """One configured FIA call: owns its outputs and workspace (torch
-    allocations) and launches plan/execute/run on a stream."""
+    allocations, made on the stream that is current where the call is) and
+    launches plan/execute/run on a stream.  Keep the object until that stream
+    has run what was launched: its workspace goes with it."""
 
     def __init__(self, prob, with_lse: bool = True, num_sms: int = 0, out=None, lse=None):
         dev = prob.q.device
@@ -147,9 +164,9 @@ class FiaCall:
 
 
 def fused_infer_attention(prob, with_lse: bool = True, num_sms: int = 0, stream=None):
-    """Run FIA on a problem object; returns (out, lse)."""
-    c = FiaCall(prob, with_lse=with_lse, num_sms=num_sms)
-    return c.run(stream)
+    """Run FIA on a problem object; returns (out, lse), made on `stream`."""
+    with _made_on(stream, prob.q.device):
+        return FiaCall(prob, with_lse=with_lse, num_sms=num_sms).run(stream)
 
 
 # ----------------------------------------------------------------------------
@@ -394,7 +411,9 @@ class KvEvictCall:
     to the lowest slot) -- and the kept keys past the budget move into the evicted
     slots below it.  run() returns (seqused_out, weights_out, positions_out); the
     outputs default to new tensors, and weights_out / positions_out may be the
-    inputs themselves."""
+    inputs themselves.  New tensors and the workspace are made on the stream that is
+    current where the call is: order a run on another stream behind it, and keep
+    the object until that stream has run it (kv_evict takes care of both)."""
 
     def __init__(self, cache: KvCache, seqused_kv: torch.Tensor, weights: torch.Tensor, *,
                  budget: int, first_tokens: int = 0, recent_tokens: int = 0,
@@ -443,8 +462,9 @@ class KvEvictCall:
 def kv_evict(cache: KvCache, seqused_kv: torch.Tensor, weights: torch.Tensor, *, stream=None,
              **kw):
     """Cut the cache down to a budget (KvEvictCall's arguments); returns
-    (seqused_out, weights_out, positions_out)."""
-    return KvEvictCall(cache, seqused_kv, weights, **kw).run(stream)
+    (seqused_out, weights_out, positions_out), made on `stream`."""
+    with _made_on(stream, cache.device):
+        return KvEvictCall(cache, seqused_kv, weights, **kw).run(stream)
 
 
 # ----------------------------------------------------------------------------

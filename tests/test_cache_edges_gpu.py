@@ -7,6 +7,7 @@ import torch
 
 import decode_tile_scheduler_gb300 as fia
 import fia_inputs as fi
+from decode_tile_scheduler_gb300 import api
 from tests import bounded
 
 pytestmark = pytest.mark.gpu
@@ -125,3 +126,68 @@ def test_decode_lengths_outside_the_tensors(num_sms, weights, fp8, bad):
     for b in fine:
         bounded.check_attention(_alone(p, b), got["out"][rows[b]], got["lse"][rows[b]],
                                 got["w"][1 + b:2 + b] if weights else None)
+
+
+# ----------------------------------------------------------------------------
+# the stream argument
+# ----------------------------------------------------------------------------
+
+def _handle(s, as_int):
+    return s.cuda_stream if as_int else s
+
+
+@pytest.mark.parametrize("as_int", [False, True])
+def test_evict_on_a_stream_while_the_current_one_is_busy(as_int):
+    """kv_evict(stream=s): the fills of the tensors that it makes come before its
+    kernel, whatever the current stream still has to do."""
+    B, KVN, D, block = 2, 2, 128, 32
+    g = torch.Generator().manual_seed(3)
+    pools = [torch.randn(20, block, KVN, D, generator=g).to(torch.bfloat16).to(DEV) for _ in "kv"]
+    table = torch.arange(8, dtype=torch.int32, device=DEV).reshape(B, 4)
+    cache = fia.KvCache(*pools, table)
+    lens = torch.tensor([100, 128], dtype=torch.int32, device=DEV)
+    w = torch.rand(B, KVN, cache.capacity, device=DEV)
+    side = torch.cuda.Stream()
+    fia.kv_evict(cache, lens.clone(), w, budget=128)  # (the library is loaded)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+    n, wo, po = fia.kv_evict(cache, lens, w, budget=64, recent_tokens=10,
+                             stream=_handle(side, as_int))
+    side.synchronize()
+    assert not torch.cuda.current_stream().query(), "the current stream was to be busy"
+    torch.cuda.synchronize()
+    assert n.tolist() == [64, 64]
+    for b in range(B):
+        for h in range(KVN):
+            kept = bounded.keep_of(w[b, h].cpu().numpy(), None, int(lens[b]), 64, 0, 10, int(lens[b]))
+            slots = po[b, h, :64].tolist()
+            assert sorted(slots) == list(kept.nonzero()[0])
+            assert torch.equal(wo[b, h, :64], w[b, h][slots])
+
+
+@pytest.mark.parametrize("as_int", [False, True])
+def test_the_workspace_of_a_call_on_a_slow_stream_stays_its_own(as_int, monkeypatch):
+    """fused_infer_attention(stream=s): its workspace is not the current stream's
+    to give away while s has not run the call."""
+    p = fi.make_fia(B=40, QN=8, KVN=2, D=128, q_lens=[1] * 40, kv_lens=[700] * 40, block_size=64,
+                    seed=35, device=DEV)
+    want = [x.clone() for x in fia.fused_infer_attention(p)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    made_on = []
+
+    class Spied(fia.FiaCall):
+        def __init__(self, *args, **kw):
+            made_on.append(torch.cuda.current_stream().cuda_stream)
+            super().__init__(*args, **kw)
+
+    monkeypatch.setattr(api, "FiaCall", Spied)
+    got = fia.fused_infer_attention(p, stream=_handle(side, as_int))
+    # (a block of the side stream's: the next tensor of that size there comes behind the call)
+    assert made_on == [side.cuda_stream]
+    torch.full((64 << 20,), 0x7f, dtype=torch.uint8, device=DEV)  # the current stream's next tensor
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
