@@ -411,7 +411,9 @@ class KvEvictCall:
     to the lowest slot) -- and the kept keys past the budget move into the evicted
     slots below it.  run() returns (seqused_out, weights_out, positions_out); the
     outputs default to new tensors, and weights_out / positions_out may be the
-    inputs themselves.  New tensors and the workspace are made on the stream that is
+    inputs themselves.  seqused_out is never seqused_kv: problems and calls that hold
+    the old length tensor go on with the old lengths until the new ones are copied
+    into it.  New tensors and the workspace are made on the stream that is
     current where the call is: order a run on another stream behind it, and keep
     the object until that stream has run it (kv_evict takes care of both)."""
 
