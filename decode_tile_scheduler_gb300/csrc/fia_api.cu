@@ -110,6 +110,10 @@ int64_t kv_capacity_of(const fia_params* p) {
   return p->block_table ? (int64_t)p->max_blocks_per_seq * p->block_size : p->max_seqlen_kv;
 }
 
+bool q_empty(const fia_params* p) {
+  return p->layout == FIA_LAYOUT_TND ? p->total_q == 0 : p->max_seqlen_q == 0;
+}
+
 fia_status validate(const fia_params* p) {
   if (!p) return FIA_ERR_NULL_ARG;
   for (int i = 0; i < 7; ++i)
@@ -151,7 +155,9 @@ fia_status validate(const fia_params* p) {
   if (p->q_token_stride && (p->q_token_stride < ND || p->q_token_stride % 8)) return FIA_ERR_BAD_SHAPE;
   if (p->out_token_stride && (p->out_token_stride < ND || p->out_token_stride % 8))
     return FIA_ERR_BAD_SHAPE;
-  if (!p->q || !p->out || !p->k_cache || !p->v_cache) return FIA_ERR_NULL_ARG;
+  // (tensors of no query rows have no address)
+  if (!q_empty(p) && (!p->q || !p->out)) return FIA_ERR_NULL_ARG;
+  if (!p->k_cache || !p->v_cache) return FIA_ERR_NULL_ARG;
   if (!aligned16(p->q) || !aligned16(p->out) || !aligned16(p->k_cache) || !aligned16(p->v_cache))
     return FIA_ERR_BAD_SHAPE;
   if (p->lse && (reinterpret_cast<uintptr_t>(p->lse) & 3u)) return FIA_ERR_BAD_SHAPE;
@@ -604,10 +610,6 @@ SparseArgs sparse_args(const sparse_attn_params* p, const SparsePlan& pl, void* 
   return a;
 }
 
-bool q_empty(const fia_params* p) {
-  return p->layout == FIA_LAYOUT_TND ? p->total_q == 0 : p->max_seqlen_q == 0;
-}
-
 // ---------------------------------------------------------------------------
 // key weights
 // ---------------------------------------------------------------------------
@@ -617,7 +619,7 @@ fia_status weights_validate(const fia_params* p, const fia_weights_params* w) {
   if (!w) return FIA_ERR_NULL_ARG;
   for (int i = 0; i < 8; ++i)
     if (w->reserved[i] != 0) return FIA_ERR_BAD_SHAPE;
-  if (!w->weights_out || !p->lse) return FIA_ERR_NULL_ARG;
+  if (!w->weights_out || (!q_empty(p) && !p->lse)) return FIA_ERR_NULL_ARG;
   if ((reinterpret_cast<uintptr_t>(w->weights_in) | reinterpret_cast<uintptr_t>(w->weights_out)) & 3u)
     return FIA_ERR_BAD_SHAPE;
   if (w->state_stride < kv_capacity_of(p)) return FIA_ERR_BAD_SHAPE;
@@ -870,7 +872,8 @@ fia_status fia_plan(const fia_params* p, void* ws, size_t ws_bytes, void* stream
   if (st != FIA_OK) return st;
   if (!ws || ws_bytes < (size_t)l.total_bytes) return FIA_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (q_empty(p)) return FIA_OK;
+  if (q_empty(p))  // nothing to plan; the error word is clean
+    return cudaMemsetAsync(ws, 0, sizeof(int32_t), s) == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
   if (l.branch == 2) {
     PrefillPlan pp;
     st = prefill_plan(p, &pp);

@@ -159,7 +159,9 @@ extern "C" fia_status fia_kv_append(const fia_append_params* p, void* stream) {
   const bool tnd = p->layout == FIA_LAYOUT_TND;
   if (tnd ? p->total_q < 0 : p->seqlen_q < 0 || p->seqlen_q > 20971520) return FIA_ERR_BAD_SHAPE;
   if (tnd && !p->cu_seqlens_q) return FIA_ERR_NULL_ARG;
-  if (!p->k_new || !p->v_new || !p->seqused_kv) return FIA_ERR_NULL_ARG;
+  const int64_t rows = tnd ? p->total_q : (int64_t)p->cache.batch * p->seqlen_q;
+  // (a tensor of no rows has no address)
+  if ((rows && (!p->k_new || !p->v_new)) || !p->seqused_kv) return FIA_ERR_NULL_ARG;
   if (!aligned_to(p->k_new, 16) || !aligned_to(p->v_new, 16)) return FIA_ERR_BAD_SHAPE;
   const int64_t nd = (int64_t)p->cache.num_kv_heads * p->cache.head_dim;
   for (const int64_t s : {p->k_token_stride, p->v_token_stride})
@@ -185,7 +187,6 @@ extern "C" fia_status fia_kv_append(const fia_append_params* p, void* stream) {
   a.stride = p->state_stride;
   a.status = p->status;
   a.S = p->seqlen_q;
-  const int64_t rows = tnd ? p->total_q : (int64_t)p->cache.batch * p->seqlen_q;
   if (rows == 0) return FIA_OK;
   const int64_t grid = (rows * a.c.KVN * (a.c.D / (a.c.fp8 ? 16 : 8)) + 255) / 256;
   // (the kernel counts rows, and groups of eight threads, in 32 bits)

@@ -137,7 +137,7 @@ typedef struct fia_params {
                               /* lengths (1 selects the decode branch)         */
     int32_t total_q;          /* TND: T (rows of q and out); BSND: ignored     */
     int32_t pad0_;
-    const void *q;            /* bf16                                          */
+    const void *q;            /* bf16 (may be NULL without query rows, as out) */
     void *out;                /* bf16, same layout and strides as q            */
     float *lse;               /* fp32, nullable: BSND [B,Q_N,S_q,1],           */
                               /* TND [T,Q_N,1]                                 */
@@ -356,7 +356,7 @@ typedef struct fia_append_params {
     int32_t seqlen_q;         /* BSND: S; TND: ignored                         */
     int32_t total_q;          /* TND: T; BSND: ignored                         */
     int32_t pad0_;
-    const void *k_new;        /* bf16, 16-byte aligned                         */
+    const void *k_new;        /* bf16, 16-byte aligned (no rows: may be NULL)  */
     const void *v_new;        /* bf16, 16-byte aligned                         */
     int64_t k_token_stride;   /* elements between tokens (0: KV_N*D), a         */
     int64_t v_token_stride;   /* multiple of 8                                 */
@@ -382,7 +382,8 @@ fia_status fia_kv_append(const fia_append_params *p, void *stream);
  * may differ from fia_run's in their last bits: few units take a kernel of
  * their own.)  Slots at
  * or past kv_len are left as they were.  weights_in may be NULL (zeros) or
- * weights_out itself; other overlaps are not allowed.  p->lse is required.
+ * weights_out itself; other overlaps are not allowed.  p->lse is required,
+ * except without query rows (weights_out is then weights_in).
  * The workspace is fia_get_weights_workspace_size's, larger than
  * fia_get_workspace_size's; fia_plan on it, then fia_execute_weights any
  * number of times, or fia_run_weights for both.  It grows with the cache's

@@ -191,3 +191,37 @@ def test_the_workspace_of_a_call_on_a_slow_stream_stays_its_own(as_int, monkeypa
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+# ----------------------------------------------------------------------------
+# no rows
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("layout", [fi.LAYOUT_TND, fi.LAYOUT_BSND])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_calls_of_no_rows(layout, fp8):
+    """A batch of which no sequence has a query row: real tensors, which are empty."""
+    B, KVN, D = 3, 2, 128
+    p = fi.make_fia(B=B, QN=8, KVN=KVN, D=D, q_lens=[0] * B, kv_lens=[70, 0, 33], layout=layout,
+                    block_size=32, seed=37, device=DEV, mask_mode=fi.MASK_RIGHT_DOWN_CAUSAL,
+                    kv_dtype=fi.KV_FP8_E4M3 if fp8 else fi.KV_BF16)
+    assert p.q.numel() == 0
+    call = fia.FiaCall(p)
+    call.ws.fill_(0x7f)
+    out, lse = call.run()
+    assert out.numel() == 0 and lse.numel() == 0 and call.error_word() == 0
+    w = torch.rand(B, KVN, p.block_table.shape[1] * 32, device=DEV)
+    call = fia.KeyWeightsCall(p, weights=w)
+    got = call.run()[2]
+    assert call.error_word() == 0
+    for b, n in enumerate(p.kv_lens):
+        assert torch.equal(got[b, :, :n], w[b, :, :n]) and torch.all(got[b, :, n:] == 0)
+    assert torch.all(fia.KeyWeightsCall(p).run()[2] == 0)
+
+    cache = fia.KvCache(p.k_cache, p.v_cache, p.block_table, k_scale=p.k_scale, v_scale=p.v_scale)
+    before = [x.clone() for x in (p.k_cache, p.v_cache, w)]
+    new = torch.zeros((0, KVN, D) if layout == fi.LAYOUT_TND else (B, 0, KVN, D),
+                      dtype=torch.bfloat16, device=DEV)
+    fia.kv_append(cache, new, new, p.seqused_kv, cu_seqlens_q=p.cu_seqlens_q, weights=w)
+    for x, y in zip((p.k_cache, p.v_cache, w), before):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
