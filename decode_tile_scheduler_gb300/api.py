@@ -1,6 +1,6 @@
 """PyTorch-facing helpers: build the C-ABI parameter structs from tensors,
-allocate outputs and workspaces with torch, and launch on torch's current
-CUDA stream.  Memory and streams only -- the computation is libfia's.
+allocate outputs and workspaces with torch, and launch on the tensors' device, on
+torch's current CUDA stream there.  Memory and streams only -- the computation is libfia's.
 """
 from __future__ import annotations
 
@@ -37,6 +37,20 @@ def _stream(stream) -> int:
     if stream is None:
         return _current_stream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(device: torch.device, stream=None):
+    """Context in which `device` is the current one.  libfia launches on the current
+    device and asks it for its SMs, whatever device the pointers belong to, and the
+    default stream's handle names no device; so every call enters its tensors'.  A
+    stream of another device is refused (a bare handle cannot be told)."""
+    of = getattr(stream, "device", None)
+    if of is not None and of != device:
+        raise ValueError(f"the stream is on {of}, the tensors on {device}")
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _made_on(stream, device: torch.device):
@@ -80,6 +94,12 @@ def make_fia_params(*, q: torch.Tensor, out: torch.Tensor, k_cache: torch.Tensor
     mask): keys below it stay visible beside the window."""
     for name, t in (("q", q), ("out", out), ("k_cache", k_cache), ("v_cache", v_cache)):
         _contig(t, name)
+    for name, t in (("out", out), ("k_cache", k_cache), ("v_cache", v_cache), ("lse", lse),
+                    ("k_scale", k_scale), ("v_scale", v_scale), ("block_table", block_table),
+                    ("cu_seqlens_q", cu_seqlens_q), ("seqused_kv", seqused_kv), ("sinks", sinks),
+                    ("atten_mask", atten_mask)):
+        if t is not None and t.device != q.device:
+            raise ValueError(f"{name} is on {t.device}, q on {q.device}")
     p = FiaParams()
     p.batch, p.num_q_heads, p.num_kv_heads, p.head_dim = batch, num_q_heads, num_kv_heads, head_dim
     p.layout, p.max_seqlen_q, p.total_q = layout, max_seqlen_q, total_q
@@ -137,27 +157,32 @@ class FiaCall:
     has run what was launched: its workspace goes with it."""
 
     def __init__(self, prob, with_lse: bool = True, num_sms: int = 0, out=None, lse=None):
-        dev = prob.q.device
+        dev = self.device = prob.q.device
         self.prob = prob
         self.out = torch.empty_like(prob.q) if out is None else out
         self.lse = (torch.empty(lse_shape(prob), dtype=torch.float32, device=dev)
                     if (with_lse and lse is None) else lse)
         self.params = params_from_problem(prob, self.out, self.lse, num_sms)
-        self.ws_bytes = _abi.fia_get_workspace_size(self.params)
+        with _on(dev):
+            self.ws_bytes = _abi.fia_get_workspace_size(self.params)
         self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=dev)
 
     def plan(self, stream=None):
-        _abi.fia_plan(self.params, self.ws.data_ptr(), self.ws_bytes, _stream(stream))
+        with _on(self.device, stream):
+            _abi.fia_plan(self.params, self.ws.data_ptr(), self.ws_bytes, _stream(stream))
 
     def execute(self, stream=None):
-        _abi.fia_execute(self.params, self.ws.data_ptr(), self.ws_bytes, _stream(stream))
+        with _on(self.device, stream):
+            _abi.fia_execute(self.params, self.ws.data_ptr(), self.ws_bytes, _stream(stream))
 
     def run(self, stream=None):
-        _abi.fia_run(self.params, self.ws.data_ptr(), self.ws_bytes, _stream(stream))
+        with _on(self.device, stream):
+            _abi.fia_run(self.params, self.ws.data_ptr(), self.ws_bytes, _stream(stream))
         return self.out, self.lse
 
     def plan_layout(self):
-        return _abi.fia_get_plan_layout(self.params)
+        with _on(self.device):
+            return _abi.fia_get_plan_layout(self.params)
 
     def error_word(self) -> int:
         return int(self.ws[:4].view(torch.int32).item())
@@ -285,9 +310,6 @@ class KvCache:
     def _state(self, t, name, dtype):
         return _state(t, name, dtype, self.batch, self.num_kv_heads, self.capacity, self.device)
 
-    def _stream(self, stream) -> int:
-        return _current_stream(self.device.index) if stream is None else _stream(stream)
-
 
 class KvAppendCall:
     """fia_kv_append with its buffers: the new rows k_new, v_new (bf16 [B, S, KV
@@ -355,7 +377,8 @@ class KvAppendCall:
         return step
 
     def run(self, stream=None):
-        _abi.fia_kv_append(self.params, self.cache._stream(stream))
+        with _on(self.cache.device, stream):
+            _abi.fia_kv_append(self.params, _stream(stream))
 
 
 def kv_append(cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, seqused_kv: torch.Tensor,
@@ -374,7 +397,7 @@ class KeyWeightsCall(FiaCall):
 
     def __init__(self, prob, weights: Optional[torch.Tensor] = None,
                  weights_out: Optional[torch.Tensor] = None, num_sms: int = 0, out=None, lse=None):
-        dev = prob.q.device
+        dev = self.device = prob.q.device
         self.prob = prob
         self.out = torch.empty_like(prob.q) if out is None else out
         self.lse = (torch.empty(lse_shape(prob), dtype=torch.float32, device=dev)
@@ -391,16 +414,19 @@ class KeyWeightsCall(FiaCall):
         w.weights_out, s2 = _state(self.weights_out, "weights_out", torch.float32, prob.B,
                                    prob.KVN, capacity, dev)
         w.state_stride = _one_stride((s1, s2), "weights and weights_out")
-        self.ws_bytes = _abi.fia_get_weights_workspace_size(self.params, w)
+        with _on(dev):
+            self.ws_bytes = _abi.fia_get_weights_workspace_size(self.params, w)
         self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=dev)
 
     def execute(self, stream=None):
-        _abi.fia_execute_weights(self.params, self.weights_params, self.ws.data_ptr(),
-                                 self.ws_bytes, _stream(stream))
+        with _on(self.device, stream):
+            _abi.fia_execute_weights(self.params, self.weights_params, self.ws.data_ptr(),
+                                     self.ws_bytes, _stream(stream))
 
     def run(self, stream=None):
-        _abi.fia_run_weights(self.params, self.weights_params, self.ws.data_ptr(), self.ws_bytes,
-                             _stream(stream))
+        with _on(self.device, stream):
+            _abi.fia_run_weights(self.params, self.weights_params, self.ws.data_ptr(),
+                                 self.ws_bytes, _stream(stream))
         return self.out, self.lse, self.weights_out
 
 
@@ -456,8 +482,8 @@ class KvEvictCall:
         self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=cache.device)
 
     def run(self, stream=None):
-        _abi.fia_kv_evict(self.params, self.ws.data_ptr(), self.ws_bytes,
-                          self.cache._stream(stream))
+        with _on(self.cache.device, stream):
+            _abi.fia_kv_evict(self.params, self.ws.data_ptr(), self.ws_bytes, _stream(stream))
         return self.seqused_out, self.weights_out, self.positions_out
 
 
@@ -515,7 +541,8 @@ class SparseCall:
         self.ws_bytes = 0
 
     def plan(self, stream=None):
-        n = _abi.sparse_attn_metadata(self.params, self.metadata.data_ptr(), _stream(stream))
+        with _on(self.out.device, stream):
+            n = _abi.sparse_attn_metadata(self.params, self.metadata.data_ptr(), _stream(stream))
         if self.ws is None or self.ws.numel() < n:
             self.ws = torch.empty(max(n, 256), dtype=torch.uint8, device=self.out.device)
         self.ws_bytes = n
@@ -523,8 +550,9 @@ class SparseCall:
     def run(self, stream=None):
         if self.ws is None:
             self.plan(stream)
-        _abi.sparse_attn_run(self.params, self.metadata.data_ptr(), self.ws.data_ptr(),
-                             self.ws_bytes, _stream(stream))
+        with _on(self.out.device, stream):
+            _abi.sparse_attn_run(self.params, self.metadata.data_ptr(), self.ws.data_ptr(),
+                                 self.ws_bytes, _stream(stream))
         return self.out, self.lse
 
 
@@ -556,5 +584,6 @@ def lse_combine(outs, lses, *, layout: int, num_heads: int, batch: int = 0, seql
     c.o_parts = ctypes.cast(o_arr, ctypes.POINTER(ctypes.c_void_p))
     c.lse_parts = ctypes.cast(l_arr, ctypes.POINTER(ctypes.c_void_p))
     c.out, c.lse, c.sinks = _ptr(out), _ptr(lse), _ptr(sinks)
-    _abi.fia_lse_combine(c, _stream(stream))
+    with _on(out.device, stream):
+        _abi.fia_lse_combine(c, _stream(stream))
     return out, lse

@@ -32,7 +32,8 @@
  * Every pointer in a params struct is a DEVICE pointer unless stated
  * otherwise.  The caller owns every buffer; the library never allocates,
  * never synchronises the host and launches only on the given stream, so the
- * execute calls can be captured in a CUDA graph.  All functions return a
+ * execute calls can be captured in a CUDA graph.  It launches on the calling
+ * thread's current device, to which the pointers and the stream must belong.  All functions return a
  * status code; no C++ exception crosses this boundary.  `stream` is a
  * cudaStream_t passed as void* (NULL = the legacy default stream).
  *

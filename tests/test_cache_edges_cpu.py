@@ -1,10 +1,14 @@
 """Edges of the attention and bounded-cache calls that need no GPU: what they take
 and refuse, and which device they launch on."""
+import contextlib
 import ctypes
+from types import SimpleNamespace
 
 import pytest
+import torch
 
 import decode_tile_scheduler_gb300 as fia
+from decode_tile_scheduler_gb300 import _abi, api
 from tests.test_bounded_cache_cpu import FAKE, _append, _fia_params, _weights_status
 
 
@@ -32,3 +36,101 @@ def test_attention_of_no_rows_takes_no_address(rows):
             fia.FIA_ERR_NULL_ARG
     p = _fia_params(k_cache=0, **rows)
     assert fia.lib().fia_get_workspace_size(ctypes.byref(p), ctypes.byref(n)) == fia.FIA_ERR_NULL_ARG
+
+
+# ----------------------------------------------------------------------------
+# the device that a call launches on (stand-ins for a second GPU)
+# ----------------------------------------------------------------------------
+
+OTHER = torch.device("cuda", 1)
+
+
+class _Tensor:
+    """What the calls ask of a tensor on the other device."""
+    device, is_cuda, shape = OTHER, True, (4, 8, 128)
+
+    def data_ptr(self):
+        return FAKE
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return 1 << 20
+
+
+@pytest.fixture
+def launches(monkeypatch):
+    """Every C call as (name, current device, stream handle), device 0 current."""
+    seen, current = [], [0]
+
+    @contextlib.contextmanager
+    def device(d):
+        before, current[0] = current[0], torch.device(d).index
+        yield
+        current[0] = before
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(api, "_current_stream", lambda index: 1000 + index)
+    for name in ("fia_plan", "fia_execute", "fia_run", "fia_execute_weights", "fia_run_weights",
+                 "fia_kv_append", "fia_kv_evict", "sparse_attn_metadata", "sparse_attn_run",
+                 "fia_lse_combine", "fia_get_plan_layout"):
+        monkeypatch.setattr(_abi, name, lambda *a, name=name: seen.append(
+            (name, current[0], a[-1] if name != "fia_get_plan_layout" else None)) or 0)
+    yield seen
+    assert current[0] == 0
+
+
+def _call(kind, **attrs):
+    c = object.__new__(kind)
+    for k, v in dict(device=OTHER, params=None, weights_params=None, ws=_Tensor(), ws_bytes=0,
+                     out=_Tensor(), lse=None, metadata=_Tensor(), weights_out=None,
+                     seqused_out=None, positions_out=None,
+                     cache=SimpleNamespace(device=OTHER), **attrs).items():
+        setattr(c, k, v)
+    return c
+
+
+CALLS = [(fia.KvAppendCall, "run"), (fia.KvEvictCall, "run"), (fia.KeyWeightsCall, "run"),
+         (fia.KeyWeightsCall, "execute"), (fia.KeyWeightsCall, "plan"), (fia.FiaCall, "run"),
+         (fia.FiaCall, "execute"), (fia.FiaCall, "plan"), (fia.SparseCall, "plan"),
+         (fia.SparseCall, "run")]
+
+
+@pytest.mark.parametrize("kind,method", CALLS)
+def test_calls_launch_on_their_tensors_device(kind, method, launches):
+    getattr(_call(kind), method)()
+    assert launches and all(x[1:] == (1, 1001) for x in launches)
+    del launches[:]
+    getattr(_call(kind), method)(77)
+    assert all(x[1:] == (1, 77) for x in launches)
+    del launches[:]
+    own = SimpleNamespace(device=OTHER, cuda_stream=78)
+    getattr(_call(kind), method)(own)
+    assert all(x[1:] == (1, 78) for x in launches)
+    del launches[:]
+    for cuda_stream in (0, 5):
+        with pytest.raises(ValueError, match="cuda:0"):
+            getattr(_call(kind), method)(SimpleNamespace(device=torch.device("cuda", 0),
+                                                         cuda_stream=cuda_stream))
+    assert not launches
+
+
+def test_combine_and_plan_layout_on_their_tensors_device(launches):
+    t = _Tensor()
+    fia.lse_combine([t], [t], layout=fia.LAYOUT_TND, num_heads=8, total_q=4, out=t, lse=t)
+    _call(fia.FiaCall).plan_layout()
+    assert launches == [("fia_lse_combine", 1, 1001), ("fia_get_plan_layout", 1, None)]
+
+
+def test_a_problem_on_two_devices_is_refused():
+    t, far = _Tensor(), _Tensor()
+    far.device = torch.device("cuda", 0)
+    names = ("out", "k_cache", "v_cache", "lse", "block_table", "seqused_kv", "sinks")
+    for name in names:
+        kw = dict.fromkeys(names, t)
+        kw[name] = far
+        with pytest.raises(ValueError, match=name):
+            api.make_fia_params(q=t, num_q_heads=8, num_kv_heads=2, head_dim=128, batch=4,
+                                layout=fia.LAYOUT_BSND, max_seqlen_q=1, **kw)
