@@ -129,6 +129,7 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
   __syncthreads();
 
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  int vexp[2] = {1, 1};  // FP8: O is kept over 2^(vexp - 127), per half of D
   float O[NV][4][4];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -243,6 +244,22 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
     }
 
     // ---- softmax: this warp's running maximum and sum ----
+    // FP8: P times its V scale is multiplied in fp16 (the codes are fp16 values, and
+    // bf16 would drop three bits of P), over a power of two near the largest scale so
+    // far, which keeps it below 4; a new one moves O by an exact factor.
+    float ratio[2], over[2];
+    if constexpr (FP8) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t bits = max(__float_as_uint(fabsf(i ? vsc[0].y : vsc[0].x)),
+                                  __float_as_uint(fabsf(i ? vsc[1].y : vsc[1].x)));
+        const int en = max(vexp[i], min((int)(__reduce_max_sync(0xffffffffu, bits) >> 23), 253));
+        // (a jump past 2^-126 leaves a negligible old sum and gives 0)
+        ratio[i] = __int_as_float(max(127 + vexp[i] - en, 0) << 23);
+        over[i] = __int_as_float((254 - en) << 23);
+        vexp[i] = en;
+      }
+    }
     float p[4];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -259,19 +276,23 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          O[i][k][e] *= corr;
-          O[i][k][2 + e] *= corr;
+          O[i][k][e] *= FP8 ? corr * ratio[i] : corr;
+          O[i][k][2 + e] *= FP8 ? corr * ratio[i] : corr;
         }
     }
 
-    // ---- O^T += V^T P: P is rounded to bf16 here (FP8: times its V scale) ----
+    // ---- O^T += V^T P: P is rounded to bf16 here (FP8: to fp16, see above) ----
+    uint32_t b0, b1;
+    if constexpr (!FP8) {
+      b0 = movmatrix_t(pack_bf16(p[0], p[1]));
+      b1 = movmatrix_t(pack_bf16(p[2], p[3]));
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      uint32_t b0, b1;
-      if (FP8 || i == 0) {
-        const float v0 = !FP8 ? 1.f : i ? vsc[0].y : vsc[0].x, v1 = !FP8 ? 1.f : i ? vsc[1].y : vsc[1].x;
-        b0 = movmatrix_t(pack_bf16(p[0] * v0, p[1] * v0));
-        b1 = movmatrix_t(pack_bf16(p[2] * v1, p[3] * v1));
+      if constexpr (FP8) {
+        const float v0 = (i ? vsc[0].y : vsc[0].x) * over[i], v1 = (i ? vsc[1].y : vsc[1].x) * over[i];
+        b0 = movmatrix_t(pack_f16(p[0] * v0, p[1] * v0));
+        b1 = movmatrix_t(pack_f16(p[2] * v1, p[3] * v1));
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -280,16 +301,17 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
           const uint32_t sel = k & 1 ? 0x7362u : 0x5140u;  // bytes (a.e, b.e, a.e+1, b.e+1)
           const uint32_t y0 = k < 2 ? vx[0][i].x : vx[0][i].y, y1 = k < 2 ? vx[1][i].x : vx[1][i].y;
           const uint32_t y2 = k < 2 ? vx[2][i].x : vx[2][i].y, y3 = k < 2 ? vx[3][i].x : vx[3][i].y;
-          codes_bf16(__byte_perm(y0, y1, sel), f[0], f[1]);
-          codes_bf16(__byte_perm(y2, y3, sel), f[2], f[3]);
+          e4m3x4_to_f16x2x2(__byte_perm(y0, y1, sel), f[0], f[1]);
+          e4m3x4_to_f16x2x2(__byte_perm(y2, y3, sel), f[2], f[3]);
+          mma_f16(O[i][k], f, b0, b1);
         } else {
           const auto word = [&](const uint4& y) { return k == 0 ? y.x : k == 1 ? y.y : k == 2 ? y.z : y.w; };
           f[0] = __byte_perm(word(vx[0][i]), word(vx[1][i]), 0x5410);
           f[1] = __byte_perm(word(vx[0][i]), word(vx[1][i]), 0x7632);
           f[2] = __byte_perm(word(vx[2][i]), word(vx[3][i]), 0x5410);
           f[3] = __byte_perm(word(vx[2][i]), word(vx[3][i]), 0x7632);
+          mma_bf16(O[i][k], f, b0, b1);
         }
-        mma_bf16(O[i][k], f, b0, b1);
       }
     }
   }
@@ -301,11 +323,13 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
     for (int d = 4; d < 32; d <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
     if (g == 0) ml_warp[wid][2 * q4 + e] = make_float2(m[e], l[e]);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      const float back = FP8 ? __int_as_float(vexp[i] << 23) : 1.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k)  // elements 2k and 2k + 1 of piece g + 8i
         *reinterpret_cast<float2*>(&o_warp[wid][2 * q4 + e][(g + 8 * i) * 8 + 2 * k]) =
-            make_float2(O[i][k][e], O[i][k][2 + e]);
+            make_float2(back * O[i][k][e], back * O[i][k][2 + e]);
+    }
   }
   __syncthreads();
   {

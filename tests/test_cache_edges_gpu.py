@@ -1,6 +1,7 @@
 """Edges of the attention and bounded-cache calls on the GPU: tables, lengths and
 tensors that lie outside what a call was given."""
 import copy
+import math
 
 import pytest
 import torch
@@ -225,3 +226,68 @@ def test_calls_of_no_rows(layout, fp8):
     fia.kv_append(cache, new, new, p.seqused_kv, cu_seqlens_q=p.cu_seqlens_q, weights=w)
     for x, y in zip((p.k_cache, p.v_cache, w), before):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+# ----------------------------------------------------------------------------
+# the bits of P over an FP8 cache
+# ----------------------------------------------------------------------------
+
+def _check_fp16_p(p, weights):
+    """P times its V scale is multiplied in fp16 on both decode paths: half a step
+    of fp16 on each term (in the subnormal range of P over a power of two of at
+    most the largest scale: 2^-25 of it, times the code), half a step of bf16 on
+    the output, and what a score and its row's sum may be off."""
+    ref = bounded.attention(p)
+    codes = p.v_cache.view(torch.float8_e4m3fn).float().abs().cpu()
+    for num_sms in (0, NO_CLUSTER):
+        call = (fia.KeyWeightsCall if weights else fia.FiaCall)(p, num_sms=num_sms)
+        out = call.run()[0].double().cpu()
+        for b, (o, l, w, mag, A) in enumerate(ref):
+            kl = p.kv_lens[b]
+            tiny = torch.zeros(p.KVN, p.D, dtype=torch.float64)
+            for j in range(kl):
+                tiny += codes[b, j].double() * 2.0 ** -25
+            top = p.v_scale[b, :, :kl].amax(1).double().cpu().repeat_interleave(64, -1)
+            tiny = (tiny * top).repeat_interleave(p.QN // p.KVN, 0)
+            tl = bounded.lse_tolerance(p, A, kl)
+            to = 1.01 * (bounded.HALF_FP16 * mag + bounded.HALF_BF16 * o.abs()) + 2 * tl * mag + tiny
+            off = (out[b] - o).abs()
+            assert torch.all(off <= to), (num_sms, b, float((off / to).max()))
+
+
+@pytest.mark.parametrize("weights", [False, True])
+def test_p_over_an_fp8_cache_keeps_fp16_bits(weights):
+    """Of 16 keys each, 15 have a probability of the first's that lies next to the
+    middle between two bf16 values, and values that cancel the first's: rounded to
+    bf16, all 15 are off to one side by 2^-8, four times the tolerance."""
+    n, p_star = 64, 0.5 + 0.49 * 2.0 ** -8
+    p = fi.make_fia(B=1, QN=1, KVN=1, D=128, q_lens=[1], kv_lens=[n], paged=False, S_kv=n,
+                    kv_dtype=fi.KV_FP8_E4M3, scale=1.0, device=DEV,
+                    **({"mask_mode": fi.MASK_RIGHT_DOWN_CAUSAL} if weights else
+                       {"mask_mode": fi.MASK_BAND, "pre_tokens": 100, "first_tokens": 4}))
+    first = torch.arange(n, device=DEV) % 16 == 0
+    p.q.zero_()
+    p.q[..., 0] = 1.0
+    p.k_cache.zero_()
+    p.k_cache[..., 0] = 0xfe  # -448
+    p.k_scale[0, 0] = torch.where(first, 0.0, -math.log(p_star) / 448)[:, None]
+    p.v_cache[0, :, 0] = torch.where(first, 0xfe, 0x7e).to(torch.uint8)[:, None]
+    for half, unit in ((0, 2.0 ** -9), (1, 2.0 ** 7)):
+        p.v_scale[0, 0, :, half] = torch.where(first, 15 * p_star * unit, unit)
+    _check_fp16_p(p, weights)
+
+
+@pytest.mark.parametrize("weights", [False, True])
+def test_p_over_an_fp8_cache_with_far_scales(weights):
+    """V scales from 2^-20 to 2^20, several steps a warp: the power of two that O is
+    kept over moves."""
+    n = 3500
+    p = fi.make_fia(B=2, QN=4, KVN=2, D=128, q_lens=[1, 1], kv_lens=[n, 1111], paged=False, S_kv=n,
+                    kv_dtype=fi.KV_FP8_E4M3, device=DEV, seed=39, poison=False,
+                    **({"mask_mode": fi.MASK_RIGHT_DOWN_CAUSAL} if weights else
+                       {"mask_mode": fi.MASK_BAND, "pre_tokens": 3000, "first_tokens": 300}))
+    g = torch.Generator().manual_seed(40)
+    p.v_scale.copy_(2.0 ** (torch.rand(p.v_scale.shape, generator=g) * 40 - 20))
+    p.v_scale[1, :, :400] = 0.0  # zeros first
+    p.v_scale[1, :, 400:500, 1] *= 2.0 ** -100
+    _check_fp16_p(p, weights)
