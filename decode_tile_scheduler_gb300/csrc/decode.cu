@@ -23,8 +23,8 @@
 // r = c - n1*C tiles (C <= r < 2C unless c < C) in small chunks of
 // c2 = ceil(C/k) tiles, k = 2 for a bf16 cache and one query row, else 1
 // (every chunk has a fixed cost, and the FP8 and multi-row units' tiles
-// cost the consumers more).  A window call (window_chunk) takes another C, and
-// c2 = C.  The claim queue lists every big chunk
+// cost the consumers more).  A window call takes another C, and c2 = C, where
+// its units are about of one size or short (window_chunk).  The claim queue lists every big chunk
 // (batch-major, then chunk, then active unit of the batch) before every small
 // chunk (same order), so the work left at the end is always small pieces.  CTAs claim
 // chunks from the queue with one atomic each: an SM that streams faster
@@ -364,7 +364,7 @@ __device__ __forceinline__ uint32_t pack_cost(int64_t cost, int ha) {
   return (uint32_t)cost | ((uint32_t)ha << 24);
 }
 
-// Chunk size of a window call (a band with first tokens), whose units cost about
+// Chunk size of a window call (a band with first tokens), whose units mostly cost
 // the same, at most cmax tiles: s chunks to a unit take R = ceil(T / z / n) rounds
 // of z = ceil(cmax / s) tiles, every chunk about 2.6 tiles' time of its own (its
 // message, query vectors and merge), and a split call as much again for the
@@ -372,9 +372,18 @@ __device__ __forceinline__ uint32_t pack_cost(int64_t cost, int ha) {
 // the other calls cuts units of 6 to 34 tiles in two to six: measured over 48
 // shapes (bf16 and FP8, windows 512, 2048, 4096, 128 to 512 units), FP8 with four
 // rows per sequence 67 -> 51 us, bf16 41 -> 35 us, none slower by over 1 %.
+//
+// Returns 0, for the other calls' rule, where lengths shorter than a wide window
+// make the units unequal (T below 3/4 of U cmax) and z is over 24 tiles: the
+// rounds do not hold then, and such a chunk claimed late is the call's end.
+// Measured over 384 shapes of 16 to 64 sequences of 256 to 65,536 keys (windows of
+// 2048, 8192 and all; bf16 and FP8, one and four rows): one of 65,536 keys among
+// 63 of 512 204 -> 98 us, 64 of 512 to 32,768 FP8 keys 355 -> 182 us; with the
+// other rule for all unequal units the calls of shorter chunks lose up to a factor
+// of two (FP8, one of 65,536 keys among 15, window 8192: 18.5 -> 38 us).
 __device__ __forceinline__ int64_t window_chunk(const DecodeArgs& a, int64_t T, int cmax) {
   if (cmax < 1) return 1;
-  if (T > 0x7fffffffLL) return cmax;  // (no need to split)
+  if (T > 0x7fffffffLL) return 0;  // (the other calls' rule counts in 64 bits)
   // (32-bit divisions: 64-bit ones cost the step half a microsecond)
   const uint32_t s = (threadIdx.x & 31) + 1, n = (uint32_t)a.num_ctas;
   const uint32_t z = ((uint32_t)cmax + s - 1) / s;
@@ -384,7 +393,8 @@ __device__ __forceinline__ int64_t window_chunk(const DecodeArgs& a, int64_t T, 
   if (s <= 16 && s <= (uint32_t)cmax && (s == 1 || a.num_units * s <= a.max_chunks))
     key = (uint32_t)min(time, (uint64_t)0x3ffffff) * 32 + s;
   key = __reduce_min_sync(0xffffffffu, key);
-  return (int64_t)__shfl_sync(0xffffffffu, z, (int)(key & 31u) - 1);
+  const int64_t best = __shfl_sync(0xffffffffu, z, (int)(key & 31u) - 1);
+  return best > 24 && 4 * T < 3 * a.num_units * cmax ? 0 : best;
 }
 
 __global__ void __launch_bounds__(1024) decode_schedule_kernel(const DecodeArgs a) {
@@ -450,11 +460,13 @@ __global__ void __launch_bounds__(1024) decode_schedule_kernel(const DecodeArgs 
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   const int64_t T = total;
-  int64_t C = 1, c2;
+  int64_t C = 0, c2;
   if (window) {
     cmax = __reduce_max_sync(0xffffffffu, lane < (int)(blockDim.x >> 5) ? ws_cost[lane] : 0);
     c2 = C = window_chunk(a, T, cmax);
-  } else {
+  }
+  if (C == 0) {
+    C = 1;
     const int64_t per = (int64_t)a.num_ctas * a.chunks_per_cta;
     // C = max(1, ceil(T / per)), with a 32-bit division whenever T allows
     if (T > 0)

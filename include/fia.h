@@ -490,7 +490,7 @@ fia_status fia_selftest_bounded_wait(int32_t *status, uint64_t limit_ns, void *s
  * units.  (A band with first_tokens and U >= n / 8: units of c_max tiles at most, cut in s
  * chunks of C = c2 = ceil(c_max / s), the s of 1 .. 16 with the least
  * ceil(ceil(T / C) / n) (5 C + 13) + (13 if s > 1), where n W + 2k U chunks
- * suffice.)
+ * suffice; but as above where that C is over 24 and T < 3/4 U c_max.)
  * sched holds int64 {C, c2, chunks N, big chunks F, split batches M, plan
  * mark 0x4649414445434F44, B, CTA count}, then Q[B+1] (partial slots before
  * batch b: chunk i of active unit a of batch b owns slot Q[b] + i*A(b) + a),

@@ -291,3 +291,49 @@ def test_p_over_an_fp8_cache_with_far_scales(weights):
     p.v_scale[1, :, :400] = 0.0  # zeros first
     p.v_scale[1, :, 400:500, 1] *= 2.0 ** -100
     _check_fp16_p(p, weights)
+
+
+# ----------------------------------------------------------------------------
+# the chunks of a window call
+# ----------------------------------------------------------------------------
+
+def _chunk_sizes(costs, A, n, k, window):
+    """(C, c2) of the decode schedule: tiles per sequence, units per sequence, CTAs."""
+    T, U, W, cmax = sum(costs) * A, len(costs) * A, 5, max(costs)
+    if window:
+        fits = [s for s in range(1, min(16, cmax) + 1) if s == 1 or U * s <= n * W + 2 * k * U]
+        times = [(-(-(-(-T // -(-cmax // s))) // n) * (5 * -(-cmax // s) + 13) + (13 if s > 1 else 0), s)
+                 for s in fits]
+        C = -(-cmax // min(times)[1])
+        if C <= 24 or 4 * T >= 3 * U * cmax:
+            return C, C
+    C = max(1, -(-T // (n * W)))
+    return C, -(-C // k)
+
+
+@pytest.mark.parametrize("fp8,rows", [(False, 1), (True, 1), (False, 2)])
+@pytest.mark.parametrize("window,lens", [
+    (1 << 20, [60000] + [600] * 9),                  # one long chat among short ones
+    (1 << 20, [300, 20000, 9000, 700, 14000, 3000]),
+    (1 << 20, [20000, 19000, 18000, 20000]),         # of one size, whatever the window
+    (1000, [300, 20000, 9000, 700, 14000, 3000]),    # short units
+    (5000, [60000] + [600] * 9),
+    (9000, [9500, 16000, 12345]),
+])
+def test_window_calls_of_unequal_units_are_cut_as_other_calls(window, lens, fp8, rows):
+    p = fi.make_fia(B=len(lens), QN=32, KVN=8, D=128, q_lens=[rows] * len(lens), kv_lens=lens,
+                    mask_mode=fi.MASK_BAND, pre_tokens=window - 1, first_tokens=4, block_size=128,
+                    kv_dtype=fi.KV_FP8_E4M3 if fp8 else fi.KV_BF16, device=DEV, poison=False)
+    call = fia.FiaCall(p, num_sms=152)
+    call.plan()
+    torch.cuda.synchronize()
+    lay = call.plan_layout()
+    C, c2 = call.ws[lay.sched_off:lay.sched_off + 16].view(torch.int64).tolist()
+    costs = []
+    for n in lens:
+        lo, last = max(n - rows - (window - 1), 0) // 128, (n - 1) // 128
+        costs.append(last + 1 if lo <= 1 else last - lo + 2)
+    k = 2 if not fp8 and rows == 1 else 1
+    assert (C, c2) == _chunk_sizes(costs, 8, 152, k, 8 * 8 * len(lens) >= 152)
+    if len(lens) == 10 and window > 5000:  # (the rule that this is about)
+        assert C < 24
