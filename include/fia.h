@@ -115,8 +115,9 @@ typedef int fia_status;
  *  - paged (block_table != NULL): k_cache/v_cache are pools
  *    [num_blocks, block_size, KV_N, D] (BnBsH); logical row j of batch b is
  *    pool row block_table[b*max_blocks_per_seq + j/block_size]*block_size
- *    + j%block_size.  Block ids are not validated; table entries past a
- *    sequence's last block are never read.  seqused_kv is required.
+ *    + j%block_size.  A page outside [0, num_blocks) reads as zeros.  Table
+ *    entries past a sequence's last block may hold anything: they may be
+ *    loaded, but are not used.  seqused_kv is required.
  *    block_size: multiple of 16, <= 1024 (FP8: multiple of 32, <= 512).
  *  - contiguous (block_table == NULL): k_cache/v_cache are [B, max_seqlen_kv,
  *    KV_N, D]; seqused_kv optional (default max_seqlen_kv for every batch).
@@ -174,7 +175,8 @@ typedef struct fia_params {
                               /* (>= 0; 0 in every other mode).  The table      */
                               /* entries of pages that no row of a sequence     */
                               /* sees -- whole 128-key tiles between the first   */
-                              /* tokens and the window -- are never read        */
+                              /* tokens and the window -- may hold anything:    */
+                              /* they may be loaded, but are not used           */
     int32_t reserved[7];      /* must be 0                                     */
 } fia_params;
 

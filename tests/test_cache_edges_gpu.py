@@ -337,3 +337,56 @@ def test_window_calls_of_unequal_units_are_cut_as_other_calls(window, lens, fp8,
     assert (C, c2) == _chunk_sizes(costs, 8, 152, k, 8 * 8 * len(lens) >= 152)
     if len(lens) == 10 and window > 5000:  # (the rule that this is about)
         assert C < 24
+
+
+# ----------------------------------------------------------------------------
+# table entries that nobody uses
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("any_id", [1 << 30, -(1 << 31), 1 << 26])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("num_sms", [0, NO_CLUSTER])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_unused_table_entries_hold_anything(rows, num_sms, fp8, any_id, monkeypatch):
+    """Behind a sequence's last page, and in whole tiles between the first tokens and
+    the window: the same bits, and nothing to report."""
+    p = fi.make_fia(B=2, QN=8, KVN=2, D=128, q_lens=[rows] * 2, kv_lens=[1500, 600], block_size=64,
+                    layout=fi.LAYOUT_TND, mask_mode=fi.MASK_BAND, pre_tokens=200, first_tokens=5,
+                    seed=43, max_blocks=30, device=DEV,
+                    kv_dtype=fi.KV_FP8_E4M3 if fp8 else fi.KV_BF16)
+    want = [x.clone() for x in fia.FiaCall(p, num_sms=num_sms).run()]
+    p.block_table[0, 24:] = any_id
+    p.block_table[1, 10:] = any_id
+    for b, n in ((0, 1500), (1, 600)):
+        p.block_table[b, 2:(n - rows - 200) // 128 * 2] = any_id
+    for debug in "01":
+        monkeypatch.setenv("FIA_DEBUG", debug)
+        call = fia.FiaCall(p, num_sms=num_sms)
+        got = call.run()
+        torch.cuda.synchronize()
+        assert call.error_word() == 0
+        if debug == "0":
+            assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_evict_takes_no_page_behind_the_last(fp8):
+    B, KVN, D, block, g = 2, 2, 128, 32, torch.Generator().manual_seed(44)
+    shape = (40, block, KVN, D)
+    pools = [torch.randint(0, 100, shape, generator=g).to(torch.uint8 if fp8 else torch.bfloat16)
+             .to(DEV) for _ in "kv"]
+    sc = dict(k_scale=torch.rand(40, KVN, block, 2, device=DEV),
+              v_scale=torch.rand(40, KVN, block, 2, device=DEV)) if fp8 else {}
+    w = torch.rand(B, KVN, 10 * block, device=DEV)
+    lens = torch.tensor([150, 97], dtype=torch.int32, device=DEV)
+    got = []
+    for entry in (3, 1 << 30):
+        table = torch.arange(20, dtype=torch.int32, device=DEV).reshape(B, 10)
+        table[0, 5:], table[1, 4:] = entry, entry
+        mine = [x.clone() for x in pools]
+        cache = fia.KvCache(*mine, table, **{k: x.clone() for k, x in sc.items()})
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        got.append([*fia.kv_evict(cache, lens, w, budget=64, status=status), *cache.tensors, status])
+    for i, (x, y) in enumerate(zip(*got)):
+        assert i == 5 or x is None or torch.equal(x, y)  # (5: the table itself)
+    assert int(got[1][-1]) == 0
