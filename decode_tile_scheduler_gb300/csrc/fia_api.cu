@@ -446,6 +446,7 @@ PrefillArgs prefill_args(const fia_params* p, const PrefillPlan& pl, void* ws) {
   a.per_pair = pl.per_pair;
   a.layout = p->layout;
   a.S_q = p->max_seqlen_q;
+  a.q_rows = q_rows_of(p);
   a.kv_layout = p->block_table ? p->kv_layout : 0;
   a.mask = p->atten_mask;
   a.mask_bstride = p->mask_batch_stride;

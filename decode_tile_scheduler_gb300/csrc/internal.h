@@ -108,6 +108,7 @@ struct PrefillArgs {
   int B, QN, KVN, D, G, npairs, per_pair;  // per_pair query heads per unit (2, or 1 if G odd)
   int layout;
   int S_q;
+  int64_t q_rows;            // rows of q and out
   int kv_layout;             // 0 [nb, bs, KVN, D], 1 [nb, KVN, bs, D]
   const uint8_t* mask;       // explicit mask (modes 0/1) or null
   int64_t mask_bstride, mask_rstride;

@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(256) scale_max_kernel(const DequantArgs a) {
     const int run = (int)(w - pair * nrun);
     const int b = (int)(pair / a.KVN), hk = (int)(pair - (int64_t)b * a.KVN);
     const int kv_len = a.seqused_kv ? a.seqused_kv[b] : a.cap;
-    const int j_end = min(kv_len, (run + 1) * kScaleRun);
+    const int j_end = min(min(kv_len, a.cap), (run + 1) * kScaleRun);
     uint32_t mk = 0, mv = 0;
     for (int j = run * kScaleRun + lane; j < j_end; j += 32) {
       int64_t off, srow;

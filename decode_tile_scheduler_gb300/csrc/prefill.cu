@@ -135,6 +135,14 @@ __device__ __forceinline__ void seq_lengths(const PrefillArgs& a, int b, int64_t
   *kv_len = a.seqused_kv ? a.seqused_kv[b] : a.S_kv;
 }
 
+// Whether a sequence's query rows lie inside q and its length inside the cache.  One
+// that does not runs as empty, with 2 in the error word.
+__device__ __forceinline__ bool lengths_fit(const PrefillArgs& a, int64_t q_start, int64_t q_len,
+                                            int64_t kv_len) {
+  return q_len == 0 || (q_start >= 0 && q_len > 0 && q_start + q_len <= a.q_rows && kv_len >= 0 &&
+                        kv_len <= a.S_kv);
+}
+
 // Position of query row i of a sequence: right-down alignment
 // (kv_len - q_len + i) for modes 3 and 4, the row itself for the left-up
 // causal mode 2 (modes 0 and 1 do not use it).
@@ -194,6 +202,7 @@ __device__ __forceinline__ int64_t kv_phys_row(const PrefillArgs& a, int b, int 
 __global__ void __launch_bounds__(1024) prefill_schedule_kernel(const PrefillArgs a) {
   __shared__ int64_t warp_sums[32];
   __shared__ int64_t carry;
+  __shared__ int unfit;  // whether some sequence's lengths lie outside the arguments
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   pdl_trigger();  // the prefill kernel may set up while the plan is built
   const int nthr = blockDim.x;
@@ -226,7 +235,10 @@ __global__ void __launch_bounds__(1024) prefill_schedule_kernel(const PrefillArg
   };
 
   // 1. units per sequence -> prefix
-  if (tid == 0) carry = 0;
+  if (tid == 0) {
+    carry = 0;
+    unfit = 0;
+  }
   __syncthreads();
   for (int base = 0; base < a.B; base += nthr) {
     const int b = base + tid;
@@ -234,14 +246,21 @@ __global__ void __launch_bounds__(1024) prefill_schedule_kernel(const PrefillArg
     if (b < a.B) {
       int64_t qs, ql, kl;
       seq_lengths(a, b, &qs, &ql, &kl);
-      nu = (ql + kQTile - 1) / kQTile * H;
+      if (lengths_fit(a, qs, ql, kl))
+        nu = (ql + kQTile - 1) / kQTile * H;
+      else
+        unfit = 1;
     }
     int64_t ex;
     block_scan(nu, &ex);
     if (b < a.B) seq_prefix[b] = ex;
   }
-  const int64_t U = carry;
-  if (tid == 0) seq_prefix[a.B] = U;
+  // (rows that several sequences share, where cu_seqlens_q falls: the list ends)
+  const int64_t U = min(carry, a.max_units);
+  if (tid == 0) {
+    if (carry > U) unfit = 1;
+    seq_prefix[a.B] = U;
+  }
   // 2. histogram of costs
   const int nb = a.max_cost + 2;
   for (int c = tid; c < nb; c += nthr) a.hist[c] = 0;
@@ -298,7 +317,7 @@ __global__ void __launch_bounds__(1024) prefill_schedule_kernel(const PrefillArg
     a.num_units[4] = a.num_ctas;
     a.claim[0] = 0;
     a.claim[1] = 0;
-    *a.err = 0;
+    *a.err = unfit ? 2 : 0;
   }
 }
 
@@ -433,9 +452,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
       int pr = (pk.y >> 26) & 0x3F;
       // an entry that names no unit of these arguments (a unit list of other
       // lengths) runs as an empty unit: nothing is loaded or written
-      const bool ent_ok = m.b >= 0 && m.b < a.B && m.hk < a.KVN && pr < a.npairs;
+      bool ent_ok = m.b >= 0 && m.b < a.B && m.hk < a.KVN && pr < a.npairs;
       if (!ent_ok) {
-        if (lane == 0) atomicExch(a.err, 2);
         m.b = 0;
         m.hk = 0;
         pr = 0;
@@ -445,6 +463,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
       m.h1 = m.h0 + 1;
       int64_t qs, ql, kl;
       seq_lengths(a, m.b, &qs, &ql, &kl);
+      ent_ok = ent_ok && lengths_fit(a, qs, ql, kl);
+      if (!ent_ok && lane == 0) atomicExch(a.err, 2);
       const int64_t i0 = (int64_t)m.t * kQTile, i1 = min(i0 + kQTile, ql) - 1;
       if (!ent_ok || i0 >= ql) ql = 0;  // no query row of the tile exists
       m.q_len = (int)ql;

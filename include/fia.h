@@ -219,8 +219,10 @@ fia_status fia_plan(const fia_params *p, void *workspace, size_t workspace_bytes
  * workspace holds no plan of these arguments (never planned, planned with
  * other shapes, or planned for the other branch since: a decode plan clears
  * the prefill plan's mark and a decode execute runs nothing while that mark
- * is set; nothing ran), when a plan entry lies outside these arguments (that
- * entry ran as empty, its loads and stores kept inside their buffers), or
+ * is set; nothing ran), when a plan entry lies outside these arguments, or a
+ * sequence's query rows outside q or its length outside the cache (that
+ * entry, that sequence ran as empty: its rows of out and lse are left as they
+ * were, its loads and stores kept inside their buffers), or
  * when a decode plan held more chunks than the workspace bound (not
  * reachable for validated inputs); 3, only with FIA_DEBUG set in the
  * environment (any value not starting with '0', read on every call), when a

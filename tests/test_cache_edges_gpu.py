@@ -390,3 +390,62 @@ def test_evict_takes_no_page_behind_the_last(fp8):
     for i, (x, y) in enumerate(zip(*got)):
         assert i == 5 or x is None or torch.equal(x, y)  # (5: the table itself)
     assert int(got[1][-1]) == 0
+
+
+# ----------------------------------------------------------------------------
+# lengths outside a prompt call's tensors
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("bad", ["rows", "negative_row", "keys", "negative_keys", "falling"])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("kind", ["causal", "window", "weights"])
+@pytest.mark.parametrize("stale", [False, True])
+def test_prompt_lengths_outside_the_tensors(stale, kind, fp8, bad):
+    """As for decode; `stale`: the lengths go wrong between the plan and the call."""
+    T, slack, q_lens = 500, 300, [150, 140, 210]
+    kw = dict(mask_mode=fi.MASK_BAND, pre_tokens=90, first_tokens=4) if kind == "window" \
+        else dict(mask_mode=fi.MASK_RIGHT_DOWN_CAUSAL)
+    p = fi.make_fia(B=3, QN=8, KVN=2, D=128, q_lens=q_lens, kv_lens=[400, 150, 300],
+                    layout=fi.LAYOUT_TND, block_size=32, seed=45, device=DEV,
+                    kv_dtype=fi.KV_FP8_E4M3 if fp8 else fi.KV_BF16, **kw)
+    wide = torch.zeros(T + 2 * slack, 8, 128, dtype=torch.bfloat16, device=DEV)
+    wide[slack:-slack] = p.q
+    p.q = wide[slack:-slack]
+    cap = p.block_table.shape[1] * 32
+    big = {"out": torch.full((T + 2 * slack, 8, 128), 3.0, dtype=torch.bfloat16, device=DEV),
+           "lse": torch.full((T + 2 * slack, 8, 1), 3.0, device=DEV),
+           "w": torch.full((5, 2, cap), 3.0, device=DEV)}
+    ends = dict(out=big["out"][slack:-slack], lse=big["lse"][slack:-slack])
+    weights = kind == "weights"
+    call = fia.KeyWeightsCall(p, weights_out=big["w"][1:4], **ends) if weights \
+        else fia.FiaCall(p, **ends)
+    if stale:
+        call.plan()
+    if bad == "rows":
+        p.cu_seqlens_q[3] += 150
+        hit = 2
+    elif bad == "negative_row":
+        p.cu_seqlens_q[0] = -130
+        hit = 0
+    elif bad == "falling":
+        p.cu_seqlens_q[2] = 140   # sequence 1 has -10 rows, sequence 2 some of sequence 0's
+        hit = 1
+    else:
+        p.seqused_kv[1] = cap + 33 if bad == "keys" else -3
+        hit = 1
+    call.execute() if stale else call.run()
+    torch.cuda.synchronize()
+    assert call.error_word() == 2
+    for name in ("out", "lse"):
+        assert torch.all(big[name][:slack] == 3.0) and torch.all(big[name][slack + T:] == 3.0)
+    assert torch.all(big["w"][0] == 3.0) and torch.all(big["w"][4] == 3.0)
+    at = slack
+    for b, n in enumerate(q_lens):
+        rows, at = slice(at, at + n), at + n
+        if bad == "falling":
+            continue  # (two sequences share rows)
+        if b == hit:
+            assert torch.all(big["out"][rows] == 3.0) and torch.all(big["lse"][rows] == 3.0)
+        else:
+            bounded.check_attention(_alone(p, b), big["out"][rows], big["lse"][rows],
+                                    big["w"][1 + b:2 + b] if weights else None)
