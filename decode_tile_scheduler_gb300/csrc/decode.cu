@@ -1151,11 +1151,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // FP8: the P V of each tile runs one tile late, beside the next tile's
     // Q K^T and softmax (two independent instruction streams per warp)
+    // Keys that count as zeros in O whatever they hold, NaN too: those past kv_len,
+    // and those between a band's first tokens and its window, which no row of the
+    // sequence sees (the other masks hide no whole key but at the end of a band).
+    const auto gone = [&](int j) {
+      return j >= kvl || (X && ((j < r.lo && j >= a.first_tokens) || j > r.hi));
+    };
     struct PendingPV {
       bool valid;
       int s;
-      int jw;
-      bool tail;
       uint32_t pb[2][NG][2];
       float fct[2][NG][2];
     } prev;
@@ -1181,18 +1185,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // V codes of KV slots 2q, 2q+1, 2q+8, 2q+9: 8 bytes per d-tile at
       // d = 64*tile + 8*g .. +7 (m-tile i covers d = 64*(i/4) + 8*g + (i%4)
-      // in fragment rows 0-7 and +4 in rows 8-15); rows past kv_len -> 0
+      // in fragment rows 0-7 and +4 in rows 8-15)
       const uint8_t* vt = smem + pp.s * Cfg::kStageBytes + Cfg::kTileBytes;
       uint2 w[4][2];
 #pragma unroll
       for (int sl = 0; sl < 4; ++sl) {
         const int slot = 2 * q4 + (sl & 1) + (sl >> 1) * 8;
         const int row = R0 + rho16(slot);
-        const bool ok = !pp.tail || (pp.jw + rho16(slot) < kvl);
 #pragma unroll
         for (int t2 = 0; t2 < 2; ++t2) {
           uint2 x = *reinterpret_cast<const uint2*>(vt + sw128(row, 4 * t2 + (g >> 1)) + 8 * (g & 1));
-          if (!ok) { x.x = 0u; x.y = 0u; }
           w[sl][t2] = x;
         }
       }
@@ -1236,7 +1238,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       // lo_last .. hi_first, and hi_first < kv_len, so a tail is an edge)
       const bool edge =
           (jw < r.lo_last) || (jw + kRowsPerWarp - 1 > r.hi_first) || (MR && a.mask != nullptr);
-      const bool tail = (jw + kRowsPerWarp > kvl);
+      // some of them are gone (the window's edges, and the tiles of first tokens)
+      const bool cut = X ? jw < r.lo || jw + kRowsPerWarp - 1 > r.hi : jw + kRowsPerWarp > kvl;
+      // all of them (seven warps of eight in a tile of a few first tokens): nothing to
+      // do, except where their scores are kept
+      if (X && !a.scores && (jw > r.hi || (jw >= a.first_tokens && jw + kRowsPerWarp <= r.lo))) {
+        // (FP8: the stage of the tile before stays held until the next one that runs.
+        // Behind a tile that ran, the window's last and the first tokens' one follow at
+        // most, and the producer needs no more than two stages for them)
+        static_assert(!FP8 || S >= 4, "a stage held over two tiles that are passed by");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+        continue;
+      }
+      if (cut) {  // their V rows (this warp alone reads its 16) become zeros
+        uint8_t* v = smem + s * Cfg::kStageBytes + Cfg::kTileBytes + (R0 + (lane >> 1)) * 128;
+        if (gone(jw + (lane >> 1))) {
+#pragma unroll
+          for (int sub = 0; sub < Cfg::kNsub; ++sub)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              *reinterpret_cast<uint4*>(v + sub * (kKvTile * 128) + (4 * (lane & 1) + k) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();  // (before the copy that overwrites them)
+        __syncwarp();
+      }
       // KV positions of fragment rows g and g+8
       const int jg0 = jw + rho16(g), jg1 = jw + rho16(g + 8);
 
@@ -1285,9 +1312,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* ks = reinterpret_cast<const float*>(stp + 2 * Cfg::kTileBytes);
         float2 k0 = *reinterpret_cast<const float2*>(ks + rowa * NT);
         float2 k1 = *reinterpret_cast<const float2*>(ks + rowb * NT);
-        if (tail) {
-          if (jg0 >= kvl) k0 = make_float2(0.f, 0.f);
-          if (jg1 >= kvl) k1 = make_float2(0.f, 0.f);
+        if (cut) {
+          if (gone(jg0)) k0 = make_float2(0.f, 0.f);
+          if (gone(jg1)) k1 = make_float2(0.f, 0.f);
         }
 #pragma unroll
         for (int ng = 0; ng < NG; ++ng) {
@@ -1409,14 +1436,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               acc[i][ng][3] *= corr[ng][1];
             }
         }
-        // rows past kv_len may hold anything (even NaN): zero their V lanes
-        bool z0 = false, z1 = false, z2 = false, z3 = false;
-        if (tail) {
-          z0 = jw + rho16(2 * q4) >= kvl;
-          z1 = jw + rho16(2 * q4 + 1) >= kvl;
-          z2 = jw + rho16(2 * q4 + 8) >= kvl;
-          z3 = jw + rho16(2 * q4 + 9) >= kvl;
-        }
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
           // A = V^T (m = d, k = KV rows): matrices (k 0-7, d lo8), (k 0-7, d hi8),
@@ -1428,12 +1447,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 sw128(row, dchunk & 7);
           uint32_t va[4];
           ldsm_x4_t(addr, va[0], va[1], va[2], va[3]);
-          if (tail) {
-            if (z0) { va[0] &= 0xffff0000u; va[1] &= 0xffff0000u; }
-            if (z1) { va[0] &= 0x0000ffffu; va[1] &= 0x0000ffffu; }
-            if (z2) { va[2] &= 0xffff0000u; va[3] &= 0xffff0000u; }
-            if (z3) { va[2] &= 0x0000ffffu; va[3] &= 0x0000ffffu; }
-          }
 #pragma unroll
           for (int ng = 0; ng < NG; ++ng) mma_bf16(acc[i][ng], va, pb[ng][0], pb[ng][1]);
         }
@@ -1442,12 +1455,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         static_assert(NT == 2, "FP8 decode is built for D = 128");
         const float* vs = reinterpret_cast<const float*>(stp + 2 * Cfg::kTileBytes + Cfg::kScaleBytes);
         const int rowa = R0 + pi8(g), rowb = R0 + 8 + pi8(g);
-        // V scales of fragment rows g, g+8 (zero past kv_len)
+        // V scales of fragment rows g, g+8 (zero where the row is gone)
         float2 v0 = *reinterpret_cast<const float2*>(vs + rowa * NT);
         float2 v1 = *reinterpret_cast<const float2*>(vs + rowb * NT);
-        if (tail) {
-          if (jg0 >= kvl) v0 = make_float2(0.f, 0.f);
-          if (jg1 >= kvl) v1 = make_float2(0.f, 0.f);
+        if (cut) {
+          if (gone(jg0)) v0 = make_float2(0.f, 0.f);
+          if (gone(jg1)) v1 = make_float2(0.f, 0.f);
         }
         // Warp-wide power-of-two reference per d-tile: 2^(e-127) with e the
         // largest exponent of a V scale seen so far (positive floats order
@@ -1488,8 +1501,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (prev.valid) pv_fp8(prev);
         prev.valid = true;
         prev.s = s;
-        prev.jw = jw;
-        prev.tail = tail;
 #pragma unroll
         for (int t2 = 0; t2 < 2; ++t2)
 #pragma unroll

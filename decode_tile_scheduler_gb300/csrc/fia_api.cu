@@ -429,6 +429,7 @@ DequantArgs dequant_args(const fia_params* p, const PrefillPlan& pl, void* ws) {
   d.debug = debug_checks();
   d.first_tokens = p->first_tokens;
   d.pre_tokens = p->pre_tokens;
+  d.next_tokens = p->next_tokens;
   d.S_q = p->max_seqlen_q;
   d.cu_seqlens_q = p->layout == FIA_LAYOUT_TND ? p->cu_seqlens_q : nullptr;
   return d;

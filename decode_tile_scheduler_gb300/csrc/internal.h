@@ -219,7 +219,7 @@ struct DequantArgs {
   int* err;                    // the workspace's error word
   int debug;                   // FIA_DEBUG: report page ids outside the pool (error word 3)
   // a band with first tokens: only the KV tiles that some row sees
-  int first_tokens, pre_tokens, S_q;
+  int first_tokens, pre_tokens, next_tokens, S_q;
   const int32_t* cu_seqlens_q; // null: S_q rows per sequence
 };
 cudaError_t launch_kv_dequant(const DequantArgs& a, int num_sms, cudaStream_t s);

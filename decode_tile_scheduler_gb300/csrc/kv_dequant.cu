@@ -55,16 +55,20 @@ __device__ __forceinline__ bool locate(const DequantArgs& a, int b, int j, int h
   return true;
 }
 
-// Whether some query row of sequence b sees a key of j's KV tile; the tiles
-// between a band's first tokens and its window are left out (a short query
-// behind a long cache would otherwise convert all of it).
-__device__ __forceinline__ bool tile_needed(const DequantArgs& a, int b, int kv_len, int j) {
-  if (a.first_tokens == 0) return true;
+// What becomes of key j of sequence b: kUsed; under a band with first tokens also
+// kZero, a key that no query row sees in a KV tile of which some are seen (it may
+// hold anything, and a scale of any size: it counts as zeros), or kLeft, a key of a
+// tile that nobody reads (a short query behind a long cache would otherwise
+// convert all of it).
+enum KeyUse { kLeft, kZero, kUsed };
+__device__ __forceinline__ KeyUse key_use(const DequantArgs& a, int b, int kv_len, int j) {
+  if (a.first_tokens == 0) return kUsed;
   const int ql = a.cu_seqlens_q ? a.cu_seqlens_q[b + 1] - a.cu_seqlens_q[b] : a.S_q;
-  const int64_t p0 = (int64_t)kv_len - ql;
-  const int64_t lo = max(p0 - a.pre_tokens, (int64_t)0) / kKvTile;
+  const int64_t lo = max((int64_t)kv_len - ql - a.pre_tokens, (int64_t)0);
+  if (j > (int64_t)kv_len - 1 + a.next_tokens) return kZero;
+  if (j >= lo || j < a.first_tokens) return kUsed;
   const int tile = j / kKvTile;
-  return tile >= lo || tile * kKvTile < a.first_tokens;
+  return tile >= lo / kKvTile || tile * kKvTile < a.first_tokens ? kZero : kLeft;
 }
 
 // Largest K and V scale of every (batch, KV head) over its visible rows: a
@@ -89,7 +93,7 @@ __global__ void __launch_bounds__(256) scale_max_kernel(const DequantArgs a) {
     uint32_t mk = 0, mv = 0;
     for (int j = run * kScaleRun + lane; j < j_end; j += 32) {
       int64_t off, srow;
-      if (!tile_needed(a, b, kv_len, j)) continue;
+      if (key_use(a, b, kv_len, j) != kUsed) continue;
       if (!locate(a, b, j, hk, 0, &off, &srow)) continue;
       for (int k = 0; k < NT; ++k) {
         mk = max(mk, __float_as_uint(fabsf(__ldg(a.k_scale + srow * NT + k))));
@@ -129,15 +133,17 @@ __global__ void __launch_bounds__(256) kv_dequant_kernel(const DequantArgs a) {
     const int b = (int)(bj / a.cap);
     const int j = (int)(bj - (int64_t)b * a.cap);
     const int kv_len = a.seqused_kv ? a.seqused_kv[b] : a.cap;
-    if (j >= kv_len || !tile_needed(a, b, kv_len, j)) continue;
+    if (j >= kv_len) continue;
+    const KeyUse use = key_use(a, b, kv_len, j);
+    if (use == kLeft) continue;
     const int hk = rest / (a.D / 16), d0 = (rest % (a.D / 16)) * 16;
     int64_t code_off, scale_row;
-    const bool in_pool = locate(a, b, j, hk, d0, &code_off, &scale_row);
+    const bool there = use == kUsed && locate(a, b, j, hk, d0, &code_off, &scale_row);
     const int64_t out_off = (((int64_t)b * a.cap + j) * a.KVN + hk) * a.D + d0;
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
       uint16_t* dst = (kv ? a.v_out : a.k_out) + out_off;
-      if (!in_pool) {  // zeros, not what an earlier call left there
+      if (!there) {  // zeros, not what an earlier call left there
         reinterpret_cast<uint4*>(dst)[0] = reinterpret_cast<uint4*>(dst)[1] = make_uint4(0u, 0u, 0u, 0u);
         continue;
       }

@@ -93,6 +93,9 @@ typedef int fia_status;
  *   4 BAND               p - pre_tokens <= j <= p + next_tokens; also, with
  *                        first_tokens = f > 0, j < f where j <= p + next_tokens
  *                        (a sliding window whose first f tokens stay visible)
+ * Keys past kv_len may hold anything, NaN too; so may the keys that no row of a
+ * sequence sees under a band with first_tokens.  Any other hidden key takes part
+ * in the products with a weight of 0: an infinite or NaN V there gives NaN.
  * Modes 2-4 are computed from positions; the pages pass them a fixed
  * 2048 x 2048 mask that encodes the same rule, which this library neither
  * needs nor reads (atten_mask must be NULL there). */

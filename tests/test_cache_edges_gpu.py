@@ -449,3 +449,46 @@ def test_prompt_lengths_outside_the_tensors(stale, kind, fp8, bad):
         else:
             bounded.check_attention(_alone(p, b), big["out"][rows], big["lse"][rows],
                                     big["w"][1 + b:2 + b] if weights else None)
+
+
+# ----------------------------------------------------------------------------
+# keys of a window call that no row sees
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows", [1, 3, 40, 150])
+@pytest.mark.parametrize("kind", ["bf16", "d64", "fp8"])
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("ahead", [0, -2])
+def test_keys_that_no_row_sees_hold_anything(ahead, weights, kind, rows):
+    """NaN, infinities and scales of any size between the first tokens and the window,
+    in tiles of which other keys are seen: the same bits as with zeros there."""
+    fp8 = kind == "fp8"
+    p = fi.make_fia(B=2, QN=8, KVN=2, D=64 if kind == "d64" else 128, q_lens=[rows] * 2,
+                    kv_lens=[1500, 700], layout=fi.LAYOUT_TND, block_size=32, seed=47,
+                    mask_mode=fi.MASK_BAND, pre_tokens=260, first_tokens=37, next_tokens=ahead,
+                    kv_dtype=fi.KV_FP8_E4M3 if fp8 else fi.KV_BF16, device=DEV)
+    hidden = []
+    for b, n in enumerate(p.kv_lens):
+        for j in list(range(37, n - rows - 260)) + list(range(n + ahead, n)):
+            hidden.append((int(p.block_table[b, j // 32]), j % 32))
+    page, row = torch.tensor(hidden).T.to(DEV)
+    scales = [3e38, float("nan"), float("inf"), 1e-3]
+    for num_sms in (0, NO_CLUSTER):
+        got = []
+        for garbage in (False, True):
+            for i, c in enumerate((p.k_cache, p.v_cache)):
+                if fp8:
+                    c[page, row] = 0x7f if garbage else 0
+                    s = (p.k_scale, p.v_scale)[i].permute(0, 2, 1, 3)
+                    s[page, row] = torch.tensor(scales, device=DEV)[row % 4][:, None, None] \
+                        if garbage else 1.0
+                else:
+                    fill = torch.tensor([float("nan"), float("inf"), -float("inf"), 3e38],
+                                        device=DEV).to(c.dtype)[row % 4]
+                    c[page, row] = fill[:, None, None] if garbage else 0.0
+            call = (fia.KeyWeightsCall if weights else fia.FiaCall)(p, num_sms=num_sms)
+            got.append([x.clone() for x in call.run()])
+        for x, y in zip(*got):
+            assert torch.isfinite(y.float()).all() and torch.equal(x, y)
+        # (as kept tensors: the 64-bit check leaves keys out that nobody sees)
+        bounded.check_attention(p, *got[1][:2], *(got[1][2:] if weights else []))
