@@ -625,6 +625,9 @@ fia_status weights_validate(const fia_params* p, const fia_weights_params* w) {
   if ((reinterpret_cast<uintptr_t>(w->weights_in) | reinterpret_cast<uintptr_t>(w->weights_out)) & 3u)
     return FIA_ERR_BAD_SHAPE;
   if (w->state_stride < kv_capacity_of(p)) return FIA_ERR_BAD_SHAPE;
+  if (rows_overlap(w->weights_in, w->weights_out, (int64_t)p->batch * p->num_kv_heads,
+                   w->state_stride, kv_capacity_of(p)))
+    return FIA_ERR_BAD_SHAPE;
   return FIA_OK;
 }
 

@@ -37,6 +37,19 @@ constexpr int kDecodeMaxRows = 16; // query rows per sequence the decode kernel 
 // consumers had 208 registers).
 inline int decode_group_heads(int rows, int cols) { return (rows == 1 && cols > 8) ? 16 : 8; }
 
+// Whether two arrays of `rows` rows, `stride` 4-byte elements apart, share an element
+// of the rows' first `cap`.  The same array twice is no overlap: calls may write
+// where they read.
+inline bool rows_overlap(const void* a, const void* b, int64_t rows, int64_t stride, int64_t cap) {
+  if (!a || !b || a == b) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  const uint64_t d = x < y ? y - x : x - y;  // bytes; rows k and k + d / (4 stride) lie next
+  const uint64_t s = 4 * (uint64_t)stride, c = 4 * (uint64_t)cap;
+  if (s == 0) return false;
+  const uint64_t k = d / s, r = d % s;
+  return (k < (uint64_t)rows && r < c) || (k + 1 < (uint64_t)rows && s - r < c);
+}
+
 // Everything the decode schedule and the decode kernel read.
 struct DecodeArgs {
   int B, QN, KVN, D, G, GH, HG;  // GH columns per unit, HG units per KV head

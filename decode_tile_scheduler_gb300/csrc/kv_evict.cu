@@ -489,6 +489,11 @@ fia_status check_evict(const fia_evict_params* p) {
     if (!aligned_to(q, 4)) return FIA_ERR_BAD_SHAPE;
   const int64_t cap = cache_capacity(p->cache);
   if (p->state_stride < cap) return FIA_ERR_BAD_SHAPE;
+  const int64_t rows = (int64_t)p->cache.batch * p->cache.num_kv_heads;
+  if (rows_overlap(p->weights_in, p->weights_out, rows, p->state_stride, cap) ||
+      rows_overlap(p->positions_in, p->positions_out, rows, p->state_stride, cap) ||
+      rows_overlap(p->seqused_kv, p->seqused_out, 1, p->cache.batch, p->cache.batch))
+    return FIA_ERR_BAD_SHAPE;
   if (p->budget < 1 || p->budget > cap) return FIA_ERR_BAD_SHAPE;
   if (p->first_tokens < 0 || p->recent_tokens < 0 ||
       (int64_t)p->first_tokens + p->recent_tokens > p->budget)

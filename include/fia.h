@@ -390,7 +390,7 @@ fia_status fia_kv_append(const fia_append_params *p, void *stream);
  * may differ from fia_run's in their last bits: few units take a kernel of
  * their own.)  Slots at
  * or past kv_len are left as they were.  weights_in may be NULL (zeros) or
- * weights_out itself; other overlaps are not allowed.  p->lse is required,
+ * weights_out itself; rows that overlap otherwise are refused.  p->lse is required,
  * except without query rows (weights_out is then weights_in).
  * The workspace is fia_get_weights_workspace_size's, larger than
  * fia_get_workspace_size's; fia_plan on it, then fia_execute_weights any
@@ -433,7 +433,8 @@ fia_status fia_run_weights(const fia_params *p, const fia_weights_params *w, voi
  *    tokens_seen NULL: seqused_kv[b].  positions_out is required with
  *    positions_in, else nullable.
  *  - weights_out and positions_out receive the kept slots' values (slots below
- *    the new length); they may be the inputs themselves or be distinct.
+ *    the new length); they may be the inputs themselves; rows that overlap
+ *    otherwise are refused, and so are lengths.
  *  - A length below 0 counts as 0, one past the capacity as the capacity.  A
  *    move whose page id lies outside [0, num_blocks) is left out (its weight
  *    and position still move) and *status (nullable, cleared by the caller)

@@ -9,7 +9,7 @@ import torch
 
 import decode_tile_scheduler_gb300 as fia
 from decode_tile_scheduler_gb300 import _abi, api
-from tests.test_bounded_cache_cpu import FAKE, _append, _fia_params, _weights_status
+from tests.test_bounded_cache_cpu import FAKE, _append, _evict, _fia_params, _weights_status
 
 
 # ----------------------------------------------------------------------------
@@ -134,3 +134,31 @@ def test_a_problem_on_two_devices_is_refused():
         with pytest.raises(ValueError, match=name):
             api.make_fia_params(q=t, num_q_heads=8, num_kv_heads=2, head_dim=128, batch=4,
                                 layout=fia.LAYOUT_BSND, max_seqlen_q=1, **kw)
+
+
+# ----------------------------------------------------------------------------
+# state that overlaps
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("shift,refused", [(0, False), (4, True), (-4, True), (1020 * 4, True),
+                                           (1024 * 4, False), (2000 * 4, True), (2048 * 4, True),
+                                           (1024 * 4 + 2048 * 4, False), (7 * 2048 * 4, True),
+                                           (8 * 2048 * 4, False), (-(7 * 2048 * 4 + 4092), True),
+                                           (-(7 * 2048 * 4 + 4096), False)])
+def test_state_rows_that_overlap_are_refused(shift, refused):
+    """Eight rows of 1024 slots, 2048 apart, against the same rows `shift` bytes on.
+    Rows between each other's, and the same tensor, are fine."""
+    far = 1 << 20
+    want = fia.FIA_ERR_BAD_SHAPE if refused else fia.FIA_OK
+    assert _evict(state_stride=2048, weights_in=far, weights_out=far + shift)[0] == want
+    assert _evict(state_stride=2048, weights_in=far, weights_out=1 << 24, positions_in=far,
+                  positions_out=far + shift)[0] == want
+    assert _weights_status(_fia_params(), state_stride=2048, weights_in=far,
+                           weights_out=far + shift)[0] == want
+
+
+def test_lengths_that_overlap_are_refused():
+    for shift in (4, 12, -4, -12):
+        assert _evict(seqused_kv=FAKE, seqused_out=FAKE + shift)[0] == fia.FIA_ERR_BAD_SHAPE
+    for shift in (16, -16):
+        assert _evict(seqused_kv=FAKE, seqused_out=FAKE + shift)[0] == fia.FIA_OK

@@ -492,3 +492,48 @@ def test_keys_that_no_row_sees_hold_anything(ahead, weights, kind, rows):
             assert torch.isfinite(y.float()).all() and torch.equal(x, y)
         # (as kept tensors: the 64-bit check leaves keys out that nobody sees)
         bounded.check_attention(p, *got[1][:2], *(got[1][2:] if weights else []))
+
+
+# ----------------------------------------------------------------------------
+# a padded batch, and a decode without a workspace
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows", [1, 3, 70])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("weights", [False, True])
+def test_rows_behind_the_last_sequence_are_left(weights, fp8, rows):
+    """q longer than cu_seqlens_q says: out and lse keep what they held there."""
+    pad = 9
+    p = fi.make_fia(B=3, QN=8, KVN=2, D=128, q_lens=[rows, 0, rows], kv_lens=[800, 90, 260],
+                    layout=fi.LAYOUT_TND, block_size=32, seed=49, mask_mode=fi.MASK_BAND,
+                    pre_tokens=200, first_tokens=4, device=DEV,
+                    kv_dtype=fi.KV_FP8_E4M3 if fp8 else fi.KV_BF16)
+    n = p.T
+    p.q, p.T = torch.cat([p.q, torch.full_like(p.q[:1], float("nan")).expand(pad, -1, -1)]), n + pad
+    for num_sms in (0, NO_CLUSTER):
+        out = torch.full_like(p.q, 3.0)
+        lse = torch.full((n + pad, 8, 1), 3.0, device=DEV)
+        call = (fia.KeyWeightsCall if weights else fia.FiaCall)(p, num_sms=num_sms, out=out, lse=lse)
+        got = call.run()
+        torch.cuda.synchronize()
+        assert call.error_word() == 0
+        assert torch.all(out[n:] == 3.0) and torch.all(lse[n:] == 3.0)
+        bounded.check_attention(p, *got)
+
+
+def test_a_window_of_few_units_without_a_workspace():
+    p = fi.make_fia(B=2, QN=8, KVN=2, D=128, q_lens=[1, 1], kv_lens=[900, 70], block_size=64, seed=51,
+                    mask_mode=fi.MASK_BAND, pre_tokens=300, first_tokens=4, device=DEV)
+    want = fia.FiaCall(p).run()
+    out, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    status = torch.full((1,), 7, dtype=torch.int32, device=DEV)
+    params = api.params_from_problem(p, out, lse)
+    for bad in (False, True):
+        if bad:
+            p.seqused_kv[1] = 1 << 20
+            out.fill_(3.0)
+        fia.fia_decode_run_noalloc(params, status.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert int(status) == (2 if bad else 0)
+        assert torch.equal(out[0], want[0][0])
+        assert torch.all(out[1] == 3.0) if bad else torch.equal(out[1], want[0][1])
