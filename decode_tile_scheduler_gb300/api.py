@@ -150,6 +150,21 @@ def lse_shape(prob):
     return (prob.T, prob.QN, 1) if prob.layout == _abi.LAYOUT_TND else (prob.B, prob.QN, prob.S_q, 1)
 
 
+def _outputs(prob, out: Optional[torch.Tensor], lse: Optional[torch.Tensor], with_lse: bool):
+    """out and lse of a call: new tensors, or the given ones, whose sizes and types
+    the kernels rely on."""
+    shape = lse_shape(prob)
+    if out is None:
+        out = torch.empty_like(prob.q)
+    elif out.numel() != prob.q.numel() or out.dtype != prob.q.dtype:
+        raise ValueError(f"out must hold q's {tuple(prob.q.shape)} in {prob.q.dtype}")
+    if lse is None:
+        lse = torch.empty(shape, dtype=torch.float32, device=prob.q.device) if with_lse else None
+    elif lse.numel() != math.prod(shape) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous float32 tensor of {shape}")
+    return out, lse
+
+
 class FiaCall:
     """One configured FIA call: owns its outputs and workspace (torch
     allocations, made on the stream that is current where the call is) and
@@ -159,9 +174,7 @@ class FiaCall:
     def __init__(self, prob, with_lse: bool = True, num_sms: int = 0, out=None, lse=None):
         dev = self.device = prob.q.device
         self.prob = prob
-        self.out = torch.empty_like(prob.q) if out is None else out
-        self.lse = (torch.empty(lse_shape(prob), dtype=torch.float32, device=dev)
-                    if (with_lse and lse is None) else lse)
+        self.out, self.lse = _outputs(prob, out, lse, with_lse)
         self.params = params_from_problem(prob, self.out, self.lse, num_sms)
         with _on(dev):
             self.ws_bytes = _abi.fia_get_workspace_size(self.params)
@@ -399,9 +412,7 @@ class KeyWeightsCall(FiaCall):
                  weights_out: Optional[torch.Tensor] = None, num_sms: int = 0, out=None, lse=None):
         dev = self.device = prob.q.device
         self.prob = prob
-        self.out = torch.empty_like(prob.q) if out is None else out
-        self.lse = (torch.empty(lse_shape(prob), dtype=torch.float32, device=dev)
-                    if lse is None else lse)
+        self.out, self.lse = _outputs(prob, out, lse, True)
         self.params = params_from_problem(prob, self.out, self.lse, num_sms)
         capacity = int(prob.S_kv if prob.block_table is None
                        else prob.block_table.shape[1] * prob.block_size)

@@ -162,3 +162,26 @@ def test_lengths_that_overlap_are_refused():
         assert _evict(seqused_kv=FAKE, seqused_out=FAKE + shift)[0] == fia.FIA_ERR_BAD_SHAPE
     for shift in (16, -16):
         assert _evict(seqused_kv=FAKE, seqused_out=FAKE + shift)[0] == fia.FIA_OK
+
+
+# ----------------------------------------------------------------------------
+# outputs that a caller brings
+# ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("layout", [fia.LAYOUT_BSND, fia.LAYOUT_TND])
+def test_outputs_of_another_size_or_type_are_refused(layout):
+    B, S, N, D = 3, 2, 4, 64
+    q = torch.zeros((B * S, N, D) if layout else (B, S, N, D), dtype=torch.bfloat16)
+    prob = SimpleNamespace(q=q, layout=layout, T=B * S, B=B, QN=N, S_q=S)
+    shape = (B * S, N, 1) if layout else (B, N, S, 1)
+    out, lse = api._outputs(prob, None, None, True)
+    assert out.shape == q.shape and out.dtype == q.dtype and tuple(lse.shape) == shape
+    assert api._outputs(prob, None, None, False)[1] is None
+    mine = torch.empty_like(q), torch.empty(shape)
+    assert all(x is y for x, y in zip(api._outputs(prob, *mine, True), mine))
+    api._outputs(prob, None, torch.empty(shape[:-1]), False)  # (without the last 1)
+    for out, lse in [(q[:1], None), (q.float(), None), (None, torch.empty(shape[1:])),
+                     (None, torch.empty(shape).double()), (None, torch.empty(*shape, 2)[..., 0])]:
+        for with_lse in (False, True):
+            with pytest.raises(ValueError):
+                api._outputs(prob, out, lse, with_lse)
