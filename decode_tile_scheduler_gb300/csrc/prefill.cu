@@ -20,8 +20,9 @@
 //               TMEM, V in shared memory), fp32 accumulators in TMEM; the two
 //               slots ping-pong, and each thread's commits and waits overlap
 //               the other slot's MMAs
-//   warp 2      V guard: zeroes V rows past kv_len in a tail tile, so that a
-//               zero probability never meets a NaN in unused cache rows
+//   warp 2      V guard: zeroes V rows past kv_len, and those that no row of the
+//               sequence sees under a band with first tokens, so that a zero
+//               probability never meets a NaN in unused cache rows
 //   warps 4-7   softmax of slot 0; warps 8-11 softmax of slot 1: one TMEM lane
 //               (query row) per thread, online softmax in the exp2 domain with
 //               a lazily moved maximum (O is rescaled only when the running

@@ -159,7 +159,9 @@ typedef struct fia_params {
     int32_t block_size;
     int32_t num_blocks;
     int32_t max_seqlen_kv;    /* contiguous KV: S_kv; paged: ignored           */
-    const int32_t *cu_seqlens_q;  /* TND: int32 [B+1], non-decreasing, last=T */
+    const int32_t *cu_seqlens_q;  /* TND: int32 [B+1], non-decreasing, last   */
+                              /* <= T: rows behind it (a padded batch) are      */
+                              /* left as they were                             */
     const int32_t *seqused_kv;    /* int32 [B]: KV length of each batch        */
     float scale;              /* multiplies Q K^T (typically 1/sqrt(D))         */
     int32_t mask_mode;        /* FIA_MASK_*                                    */
