@@ -46,9 +46,9 @@ def _on(device: torch.device, stream=None):
     """Context in which `device` is the current one.  libfia launches on the current
     device and asks it for its SMs, whatever device the pointers belong to, and the
     default stream's handle names no device; so every call enters its tensors'.  A
-    stream of another device is refused (a bare handle cannot be told)."""
+    torch stream of another device is refused (other handles cannot be told)."""
     of = getattr(stream, "device", None)
-    if of is not None and of != device:
+    if isinstance(of, torch.device) and of != device:
         raise ValueError(f"the stream is on {of}, the tensors on {device}")
     return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 

@@ -106,9 +106,9 @@ def test_calls_launch_on_their_tensors_device(kind, method, launches):
     getattr(_call(kind), method)(77)
     assert all(x[1:] == (1, 77) for x in launches)
     del launches[:]
-    own = SimpleNamespace(device=OTHER, cuda_stream=78)
-    getattr(_call(kind), method)(own)
-    assert all(x[1:] == (1, 78) for x in launches)
+    for own in (OTHER, 1, None):  # (another library's stream names its device in its own way)
+        getattr(_call(kind), method)(SimpleNamespace(device=own, cuda_stream=78))
+        assert launches and all(x[1:] == (1, 78) for x in launches)
     del launches[:]
     for cuda_stream in (0, 5):
         with pytest.raises(ValueError, match="cuda:0"):
