@@ -675,32 +675,37 @@ __global__ void __launch_bounds__(kPThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&mempty[ms]);
       if (m.done || *reinterpret_cast<volatile int*>(misc)) break;
-      // the tile's rows past `end` become zeros (past kv_len, or past what the last
-      // row sees), and so do the keys between a band's first tokens and its window
-      // that no row of the sequence sees (FP8: zeros in the converted copy)
-      const int end = X ? m.kv_len + min(a.next_tokens, 0) : m.kv_len;
+      // keys between a band's first tokens and its window, and past what the last row
+      // sees, that no row of the sequence sees: zeros too (FP8: in the converted copy)
+      constexpr bool kUnseen = X && !F16;
+      const int end = kUnseen ? m.kv_len + min(a.next_tokens, 0) : m.kv_len;
       const int gap_end =
-          X && !F16 ? (int)min((int64_t)m.kv_len - m.q_len - a.pre_tokens, (int64_t)m.kv_len) : 0;
-      const bool gap = X && !F16 && gap_end > a.first_tokens;
+          kUnseen ? (int)min((int64_t)m.kv_len - m.q_len - a.pre_tokens, (int64_t)m.kv_len) : 0;
+      const bool gap = kUnseen && gap_end > a.first_tokens;
       for (int j = 0; j < m.ntiles; ++j, ++kv_it) {
         const int vs = kv_it % VS;
         pwait(&vfull[vs], (kv_it / VS) & 1, a.err, misc);
-        const int j0 = (int)tile_key<X>(m, j);
-        const int nv = end - j0 < kKvTile ? max(end - j0, 0) : kKvTile;
-        if (nv < kKvTile || (gap && j0 < gap_end && j0 + kKvTile > a.first_tokens)) {
+        const int64_t j0 = tile_key<X>(m, j);
+        const auto zero = [&](int r0, int r1) {
           uint8_t* vt = smem + Cfg::kOffV + vs * Cfg::kTileBytes;
-          const auto zero = [&](int r0, int r1) {
-            for (int x = r0 * 8 + lane; x < r1 * 8; x += 32) {  // 16-byte pieces
-              const int row = x >> 3, piece = x & 7;
+          for (int x = r0 * 8 + lane; x < r1 * 8; x += 32) {  // 16-byte pieces
+            const int row = x >> 3, piece = x & 7;
 #pragma unroll
-              for (int sub = 0; sub < NSUB; ++sub)
-                *reinterpret_cast<uint4*>(vt + sub * 16384 + row * 128 + piece * 16) =
-                    make_uint4(0u, 0u, 0u, 0u);
-            }
-          };
-          if (gap) zero(max(a.first_tokens - j0, 0), min(gap_end - j0, (int)kKvTile));
-          zero(nv, kKvTile);
+            for (int sub = 0; sub < NSUB; ++sub)
+              *reinterpret_cast<uint4*>(vt + sub * 16384 + row * 128 + piece * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+          }
           fence_proxy_async_smem();
+        };
+        if constexpr (kUnseen) {
+          const int t0 = (int)j0;
+          if (end - t0 < kKvTile || (gap && t0 < gap_end && t0 + kKvTile > a.first_tokens)) {
+            if (gap) zero(max(a.first_tokens - t0, 0), min(gap_end - t0, (int)kKvTile));
+            zero(max(end - t0, 0), kKvTile);
+          }
+        } else {
+          const int nv = (int)min((int64_t)kKvTile, (int64_t)end - j0);
+          if (nv < kKvTile) zero(nv, kKvTile);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&vready[vs]);
