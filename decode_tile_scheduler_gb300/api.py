@@ -22,9 +22,11 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return t.data_ptr()
 
 
-# The current stream's handle without a Stream object around it (2 us of a call
-# that takes 6), where this PyTorch has the accessor.
+# The current stream's handle without a Stream object around it (2 us of a call that
+# takes 6), and the current device without a look at whether CUDA is up (0.3 us: the
+# tensors of a call are on it), where this PyTorch has the accessors.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _current_stream(device_index: int) -> int:
@@ -33,24 +35,34 @@ def _current_stream(device_index: int) -> int:
     return torch.cuda.current_stream(device_index).cuda_stream
 
 
-def _stream(stream) -> int:
-    if stream is None:
-        return _current_stream(torch.cuda.current_device())
+def _handle(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 _HERE = contextlib.nullcontext()
 
 
-def _on(device: torch.device, stream=None):
-    """Context in which `device` is the current one.  libfia launches on the current
-    device and asks it for its SMs, whatever device the pointers belong to, and the
-    default stream's handle names no device; so every call enters its tensors'.  A
-    torch stream of another device is refused (other handles cannot be told)."""
-    of = getattr(stream, "device", None)
-    if isinstance(of, torch.device) and of != device:
-        raise ValueError(f"the stream is on {of}, the tensors on {device}")
-    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _on(device: torch.device):
+    """Context in which `device` is the current one."""
+    return _HERE if device.index == _current_device() else torch.cuda.device(device)
+
+
+def _launch(device: torch.device, stream, call, *args):
+    """call(*args, stream's handle) with `device` as the current one.  libfia launches on
+    the current device and asks it for its SMs, whatever device the pointers belong
+    to, and the default stream's handle names no device; so every call enters its
+    tensors'.  A torch stream of another device is refused (other handles cannot be
+    told)."""
+    index = device.index
+    if stream is None:
+        if index == _current_device():
+            return call(*args, _current_stream(index))
+    else:
+        of = getattr(stream, "device", None)
+        if isinstance(of, torch.device) and of != device:
+            raise ValueError(f"the stream is on {of}, the tensors on {device}")
+    with _on(device):
+        return call(*args, _current_stream(index) if stream is None else _handle(stream))
 
 
 def _made_on(stream, device: torch.device):
@@ -61,7 +73,7 @@ def _made_on(stream, device: torch.device):
     if stream is None:
         return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
-        handle = _stream(stream)
+        handle = _handle(stream)
         stream = (torch.cuda.ExternalStream(handle, device=device) if handle
                   else torch.cuda.default_stream(device))
     return torch.cuda.stream(stream)
@@ -181,16 +193,14 @@ class FiaCall:
         self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=dev)
 
     def plan(self, stream=None):
-        with _on(self.device, stream):
-            _abi.fia_plan(self.params, self.ws.data_ptr(), self.ws_bytes, _stream(stream))
+        _launch(self.device, stream, _abi.fia_plan, self.params, self.ws.data_ptr(), self.ws_bytes)
 
     def execute(self, stream=None):
-        with _on(self.device, stream):
-            _abi.fia_execute(self.params, self.ws.data_ptr(), self.ws_bytes, _stream(stream))
+        _launch(self.device, stream, _abi.fia_execute, self.params, self.ws.data_ptr(),
+                self.ws_bytes)
 
     def run(self, stream=None):
-        with _on(self.device, stream):
-            _abi.fia_run(self.params, self.ws.data_ptr(), self.ws_bytes, _stream(stream))
+        _launch(self.device, stream, _abi.fia_run, self.params, self.ws.data_ptr(), self.ws_bytes)
         return self.out, self.lse
 
     def plan_layout(self):
@@ -390,8 +400,7 @@ class KvAppendCall:
         return step
 
     def run(self, stream=None):
-        with _on(self.cache.device, stream):
-            _abi.fia_kv_append(self.params, _stream(stream))
+        _launch(self.cache.device, stream, _abi.fia_kv_append, self.params)
 
 
 def kv_append(cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, seqused_kv: torch.Tensor,
@@ -430,14 +439,12 @@ class KeyWeightsCall(FiaCall):
         self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=dev)
 
     def execute(self, stream=None):
-        with _on(self.device, stream):
-            _abi.fia_execute_weights(self.params, self.weights_params, self.ws.data_ptr(),
-                                     self.ws_bytes, _stream(stream))
+        _launch(self.device, stream, _abi.fia_execute_weights, self.params, self.weights_params,
+                self.ws.data_ptr(), self.ws_bytes)
 
     def run(self, stream=None):
-        with _on(self.device, stream):
-            _abi.fia_run_weights(self.params, self.weights_params, self.ws.data_ptr(),
-                                 self.ws_bytes, _stream(stream))
+        _launch(self.device, stream, _abi.fia_run_weights, self.params, self.weights_params,
+                self.ws.data_ptr(), self.ws_bytes)
         return self.out, self.lse, self.weights_out
 
 
@@ -493,8 +500,8 @@ class KvEvictCall:
         self.ws = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=cache.device)
 
     def run(self, stream=None):
-        with _on(self.cache.device, stream):
-            _abi.fia_kv_evict(self.params, self.ws.data_ptr(), self.ws_bytes, _stream(stream))
+        _launch(self.cache.device, stream, _abi.fia_kv_evict, self.params, self.ws.data_ptr(),
+                self.ws_bytes)
         return self.seqused_out, self.weights_out, self.positions_out
 
 
@@ -552,8 +559,8 @@ class SparseCall:
         self.ws_bytes = 0
 
     def plan(self, stream=None):
-        with _on(self.out.device, stream):
-            n = _abi.sparse_attn_metadata(self.params, self.metadata.data_ptr(), _stream(stream))
+        n = _launch(self.out.device, stream, _abi.sparse_attn_metadata, self.params,
+                    self.metadata.data_ptr())
         if self.ws is None or self.ws.numel() < n:
             self.ws = torch.empty(max(n, 256), dtype=torch.uint8, device=self.out.device)
         self.ws_bytes = n
@@ -561,9 +568,8 @@ class SparseCall:
     def run(self, stream=None):
         if self.ws is None:
             self.plan(stream)
-        with _on(self.out.device, stream):
-            _abi.sparse_attn_run(self.params, self.metadata.data_ptr(), self.ws.data_ptr(),
-                                 self.ws_bytes, _stream(stream))
+        _launch(self.out.device, stream, _abi.sparse_attn_run, self.params,
+                self.metadata.data_ptr(), self.ws.data_ptr(), self.ws_bytes)
         return self.out, self.lse
 
 
@@ -595,6 +601,5 @@ def lse_combine(outs, lses, *, layout: int, num_heads: int, batch: int = 0, seql
     c.o_parts = ctypes.cast(o_arr, ctypes.POINTER(ctypes.c_void_p))
     c.lse_parts = ctypes.cast(l_arr, ctypes.POINTER(ctypes.c_void_p))
     c.out, c.lse, c.sinks = _ptr(out), _ptr(lse), _ptr(sinks)
-    with _on(out.device, stream):
-        _abi.fia_lse_combine(c, _stream(stream))
+    _launch(out.device, stream, _abi.fia_lse_combine, c)
     return out, lse

@@ -70,7 +70,7 @@ def launches(monkeypatch):
         yield
         current[0] = before
 
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(api, "_current_device", lambda: current[0])
     monkeypatch.setattr(torch.cuda, "device", device)
     monkeypatch.setattr(api, "_current_stream", lambda index: 1000 + index)
     for name in ("fia_plan", "fia_execute", "fia_run", "fia_execute_weights", "fia_run_weights",
