@@ -357,8 +357,7 @@ def _plain_pages(s):
     s.block_table.copy_(torch.where(new, torch.where(at >= 0, stack[at.clamp(min=0)], -1), s.block_table))
     got = torch.minimum(take, (top - (taken - take)).clamp(min=0))
     left = (top - taken[-1]).clamp(min=0)
-    place = torch.arange(nb, device=dev)
-    s.free_pages.copy_(torch.where((place >= count) & (place < left), stack[:nb], s.free_pages))
+    s.free_pages.copy_(stack[:nb])
     s.held_out.copy_(torch.minimum(held, need) + got)
     s.count_out.copy_(left)
     b, i, q_len = _rows_of(s, dev)
