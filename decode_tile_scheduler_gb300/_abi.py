@@ -24,6 +24,7 @@ LAYOUT_BSND = 0
 LAYOUT_TND = 1
 KV_BF16 = 0
 KV_FP8_E4M3 = 1
+KV_MXFP4 = 4
 MASK_NONE = 0
 MASK_ALL = 1
 MASK_LEFT_UP_CAUSAL = 2
@@ -126,6 +127,29 @@ class EvictParams(ctypes.Structure):
     ]
 
 
+class PagesParams(ctypes.Structure):
+    _fields_ = [
+        ("batch", _I), ("block_size", _I), ("max_blocks_per_seq", _I), ("num_blocks", _I),
+        ("layout", _I), ("seqlen_q", _I), ("total_q", _I), ("pad0_", _I),
+        ("seqused_kv", _P), ("cu_seqlens_q", _P), ("tokens_seen", _P), ("block_table", _P),
+        ("pages_held", _P), ("pages_held_out", _P), ("free_pages", _P), ("free_count", _P),
+        ("free_count_out", _P), ("slots", _P), ("positions", _P), ("status", _P),
+        ("reserved", _I * 8),
+    ]
+
+
+class NormRopeParams(ctypes.Structure):
+    _fields_ = [
+        ("cache", KvCacheParams),
+        ("tokens", _I), ("num_q_heads", _I), ("rotary_dim", _I), ("interleaved", _I),
+        ("max_positions", _I), ("eps", ctypes.c_float),
+        ("q", _P), ("k", _P), ("v", _P),
+        ("q_token_stride", _L), ("k_token_stride", _L), ("v_token_stride", _L),
+        ("q_out", _P), ("q_out_token_stride", _L), ("q_weight", _P), ("k_weight", _P),
+        ("cos_sin", _P), ("positions", _P), ("slots", _P), ("status", _P), ("reserved", _I * 8),
+    ]
+
+
 class FiaPlanLayout(ctypes.Structure):
     _fields_ = [
         ("branch", _I), ("num_ctas", _I), ("num_units", _L), ("max_chunks", _L),
@@ -143,6 +167,8 @@ EXPORTS = (
     "fia_kv_append", "fia_get_weights_workspace_size", "fia_execute_weights", "fia_run_weights",
     "fia_get_evict_workspace_size", "fia_kv_evict",
     "fia_sizeof_append_params", "fia_sizeof_weights_params", "fia_sizeof_evict_params",
+    "fia_assign_pages", "fia_norm_rope_append", "fia_sizeof_pages_params",
+    "fia_sizeof_norm_rope_params",
 )
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
@@ -183,7 +209,7 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
             L.fia_sizeof_params.restype = ctypes.c_size_t
             L.fia_sizeof_sparse_params.restype = ctypes.c_size_t
             L.fia_sizeof_combine_params.restype = ctypes.c_size_t
-            for f in ("append", "weights", "evict"):
+            for f in ("append", "weights", "evict", "pages", "norm_rope"):
                 getattr(L, f"fia_sizeof_{f}_params").restype = ctypes.c_size_t
             L.fia_get_workspace_size.argtypes = [ctypes.POINTER(FiaParams),
                                                  ctypes.POINTER(ctypes.c_size_t)]
@@ -199,6 +225,8 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
             L.fia_lse_combine.argtypes = [ctypes.POINTER(CombineParams), _P]
             L.fia_selftest_bounded_wait.argtypes = [_P, ctypes.c_uint64, _P]
             L.fia_kv_append.argtypes = [ctypes.POINTER(AppendParams), _P]
+            L.fia_assign_pages.argtypes = [ctypes.POINTER(PagesParams), _P]
+            L.fia_norm_rope_append.argtypes = [ctypes.POINTER(NormRopeParams), _P]
             L.fia_get_weights_workspace_size.argtypes = [
                 ctypes.POINTER(FiaParams), ctypes.POINTER(WeightsParams),
                 ctypes.POINTER(ctypes.c_size_t)]
@@ -220,7 +248,8 @@ def lib(build_if_missing: bool = True) -> ctypes.CDLL:
             if L.fia_sizeof_combine_params() != ctypes.sizeof(CombineParams):
                 raise RuntimeError("fia_combine_params layout mismatch")
             for f, t in (("append", AppendParams), ("weights", WeightsParams),
-                         ("evict", EvictParams)):
+                         ("evict", EvictParams), ("pages", PagesParams),
+                         ("norm_rope", NormRopeParams)):
                 if getattr(L, f"fia_sizeof_{f}_params")() != ctypes.sizeof(t):
                     raise RuntimeError(f"fia_{f}_params layout mismatch")
             _lib = L
@@ -274,6 +303,14 @@ def fia_lse_combine(p: CombineParams, stream: int = 0):
 
 def fia_kv_append(p: AppendParams, stream: int = 0):
     _check(lib().fia_kv_append(ctypes.byref(p), stream), "fia_kv_append")
+
+
+def fia_assign_pages(p: PagesParams, stream: int = 0):
+    _check(lib().fia_assign_pages(ctypes.byref(p), stream), "fia_assign_pages")
+
+
+def fia_norm_rope_append(p: NormRopeParams, stream: int = 0):
+    _check(lib().fia_norm_rope_append(ctypes.byref(p), stream), "fia_norm_rope_append")
 
 
 def fia_get_weights_workspace_size(p: FiaParams, w: WeightsParams) -> int:

@@ -100,7 +100,8 @@ def make_fia_params(*, q: torch.Tensor, out: torch.Tensor, k_cache: torch.Tensor
                     kv_layout: int = _abi.KV_LAYOUT_BNBSH,
                     atten_mask: Optional[torch.Tensor] = None,
                     first_tokens: int = 0) -> FiaParams:
-    """`atten_mask`: int8/uint8/bool [B or 1, rows, cols] (nonzero = masked
+    """`kv_dtype` KV_MXFP4: caches of bytes, two E2M1 codes each ([.., D/2]), and scales
+    of bytes [pages or B, KV heads, rows, D/32].  `atten_mask`: int8/uint8/bool [B or 1, rows, cols] (nonzero = masked
     out), rows >= the query length, cols a multiple of 16 >= the KV capacity;
     a first dimension of 1 is shared by every batch.  `first_tokens` (band
     mask): keys below it stay visible beside the window."""
@@ -112,6 +113,15 @@ def make_fia_params(*, q: torch.Tensor, out: torch.Tensor, k_cache: torch.Tensor
                     ("atten_mask", atten_mask)):
         if t is not None and t.device != q.device:
             raise ValueError(f"{name} is on {t.device}, q on {q.device}")
+    if kv_dtype == _abi.KV_MXFP4:  # (bytes: sizes and type are all that tells them from others)
+        n, rows = int(k_cache.shape[0]), block_size if block_table is not None else max_seqlen_kv
+        for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+            if t.dtype != torch.uint8 or t.numel() != n * rows * num_kv_heads * (head_dim // 2):
+                raise ValueError(f"{name}: an MXFP4 cache holds D/2 bytes a row (uint8)")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is None or t.dtype not in (torch.uint8, torch.float8_e8m0fnu):
+                raise ValueError(f"{name}: an MXFP4 cache has E8M0 scales (uint8, float8_e8m0fnu)")
+            _checked(t, name, t.dtype, (n, num_kv_heads, rows, head_dim // 32), k_cache.device)
     p = FiaParams()
     p.batch, p.num_q_heads, p.num_kv_heads, p.head_dim = batch, num_q_heads, num_kv_heads, head_dim
     p.layout, p.max_seqlen_q, p.total_q = layout, max_seqlen_q, total_q
@@ -119,7 +129,7 @@ def make_fia_params(*, q: torch.Tensor, out: torch.Tensor, k_cache: torch.Tensor
     p.k_cache, p.v_cache = _ptr(k_cache), _ptr(v_cache)
     p.k_scale, p.v_scale = _ptr(k_scale), _ptr(v_scale)
     p.kv_dtype = kv_dtype
-    p.quant_tile = 64 if kv_dtype == _abi.KV_FP8_E4M3 else 0
+    p.quant_tile = {_abi.KV_FP8_E4M3: 64, _abi.KV_MXFP4: 32}.get(kv_dtype, 0)
     p.block_table = _ptr(block_table)
     p.max_blocks_per_seq = 0 if block_table is None else int(block_table.shape[1])
     p.block_size, p.num_blocks, p.max_seqlen_kv = block_size, num_blocks, max_seqlen_kv
@@ -281,7 +291,9 @@ class KvCache:
     (KV_LAYOUT_BNBSH) or [pages, KV heads, page rows, D] (KV_LAYOUT_BNNBSD)
     with an int32 block table [B, max pages], or contiguous tensors [B, S, KV
     heads, D]; bf16, or E4M3 codes (uint8 or float8_e4m3fn) with fp32 scales
-    [pages or B, KV heads, rows, D/64]."""
+    [pages or B, KV heads, rows, D/64], or MXFP4: bytes of two E2M1 codes (uint8,
+    D/2 in the place of D) with E8M0 scales (uint8 or float8_e8m0fnu) [pages or B,
+    KV heads, rows, D/32]."""
 
     def __init__(self, k_cache: torch.Tensor, v_cache: torch.Tensor,
                  block_table: Optional[torch.Tensor] = None, *,
@@ -293,13 +305,17 @@ class KvCache:
         n, rows, heads, dim = (int(x) for x in k_cache.shape)
         if head_major:
             rows, heads = heads, rows
-        fp8 = k_cache.dtype in (torch.uint8, torch.float8_e4m3fn)
-        if not fp8 and k_cache.dtype != torch.bfloat16:
-            raise ValueError("a cache is bfloat16, or E4M3 codes (uint8, float8_e4m3fn)")
-        if fp8 and (k_scale is None or v_scale is None):
-            raise ValueError("an FP8 cache needs k_scale and v_scale")
-        if not fp8 and (k_scale is not None or v_scale is not None):
-            raise ValueError("scales belong to an FP8 cache")
+        coded = k_cache.dtype in (torch.uint8, torch.float8_e4m3fn)
+        if not coded and k_cache.dtype != torch.bfloat16:
+            raise ValueError("a cache is bfloat16, E4M3 codes (uint8, float8_e4m3fn) or bytes of "
+                             "two E2M1 codes (uint8)")
+        if coded and (k_scale is None or v_scale is None):
+            raise ValueError("an FP8 or MXFP4 cache needs k_scale and v_scale")
+        if not coded and (k_scale is not None or v_scale is not None):
+            raise ValueError("scales belong to an FP8 or MXFP4 cache")
+        # (both hold bytes: the type of the scales tells them apart)
+        mx = k_cache.dtype == torch.uint8 and k_scale.dtype in (torch.uint8, torch.float8_e8m0fnu)
+        dim = 2 * dim if mx else dim
         self.device = k_cache.device
         self.num_kv_heads, self.head_dim = heads, dim
         self.tensors = (k_cache, v_cache, block_table, k_scale, v_scale)  # kept alive
@@ -308,12 +324,13 @@ class KvCache:
         c.k_cache, c.v_cache = _ptr(_contig(k_cache, "k_cache")), _ptr(_contig(v_cache, "v_cache"))
         if v_cache.device != self.device:
             raise ValueError("k_cache and v_cache must be on one device")
-        c.kv_dtype = _abi.KV_FP8_E4M3 if fp8 else _abi.KV_BF16
-        if fp8:
-            c.quant_tile = 64
-            shape = (n, heads, rows, dim // 64)
-            c.k_scale = _checked(k_scale, "k_scale", torch.float32, shape, self.device)
-            c.v_scale = _checked(v_scale, "v_scale", torch.float32, shape, self.device)
+        c.kv_dtype = _abi.KV_MXFP4 if mx else _abi.KV_FP8_E4M3 if coded else _abi.KV_BF16
+        if coded:
+            c.quant_tile = 32 if mx else 64
+            shape = (n, heads, rows, dim // c.quant_tile)
+            dtype = k_scale.dtype if mx else torch.float32
+            c.k_scale = _checked(k_scale, "k_scale", dtype, shape, self.device)
+            c.v_scale = _checked(v_scale, "v_scale", dtype, shape, self.device)
         if block_table is None:
             self.batch, self.capacity = n, rows
             c.max_seqlen_kv = rows
@@ -408,6 +425,151 @@ def kv_append(cache: KvCache, k_new: torch.Tensor, v_new: torch.Tensor, seqused_
     """Write the K and V rows of new tokens to the cache (KvAppendCall's
     arguments)."""
     KvAppendCall(cache, k_new, v_new, seqused_kv, **kw).run(stream)
+
+
+class AssignPagesCall:
+    """fia_assign_pages with its buffers: the pages of a paged cache brought up to the
+    lengths `seqused_kv` (int32 [B], the new rows counted).  `block_table` [B, max pages]
+    and `free_pages` [pages of the pool] are changed in place; `pages_held` [B] and
+    `free_count` [1] give how many pages each sequence holds and how many are free, and
+    become `pages_held_out` and `free_count_out` (by default: themselves).  The new rows
+    are T tokens with `cu_seqlens_q` (T from `slots`, `positions` or `total_q`), else
+    `seqlen_q` for every sequence; run() returns (slots, positions), int32 [T], new
+    tensors unless given (None without rows): where each token goes in the pool, and its
+    position.  `tokens_seen` (int32 [B]) counts the sequences' tokens where slots are no
+    positions.  `status` (int32 [1]) becomes 3 where a page was missing.  New tensors are
+    made on the stream that is current where the call is."""
+
+    def __init__(self, block_table: torch.Tensor, pages_held: torch.Tensor,
+                 free_pages: torch.Tensor, free_count: torch.Tensor, seqused_kv: torch.Tensor, *,
+                 block_size: int, cu_seqlens_q: Optional[torch.Tensor] = None, seqlen_q: int = 0,
+                 total_q: Optional[int] = None, tokens_seen: Optional[torch.Tensor] = None,
+                 slots: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                 pages_held_out: Optional[torch.Tensor] = None,
+                 free_count_out: Optional[torch.Tensor] = None,
+                 status: Optional[torch.Tensor] = None):
+        if block_table.dim() != 2 or free_pages.dim() != 1:
+            raise ValueError("block_table must be [B, max pages], free_pages [pages]")
+        dev = self.device = block_table.device
+        batch, pages = (int(x) for x in block_table.shape)
+
+        def ints(t, name, n):
+            return _checked(t, name, torch.int32, (n,), dev)
+
+        for name, t in (("pages_held", pages_held), ("free_count", free_count),
+                        ("seqused_kv", seqused_kv)):
+            if t is None:
+                raise ValueError(f"{name} is required")
+        p = self.params = _abi.PagesParams()
+        p.batch, p.max_blocks_per_seq = batch, pages
+        p.block_size, p.num_blocks = _int32(block_size, "block_size"), int(free_pages.numel())
+        p.block_table = _checked(block_table, "block_table", torch.int32, (batch, pages), dev)
+        p.free_pages = ints(free_pages, "free_pages", p.num_blocks)
+        p.seqused_kv, p.tokens_seen = ints(seqused_kv, "seqused_kv", batch), ints(
+            tokens_seen, "tokens_seen", batch)
+        p.pages_held, p.free_count = ints(pages_held, "pages_held", batch), ints(
+            free_count, "free_count", 1)
+        self.pages_held_out = pages_held if pages_held_out is None else pages_held_out
+        self.free_count_out = free_count if free_count_out is None else free_count_out
+        p.pages_held_out = ints(self.pages_held_out, "pages_held_out", batch)
+        p.free_count_out = ints(self.free_count_out, "free_count_out", 1)
+        if cu_seqlens_q is None:
+            p.layout, p.seqlen_q = _abi.LAYOUT_BSND, _int32(seqlen_q, "seqlen_q")
+            rows = batch * p.seqlen_q
+        else:
+            given = [int(t.numel()) for t in (slots, positions) if t is not None]
+            rows = given[0] if total_q is None and given else total_q
+            if rows is None:
+                raise ValueError("total_q is required without slots and positions")
+            p.layout, p.total_q = _abi.LAYOUT_TND, _int32(rows, "total_q")
+            p.cu_seqlens_q = ints(cu_seqlens_q, "cu_seqlens_q", batch + 1)
+        if rows > 0 and slots is None:
+            slots = torch.empty(rows, dtype=torch.int32, device=dev)
+        if rows > 0 and positions is None:
+            positions = torch.empty(rows, dtype=torch.int32, device=dev)
+        self.slots, self.positions = slots, positions
+        p.slots, p.positions = ints(slots, "slots", max(rows, 0)), ints(positions, "positions",
+                                                                        max(rows, 0))
+        p.status = ints(status, "status", 1)
+        self.tensors = (block_table, pages_held, free_pages, free_count, seqused_kv, cu_seqlens_q,
+                        tokens_seen, status)
+
+    def run(self, stream=None):
+        _launch(self.device, stream, _abi.fia_assign_pages, self.params)
+        return self.slots, self.positions
+
+
+def assign_pages(block_table: torch.Tensor, pages_held: torch.Tensor, free_pages: torch.Tensor,
+                 free_count: torch.Tensor, seqused_kv: torch.Tensor, *, stream=None, **kw):
+    """Bring a cache's pages up to its lengths (AssignPagesCall's arguments); returns
+    (slots, positions), made on `stream`."""
+    with _made_on(stream, block_table.device):
+        return AssignPagesCall(block_table, pages_held, free_pages, free_count, seqused_kv,
+                               **kw).run(stream)
+
+
+class NormRopeAppendCall:
+    """fia_norm_rope_append with its buffers: the heads of q and k_new normed (x * weight /
+    sqrt(mean x^2 + eps), where there is a weight, bf16 [D]) and rotated to `positions`
+    (int32 [T]) by `cos_sin` (fp32 [max positions, rotary dim], cosines then sines; None:
+    no rotation; `interleaved`: neighbours are pairs, else halves of the rotary
+    dimension), the queries to `q_out` (bf16, a new tensor unless given; may be q), k_new
+    and v_new to `slots` (int32 [T]) of the cache.  q, k_new, v_new are bf16 [T, heads,
+    D] or [B, S, heads, D], and tokens may be strided (slices of a fused projection).
+    Rows with a position below 0 are left out; `status` (int32 [1]) becomes 3 where a
+    slot or a position lies outside.  run() returns q_out."""
+
+    def __init__(self, cache: KvCache, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                 slots: torch.Tensor, positions: torch.Tensor,
+                 cos_sin: Optional[torch.Tensor] = None, *,
+                 q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                 eps: float = 1e-6, interleaved: bool = False,
+                 q_out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None):
+        self.cache = cache
+        if k_new.shape != v_new.shape or q.dim() not in (3, 4) or k_new.dim() != q.dim() \
+                or q.shape[:-2] != k_new.shape[:-2]:
+            raise ValueError("q, k_new and v_new must have the same tokens: [T, heads, D] or "
+                             "[B, S, heads, D]")
+        if tuple(k_new.shape[-2:]) != (cache.num_kv_heads, cache.head_dim) \
+                or q.shape[-1] != cache.head_dim:
+            raise ValueError("k_new does not have the cache's heads")
+        self.q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        if self.q_out.shape != q.shape:
+            raise ValueError(f"q_out must be {tuple(q.shape)}")
+        p = self.params = _abi.NormRopeParams()
+        p.cache = cache.params
+        p.tokens, p.num_q_heads = math.prod(q.shape[:-2]), int(q.shape[-2])
+        for name, t in (("q", q), ("k", k_new), ("v", v_new), ("q_out", self.q_out)):
+            if t.dtype != torch.bfloat16 or t.device != cache.device:
+                raise ValueError(f"{name} must be bfloat16 on the cache's device")
+            setattr(p, name, _ptr(t))
+            setattr(p, name + "_token_stride", KvAppendCall._token_stride(t, name))
+        for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+            setattr(p, name, _checked(t, name, torch.bfloat16, (cache.head_dim,), cache.device))
+        p.eps, p.interleaved = eps, int(interleaved)
+        if cos_sin is not None:
+            if cos_sin.dim() != 2:
+                raise ValueError("cos_sin must be [max positions, rotary dim]")
+            p.max_positions, p.rotary_dim = (int(x) for x in cos_sin.shape)
+            p.cos_sin = _checked(cos_sin, "cos_sin", torch.float32, cos_sin.shape, cache.device)
+        for name, t in (("slots", slots), ("positions", positions)):
+            setattr(p, name, _checked(t, name, torch.int32, (p.tokens,), cache.device))
+        p.status = _checked(status, "status", torch.int32, (1,), cache.device)
+        self.tensors = (q, k_new, v_new, slots, positions, cos_sin, q_weight, k_weight, status)
+
+    def run(self, stream=None):
+        _launch(self.cache.device, stream, _abi.fia_norm_rope_append, self.params)
+        return self.q_out
+
+
+def norm_rope_append(cache: KvCache, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                     slots: torch.Tensor, positions: torch.Tensor,
+                     cos_sin: Optional[torch.Tensor] = None, *, stream=None, **kw):
+    """Norm and rotate the heads of new tokens and write K and V to their slots
+    (NormRopeAppendCall's arguments); returns q_out, made on `stream`."""
+    with _made_on(stream, cache.device):
+        return NormRopeAppendCall(cache, q, k_new, v_new, slots, positions, cos_sin,
+                                  **kw).run(stream)
 
 
 class KeyWeightsCall(FiaCall):

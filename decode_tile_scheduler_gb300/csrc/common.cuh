@@ -246,6 +246,17 @@ __device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t codes, uint32_t& lo, 
       : "r"(codes));
 }
 
+// Eight E2M1 codes (one 32-bit word, the lower half of a byte first) to four fp16
+// pairs, a byte each (exact).
+__device__ __forceinline__ void e2m1x8_to_f16x2x4(uint32_t codes, uint32_t& p0, uint32_t& p1,
+                                                  uint32_t& p2, uint32_t& p3) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(p0), "=r"(p1), "=r"(p2), "=r"(p3)
+      : "r"(codes));
+}
+
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -12,6 +12,7 @@
 
 #include "../../include/fia.h"
 #include "internal.h"
+#include "kv_cache.cuh"
 
 using namespace fia;
 
@@ -74,11 +75,13 @@ fia_status sm_count(int requested, int* n) {
   return FIA_OK;
 }
 
-// 2-D tiled map over a row-major [rows, cols] matrix with 128-byte swizzling.
+// 2-D tiled map over a row-major [rows, cols] matrix, swizzled over 128 bytes unless
+// asked otherwise.
 fia_status make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esize,
                     uint64_t cols, uint64_t rows, uint32_t box_cols, uint32_t box_rows,
                     uint64_t row_stride_elems,
-                    CUtensorMapL2promotion promo = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
+                    CUtensorMapL2promotion promo = CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   PFN_cuTensorMapEncodeTiled_v12000 enc;
   fia_status st = get_encoder(&enc);
   if (st != FIA_OK) return st;
@@ -87,7 +90,7 @@ fia_status make_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, in
   cuuint32_t box[2] = {box_cols, box_rows};
   cuuint32_t es[2] = {1, 1};
   CUresult r = enc(m, dt, 2, const_cast<void*>(base), dims, strides, box, es,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promo,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promo,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? FIA_OK : FIA_ERR_CUDA;
 }
@@ -130,7 +133,8 @@ fia_status validate(const fia_params* p) {
     if (p->total_q < 0) return FIA_ERR_BAD_SHAPE;
     if (!p->cu_seqlens_q) return FIA_ERR_NULL_ARG;
   }
-  if (p->kv_dtype != FIA_KV_BF16 && p->kv_dtype != FIA_KV_FP8_E4M3) return FIA_ERR_BAD_DTYPE;
+  if (p->kv_dtype != FIA_KV_BF16 && p->kv_dtype != FIA_KV_FP8_E4M3 && p->kv_dtype != FIA_KV_MXFP4)
+    return FIA_ERR_BAD_DTYPE;
   if (p->mask_mode < FIA_MASK_NONE || p->mask_mode > FIA_MASK_BAND) return FIA_ERR_BAD_SHAPE;
   // an explicit mask goes with modes 0 and 1 only; mode 1 needs one
   if (p->mask_mode == FIA_MASK_ALL && !p->atten_mask) return FIA_ERR_NULL_ARG;
@@ -161,18 +165,16 @@ fia_status validate(const fia_params* p) {
   if (!aligned16(p->q) || !aligned16(p->out) || !aligned16(p->k_cache) || !aligned16(p->v_cache))
     return FIA_ERR_BAD_SHAPE;
   if (p->lse && (reinterpret_cast<uintptr_t>(p->lse) & 3u)) return FIA_ERR_BAD_SHAPE;
-  if (p->kv_dtype == FIA_KV_FP8_E4M3) {
-    if (!p->k_scale || !p->v_scale) return FIA_ERR_NULL_ARG;
-    if (p->quant_tile != 64) return FIA_ERR_BAD_SHAPE;
-    if (p->head_dim % 64) return FIA_ERR_BAD_SHAPE;
-    if (!aligned16(p->k_scale) || !aligned16(p->v_scale)) return FIA_ERR_BAD_SHAPE;
-    // scale pieces of a contiguous cache are copied in 16-byte units
-    if (!p->block_table && (p->max_seqlen_kv & 1)) return FIA_ERR_BAD_SHAPE;
+  const bool coded = p->kv_dtype != FIA_KV_BF16;
+  if (coded) {
+    const fia_status st = check_scales(p->kv_dtype, p->k_scale, p->v_scale, p->quant_tile, p->head_dim,
+                                       p->block_table ? 0 : p->max_seqlen_kv);
+    if (st != FIA_OK) return st;
   }
   if (p->block_table) {
     if (!p->seqused_kv) return FIA_ERR_NULL_ARG;
     if (p->block_size <= 0 || p->block_size % 16 || p->block_size > 1024) return FIA_ERR_BAD_SHAPE;
-    if (p->kv_dtype == FIA_KV_FP8_E4M3 && (p->block_size % 32 || p->block_size > 512))
+    if (coded && (p->block_size % 32 || p->block_size > 512))
       return FIA_ERR_BAD_SHAPE;
     if (p->num_blocks <= 0 || p->max_blocks_per_seq <= 0) return FIA_ERR_BAD_SHAPE;
     if ((int64_t)p->num_blocks * p->block_size *
@@ -190,9 +192,12 @@ fia_status validate(const fia_params* p) {
   }
   // what is built
   if (p->head_dim != 64 && p->head_dim != 128) return FIA_ERR_UNSUPPORTED;
-  if (p->kv_dtype == FIA_KV_FP8_E4M3 && p->head_dim != 128) return FIA_ERR_UNSUPPORTED;
+  if (coded && p->head_dim != 128) return FIA_ERR_UNSUPPORTED;
   return FIA_OK;
 }
+
+// A cache whose prompts run on a copy of it in 16 bits.
+bool copied(const fia_params* p) { return p->kv_dtype != FIA_KV_BF16; }
 
 
 struct DecodePlan {
@@ -219,7 +224,7 @@ int debug_checks() {
 // heads per KV head 120.3 -> 113.6 us, 4-row decode 88.2 -> 79.9 us against
 // k = 6, 6 and 3; one-row bf16 decode 58.9 -> 58.6 us against k = 3).
 int decode_small_div(const fia_params* p) {
-  return (p->kv_dtype == FIA_KV_FP8_E4M3 || p->max_seqlen_q > 1) ? 1 : 2;
+  return (p->kv_dtype != FIA_KV_BF16 || p->max_seqlen_q > 1) ? 1 : 2;
 }
 
 // Decode workspace: [0, 256) error word (offset 0) and the claim counters
@@ -285,8 +290,8 @@ DecodeArgs decode_args(const fia_params* p, const DecodePlan& pl, void* ws) {
   a.block_size = p->block_table ? p->block_size : 1;
   a.box_rows = p->block_table ? gcd_i(p->block_size, kKvTile) : kKvTile;
   fast_divisor(a.block_size, &a.bs_magic, &a.bs_shift);
-  a.k_scale = p->k_scale;
-  a.v_scale = p->v_scale;
+  a.k_scale = static_cast<const float*>(p->k_scale);
+  a.v_scale = static_cast<const float*>(p->v_scale);
   a.scale_log2 = p->scale * 1.4426950408889634f;
   a.mask_mode = p->mask_mode;
   a.pre_tokens = p->pre_tokens;
@@ -314,27 +319,30 @@ DecodeArgs decode_args(const fia_params* p, const DecodePlan& pl, void* ws) {
 // pools [num_blocks, KV_N, block_size, D] as one of D columns with one row per
 // (block, head, token).
 fia_status kv_maps(const fia_params* p, int box_rows, CUtensorMap* tk, CUtensorMap* tv) {
-  const bool fp8 = p->kv_dtype == FIA_KV_FP8_E4M3;
+  const bool fp8 = p->kv_dtype == FIA_KV_FP8_E4M3, mx = p->kv_dtype == FIA_KV_MXFP4;
   const bool head_major = p->block_table && p->kv_layout == FIA_KV_LAYOUT_BNNBSD;
-  const uint64_t cols = head_major ? (uint64_t)p->head_dim
-                                   : (uint64_t)p->num_kv_heads * p->head_dim;
+  // (MXFP4: bytes, two elements each)
+  const uint64_t dim = (uint64_t)(mx ? p->head_dim / 2 : p->head_dim);
+  const uint64_t cols = head_major ? dim : (uint64_t)p->num_kv_heads * dim;
   const uint64_t rows = p->block_table
                             ? (uint64_t)p->num_blocks * p->block_size * (head_major ? p->num_kv_heads : 1)
                             : (uint64_t)p->batch * p->max_seqlen_kv;
-  const CUtensorMapDataType dt = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const int es = fp8 ? 1 : 2;
-  const uint32_t bc = fp8 ? 128 : 64;
+  const CUtensorMapDataType dt =
+      fp8 || mx ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const int es = fp8 || mx ? 1 : 2;
+  const uint32_t bc = fp8 ? 128 : 64;  // (MXFP4: one head's 64 bytes)
+  const CUtensorMapSwizzle swizzle = mx ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   // One head's slice of a token is D * esize bytes: 256 for bf16 D=128 (two
   // 128-byte boxes, so a 256-byte L2 fill is used in full) but 128 for FP8,
   // where a 256-byte fill would also drag in the next head's slice.
-  const CUtensorMapL2promotion promo = (uint64_t)p->head_dim * es >= 256
+  const CUtensorMapL2promotion promo = dim * es >= 256
                                            ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
                                            : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
   fia_status st = make_map(tk, p->k_cache, dt, es, cols, rows ? rows : 1, bc, (uint32_t)box_rows,
-                           cols, promo);
+                           cols, promo, swizzle);
   if (st != FIA_OK) return st;
   return make_map(tv, p->v_cache, dt, es, cols, rows ? rows : 1, bc, (uint32_t)box_rows, cols,
-                  promo);
+                  promo, swizzle);
 }
 
 struct PrefillPlan {
@@ -343,7 +351,8 @@ struct PrefillPlan {
   int64_t off_seq, off_hist, off_list, total;
   // FP8 caches: their fp16 copies [B, cap, KVN, D], the largest scales and
   // the K/V factors [B * KVN * 2] (all 0 for bf16 caches; the queries are
-  // converted to fp16 inside the prefill kernel)
+  // converted to fp16 inside the prefill kernel).  MXFP4 caches: bf16 copies, which
+  // hold every value exactly.
   int64_t off_kbf, off_vbf, off_smax, off_kvfac;
 };
 
@@ -368,16 +377,18 @@ fia_status prefill_plan(const fia_params* p, PrefillPlan* pl) {
   pl->off_list = off;
   off = align_up(off + 8 * pl->U_max);
   pl->off_kbf = pl->off_vbf = pl->off_smax = pl->off_kvfac = 0;
-  if (p->kv_dtype == FIA_KV_FP8_E4M3) {
+  if (copied(p)) {
     const int64_t bytes = 2 * (int64_t)p->batch * kv_capacity_of(p) * p->num_kv_heads * p->head_dim;
     pl->off_kbf = off;
     off = align_up(off + bytes);
     pl->off_vbf = off;
     off = align_up(off + bytes);
-    pl->off_smax = off;
-    off = align_up(off + 8 * (int64_t)p->batch * p->num_kv_heads);
-    pl->off_kvfac = off;
-    off = align_up(off + 8 * (int64_t)p->batch * p->num_kv_heads);
+    if (p->kv_dtype == FIA_KV_FP8_E4M3) {
+      pl->off_smax = off;
+      off = align_up(off + 8 * (int64_t)p->batch * p->num_kv_heads);
+      pl->off_kvfac = off;
+      off = align_up(off + 8 * (int64_t)p->batch * p->num_kv_heads);
+    }
   }
   pl->total = off;
   return FIA_OK;
@@ -386,10 +397,10 @@ fia_status prefill_plan(const fia_params* p, PrefillPlan* pl) {
 // The parameters the tcgen05 prefill kernel runs on: for FP8 caches, their
 // fp16 copies in the workspace as contiguous caches [B, cap, KVN, D] (16-bit
 // elements move through the same tensor maps; the bf16 queries are converted
-// to fp16 by the kernel itself).
+// to fp16 by the kernel itself); for MXFP4 caches their bf16 copies.
 fia_params prefill_view(const fia_params* p, const PrefillPlan& pl, void* ws) {
   fia_params v = *p;
-  if (p->kv_dtype != FIA_KV_FP8_E4M3) return v;
+  if (!copied(p)) return v;
   char* w = static_cast<char*>(ws);
   v.k_cache = w + pl.off_kbf;
   v.v_cache = w + pl.off_vbf;
@@ -413,8 +424,9 @@ DequantArgs dequant_args(const fia_params* p, const PrefillPlan& pl, void* ws) {
   d.kv_layout = p->block_table ? p->kv_layout : 0;
   d.k = static_cast<const uint8_t*>(p->k_cache);
   d.v = static_cast<const uint8_t*>(p->v_cache);
-  d.k_scale = p->k_scale;
-  d.v_scale = p->v_scale;
+  d.k_scale = static_cast<const float*>(p->k_scale);
+  d.v_scale = static_cast<const float*>(p->v_scale);
+  d.mx = p->kv_dtype == FIA_KV_MXFP4;
   d.block_table = p->block_table;
   d.max_blocks = p->max_blocks_per_seq;
   d.block_size = p->block_table ? p->block_size : 1;
@@ -707,8 +719,8 @@ fia_kv_cache cache_of(const fia_params* p) {
   c.kv_layout = p->kv_layout;
   c.k_cache = const_cast<void*>(p->k_cache);
   c.v_cache = const_cast<void*>(p->v_cache);
-  c.k_scale = const_cast<float*>(p->k_scale);
-  c.v_scale = const_cast<float*>(p->v_scale);
+  c.k_scale = const_cast<void*>(p->k_scale);
+  c.v_scale = const_cast<void*>(p->v_scale);
   c.block_table = p->block_table;
   c.max_blocks_per_seq = p->max_blocks_per_seq;
   c.block_size = p->block_size;
@@ -730,14 +742,15 @@ fia_status execute_decode(const fia_params* p, void* ws, cudaStream_t s, bool pl
   fia_status st = decode_plan(p, &pl);
   if (st != FIA_OK) return st;
   DecodeArgs a = decode_args(p, pl, ws);
-  if (decode_is_few(a, w != nullptr))
+  // (the kernel of few units takes no MXFP4 cache)
+  if (p->kv_dtype != FIA_KV_MXFP4 && decode_is_few(a, w != nullptr))
     return launch_decode_few(a, cache_of(p), w, planned, s) == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
   a.scores = scores;
   a.score_cols = cols;
   CUtensorMap tk, tv;
   st = kv_maps(p, a.box_rows, &tk, &tv);
   if (st != FIA_OK) return st;
-  return launch_decode(a, tk, tv, p->kv_dtype == FIA_KV_FP8_E4M3, w, s) == cudaSuccess
+  return launch_decode(a, tk, tv, p->kv_dtype, w, s) == cudaSuccess
              ? FIA_OK
              : FIA_ERR_CUDA;
 }
@@ -767,7 +780,7 @@ fia_status execute(const fia_params* p, void* ws, size_t ws_bytes, void* stream,
     if (st != FIA_OK) return st;
     st = kv_maps(&v, a.box_rows, &tk, &tv);
     if (st != FIA_OK) return st;
-    if (p->kv_dtype == FIA_KV_FP8_E4M3) {
+    if (copied(p)) {
       int n;
       st = sm_count(p->num_sms, &n);
       if (st != FIA_OK) return st;
@@ -792,15 +805,23 @@ fia_status execute_weights(const fia_params* p, const fia_weights_params* w, voi
   }
   st = execute(p, ws, ws_bytes, stream, planned);
   if (st != FIA_OK) return st;
-  const WeightsArgs a = weights_args(p, w, pl, ws);
   if (pl.lay.branch == 0)  // no query row
-    return launch_key_weights_fold(a, s) == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
+    return launch_key_weights_fold(weights_args(p, w, pl, ws), s) == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
+  // (MXFP4: the bf16 copy of K that the attention made)
+  fia_params v = *p;
+  if (p->kv_dtype == FIA_KV_MXFP4) {
+    PrefillPlan pp;
+    st = prefill_plan(p, &pp);
+    if (st != FIA_OK) return st;
+    v = prefill_view(p, pp, ws);
+  }
   CUtensorMap tq, tk, tv;
-  st = q_map(p, &tq);
+  st = q_map(&v, &tq);
   if (st != FIA_OK) return st;
-  st = kv_maps(p, a.box_rows, &tk, &tv);
+  const WeightsArgs a = weights_args(&v, w, pl, ws);
+  st = kv_maps(&v, a.box_rows, &tk, &tv);
   if (st != FIA_OK) return st;
-  return launch_key_weights(a, cache_of(p), tq, tk, s) == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
+  return launch_key_weights(a, cache_of(&v), tq, tk, s) == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
 }
 
 }  // namespace

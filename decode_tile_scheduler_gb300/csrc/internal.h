@@ -73,7 +73,7 @@ struct DecodeArgs {
   int max_blocks, block_size, box_rows;
   uint32_t bs_magic;           // j / block_size == (j * bs_magic) >> bs_shift, 0 <= j < 2^31
   int bs_shift;
-  const float* k_scale;
+  const float* k_scale;        // MXFP4: four E8M0 bytes in each element
   const float* v_scale;
   float scale_log2;      // scale * log2(e)
   int mask_mode, pre_tokens, next_tokens;
@@ -199,7 +199,7 @@ struct KeyWeightsOut {
 };
 // The decode kernel and its combine; with `w` (and a.scores) the key weights too.
 cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
-                          int fp8, const KeyWeightsOut* w, cudaStream_t s);
+                          int kv_dtype, const KeyWeightsOut* w, cudaStream_t s);
 // Whether a call has few units and few keys (a rule on sizes), and its one kernel:
 // `planned` if it has to find a plan in the workspace, else the plan's launch goes
 // before it and need not be done.
@@ -229,6 +229,8 @@ struct DequantArgs {
   uint16_t* v_out;
   uint32_t* smax;              // [B * KVN * 2] largest K and V scale (bits), zeroed first
   float* kvfac;                // [B * KVN * 2] the power of two taken out of K and V
+  int mx;                      // MXFP4 instead: two E2M1 codes a byte, E8M0 bytes at k_scale and
+                               // v_scale, bf16 copies; smax and kvfac are not used
   int* err;                    // the workspace's error word
   int debug;                   // FIA_DEBUG: report page ids outside the pool (error word 3)
   // a band with first tokens: only the KV tiles that some row sees

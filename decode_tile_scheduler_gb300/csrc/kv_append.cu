@@ -6,17 +6,19 @@
 // Row i of a sequence's q_len new rows goes to slot kv_len - q_len + i.  FP8:
 // scale = amax / 448 and code = rn(x / scale), both divisions in fp32 as IEEE
 // rounds them (the format's definition; a reciprocal would move codes that lie
-// near a rounding border).
+// near a rounding border).  MXFP4: E2M1 codes under the smallest power of two that
+// leaves none over 6, where every step but the last rounding is exact.
 //
 // Memory-bound: every new element is read once and written once.  A thread
 // takes 16 bytes of a K row and the same 16 bytes of the V row (bf16), or 16
-// elements of each (FP8; the four threads of a 64-element tile share its
+// elements of each (FP8, MXFP4; the four or two threads of a tile share its
 // largest magnitude by shuffles), so both loads are in flight together and the
 // stores are 16 bytes wide.  20,642 rows of 8 heads of 128 in bf16 (170 MB): 29.5 us,
 // 5.8 TB/s, 0.85 of the measured copy rate.
 #include <algorithm>
 
 #include "kv_cache.cuh"
+#include "kv_quant.cuh"
 
 namespace fia {
 
@@ -37,9 +39,6 @@ struct AppendArgs {
   int T, S;                // new rows, in all and (BSND) per sequence
 };
 
-constexpr float kFp8Max = 448.f;
-constexpr float kBf16Max = 3.38953139e38f;  // largest finite bf16 value
-
 // Largest magnitude among the 16 bf16 values of a and b, NaN left out.
 __device__ __forceinline__ float amax16(const uint4& a, const uint4& b) {
   const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -53,16 +52,8 @@ __device__ __forceinline__ float amax16(const uint4& a, const uint4& b) {
 }
 
 __device__ __forceinline__ uint32_t quant4(uint32_t w0, uint32_t w1, float scale) {
-  const float x0 = __fdiv_rn(__uint_as_float(w0 << 16), scale);
-  const float x1 = __fdiv_rn(__uint_as_float(w0 & 0xffff0000u), scale);
-  const float x2 = __fdiv_rn(__uint_as_float(w1 << 16), scale);
-  const float x3 = __fdiv_rn(__uint_as_float(w1 & 0xffff0000u), scale);
-  uint32_t r;  // (the first source of a pair lands in its upper byte)
-  asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\tmov.b32 %0, {l, h};\n\t}"
-      : "=r"(r)
-      : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
-  return r;
+  return e4m3x4(__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xffff0000u),
+                __uint_as_float(w1 << 16), __uint_as_float(w1 & 0xffff0000u), scale);
 }
 
 // The 16 elements of a and b as codes at dst, the tile's scale from its first
@@ -80,17 +71,65 @@ __device__ __forceinline__ void store_fp8(uint8_t* dst, float* scale_dst, const 
   if (first) *scale_dst = scale;
 }
 
-template <bool FP8>
+// Whether one of the eight bf16 values of x is a NaN.
+__device__ __forceinline__ bool any_nan(const uint4& x) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  bool n = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    n = n || (w[i] & 0x7fffu) > 0x7f80u || (w[i] & 0x7fff0000u) > 0x7f800000u;
+  return n;
+}
+
+// Infinities as the largest finite values of their sign.
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  if ((w & 0x7fffu) == 0x7f80u) w -= 1u;
+  if ((w & 0x7fff0000u) == 0x7f800000u) w -= 0x10000u;
+  return w;
+}
+__device__ __forceinline__ uint4 finite8(const uint4& x) {
+  return make_uint4(finite2(x.x), finite2(x.y), finite2(x.z), finite2(x.w));
+}
+
+__device__ __forceinline__ uint32_t quant8_mx(const uint4& x, float inv) {
+  return e2m1x8(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u),
+                __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u),
+                __uint_as_float(x.z << 16), __uint_as_float(x.z & 0xffff0000u),
+                __uint_as_float(x.w << 16), __uint_as_float(x.w & 0xffff0000u), inv);
+}
+
+// The same as E2M1 codes: lanes 2k and 2k + 1 hold one tile of 32.
+__device__ __forceinline__ void store_mx(uint8_t* dst, uint8_t* scale_dst, uint4 a, uint4 b, bool ok,
+                                         bool first) {
+  float m = amax16(a, b);
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  if (m > kBf16Max) {  // (saturated at 6, they would be half as large again)
+    a = finite8(a);
+    b = finite8(b);
+    m = kBf16Max;
+  }
+  int nan = any_nan(a) || any_nan(b);
+  nan |= __shfl_xor_sync(0xffffffffu, nan, 1);
+  if (!ok) return;
+  const int e = nan ? 255 : mx_scale(m);
+  uint2 codes = make_uint2(0u, 0u);
+  if (!nan) codes = make_uint2(quant8_mx(a, mx_inverse(e)), quant8_mx(b, mx_inverse(e)));
+  *reinterpret_cast<uint2*>(dst) = codes;
+  if (first) *scale_dst = (uint8_t)e;
+}
+
+enum Format { kBf16, kFp8, kMx };
+
+template <int F>
 __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
-  constexpr int E = FP8 ? 16 : 8;         // elements per thread
+  constexpr int E = F ? 16 : 8;           // elements per thread
   // eight threads are a group, one or two groups a (row, head): one 32-bit
   // division finds a thread's place (64-bit ones made the kernel issue-bound,
   // 72 % of its issue slots at half of the DRAM rate)
   const uint32_t two = a.c.D / E == 16;
   const uint32_t u = blockIdx.x * 32u + threadIdx.x / 8, per_row = (uint32_t)a.c.KVN << two;
   const uint32_t row = u / per_row, in_row = u - row * per_row;
-  // (FP8: a tile's four threads are past the end together, and take part in
-  // its shuffles)
+  // (a tile's threads are past the end together, and take part in its shuffles)
   const bool inside = row < (uint32_t)a.T;
   const int t = inside ? (int)row : 0;
   const int hk = (int)(in_row >> two);
@@ -119,7 +158,13 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const AppendArgs a) {
   const int64_t src = (int64_t)hk * a.c.D + part * E;
   const uint4* ks = reinterpret_cast<const uint4*>(a.k_new + (int64_t)t * a.k_stride + src);
   const uint4* vs = reinterpret_cast<const uint4*>(a.v_new + (int64_t)t * a.v_stride + src);
-  if constexpr (FP8) {
+  if constexpr (F == kMx) {
+    const uint4 k0 = __ldg(ks), k1 = __ldg(ks + 1), v0 = __ldg(vs), v1 = __ldg(vs + 1);
+    const int64_t dst = (r.row * a.c.D + part * E) / 2;
+    const int64_t sc = r.srow * (a.c.D / 32) + part / 2;
+    store_mx(a.c.k + dst, reinterpret_cast<uint8_t*>(a.c.ks) + sc, k0, k1, ok, part % 2 == 0);
+    store_mx(a.c.v + dst, reinterpret_cast<uint8_t*>(a.c.vs) + sc, v0, v1, ok, part % 2 == 0);
+  } else if constexpr (F == kFp8) {
     const uint4 k0 = __ldg(ks), k1 = __ldg(ks + 1), v0 = __ldg(vs), v1 = __ldg(vs + 1);
     const int64_t dst = r.row * a.c.D + part * E;
     const int64_t sc = r.srow * (a.c.D / 64) + part / 4;
@@ -188,12 +233,13 @@ extern "C" fia_status fia_kv_append(const fia_append_params* p, void* stream) {
   a.status = p->status;
   a.S = p->seqlen_q;
   if (rows == 0) return FIA_OK;
-  const int64_t grid = (rows * a.c.KVN * (a.c.D / (a.c.fp8 ? 16 : 8)) + 255) / 256;
+  const int64_t grid = (rows * a.c.KVN * (a.c.D / (a.c.fp8 || a.c.mx ? 16 : 8)) + 255) / 256;
   // (the kernel counts rows, and groups of eight threads, in 32 bits)
   if (rows > INT32_MAX || grid >= (1 << 27)) return FIA_ERR_BAD_SHAPE;
   a.T = (int)rows;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (a.c.fp8) kv_append_kernel<true><<<(int)grid, 256, 0, s>>>(a);
-  else kv_append_kernel<false><<<(int)grid, 256, 0, s>>>(a);
+  if (a.c.mx) kv_append_kernel<kMx><<<(int)grid, 256, 0, s>>>(a);
+  else if (a.c.fp8) kv_append_kernel<kFp8><<<(int)grid, 256, 0, s>>>(a);
+  else kv_append_kernel<kBf16><<<(int)grid, 256, 0, s>>>(a);
   return cudaGetLastError() == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
 }

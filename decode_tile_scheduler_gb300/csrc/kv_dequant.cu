@@ -25,6 +25,10 @@
 // per 16 elements of a (batch, row, head) vector).  Rows at or past a batch's
 // KV length are not touched (the prefill kernel masks their scores and
 // zeroes their V rows).
+//
+// MXFP4 caches take one pass (mx_dequant_kernel): an E2M1 code times its E8M0 scale
+// is a bf16 value as it is, so the copies are exact and the prompt runs as over a
+// bf16 cache.
 #include <algorithm>
 
 #include "common.cuh"
@@ -38,6 +42,7 @@ namespace {
 // when the row's page lies outside the pool.
 __device__ __forceinline__ bool locate(const DequantArgs& a, int b, int j, int hk, int d0,
                                        int64_t* code_off, int64_t* scale_row) {
+  // (code_off in elements)
   if (a.block_table) {
     const int64_t blk = a.block_table[(int64_t)b * a.max_blocks + j / a.block_size];
     if (blk < 0 || blk >= a.num_blocks) {
@@ -168,9 +173,61 @@ __global__ void __launch_bounds__(256) kv_dequant_kernel(const DequantArgs a) {
   }
 }
 
+// A thread takes the 32 elements of one scale: 16 bytes of codes, 64 bytes of bf16.
+__global__ void __launch_bounds__(256) mx_dequant_kernel(const DequantArgs a) {
+  const int groups = a.D / 32, per_row = a.KVN * groups;
+  const int64_t total = (int64_t)a.B * a.cap * per_row;
+  for (int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; t < total;
+       t += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t bj = t / per_row;
+    const int rest = (int)(t - bj * per_row);
+    const int b = (int)(bj / a.cap);
+    const int j = (int)(bj - (int64_t)b * a.cap);
+    const int kv_len = a.seqused_kv ? a.seqused_kv[b] : a.cap;
+    if (j >= kv_len) continue;
+    const KeyUse use = key_use(a, b, kv_len, j);
+    if (use == kLeft) continue;
+    const int hk = rest / groups, gr = rest % groups;
+    int64_t code_off, scale_row;
+    const bool there = use == kUsed && locate(a, b, j, hk, 32 * gr, &code_off, &scale_row);
+    const int64_t out_off = (((int64_t)b * a.cap + j) * a.KVN + hk) * a.D + 32 * gr;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      uint4* dst = reinterpret_cast<uint4*>((kv ? a.v_out : a.k_out) + out_off);
+      uint4 c = make_uint4(0u, 0u, 0u, 0u);  // zeros, not what an earlier call left there
+      uint32_t e = 127;
+      if (there) {
+        c = __ldg(reinterpret_cast<const uint4*>((kv ? a.v : a.k) + code_off / 2));
+        e = __ldg(reinterpret_cast<const uint8_t*>(kv ? a.v_scale : a.k_scale) + scale_row * groups + gr);
+      }
+      const float sc = e == 255 ? __int_as_float(0x7fffffff) : __int_as_float(e ? e << 23 : 1u << 22);
+      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t p[4], o[4];
+        e2m1x8_to_f16x2x4(w[i], p[0], p[1], p[2], p[3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[k]));
+          o[k] = pack_bf16(f.x * sc, f.y * sc);
+        }
+        dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_kv_dequant(const DequantArgs& a, int num_sms, cudaStream_t s) {
+  if (a.mx) {
+    const int64_t total = (int64_t)a.B * a.cap * a.KVN * (a.D / 32);
+    if (total > 0) {
+      const int grid = (int)std::min<int64_t>((total + 255) / 256, (int64_t)num_sms * 32);
+      mx_dequant_kernel<<<grid, 256, 0, s>>>(a);
+    }
+    return cudaGetLastError();
+  }
   cudaError_t e = cudaMemsetAsync(a.smax, 0, sizeof(uint32_t) * 2 * (size_t)a.B * a.KVN, s);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)a.B * a.cap * a.KVN;

@@ -375,8 +375,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv_evict_kernel(const EvictArgs a
   // makes its small copies (weight, position, scales); then the warp copies the
   // rows, 16 bytes of K or V per lane, kInFlight moves in flight.  (With every lane
   // finding the rows of every move the address arithmetic bound the phase.)
-  const int row_pieces = a.c.D * (a.c.fp8 ? 1 : 2) / 16;  // 16-byte pieces of a K row: 8 or 16
-  const int per = 16 / row_pieces;           // moves a warp makes side by side: 2 or 1
+  // 16-byte pieces of a K row: 16 or 8 (bf16), 8 (FP8), 4 (MXFP4)
+  const int row_pieces = a.c.D * (a.c.mx ? 1 : a.c.fp8 ? 2 : 4) / 32;
+  const int per = 16 / row_pieces;           // moves a warp makes side by side: 1, 2, 4
   const int grp = lane / (2 * row_pieces), x = lane % (2 * row_pieces);
   uint4* pool = reinterpret_cast<uint4*>(x >= row_pieces ? a.c.v : a.c.k) + x % row_pieces;
   auto row_of = [&](int j) {
@@ -406,6 +407,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv_evict_kernel(const EvictArgs a
       if (a.c.fp8 && ok) {  // (D = 128: two scales a row)
         ks = reinterpret_cast<const float2*>(a.c.ks)[f.srow];
         vs = reinterpret_cast<const float2*>(a.c.vs)[f.srow];
+      } else if (a.c.mx && ok) {  // (four bytes)
+        ks.x = a.c.ks[f.srow];
+        vs.x = a.c.vs[f.srow];
       }
     }
     const uint32_t fine = __ballot_sync(0xffffffffu, ok);
@@ -430,6 +434,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv_evict_kernel(const EvictArgs a
       if (a.c.fp8 && ok) {
         reinterpret_cast<float2*>(a.c.ks)[scale_to] = ks;
         reinterpret_cast<float2*>(a.c.vs)[scale_to] = vs;
+      } else if (a.c.mx && ok) {
+        a.c.ks[scale_to] = ks.x;
+        a.c.vs[scale_to] = vs.x;
       }
       if (!ok && a.status) atomicExch(a.status, 3);
     }

@@ -17,6 +17,11 @@
  *           attention weight goes by.
  *   APPEND  new K and V rows written to their pages, quantised where the cache
  *           is FP8 (fia_kv_append).
+ *   PAGES   pages given to the sequences that grew and taken back from those that
+ *           shrank, and the slot and position of every new token
+ *           (fia_assign_pages).
+ *   ROTATE  the heads of new queries and keys normed and rotated to their
+ *           positions, K and V written to their slots (fia_norm_rope_append).
  *   EVICT   a cache cut down to a budget of keys per KV head: the first and the
  *           newest tokens stay, and of the others those with the largest
  *           weights (fia_kv_evict).
@@ -51,7 +56,10 @@
  *    lse = +inf, with or without a sink ("...V4" empty-tensor rule; "...V2"
  *    invalid-row correction);
  *  - FP8 KV: E4M3 codes with one fp32 scale per 64 consecutive elements of D,
- *    value = code * scale; sparse packed FP8 rows carry E8M0 tile scales.
+ *    value = code * scale; sparse packed FP8 rows carry E8M0 tile scales;
+ *  - MXFP4 KV: E2M1 codes (sign, two exponent bits, one of mantissa: 0, 0.5, 1,
+ *    1.5, 2, 3, 4, 6) with one E8M0 scale byte s per 32 consecutive elements of
+ *    D, value = code * 2^(s - 127); s = 255 makes the 32 values NaN.
  */
 #ifndef FIA_H_
 #define FIA_H_
@@ -82,6 +90,7 @@ typedef int fia_status;
 
 #define FIA_KV_BF16 0
 #define FIA_KV_FP8_E4M3 1
+#define FIA_KV_MXFP4 4 /* E2M1 codes, one E8M0 scale per 32 elements               */
 
 /* Mask modes ("...V5" Attention Mask group, sparseMode 0-4).  Row i of a
  * sequence with q_len query rows and kv_len keys sees key j (0 <= j < kv_len)
@@ -130,6 +139,10 @@ typedef int fia_status;
  *    per-token, per-head scale shape (blockNum, N, blockSize) of the "V5"
  *    dequantisation parameter group (DequantChecker), and its non-paged form
  *    (B, N, KV_S), with the D/64 tiles of a row as the last axis.
+ *  - MXFP4 (D = 128): k_cache/v_cache are bytes [.., D/2], element 2i in the lower
+ *    half of byte i, element 2i + 1 in its upper half; k_scale/v_scale bytes
+ *    [num_blocks, KV_N, block_size, D/32] (paged) or [B, KV_N, max_seqlen_kv,
+ *    D/32] (contiguous; max_seqlen_kv a multiple of 4).  block_size as for FP8.
  * Alignment: q, out, k_cache, v_cache, k_scale, v_scale 16-byte aligned;
  * token strides multiples of 8 elements. */
 typedef struct fia_params {
@@ -150,10 +163,10 @@ typedef struct fia_params {
     int64_t out_token_stride; /* elements between tokens of out (0: Q_N*D)     */
     const void *k_cache;
     const void *v_cache;
-    const float *k_scale;     /* FP8 only                                      */
-    const float *v_scale;     /* FP8 only                                      */
+    const void *k_scale;      /* FP8: fp32; MXFP4: E8M0 bytes                  */
+    const void *v_scale;      /* the same                                      */
     int32_t kv_dtype;         /* FIA_KV_*                                      */
-    int32_t quant_tile;       /* FP8: 64                                       */
+    int32_t quant_tile;       /* FP8: 64; MXFP4: 32                            */
     const int32_t *block_table;   /* int32 [B, max_blocks_per_seq] or NULL     */
     int32_t max_blocks_per_seq;
     int32_t block_size;
@@ -320,12 +333,12 @@ typedef struct fia_kv_cache {
     int32_t num_kv_heads;     /* KV_N                                          */
     int32_t head_dim;         /* D                                             */
     int32_t kv_dtype;         /* FIA_KV_*                                      */
-    int32_t quant_tile;       /* FP8: 64                                       */
+    int32_t quant_tile;       /* FP8: 64; MXFP4: 32                            */
     int32_t kv_layout;        /* FIA_KV_LAYOUT_* (paged caches)                */
     void *k_cache;
     void *v_cache;
-    float *k_scale;           /* FP8 only                                      */
-    float *v_scale;           /* FP8 only                                      */
+    void *k_scale;            /* FP8: fp32; MXFP4: E8M0 bytes                  */
+    void *v_scale;            /* the same                                      */
     const int32_t *block_table;   /* int32 [B, max_blocks_per_seq] or NULL     */
     int32_t max_blocks_per_seq;
     int32_t block_size;
@@ -347,7 +360,11 @@ typedef struct fia_kv_cache {
  *    amax is 0) and code = x / scale rounded to nearest even, saturated at
  *    448, both in fp32 with correctly rounded divisions.  A NaN element gets
  *    the NaN code and does not count in amax; an infinite one counts as the
- *    largest finite bf16 value.
+ *    largest finite bf16 value.  MXFP4: per 32 elements the scale is the smallest
+ *    2^e, -127 <= e, with amax <= 6 * 2^e (1 where amax is 0) and code = x / 2^e
+ *    rounded to nearest, ties to the even code, saturated at 6; 32 elements with
+ *    a NaN among them get the scale 255 and codes of 0; an infinite one counts as
+ *    the largest finite bf16 value.
  *  - weights (nullable): 0 for the new slots.  positions (nullable):
  *    tokens_seen[b] - q_len + i with tokens_seen (int32 [B], the tokens of the
  *    sequence so far, the new ones among them), else the slot.
@@ -381,6 +398,108 @@ typedef struct fia_append_params {
     int32_t reserved[8];      /* must be 0                                     */
 } fia_append_params;
 fia_status fia_kv_append(const fia_append_params *p, void *stream);
+
+/* PAGES.  The block table of a paged cache brought up to the sequences' lengths, on
+ * the device.  A sequence of n = seqused_kv[b] keys (the new rows counted; below 0
+ * counts as 0) needs ceil(n / block_size) pages, at most max_blocks_per_seq; it holds
+ * pages_held[b], its first entries of the table.
+ *  - Pages past the need go back: in the order of the sequences, and of their entries,
+ *    they are stored at free_pages[free_count], free_pages[free_count + 1], ... (their
+ *    entries stay as they are).  Then the missing ones are taken, in the same order,
+ *    from the end of that list backwards, and stored in the table.  So the list's first
+ *    free_count entries stay as they were, and those at and past the new count may hold
+ *    anything.
+ *  - pages_held_out[b] is what each sequence then holds, *free_count_out what is left.
+ *    They may be the inputs themselves; where they are others, the same call again does
+ *    the same again.
+ *  - Where the list runs out, the missing entries become -1 (no page: they read as
+ *    zeros, and appends leave their rows out), pages_held_out counts the pages that
+ *    were there, and *status (nullable, a device int32 that the caller has cleared)
+ *    becomes 3; so it does where free_pages has no room for what comes back.
+ *  - slots and positions (nullable, int32, one per token row): row i of a sequence's
+ *    q_len new rows is key j = n - q_len + i; its slot is page * block_size +
+ *    j % block_size, its position j, or with tokens_seen (int32 [B], the tokens of the
+ *    sequence so far, the new ones among them) tokens_seen[b] - q_len + i.  A row of no
+ *    sequence (below cu_seqlens_q[0], at or past cu_seqlens_q[B]) or before its first key
+ *    (j < 0) gets -1 and -1.  A row past the capacity, or whose page lies outside
+ *    [0, num_blocks), gets the slot -1, and *status becomes 3.
+ *  - Counts outside their ranges are taken at the range's end.  A page that is listed
+ *    twice is given twice.  One launch, no workspace, deterministic. */
+typedef struct fia_pages_params {
+    int32_t batch;            /* B, 1 .. 65536                                 */
+    int32_t block_size;       /* a multiple of 16, <= 1024                     */
+    int32_t max_blocks_per_seq;   /* entries of a table row (B times it < 2^31) */
+    int32_t num_blocks;       /* pages in the pool, entries of free_pages      */
+    int32_t layout;           /* FIA_LAYOUT_*: rows [B, S], or [T]             */
+    int32_t seqlen_q;         /* BSND: S (0: no rows)                          */
+    int32_t total_q;          /* TND: T                                        */
+    int32_t pad0_;
+    const int32_t *seqused_kv;    /* int32 [B], the new rows counted           */
+    const int32_t *cu_seqlens_q;  /* TND: int32 [B+1], non-decreasing          */
+    const int32_t *tokens_seen;   /* int32 [B] or NULL                         */
+    int32_t *block_table;         /* int32 [B, max_blocks_per_seq]             */
+    const int32_t *pages_held;    /* int32 [B]                                 */
+    int32_t *pages_held_out;      /* int32 [B]                                 */
+    int32_t *free_pages;          /* int32 [num_blocks]                        */
+    const int32_t *free_count;    /* int32 [1]                                 */
+    int32_t *free_count_out;      /* int32 [1]                                 */
+    int32_t *slots;           /* int32, one per row, or NULL                   */
+    int32_t *positions;       /* int32, one per row, or NULL                   */
+    int32_t *status;          /* device int32 or NULL                          */
+    int32_t reserved[8];      /* must be 0                                     */
+} fia_pages_params;
+fia_status fia_assign_pages(const fia_pages_params *p, void *stream);
+
+/* ROTATE.  For every token row t with positions[t] >= 0 and every head x (D values):
+ *   y = x * weight / sqrt(mean(x^2) + eps)      (no weight: y = x)
+ *   the first rotary_dim values of y in pairs (a, b), pair i of rotary_dim / 2:
+ *     (a cos - b sin, b cos + a sin),  cos = cos_sin[positions[t]][i],
+ *     sin = cos_sin[positions[t]][rotary_dim / 2 + i]
+ *   pair i is (y[i], y[i + rotary_dim / 2]), or with interleaved (y[2i], y[2i + 1]).
+ * All in fp32, rounded once: queries to bf16 in q_out; keys to the cache's type as
+ * fia_kv_append rounds (quantised from the fp32 values); values are appended as they
+ * are.  K and V of token t go to slot slots[t] of the cache: the pool row page *
+ * block_size + row (contiguous caches: b * max_seqlen_kv + j), as fia_assign_pages
+ * names them; the cache's block table is not read.
+ *  - A row with a position below 0 belongs to no sequence: nothing of it is written.
+ *    A position at or past max_positions: the same, and *status (nullable, a device
+ *    int32 that the caller has cleared) becomes 3.  A slot outside the cache: K and V
+ *    are left out, and *status becomes 3.
+ *  - q_out may be q itself (of the same token stride); otherwise the outputs share no
+ *    memory with the inputs.  Two rows with the same slot leave either's values.
+ *  - Nothing else is written.  One launch, no workspace, deterministic. */
+typedef struct fia_norm_rope_params {
+    fia_kv_cache cache;       /* its D is the heads' D; block_table as elsewhere  */
+                              /* (non-NULL for a paged cache)                   */
+    int32_t tokens;           /* T                                             */
+    int32_t num_q_heads;      /* Q_N, 0 .. 256                                 */
+    int32_t rotary_dim;       /* 0 .. D, a multiple of 16                      */
+    int32_t interleaved;      /* 0 or 1                                        */
+    int32_t max_positions;    /* rows of cos_sin                               */
+    float eps;                /* >= 0                                          */
+    const void *q;            /* bf16 [T, Q_N, D], 16-byte aligned             */
+    const void *k;            /* bf16 [T, KV_N, D]                             */
+    const void *v;            /* bf16 [T, KV_N, D]                             */
+    int64_t q_token_stride;   /* elements between tokens (0: heads * D), a      */
+    int64_t k_token_stride;   /* multiple of 8                                 */
+    int64_t v_token_stride;
+    void *q_out;              /* bf16 [T, Q_N, D]                              */
+    int64_t q_out_token_stride;
+    const void *q_weight;     /* bf16 [D], 16-byte aligned, or NULL            */
+    const void *k_weight;     /* bf16 [D], 16-byte aligned, or NULL            */
+    const float *cos_sin;     /* fp32 [max_positions, rotary_dim], 16-byte     */
+                              /* aligned (NULL where rotary_dim is 0)          */
+    const int32_t *positions; /* int32 [T]                                     */
+    const int32_t *slots;     /* int32 [T]                                     */
+    int32_t *status;          /* device int32 or NULL                          */
+    int32_t reserved[8];      /* must be 0                                     */
+} fia_norm_rope_params;
+fia_status fia_norm_rope_append(const fia_norm_rope_params *p, void *stream);
+
+/* sizeof(fia_pages_params) and sizeof(fia_norm_rope_params) as compiled into the
+ * library. */
+size_t fia_sizeof_pages_params(void);
+size_t fia_sizeof_norm_rope_params(void);
 
 /* WEIGHTS.  fia_run, and for every slot j < kv_len of every KV head g
  *   weights_out[b,g,j] = weights_in[b,g,j]
