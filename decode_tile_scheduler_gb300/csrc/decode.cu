@@ -43,9 +43,8 @@
 // movmatrix.  Softmax is online, in the exp2 domain, per column.  FP8 E4M3
 // pages are widened to fp16 in registers (exact); K tile scales multiply the
 // per-64-column partial scores and V tile scales are folded into P^T, so the
-// dequantised cache is never materialised.  MXFP4 pages take the same way with four
-// scales a row: E2M1 codes are fp16 values too, K scales multiply the partial scores
-// of each 32 elements, V scales are folded into a P^T for each 32.
+// dequantised cache is never materialised.  MXFP4 caches have a kernel of their own on the
+// same plan (decode_mx.cuh).
 #include <algorithm>
 #include <atomic>
 
@@ -75,23 +74,16 @@ __device__ __forceinline__ int pi8(int n) { return (n & 1) ? ((n + 4) & 7) : n; 
 // KV row (0..15, within a warp's 16 rows) of fragment row m
 __device__ __forceinline__ int rho16(int m) { return (m & 8) + pi8(m & 7); }
 
-// Cache formats of the kernel variants: bf16, E4M3 with an fp32 scale per 64
-// elements, E2M1 with an E8M0 scale per 32 (64-byte rows, swizzled over 64 bytes).
-enum Format { kBf16, kFp8, kMx };
-
-template <int D, int F>
+template <int D, bool FP8>
 struct DecodeCfg {
-  static constexpr bool FP8 = F == kFp8, MX = F == kMx;
-  static constexpr int kNsub = F ? 1 : D / 64;              // slices per row
-  static constexpr int kRowBytes = MX ? D / 2 : 128;        // of a slice
-  static constexpr int kTileBytes = kNsub * kKvTile * kRowBytes;  // one of K or V
-  static constexpr int kScaleWords = FP8 ? D / 64 : MX ? D / 128 : 0;  // 4-byte words of a row's scales
-  static constexpr int kScaleBytes = kKvTile * kScaleWords * 4;
+  static constexpr int kNsub = FP8 ? 1 : D / 64;            // 128-byte slices per row
+  static constexpr int kTileBytes = kNsub * kKvTile * 128;  // one of K or V
+  static constexpr int kScaleBytes = FP8 ? kKvTile * (D / 64) * 4 : 0;
   // explicit mask: one 128-byte row slice per query row of the unit
   static constexpr int kMaskBytes = kDecodeMaxRows * kKvTile;
   static constexpr int kOffMask = 2 * kTileBytes + 2 * kScaleBytes;  // inside a stage
   static constexpr int kStageBytes = 2 * kTileBytes + 2 * kScaleBytes + kMaskBytes;
-  static constexpr int kStages = MX ? 10 : FP8 ? 5 : (D == 128 ? 3 : 6);
+  static constexpr int kStages = FP8 ? 5 : (D == 128 ? 3 : 6);
   static constexpr int kQBytes = kMaxGH * D * 2;
   static constexpr int kRedBytes = 4 * kConsumers * 32 * 16;  // merge rounds: [4][8 warps][32] float4
   static constexpr int kRedMlBytes = kConsumers * kMaxGH * 2 * 4;
@@ -301,41 +293,6 @@ __device__ __forceinline__ int64_t scale_row_in(const DecodeArgs& a, int b, int 
                                                 int64_t j, int64_t jp) {
   return a.block_table ? (blk * a.KVN + hk) * a.block_size + jp
                        : ((int64_t)b * a.KVN + hk) * a.S_kv + j;
-}
-
-// MXFP4: byte offset of 16-byte chunk `chunk` (0..3) of row `row` in a tile of 64-byte
-// rows written by TMA with 64-byte swizzling.
-__device__ __forceinline__ uint32_t sw64(uint32_t row, uint32_t chunk) {
-  return row * 64u + ((chunk ^ ((row >> 1) & 3u)) << 4);
-}
-// Four E8M0 bytes as two bf16 pairs (exact; 255 is NaN, 0 is 2^-127), as four floats.
-__device__ __forceinline__ void e8m0x4_to_bf16x2x2(uint32_t w, __nv_bfloat162 (&v)[2]) {
-  uint32_t lo, hi;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-      "cvt.rn.bf16x2.ue8m0x2 %0, l;\n\tcvt.rn.bf16x2.ue8m0x2 %1, h;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-  v[0] = *reinterpret_cast<const __nv_bfloat162*>(&lo);
-  v[1] = *reinterpret_cast<const __nv_bfloat162*>(&hi);
-}
-__device__ __forceinline__ void bf16x2x2_to_f32x4(__nv_bfloat162 a, __nv_bfloat162 b, float (&f)[4]) {
-  const uint32_t x = *reinterpret_cast<const uint32_t*>(&a), y = *reinterpret_cast<const uint32_t*>(&b);
-  f[0] = __uint_as_float(x << 16);
-  f[1] = __uint_as_float(x & 0xffff0000u);
-  f[2] = __uint_as_float(y << 16);
-  f[3] = __uint_as_float(y & 0xffff0000u);
-}
-__device__ __forceinline__ void e8m0x4_to_f32x4(uint32_t w, float (&f)[4]) {
-  __nv_bfloat162 v[2];
-  e8m0x4_to_bf16x2x2(w, v);
-  bf16x2x2_to_f32x4(v[0], v[1], f);
-}
-// 2^(6 - (code - 127)) twice, for kMxRefMin <= code <= 254: a V scale times it is at
-// most 2^6.
-constexpr int kMxRefMin = 27;
-__device__ __forceinline__ __nv_bfloat162 mx_over(int code) {
-  const uint32_t h = (uint32_t)(127 + 6 + 127 - code) << 7, w = h | h << 16;
-  return *reinterpret_cast<const __nv_bfloat162*>(&w);
 }
 
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
@@ -696,14 +653,13 @@ __device__ __forceinline__ void combine_store(const DecodeArgs& a, int b, int64_
 // for the key weights; a variant of its own, so that the others keep their
 // registers (with the extra tile order in every variant the FP8 one-row kernel
 // spilled, 0 -> 12 bytes).
-template <int D, int F, int NG, bool MR, bool X>
+template <int D, bool FP8, int NG, bool MR, bool X>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv) {
-  using Cfg = DecodeCfg<D, F>;
-  constexpr bool FP8 = F == kFp8, MX = F == kMx;
+  using Cfg = DecodeCfg<D, FP8>;
   constexpr int S = Cfg::kStages;
-  constexpr int kProdWarps = F ? 4 : 2;  // producer warps (a whole warpgroup is reserved)
+  constexpr int kProdWarps = FP8 ? 4 : 2;  // producer warps (a whole warpgroup is reserved)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -828,18 +784,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (a.debug && mine && a.block_table && blk == a.num_blocks)
         atomicExch(a.err, 3);  // (read as zeros by the TMA box all the same)
       const int prow = mine ? (int)pool_row(a, r.b, r.hk, blk, jb, jp) : 0;
-      constexpr int NT = Cfg::kScaleWords;
+      constexpr int NT = D / 64;
       // FP8: the scales of one head inside a page are contiguous rows of NT
-      // floats (MXFP4: of four bytes), so each (K or V, page piece) is one bulk
-      // copy next to its TMA box.  Pieces are whole 16-byte units on 16-byte
-      // boundaries: block sizes are multiples of 32, lengths of contiguous caches
-      // even (MXFP4: multiples of 4).
+      // floats, so each (K or V, page piece) is one bulk copy next to its
+      // TMA box.  Pieces are even-length at even rows (block sizes are
+      // multiples of 32; contiguous caches have an even length), hence
+      // 16-byte aligned.
       // (a page id outside the pool reads zeros through TMA; its FP8
       // scales, which come by plain bulk copy, are zeros from zero_scales:
       // what the stage held before may be no number)
       const float* ssrc = zero_scales;
       int srows = a.box_rows;
-      if constexpr (F != kBf16) {
+      if constexpr (FP8) {
         if (mine && (!a.block_table || blk < a.num_blocks))
           ssrc = (isv ? a.v_scale : a.k_scale) + scale_row_in(a, r.b, r.hk, blk, jb, jp) * NT;
         if (!a.block_table) srows = (int)min((int64_t)a.box_rows, (int64_t)a.S_kv - jb);
@@ -848,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int q = 0; q < nrb; ++q)
         if (j0 + (int64_t)q * a.box_rows < r.kv_len) ++nvalid;
       uint32_t scale_bytes = 0;
-      if constexpr (F != kBf16)
+      if constexpr (FP8)
         scale_bytes = __reduce_add_sync(0xffffffffu, mine ? (uint32_t)(srows * NT * 4) : 0u);
       // explicit mask (K warp): the tile's slice of each of the unit's query
       // rows, 16-byte pieces up to kv_len (row strides are multiples of 16
@@ -861,8 +817,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (*reinterpret_cast<volatile int*>(misc)) return false;  // issue nothing after a time-out
       uint8_t* st = smem + s * Cfg::kStageBytes;
       if (lane == 0) {
-        uint32_t bytes = (uint32_t)(nvalid * Cfg::kNsub * a.box_rows * Cfg::kRowBytes);
-        if constexpr (F != kBf16) bytes += scale_bytes;
+        uint32_t bytes = (uint32_t)(nvalid * Cfg::kNsub * a.box_rows * 128);
+        if constexpr (FP8) bytes += scale_bytes;
         bytes += (uint32_t)(nmrows * mrow_bytes);
         mbar_arrive_expect_tx(&full[s], bytes);
       }
@@ -873,13 +829,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                       j0,
                   (uint32_t)mrow_bytes, &full[s]);
       if (mine) {
-        uint8_t* dst = st + isv * Cfg::kTileBytes + sub * (kKvTile * 128) + rb * a.box_rows * Cfg::kRowBytes;
-        const int col = (a.kv_layout == 1 ? 0 : r.hk * (MX ? D / 2 : D)) + (F ? 0 : sub * 64);
+        uint8_t* dst = st + isv * Cfg::kTileBytes + sub * (kKvTile * 128) + rb * a.box_rows * 128;
+        const int col = (a.kv_layout == 1 ? 0 : r.hk * D) + (FP8 ? 0 : sub * 64);
         if (once)
           tma_load_2d_hint(dst, isv ? &tv : &tk, &full[s], col, prow, pol);
         else
           tma_load_2d(dst, isv ? &tv : &tk, &full[s], col, prow);
-        if constexpr (F != kBf16) {
+        if constexpr (FP8) {
           float* sdst = reinterpret_cast<float*>(st + 2 * Cfg::kTileBytes) + isv * (kKvTile * NT) +
                         rb * a.box_rows * NT;
           bulk_load(sdst, ssrc, (uint32_t)(srows * NT * 4), &full[s]);
@@ -1119,7 +1075,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float slc = a.scale_log2;
     {
       const uint16_t* qsm = reinterpret_cast<const uint16_t*>(smem + Cfg::kOffQ + qs * Cfg::kQBytes);
-      if constexpr (F == kBf16) {
+      if constexpr (!FP8) {
 #pragma unroll
         for (int ng = 0; ng < NG; ++ng) {
           const int head = ng * 8 + g;  // the unit's column in this lane's B fragments
@@ -1142,10 +1098,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // in their scale factor.  Powers of two scale exactly.
         // k-step kk = 4*tile + j covers d = 64*tile + 16*q + 4*j + {0..3}:
         // slots 2q,2q+1 <- the first two, slots 2q+8,2q+9 <- the last two
-        // (MXFP4: kk = 2*group + j covers d = 32*group + 8*q + 4*j + {0..3})
-        const auto d_of = [&](int kk) {
-          return MX ? (kk >> 1) * 32 + 8 * q4 + 4 * (kk & 1) : (kk >> 2) * 64 + 16 * q4 + 4 * (kk & 3);
-        };
         uint32_t emax = 0;
 #pragma unroll
         for (int ng = 0; ng < NG; ++ng) {
@@ -1153,7 +1105,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (head < r.ncols) {
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
-              const int d0 = d_of(kk);
+              const int d0 = (kk >> 2) * 64 + 16 * q4 + 4 * (kk & 3);
               const uint2 v = *reinterpret_cast<const uint2*>(qsm + head * D + d0);
               emax = max(emax, max(max((v.x >> 7) & 0xffu, (v.x >> 23) & 0xffu),
                                    max((v.y >> 7) & 0xffu, (v.y >> 23) & 0xffu)));
@@ -1170,7 +1122,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool ok = head < r.ncols;
 #pragma unroll
           for (int kk = 0; kk < KS; ++kk) {
-            const int d0 = d_of(kk);
+            const int d0 = (kk >> 2) * 64 + 16 * q4 + 4 * (kk & 3);
             if (ok) {
               const uint2 v = *reinterpret_cast<const uint2*>(qsm + head * D + d0);
               const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
@@ -1201,9 +1153,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       l_r[ng][0] = l_r[ng][1] = 0.f;
     }
     int vexp[2] = {0, 0};  // FP8: exponent of the V scale reference per d-tile (0: none yet)
-    // MXFP4: the code of the V scale reference, and its 2^(6 - e) (see P V below)
-    int vref = kMxRefMin;
-    __nv_bfloat162 vinv = mx_over(kMxRefMin);
 
     // FP8: the P V of each tile runs one tile late, beside the next tile's
     // Q K^T and softmax (two independent instruction streams per warp)
@@ -1217,69 +1166,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     // memory, once for a warp's 16 rows where some are gone: under a band with first
     // tokens, where that is often, and for FP8 units of 8 columns (long FP8 135.8 ->
     // 132.2 us; the FP8 kernel of 16 columns 115.0 -> 118.5, four bf16 rows 78.9 -> 79.6).
-    // (E2M1 codes are all numbers: MXFP4 rows that are gone count as zeros by their scales.)
-    constexpr bool kClear = !MX && (X || (FP8 && NG == 1));
-    constexpr int kPb = MX ? 4 : 2;  // P^T operands: one for each scale of a V row
+    constexpr bool kClear = X || (FP8 && NG == 1);
     struct PendingPV {
       bool valid;
       int s;
       int jw;
       bool cut;
-      uint32_t pb[kPb][NG][2];
-      float fct[2][NG][2];  // (MXFP4: the first)
+      uint32_t pb[2][NG][2];
+      float fct[2][NG][2];
     } prev;
     prev.valid = false;
-    auto pv_mx = [&](const PendingPV& pp) {
-      bool resc = false;
-#pragma unroll
-      for (int ng = 0; ng < NG; ++ng) resc |= (pp.fct[0][ng][0] != 1.f) | (pp.fct[0][ng][1] != 1.f);
-      if (__any_sync(0xffffffffu, resc)) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int ng = 0; ng < NG; ++ng) {
-            acc[i][ng][0] *= pp.fct[0][ng][0];
-            acc[i][ng][1] *= pp.fct[0][ng][1];
-            acc[i][ng][2] *= pp.fct[0][ng][0];
-            acc[i][ng][3] *= pp.fct[0][ng][1];
-          }
-      }
-      // A lane takes four elements d = 32*j + 4*g .. +3 of each group j (two bytes) of
-      // its keys 2q, 2q+1, 2q+8, 2q+9; m-tile 2j + h holds the elements 2h of them in
-      // its fragment rows 0-7, 2h + 1 in rows 8-15, so that an m-tile lies in one group.
-      const uint8_t* vt = smem + pp.s * Cfg::kStageBytes + Cfg::kTileBytes;
-#pragma unroll
-      for (int jj = 0; jj < 4; jj += 2) {  // two groups at a time
-        uint32_t w[4];
-#pragma unroll
-        for (int sl = 0; sl < 4; ++sl) {
-          const int row = R0 + rho16(2 * q4 + (sl & 1) + (sl >> 1) * 8);
-          const uint32_t x = *reinterpret_cast<const uint16_t*>(vt + sw64(row, jj) + 2 * g);
-          const uint32_t y = *reinterpret_cast<const uint16_t*>(vt + sw64(row, jj + 1) + 2 * g);
-          w[sl] = x | y << 16;
-        }
-        // bytes of two keys' codes of one element: elements 0, 2 of each group, and 1, 3
-        uint32_t ev[2], od[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          ev[k] = (w[2 * k] & 0x0f0f0f0fu) | ((w[2 * k + 1] << 4) & 0xf0f0f0f0u);
-          od[k] = ((w[2 * k] >> 4) & 0x0f0f0f0fu) | (w[2 * k + 1] & 0xf0f0f0f0u);
-        }
-        uint32_t va[4][4];  // [m-tile of the four][fragment register]
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          e2m1x8_to_f16x2x4(ev[k], va[0][2 * k], va[1][2 * k], va[2][2 * k], va[3][2 * k]);
-          e2m1x8_to_f16x2x4(od[k], va[0][2 * k + 1], va[1][2 * k + 1], va[2][2 * k + 1], va[3][2 * k + 1]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int ng = 0; ng < NG; ++ng)
-            mma_f16(acc[2 * jj + i][ng], va[i], pp.pb[jj + (i >> 1)][ng][0], pp.pb[jj + (i >> 1)][ng][1]);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[pp.s]);
-    };
     auto pv_fp8 = [&](const PendingPV& pp) {
       bool resc = false;
 #pragma unroll
@@ -1364,7 +1260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (FP8: the stage of the tile before stays held until the next one that runs.
         // Behind a tile that ran, the window's last and the first tokens' one follow at
         // most, and the producer needs no more than two stages for them)
-        static_assert(F == kBf16 || S >= 4, "a stage held over two tiles that are passed by");
+        static_assert(!FP8 || S >= 4, "a stage held over two tiles that are passed by");
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[s]);
         continue;
@@ -1389,33 +1285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float sc[NG][4];
 #pragma unroll
       for (int ng = 0; ng < NG; ++ng) sc[ng][0] = sc[ng][1] = sc[ng][2] = sc[ng][3] = 0.f;
-      if constexpr (MX) {
-        const int rowa = R0 + pi8(g), rowb = R0 + 8 + pi8(g);
-        // the four scales of rows g and g + 8 (NaN: the row's scores are NaN)
-        const uint32_t* ks = reinterpret_cast<const uint32_t*>(stp + 2 * Cfg::kTileBytes);
-        float fa[4], fb[4];
-        e8m0x4_to_f32x4(ks[rowa], fa);
-        e8m0x4_to_f32x4(ks[rowb], fb);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // 8 elements of each row: d = 32*j + 8*q .. +7
-          const uint32_t wa = *reinterpret_cast<const uint32_t*>(stp + sw64(rowa, j) + 4 * q4);
-          const uint32_t wb = *reinterpret_cast<const uint32_t*>(stp + sw64(rowb, j) + 4 * q4);
-          uint32_t ka[2][4];
-          e2m1x8_to_f16x2x4(wa, ka[0][0], ka[0][2], ka[1][0], ka[1][2]);
-          e2m1x8_to_f16x2x4(wb, ka[0][1], ka[0][3], ka[1][1], ka[1][3]);
-#pragma unroll
-          for (int ng = 0; ng < NG; ++ng) {
-            float s4[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(s4, ka[0], qb[ng][2 * j][0], qb[ng][2 * j][1]);
-            mma_f16(s4, ka[1], qb[ng][2 * j + 1][0], qb[ng][2 * j + 1][1]);
-            sc[ng][0] += s4[0] * fa[j];
-            sc[ng][1] += s4[1] * fa[j];
-            sc[ng][2] += s4[2] * fb[j];
-            sc[ng][3] += s4[3] * fb[j];
-          }
-        }
-      } else if constexpr (!FP8) {
+      if constexpr (!FP8) {
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
           // matrices: (rows 0-7, lo 8 d), (rows 8-15, lo), (rows 0-7, hi), (rows 8-15, hi)
@@ -1558,61 +1428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       // ---------------- O^T += V^T P^T ----------------
-      if constexpr (MX) {
-        // P times a V scale is multiplied in fp16, over 2^(vref - 127 - 6): vref is the
-        // largest scale code that the warp's tiles had so far, so the products stay
-        // below 2^14, and a key of P = 1 keeps fp16's bits down to scales 2^20 below the
-        // largest.  A new vref moves O by an exact power of two.
-        const uint32_t* vs = reinterpret_cast<const uint32_t*>(stp + 2 * Cfg::kTileBytes + Cfg::kScaleBytes);
-        uint32_t w0 = vs[R0 + pi8(g)], w1 = vs[R0 + 8 + pi8(g)];
-        if (cut) {  // rows that are gone count as zeros
-          if (gone(jg0)) w0 = 0u;
-          if (gone(jg1)) w1 = 0u;
-        }
-        __nv_bfloat162 v0[2], v1[2];
-        e8m0x4_to_bf16x2x2(w0, v0);
-        e8m0x4_to_bf16x2x2(w1, v1);
-        // (the larger of two drops a NaN)
-        const __nv_bfloat162 mx2 = __hmax2(__hmax2(v0[0], v0[1]), __hmax2(v1[0], v1[1]));
-        const uint32_t mxb = *reinterpret_cast<const uint32_t*>(&mx2);
-        // (positive: their bits order as they do; NaN alone, 0x7fff, is no reference)
-        uint32_t top = max(mxb >> 16, mxb & 0xffffu);
-        if (top >= 0x7f80u) top = min(mxb >> 16, mxb & 0xffffu) >= 0x7f80u ? 0u : min(mxb >> 16, mxb & 0xffffu);
-        float ratio = 1.f;
-        if (__any_sync(0xffffffffu, (int)(top >> 7) > vref)) {
-          const int en = max(vref, (int)(__reduce_max_sync(0xffffffffu, top) >> 7));
-          // (a jump past 2^-126 leaves a negligible old sum and gives 0)
-          ratio = __int_as_float(max(127 + vref - en, 0) << 23);
-          vref = en;
-          vinv = mx_over(en);
-        }
-        float fa[4], fb[4];
-        bf16x2x2_to_f32x4(__hmul2(v0[0], vinv), __hmul2(v0[1], vinv), fa);
-        bf16x2x2_to_f32x4(__hmul2(v1[0], vinv), __hmul2(v1[1], vinv), fb);
-        uint32_t pb[4][NG][2];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int ng = 0; ng < NG; ++ng) {
-            pb[j][ng][0] = movmatrix_t(pack_f16(sc[ng][0] * fa[j], sc[ng][1] * fa[j]));
-            pb[j][ng][1] = movmatrix_t(pack_f16(sc[ng][2] * fb[j], sc[ng][3] * fb[j]));
-          }
-        // the previous tile's P V beside this tile's work above, as below for FP8
-        if (prev.valid) pv_mx(prev);
-        prev.valid = true;
-        prev.s = s;
-#pragma unroll
-        for (int ng = 0; ng < NG; ++ng) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            prev.pb[j][ng][0] = pb[j][ng][0];
-            prev.pb[j][ng][1] = pb[j][ng][1];
-          }
-          prev.fct[0][ng][0] = corr[ng][0] * ratio;
-          prev.fct[0][ng][1] = corr[ng][1] * ratio;
-        }
-        continue;
-      } else if constexpr (!FP8) {
+      if constexpr (!FP8) {
         // P^T as the B operand: transpose the two 8x8 halves of S^T
         uint32_t pb[NG][2];
 #pragma unroll
@@ -1732,20 +1548,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (FP8) {
       if (prev.valid) pv_fp8(prev);  // the chunk's last tile
     }
-    if constexpr (MX) {
-      if (prev.valid) pv_mx(prev);
-    }
 
     // ---------------- merge the eight warps' states ----------------
-    if constexpr (MX) {
-      const float f = __int_as_float((vref - 6) << 23);  // 2^(vref - 127 - 6)
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int ng = 0; ng < NG; ++ng) {
-          acc[i][ng][0] *= f; acc[i][ng][1] *= f; acc[i][ng][2] *= f; acc[i][ng][3] *= f;
-        }
-    }
     if constexpr (FP8) {
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
@@ -1758,8 +1562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // d index of accumulator row: m-tile i, fragment row gg (0..15)
     auto drow = [&](int i, int gg) -> int {
-      if constexpr (MX) return 32 * (i >> 1) + 4 * (gg & 7) + 2 * (i & 1) + (gg >> 3);
-      else if constexpr (!FP8) return 16 * i + gg;
+      if constexpr (!FP8) return 16 * i + gg;
       else return 64 * (i >> 2) + 8 * (gg & 7) + 4 * (gg >> 3) + (i & 3);
     };
 #pragma unroll
@@ -2196,6 +1999,7 @@ __global__ void __launch_bounds__(256, 4)
 }  // namespace fia
 
 #include "decode_cluster.cuh"
+#include "decode_mx.cuh"
 
 namespace fia {
 
@@ -2203,8 +2007,8 @@ namespace fia {
 // host launchers
 // ---------------------------------------------------------------------------
 size_t decode_smem_bytes(int D, int fp8) {
-  if (fp8) return DecodeCfg<128, kFp8>::kSmem;
-  return D == 64 ? DecodeCfg<64, kBf16>::kSmem : DecodeCfg<128, kBf16>::kSmem;
+  if (fp8) return DecodeCfg<128, true>::kSmem;
+  return D == 64 ? DecodeCfg<64, false>::kSmem : DecodeCfg<128, false>::kSmem;
 }
 
 cudaError_t launch_decode_schedule(const DecodeArgs& a, cudaStream_t s) {
@@ -2212,11 +2016,11 @@ cudaError_t launch_decode_schedule(const DecodeArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <int D, int F, int NG, bool MR, bool X>
+template <int D, bool FP8, int NG, bool MR, bool X>
 static cudaError_t launch_decode_t(const DecodeArgs& a, const CUtensorMap& tk,
                                    const CUtensorMap& tv, cudaStream_t s) {
-  using Cfg = DecodeCfg<D, F>;
-  auto kern = decode_kernel<D, F, NG, MR, X>;
+  using Cfg = DecodeCfg<D, FP8>;
+  auto kern = decode_kernel<D, FP8, NG, MR, X>;
   // the shared-memory opt-in is per device and function: set it once for each
   static std::atomic<uint64_t> done_mask[4];
   int dev = 0;
@@ -2231,30 +2035,28 @@ static cudaError_t launch_decode_t(const DecodeArgs& a, const CUtensorMap& tk,
   return launch_pdl(kern, dim3(a.num_ctas), dim3(kThreads), Cfg::kSmem, s, a, tk, tv);
 }
 
-template <int D, int F, int NG>
+template <int D, bool FP8, int NG>
 static cudaError_t launch_decode_mr(const DecodeArgs& a, const CUtensorMap& tk,
                                     const CUtensorMap& tv, cudaStream_t s) {
   const bool mr = a.S_max > 1 || a.mask != nullptr;
   if (a.first_tokens > 0 || a.scores)
-    return mr ? launch_decode_t<D, F, NG, true, true>(a, tk, tv, s)
-              : launch_decode_t<D, F, NG, false, true>(a, tk, tv, s);
-  return mr ? launch_decode_t<D, F, NG, true, false>(a, tk, tv, s)
-            : launch_decode_t<D, F, NG, false, false>(a, tk, tv, s);
+    return mr ? launch_decode_t<D, FP8, NG, true, true>(a, tk, tv, s)
+              : launch_decode_t<D, FP8, NG, false, true>(a, tk, tv, s);
+  return mr ? launch_decode_t<D, FP8, NG, true, false>(a, tk, tv, s)
+            : launch_decode_t<D, FP8, NG, false, false>(a, tk, tv, s);
 }
 
 static cudaError_t launch_decode_main(const DecodeArgs& a, const CUtensorMap& tk,
                                       const CUtensorMap& tv, int kv_dtype, cudaStream_t s) {
   const bool two = a.GH > 8;
-  if (kv_dtype == FIA_KV_MXFP4)
-    return two ? launch_decode_mr<128, kMx, 2>(a, tk, tv, s)
-               : launch_decode_mr<128, kMx, 1>(a, tk, tv, s);
+  if (kv_dtype == FIA_KV_MXFP4) return launch_decode_mx(a, tk, tv, s);
   if (kv_dtype == FIA_KV_FP8_E4M3)
-    return two ? launch_decode_mr<128, kFp8, 2>(a, tk, tv, s)
-               : launch_decode_mr<128, kFp8, 1>(a, tk, tv, s);
-  if (a.D == 64) return two ? launch_decode_mr<64, kBf16, 2>(a, tk, tv, s)
-                            : launch_decode_mr<64, kBf16, 1>(a, tk, tv, s);
-  return two ? launch_decode_mr<128, kBf16, 2>(a, tk, tv, s)
-             : launch_decode_mr<128, kBf16, 1>(a, tk, tv, s);
+    return two ? launch_decode_mr<128, true, 2>(a, tk, tv, s)
+               : launch_decode_mr<128, true, 1>(a, tk, tv, s);
+  if (a.D == 64) return two ? launch_decode_mr<64, false, 2>(a, tk, tv, s)
+                            : launch_decode_mr<64, false, 1>(a, tk, tv, s);
+  return two ? launch_decode_mr<128, false, 2>(a, tk, tv, s)
+             : launch_decode_mr<128, false, 1>(a, tk, tv, s);
 }
 
 template <int D>

@@ -1,0 +1,750 @@
+// decode_mx.cuh -- the decode kernel over an MXFP4 cache (part of decode.cu: the same
+// plan, queue, units and combine).
+//
+// A key is 68 bytes of K and of V where FP8 has 136, for the same number of elements to
+// widen, so the kernel is bound by the instructions of an element, not by memory.  What
+// it does about that:
+//  - Three CTAs to an SM (two with 16 columns), each with one producer warp and four
+//    consumer warps of 32 rows of a tile, so that a chunk's set-up, waits and merge run
+//    beside the others' products, and twelve consumer warps hide each other's latencies.
+//  - Codes go from shared memory to mma fragments by ldmatrix.  K: 32 bits of a row are
+//    eight elements of one scale group, two k-steps of m16n8k16 (the order of a
+//    contraction is free).  V: to the transposing ldmatrix four elements of a key are
+//    one 16-bit unit, so a lane gets two keys' units in a register; masks and shifts
+//    pair the keys' codes in bytes, and cvt makes an fp16 pair of a byte.
+//  - E2M1 codes are fp16 values as they are.  K scales multiply the partial scores of
+//    their 32 elements in fp32; V scales multiply P in fp32, before it is rounded to
+//    fp16 for the products (a P^T for each of the four groups of 32 elements).
+//
+// Measured issue costs (clocks per warp instruction and scheduler): cvt of a byte, prmt,
+// lop3 2, movmatrix and ex2 4.
+#pragma once
+
+namespace fia {
+namespace {
+
+template <int NG, bool MR>
+struct MxCfg {
+  static constexpr int D = 128, kRowBytes = D / 2;
+  static constexpr int kWarps = 4, kRows = kKvTile / kWarps;  // consumers, rows of a tile each
+  static constexpr int kThreads = 32 * (kWarps + 1);
+  static constexpr int kCtas = NG == 1 ? 3 : 2;               // to an SM
+  static constexpr int kTileBytes = kKvTile * kRowBytes;      // K, or V
+  static constexpr int kScaleBytes = kKvTile * 4;
+  static constexpr int kOffScale = 2 * kTileBytes, kOffMask = kOffScale + 2 * kScaleBytes;
+  static constexpr int kStageBytes = kOffMask + (MR ? kDecodeMaxRows * kKvTile : 0);
+  static constexpr int kStages = NG == 1 ? 3 : 5;
+  static constexpr int kQBytes = 8 * NG * D * 2;
+  static constexpr int kOffQ = kStages * kStageBytes;
+  static constexpr int kOffRed = kOffQ + 2 * kQBytes;         // [4][warps][32] float4
+  static constexpr int kOffRedMl = kOffRed + 4 * kWarps * 32 * 16;
+  static constexpr int kOffBar = kOffRedMl + kWarps * 8 * NG * 8;
+  static constexpr int kOffMsg = kOffBar + 8 * (2 * kStages + 4);
+  static constexpr int kOffMisc = kOffMsg + 2 * 128;
+  static constexpr int kSmem = kOffMisc + 16 + 1024;          // + alignment slack
+  static_assert(kStageBytes % 1024 == 0 && kOffMsg % 16 == 0, "alignment");
+  static_assert(kCtas * (kSmem + 1024) <= 233472, "shared memory");
+};
+
+// Byte offset of 16-byte chunk `chunk` (0..3) of row `row` in a tile of 64-byte rows
+// written by TMA with 64-byte swizzling.
+__device__ __forceinline__ uint32_t sw64(uint32_t row, uint32_t chunk) {
+  return row * 64u + ((chunk ^ ((row >> 1) & 3u)) << 4);
+}
+// Four E8M0 bytes as two bf16 pairs (exact; 255 is NaN, 0 is 2^-127), as four floats.
+__device__ __forceinline__ void e8m0x4_to_bf16x2x2(uint32_t w, __nv_bfloat162 (&v)[2]) {
+  uint32_t lo, hi;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.bf16x2.ue8m0x2 %0, l;\n\tcvt.rn.bf16x2.ue8m0x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+  v[0] = *reinterpret_cast<const __nv_bfloat162*>(&lo);
+  v[1] = *reinterpret_cast<const __nv_bfloat162*>(&hi);
+}
+__device__ __forceinline__ void bf16x2x2_to_f32x4(__nv_bfloat162 a, __nv_bfloat162 b, float (&f)[4]) {
+  const uint32_t x = *reinterpret_cast<const uint32_t*>(&a), y = *reinterpret_cast<const uint32_t*>(&b);
+  f[0] = __uint_as_float(x << 16);
+  f[1] = __uint_as_float(x & 0xffff0000u);
+  f[2] = __uint_as_float(y << 16);
+  f[3] = __uint_as_float(y & 0xffff0000u);
+}
+__device__ __forceinline__ void e8m0x4_to_f32x4(uint32_t w, float (&f)[4]) {
+  __nv_bfloat162 v[2];
+  e8m0x4_to_bf16x2x2(w, v);
+  bf16x2x2_to_f32x4(v[0], v[1], f);
+}
+// 2^(6 - (code - 127)) twice, for kMxRefMin <= code <= 254: a V scale times it is at
+// most 2^6.
+constexpr int kMxRefMin = 27;
+__device__ __forceinline__ __nv_bfloat162 mx_over(int code) {
+  const uint32_t h = (uint32_t)(127 + 6 + 127 - code) << 7, w = h | h << 16;
+  return *reinterpret_cast<const __nv_bfloat162*>(&w);
+}
+
+// NG, MR, X: as decode_kernel's.
+template <int NG, bool MR, bool X>
+__global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
+    decode_mx_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tk,
+                     const __grid_constant__ CUtensorMap tv) {
+  using Cfg = MxCfg<NG, MR>;
+  constexpr int D = Cfg::D, S = Cfg::kStages, W = Cfg::kWarps;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::kOffBar);
+  uint64_t* empty = full + S;
+  uint64_t* qfull = empty + S;
+  uint64_t* qempty = qfull + 2;
+  int* misc = reinterpret_cast<int*>(smem + Cfg::kOffMisc);
+  UnitMsg* msg = reinterpret_cast<UnitMsg*>(smem + Cfg::kOffMsg);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], W);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&qfull[s], 1);
+      mbar_init(&qempty[s], W);
+    }
+    misc[0] = 0;  // abort flag
+    fence_barrier_init();
+    tma_prefetch_desc(&tk);
+    tma_prefetch_desc(&tv);
+  }
+  __syncthreads();
+  pdl_wait();  // the plan (and anything else before us on the stream) is complete
+
+  if (warp == W) {
+    // ======================= producer =======================
+    // Lanes 0-15 issue the K boxes (and the explicit-mask slices), 16-31 the V boxes, each
+    // with its scales beside it; page ids as in decode_kernel, one per lane.
+    const int isv = lane >> 4, rb = lane & 15;
+    const int nrb = kKvTile / a.box_rows;
+    int it = 0, ucount = 0;
+    bool aborted = false;
+    const bool once = a.HG == 1;
+    const uint64_t pol = l2_evict_first_policy();
+    const int4 ent0 = a.queue[blockIdx.x];
+    int64_t hd[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) hd[k] = a.sched[k];
+    const int64_t pmark = *a.prefill_mark;
+    const bool plan_ok = (hd[5] == kDecodePlanMark) & (hd[6] == a.B) & (hd[7] == a.num_ctas) &
+                         (hd[0] >= 1) & (hd[1] >= 1) & (hd[2] >= 0) & (hd[2] <= a.max_chunks) &
+                         (pmark != kPrefillPlanMark);
+    if (!plan_ok && lane == 0 && blockIdx.x == 0) atomicExch(a.err, 2);
+    const int64_t C = plan_ok ? hd[0] : 1, c2 = plan_ok ? hd[1] : 1;
+    const int64_t N = plan_ok ? hd[2] : 0;
+    const int UPB = a.KVN * a.HG;
+    int64_t g = plan_ok ? (int64_t)blockIdx.x : N;
+    int4 ent = g < N ? ent0 : make_int4(0, 0, 0, 0);
+    while (g < N) {
+      int gn_l = 0;  // the next claim, read behind this chunk's first tile
+      if (lane == 0) gn_l = (int)gridDim.x + atomicAdd(a.claim, 1);
+      int64_t gn = N;
+      int4 ent_n = make_int4(0, 0, 0, 0);
+      bool fetched = false;
+      const int b = ent.x & 0xffff, ql = (int)((uint32_t)ent.x >> 16);
+      const int ci = (int)((uint32_t)ent.y >> 16), w = ent.y & 0xffff;
+      bool ent_ok = b < a.B && ql >= 1 && ql <= a.S_max && w < UPB && ent.z >= 0 &&
+                    ent.z <= a.S_kv && ent.w >= 0 && (int64_t)ent.w + ql <= a.q_rows;
+      const UnitInfo r = unit_from(a, b, w, ent.w, ql, ent.z);
+      const int ha = active_groups(a, r.q_len);
+      ent_ok = ent_ok && r.hg < ha && r.ncols > 0;  // an active unit of the batch
+      if (!ent_ok && lane == 0) atomicExch(a.err, 2);
+      const int64_t cost = max(1, r.ntiles);
+      const ChunkGeom gm = chunk_geom(cost, C, c2);
+      int t_begin, t_end;
+      if (ci < gm.n1) {
+        t_begin = (int)(ci * C);
+        t_end = (int)(t_begin + C);
+      } else {
+        t_begin = (int)(gm.n1 * C + (ci - gm.n1) * c2);
+        t_end = (int)min(cost, t_begin + c2);
+      }
+      if (!ent_ok || ci >= gm.nch) t_begin = t_end = 0;  // nothing of a bad entry runs
+      const int i_first = MR ? r.c0 / a.G : 0;
+      const int i_last = MR ? (r.c0 + max(r.ncols, 1) - 1) / a.G : 0;
+      // the chunk's page ids: the window's tiles, then the first tokens'
+      int pg0 = 0, fg0 = 0, npg = 0, nfg = 0, mypage = 0;
+      if (a.block_table && r.ntiles > 0 && t_begin < t_end) {
+        const int we = X ? min(t_end, r.nwin) : t_end;
+        if (t_begin < we) {
+          pg0 = (int)page_index(a, (int64_t)(r.tile0 + t_begin) * kKvTile);
+          npg = (int)page_index(a, min((int64_t)(r.tile0 + we) * kKvTile, (int64_t)r.kv_len) - 1) - pg0 + 1;
+        }
+        if (X && t_end > r.nwin) {
+          fg0 = (int)page_index(a, (int64_t)max(t_begin - r.nwin, 0) * kKvTile);
+          nfg = (int)page_index(a, min((int64_t)(t_end - r.nwin) * kKvTile, (int64_t)r.kv_len) - 1) - fg0 + 1;
+        }
+        if (npg + nfg <= 32 && lane < npg + nfg)
+          mypage = a.block_table[(int64_t)r.b * a.max_blocks +
+                                 (lane < npg ? pg0 + lane : fg0 + lane - npg)];
+      }
+      if (ent_ok && ci < gm.nch) {  // chunk description + the columns' query vectors
+        const int qs = ucount & 1;
+        wait_or_abort(&qempty[qs], ((ucount >> 1) & 1) ^ 1, a.err, misc);
+        if (lane == 0) {
+          UnitMsg& m = msg[qs];
+          m.r = r;
+          m.slot = (int64_t)ci * (a.KVN * ha) + r.hk * ha + r.hg;
+          m.ci = ci;
+          m.nch = gm.nch;
+          m.t_begin = t_begin;
+          m.t_end = t_end;
+          m.done = 0;
+          mbar_arrive_expect_tx(&qfull[qs], (uint32_t)(r.ncols * D * 2));
+        }
+        __syncwarp();
+        for (int i = i_first + lane; i <= i_last; i += 32) {
+          const int cb = max(r.c0, i * a.G), ce = min(r.c0 + r.ncols, (i + 1) * a.G);
+          bulk_load(smem + Cfg::kOffQ + qs * Cfg::kQBytes + (cb - r.c0) * D * 2,
+                    a.q + ((int64_t)r.qrow0 + i) * a.q_stride +
+                        ((int64_t)r.hk * a.G + cb - i * a.G) * D,
+                    (uint32_t)((ce - cb) * D * 2), &qfull[qs]);
+        }
+        ++ucount;
+      }
+      for (int t = t_begin; r.ntiles > 0 && t < t_end; ++t) {
+        const int s = it % S;
+        const int j0 = tile_at<X>(r, t) * kKvTile;
+        const int jb = j0 + rb * a.box_rows;
+        const bool mine = rb < nrb && jb < r.kv_len;
+        int blk = 0, jp = 0;
+        if (a.block_table) {
+          const int pj = mine ? (int)page_index(a, jb) : 0;
+          jp = jb - pj * a.block_size;
+          if (npg + nfg <= 32)
+            blk = pool_page(a, __shfl_sync(0xffffffffu, mypage, !X || t < r.nwin ? pj - pg0 : npg + pj - fg0));
+          else if (mine)
+            blk = pool_page(a, a.block_table[(int64_t)r.b * a.max_blocks + pj]);
+        }
+        if (a.debug && mine && a.block_table && blk == a.num_blocks) atomicExch(a.err, 3);
+        const int prow = mine ? (int)pool_row(a, r.b, r.hk, blk, jb, jp) : 0;
+        // the scales of a piece are contiguous, on 16-byte boundaries in 16-byte units:
+        // pages are multiples of 32 rows, lengths of contiguous caches of 4
+        const float* ssrc = zero_scales;  // (a page outside the pool: zeros)
+        if (mine && (!a.block_table || blk < a.num_blocks))
+          ssrc = (isv ? a.v_scale : a.k_scale) + scale_row_in(a, r.b, r.hk, blk, jb, jp);
+        const int srows = a.block_table ? a.box_rows : min(a.box_rows, a.S_kv - jb);
+        const int nvalid = min(nrb, (r.kv_len - j0 + a.box_rows - 1) / a.box_rows);
+        const uint32_t bytes = 2u * (uint32_t)(nvalid * a.box_rows * Cfg::kRowBytes +
+                                               (a.block_table ? nvalid * a.box_rows
+                                                              : min(a.box_rows, a.S_kv - j0)) * 4);
+        const bool with_mask = MR && a.mask;
+        const int mrow_bytes = with_mask ? min(kKvTile, (r.kv_len - j0 + 15) & ~15) : 0;
+        const int nmrows = with_mask ? i_last - i_first + 1 : 0;
+        wait_or_abort(&empty[s], ((it / S) & 1) ^ 1, a.err, misc);
+        if (*reinterpret_cast<volatile int*>(misc)) {  // issue nothing after a time-out
+          aborted = true;
+          break;
+        }
+        uint8_t* st = smem + s * Cfg::kStageBytes;
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes + (uint32_t)(nmrows * mrow_bytes));
+        __syncwarp();
+        if (with_mask && lane < nmrows)
+          bulk_load(st + Cfg::kOffMask + lane * kKvTile,
+                    a.mask + (int64_t)r.b * a.mask_bstride + (int64_t)(i_first + lane) * a.mask_rstride + j0,
+                    (uint32_t)mrow_bytes, &full[s]);
+        if (mine) {
+          uint8_t* dst = st + isv * Cfg::kTileBytes + rb * a.box_rows * Cfg::kRowBytes;
+          const int col = a.kv_layout == 1 ? 0 : r.hk * Cfg::kRowBytes;
+          if (once) tma_load_2d_hint(dst, isv ? &tv : &tk, &full[s], col, prow, pol);
+          else tma_load_2d(dst, isv ? &tv : &tk, &full[s], col, prow);
+          bulk_load(st + Cfg::kOffScale + isv * Cfg::kScaleBytes + rb * a.box_rows * 4, ssrc,
+                    (uint32_t)(srows * 4), &full[s]);
+        }
+        ++it;
+        if (!fetched) {
+          gn = __shfl_sync(0xffffffffu, (int64_t)gn_l, 0);
+          if (gn < N) ent_n = a.queue[gn];
+          fetched = true;
+        }
+      }
+      if (aborted || *reinterpret_cast<volatile int*>(misc)) {
+        aborted = true;
+        break;
+      }
+      if (!fetched) {
+        gn = __shfl_sync(0xffffffffu, (int64_t)gn_l, 0);
+        if (gn < N) ent_n = a.queue[gn];
+      }
+      g = gn;
+      ent = ent_n;
+    }
+    if (aborted) {
+      // issue nothing more, and give the copies in flight a bounded time to land
+      for (int k = max(0, it - S); k < it; ++k) mbar_wait(&full[k % S], (k / S) & 1, a.err);
+      return;
+    }
+    pdl_trigger();  // this CTA loads nothing more: the combine kernel may launch
+    if (lane == 0 && plan_ok) {  // the last CTA out resets the queue for the next execute
+      __threadfence();
+      if (atomicAdd(a.claim + 1, 1) == a.num_ctas - 1) {
+        a.claim[0] = 0;
+        a.claim[1] = 0;
+      }
+    }
+    const int qs = ucount & 1;  // the end of the CTA's work: an empty message
+    wait_or_abort(&qempty[qs], ((ucount >> 1) & 1) ^ 1, a.err, misc);
+    if (lane == 0) {
+      msg[qs].done = 1;
+      mbar_arrive(&qfull[qs]);
+    }
+    return;
+  }
+
+  // ======================= consumers =======================
+  const int g = lane >> 2, q4 = lane & 3;
+  const int R0 = warp * Cfg::kRows;
+  const uint32_t smem_base = smem_u32(smem);
+  constexpr int KS = D / 16, MT = D / 16;  // k-steps, m-tiles
+  // blocks of 16 rows that a warp takes side by side (with 16 columns one after the other:
+  // 128 registers of accumulators and queries)
+  constexpr int NB = NG == 1 ? 2 : 1, kStep = 16 * NB;
+  // This lane's row in the ldmatrix of groups 0, 1 and of groups 2, 3 of a block of 16
+  // rows: matrices (rows 0-7, even group), (8-15, even), (0-7, odd), (8-15, odd).
+  const uint32_t off01 = sw64(R0 + (lane & 15), lane >> 4), off23 = sw64(R0 + (lane & 15), 2 + (lane >> 4));
+  float* red_ml = reinterpret_cast<float*>(smem + Cfg::kOffRedMl);
+  float4* red4 = reinterpret_cast<float4*>(smem + Cfg::kOffRed);
+
+  int it = 0, ucount = 0;
+  while (true) {
+    const int qs = ucount & 1;
+    wait_or_abort(&qfull[qs], (ucount >> 1) & 1, a.err, misc);
+    // (the warps leave together: the merge meets at a named barrier)
+    if (named_bar_or(1, 32 * W, msg[qs].done || *reinterpret_cast<volatile int*>(misc))) break;
+    const UnitInfo r = msg[qs].r;
+    const int kvl = r.kv_len;
+    const int64_t slot0 = a.sched[kSchedHeader + r.b] + msg[qs].slot;
+    const int t_begin = msg[qs].t_begin, t_end = msg[qs].t_end;
+    const bool split = msg[qs].nch > 1;
+    // keys seen by the columns of this lane's accumulators, and their mask rows
+    int loc[NG][2], hic[NG][2], mrow[NG][2];
+#pragma unroll
+    for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if constexpr (MR) {
+          const int i = (r.c0 + min(ng * 8 + 2 * q4 + e, max(r.ncols, 1) - 1)) / a.G;
+          row_bounds(a, r.q_len, kvl, i, &loc[ng][e], &hic[ng][e]);
+          mrow[ng][e] = (i - r.c0 / a.G) * kKvTile;
+        } else {
+          loc[ng][e] = r.lo;
+          hic[ng][e] = r.hi;
+          mrow[ng][e] = 0;
+        }
+      }
+    // Q^T fragments in fp16, times a power of two that puts the unit's largest element at
+    // exponent 15 (decode_kernel tells why); k-step kk = 2*group + j covers
+    // d = 32*group + 8*q + 4*j + {0..3}
+    uint32_t qb[NG][KS][2];
+    float slc;
+    {
+      const uint16_t* qsm = reinterpret_cast<const uint16_t*>(smem + Cfg::kOffQ + qs * Cfg::kQBytes);
+      uint32_t emax = 0;
+#pragma unroll
+      for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+        for (int kk = 0; kk < KS; ++kk) {
+          uint2 v = make_uint2(0u, 0u);
+          if (ng * 8 + g < r.ncols)
+            v = *reinterpret_cast<const uint2*>(qsm + (ng * 8 + g) * D + (kk >> 1) * 32 + 8 * q4 + 4 * (kk & 1));
+          qb[ng][kk][0] = v.x;
+          qb[ng][kk][1] = v.y;
+          emax = max(emax, max(max((v.x >> 7) & 0xffu, (v.x >> 23) & 0xffu),
+                               max((v.y >> 7) & 0xffu, (v.y >> 23) & 0xffu)));
+        }
+      emax = __reduce_max_sync(0xffffffffu, emax);
+      const int sh = min(max(142 - (int)emax, -100), 100);  // 15 - (emax - 127)
+      const float up = __int_as_float((127 + sh) << 23);
+      slc = a.scale_log2 * __int_as_float((127 - sh) << 23);
+#pragma unroll
+      for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+        for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t v = qb[ng][kk][k];
+            qb[ng][kk][k] = pack_f16(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up);
+          }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qempty[qs]);
+      ++ucount;
+    }
+    float acc[MT][NG][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int ng = 0; ng < NG; ++ng) acc[i][ng][0] = acc[i][ng][1] = acc[i][ng][2] = acc[i][ng][3] = 0.f;
+    float m_r[NG][2], l_r[NG][2];
+#pragma unroll
+    for (int ng = 0; ng < NG; ++ng) {
+      m_r[ng][0] = m_r[ng][1] = -INFINITY;
+      l_r[ng][0] = l_r[ng][1] = 0.f;
+    }
+    int vref = kMxRefMin;  // the code of the V scale reference
+    __nv_bfloat162 vinv = mx_over(kMxRefMin);
+    // Keys that count as zeros in O whatever they hold: past kv_len, and between a band's
+    // first tokens and its window.  (Codes are numbers all: a scale of 0 is enough.)
+    const auto gone = [&](int j) {
+      return j >= kvl || (X && ((j < r.lo && j >= a.first_tokens) || j > r.hi));
+    };
+
+    const int ntile_here = r.ntiles == 0 ? 0 : (t_end - t_begin);
+    for (int tt = 0; tt < ntile_here; ++tt, ++it) {
+      const int s = it % S;
+      wait_or_abort(&full[s], (it / S) & 1, a.err, misc);
+      const int jt = tile_at<X>(r, t_begin + tt) * kKvTile;
+#pragma unroll 1
+      for (int R = R0; R < R0 + Cfg::kRows; R += kStep) {
+      const uint32_t st = smem_base + s * Cfg::kStageBytes + (R - R0) * Cfg::kRowBytes;
+      const uint8_t* stp = smem + s * Cfg::kStageBytes;
+      const int jw = jt + R;  // the step's first KV row
+      const bool edge = (jw < r.lo_last) || (jw + kStep - 1 > r.hi_first) || (MR && a.mask != nullptr);
+      const bool cut = X ? jw < r.lo || jw + kStep - 1 > r.hi : jw + kStep > kvl;
+      if (X && !a.scores && (jw > r.hi || (jw >= a.first_tokens && jw + kStep <= r.lo)))
+        continue;  // no row sees any of them
+      // ---------------- S^T = K Q^T ----------------
+      const uint32_t* ks = reinterpret_cast<const uint32_t*>(stp + Cfg::kOffScale) + R + g;
+      float x[NB][NG][4];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        // the four scales of rows g and g + 8 (NaN: the row's scores are NaN)
+        float fa[4], fb[4];
+        e8m0x4_to_f32x4(ks[16 * b], fa);
+        e8m0x4_to_f32x4(ks[16 * b + 8], fb);
+        // 8 elements of each row and group: d = 32*j + 8*q .. +7
+        uint32_t kw[2][4];
+        ldsm_x4(st + off01 + 1024 * b, kw[0][0], kw[0][1], kw[0][2], kw[0][3]);
+        ldsm_x4(st + off23 + 1024 * b, kw[1][0], kw[1][1], kw[1][2], kw[1][3]);
+#pragma unroll
+        for (int ng = 0; ng < NG; ++ng) x[b][ng][0] = x[b][ng][1] = x[b][ng][2] = x[b][ng][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t ka[2][4];
+          e2m1x8_to_f16x2x4(kw[j >> 1][2 * (j & 1)], ka[0][0], ka[0][2], ka[1][0], ka[1][2]);
+          e2m1x8_to_f16x2x4(kw[j >> 1][2 * (j & 1) + 1], ka[0][1], ka[0][3], ka[1][1], ka[1][3]);
+#pragma unroll
+          for (int ng = 0; ng < NG; ++ng) {
+            float s4[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_f16(s4, ka[0], qb[ng][2 * j][0], qb[ng][2 * j][1]);
+            mma_f16(s4, ka[1], qb[ng][2 * j + 1][0], qb[ng][2 * j + 1][1]);
+            x[b][ng][0] += s4[0] * fa[j];
+            x[b][ng][1] += s4[1] * fa[j];
+            x[b][ng][2] += s4[2] * fb[j];
+            x[b][ng][3] += s4[3] * fb[j];
+          }
+        }
+#pragma unroll
+        for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[b][ng][k] *= slc;
+      }
+      // ---------------- mask ----------------
+      if (edge) {
+        const uint8_t* mk = stp + Cfg::kOffMask + R + g;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int e = k & 1, row = 16 * b + 8 * (k >> 1), j = jw + row + g;
+              bool ok = j >= loc[ng][e];
+              if (X) ok = ok || j < a.first_tokens;
+              ok = ok && j <= hic[ng][e];
+              if (MR && a.mask) ok = ok && mk[mrow[ng][e] + row] == 0;
+              if (!ok) x[b][ng][k] = -INFINITY;
+            }
+      }
+      if (X && a.scores) {  // (decode_kernel: key weights)
+        const int64_t base = ((int64_t)r.b * a.KVN + r.hk) * a.S_kv;
+        const int end = min(kvl, a.S_kv);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+              const int cl = ng * 8 + 2 * q4, j = jw + 16 * b + 4 * k + g;
+              if (cl < r.ncols && j < end)
+                *reinterpret_cast<float2*>(a.scores + (base + j) * a.score_cols + r.c0 + cl) =
+                    make_float2(x[b][ng][k], x[b][ng][k + 1]);
+            }
+      }
+      // ---------------- online softmax per column ----------------
+      // (the reference moves only when a score passes it by more than 8, as in
+      // decode_kernel: P stays below 2^8)
+      float top[NG][2];
+      bool over = false;
+#pragma unroll
+      for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = fmaxf(x[0][ng][e], x[0][ng][2 + e]);
+#pragma unroll
+          for (int b = 1; b < NB; ++b) mx = fmaxf(mx, fmaxf(x[b][ng][e], x[b][ng][2 + e]));
+          top[ng][e] = mx;
+          over |= mx > m_r[ng][e] + 8.f;
+        }
+      float fct[NG][2];  // what O is multiplied by before this tile's P V
+#pragma unroll
+      for (int ng = 0; ng < NG; ++ng) fct[ng][0] = fct[ng][1] = 1.f;
+      bool resc = false;
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = top[ng][e];
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float mold = m_r[ng][e];
+            if (mx > mold + 8.f) {
+              fct[ng][e] = mold == -INFINITY ? 0.f : fast_exp2(mold - mx);
+              m_r[ng][e] = mx;
+              l_r[ng][e] *= fct[ng][e];
+            }
+          }
+        resc = true;
+      }
+#pragma unroll
+      for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float mu = m_r[ng][e] == -INFINITY ? 0.f : m_r[ng][e];
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const float p0 = fast_exp2(x[b][ng][e] - mu), p1 = fast_exp2(x[b][ng][2 + e] - mu);
+            x[b][ng][e] = p0;
+            x[b][ng][2 + e] = p1;
+            l_r[ng][e] += p0 + p1;
+          }
+        }
+      // ---------------- O^T += V^T P^T ----------------
+      // P times a V scale is held in fp16 over 2^(vref - 127 - 6): vref is the largest
+      // scale code that the warp's tiles had so far, so the products stay below 2^14, and
+      // a key of P = 1 keeps fp16's bits down to scales 2^20 below the largest.  A new
+      // vref moves O by an exact power of two.
+      const uint32_t* vs = ks + kKvTile;
+      __nv_bfloat162 v[NB][2][2];
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w = vs[16 * b + 8 * h];
+          if (cut && gone(jw + 16 * b + 8 * h + g)) w = 0u;
+          e8m0x4_to_bf16x2x2(w, v[b][h]);
+        }
+      // (the larger of two drops a NaN)
+      __nv_bfloat162 mx2 = __hmax2(__hmax2(v[0][0][0], v[0][0][1]), __hmax2(v[0][1][0], v[0][1][1]));
+#pragma unroll
+      for (int b = 1; b < NB; ++b)
+        mx2 = __hmax2(mx2, __hmax2(__hmax2(v[b][0][0], v[b][0][1]), __hmax2(v[b][1][0], v[b][1][1])));
+      const uint32_t mxb = *reinterpret_cast<const uint32_t*>(&mx2);
+      if (__any_sync(0xffffffffu, (int)(max(mxb >> 16, mxb & 0xffffu) >> 7) > vref)) {
+        // (positive: their bits order as they do; NaN alone is no reference)
+        const uint32_t hi = mxb >> 16, lo = mxb & 0xffffu;
+        const uint32_t best = max(hi >= 0x7f80u ? 0u : hi, lo >= 0x7f80u ? 0u : lo);
+        const int en = max(vref, (int)(__reduce_max_sync(0xffffffffu, best) >> 7));
+        // (a jump past 2^-126 leaves a negligible old sum and gives 0)
+        const float ratio = __int_as_float(max(127 + vref - en, 0) << 23);
+        vref = en;
+        vinv = mx_over(en);
+#pragma unroll
+        for (int ng = 0; ng < NG; ++ng) {
+          fct[ng][0] *= ratio;
+          fct[ng][1] *= ratio;
+        }
+        resc = true;
+      }
+      if (resc) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int ng = 0; ng < NG; ++ng) {
+            acc[i][ng][0] *= fct[ng][0];
+            acc[i][ng][1] *= fct[ng][1];
+            acc[i][ng][2] *= fct[ng][0];
+            acc[i][ng][3] *= fct[ng][1];
+          }
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        float fa[4], fb[4];
+        bf16x2x2_to_f32x4(__hmul2(v[b][0][0], vinv), __hmul2(v[b][0][1], vinv), fa);
+        bf16x2x2_to_f32x4(__hmul2(v[b][1][0], vinv), __hmul2(v[b][1][1], vinv), fb);
+        // A lane takes four elements d = 32*j + 4*g .. +3 of each group j (a 16-bit unit) of
+        // its keys 2q, 2q+1, 2q+8, 2q+9; m-tile 2j + h holds the elements 2h of them in its
+        // fragment rows 0-7, 2h + 1 in rows 8-15, so that an m-tile lies in one group.
+        const uint32_t vt = st + Cfg::kTileBytes + 1024 * b;
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) {  // groups 2*jj, 2*jj + 1
+          uint32_t w[4];  // (group 2*jj: keys 2q, 2q+1), (keys 2q+8, 2q+9), (group 2*jj + 1: ...)
+          ldsm_x4_t(vt + (jj ? off23 : off01), w[0], w[1], w[2], w[3]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int j = 2 * jj + k;
+            const uint32_t lo = __byte_perm(w[2 * k], w[2 * k + 1], 0x5410);  // keys 2q, 2q+8
+            const uint32_t hi = __byte_perm(w[2 * k], w[2 * k + 1], 0x7632);  // keys 2q+1, 2q+9
+            // bytes of two keys' codes of one element: 0, 2 (keys 2q, 2q+1), 0, 2 (2q+8, 2q+9)
+            const uint32_t ev = (lo & 0x0f0f0f0fu) | ((hi << 4) & 0xf0f0f0f0u);
+            const uint32_t od = ((lo >> 4) & 0x0f0f0f0fu) | (hi & 0xf0f0f0f0u);  // and 1, 3
+            uint32_t va[2][4];  // [m-tile of the two][fragment register]
+            e2m1x8_to_f16x2x4(ev, va[0][0], va[1][0], va[0][2], va[1][2]);
+            e2m1x8_to_f16x2x4(od, va[0][1], va[1][1], va[0][3], va[1][3]);
+#pragma unroll
+            for (int ng = 0; ng < NG; ++ng) {
+              const uint32_t b0 = movmatrix_t(pack_f16(x[b][ng][0] * fa[j], x[b][ng][1] * fa[j]));
+              const uint32_t b1 = movmatrix_t(pack_f16(x[b][ng][2] * fb[j], x[b][ng][3] * fb[j]));
+              mma_f16(acc[2 * j][ng], va[0], b0, b1);
+              mma_f16(acc[2 * j + 1][ng], va[1], b0, b1);
+            }
+          }
+        }
+      }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+    }
+
+    // ---------------- merge the warps' states ----------------
+#pragma unroll
+    for (int ng = 0; ng < NG; ++ng) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float l = l_r[ng][e];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        l_r[ng][e] = l;
+      }
+      if (g == 0)
+        *reinterpret_cast<float4*>(red_ml + (warp * 8 * NG + ng * 8 + 2 * q4) * 2) =
+            make_float4(m_r[ng][0], l_r[ng][0], m_r[ng][1], l_r[ng][1]);
+    }
+    named_bar_sync(1, 32 * W);
+    float Mh[NG][2], Lh[NG][2];
+    const float back = __int_as_float((vref - 6) << 23);  // 2^(vref - 127 - 6)
+#pragma unroll
+    for (int ng = 0; ng < NG; ++ng) {
+      float4 ml[W];  // (m, l) of this lane's two columns
+      float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f};
+#pragma unroll
+      for (int w2 = 0; w2 < W; ++w2) {
+        ml[w2] = *reinterpret_cast<const float4*>(red_ml + (w2 * 8 * NG + ng * 8 + 2 * q4) * 2);
+        M[0] = fmaxf(M[0], ml[w2].x);
+        M[1] = fmaxf(M[1], ml[w2].z);
+      }
+#pragma unroll
+      for (int w2 = 0; w2 < W; ++w2) {
+        L[0] += ml[w2].x == -INFINITY ? 0.f : ml[w2].y * exp2f(ml[w2].x - M[0]);
+        L[1] += ml[w2].z == -INFINITY ? 0.f : ml[w2].w * exp2f(ml[w2].z - M[1]);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        Mh[ng][e] = M[e];
+        Lh[ng][e] = L[e];
+        const float f = m_r[ng][e] == -INFINITY ? 0.f : back * exp2f(m_r[ng][e] - M[e]);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          acc[i][ng][e] *= f;
+          acc[i][ng][2 + e] *= f;
+        }
+      }
+    }
+    // Warp w ends with m-tiles 2w and 2w + 1 (the elements of group w) summed over the
+    // warps: in each of two rounds every warp stores the four m-tiles 2k + round but its
+    // own, then adds the others' copies to its own.
+    const int64_t slot = min(max(slot0, (int64_t)0), a.max_chunks - 1);
+    const int64_t pstride = (int64_t)a.GH * (D + 2);
+#pragma unroll
+    for (int ng = 0; ng < NG; ++ng) {
+      float4 own[2];  // (d, column 2q), (d, 2q+1), (d+1, 2q), (d+1, 2q+1), d = 32 warp + 4 g + 2 rnd
+#pragma unroll
+      for (int rnd = 0; rnd < 2; ++rnd) {
+        if (ng > 0 || rnd > 0) named_bar_sync(1, 32 * W);  // the round before has been read
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float (&c)[4] = acc[2 * k + rnd][ng];
+          const float4 mine = make_float4(c[0], c[1], c[2], c[3]);
+          if (k == warp) own[rnd] = mine;
+          else red4[(k * W + warp) * 32 + lane] = mine;
+        }
+        named_bar_sync(1, 32 * W);
+#pragma unroll
+        for (int w2 = 0; w2 < W; ++w2) {
+          if (w2 == warp) continue;
+          const float4 o = red4[(warp * W + w2) * 32 + lane];
+          own[rnd].x += o.x; own[rnd].y += o.y; own[rnd].z += o.z; own[rnd].w += o.w;
+        }
+      }
+      const int d = 32 * warp + 4 * g;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int hh = ng * 8 + 2 * q4 + e;  // the unit's column
+        if (hh >= r.ncols) continue;
+        const float4 o = e ? make_float4(own[0].y, own[0].w, own[1].y, own[1].w)
+                           : make_float4(own[0].x, own[0].z, own[1].x, own[1].z);
+        if (!split) {
+          const int c = r.c0 + hh;
+          const int i = c / a.G, h = r.hk * a.G + (c - i * a.G);
+          const int64_t tok = (int64_t)r.qrow0 + i;
+          float scl, lse;
+          finish_head(a, h, Mh[ng][e], Lh[ng][e], &scl, &lse);
+          *reinterpret_cast<uint2*>(a.out + tok * a.out_stride + (int64_t)h * D + d) =
+              make_uint2(pack_bf16(o.x * scl, o.y * scl), pack_bf16(o.z * scl, o.w * scl));
+          if (a.lse && warp == 0 && g == 0)
+            a.lse[a.layout == 1 ? tok * a.QN + h : ((int64_t)r.b * a.QN + h) * a.S_q + i] = lse;
+        } else {
+          // (the slot is clamped, as in decode_kernel; rows of D + 2 floats: 8-byte stores)
+          float* col = a.partials + slot * pstride + (int64_t)hh * (D + 2);
+          *reinterpret_cast<float2*>(col + d) = make_float2(o.x, o.y);
+          *reinterpret_cast<float2*>(col + d + 2) = make_float2(o.z, o.w);
+          if (warp == 0 && g == 0)
+            *reinterpret_cast<float2*>(col + D) = make_float2(Mh[ng][e], Lh[ng][e]);
+        }
+      }
+    }
+  }
+}
+
+template <int NG, bool MR, bool X>
+cudaError_t launch_mx_t(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  using Cfg = MxCfg<NG, MR>;
+  auto kern = decode_mx_kernel<NG, MR, X>;
+  static std::atomic<uint64_t> done_mask[4];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(done_mask[(dev >> 6) & 3].load() & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+    if (e != cudaSuccess) return e;
+    done_mask[(dev >> 6) & 3].fetch_or(bit);
+  }
+  return launch_pdl(kern, dim3(a.num_ctas), dim3(Cfg::kThreads), Cfg::kSmem, s, a, tk, tv);
+}
+
+template <int NG>
+cudaError_t launch_mx_ng(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  const bool mr = a.S_max > 1 || a.mask != nullptr;
+  if (a.first_tokens > 0 || a.scores)
+    return mr ? launch_mx_t<NG, true, true>(a, tk, tv, s) : launch_mx_t<NG, false, true>(a, tk, tv, s);
+  return mr ? launch_mx_t<NG, true, false>(a, tk, tv, s) : launch_mx_t<NG, false, false>(a, tk, tv, s);
+}
+
+}  // namespace
+
+int decode_mx_ctas(int GH) { return GH > 8 ? MxCfg<2, false>::kCtas : MxCfg<1, false>::kCtas; }
+
+static cudaError_t launch_decode_mx(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                                    cudaStream_t s) {
+  return a.GH > 8 ? launch_mx_ng<2>(a, tk, tv, s) : launch_mx_ng<1>(a, tk, tv, s);
+}
+
+}  // namespace fia

@@ -201,7 +201,7 @@ bool copied(const fia_params* p) { return p->kv_dtype != FIA_KV_BF16; }
 
 
 struct DecodePlan {
-  int n;
+  int n, W;  // CTAs; chunks to a CTA that the chunk size aims at
   int64_t U, max_chunks;
   int64_t off_sched, off_queue, off_part, total;
 };
@@ -224,7 +224,14 @@ int debug_checks() {
 // heads per KV head 120.3 -> 113.6 us, 4-row decode 88.2 -> 79.9 us against
 // k = 6, 6 and 3; one-row bf16 decode 58.9 -> 58.6 us against k = 3).
 int decode_small_div(const fia_params* p) {
+  if (const char* e = getenv("MXD")) return p->kv_dtype == FIA_KV_MXFP4 ? atoi(e) : 1;
   return (p->kv_dtype != FIA_KV_BF16 || p->max_seqlen_q > 1) ? 1 : 2;
+}
+
+int decode_chunks_per_cta(const fia_params* p) {
+  if (p->kv_dtype != FIA_KV_MXFP4) return kDecodeChunksPerCta;
+  const char* e = getenv("MXW");
+  return e ? atoi(e) : 2;
 }
 
 // Decode workspace: [0, 256) error word (offset 0) and the claim counters
@@ -240,9 +247,11 @@ fia_status decode_plan(const fia_params* p, DecodePlan* pl) {
   const int cols = p->max_seqlen_q * G;  // (query row, head) columns of a KV head
   const int GH = decode_group_heads(p->max_seqlen_q, cols);
   const int HG = (int)ceil_div(cols, GH);
+  if (p->kv_dtype == FIA_KV_MXFP4) n *= decode_mx_ctas(GH);  // (several CTAs to an SM)
   pl->n = n;
   pl->U = (int64_t)p->batch * p->num_kv_heads * HG;
-  pl->max_chunks = (int64_t)n * kDecodeChunksPerCta + 2 * decode_small_div(p) * pl->U;
+  pl->W = decode_chunks_per_cta(p);
+  pl->max_chunks = (int64_t)n * pl->W + 2 * decode_small_div(p) * pl->U;
   // queue positions and slots are 32-bit in the kernels
   if (pl->max_chunks >= INT32_MAX) return FIA_ERR_BAD_SHAPE;
   int64_t off = kAlign;
@@ -300,7 +309,7 @@ DecodeArgs decode_args(const fia_params* p, const DecodePlan& pl, void* ws) {
   a.sinks = p->sinks;
   a.num_ctas = pl.n;
   a.num_units = pl.U;
-  a.chunks_per_cta = kDecodeChunksPerCta;
+  a.chunks_per_cta = pl.W;
   a.small_div = decode_small_div(p);
   a.max_chunks = pl.max_chunks;
   char* w = static_cast<char*>(ws);

@@ -204,6 +204,8 @@ cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& tk, const CUte
 // `planned` if it has to find a plan in the workspace, else the plan's launch goes
 // before it and need not be done.
 bool decode_is_few(const DecodeArgs& a, bool weights);
+// CTAs of the MXFP4 decode kernel to an SM, for units of up to GH columns.
+int decode_mx_ctas(int GH);
 cudaError_t launch_decode_few(const DecodeArgs& a, const fia_kv_cache& cache, const KeyWeightsOut* w,
                               bool planned, cudaStream_t s);
 size_t decode_smem_bytes(int D, int fp8);
