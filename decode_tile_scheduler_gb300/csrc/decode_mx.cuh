@@ -13,8 +13,9 @@
 //    one 16-bit unit, so a lane gets two keys' units in a register; masks and shifts
 //    pair the keys' codes in bytes, and cvt makes an fp16 pair of a byte.
 //  - E2M1 codes are fp16 values as they are.  K scales multiply the partial scores of
-//    their 32 elements in fp32; V scales multiply P in fp32, before it is rounded to
-//    fp16 for the products (a P^T for each of the four groups of 32 elements).
+//    their 32 elements in fp32; V scales multiply P, already in fp16 and transposed, as
+//    fp16 pairs (a P^T for each of the four groups of 32 elements).  A lane makes both
+//    from the bytes of one row, through shared memory, for the four lanes that use them.
 //
 // Measured issue costs (clocks per warp instruction and scheduler): cvt of a byte, prmt,
 // lop3 2, movmatrix and ex2 4.
@@ -33,12 +34,16 @@ struct MxCfg {
   static constexpr int kScaleBytes = kKvTile * 4;
   static constexpr int kOffScale = 2 * kTileBytes, kOffMask = kOffScale + 2 * kScaleBytes;
   static constexpr int kStageBytes = kOffMask + (MR ? kDecodeMaxRows * kKvTile : 0);
-  static constexpr int kStages = NG == 1 ? 3 : 5;
+  static constexpr int kStages = NG == 1 ? 3 : 4;
   static constexpr int kQBytes = 8 * NG * D * 2;
   static constexpr int kOffQ = kStages * kStageBytes;
   static constexpr int kOffRed = kOffQ + 2 * kQBytes;         // [4][warps][32] float4
   static constexpr int kOffRedMl = kOffRed + 4 * kWarps * 32 * 16;
-  static constexpr int kOffBar = kOffRedMl + kWarps * 8 * NG * 8;
+  // a tile's scales as the products take them: K's of a row as four floats, V's of two
+  // rows as four fp16 pairs
+  static constexpr int kOffKs = kOffRedMl + kWarps * 8 * NG * 8;
+  static constexpr int kOffVs = kOffKs + kKvTile * 16;
+  static constexpr int kOffBar = kOffVs + kKvTile / 2 * 16;
   static constexpr int kOffMsg = kOffBar + 8 * (2 * kStages + 4);
   static constexpr int kOffMisc = kOffMsg + 2 * 128;
   static constexpr int kSmem = kOffMisc + 16 + 1024;          // + alignment slack
@@ -68,16 +73,20 @@ __device__ __forceinline__ void bf16x2x2_to_f32x4(__nv_bfloat162 a, __nv_bfloat1
   f[2] = __uint_as_float(y << 16);
   f[3] = __uint_as_float(y & 0xffff0000u);
 }
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  const __half2 c = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&c);
+}
 __device__ __forceinline__ void e8m0x4_to_f32x4(uint32_t w, float (&f)[4]) {
   __nv_bfloat162 v[2];
   e8m0x4_to_bf16x2x2(w, v);
   bf16x2x2_to_f32x4(v[0], v[1], f);
 }
-// 2^(6 - (code - 127)) twice, for kMxRefMin <= code <= 254: a V scale times it is at
-// most 2^6.
-constexpr int kMxRefMin = 27;
-__device__ __forceinline__ __nv_bfloat162 mx_over(int code) {
-  const uint32_t h = (uint32_t)(127 + 6 + 127 - code) << 7, w = h | h << 16;
+// The V scale references: codes from kMxRefMin to kMxRefMax, as bf16 values, and what a
+// scale is multiplied by.
+constexpr int kMxRefMin = 27, kMxRefMax = 253;
+__device__ __forceinline__ __nv_bfloat162 mx_pair(uint32_t lo, uint32_t hi) {
+  const uint32_t w = lo | hi << 16;
   return *reinterpret_cast<const __nv_bfloat162*>(&w);
 }
 
@@ -379,14 +388,27 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int ng = 0; ng < NG; ++ng) acc[i][ng][0] = acc[i][ng][1] = acc[i][ng][2] = acc[i][ng][3] = 0.f;
-    float m_r[NG][2], l_r[NG][2];
+    // Softmax references m_r (-inf: none yet; mu is 0 then), lazy: a score may pass its
+    // column's by kOver.  They are kept kLift below the scores that set them, so that P,
+    // at most 2^kOver, has fp16's bits down to 2^-(14 + kLift) of the largest.
+    constexpr float kLift = 5.f, kOver = 13.f;
+    float m_r[NG][2], mu[NG][2], l_r[NG][2];
 #pragma unroll
-    for (int ng = 0; ng < NG; ++ng) {
-      m_r[ng][0] = m_r[ng][1] = -INFINITY;
-      l_r[ng][0] = l_r[ng][1] = 0.f;
+    for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m_r[ng][e] = -INFINITY;
+        mu[ng][e] = l_r[ng][e] = 0.f;
+      }
+    // V scale references, one for each group of 32 elements (0, 1 and 2, 3): the largest
+    // scale that the warp's tiles had so far.  V scales over them, at most 1, multiply P
+    // in fp16 (exact powers of two, down to 2^-24); O is kept over them.
+    __nv_bfloat162 vref[2], vinv[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      vref[k] = mx_pair(kMxRefMin << 7, kMxRefMin << 7);
+      vinv[k] = mx_pair((254 - kMxRefMin) << 7, (254 - kMxRefMin) << 7);
     }
-    int vref = kMxRefMin;  // the code of the V scale reference
-    __nv_bfloat162 vinv = mx_over(kMxRefMin);
     // Keys that count as zeros in O whatever they hold: past kv_len, and between a band's
     // first tokens and its window.  (Codes are numbers all: a scale of 0 is enough.)
     const auto gone = [&](int j) {
@@ -398,24 +420,68 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
       const int s = it % S;
       wait_or_abort(&full[s], (it / S) & 1, a.err, misc);
       const int jt = tile_at<X>(r, t_begin + tt) * kKvTile;
+      // ---------------- scales: a lane takes those of one row ----------------
+      float vfct[4] = {1.f, 1.f, 1.f, 1.f};  // what O's groups are multiplied by before this tile
+      bool vmove = false;
+      {
+        const uint32_t* sc = reinterpret_cast<const uint32_t*>(smem + s * Cfg::kStageBytes + Cfg::kOffScale) +
+                             R0 + lane;
+        uint32_t vw = sc[kKvTile];
+        float kf[4];  // (NaN: the row's scores are NaN)
+        e8m0x4_to_f32x4(sc[0], kf);
+        *reinterpret_cast<float4*>(smem + Cfg::kOffKs + (R0 + lane) * 16) = make_float4(kf[0], kf[1], kf[2], kf[3]);
+        if (jt + R0 + lane >= kvl || X) vw = gone(jt + R0 + lane) ? 0u : vw;
+        __nv_bfloat162 v[2];
+        e8m0x4_to_bf16x2x2(vw, v);
+        // (a NaN is larger than nothing)
+        const bool past = __any_sync(0xffffffffu, __hgt(v[0].x, vref[0].x) | __hgt(v[0].y, vref[0].y) |
+                                                      __hgt(v[1].x, vref[1].x) | __hgt(v[1].y, vref[1].y));
+        if (past) {
+          // new references: O moves by exact powers of two
+          vmove = true;
+          const uint32_t u[2] = {*reinterpret_cast<const uint32_t*>(&v[0]), *reinterpret_cast<const uint32_t*>(&v[1])};
+          const uint32_t o[2] = {*reinterpret_cast<const uint32_t*>(&vref[0]), *reinterpret_cast<const uint32_t*>(&vref[1])};
+          uint32_t en[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t c = (u[j >> 1] >> (16 * (j & 1)) & 0xffffu) >> 7;
+            const uint32_t old = (o[j >> 1] >> (16 * (j & 1)) & 0xffffu) >> 7;
+            en[j] = max(old, min(__reduce_max_sync(0xffffffffu, c == 255u ? 0u : c), (uint32_t)kMxRefMax));
+            // (a jump past 2^-126 leaves a negligible old sum and gives 0)
+            vfct[j] = __int_as_float(max(127 + (int)old - (int)en[j], 0) << 23);
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            vref[k] = mx_pair(en[2 * k] << 7, en[2 * k + 1] << 7);
+            vinv[k] = mx_pair((254 - en[2 * k]) << 7, (254 - en[2 * k + 1]) << 7);
+          }
+        }
+        float vf[4];
+        bf16x2x2_to_f32x4(__hmul2(v[0], vinv[0]), __hmul2(v[1], vinv[1]), vf);
+        // the other row of the pair: even lanes make groups 0 and 1, odd lanes 2 and 3
+        const uint32_t h01 = pack_f16(vf[0], vf[1]), h23 = pack_f16(vf[2], vf[3]);
+        const uint32_t theirs = __shfl_xor_sync(0xffffffffu, lane & 1 ? h01 : h23, 1);
+        const uint32_t even = lane & 1 ? theirs : h01, odd = lane & 1 ? h23 : theirs;
+        *reinterpret_cast<uint2*>(smem + Cfg::kOffVs + (R0 + lane) * 8) =
+            make_uint2(__byte_perm(even, odd, 0x5410), __byte_perm(even, odd, 0x7632));
+        __syncwarp();
+      }
 #pragma unroll 1
       for (int R = R0; R < R0 + Cfg::kRows; R += kStep) {
       const uint32_t st = smem_base + s * Cfg::kStageBytes + (R - R0) * Cfg::kRowBytes;
       const uint8_t* stp = smem + s * Cfg::kStageBytes;
       const int jw = jt + R;  // the step's first KV row
       const bool edge = (jw < r.lo_last) || (jw + kStep - 1 > r.hi_first) || (MR && a.mask != nullptr);
-      const bool cut = X ? jw < r.lo || jw + kStep - 1 > r.hi : jw + kStep > kvl;
       if (X && !a.scores && (jw > r.hi || (jw >= a.first_tokens && jw + kStep <= r.lo)))
         continue;  // no row sees any of them
       // ---------------- S^T = K Q^T ----------------
-      const uint32_t* ks = reinterpret_cast<const uint32_t*>(stp + Cfg::kOffScale) + R + g;
+      const float4* ks = reinterpret_cast<const float4*>(smem + Cfg::kOffKs) + R + g;
       float x[NB][NG][4];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        // the four scales of rows g and g + 8 (NaN: the row's scores are NaN)
-        float fa[4], fb[4];
-        e8m0x4_to_f32x4(ks[16 * b], fa);
-        e8m0x4_to_f32x4(ks[16 * b + 8], fb);
+        // the four scales of rows g and g + 8
+        const float4 f0 = ks[16 * b], f1 = ks[16 * b + 8];
+        const float fa[4] = {f0.x, f0.y, f0.z, f0.w}, fb[4] = {f1.x, f1.y, f1.z, f1.w};
         // 8 elements of each row and group: d = 32*j + 8*q .. +7
         uint32_t kw[2][4];
         ldsm_x4(st + off01 + 1024 * b, kw[0][0], kw[0][1], kw[0][2], kw[0][3]);
@@ -476,8 +542,6 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
             }
       }
       // ---------------- online softmax per column ----------------
-      // (the reference moves only when a score passes it by more than 8, as in
-      // decode_kernel: P stays below 2^8)
       float top[NG][2];
       bool over = false;
 #pragma unroll
@@ -488,13 +552,10 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
 #pragma unroll
           for (int b = 1; b < NB; ++b) mx = fmaxf(mx, fmaxf(x[b][ng][e], x[b][ng][2 + e]));
           top[ng][e] = mx;
-          over |= mx > m_r[ng][e] + 8.f;
+          over |= mx > m_r[ng][e] + kOver;
         }
-      float fct[NG][2];  // what O is multiplied by before this tile's P V
-#pragma unroll
-      for (int ng = 0; ng < NG; ++ng) fct[ng][0] = fct[ng][1] = 1.f;
-      bool resc = false;
-      if (__any_sync(0xffffffffu, over)) {
+      if (__any_sync(0xffffffffu, over) || vmove) {
+        float fct[NG][2];
 #pragma unroll
         for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
@@ -504,80 +565,47 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
             const float mold = m_r[ng][e];
-            if (mx > mold + 8.f) {
-              fct[ng][e] = mold == -INFINITY ? 0.f : fast_exp2(mold - mx);
-              m_r[ng][e] = mx;
+            fct[ng][e] = 1.f;
+            if (mx > mold + kOver) {
+              m_r[ng][e] = mu[ng][e] = mx - kLift;
+              fct[ng][e] = mold == -INFINITY ? 0.f : fast_exp2(mold - mu[ng][e]);
               l_r[ng][e] *= fct[ng][e];
             }
           }
-        resc = true;
-      }
-#pragma unroll
-      for (int ng = 0; ng < NG; ++ng)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float mu = m_r[ng][e] == -INFINITY ? 0.f : m_r[ng][e];
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const float p0 = fast_exp2(x[b][ng][e] - mu), p1 = fast_exp2(x[b][ng][2 + e] - mu);
-            x[b][ng][e] = p0;
-            x[b][ng][2 + e] = p1;
-            l_r[ng][e] += p0 + p1;
-          }
-        }
-      // ---------------- O^T += V^T P^T ----------------
-      // P times a V scale is held in fp16 over 2^(vref - 127 - 6): vref is the largest
-      // scale code that the warp's tiles had so far, so the products stay below 2^14, and
-      // a key of P = 1 keeps fp16's bits down to scales 2^20 below the largest.  A new
-      // vref moves O by an exact power of two.
-      const uint32_t* vs = ks + kKvTile;
-      __nv_bfloat162 v[NB][2][2];
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w = vs[16 * b + 8 * h];
-          if (cut && gone(jw + 16 * b + 8 * h + g)) w = 0u;
-          e8m0x4_to_bf16x2x2(w, v[b][h]);
-        }
-      // (the larger of two drops a NaN)
-      __nv_bfloat162 mx2 = __hmax2(__hmax2(v[0][0][0], v[0][0][1]), __hmax2(v[0][1][0], v[0][1][1]));
-#pragma unroll
-      for (int b = 1; b < NB; ++b)
-        mx2 = __hmax2(mx2, __hmax2(__hmax2(v[b][0][0], v[b][0][1]), __hmax2(v[b][1][0], v[b][1][1])));
-      const uint32_t mxb = *reinterpret_cast<const uint32_t*>(&mx2);
-      if (__any_sync(0xffffffffu, (int)(max(mxb >> 16, mxb & 0xffffu) >> 7) > vref)) {
-        // (positive: their bits order as they do; NaN alone is no reference)
-        const uint32_t hi = mxb >> 16, lo = mxb & 0xffffu;
-        const uint32_t best = max(hi >= 0x7f80u ? 0u : hi, lo >= 0x7f80u ? 0u : lo);
-        const int en = max(vref, (int)(__reduce_max_sync(0xffffffffu, best) >> 7));
-        // (a jump past 2^-126 leaves a negligible old sum and gives 0)
-        const float ratio = __int_as_float(max(127 + vref - en, 0) << 23);
-        vref = en;
-        vinv = mx_over(en);
-#pragma unroll
-        for (int ng = 0; ng < NG; ++ng) {
-          fct[ng][0] *= ratio;
-          fct[ng][1] *= ratio;
-        }
-        resc = true;
-      }
-      if (resc) {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int ng = 0; ng < NG; ++ng) {
-            acc[i][ng][0] *= fct[ng][0];
-            acc[i][ng][1] *= fct[ng][1];
-            acc[i][ng][2] *= fct[ng][0];
-            acc[i][ng][3] *= fct[ng][1];
+            acc[i][ng][0] *= fct[ng][0] * vfct[i >> 1];
+            acc[i][ng][1] *= fct[ng][1] * vfct[i >> 1];
+            acc[i][ng][2] *= fct[ng][0] * vfct[i >> 1];
+            acc[i][ng][3] *= fct[ng][1] * vfct[i >> 1];
           }
+        vmove = false;  // (once a tile)
+        vfct[0] = vfct[1] = vfct[2] = vfct[3] = 1.f;
       }
+      // P^T in fp16, transposed: keys 2q, 2q+1 and 2q+8, 2q+9 of column g
+      uint32_t pt[NB][NG][2];
+#pragma unroll
+      for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          float pr[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            pr[k] = fast_exp2(x[b][ng][k] - mu[ng][k & 1]);
+            l_r[ng][k & 1] += pr[k];
+          }
+          pt[b][ng][0] = movmatrix_t(pack_f16(pr[0], pr[1]));
+          pt[b][ng][1] = movmatrix_t(pack_f16(pr[2], pr[3]));
+        }
+      // ---------------- O^T += V^T P^T ----------------
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        float fa[4], fb[4];
-        bf16x2x2_to_f32x4(__hmul2(v[b][0][0], vinv), __hmul2(v[b][0][1], vinv), fa);
-        bf16x2x2_to_f32x4(__hmul2(v[b][1][0], vinv), __hmul2(v[b][1][1], vinv), fb);
+        // the V scales of those keys, a pair for each group
+        const uint4* vp = reinterpret_cast<const uint4*>(smem + Cfg::kOffVs) + R / 2 + 8 * b + q4;
+        const uint4 s0 = vp[0], s1 = vp[4];
+        const uint32_t va0[4] = {s0.x, s0.y, s0.z, s0.w}, va1[4] = {s1.x, s1.y, s1.z, s1.w};
         // A lane takes four elements d = 32*j + 4*g .. +3 of each group j (a 16-bit unit) of
         // its keys 2q, 2q+1, 2q+8, 2q+9; m-tile 2j + h holds the elements 2h of them in its
         // fragment rows 0-7, 2h + 1 in rows 8-15, so that an m-tile lies in one group.
@@ -599,8 +627,7 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
             e2m1x8_to_f16x2x4(od, va[0][1], va[1][1], va[0][3], va[1][3]);
 #pragma unroll
             for (int ng = 0; ng < NG; ++ng) {
-              const uint32_t b0 = movmatrix_t(pack_f16(x[b][ng][0] * fa[j], x[b][ng][1] * fa[j]));
-              const uint32_t b1 = movmatrix_t(pack_f16(x[b][ng][2] * fb[j], x[b][ng][3] * fb[j]));
+              const uint32_t b0 = mul_f16x2(pt[b][ng][0], va0[j]), b1 = mul_f16x2(pt[b][ng][1], va1[j]);
               mma_f16(acc[2 * j][ng], va[0], b0, b1);
               mma_f16(acc[2 * j + 1][ng], va[1], b0, b1);
             }
@@ -629,7 +656,8 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
     }
     named_bar_sync(1, 32 * W);
     float Mh[NG][2], Lh[NG][2];
-    const float back = __int_as_float((vref - 6) << 23);  // 2^(vref - 127 - 6)
+    float back[4];
+    bf16x2x2_to_f32x4(vref[0], vref[1], back);
 #pragma unroll
     for (int ng = 0; ng < NG; ++ng) {
       float4 ml[W];  // (m, l) of this lane's two columns
@@ -649,11 +677,11 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
       for (int e = 0; e < 2; ++e) {
         Mh[ng][e] = M[e];
         Lh[ng][e] = L[e];
-        const float f = m_r[ng][e] == -INFINITY ? 0.f : back * exp2f(m_r[ng][e] - M[e]);
+        const float f = m_r[ng][e] == -INFINITY ? 0.f : exp2f(m_r[ng][e] - M[e]);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-          acc[i][ng][e] *= f;
-          acc[i][ng][2 + e] *= f;
+          acc[i][ng][e] *= f * back[i >> 1];
+          acc[i][ng][2 + e] *= f * back[i >> 1];
         }
       }
     }

@@ -224,14 +224,14 @@ int debug_checks() {
 // heads per KV head 120.3 -> 113.6 us, 4-row decode 88.2 -> 79.9 us against
 // k = 6, 6 and 3; one-row bf16 decode 58.9 -> 58.6 us against k = 3).
 int decode_small_div(const fia_params* p) {
-  if (const char* e = getenv("MXD")) return p->kv_dtype == FIA_KV_MXFP4 ? atoi(e) : 1;
   return (p->kv_dtype != FIA_KV_BF16 || p->max_seqlen_q > 1) ? 1 : 2;
 }
 
+// Chunks to a CTA that the chunk size aims at.  MXFP4: two, of CTAs three to an SM
+// (attend 32 x 512-4096 keys 36.9 us; one 48.7, three 38.9, four 41.6; 4 of 32 to 128 k
+// keys 101, 141, 102, 105).
 int decode_chunks_per_cta(const fia_params* p) {
-  if (p->kv_dtype != FIA_KV_MXFP4) return kDecodeChunksPerCta;
-  const char* e = getenv("MXW");
-  return e ? atoi(e) : 2;
+  return p->kv_dtype == FIA_KV_MXFP4 ? 2 : kDecodeChunksPerCta;
 }
 
 // Decode workspace: [0, 256) error word (offset 0) and the claim counters
