@@ -34,20 +34,21 @@ struct MxCfg {
   static constexpr int kScaleBytes = kKvTile * 4;
   static constexpr int kOffScale = 2 * kTileBytes, kOffMask = kOffScale + 2 * kScaleBytes;
   static constexpr int kStageBytes = kOffMask + (MR ? kDecodeMaxRows * kKvTile : 0);
-  static constexpr int kStages = NG == 1 ? 3 : 4;
+  static constexpr int kStages = NG == 1 ? (MR ? 3 : 4) : (MR ? 4 : 5);
   static constexpr int kQBytes = 8 * NG * D * 2;
   static constexpr int kOffQ = kStages * kStageBytes;
-  static constexpr int kOffRed = kOffQ + 2 * kQBytes;         // [4][warps][32] float4
-  static constexpr int kOffRedMl = kOffRed + 4 * kWarps * 32 * 16;
+  static constexpr int kOffRedMl = kOffQ + kQBytes;
+  // (the merge's [4][warps][32] float4 lie in the chunk's last stage)
+  static_assert(4 * kWarps * 32 * 16 <= 2 * kTileBytes, "merge");
   // a tile's scales as the products take them: K's of a row as four floats, V's of two
   // rows as four fp16 pairs
   static constexpr int kOffKs = kOffRedMl + kWarps * 8 * NG * 8;
   static constexpr int kOffVs = kOffKs + kKvTile * 16;
   static constexpr int kOffBar = kOffVs + kKvTile / 2 * 16;
-  static constexpr int kOffMsg = kOffBar + 8 * (2 * kStages + 4);
-  static constexpr int kOffMisc = kOffMsg + 2 * 128;
-  static constexpr int kSmem = kOffMisc + 16 + 1024;          // + alignment slack
-  static_assert(kStageBytes % 1024 == 0 && kOffMsg % 16 == 0, "alignment");
+  static constexpr int kOffMsg = (kOffBar + 8 * (2 * kStages + 2) + 15) / 16 * 16;
+  static constexpr int kOffMisc = kOffMsg + 128;
+  static constexpr int kSmem = kOffMisc + 16 + 512;           // + alignment slack (a swizzle's 512 bytes)
+  static_assert(kStageBytes % 512 == 0, "alignment");
   static_assert(kCtas * (kSmem + 1024) <= 233472, "shared memory");
 };
 
@@ -98,14 +99,14 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
   using Cfg = MxCfg<NG, MR>;
   constexpr int D = Cfg::D, S = Cfg::kStages, W = Cfg::kWarps;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 511) &
+                                             ~uintptr_t(511));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::kOffBar);
   uint64_t* empty = full + S;
   uint64_t* qfull = empty + S;
-  uint64_t* qempty = qfull + 2;
+  uint64_t* qempty = qfull + 1;
   int* misc = reinterpret_cast<int*>(smem + Cfg::kOffMisc);
-  UnitMsg* msg = reinterpret_cast<UnitMsg*>(smem + Cfg::kOffMsg);
+  UnitMsg& msg = *reinterpret_cast<UnitMsg*>(smem + Cfg::kOffMsg);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -113,10 +114,8 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], W);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&qfull[s], 1);
-      mbar_init(&qempty[s], W);
-    }
+    mbar_init(qfull, 1);  // a chunk's message and query vectors
+    mbar_init(qempty, W);
     misc[0] = 0;  // abort flag
     fence_barrier_init();
     tma_prefetch_desc(&tk);
@@ -193,10 +192,10 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
                                  (lane < npg ? pg0 + lane : fg0 + lane - npg)];
       }
       if (ent_ok && ci < gm.nch) {  // chunk description + the columns' query vectors
-        const int qs = ucount & 1;
-        wait_or_abort(&qempty[qs], ((ucount >> 1) & 1) ^ 1, a.err, misc);
+        // (the consumers take both before the chunk's first tile)
+        wait_or_abort(qempty, (ucount & 1) ^ 1, a.err, misc);
         if (lane == 0) {
-          UnitMsg& m = msg[qs];
+          UnitMsg& m = msg;
           m.r = r;
           m.slot = (int64_t)ci * (a.KVN * ha) + r.hk * ha + r.hg;
           m.ci = ci;
@@ -204,15 +203,15 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
           m.t_begin = t_begin;
           m.t_end = t_end;
           m.done = 0;
-          mbar_arrive_expect_tx(&qfull[qs], (uint32_t)(r.ncols * D * 2));
+          mbar_arrive_expect_tx(qfull, (uint32_t)(r.ncols * D * 2));
         }
         __syncwarp();
         for (int i = i_first + lane; i <= i_last; i += 32) {
           const int cb = max(r.c0, i * a.G), ce = min(r.c0 + r.ncols, (i + 1) * a.G);
-          bulk_load(smem + Cfg::kOffQ + qs * Cfg::kQBytes + (cb - r.c0) * D * 2,
+          bulk_load(smem + Cfg::kOffQ + (cb - r.c0) * D * 2,
                     a.q + ((int64_t)r.qrow0 + i) * a.q_stride +
                         ((int64_t)r.hk * a.G + cb - i * a.G) * D,
-                    (uint32_t)((ce - cb) * D * 2), &qfull[qs]);
+                    (uint32_t)((ce - cb) * D * 2), qfull);
         }
         ++ucount;
       }
@@ -296,11 +295,10 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
         a.claim[1] = 0;
       }
     }
-    const int qs = ucount & 1;  // the end of the CTA's work: an empty message
-    wait_or_abort(&qempty[qs], ((ucount >> 1) & 1) ^ 1, a.err, misc);
+    wait_or_abort(qempty, (ucount & 1) ^ 1, a.err, misc);  // the end: an empty message
     if (lane == 0) {
-      msg[qs].done = 1;
-      mbar_arrive(&qfull[qs]);
+      msg.done = 1;
+      mbar_arrive(qfull);
     }
     return;
   }
@@ -316,20 +314,23 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
   // This lane's row in the ldmatrix of groups 0, 1 and of groups 2, 3 of a block of 16
   // rows: matrices (rows 0-7, even group), (8-15, even), (0-7, odd), (8-15, odd).
   const uint32_t off01 = sw64(R0 + (lane & 15), lane >> 4), off23 = sw64(R0 + (lane & 15), 2 + (lane >> 4));
+  // The same for the transposed V: matrices (keys 0, 8, 2, 10, 4, ..., even group), (1, 9, 3,
+  // 11, ..., even), and of the odd group.  A lane's first register then holds keys 2q and
+  // 2q + 8, its second 2q + 1 and 2q + 9, and one mask pairs the neighbours of both.
+  const int vrow = R0 + 2 * ((lane & 7) >> 1) + 8 * (lane & 1) + ((lane >> 3) & 1);
+  const uint32_t voff01 = sw64(vrow, lane >> 4), voff23 = sw64(vrow, 2 + (lane >> 4));
   float* red_ml = reinterpret_cast<float*>(smem + Cfg::kOffRedMl);
-  float4* red4 = reinterpret_cast<float4*>(smem + Cfg::kOffRed);
 
   int it = 0, ucount = 0;
   while (true) {
-    const int qs = ucount & 1;
-    wait_or_abort(&qfull[qs], (ucount >> 1) & 1, a.err, misc);
+    wait_or_abort(qfull, ucount & 1, a.err, misc);
     // (the warps leave together: the merge meets at a named barrier)
-    if (named_bar_or(1, 32 * W, msg[qs].done || *reinterpret_cast<volatile int*>(misc))) break;
-    const UnitInfo r = msg[qs].r;
+    if (named_bar_or(1, 32 * W, msg.done || *reinterpret_cast<volatile int*>(misc))) break;
+    const UnitInfo r = msg.r;
     const int kvl = r.kv_len;
-    const int64_t slot0 = a.sched[kSchedHeader + r.b] + msg[qs].slot;
-    const int t_begin = msg[qs].t_begin, t_end = msg[qs].t_end;
-    const bool split = msg[qs].nch > 1;
+    const int64_t slot0 = a.sched[kSchedHeader + r.b] + msg.slot;
+    const int t_begin = msg.t_begin, t_end = msg.t_end;
+    const bool split = msg.nch > 1;
     // keys seen by the columns of this lane's accumulators, and their mask rows
     int loc[NG][2], hic[NG][2], mrow[NG][2];
 #pragma unroll
@@ -352,7 +353,7 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
     uint32_t qb[NG][KS][2];
     float slc;
     {
-      const uint16_t* qsm = reinterpret_cast<const uint16_t*>(smem + Cfg::kOffQ + qs * Cfg::kQBytes);
+      const uint16_t* qsm = reinterpret_cast<const uint16_t*>(smem + Cfg::kOffQ);
       uint32_t emax = 0;
 #pragma unroll
       for (int ng = 0; ng < NG; ++ng)
@@ -368,8 +369,9 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
         }
       emax = __reduce_max_sync(0xffffffffu, emax);
       const int sh = min(max(142 - (int)emax, -100), 100);  // 15 - (emax - 127)
-      const float up = __int_as_float((127 + sh) << 23);
-      slc = a.scale_log2 * __int_as_float((127 - sh) << 23);
+      // (the score factor is positive, its sign in the queries: hidden scores stay -inf)
+      const float up = copysignf(__int_as_float((127 + sh) << 23), a.scale_log2);
+      slc = fmaxf(fabsf(a.scale_log2) * __int_as_float((127 - sh) << 23), 1e-36f);
 #pragma unroll
       for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
             qb[ng][kk][k] = pack_f16(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up);
           }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&qempty[qs]);
+      if (lane == 0) mbar_arrive(qempty);
       ++ucount;
     }
     float acc[MT][NG][4];
@@ -433,10 +435,11 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
         if (jt + R0 + lane >= kvl || X) vw = gone(jt + R0 + lane) ? 0u : vw;
         __nv_bfloat162 v[2];
         e8m0x4_to_bf16x2x2(vw, v);
-        // (a NaN is larger than nothing)
-        const bool past = __any_sync(0xffffffffu, __hgt(v[0].x, vref[0].x) | __hgt(v[0].y, vref[0].y) |
-                                                      __hgt(v[1].x, vref[1].x) | __hgt(v[1].y, vref[1].y));
-        if (past) {
+        // (the larger of two drops a NaN)
+        const __nv_bfloat162 m0 = __hmax2(v[0], vref[0]), m1 = __hmax2(v[1], vref[1]);
+        const bool past = *reinterpret_cast<const uint32_t*>(&m0) != *reinterpret_cast<const uint32_t*>(&vref[0]) ||
+                          *reinterpret_cast<const uint32_t*>(&m1) != *reinterpret_cast<const uint32_t*>(&vref[1]);
+        if (__any_sync(0xffffffffu, past)) {
           // new references: O moves by exact powers of two
           vmove = true;
           const uint32_t u[2] = {*reinterpret_cast<const uint32_t*>(&v[0]), *reinterpret_cast<const uint32_t*>(&v[1])};
@@ -504,10 +507,6 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
             x[b][ng][3] += s4[3] * fb[j];
           }
         }
-#pragma unroll
-        for (int ng = 0; ng < NG; ++ng)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[b][ng][k] *= slc;
       }
       // ---------------- mask ----------------
       if (edge) {
@@ -538,7 +537,7 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
               const int cl = ng * 8 + 2 * q4, j = jw + 16 * b + 4 * k + g;
               if (cl < r.ncols && j < end)
                 *reinterpret_cast<float2*>(a.scores + (base + j) * a.score_cols + r.c0 + cl) =
-                    make_float2(x[b][ng][k], x[b][ng][k + 1]);
+                    make_float2(x[b][ng][k] * slc, x[b][ng][k + 1] * slc);
             }
       }
       // ---------------- online softmax per column ----------------
@@ -551,8 +550,8 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
           float mx = fmaxf(x[0][ng][e], x[0][ng][2 + e]);
 #pragma unroll
           for (int b = 1; b < NB; ++b) mx = fmaxf(mx, fmaxf(x[b][ng][e], x[b][ng][2 + e]));
-          top[ng][e] = mx;
-          over |= mx > m_r[ng][e] + kOver;
+          top[ng][e] = mx * slc;
+          over |= top[ng][e] > m_r[ng][e] + kOver;
         }
       if (__any_sync(0xffffffffu, over) || vmove) {
         float fct[NG][2];
@@ -593,7 +592,7 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
           float pr[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            pr[k] = fast_exp2(x[b][ng][k] - mu[ng][k & 1]);
+            pr[k] = fast_exp2(fmaf(x[b][ng][k], slc, -mu[ng][k & 1]));
             l_r[ng][k & 1] += pr[k];
           }
           pt[b][ng][0] = movmatrix_t(pack_f16(pr[0], pr[1]));
@@ -612,13 +611,12 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
         const uint32_t vt = st + Cfg::kTileBytes + 1024 * b;
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj) {  // groups 2*jj, 2*jj + 1
-          uint32_t w[4];  // (group 2*jj: keys 2q, 2q+1), (keys 2q+8, 2q+9), (group 2*jj + 1: ...)
-          ldsm_x4_t(vt + (jj ? off23 : off01), w[0], w[1], w[2], w[3]);
+          uint32_t w[4];  // (group 2*jj: keys 2q, 2q+8), (keys 2q+1, 2q+9), (group 2*jj + 1: ...)
+          ldsm_x4_t(vt + (jj ? voff23 : voff01), w[0], w[1], w[2], w[3]);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int j = 2 * jj + k;
-            const uint32_t lo = __byte_perm(w[2 * k], w[2 * k + 1], 0x5410);  // keys 2q, 2q+8
-            const uint32_t hi = __byte_perm(w[2 * k], w[2 * k + 1], 0x7632);  // keys 2q+1, 2q+9
+            const uint32_t lo = w[2 * k], hi = w[2 * k + 1];
             // bytes of two keys' codes of one element: 0, 2 (keys 2q, 2q+1), 0, 2 (2q+8, 2q+9)
             const uint32_t ev = (lo & 0x0f0f0f0fu) | ((hi << 4) & 0xf0f0f0f0u);
             const uint32_t od = ((lo >> 4) & 0x0f0f0f0fu) | (hi & 0xf0f0f0f0u);  // and 1, 3
@@ -636,7 +634,7 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
       }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[s]);
+      if (lane == 0 && tt + 1 < ntile_here) mbar_arrive(&empty[s]);  // (the last: behind the merge)
     }
 
     // ---------------- merge the warps' states ----------------
@@ -685,6 +683,7 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
         }
       }
     }
+    float4* red4 = reinterpret_cast<float4*>(smem + (it + S - 1) % S * Cfg::kStageBytes);
     // Warp w ends with m-tiles 2w and 2w + 1 (the elements of group w) summed over the
     // warps: in each of two rounds every warp stores the four m-tiles 2k + round but its
     // own, then adds the others' copies to its own.
@@ -695,6 +694,10 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
       float4 own[2];  // (d, column 2q), (d, 2q+1), (d+1, 2q), (d+1, 2q+1), d = 32 warp + 4 g + 2 rnd
 #pragma unroll
       for (int rnd = 0; rnd < 2; ++rnd) {
+        if (ntile_here == 0) {  // (no stage, and nothing to add up)
+          own[rnd] = make_float4(0.f, 0.f, 0.f, 0.f);
+          continue;
+        }
         if (ng > 0 || rnd > 0) named_bar_sync(1, 32 * W);  // the round before has been read
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -710,6 +713,11 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
           const float4 o = red4[(warp * W + w2) * 32 + lane];
           own[rnd].x += o.x; own[rnd].y += o.y; own[rnd].z += o.z; own[rnd].w += o.w;
         }
+      }
+      if (ng == NG - 1 && ntile_here > 0) {  // the stage goes back
+        fence_proxy_async_smem();  // (the merge wrote it; a copy will)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[(it + S - 1) % S]);
       }
       const int d = 32 * warp + 4 * g;
 #pragma unroll
