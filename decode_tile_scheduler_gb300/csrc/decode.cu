@@ -1998,8 +1998,8 @@ __global__ void __launch_bounds__(256, 4)
 
 }  // namespace fia
 
-#include "decode_cluster.cuh"
 #include "decode_mx.cuh"
+#include "decode_cluster.cuh"
 
 namespace fia {
 

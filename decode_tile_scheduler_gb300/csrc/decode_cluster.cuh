@@ -1,6 +1,7 @@
 // decode_cluster.cuh -- decode calls of few units and few keys in one kernel (part of
 // decode.cu): a cluster of eight CTAs per unit instead of plan, chunks, partials in
-// global memory and a combine.  For a window with first tokens and for key weights.
+// global memory and a combine.  For a window with first tokens, for key weights, and for
+// MXFP4 caches.
 //
 // A unit is (sequence, KV head, 8 columns (query row, head)).  Its warps, 64 in the
 // cluster, take 16 keys at a time, straight from global memory into the fragments of
@@ -12,6 +13,9 @@
 // in shared memory, the CTAs' through distributed shared memory, each CTA an eighth
 // of D.  Key weights need no second look at K: a warp keeps its scores in shared
 // memory until the columns' lse is known.
+//
+// MXFP4: a warp's 16 rows go through its part of shared memory, and from there as in
+// decode_mx.cuh.
 //
 // Bound by latency: lengths and page table, then K and V, then two folds.  One sequence,
 // 8 KV heads, a window of 1024 and 4 first tokens: 7.7 us a call in a graph (plan, decode
@@ -43,10 +47,13 @@ __device__ __forceinline__ void codes_bf16(uint32_t codes, uint32_t& lo, uint32_
   hi = pack_bf16(fh.x, fh.y);
 }
 
-template <int D, bool FP8, bool WT>
+enum FewFormat { kFewBf16, kFewFp8, kFewMx };
+
+template <int D, int F, bool WT>
 __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 2)
     decode_few_kernel(const DecodeArgs a, const CacheView c, const KeyWeightsOut o, int groups,
                       int planned) {
+  constexpr bool FP8 = F == kFewFp8, MX = F == kFewMx;
   constexpr int NK = FP8 ? 4 : D / 32;   // 16-byte pieces of a lane's Q row
   constexpr int NV = D / 64;             // pieces of a V row per lane, 8 elements each
   extern __shared__ float kept[];        // WT: per step of a warp, 16 keys x 8 scores, 16 old weights
@@ -111,7 +118,35 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
       const int col = c0 + g, row = col / a.G, h = hk * a.G + col - row * a.G;
       const uint4* src = reinterpret_cast<const uint4*>(a.q + (qrow + row) * a.q_stride + (int64_t)h * D);
       // bf16: piece q4 + 4i of 8 elements; FP8: the two halves of piece q4 + 4 (i / 2) of 16
+      // (MXFP4: as bf16: the eight elements of group i at 8 q4)
       q[i] = __ldg(src + (FP8 ? 2 * (q4 + 4 * (i >> 1)) + (i & 1) : q4 + 4 * i));
+    }
+  }
+  // MXFP4: Q in fp16 times a power of two, K's 2 k-steps a group, the score factor (all
+  // as in decode_mx_kernel)
+  float slc = a.scale_log2;
+  __nv_bfloat162 vref[2], vinv[2];
+  if constexpr (MX) {
+    uint32_t emax = 0;
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) emax = max(emax, max((w[k] >> 7) & 0xffu, (w[k] >> 23) & 0xffu));
+    }
+    emax = __reduce_max_sync(0xffffffffu, emax);
+    const int sh = min(max(142 - (int)emax, -100), 100);
+    const float up = __int_as_float((127 + sh) << 23);
+    slc = a.scale_log2 * __int_as_float((127 - sh) << 23);
+    const auto half = [&](uint32_t w) {
+      return pack_f16(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
+    };
+#pragma unroll
+    for (int i = 0; i < NK; ++i) q[i] = make_uint4(half(q[i].x), half(q[i].y), half(q[i].z), half(q[i].w));
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      vref[k] = mx_pair(kMxRefMin << 7, kMxRefMin << 7);
+      vinv[k] = mx_pair((254 - kMxRefMin) << 7, (254 - kMxRefMin) << 7);
     }
   }
   // the bounds of this lane's two columns
@@ -137,7 +172,7 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int k = 0; k < 4; ++k) O[i][t][k] = 0.f;
-  const int64_t row_bytes = (int64_t)D * (FP8 ? 1 : 2);
+  const int64_t row_bytes = MX ? D / 2 : (int64_t)D * (FP8 ? 1 : 2);
   const int64_t key_bytes = c.head_major ? row_bytes : row_bytes * a.KVN;
   for (int n = 0, t = wid * kFewCtas + rank; t < steps; ++n, t += kFewSpan) {
     const int j0 = (t < nwin ? s0 + t : t - nwin) * kFewKeys;
@@ -155,9 +190,28 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
     const auto seen = [&](int k) {
       return k < end && j0 + k <= r.hi && (j0 + k >= r.lo || j0 + k < a.first_tokens);
     };
+    // (MXFP4: 16-byte pieces of rows on their way to shared memory, piece lane % 4 of rows
+    // lane / 4 and 8 more; the scales of row lane)
+    uint8_t* rows = reinterpret_cast<uint8_t*>(o_warp[wid]);  // K, V, the scales as products take them
+    uint4 kt[2], vt[2];
+    uint32_t ksw = 0u, vsw = 0u;
+    if constexpr (MX) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        kt[k] = vt[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (seen(g + 8 * k)) {
+          kt[k] = __ldg(reinterpret_cast<const uint4*>(kb + (g + 8 * k) * key_bytes) + q4);
+          vt[k] = __ldg(reinterpret_cast<const uint4*>(vb + (g + 8 * k) * key_bytes) + q4);
+        }
+      }
+      if (lane < kFewKeys && seen(lane)) {
+        ksw = __ldg(reinterpret_cast<const uint32_t*>(c.ks) + at.srow + lane);
+        vsw = __ldg(reinterpret_cast<const uint32_t*>(c.vs) + at.srow + lane);
+      }
+    }
     uint4 kx[2][FP8 ? 2 : NK];
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < 2 && !MX; ++k)
 #pragma unroll
       for (int i = 0; i < (FP8 ? 2 : NK); ++i) {
         kx[k][i] = make_uint4(0u, 0u, 0u, 0u);
@@ -166,7 +220,7 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
       }
     uint4 vx[4][NV];  // FP8: the first 8 bytes of each
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 4 && !MX; ++k) {
       const int key = 2 * q4 + (k & 1) + 8 * (k >> 1);
       const bool on = seen(key);
 #pragma unroll
@@ -200,7 +254,51 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
 
     // ---- scores ----
     float x[4];  // keys g, g, g + 8, g + 8; columns 2 q4, 2 q4 + 1, ...
-    if constexpr (FP8) {
+    float vfct[4] = {1.f, 1.f, 1.f, 1.f};  // MXFP4: what O's groups are multiplied by
+    if constexpr (MX) {
+      __syncwarp();  // (the step before has read its rows)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        *reinterpret_cast<uint4*>(rows + sw64(g + 8 * k, q4)) = kt[k];
+        *reinterpret_cast<uint4*>(rows + 1024 + sw64(g + 8 * k, q4)) = vt[k];
+      }
+      float kf[4];
+      e8m0x4_to_f32x4(ksw, kf);
+      __nv_bfloat162 v[2];
+      e8m0x4_to_bf16x2x2(vsw, v);
+      mx_references(v, vref, vinv, vfct);
+      const uint2 pairs = mx_scale_pairs(v, vinv, lane);
+      if (lane < kFewKeys) {
+        *reinterpret_cast<float4*>(rows + 2048 + lane * 16) = make_float4(kf[0], kf[1], kf[2], kf[3]);
+        *reinterpret_cast<uint2*>(rows + 2304 + lane * 8) = pairs;
+      }
+      __syncwarp();
+      const float4 f0 = *reinterpret_cast<const float4*>(rows + 2048 + g * 16);
+      const float4 f1 = *reinterpret_cast<const float4*>(rows + 2048 + (g + 8) * 16);
+      const float fa[4] = {f0.x, f0.y, f0.z, f0.w}, fb[4] = {f1.x, f1.y, f1.z, f1.w};
+      x[0] = x[1] = x[2] = x[3] = 0.f;
+#pragma unroll
+      for (int jj = 0; jj < 2; ++jj) {
+        uint32_t w[4];
+        ldsm_x4(smem_u32(rows) + sw64(lane & 15, 2 * jj + (lane >> 4)), w[0], w[1], w[2], w[3]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int j = 2 * jj + k;
+          uint32_t ka[2][4];
+          e2m1x8_to_f16x2x4(w[2 * k], ka[0][0], ka[0][2], ka[1][0], ka[1][2]);
+          e2m1x8_to_f16x2x4(w[2 * k + 1], ka[0][1], ka[0][3], ka[1][1], ka[1][3]);
+          float s4[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_f16(s4, ka[0], q[j].x, q[j].y);
+          mma_f16(s4, ka[1], q[j].z, q[j].w);
+          x[0] += s4[0] * fa[j];
+          x[1] += s4[1] * fa[j];
+          x[2] += s4[2] * fb[j];
+          x[3] += s4[3] * fb[j];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] *= slc;
+    } else if constexpr (FP8) {
       float h[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {  // the halves of D apart: each has its scale
@@ -263,7 +361,8 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
     float p[4];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float mx = fmaxf(m[e], fmaxf(x[e], x[2 + e]));
+      // (MXFP4: the reference lies 13 lower, which keeps P's bits in fp16)
+      float mx = fmaxf(m[e], fmaxf(x[e], x[2 + e]) - (MX ? 13.f : 0.f));
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
       const float mu = mx == -INFINITY ? 0.f : mx;
@@ -276,19 +375,39 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          O[i][k][e] *= FP8 ? corr * ratio[i] : corr;
-          O[i][k][2 + e] *= FP8 ? corr * ratio[i] : corr;
+          const float f = MX ? corr * vfct[2 * i + (k >> 1)] : FP8 ? corr * ratio[i] : corr;
+          O[i][k][e] *= f;
+          O[i][k][2 + e] *= f;
         }
     }
 
     // ---- O^T += V^T P: P is rounded to bf16 here (FP8: to fp16, see above) ----
     uint32_t b0, b1;
-    if constexpr (!FP8) {
+    if constexpr (MX) {
+      const uint32_t p0 = movmatrix_t(pack_f16(p[0], p[1])), p1 = movmatrix_t(pack_f16(p[2], p[3]));
+      const uint4 s0 = *reinterpret_cast<const uint4*>(rows + 2304 + q4 * 16);
+      const uint4 s1 = *reinterpret_cast<const uint4*>(rows + 2304 + (q4 + 4) * 16);
+      const uint32_t sa[4] = {s0.x, s0.y, s0.z, s0.w}, sb[4] = {s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+      for (int jj = 0; jj < 2; ++jj) {
+        uint32_t w[4];
+        ldsm_x4_t(smem_u32(rows) + 1024 + sw64(mx_v_row(lane), 2 * jj + (lane >> 4)), w[0], w[1], w[2], w[3]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {  // group 2 jj + k: O's m-tiles 2 k and 2 k + 1 of half jj
+          uint32_t va[2][4];
+          mx_v_fragments(w[2 * k], w[2 * k + 1], va);
+          b0 = mul_f16x2(p0, sa[2 * jj + k]);
+          b1 = mul_f16x2(p1, sb[2 * jj + k]);
+          mma_f16(O[jj][2 * k], va[0], b0, b1);
+          mma_f16(O[jj][2 * k + 1], va[1], b0, b1);
+        }
+      }
+    } else if constexpr (!FP8) {
       b0 = movmatrix_t(pack_bf16(p[0], p[1]));
       b1 = movmatrix_t(pack_bf16(p[2], p[3]));
     }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
+    for (int i = 0; i < NV && !MX; ++i) {
       if constexpr (FP8) {
         const float v0 = (i ? vsc[0].y : vsc[0].x) * over[i], v1 = (i ? vsc[1].y : vsc[1].x) * over[i];
         b0 = movmatrix_t(pack_f16(p[0] * v0, p[1] * v0));
@@ -322,8 +441,17 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
 #pragma unroll
     for (int d = 4; d < 32; d <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
     if (g == 0) ml_warp[wid][2 * q4 + e] = make_float2(m[e], l[e]);
+    if constexpr (MX) {
+      if (e == 0) __syncwarp();  // (o_warp held the last step's rows)
+      float back[4];
+      bf16x2x2_to_f32x4(vref[0], vref[1], back);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
+      for (int t = 0; t < 8; ++t)  // group t / 2, elements 4g + 2 (t % 2) and the next
+        *reinterpret_cast<float2*>(&o_warp[wid][2 * q4 + e][32 * (t >> 1) + 4 * g + 2 * (t & 1)]) =
+            make_float2(back[t >> 1] * O[t >> 2][t & 3][e], back[t >> 1] * O[t >> 2][t & 3][2 + e]);
+    }
+#pragma unroll
+    for (int i = 0; i < NV && !MX; ++i) {
       const float back = FP8 ? __int_as_float(vexp[i] << 23) : 1.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k)  // elements 2k and 2k + 1 of piece g + 8i
@@ -448,13 +576,13 @@ int64_t few_steps(const DecodeArgs& a) {
   return std::min(all, keys / kFewKeys + 3);
 }
 
-template <int D, bool FP8, bool WT>
+template <int D, int F, bool WT>
 cudaError_t launch_few_t(const DecodeArgs& a, const CacheView& c, const KeyWeightsOut* w,
                          bool planned, cudaStream_t s) {
   const int groups = (a.S_max * a.G + 7) / 8;
   const size_t smem = WT ? 4 * (size_t)kFewKept * kFewWarps * ((few_steps(a) + kFewSpan - 1) / kFewSpan) : 0;
   const KeyWeightsOut o = WT ? *w : KeyWeightsOut{};
-  auto kern = decode_few_kernel<D, FP8, WT>;
+  auto kern = decode_few_kernel<D, F, WT>;
   static std::atomic<uint64_t> done_mask[4];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -480,25 +608,29 @@ cudaError_t launch_few_t(const DecodeArgs& a, const CacheView& c, const KeyWeigh
 // of 4000 14.1 / 14.5, of 8000 22.3 / 17.5; 32 units 10.8 / 17.6, 18.8 / 26.3, 37.3 /
 // 36.1; 48 units of 2000 keys 24.1 / 23.3.  FP8 gains more.  (With FIA_DEBUG the other
 // kernels run: they report pages outside the pool.)
-bool decode_is_few(const DecodeArgs& a, bool weights) {
-  if ((a.first_tokens == 0 && !weights) || a.mask || a.debug || a.num_ctas < kFewCtas) return false;
+bool decode_is_few(const DecodeArgs& a, bool mx, bool weights) {
+  const int sms = mx ? a.num_ctas / decode_mx_ctas() : a.num_ctas;
+  if ((a.first_tokens == 0 && !weights && !mx) || a.mask || a.debug || sms < kFewCtas) return false;
   const int64_t groups = (a.S_max * a.G + 7) / 8;
   if (weights && groups > 1) return false;  // (a key's weight is a sum within one unit)
-  return (int64_t)a.B * a.KVN * groups * 9 <= 2 * a.num_ctas &&
+  return (int64_t)a.B * a.KVN * groups * 9 <= 2 * sms &&
          few_steps(a) <= kFewSpan * (weights ? kFewMaxKept : kFewMaxRounds);
 }
 
 cudaError_t launch_decode_few(const DecodeArgs& a, const fia_kv_cache& cache, const KeyWeightsOut* w,
                               bool planned, cudaStream_t s) {
   const CacheView c = cache_view(cache);
+  if (c.mx)
+    return w ? launch_few_t<128, kFewMx, true>(a, c, w, planned, s)
+             : launch_few_t<128, kFewMx, false>(a, c, w, planned, s);
   if (c.fp8)
-    return w ? launch_few_t<128, true, true>(a, c, w, planned, s)
-             : launch_few_t<128, true, false>(a, c, w, planned, s);
+    return w ? launch_few_t<128, kFewFp8, true>(a, c, w, planned, s)
+             : launch_few_t<128, kFewFp8, false>(a, c, w, planned, s);
   if (a.D == 64)
-    return w ? launch_few_t<64, false, true>(a, c, w, planned, s)
-             : launch_few_t<64, false, false>(a, c, w, planned, s);
-  return w ? launch_few_t<128, false, true>(a, c, w, planned, s)
-           : launch_few_t<128, false, false>(a, c, w, planned, s);
+    return w ? launch_few_t<64, kFewBf16, true>(a, c, w, planned, s)
+             : launch_few_t<64, kFewBf16, false>(a, c, w, planned, s);
+  return w ? launch_few_t<128, kFewBf16, true>(a, c, w, planned, s)
+           : launch_few_t<128, kFewBf16, false>(a, c, w, planned, s);
 }
 
 }  // namespace fia

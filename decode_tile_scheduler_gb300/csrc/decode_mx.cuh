@@ -4,9 +4,11 @@
 // A key is 68 bytes of K and of V where FP8 has 136, for the same number of elements to
 // widen, so the kernel is bound by the instructions of an element, not by memory.  What
 // it does about that:
-//  - Three CTAs to an SM (two with 16 columns), each with one producer warp and four
-//    consumer warps of 32 rows of a tile, so that a chunk's set-up, waits and merge run
-//    beside the others' products, and twelve consumer warps hide each other's latencies.
+//  - Three CTAs to an SM, each with one producer warp and four consumer warps of 32 rows
+//    of a tile, so that a chunk's set-up, waits and merge run beside the others' products,
+//    and twelve consumer warps hide each other's latencies.  Units have 8 columns: 16, in
+//    two CTAs to an SM with the blocks of 16 rows one after the other, widen the codes once
+//    for both halves, but took 52 us where 8 take 45 (16 sequences, 1 to 4 rows of 4 heads).
 //  - Codes go from shared memory to mma fragments by ldmatrix.  K: 32 bits of a row are
 //    eight elements of one scale group, two k-steps of m16n8k16 (the order of a
 //    contraction is free).  V: to the transposing ldmatrix four elements of a key are
@@ -24,25 +26,25 @@
 namespace fia {
 namespace {
 
-template <int NG, bool MR>
+template <bool MR>
 struct MxCfg {
   static constexpr int D = 128, kRowBytes = D / 2;
   static constexpr int kWarps = 4, kRows = kKvTile / kWarps;  // consumers, rows of a tile each
   static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kCtas = NG == 1 ? 3 : 2;               // to an SM
+  static constexpr int kCtas = 3;                             // to an SM
   static constexpr int kTileBytes = kKvTile * kRowBytes;      // K, or V
   static constexpr int kScaleBytes = kKvTile * 4;
   static constexpr int kOffScale = 2 * kTileBytes, kOffMask = kOffScale + 2 * kScaleBytes;
   static constexpr int kStageBytes = kOffMask + (MR ? kDecodeMaxRows * kKvTile : 0);
-  static constexpr int kStages = NG == 1 ? (MR ? 3 : 4) : (MR ? 4 : 5);
-  static constexpr int kQBytes = 8 * NG * D * 2;
+  static constexpr int kStages = MR ? 3 : 4;
+  static constexpr int kQBytes = 8 * D * 2;
   static constexpr int kOffQ = kStages * kStageBytes;
   static constexpr int kOffRedMl = kOffQ + kQBytes;
   // (the merge's [4][warps][32] float4 lie in the chunk's last stage)
   static_assert(4 * kWarps * 32 * 16 <= 2 * kTileBytes, "merge");
   // a tile's scales as the products take them: K's of a row as four floats, V's of two
   // rows as four fp16 pairs
-  static constexpr int kOffKs = kOffRedMl + kWarps * 8 * NG * 8;
+  static constexpr int kOffKs = kOffRedMl + kWarps * 8 * 8;
   static constexpr int kOffVs = kOffKs + kKvTile * 16;
   static constexpr int kOffBar = kOffVs + kKvTile / 2 * 16;
   static constexpr int kOffMsg = (kOffBar + 8 * (2 * kStages + 2) + 15) / 16 * 16;
@@ -91,12 +93,66 @@ __device__ __forceinline__ __nv_bfloat162 mx_pair(uint32_t lo, uint32_t hi) {
   return *reinterpret_cast<const __nv_bfloat162*>(&w);
 }
 
-// NG, MR, X: as decode_kernel's.
-template <int NG, bool MR, bool X>
-__global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
+// A row's V scales v (bf16, a lane each) against the references: where one is past its
+// group's (a NaN is past nothing), the warp's new references, and the exact powers of two
+// that O's groups move by in f.  Returns whether they moved.
+__device__ __forceinline__ bool mx_references(const __nv_bfloat162 (&v)[2], __nv_bfloat162 (&vref)[2],
+                                              __nv_bfloat162 (&vinv)[2], float (&f)[4]) {
+  const auto bits = [](const __nv_bfloat162& x) { return *reinterpret_cast<const uint32_t*>(&x); };
+  // (the larger of two drops a NaN)
+  const bool past = bits(__hmax2(v[0], vref[0])) != bits(vref[0]) || bits(__hmax2(v[1], vref[1])) != bits(vref[1]);
+  if (!__any_sync(0xffffffffu, past)) return false;
+  uint32_t en[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t c = (bits(v[j >> 1]) >> (16 * (j & 1)) & 0xffffu) >> 7;
+    const uint32_t old = (bits(vref[j >> 1]) >> (16 * (j & 1)) & 0xffffu) >> 7;
+    en[j] = max(old, min(__reduce_max_sync(0xffffffffu, c == 255u ? 0u : c), (uint32_t)kMxRefMax));
+    // (a jump past 2^-126 leaves a negligible old sum and gives 0)
+    f[j] = __int_as_float(max(127 + (int)old - (int)en[j], 0) << 23);
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    vref[k] = mx_pair(en[2 * k] << 7, en[2 * k + 1] << 7);
+    vinv[k] = mx_pair((254 - en[2 * k]) << 7, (254 - en[2 * k + 1]) << 7);
+  }
+  return true;
+}
+// V scales over their references as fp16 pairs of rows 2k, 2k + 1 (lanes): groups 0 and 1
+// from the even lane, 2 and 3 from the odd one.
+__device__ __forceinline__ uint2 mx_scale_pairs(const __nv_bfloat162 (&v)[2], const __nv_bfloat162 (&vinv)[2],
+                                                int lane) {
+  float vf[4];
+  bf16x2x2_to_f32x4(__hmul2(v[0], vinv[0]), __hmul2(v[1], vinv[1]), vf);
+  const uint32_t h01 = pack_f16(vf[0], vf[1]), h23 = pack_f16(vf[2], vf[3]);
+  const uint32_t theirs = __shfl_xor_sync(0xffffffffu, lane & 1 ? h01 : h23, 1);
+  const uint32_t even = lane & 1 ? theirs : h01, odd = lane & 1 ? h23 : theirs;
+  return make_uint2(__byte_perm(even, odd, 0x5410), __byte_perm(even, odd, 0x7632));
+}
+// The row of a block of 16 whose address this lane gives the transposing ldmatrix of V:
+// matrices (keys 0, 8, 2, 10, 4, ..., even group), (1, 9, 3, 11, ..., even), and of the odd
+// group.  A lane's first register then holds keys 2q and 2q + 8, its second 2q + 1 and
+// 2q + 9, and one mask pairs the neighbours of both.
+__device__ __forceinline__ int mx_v_row(int lane) {
+  return 2 * ((lane & 7) >> 1) + 8 * (lane & 1) + ((lane >> 3) & 1);
+}
+// The fragments of a group's two m-tiles.  A lane has four elements d = 4g .. +3 of the
+// group of its four keys; m-tile h holds the elements 2h in its fragment rows 0-7, 2h + 1
+// in rows 8-15.
+__device__ __forceinline__ void mx_v_fragments(uint32_t lo, uint32_t hi, uint32_t (&va)[2][4]) {
+  // bytes of two keys' codes of one element: 0, 2 (keys 2q, 2q+1), 0, 2 (2q+8, 2q+9)
+  const uint32_t ev = (lo & 0x0f0f0f0fu) | ((hi << 4) & 0xf0f0f0f0u);
+  const uint32_t od = ((lo >> 4) & 0x0f0f0f0fu) | (hi & 0xf0f0f0f0u);  // and 1, 3
+  e2m1x8_to_f16x2x4(ev, va[0][0], va[1][0], va[0][2], va[1][2]);
+  e2m1x8_to_f16x2x4(od, va[0][1], va[1][1], va[0][3], va[1][3]);
+}
+
+// MR, X: as decode_kernel's.
+template <bool MR, bool X>
+__global__ void __launch_bounds__(MxCfg<MR>::kThreads, MxCfg<MR>::kCtas)
     decode_mx_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv) {
-  using Cfg = MxCfg<NG, MR>;
+  using Cfg = MxCfg<MR>;
   constexpr int D = Cfg::D, S = Cfg::kStages, W = Cfg::kWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 511) &
@@ -308,17 +364,12 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
   const int R0 = warp * Cfg::kRows;
   const uint32_t smem_base = smem_u32(smem);
   constexpr int KS = D / 16, MT = D / 16;  // k-steps, m-tiles
-  // blocks of 16 rows that a warp takes side by side (with 16 columns one after the other:
-  // 128 registers of accumulators and queries)
-  constexpr int NB = NG == 1 ? 2 : 1, kStep = 16 * NB;
+  constexpr int NB = Cfg::kRows / 16;      // blocks of 16 rows, side by side
   // This lane's row in the ldmatrix of groups 0, 1 and of groups 2, 3 of a block of 16
-  // rows: matrices (rows 0-7, even group), (8-15, even), (0-7, odd), (8-15, odd).
-  const uint32_t off01 = sw64(R0 + (lane & 15), lane >> 4), off23 = sw64(R0 + (lane & 15), 2 + (lane >> 4));
-  // The same for the transposed V: matrices (keys 0, 8, 2, 10, 4, ..., even group), (1, 9, 3,
-  // 11, ..., even), and of the odd group.  A lane's first register then holds keys 2q and
-  // 2q + 8, its second 2q + 1 and 2q + 9, and one mask pairs the neighbours of both.
-  const int vrow = R0 + 2 * ((lane & 7) >> 1) + 8 * (lane & 1) + ((lane >> 3) & 1);
-  const uint32_t voff01 = sw64(vrow, lane >> 4), voff23 = sw64(vrow, 2 + (lane >> 4));
+  // rows: matrices (rows 0-7, even group), (8-15, even), (0-7, odd), (8-15, odd).  And in
+  // the transposing one of V.
+  const uint32_t off[2] = {sw64(R0 + (lane & 15), lane >> 4), sw64(R0 + (lane & 15), 2 + (lane >> 4))};
+  const uint32_t voff[2] = {sw64(R0 + mx_v_row(lane), lane >> 4), sw64(R0 + mx_v_row(lane), 2 + (lane >> 4))};
   float* red_ml = reinterpret_cast<float*>(smem + Cfg::kOffRedMl);
 
   int it = 0, ucount = 0;
@@ -331,77 +382,62 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
     const int64_t slot0 = a.sched[kSchedHeader + r.b] + msg.slot;
     const int t_begin = msg.t_begin, t_end = msg.t_end;
     const bool split = msg.nch > 1;
-    // keys seen by the columns of this lane's accumulators, and their mask rows
-    int loc[NG][2], hic[NG][2], mrow[NG][2];
+    // keys seen by this lane's two columns, and their mask rows
+    int loc[2], hic[2], mrow[2];
 #pragma unroll
-    for (int ng = 0; ng < NG; ++ng)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if constexpr (MR) {
-          const int i = (r.c0 + min(ng * 8 + 2 * q4 + e, max(r.ncols, 1) - 1)) / a.G;
-          row_bounds(a, r.q_len, kvl, i, &loc[ng][e], &hic[ng][e]);
-          mrow[ng][e] = (i - r.c0 / a.G) * kKvTile;
-        } else {
-          loc[ng][e] = r.lo;
-          hic[ng][e] = r.hi;
-          mrow[ng][e] = 0;
-        }
+    for (int e = 0; e < 2; ++e) {
+      if constexpr (MR) {
+        const int i = (r.c0 + min(2 * q4 + e, max(r.ncols, 1) - 1)) / a.G;
+        row_bounds(a, r.q_len, kvl, i, &loc[e], &hic[e]);
+        mrow[e] = (i - r.c0 / a.G) * kKvTile;
+      } else {
+        loc[e] = r.lo;
+        hic[e] = r.hi;
+        mrow[e] = 0;
       }
+    }
     // Q^T fragments in fp16, times a power of two that puts the unit's largest element at
     // exponent 15 (decode_kernel tells why); k-step kk = 2*group + j covers
     // d = 32*group + 8*q + 4*j + {0..3}
-    uint32_t qb[NG][KS][2];
+    uint32_t qb[KS][2];
     float slc;
     {
-      const uint16_t* qsm = reinterpret_cast<const uint16_t*>(smem + Cfg::kOffQ);
+      const uint16_t* qsm = reinterpret_cast<const uint16_t*>(smem + Cfg::kOffQ) + g * D + 8 * q4;
       uint32_t emax = 0;
 #pragma unroll
-      for (int ng = 0; ng < NG; ++ng)
-#pragma unroll
-        for (int kk = 0; kk < KS; ++kk) {
-          uint2 v = make_uint2(0u, 0u);
-          if (ng * 8 + g < r.ncols)
-            v = *reinterpret_cast<const uint2*>(qsm + (ng * 8 + g) * D + (kk >> 1) * 32 + 8 * q4 + 4 * (kk & 1));
-          qb[ng][kk][0] = v.x;
-          qb[ng][kk][1] = v.y;
-          emax = max(emax, max(max((v.x >> 7) & 0xffu, (v.x >> 23) & 0xffu),
-                               max((v.y >> 7) & 0xffu, (v.y >> 23) & 0xffu)));
-        }
+      for (int kk = 0; kk < KS; ++kk) {
+        uint2 v = make_uint2(0u, 0u);
+        if (g < r.ncols) v = *reinterpret_cast<const uint2*>(qsm + (kk >> 1) * 32 + 4 * (kk & 1));
+        qb[kk][0] = v.x;
+        qb[kk][1] = v.y;
+        emax = max(emax, max(max((v.x >> 7) & 0xffu, (v.x >> 23) & 0xffu),
+                             max((v.y >> 7) & 0xffu, (v.y >> 23) & 0xffu)));
+      }
       emax = __reduce_max_sync(0xffffffffu, emax);
       const int sh = min(max(142 - (int)emax, -100), 100);  // 15 - (emax - 127)
       // (the score factor is positive, its sign in the queries: hidden scores stay -inf)
       const float up = copysignf(__int_as_float((127 + sh) << 23), a.scale_log2);
       slc = fmaxf(fabsf(a.scale_log2) * __int_as_float((127 - sh) << 23), 1e-36f);
 #pragma unroll
-      for (int ng = 0; ng < NG; ++ng)
+      for (int kk = 0; kk < KS; ++kk)
 #pragma unroll
-        for (int kk = 0; kk < KS; ++kk)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t v = qb[ng][kk][k];
-            qb[ng][kk][k] = pack_f16(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up);
-          }
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t v = qb[kk][k];
+          qb[kk][k] = pack_f16(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up);
+        }
       __syncwarp();
       if (lane == 0) mbar_arrive(qempty);
       ++ucount;
     }
-    float acc[MT][NG][4];
+    // O^T: m-tiles 2j and 2j + 1 are the elements of group j (mx_v_fragments)
+    float acc[MT][4];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int ng = 0; ng < NG; ++ng) acc[i][ng][0] = acc[i][ng][1] = acc[i][ng][2] = acc[i][ng][3] = 0.f;
+    for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
     // Softmax references m_r (-inf: none yet; mu is 0 then), lazy: a score may pass its
     // column's by kOver.  They are kept kLift below the scores that set them, so that P,
     // at most 2^kOver, has fp16's bits down to 2^-(14 + kLift) of the largest.
     constexpr float kLift = 5.f, kOver = 13.f;
-    float m_r[NG][2], mu[NG][2], l_r[NG][2];
-#pragma unroll
-    for (int ng = 0; ng < NG; ++ng)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        m_r[ng][e] = -INFINITY;
-        mu[ng][e] = l_r[ng][e] = 0.f;
-      }
+    float m_r[2] = {-INFINITY, -INFINITY}, mu[2] = {0.f, 0.f}, l_r[2] = {0.f, 0.f};
     // V scale references, one for each group of 32 elements (0, 1 and 2, 3): the largest
     // scale that the warp's tiles had so far.  V scales over them, at most 1, multiply P
     // in fp16 (exact powers of two, down to 2^-24); O is kept over them.
@@ -421,109 +457,72 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
     for (int tt = 0; tt < ntile_here; ++tt, ++it) {
       const int s = it % S;
       wait_or_abort(&full[s], (it / S) & 1, a.err, misc);
-      const int jt = tile_at<X>(r, t_begin + tt) * kKvTile;
+      const uint32_t st = smem_base + s * Cfg::kStageBytes;
+      const uint8_t* stp = smem + s * Cfg::kStageBytes;
+      const int jw = tile_at<X>(r, t_begin + tt) * kKvTile + R0;  // first KV row of this warp
+      const bool edge = (jw < r.lo_last) || (jw + Cfg::kRows - 1 > r.hi_first) || (MR && a.mask != nullptr);
+      if (X && !a.scores && (jw > r.hi || (jw >= a.first_tokens && jw + Cfg::kRows <= r.lo))) {
+        __syncwarp();  // no row sees any of them
+        if (lane == 0 && tt + 1 < ntile_here) mbar_arrive(&empty[s]);
+        continue;
+      }
       // ---------------- scales: a lane takes those of one row ----------------
-      float vfct[4] = {1.f, 1.f, 1.f, 1.f};  // what O's groups are multiplied by before this tile
-      bool vmove = false;
+      float vfct[4] = {1.f, 1.f, 1.f, 1.f};  // what O's groups are multiplied by
+      bool vmove;
       {
-        const uint32_t* sc = reinterpret_cast<const uint32_t*>(smem + s * Cfg::kStageBytes + Cfg::kOffScale) +
-                             R0 + lane;
-        uint32_t vw = sc[kKvTile];
+        const uint32_t* sc = reinterpret_cast<const uint32_t*>(stp + Cfg::kOffScale) + R0 + lane;
+        const uint32_t vw = gone(jw + lane) ? 0u : sc[kKvTile];
         float kf[4];  // (NaN: the row's scores are NaN)
         e8m0x4_to_f32x4(sc[0], kf);
         *reinterpret_cast<float4*>(smem + Cfg::kOffKs + (R0 + lane) * 16) = make_float4(kf[0], kf[1], kf[2], kf[3]);
-        if (jt + R0 + lane >= kvl || X) vw = gone(jt + R0 + lane) ? 0u : vw;
         __nv_bfloat162 v[2];
         e8m0x4_to_bf16x2x2(vw, v);
-        // (the larger of two drops a NaN)
-        const __nv_bfloat162 m0 = __hmax2(v[0], vref[0]), m1 = __hmax2(v[1], vref[1]);
-        const bool past = *reinterpret_cast<const uint32_t*>(&m0) != *reinterpret_cast<const uint32_t*>(&vref[0]) ||
-                          *reinterpret_cast<const uint32_t*>(&m1) != *reinterpret_cast<const uint32_t*>(&vref[1]);
-        if (__any_sync(0xffffffffu, past)) {
-          // new references: O moves by exact powers of two
-          vmove = true;
-          const uint32_t u[2] = {*reinterpret_cast<const uint32_t*>(&v[0]), *reinterpret_cast<const uint32_t*>(&v[1])};
-          const uint32_t o[2] = {*reinterpret_cast<const uint32_t*>(&vref[0]), *reinterpret_cast<const uint32_t*>(&vref[1])};
-          uint32_t en[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t c = (u[j >> 1] >> (16 * (j & 1)) & 0xffffu) >> 7;
-            const uint32_t old = (o[j >> 1] >> (16 * (j & 1)) & 0xffffu) >> 7;
-            en[j] = max(old, min(__reduce_max_sync(0xffffffffu, c == 255u ? 0u : c), (uint32_t)kMxRefMax));
-            // (a jump past 2^-126 leaves a negligible old sum and gives 0)
-            vfct[j] = __int_as_float(max(127 + (int)old - (int)en[j], 0) << 23);
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            vref[k] = mx_pair(en[2 * k] << 7, en[2 * k + 1] << 7);
-            vinv[k] = mx_pair((254 - en[2 * k]) << 7, (254 - en[2 * k + 1]) << 7);
-          }
-        }
-        float vf[4];
-        bf16x2x2_to_f32x4(__hmul2(v[0], vinv[0]), __hmul2(v[1], vinv[1]), vf);
-        // the other row of the pair: even lanes make groups 0 and 1, odd lanes 2 and 3
-        const uint32_t h01 = pack_f16(vf[0], vf[1]), h23 = pack_f16(vf[2], vf[3]);
-        const uint32_t theirs = __shfl_xor_sync(0xffffffffu, lane & 1 ? h01 : h23, 1);
-        const uint32_t even = lane & 1 ? theirs : h01, odd = lane & 1 ? h23 : theirs;
-        *reinterpret_cast<uint2*>(smem + Cfg::kOffVs + (R0 + lane) * 8) =
-            make_uint2(__byte_perm(even, odd, 0x5410), __byte_perm(even, odd, 0x7632));
+        vmove = mx_references(v, vref, vinv, vfct);
+        *reinterpret_cast<uint2*>(smem + Cfg::kOffVs + (R0 + lane) * 8) = mx_scale_pairs(v, vinv, lane);
         __syncwarp();
       }
-#pragma unroll 1
-      for (int R = R0; R < R0 + Cfg::kRows; R += kStep) {
-      const uint32_t st = smem_base + s * Cfg::kStageBytes + (R - R0) * Cfg::kRowBytes;
-      const uint8_t* stp = smem + s * Cfg::kStageBytes;
-      const int jw = jt + R;  // the step's first KV row
-      const bool edge = (jw < r.lo_last) || (jw + kStep - 1 > r.hi_first) || (MR && a.mask != nullptr);
-      if (X && !a.scores && (jw > r.hi || (jw >= a.first_tokens && jw + kStep <= r.lo)))
-        continue;  // no row sees any of them
       // ---------------- S^T = K Q^T ----------------
-      const float4* ks = reinterpret_cast<const float4*>(smem + Cfg::kOffKs) + R + g;
-      float x[NB][NG][4];
+      const float4* ks = reinterpret_cast<const float4*>(smem + Cfg::kOffKs) + R0 + g;
+      float x[NB][4];  // keys g, g, g + 8, g + 8; columns 2q, 2q + 1, ...
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        // the four scales of rows g and g + 8
         const float4 f0 = ks[16 * b], f1 = ks[16 * b + 8];
         const float fa[4] = {f0.x, f0.y, f0.z, f0.w}, fb[4] = {f1.x, f1.y, f1.z, f1.w};
-        // 8 elements of each row and group: d = 32*j + 8*q .. +7
-        uint32_t kw[2][4];
-        ldsm_x4(st + off01 + 1024 * b, kw[0][0], kw[0][1], kw[0][2], kw[0][3]);
-        ldsm_x4(st + off23 + 1024 * b, kw[1][0], kw[1][1], kw[1][2], kw[1][3]);
+        x[b][0] = x[b][1] = x[b][2] = x[b][3] = 0.f;
 #pragma unroll
-        for (int ng = 0; ng < NG; ++ng) x[b][ng][0] = x[b][ng][1] = x[b][ng][2] = x[b][ng][3] = 0.f;
+        for (int jj = 0; jj < 2; ++jj) {  // groups 2*jj, 2*jj + 1
+          uint32_t w[4];  // (group 2*jj: rows g, g + 8), (group 2*jj + 1: ...), d = 8*q .. +7 of each
+          ldsm_x4(st + off[jj] + 1024 * b, w[0], w[1], w[2], w[3]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t ka[2][4];
-          e2m1x8_to_f16x2x4(kw[j >> 1][2 * (j & 1)], ka[0][0], ka[0][2], ka[1][0], ka[1][2]);
-          e2m1x8_to_f16x2x4(kw[j >> 1][2 * (j & 1) + 1], ka[0][1], ka[0][3], ka[1][1], ka[1][3]);
-#pragma unroll
-          for (int ng = 0; ng < NG; ++ng) {
+          for (int k = 0; k < 2; ++k) {
+            const int j = 2 * jj + k;
+            uint32_t ka[2][4];
+            e2m1x8_to_f16x2x4(w[2 * k], ka[0][0], ka[0][2], ka[1][0], ka[1][2]);
+            e2m1x8_to_f16x2x4(w[2 * k + 1], ka[0][1], ka[0][3], ka[1][1], ka[1][3]);
             float s4[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(s4, ka[0], qb[ng][2 * j][0], qb[ng][2 * j][1]);
-            mma_f16(s4, ka[1], qb[ng][2 * j + 1][0], qb[ng][2 * j + 1][1]);
-            x[b][ng][0] += s4[0] * fa[j];
-            x[b][ng][1] += s4[1] * fa[j];
-            x[b][ng][2] += s4[2] * fb[j];
-            x[b][ng][3] += s4[3] * fb[j];
+            mma_f16(s4, ka[0], qb[2 * j][0], qb[2 * j][1]);
+            mma_f16(s4, ka[1], qb[2 * j + 1][0], qb[2 * j + 1][1]);
+            x[b][0] += s4[0] * fa[j];
+            x[b][1] += s4[1] * fa[j];
+            x[b][2] += s4[2] * fb[j];
+            x[b][3] += s4[3] * fb[j];
           }
         }
       }
       // ---------------- mask ----------------
       if (edge) {
-        const uint8_t* mk = stp + Cfg::kOffMask + R + g;
+        const uint8_t* mk = stp + Cfg::kOffMask + R0 + g;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int ng = 0; ng < NG; ++ng)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int e = k & 1, row = 16 * b + 8 * (k >> 1), j = jw + row + g;
-              bool ok = j >= loc[ng][e];
-              if (X) ok = ok || j < a.first_tokens;
-              ok = ok && j <= hic[ng][e];
-              if (MR && a.mask) ok = ok && mk[mrow[ng][e] + row] == 0;
-              if (!ok) x[b][ng][k] = -INFINITY;
-            }
+          for (int k = 0; k < 4; ++k) {
+            const int e = k & 1, row = 16 * b + 8 * (k >> 1), j = jw + row + g;
+            bool ok = j >= loc[e];
+            if (X) ok = ok || j < a.first_tokens;
+            ok = ok && j <= hic[e];
+            if (MR && a.mask) ok = ok && mk[mrow[e] + row] == 0;
+            if (!ok) x[b][k] = -INFINITY;
+          }
       }
       if (X && a.scores) {  // (decode_kernel: key weights)
         const int64_t base = ((int64_t)r.b * a.KVN + r.hk) * a.S_kv;
@@ -531,107 +530,78 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int ng = 0; ng < NG; ++ng)
-#pragma unroll
-            for (int k = 0; k < 4; k += 2) {
-              const int cl = ng * 8 + 2 * q4, j = jw + 16 * b + 4 * k + g;
-              if (cl < r.ncols && j < end)
-                *reinterpret_cast<float2*>(a.scores + (base + j) * a.score_cols + r.c0 + cl) =
-                    make_float2(x[b][ng][k] * slc, x[b][ng][k + 1] * slc);
-            }
+          for (int k = 0; k < 4; k += 2) {
+            const int j = jw + 16 * b + 4 * k + g;
+            if (2 * q4 < r.ncols && j < end)
+              *reinterpret_cast<float2*>(a.scores + (base + j) * a.score_cols + r.c0 + 2 * q4) =
+                  make_float2(x[b][k] * slc, x[b][k + 1] * slc);
+          }
       }
       // ---------------- online softmax per column ----------------
-      float top[NG][2];
+      float top[2];
       bool over = false;
 #pragma unroll
-      for (int ng = 0; ng < NG; ++ng)
+      for (int e = 0; e < 2; ++e) {
+        float mx = fmaxf(x[0][e], x[0][2 + e]);
+#pragma unroll
+        for (int b = 1; b < NB; ++b) mx = fmaxf(mx, fmaxf(x[b][e], x[b][2 + e]));
+        top[e] = mx * slc;
+        over |= top[e] > m_r[e] + kOver;
+      }
+      if (__any_sync(0xffffffffu, over) || vmove) {
+        float fct[2] = {1.f, 1.f};
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float mx = fmaxf(x[0][ng][e], x[0][ng][2 + e]);
-#pragma unroll
-          for (int b = 1; b < NB; ++b) mx = fmaxf(mx, fmaxf(x[b][ng][e], x[b][ng][2 + e]));
-          top[ng][e] = mx * slc;
-          over |= top[ng][e] > m_r[ng][e] + kOver;
-        }
-      if (__any_sync(0xffffffffu, over) || vmove) {
-        float fct[NG][2];
-#pragma unroll
-        for (int ng = 0; ng < NG; ++ng)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float mx = top[ng][e];
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float mold = m_r[ng][e];
-            fct[ng][e] = 1.f;
-            if (mx > mold + kOver) {
-              m_r[ng][e] = mu[ng][e] = mx - kLift;
-              fct[ng][e] = mold == -INFINITY ? 0.f : fast_exp2(mold - mu[ng][e]);
-              l_r[ng][e] *= fct[ng][e];
-            }
+          float mx = top[e];
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const float mold = m_r[e];
+          if (mx > mold + kOver) {
+            m_r[e] = mu[e] = mx - kLift;
+            fct[e] = mold == -INFINITY ? 0.f : fast_exp2(mold - mu[e]);
+            l_r[e] *= fct[e];
           }
+        }
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int ng = 0; ng < NG; ++ng) {
-            acc[i][ng][0] *= fct[ng][0] * vfct[i >> 1];
-            acc[i][ng][1] *= fct[ng][1] * vfct[i >> 1];
-            acc[i][ng][2] *= fct[ng][0] * vfct[i >> 1];
-            acc[i][ng][3] *= fct[ng][1] * vfct[i >> 1];
-          }
-        vmove = false;  // (once a tile)
-        vfct[0] = vfct[1] = vfct[2] = vfct[3] = 1.f;
+          for (int k = 0; k < 4; ++k) acc[i][k] *= fct[k & 1] * vfct[i >> 1];
       }
       // P^T in fp16, transposed: keys 2q, 2q+1 and 2q+8, 2q+9 of column g
-      uint32_t pt[NB][NG][2];
+      uint32_t pt[NB][2];
 #pragma unroll
-      for (int ng = 0; ng < NG; ++ng)
+      for (int b = 0; b < NB; ++b) {
+        float pr[4];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          float pr[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            pr[k] = fast_exp2(fmaf(x[b][ng][k], slc, -mu[ng][k & 1]));
-            l_r[ng][k & 1] += pr[k];
-          }
-          pt[b][ng][0] = movmatrix_t(pack_f16(pr[0], pr[1]));
-          pt[b][ng][1] = movmatrix_t(pack_f16(pr[2], pr[3]));
+        for (int k = 0; k < 4; ++k) {
+          pr[k] = fast_exp2(fmaf(x[b][k], slc, -mu[k & 1]));
+          l_r[k & 1] += pr[k];
         }
+        pt[b][0] = movmatrix_t(pack_f16(pr[0], pr[1]));
+        pt[b][1] = movmatrix_t(pack_f16(pr[2], pr[3]));
+      }
       // ---------------- O^T += V^T P^T ----------------
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         // the V scales of those keys, a pair for each group
-        const uint4* vp = reinterpret_cast<const uint4*>(smem + Cfg::kOffVs) + R / 2 + 8 * b + q4;
+        const uint4* vp = reinterpret_cast<const uint4*>(smem + Cfg::kOffVs) + R0 / 2 + 8 * b + q4;
         const uint4 s0 = vp[0], s1 = vp[4];
-        const uint32_t va0[4] = {s0.x, s0.y, s0.z, s0.w}, va1[4] = {s1.x, s1.y, s1.z, s1.w};
-        // A lane takes four elements d = 32*j + 4*g .. +3 of each group j (a 16-bit unit) of
-        // its keys 2q, 2q+1, 2q+8, 2q+9; m-tile 2j + h holds the elements 2h of them in its
-        // fragment rows 0-7, 2h + 1 in rows 8-15, so that an m-tile lies in one group.
-        const uint32_t vt = st + Cfg::kTileBytes + 1024 * b;
+        const uint32_t sa[4] = {s0.x, s0.y, s0.z, s0.w}, sb[4] = {s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
-        for (int jj = 0; jj < 2; ++jj) {  // groups 2*jj, 2*jj + 1
+        for (int jj = 0; jj < 2; ++jj) {
           uint32_t w[4];  // (group 2*jj: keys 2q, 2q+8), (keys 2q+1, 2q+9), (group 2*jj + 1: ...)
-          ldsm_x4_t(vt + (jj ? voff23 : voff01), w[0], w[1], w[2], w[3]);
+          ldsm_x4_t(st + Cfg::kTileBytes + voff[jj] + 1024 * b, w[0], w[1], w[2], w[3]);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int j = 2 * jj + k;
-            const uint32_t lo = w[2 * k], hi = w[2 * k + 1];
-            // bytes of two keys' codes of one element: 0, 2 (keys 2q, 2q+1), 0, 2 (2q+8, 2q+9)
-            const uint32_t ev = (lo & 0x0f0f0f0fu) | ((hi << 4) & 0xf0f0f0f0u);
-            const uint32_t od = ((lo >> 4) & 0x0f0f0f0fu) | (hi & 0xf0f0f0f0u);  // and 1, 3
-            uint32_t va[2][4];  // [m-tile of the two][fragment register]
-            e2m1x8_to_f16x2x4(ev, va[0][0], va[1][0], va[0][2], va[1][2]);
-            e2m1x8_to_f16x2x4(od, va[0][1], va[1][1], va[0][3], va[1][3]);
-#pragma unroll
-            for (int ng = 0; ng < NG; ++ng) {
-              const uint32_t b0 = mul_f16x2(pt[b][ng][0], va0[j]), b1 = mul_f16x2(pt[b][ng][1], va1[j]);
-              mma_f16(acc[2 * j][ng], va[0], b0, b1);
-              mma_f16(acc[2 * j + 1][ng], va[1], b0, b1);
-            }
+            uint32_t va[2][4];
+            mx_v_fragments(w[2 * k], w[2 * k + 1], va);
+            const uint32_t b0 = mul_f16x2(pt[b][0], sa[j]), b1 = mul_f16x2(pt[b][1], sb[j]);
+            mma_f16(acc[2 * j], va[0], b0, b1);
+            mma_f16(acc[2 * j + 1], va[1], b0, b1);
           }
         }
-      }
       }
       __syncwarp();
       if (lane == 0 && tt + 1 < ntile_here) mbar_arrive(&empty[s]);  // (the last: behind the merge)
@@ -639,30 +609,20 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
 
     // ---------------- merge the warps' states ----------------
 #pragma unroll
-    for (int ng = 0; ng < NG; ++ng) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float l = l_r[ng][e];
-        l += __shfl_xor_sync(0xffffffffu, l, 4);
-        l += __shfl_xor_sync(0xffffffffu, l, 8);
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        l_r[ng][e] = l;
-      }
-      if (g == 0)
-        *reinterpret_cast<float4*>(red_ml + (warp * 8 * NG + ng * 8 + 2 * q4) * 2) =
-            make_float4(m_r[ng][0], l_r[ng][0], m_r[ng][1], l_r[ng][1]);
+    for (int e = 0; e < 2; ++e) {
+      l_r[e] += __shfl_xor_sync(0xffffffffu, l_r[e], 4);
+      l_r[e] += __shfl_xor_sync(0xffffffffu, l_r[e], 8);
+      l_r[e] += __shfl_xor_sync(0xffffffffu, l_r[e], 16);
     }
+    if (g == 0)
+      *reinterpret_cast<float4*>(red_ml + (warp * 8 + 2 * q4) * 2) = make_float4(m_r[0], l_r[0], m_r[1], l_r[1]);
     named_bar_sync(1, 32 * W);
-    float Mh[NG][2], Lh[NG][2];
-    float back[4];
-    bf16x2x2_to_f32x4(vref[0], vref[1], back);
-#pragma unroll
-    for (int ng = 0; ng < NG; ++ng) {
+    float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f};
+    {
       float4 ml[W];  // (m, l) of this lane's two columns
-      float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f};
 #pragma unroll
       for (int w2 = 0; w2 < W; ++w2) {
-        ml[w2] = *reinterpret_cast<const float4*>(red_ml + (w2 * 8 * NG + ng * 8 + 2 * q4) * 2);
+        ml[w2] = *reinterpret_cast<const float4*>(red_ml + (w2 * 8 + 2 * q4) * 2);
         M[0] = fmaxf(M[0], ml[w2].x);
         M[1] = fmaxf(M[1], ml[w2].z);
       }
@@ -671,37 +631,32 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
         L[0] += ml[w2].x == -INFINITY ? 0.f : ml[w2].y * exp2f(ml[w2].x - M[0]);
         L[1] += ml[w2].z == -INFINITY ? 0.f : ml[w2].w * exp2f(ml[w2].z - M[1]);
       }
+      float back[4];
+      bf16x2x2_to_f32x4(vref[0], vref[1], back);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        Mh[ng][e] = M[e];
-        Lh[ng][e] = L[e];
-        const float f = m_r[ng][e] == -INFINITY ? 0.f : exp2f(m_r[ng][e] - M[e]);
+        const float f = m_r[e] == -INFINITY ? 0.f : exp2f(m_r[e] - M[e]);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-          acc[i][ng][e] *= f * back[i >> 1];
-          acc[i][ng][2 + e] *= f * back[i >> 1];
+          acc[i][e] *= f * back[i >> 1];
+          acc[i][2 + e] *= f * back[i >> 1];
         }
       }
     }
-    float4* red4 = reinterpret_cast<float4*>(smem + (it + S - 1) % S * Cfg::kStageBytes);
     // Warp w ends with m-tiles 2w and 2w + 1 (the elements of group w) summed over the
     // warps: in each of two rounds every warp stores the four m-tiles 2k + round but its
-    // own, then adds the others' copies to its own.
-    const int64_t slot = min(max(slot0, (int64_t)0), a.max_chunks - 1);
-    const int64_t pstride = (int64_t)a.GH * (D + 2);
-#pragma unroll
-    for (int ng = 0; ng < NG; ++ng) {
-      float4 own[2];  // (d, column 2q), (d, 2q+1), (d+1, 2q), (d+1, 2q+1), d = 32 warp + 4 g + 2 rnd
+    // own, in the chunk's last stage, then adds the others' copies to its own.
+    float4 own[2];  // (d, column 2q), (d, 2q+1), (d+1, 2q), (d+1, 2q+1), d = 32 warp + 4 g + 2 round
+    own[0] = own[1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (ntile_here > 0) {  // (else no stage, and nothing to add up)
+      const int s = (it + S - 1) % S;
+      float4* red4 = reinterpret_cast<float4*>(smem + s * Cfg::kStageBytes);
 #pragma unroll
       for (int rnd = 0; rnd < 2; ++rnd) {
-        if (ntile_here == 0) {  // (no stage, and nothing to add up)
-          own[rnd] = make_float4(0.f, 0.f, 0.f, 0.f);
-          continue;
-        }
-        if (ng > 0 || rnd > 0) named_bar_sync(1, 32 * W);  // the round before has been read
+        if (rnd > 0) named_bar_sync(1, 32 * W);  // the round before has been read
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float (&c)[4] = acc[2 * k + rnd][ng];
+          const float (&c)[4] = acc[2 * k + rnd];
           const float4 mine = make_float4(c[0], c[1], c[2], c[3]);
           if (k == warp) own[rnd] = mine;
           else red4[(k * W + warp) * 32 + lane] = mine;
@@ -714,45 +669,43 @@ __global__ void __launch_bounds__(MxCfg<NG, MR>::kThreads, MxCfg<NG, MR>::kCtas)
           own[rnd].x += o.x; own[rnd].y += o.y; own[rnd].z += o.z; own[rnd].w += o.w;
         }
       }
-      if (ng == NG - 1 && ntile_here > 0) {  // the stage goes back
-        fence_proxy_async_smem();  // (the merge wrote it; a copy will)
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[(it + S - 1) % S]);
-      }
-      const int d = 32 * warp + 4 * g;
+      fence_proxy_async_smem();  // (the stage was written here; a copy will write it next)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+    }
+    const int64_t slot = min(max(slot0, (int64_t)0), a.max_chunks - 1);
+    const int d = 32 * warp + 4 * g;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int hh = ng * 8 + 2 * q4 + e;  // the unit's column
-        if (hh >= r.ncols) continue;
-        const float4 o = e ? make_float4(own[0].y, own[0].w, own[1].y, own[1].w)
-                           : make_float4(own[0].x, own[0].z, own[1].x, own[1].z);
-        if (!split) {
-          const int c = r.c0 + hh;
-          const int i = c / a.G, h = r.hk * a.G + (c - i * a.G);
-          const int64_t tok = (int64_t)r.qrow0 + i;
-          float scl, lse;
-          finish_head(a, h, Mh[ng][e], Lh[ng][e], &scl, &lse);
-          *reinterpret_cast<uint2*>(a.out + tok * a.out_stride + (int64_t)h * D + d) =
-              make_uint2(pack_bf16(o.x * scl, o.y * scl), pack_bf16(o.z * scl, o.w * scl));
-          if (a.lse && warp == 0 && g == 0)
-            a.lse[a.layout == 1 ? tok * a.QN + h : ((int64_t)r.b * a.QN + h) * a.S_q + i] = lse;
-        } else {
-          // (the slot is clamped, as in decode_kernel; rows of D + 2 floats: 8-byte stores)
-          float* col = a.partials + slot * pstride + (int64_t)hh * (D + 2);
-          *reinterpret_cast<float2*>(col + d) = make_float2(o.x, o.y);
-          *reinterpret_cast<float2*>(col + d + 2) = make_float2(o.z, o.w);
-          if (warp == 0 && g == 0)
-            *reinterpret_cast<float2*>(col + D) = make_float2(Mh[ng][e], Lh[ng][e]);
-        }
+    for (int e = 0; e < 2; ++e) {
+      const int hh = 2 * q4 + e;  // the unit's column
+      if (hh >= r.ncols) continue;
+      const float4 o = e ? make_float4(own[0].y, own[0].w, own[1].y, own[1].w)
+                         : make_float4(own[0].x, own[0].z, own[1].x, own[1].z);
+      if (!split) {
+        const int c = r.c0 + hh;
+        const int i = c / a.G, h = r.hk * a.G + (c - i * a.G);
+        const int64_t tok = (int64_t)r.qrow0 + i;
+        float scl, lse;
+        finish_head(a, h, M[e], L[e], &scl, &lse);
+        *reinterpret_cast<uint2*>(a.out + tok * a.out_stride + (int64_t)h * D + d) =
+            make_uint2(pack_bf16(o.x * scl, o.y * scl), pack_bf16(o.z * scl, o.w * scl));
+        if (a.lse && warp == 0 && g == 0)
+          a.lse[a.layout == 1 ? tok * a.QN + h : ((int64_t)r.b * a.QN + h) * a.S_q + i] = lse;
+      } else {
+        // (the slot is clamped, as in decode_kernel; rows of D + 2 floats: 8-byte stores)
+        float* col = a.partials + slot * (int64_t)a.GH * (D + 2) + (int64_t)hh * (D + 2);
+        *reinterpret_cast<float2*>(col + d) = make_float2(o.x, o.y);
+        *reinterpret_cast<float2*>(col + d + 2) = make_float2(o.z, o.w);
+        if (warp == 0 && g == 0) *reinterpret_cast<float2*>(col + D) = make_float2(M[e], L[e]);
       }
     }
   }
 }
 
-template <int NG, bool MR, bool X>
+template <bool MR, bool X>
 cudaError_t launch_mx_t(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
-  using Cfg = MxCfg<NG, MR>;
-  auto kern = decode_mx_kernel<NG, MR, X>;
+  using Cfg = MxCfg<MR>;
+  auto kern = decode_mx_kernel<MR, X>;
   static std::atomic<uint64_t> done_mask[4];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -766,21 +719,16 @@ cudaError_t launch_mx_t(const DecodeArgs& a, const CUtensorMap& tk, const CUtens
   return launch_pdl(kern, dim3(a.num_ctas), dim3(Cfg::kThreads), Cfg::kSmem, s, a, tk, tv);
 }
 
-template <int NG>
-cudaError_t launch_mx_ng(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
-  const bool mr = a.S_max > 1 || a.mask != nullptr;
-  if (a.first_tokens > 0 || a.scores)
-    return mr ? launch_mx_t<NG, true, true>(a, tk, tv, s) : launch_mx_t<NG, false, true>(a, tk, tv, s);
-  return mr ? launch_mx_t<NG, true, false>(a, tk, tv, s) : launch_mx_t<NG, false, false>(a, tk, tv, s);
-}
-
 }  // namespace
 
-int decode_mx_ctas(int GH) { return GH > 8 ? MxCfg<2, false>::kCtas : MxCfg<1, false>::kCtas; }
+int decode_mx_ctas() { return MxCfg<false>::kCtas; }
 
 static cudaError_t launch_decode_mx(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
                                     cudaStream_t s) {
-  return a.GH > 8 ? launch_mx_ng<2>(a, tk, tv, s) : launch_mx_ng<1>(a, tk, tv, s);
+  const bool mr = a.S_max > 1 || a.mask != nullptr;
+  if (a.first_tokens > 0 || a.scores)
+    return mr ? launch_mx_t<true, true>(a, tk, tv, s) : launch_mx_t<false, true>(a, tk, tv, s);
+  return mr ? launch_mx_t<true, false>(a, tk, tv, s) : launch_mx_t<false, false>(a, tk, tv, s);
 }
 
 }  // namespace fia

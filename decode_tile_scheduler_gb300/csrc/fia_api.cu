@@ -245,9 +245,9 @@ fia_status decode_plan(const fia_params* p, DecodePlan* pl) {
   if (st != FIA_OK) return st;
   const int G = p->num_q_heads / p->num_kv_heads;
   const int cols = p->max_seqlen_q * G;  // (query row, head) columns of a KV head
-  const int GH = decode_group_heads(p->max_seqlen_q, cols);
+  const int GH = decode_group_heads(p->max_seqlen_q, cols, p->kv_dtype == FIA_KV_MXFP4);
   const int HG = (int)ceil_div(cols, GH);
-  if (p->kv_dtype == FIA_KV_MXFP4) n *= decode_mx_ctas(GH);  // (several CTAs to an SM)
+  if (p->kv_dtype == FIA_KV_MXFP4) n *= decode_mx_ctas();  // (several CTAs to an SM)
   pl->n = n;
   pl->U = (int64_t)p->batch * p->num_kv_heads * HG;
   pl->W = decode_chunks_per_cta(p);
@@ -274,7 +274,7 @@ DecodeArgs decode_args(const fia_params* p, const DecodePlan& pl, void* ws) {
   a.KVN = p->num_kv_heads;
   a.D = p->head_dim;
   a.G = G;
-  a.GH = decode_group_heads(p->max_seqlen_q, p->max_seqlen_q * G);
+  a.GH = decode_group_heads(p->max_seqlen_q, p->max_seqlen_q * G, p->kv_dtype == FIA_KV_MXFP4);
   a.HG = (int)ceil_div(p->max_seqlen_q * G, a.GH);
   a.layout = p->layout;
   a.S_q = p->layout == FIA_LAYOUT_BSND ? p->max_seqlen_q : 1;
@@ -343,10 +343,11 @@ fia_status kv_maps(const fia_params* p, int box_rows, CUtensorMap* tk, CUtensorM
   const CUtensorMapSwizzle swizzle = mx ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
   // One head's slice of a token is D * esize bytes: 256 for bf16 D=128 (two
   // 128-byte boxes, so a 256-byte L2 fill is used in full) but 128 for FP8,
-  // where a 256-byte fill would also drag in the next head's slice.
-  const CUtensorMapL2promotion promo = dim * es >= 256
-                                           ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
-                                           : CU_TENSOR_MAP_L2_PROMOTION_L2_128B;
+  // where a 256-byte fill would also drag in the next head's slice, and 64 for MXFP4
+  // (4 x 32 to 128 k keys 92 us, with 128-byte fills 100, with 256-byte ones 106).
+  const CUtensorMapL2promotion promo = dim * es >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                       : dim * es >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                         : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
   fia_status st = make_map(tk, p->k_cache, dt, es, cols, rows ? rows : 1, bc, (uint32_t)box_rows,
                            cols, promo, swizzle);
   if (st != FIA_OK) return st;
@@ -751,8 +752,7 @@ fia_status execute_decode(const fia_params* p, void* ws, cudaStream_t s, bool pl
   fia_status st = decode_plan(p, &pl);
   if (st != FIA_OK) return st;
   DecodeArgs a = decode_args(p, pl, ws);
-  // (the kernel of few units takes no MXFP4 cache)
-  if (p->kv_dtype != FIA_KV_MXFP4 && decode_is_few(a, w != nullptr))
+  if (decode_is_few(a, p->kv_dtype == FIA_KV_MXFP4, w != nullptr))
     return launch_decode_few(a, cache_of(p), w, planned, s) == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
   a.scores = scores;
   a.score_cols = cols;

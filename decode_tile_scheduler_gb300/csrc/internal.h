@@ -35,7 +35,10 @@ constexpr int kDecodeMaxRows = 16; // query rows per sequence the decode kernel 
 // 4-row GQA-4 decode: 92.2 against 100.4 us per execute while 16-column
 // units spilled registers; the same, 88.0 against 88.2 us, once the
 // consumers had 208 registers).
-inline int decode_group_heads(int rows, int cols) { return (rows == 1 && cols > 8) ? 16 : 8; }
+// (MXFP4: always 8; decode_mx.cuh tells why.)
+inline int decode_group_heads(int rows, int cols, bool mx) {
+  return rows == 1 && cols > 8 && !mx ? 16 : 8;
+}
 
 // Whether two arrays of `rows` rows, `stride` 4-byte elements apart, share an element
 // of the rows' first `cap`.  The same array twice is no overlap: calls may write
@@ -203,9 +206,9 @@ cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& tk, const CUte
 // Whether a call has few units and few keys (a rule on sizes), and its one kernel:
 // `planned` if it has to find a plan in the workspace, else the plan's launch goes
 // before it and need not be done.
-bool decode_is_few(const DecodeArgs& a, bool weights);
-// CTAs of the MXFP4 decode kernel to an SM, for units of up to GH columns.
-int decode_mx_ctas(int GH);
+bool decode_is_few(const DecodeArgs& a, bool mx, bool weights);
+// CTAs of the MXFP4 decode kernel to an SM.
+int decode_mx_ctas();
 cudaError_t launch_decode_few(const DecodeArgs& a, const fia_kv_cache& cache, const KeyWeightsOut* w,
                               bool planned, cudaStream_t s);
 size_t decode_smem_bytes(int D, int fp8);

@@ -181,7 +181,8 @@ typedef struct fia_params {
     int32_t pre_tokens;       /* band: keys before p (may be negative)         */
     int32_t next_tokens;      /* band: keys after p;  pre + next >= 0          */
     const float *sinks;       /* fp32 [Q_N] or NULL                            */
-    int32_t num_sms;          /* persistent CTAs; 0 = the device's SM count    */
+    int32_t num_sms;          /* persistent CTAs (decode over MXFP4: a third    */
+                              /* of them); 0 = the device's SM count           */
     int32_t kv_layout;        /* FIA_KV_LAYOUT_* (paged caches)                */
     const uint8_t *atten_mask;    /* modes 0/1: int8/uint8/bool bytes, nonzero  */
                               /* = masked out; element (b, i, j) at            */
@@ -606,14 +607,15 @@ fia_status fia_selftest_bounded_wait(int32_t *status, uint64_t limit_ns, void *s
  *
  * Decode schedule (written by fia_plan): the columns of a KV head are its
  * (query row, query head) pairs, S*G of them (S = max_seqlen_q <= 16), taken
- * in groups of GH = 16 (S = 1 and G > 8) or 8 (otherwise); work unit
+ * in groups of GH = 16 (S = 1 and G > 8, not MXFP4), else 8; work unit
  * u = (b, kv head, group),
  * UPB = KV_N * ceil(S*G/GH) units per batch, of which the first
  * A(b) = KV_N * ceil(q_len(b)*G/GH) hold columns of batch b ("active", active
  * index a).  Cost of an active unit = KV tiles (128 positions) its rows see
  * together, at least 1 (0 when the batch has no query row).  With T the total
- * cost, n CTAs and W = 5 chunks per CTA, C = max(1, ceil(T / (n W))) and
- * c2 = ceil(C / k), k = 2 for a bf16 cache and S = 1, else 1.  A unit of
+ * cost, n CTAs and W = 5 chunks per CTA (MXFP4: three CTAs to each of num_sms, W = 2),
+ * C = max(1, ceil(T / (n W))) and c2 = ceil(C / k), k = 2 for a bf16 cache and S = 1,
+ * else 1.  A unit of
  * cost c gets n1 = max(0, floor(c/C) - 1) chunks of C tiles, then chunks of
  * c2 tiles over the rest (at most 2k), so n W + 2k U bounds the chunks of U
  * units.  (A band with first_tokens and U >= n / 8: units of c_max tiles at most, cut in s
