@@ -440,6 +440,7 @@ DequantArgs dequant_args(const fia_params* p, const PrefillPlan& pl, void* ws) {
   d.block_table = p->block_table;
   d.max_blocks = p->max_blocks_per_seq;
   d.block_size = p->block_table ? p->block_size : 1;
+  fast_divisor(d.block_size, &d.bs_magic, &d.bs_shift);
   d.num_blocks = p->num_blocks;
   d.seqused_kv = p->seqused_kv;
   char* w = static_cast<char*>(ws);
@@ -793,7 +794,7 @@ fia_status execute(const fia_params* p, void* ws, size_t ws_bytes, void* stream,
       int n;
       st = sm_count(p->num_sms, &n);
       if (st != FIA_OK) return st;
-      if (launch_kv_dequant(dequant_args(p, pp, ws), n, s) != cudaSuccess) return FIA_ERR_CUDA;
+      if (launch_kv_dequant(dequant_args(p, pp, ws), n, !planned, s) != cudaSuccess) return FIA_ERR_CUDA;
     }
     return launch_prefill(a, tq, tk, tv, s) == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
   }

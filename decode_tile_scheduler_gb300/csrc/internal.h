@@ -228,6 +228,8 @@ struct DequantArgs {
   const float* v_scale;
   const int32_t* block_table;  // null: contiguous [B, cap, KVN, D]
   int max_blocks, block_size;
+  uint32_t bs_magic;           // j / block_size == (j * bs_magic) >> bs_shift, 0 <= j < 2^31
+  int bs_shift;
   int64_t num_blocks;
   const int32_t* seqused_kv;   // null: cap for every batch
   uint16_t* k_out;
@@ -242,7 +244,8 @@ struct DequantArgs {
   int first_tokens, pre_tokens, next_tokens, S_q;
   const int32_t* cu_seqlens_q; // null: S_q rows per sequence
 };
-cudaError_t launch_kv_dequant(const DequantArgs& a, int num_sms, cudaStream_t s);
+// `beside_plan`: the launch before it on the stream is the plan's (MXFP4 starts at once).
+cudaError_t launch_kv_dequant(const DequantArgs& a, int num_sms, bool beside_plan, cudaStream_t s);
 cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& tq, const CUtensorMap& tk,
                            const CUtensorMap& tv, cudaStream_t s);
 

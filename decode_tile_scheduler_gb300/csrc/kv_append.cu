@@ -71,14 +71,14 @@ __device__ __forceinline__ void store_fp8(uint8_t* dst, float* scale_dst, const 
   if (first) *scale_dst = scale;
 }
 
-// Whether one of the eight bf16 values of x is a NaN.
-__device__ __forceinline__ bool any_nan(const uint4& x) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  bool n = false;
+// The largest magnitude bits among the 16 bf16 values of a and b: bf16 magnitudes order
+// as integers, with NaN above infinity.
+__device__ __forceinline__ uint32_t top16(const uint4& a, const uint4& b) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t m = 0u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    n = n || (w[i] & 0x7fffu) > 0x7f80u || (w[i] & 0x7fff0000u) > 0x7f800000u;
-  return n;
+  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+  return max(m >> 16, m & 0xffffu);
 }
 
 // Infinities as the largest finite values of their sign.
@@ -101,17 +101,16 @@ __device__ __forceinline__ uint32_t quant8_mx(const uint4& x, float inv) {
 // The same as E2M1 codes: lanes 2k and 2k + 1 hold one tile of 32.
 __device__ __forceinline__ void store_mx(uint8_t* dst, uint8_t* scale_dst, uint4 a, uint4 b, bool ok,
                                          bool first) {
-  float m = amax16(a, b);
-  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  if (m > kBf16Max) {  // (saturated at 6, they would be half as large again)
+  uint32_t m = top16(a, b);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  if (!ok) return;
+  if (m == 0x7f80u) {  // infinities (saturated at 6, they would be half as large again)
     a = finite8(a);
     b = finite8(b);
-    m = kBf16Max;
+    m = 0x7f7fu;
   }
-  int nan = any_nan(a) || any_nan(b);
-  nan |= __shfl_xor_sync(0xffffffffu, nan, 1);
-  if (!ok) return;
-  const int e = nan ? 255 : mx_scale(m);
+  const bool nan = m > 0x7f80u;
+  const int e = nan ? 255 : mx_scale(__uint_as_float(m << 16));
   uint2 codes = make_uint2(0u, 0u);
   if (!nan) codes = make_uint2(quant8_mx(a, mx_inverse(e)), quant8_mx(b, mx_inverse(e)));
   *reinterpret_cast<uint2*>(dst) = codes;

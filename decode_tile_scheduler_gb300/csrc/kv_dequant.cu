@@ -44,12 +44,13 @@ __device__ __forceinline__ bool locate(const DequantArgs& a, int b, int j, int h
                                        int64_t* code_off, int64_t* scale_row) {
   // (code_off in elements)
   if (a.block_table) {
-    const int64_t blk = a.block_table[(int64_t)b * a.max_blocks + j / a.block_size];
+    const int pg = (int)(((uint64_t)(uint32_t)j * a.bs_magic) >> a.bs_shift);
+    const int64_t blk = a.block_table[(int64_t)b * a.max_blocks + pg];
     if (blk < 0 || blk >= a.num_blocks) {
       if (a.debug) atomicExch(a.err, 3);
       return false;
     }
-    const int jp = j % a.block_size;
+    const int jp = j - pg * a.block_size;
     *code_off = a.kv_layout == 1 ? ((blk * a.KVN + hk) * a.block_size + jp) * a.D + d0
                                  : ((blk * a.block_size + jp) * a.KVN + hk) * a.D + d0;
     *scale_row = (blk * a.KVN + hk) * a.block_size + jp;
@@ -173,59 +174,69 @@ __global__ void __launch_bounds__(256) kv_dequant_kernel(const DequantArgs a) {
   }
 }
 
-// A thread takes the 32 elements of one scale: 16 bytes of codes, 64 bytes of bf16.
-__global__ void __launch_bounds__(256) mx_dequant_kernel(const DequantArgs a) {
-  const int groups = a.D / 32, per_row = a.KVN * groups;
-  const int64_t total = (int64_t)a.B * a.cap * per_row;
-  for (int64_t t = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; t < total;
-       t += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t bj = t / per_row;
-    const int rest = (int)(t - bj * per_row);
-    const int b = (int)(bj / a.cap);
-    const int j = (int)(bj - (int64_t)b * a.cap);
-    const int kv_len = a.seqused_kv ? a.seqused_kv[b] : a.cap;
-    if (j >= kv_len) continue;
-    const KeyUse use = key_use(a, b, kv_len, j);
-    if (use == kLeft) continue;
-    const int hk = rest / groups, gr = rest % groups;
-    int64_t code_off, scale_row;
-    const bool there = use == kUsed && locate(a, b, j, hk, 32 * gr, &code_off, &scale_row);
-    const int64_t out_off = (((int64_t)b * a.cap + j) * a.KVN + hk) * a.D + 32 * gr;
+// A block takes `rows` keys of a sequence, about 64 (key, head) vectors, a half-warp two of
+// them at once: 64 bytes of codes, four scales, 256 bytes of bf16 in 16-byte pieces of K and
+// of V each.  (Blocks of 512 vectors, eight rounds of these, 36.9 us for 15 k keys of 8
+// heads: each round is a chain of page, codes and stores.)
+__global__ void __launch_bounds__(256, 6) mx_dequant_kernel(const DequantArgs a, int rows, int blocks) {
+  constexpr int U = 2;
+  const int b = blockIdx.x / blocks, j0 = (blockIdx.x - b * blocks) * rows;
+  const int kv_len = min(a.seqused_kv ? a.seqused_kv[b] : a.cap, a.cap);
+  const int vectors = min(rows, kv_len - j0) * a.KVN, piece = threadIdx.x & 15;
+  for (int v0 = threadIdx.x >> 4; v0 < vectors; v0 += 16 * U) {
+    uint32_t code[2][U], scale[2][U];
+    KeyUse use[U];
+    int64_t to[U];
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      uint4* dst = reinterpret_cast<uint4*>((kv ? a.v_out : a.k_out) + out_off);
-      uint4 c = make_uint4(0u, 0u, 0u, 0u);  // zeros, not what an earlier call left there
-      uint32_t e = 127;
-      if (there) {
-        c = __ldg(reinterpret_cast<const uint4*>((kv ? a.v : a.k) + code_off / 2));
-        e = __ldg(reinterpret_cast<const uint8_t*>(kv ? a.v_scale : a.k_scale) + scale_row * groups + gr);
+    for (int u = 0; u < U; ++u) {
+      const int v = v0 + 16 * u, row = v / a.KVN, j = j0 + row, hk = v - row * a.KVN;
+      use[u] = v < vectors ? key_use(a, b, kv_len, j) : kLeft;
+      code[0][u] = code[1][u] = 0u;  // zeros, not what an earlier call left there
+      scale[0][u] = scale[1][u] = 127u;
+      to[u] = (((int64_t)b * a.cap + j) * a.KVN + hk) * a.D + 8 * piece;
+      int64_t from, srow;
+      if (use[u] == kUsed && locate(a, b, j, hk, 8 * piece, &from, &srow)) {
+        code[0][u] = __ldg(reinterpret_cast<const uint32_t*>(a.k + from / 2));
+        code[1][u] = __ldg(reinterpret_cast<const uint32_t*>(a.v + from / 2));
+        scale[0][u] = __ldg(reinterpret_cast<const uint8_t*>(a.k_scale) + 4 * srow + piece / 4);
+        scale[1][u] = __ldg(reinterpret_cast<const uint8_t*>(a.v_scale) + 4 * srow + piece / 4);
       }
-      const float sc = e == 255 ? __int_as_float(0x7fffffff) : __int_as_float(e ? e << 23 : 1u << 22);
-      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+    for (int u = 0; u < U; ++u) {
+      if (use[u] == kLeft) continue;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t e = scale[kv][u];
+        const float sc = e == 255u ? __int_as_float(0x7fffffff) : __int_as_float(e ? e << 23 : 1u << 22);
         uint32_t p[4], o[4];
-        e2m1x8_to_f16x2x4(w[i], p[0], p[1], p[2], p[3]);
+        e2m1x8_to_f16x2x4(code[kv][u], p[0], p[1], p[2], p[3]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[k]));
           o[k] = pack_bf16(f.x * sc, f.y * sc);
         }
-        dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<uint4*>((kv ? a.v_out : a.k_out) + to[u]) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }
+  // (beside the plan's launch: what waits for this kernel waits for the plan too)
+  pdl_wait();
 }
 
 }  // namespace
 
-cudaError_t launch_kv_dequant(const DequantArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t launch_kv_dequant(const DequantArgs& a, int num_sms, bool beside_plan, cudaStream_t s) {
   if (a.mx) {
-    const int64_t total = (int64_t)a.B * a.cap * a.KVN * (a.D / 32);
-    if (total > 0) {
-      const int grid = (int)std::min<int64_t>((total + 255) / 256, (int64_t)num_sms * 32);
-      mx_dequant_kernel<<<grid, 256, 0, s>>>(a);
-    }
+    const int rows = (63 + a.KVN) / a.KVN;
+    const int64_t blocks = (a.cap + rows - 1) / rows, grid = blocks * a.B;
+    if (grid == 0) return cudaSuccess;
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    // (behind the plan's own launch it need not wait: that one began after all before it;
+    // with FIA_DEBUG both write the error word)
+    if (beside_plan && !a.debug)
+      return launch_pdl(mx_dequant_kernel, dim3((unsigned)grid), dim3(256), 0, s, a, rows, (int)blocks);
+    mx_dequant_kernel<<<(unsigned)grid, 256, 0, s>>>(a, rows, (int)blocks);
     return cudaGetLastError();
   }
   cudaError_t e = cudaMemsetAsync(a.smax, 0, sizeof(uint32_t) * 2 * (size_t)a.B * a.KVN, s);

@@ -5,8 +5,10 @@
 // Memory-bound: every element is read once and written once.  A head's D / 8 lanes
 // take 16 bytes each; the sum of squares is joined by shuffles, the other value of a
 // rotated pair comes from the lane D's half away as the 16 bytes that it loaded.  A warp
-// keeps its token, and with it the cosines and sines and both weights, for kHeads
-// rounds of heads, whose loads are in flight together.
+// keeps its token and one kind of head (query, key, value) for kRounds rounds of heads,
+// whose loads are in flight together: weights times cosines and weights times sines are
+// made once for all of them, which leaves an element a product, a product and sum, and
+// the head's factor, in packed pairs of fp32.
 #include <cmath>
 
 #include "kv_cache.cuh"
@@ -16,7 +18,7 @@ namespace fia {
 
 namespace {
 
-constexpr int kRounds = 4;  // rounds of heads a warp takes
+constexpr int kRounds = 4, kThreads = 128;  // rounds of heads a warp takes; of a block
 
 struct RopeArgs {
   CacheView c;
@@ -35,7 +37,7 @@ struct RopeArgs {
   int32_t* status;
   int unit;              // rows of a page, or of a contiguous cache's sequence
   int64_t pool;          // rows of the cache
-  int groups;            // warps of a token
+  int q_groups, kv_groups, groups;  // warps of a token's queries, of its keys (values), in all
 };
 
 __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
@@ -45,6 +47,27 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
     x[2 * i] = __uint_as_float(u[i] << 16);
     x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
   }
+}
+// Pairs of fp32 in one instruction.
+union Pair {
+  float f[2];
+  unsigned long long u;
+};
+__device__ __forceinline__ Pair pair_of(uint32_t w) {  // two bf16
+  Pair p;
+  p.f[0] = __uint_as_float(w << 16);
+  p.f[1] = __uint_as_float(w & 0xffff0000u);
+  return p;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.u) : "l"(a.u), "l"(b.u));
+  return d;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.u) : "l"(a.u), "l"(b.u), "l"(c.u));
+  return d;
 }
 
 __device__ __forceinline__ uint4 pack8(const float (&y)[8]) {
@@ -95,128 +118,156 @@ __device__ __forceinline__ void store_row(uint8_t* pool, float* scales, int64_t 
 }
 
 template <int D, int F, bool PAIRS>
-__global__ void __launch_bounds__(256) norm_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 8) norm_rope_kernel(const RopeArgs a) {
   constexpr int L = D / 8, H = 32 / L;  // lanes of a head, heads side by side
   const int lane = threadIdx.x & 31, chunk = lane % L;
-  const uint32_t w = blockIdx.x * 8u + (threadIdx.x >> 5);
-  const uint32_t t = w / (uint32_t)a.groups, grp = w - t * a.groups;
+  const uint32_t w = blockIdx.x * (kThreads / 32u) + (threadIdx.x >> 5);
+  const uint32_t t = w / (uint32_t)a.groups;
+  int grp = (int)(w - t * a.groups);
   if (t >= (uint32_t)a.T) return;  // whole warps
-  const int KVN = a.c.KVN, heads = a.QN + 2 * KVN;
-  const int h0 = (int)grp * (kRounds * H) + lane / L;
-  // the heads' loads first
+  // the warp's kind of head, and its first one
+  const int KVN = a.c.KVN;
+  const int kind = grp < a.q_groups ? 0 : grp < a.q_groups + a.kv_groups ? 1 : 2;
+  const int heads = kind == 0 ? a.QN : KVN;
+  grp -= kind == 0 ? 0 : a.q_groups + (kind - 1) * a.kv_groups;
+  const int h0 = grp * (kRounds * H) + lane / L;
+  const uint16_t* src = kind == 0 ? a.q + t * a.q_stride : kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride;
+  src += (int64_t)h0 * D + 8 * chunk;
   uint4 x[kRounds];
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) {
-    const int h = h0 + r * H;
     x[r] = make_uint4(0u, 0u, 0u, 0u);
-    if (h < heads) {
-      const uint16_t* src = h < a.QN ? a.q + t * a.q_stride + (int64_t)h * D
-                            : h < a.QN + KVN ? a.k + t * a.k_stride + (int64_t)(h - a.QN) * D
-                                             : a.v + t * a.v_stride + (int64_t)(h - a.QN - KVN) * D;
-      x[r] = *(reinterpret_cast<const uint4*>(src) + chunk);
-    }
+    if (h0 + r * H < heads) x[r] = *reinterpret_cast<const uint4*>(src + r * H * D);
   }
   const int position = __ldg(a.positions + t), slot = __ldg(a.slots + t);
-  const bool inside = slot >= 0 && slot < a.pool;
   if (position < 0 || (position >= a.P && a.rot > 0)) {
     if (position >= 0 && lane == 0 && a.status) atomicExch(a.status, 3);
     return;
   }
+  const bool inside = slot >= 0 && slot < a.pool;
   if (!inside && lane == 0 && a.status) atomicExch(a.status, 3);
-  const int page = inside ? slot / a.unit : 0, in_page = inside ? slot - page * a.unit : 0;
-
-  // the rotation of this lane's eight elements: y' = y cos + other * sin, with the sine's
-  // sign of the pair's half in it
-  const int half = a.rot / 2, e0 = 8 * chunk;
-  const bool turned = e0 < a.rot;
-  float cs[8], sn[8];
-  if (turned) {
-    const float* row = a.cos_sin + (int64_t)position * a.rot;
-    if constexpr (PAIRS) {
-      const float4 c4 = __ldg(reinterpret_cast<const float4*>(row + e0 / 2));
-      const float4 s4 = __ldg(reinterpret_cast<const float4*>(row + half + e0 / 2));
-      cs[0] = cs[1] = c4.x; cs[2] = cs[3] = c4.y; cs[4] = cs[5] = c4.z; cs[6] = cs[7] = c4.w;
-      sn[0] = -s4.x; sn[1] = s4.x; sn[2] = -s4.y; sn[3] = s4.y;
-      sn[4] = -s4.z; sn[5] = s4.z; sn[6] = -s4.w; sn[7] = s4.w;
-    } else {
-      const bool second = e0 >= half;
-      const int i0 = second ? e0 - half : e0;
+  // the place of KV head 0's row in the cache, and from head to head
+  int64_t row = 0, srow = 0;
+  int step = 0, sstep = 0;
+  if (kind > 0 && inside) {
+    const int page = slot / a.unit, in_page = slot - page * a.unit;
+    srow = (int64_t)page * KVN * a.unit + in_page;
+    sstep = a.unit;
+    row = a.c.head_major ? srow : (int64_t)slot * KVN;
+    step = a.c.head_major ? a.unit : 1;
+  }
+  if (kind == 2) {  // values: as they are
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float4 c4 = __ldg(reinterpret_cast<const float4*>(row + i0) + i);
-        const float4 s4 = __ldg(reinterpret_cast<const float4*>(row + half + i0) + i);
-        cs[4 * i] = c4.x; cs[4 * i + 1] = c4.y; cs[4 * i + 2] = c4.z; cs[4 * i + 3] = c4.w;
-        sn[4 * i] = second ? s4.x : -s4.x; sn[4 * i + 1] = second ? s4.y : -s4.y;
-        sn[4 * i + 2] = second ? s4.z : -s4.z; sn[4 * i + 3] = second ? s4.w : -s4.w;
-      }
+    for (int r = 0; r < kRounds; ++r) {
+      const int h = h0 + r * H;
+      float y[8];
+      unpack8(x[r], y);
+      store_row<D, F>(a.c.v, a.c.vs, row + (int64_t)h * step, srow + (int64_t)h * sstep, chunk, y, x[r],
+                      inside && h < heads);
     }
-  } else {
+    return;
+  }
+
+  // What this lane's eight elements are multiplied by, their own values and the others of
+  // their pairs (the sine with the sign of the pair's half), both with the norm's weights.
+  const int half = a.rot / 2, e0 = 8 * chunk;
+  const bool turned = e0 < a.rot, second = e0 >= half;
+  // the lane with the other values of this one's pairs
+  const int other = PAIRS || !turned ? lane : lane + (second ? -half / 8 : half / 8);
+  const uint16_t* weight = kind ? a.kw : a.qw;
+  Pair own[4], oth[4];
+  {
+    uint4 wy = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u), wo = wy;  // ones
+    if (weight) {
+      wy = __ldg(reinterpret_cast<const uint4*>(weight) + chunk);
+      wo = __ldg(reinterpret_cast<const uint4*>(weight) + other % L);
+    }
+    const uint32_t y4[4] = {wy.x, wy.y, wy.z, wy.w}, o4[4] = {wo.x, wo.y, wo.z, wo.w};
+    float cs[8], sn[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       cs[i] = 1.f;
       sn[i] = 0.f;
     }
+    if (turned) {
+      const float* table = a.cos_sin + (int64_t)position * a.rot;
+      if constexpr (PAIRS) {
+        const float4 c4 = __ldg(reinterpret_cast<const float4*>(table + e0 / 2));
+        const float4 s4 = __ldg(reinterpret_cast<const float4*>(table + half + e0 / 2));
+        cs[0] = cs[1] = c4.x; cs[2] = cs[3] = c4.y; cs[4] = cs[5] = c4.z; cs[6] = cs[7] = c4.w;
+        sn[0] = -s4.x; sn[1] = s4.x; sn[2] = -s4.y; sn[3] = s4.y;
+        sn[4] = -s4.z; sn[5] = s4.z; sn[6] = -s4.w; sn[7] = s4.w;
+      } else {
+        const int i0 = second ? e0 - half : e0;
+        const float sign = second ? 1.f : -1.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float4 c4 = __ldg(reinterpret_cast<const float4*>(table + i0) + i);
+          const float4 s4 = __ldg(reinterpret_cast<const float4*>(table + half + i0) + i);
+          cs[4 * i] = c4.x; cs[4 * i + 1] = c4.y; cs[4 * i + 2] = c4.z; cs[4 * i + 3] = c4.w;
+          sn[4 * i] = sign * s4.x; sn[4 * i + 1] = sign * s4.y;
+          sn[4 * i + 2] = sign * s4.z; sn[4 * i + 3] = sign * s4.w;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const Pair py = pair_of(y4[i]), po = PAIRS ? py : pair_of(o4[i]);
+      own[i].f[0] = py.f[0] * cs[2 * i];
+      own[i].f[1] = py.f[1] * cs[2 * i + 1];
+      oth[i].f[0] = po.f[PAIRS ? 1 : 0] * sn[2 * i];
+      oth[i].f[1] = po.f[PAIRS ? 0 : 1] * sn[2 * i + 1];
+    }
   }
-  // the lane with the other values of this one's pairs
-  const int step = half / 8;
-  const int other = PAIRS || !turned ? lane : lane + (e0 >= half ? -step : step);
-  const int other_chunk = other % L;
 
 #pragma unroll
   for (int r = 0; r < kRounds; ++r) {
     const int h = h0 + r * H;
-    const int kind = h < a.QN ? 0 : h < a.QN + KVN ? 1 : 2;  // query, key, value
-    float y[8];
-    unpack8(x[r], y);
-    uint4 xo = x[r];
-    if constexpr (!PAIRS) {
-      xo.x = __shfl_sync(0xffffffffu, x[r].x, other);
-      xo.y = __shfl_sync(0xffffffffu, x[r].y, other);
-      xo.z = __shfl_sync(0xffffffffu, x[r].z, other);
-      xo.w = __shfl_sync(0xffffffffu, x[r].w, other);
+    const uint32_t xw[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
+    Pair y[4], z[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = pair_of(xw[i]);
+    float f = 1.f;
+    if (weight) {
+      Pair ss = mul2(y[0], y[0]);
+#pragma unroll
+      for (int i = 1; i < 4; ++i) ss = fma2(y[i], y[i], ss);
+      float s = ss.f[0] + ss.f[1];
+#pragma unroll
+      for (int d = 1; d < L; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+      f = rsqrtf(s * (1.f / D) + a.eps);
     }
-    float o[8];
-    unpack8(xo, o);
-    float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss += y[i] * y[i];
-#pragma unroll
-    for (int d = 1; d < L; d <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-    if (kind < 2) {
-      const uint16_t* weight = kind ? a.kw : a.qw;
+    for (int i = 0; i < 4; ++i) {
+      Pair o;
+      if constexpr (PAIRS) {
+        o.f[0] = y[i].f[1];
+        o.f[1] = y[i].f[0];
+      } else {
+        o = pair_of(__shfl_sync(0xffffffffu, xw[i], other));
+      }
+      if (!turned) o.u = 0;  // (an infinite value is no NaN of it)
+      z[i] = fma2(o, oth[i], mul2(y[i], own[i]));
       if (weight) {
-        const float f = 1.f / sqrtf(ss * (1.f / D) + a.eps);
-        float wy[8], wo[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(weight) + chunk), wy);
-        unpack8(__ldg(reinterpret_cast<const uint4*>(weight) + other_chunk), wo);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          y[i] = y[i] * f * wy[i];
-          o[i] = o[i] * f * wo[i];
-        }
+        const Pair ff = {{f, f}};
+        z[i] = mul2(z[i], ff);
       }
-      if (turned) {
-        float z[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = y[i] * cs[i] + (PAIRS ? y[i ^ 1] : o[i]) * sn[i];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = z[i];
-      }
-      if (kind == 0 && h < heads)
-        *(reinterpret_cast<uint4*>(a.out + t * a.out_stride + (int64_t)h * D) + chunk) = pack8(y);
     }
-    const int hk = kind == 2 ? h - a.QN - KVN : h - a.QN;
-    const int64_t srow = ((int64_t)page * KVN + hk) * a.unit + in_page;
-    const int64_t row = a.c.head_major ? srow : (int64_t)slot * KVN + hk;
-    store_row<D, F>(kind == 2 ? a.c.v : a.c.k, kind == 2 ? a.c.vs : a.c.ks, row, srow, chunk, y,
-                    kind == 2 ? x[r] : pack8(y), inside && kind > 0 && h < heads);
+    float v[8] = {z[0].f[0], z[0].f[1], z[1].f[0], z[1].f[1], z[2].f[0], z[2].f[1], z[3].f[0], z[3].f[1]};
+    if (kind == 0) {
+      if (h < heads)
+        *(reinterpret_cast<uint4*>(a.out + t * a.out_stride + (int64_t)h * D) + chunk) = pack8(v);
+    } else {
+      store_row<D, F>(a.c.k, a.c.ks, row + (int64_t)h * step, srow + (int64_t)h * sstep, chunk, v, pack8(v),
+                      inside && h < heads);
+    }
   }
 }
 
 template <int D, int F>
 cudaError_t launch_rope(const RopeArgs& a, bool pairs, int grid, cudaStream_t s) {
-  if (pairs) norm_rope_kernel<D, F, true><<<grid, 256, 0, s>>>(a);
-  else norm_rope_kernel<D, F, false><<<grid, 256, 0, s>>>(a);
+  if (pairs) norm_rope_kernel<D, F, true><<<grid, kThreads, 0, s>>>(a);
+  else norm_rope_kernel<D, F, false><<<grid, kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -278,8 +329,10 @@ extern "C" fia_status fia_norm_rope_append(const fia_norm_rope_params* p, void* 
   a.pool = a.c.bt ? a.c.num_blocks * a.c.bs : (int64_t)a.c.B * a.c.cap;
   if (a.T == 0) return FIA_OK;
   const int per = kRounds * (256 / D);  // heads of a warp
-  a.groups = (a.QN + 2 * KVN + per - 1) / per;
-  const int64_t grid = ((int64_t)a.T * a.groups + 7) / 8;
+  a.q_groups = (a.QN + per - 1) / per;
+  a.kv_groups = (KVN + per - 1) / per;
+  a.groups = a.q_groups + 2 * a.kv_groups;
+  const int64_t grid = ((int64_t)a.T * a.groups + kThreads / 32 - 1) / (kThreads / 32);
   if (grid > INT32_MAX / 8) return FIA_ERR_BAD_SHAPE;  // (warps are counted in 32 bits)
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool pairs = p->interleaved != 0;

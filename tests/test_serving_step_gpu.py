@@ -123,6 +123,26 @@ def test_assign_pages_edges():
     assert free.tolist() == [1, 7] and int(n) == 2 and int(held) == 0 and int(status) == 3
 
 
+def test_assign_pages_of_bad_row_counts():
+    """cu_seqlens_q below 0 or past the rows: nothing is written outside."""
+    lens, T = [40, 33, 70], 10
+    for cu in ([-3, 2, 6, 9], [0, 4, 12, 30], [5, 5, 8, 8]):
+        table, held, free, n = _i32(np.full((3, 5), -1)), _i32([0] * 3), _i32(range(20)), _i32([20])
+        big = torch.full((2, T + 40), 77, dtype=torch.int32, device=DEV)
+        fia.assign_pages(table, held, free, n, _i32(lens), block_size=16, cu_seqlens_q=_i32(cu),
+                         slots=big[0, 20:20 + T], positions=big[1, 20:20 + T])
+        assert torch.all(big[:, :20] == 77) and torch.all(big[:, 20 + T:] == 77)
+        want = serving.pages(np.full((3, 5), -1), [0] * 3, list(range(20)), 20, lens, 16, cu=cu, T=T)
+        assert big[0, 20:20 + T].tolist() == want[4].tolist()
+        assert big[1, 20:20 + T].tolist() == want[5].tolist()
+
+
+@pytest.mark.parametrize("block", [16, 144, 256, 1024])
+def test_assign_pages_of_long_pages(block):
+    _pages_case(9, block, 6, seed=55, tnd=True, q_lens=[0, 1, 700, 130, 128, 129, 2, 1500, 64],
+                lens=[3, 5, 700, 1000, 129, 128, 1, 1600, 64], held=[1] * 9, spare=400, seen=True)
+
+
 def test_assign_pages_without_rows_and_on_a_stream():
     table, held, free, n = _i32(np.zeros((2, 3))), _i32([0, 0]), _i32([4, 3, 2, 1, 0]), _i32([5])
     lens = _i32([0, 0])
