@@ -190,7 +190,9 @@ __global__ void __launch_bounds__(kThreads) assign_pages_kernel(const PagesArgs 
 #pragma unroll
     for (int k = 0; k < 3; ++k) all[k] = seq.before(k, nc);
   }
-  cluster_bar_arrive();  // this CTA has read the counts: they may be written behind the wait
+  // This CTA has read the counts: they may be written behind the wait.  (One CTA: the scan's
+  // barriers lie between.)
+  if (nc > 1) cluster_bar_arrive();
   bool bad = false;
   const int64_t top = min((int64_t)count + all[0], (int64_t)a.nb);  // the list's length after the returns
   // Entry `at` of that list, -1 below its start.
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(kThreads) assign_pages_kernel(const PagesArgs 
   if (bad && a.status) atomicExch(a.status, 3);
 
   // ---- counts ----
-  cluster_bar_wait();
+  if (nc > 1) cluster_bar_wait();
   for (int b = me; b < a.B; b += everyone) {
     const int need = need_of(seq.at(kLen, b)), held = seq.at(kHeld, b);
     const int64_t left = max(top - seq.at(kTake, b), (int64_t)0);

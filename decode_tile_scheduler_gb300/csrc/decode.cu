@@ -480,6 +480,7 @@ __global__ void __launch_bounds__(1024) decode_schedule_kernel(const DecodeArgs 
               : (T - 1) / per + 1;
     c2 = C <= 0x7fffffffLL ? (int64_t)((uint32_t)(C + a.small_div - 1) / (uint32_t)a.small_div)
                            : (C + a.small_div - 1) / a.small_div;
+    c2 = max(c2, min(C, (int64_t)a.small_min));
   }
 
   // per batch: big and small chunks of its active units and whether it is

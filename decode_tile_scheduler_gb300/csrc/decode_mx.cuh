@@ -248,12 +248,13 @@ __global__ void __launch_bounds__(MxCfg<MR>::kThreads, MxCfg<MR>::kCtas)
                                  (lane < npg ? pg0 + lane : fg0 + lane - npg)];
       }
       if (ent_ok && ci < gm.nch) {  // chunk description + the columns' query vectors
+        const int64_t slot0 = a.sched[kSchedHeader + b];  // (in flight with the page ids)
         // (the consumers take both before the chunk's first tile)
         wait_or_abort(qempty, (ucount & 1) ^ 1, a.err, misc);
         if (lane == 0) {
           UnitMsg& m = msg;
           m.r = r;
-          m.slot = (int64_t)ci * (a.KVN * ha) + r.hk * ha + r.hg;
+          m.slot = slot0 + (int64_t)ci * (a.KVN * ha) + r.hk * ha + r.hg;
           m.ci = ci;
           m.nch = gm.nch;
           m.t_begin = t_begin;
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(MxCfg<MR>::kThreads, MxCfg<MR>::kCtas)
     if (named_bar_or(1, 32 * W, msg.done || *reinterpret_cast<volatile int*>(misc))) break;
     const UnitInfo r = msg.r;
     const int kvl = r.kv_len;
-    const int64_t slot0 = a.sched[kSchedHeader + r.b] + msg.slot;
+    const int64_t slot0 = msg.slot;
     const int t_begin = msg.t_begin, t_end = msg.t_end;
     const bool split = msg.nch > 1;
     // keys seen by this lane's two columns, and their mask rows
@@ -403,17 +404,16 @@ __global__ void __launch_bounds__(MxCfg<MR>::kThreads, MxCfg<MR>::kCtas)
     float slc;
     {
       const uint16_t* qsm = reinterpret_cast<const uint16_t*>(smem + Cfg::kOffQ) + g * D + 8 * q4;
-      uint32_t emax = 0;
+      uint32_t top = 0;  // (bf16 magnitudes order as integers)
 #pragma unroll
       for (int kk = 0; kk < KS; ++kk) {
         uint2 v = make_uint2(0u, 0u);
         if (g < r.ncols) v = *reinterpret_cast<const uint2*>(qsm + (kk >> 1) * 32 + 4 * (kk & 1));
         qb[kk][0] = v.x;
         qb[kk][1] = v.y;
-        emax = max(emax, max(max((v.x >> 7) & 0xffu, (v.x >> 23) & 0xffu),
-                             max((v.y >> 7) & 0xffu, (v.y >> 23) & 0xffu)));
+        top = __vmaxu2(top, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu));
       }
-      emax = __reduce_max_sync(0xffffffffu, emax);
+      const uint32_t emax = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu)) >> 7;
       const int sh = min(max(142 - (int)emax, -100), 100);  // 15 - (emax - 127)
       // (the score factor is positive, its sign in the queries: hidden scores stay -inf)
       const float up = copysignf(__int_as_float((127 + sh) << 23), a.scale_log2);
@@ -628,14 +628,14 @@ __global__ void __launch_bounds__(MxCfg<MR>::kThreads, MxCfg<MR>::kCtas)
       }
 #pragma unroll
       for (int w2 = 0; w2 < W; ++w2) {
-        L[0] += ml[w2].x == -INFINITY ? 0.f : ml[w2].y * exp2f(ml[w2].x - M[0]);
-        L[1] += ml[w2].z == -INFINITY ? 0.f : ml[w2].w * exp2f(ml[w2].z - M[1]);
+        L[0] += ml[w2].x == -INFINITY ? 0.f : ml[w2].y * fast_exp2(ml[w2].x - M[0]);
+        L[1] += ml[w2].z == -INFINITY ? 0.f : ml[w2].w * fast_exp2(ml[w2].z - M[1]);
       }
       float back[4];
       bf16x2x2_to_f32x4(vref[0], vref[1], back);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float f = m_r[e] == -INFINITY ? 0.f : exp2f(m_r[e] - M[e]);
+        const float f = m_r[e] == -INFINITY ? 0.f : fast_exp2(m_r[e] - M[e]);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
           acc[i][e] *= f * back[i >> 1];

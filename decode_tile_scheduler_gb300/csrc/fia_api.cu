@@ -223,13 +223,17 @@ int debug_checks() {
 // finer tail (fia_execute: long FP8 decode 139.4 -> 134.8 us, FP8 with 16
 // heads per KV head 120.3 -> 113.6 us, 4-row decode 88.2 -> 79.9 us against
 // k = 6, 6 and 3; one-row bf16 decode 58.9 -> 58.6 us against k = 3).
+// MXFP4: 2, but chunks of six tiles at least, whose fixed cost is larger against their
+// tiles (64 sequences of 1000 to 9000 keys 91.2 us with 1, 82.2 so; 4 of 32 to 128 k keys
+// 91.9 -> 86.7; 32 of 512 to 4096 keys 35.5 -> 36.0, without the least size 38.1).
 int decode_small_div(const fia_params* p) {
+  if (p->kv_dtype == FIA_KV_MXFP4) return 2;
   return (p->kv_dtype != FIA_KV_BF16 || p->max_seqlen_q > 1) ? 1 : 2;
 }
 
-// Chunks to a CTA that the chunk size aims at.  MXFP4: two, of CTAs three to an SM
-// (attend 32 x 512-4096 keys 36.9 us; one 48.7, three 38.9, four 41.6; 4 of 32 to 128 k
-// keys 101, 141, 102, 105).
+// Chunks to a CTA that the chunk size aims at.  MXFP4: two, of CTAs three to an SM (32
+// sequences of 512 to 4096 keys 36.0 us; one 37.0, three 38.8, four 41.5; 4 of 32 to 128 k
+// keys 86.7, 104.5, 88.4, 91.9).
 int decode_chunks_per_cta(const fia_params* p) {
   return p->kv_dtype == FIA_KV_MXFP4 ? 2 : kDecodeChunksPerCta;
 }
@@ -311,6 +315,7 @@ DecodeArgs decode_args(const fia_params* p, const DecodePlan& pl, void* ws) {
   a.num_units = pl.U;
   a.chunks_per_cta = pl.W;
   a.small_div = decode_small_div(p);
+  a.small_min = p->kv_dtype == FIA_KV_MXFP4 ? 6 : 1;
   a.max_chunks = pl.max_chunks;
   char* w = static_cast<char*>(ws);
   a.sched = reinterpret_cast<int64_t*>(w + pl.off_sched);

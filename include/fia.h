@@ -615,7 +615,7 @@ fia_status fia_selftest_bounded_wait(int32_t *status, uint64_t limit_ns, void *s
  * together, at least 1 (0 when the batch has no query row).  With T the total
  * cost, n CTAs and W = 5 chunks per CTA (MXFP4: three CTAs to each of num_sms, W = 2),
  * C = max(1, ceil(T / (n W))) and c2 = ceil(C / k), k = 2 for a bf16 cache and S = 1,
- * else 1.  A unit of
+ * else 1 (MXFP4: k = 2, and c2 at least min(C, 6)).  A unit of
  * cost c gets n1 = max(0, floor(c/C) - 1) chunks of C tiles, then chunks of
  * c2 tiles over the rest (at most 2k), so n W + 2k U bounds the chunks of U
  * units.  (A band with first_tokens and U >= n / 8: units of c_max tiles at most, cut in s
