@@ -14,6 +14,9 @@ pytestmark = pytest.mark.gpu
 
 DEV = "cuda:0"
 
+# CTAs too few for a cluster: a call of few units takes the kernel of larger ones
+NO_CLUSTER = 7
+
 
 def _run(p, weights=False, num_sms=0, w_in=None):
     d = p.to(DEV)
@@ -33,9 +36,10 @@ def _check(p, weights=False, num_sms=0):
     if weights:
         cap = p.S_kv if p.block_table is None else p.block_table.shape[1] * p.block_size
         w_in = torch.rand(p.B, p.KVN, cap, generator=torch.Generator().manual_seed(8))
-    got = _run(p, weights, num_sms, w_in)
-    serving.check_mx(p, got[0], got[1], got[2] if weights else None, w_in)
-    return got
+    # (both decode kernels)
+    for n in (num_sms, NO_CLUSTER) if max(p.q_lens) <= 16 and num_sms == 0 else (num_sms,):
+        got = _run(p, weights, n, w_in)
+        serving.check_mx(p, got[0], got[1], got[2] if weights else None, w_in)
 
 
 # ----------------------------------------------------------------------------
@@ -187,8 +191,8 @@ def test_decode_query_ranges(mult):
     _check(p)
 
 
-@pytest.mark.parametrize("rows", [1, 40])
-def test_far_scales(rows):
+@pytest.mark.parametrize("rows,num_sms", [(1, 0), (1, NO_CLUSTER), (40, 0)])
+def test_far_scales(rows, num_sms):
     """Scales of V from 2^-20 to 2^20, and of K within what scores stand: the power of
     two that O is kept over moves from tile to tile."""
     p = serving.make_mx(B=2, QN=4, KVN=2, q_lens=[rows] * 2, kv_lens=[3000, 1111], block_size=64,
@@ -197,28 +201,30 @@ def test_far_scales(rows):
     p.v_scale = torch.randint(107, 148, p.v_scale.shape, generator=g).to(torch.uint8)
     p.k_scale = torch.randint(120, 129, p.k_scale.shape, generator=g).to(torch.uint8)
     ref = bounded.attention(serving.decoded(p))
-    out = _run(p)[0].cpu().double()
+    out = _run(p, num_sms=num_sms)[0].cpu().double()
     for b, (o, l, w, mag, A) in enumerate(ref):
-        # P times its scale over the largest (2^20) is rounded to half a step of fp16, of
-        # 2^-24 over the factor 2^6 in its subnormal range, times codes of up to 6; a
-        # prompt's P, in bf16, by half a step of it
+        # P (32 at the least where it is largest) times its scale over the largest, 2^20, is
+        # rounded to half a step of fp16, at most 2^-25, and a scale below 2^-24 of the
+        # largest counts as 0 (P up to 2^13 over 32: 2^-17 at most, but where P is that large
+        # it is the sum too), times codes of up to 6; a prompt's P, in bf16, by half a step
         tl = bounded.lse_tolerance(serving.decoded(p), A, p.kv_lens[b])
         half = bounded.HALF_FP16 if rows <= 16 else bounded.HALF_BF16
         to = 1.01 * (half * mag + bounded.HALF_BF16 * o.abs()) + 2 * tl * mag
-        if rows <= 16:  # (p of the largest is 1 at the least: l >= 1)
-            to = to + 2.0 ** 20 * 2.0 ** -31 * 6 * p.kv_lens[b]
+        if rows <= 16:
+            to = to + 2.0 ** 20 * 6 * (2.0 ** -30 * p.kv_lens[b] + 2.0 ** -25)
         assert torch.all((out[b] - o).abs() <= to)
 
 
-def test_a_nan_scale_reaches_the_rows_that_see_it():
+@pytest.mark.parametrize("num_sms", [0, NO_CLUSTER])
+def test_a_nan_scale_reaches_the_rows_that_see_it(num_sms):
     p = serving.make_mx(B=2, QN=4, KVN=2, q_lens=[1, 1], kv_lens=[300, 200], block_size=32, seed=13,
                         mask_mode=3, poison=False)
-    clean = _run(p)
+    clean = _run(p, num_sms=num_sms)
     page, row = int(p.block_table[0, 100 // 32]), 100 % 32
     v = copy.copy(p)
     v.v_scale = p.v_scale.clone()
     v.v_scale[page, 1, row, 2] = 255  # sequence 0, KV head 1 (heads 2, 3), elements 64..95
-    got = _run(v)
+    got = _run(v, num_sms=num_sms)
     bad = torch.zeros_like(got[0], dtype=torch.bool)
     bad[0, :, 2:, 64:96] = True
     assert torch.equal(torch.isnan(got[0]), bad) and torch.equal(got[0][~bad], clean[0][~bad])
@@ -226,11 +232,11 @@ def test_a_nan_scale_reaches_the_rows_that_see_it():
     k = copy.copy(p)
     k.k_scale = p.k_scale.clone()
     k.k_scale[page, 1, row, 2] = 255
-    got = _run(k)
+    got = _run(k, num_sms=num_sms)
     bad[0, :, 2:] = True
     assert torch.equal(torch.isnan(got[0]), bad) and torch.equal(got[0][~bad], clean[0][~bad])
     k.seqused_kv = torch.tensor([100, 200], dtype=torch.int32)  # behind the last key: anything
-    assert torch.isfinite(_run(k)[0]).all()
+    assert torch.isfinite(_run(k, num_sms=num_sms)[0]).all()
 
 
 # ----------------------------------------------------------------------------
@@ -263,9 +269,10 @@ def test_prompt_explicit_mask():
 # edges
 # ----------------------------------------------------------------------------
 
+@pytest.mark.parametrize("num_sms", [0, NO_CLUSTER])
 @pytest.mark.parametrize("page", [1 << 26, -(1 << 26), -1, 5000])
 @pytest.mark.parametrize("kind", ["decode", "window", "weights", "prompt", "weights_prompt"])
-def test_pages_outside_the_pool_read_as_zeros(kind, page):
+def test_pages_outside_the_pool_read_as_zeros(kind, page, num_sms):
     prompt = kind.endswith("prompt")
     kw = dict(mask_mode=4, pre_tokens=150, first_tokens=4) if kind == "window" else dict(mask_mode=3)
     p = serving.make_mx(B=3, QN=8, KVN=2, q_lens=[200, 40, 77] if prompt else [1, 2, 1],
@@ -279,7 +286,7 @@ def test_pages_outside_the_pool_read_as_zeros(kind, page):
     for entry in (p.num_blocks - 1, page):
         p.block_table[0, 4], p.block_table[2, 0], p.block_table[2, 6] = entry, entry, entry
         d = p.to(DEV)
-        call = (fia.KeyWeightsCall if "weights" in kind else fia.FiaCall)(d)
+        call = (fia.KeyWeightsCall if "weights" in kind else fia.FiaCall)(d, num_sms=num_sms)
         call.ws.fill_(0x7f)
         got.append([x.clone() for x in call.run()])
         torch.cuda.synchronize()
@@ -288,15 +295,15 @@ def test_pages_outside_the_pool_read_as_zeros(kind, page):
         assert torch.isfinite(a.float()).all() and torch.equal(a, b)
 
 
-@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("rows,num_sms", [(1, 0), (1, NO_CLUSTER), (3, NO_CLUSTER), (40, 0)])
 @pytest.mark.parametrize("bad", ["rows", "keys", "negative_keys"])
-def test_lengths_outside_the_tensors(rows, bad):
+def test_lengths_outside_the_tensors(rows, num_sms, bad):
     p = serving.make_mx(B=3, QN=4, KVN=2, q_lens=[rows] * 3, kv_lens=[100, 70, 60], block_size=32,
                         layout=fi.LAYOUT_TND, seed=33, mask_mode=3)
     d = p.to(DEV)
     T = 3 * rows
     out = torch.full((T + 8, 4, 128), 3.0, dtype=torch.bfloat16, device=DEV)
-    call = fia.FiaCall(d, out=out[:T])
+    call = fia.FiaCall(d, out=out[:T], num_sms=num_sms)
     if bad == "rows":
         d.cu_seqlens_q[2:] += 3
         hit, fine = slice(2 * rows, T), [0]
@@ -328,10 +335,11 @@ def test_rows_behind_the_last_sequence_are_left():
         assert torch.isfinite(out).all()
 
 
-def test_without_a_workspace_and_captured():
+@pytest.mark.parametrize("B", [3, 40])
+def test_without_a_workspace_and_captured(B):
     """The workspace-free entry, a plan used twice, and a replayed graph give the same bits."""
-    p = serving.make_mx(B=3, QN=8, KVN=2, q_lens=[1] * 3, kv_lens=[3000, 200, 77], block_size=64,
-                        seed=35, mask_mode=3).to(DEV)
+    p = serving.make_mx(B=B, QN=8, KVN=2, q_lens=[1] * B, kv_lens=[3000, 200, 77] + [500] * (B - 3),
+                        block_size=64, seed=35, mask_mode=3).to(DEV)
     want = [x.clone() for x in fia.FiaCall(p).run()]
     call = fia.FiaCall(p)
     call.plan()
@@ -377,6 +385,38 @@ def test_pools_past_two_to_the_31_bytes():
     codes, scale = serving.mx_quantised(new.cpu()[0, 0])
     assert torch.equal(d.k_cache[nb - 1, 122].cpu(), torch.from_numpy(codes))
     assert torch.equal(d.v_scale[nb - 1, :, 122].cpu(), torch.from_numpy(scale))
+
+
+def test_calls_side_by_side():
+    """Two calls on two streams, each with its workspace, many times: the same bits as alone."""
+    ps = [serving.make_mx(B=12, QN=16, KVN=2, q_lens=[2] * 12, kv_lens=[900 + 70 * i for i in range(12)],
+                          block_size=32, seed=s, mask_mode=3).to(DEV) for s in (50, 51)]
+    want = [[x.clone() for x in fia.FiaCall(p).run()] for p in ps]
+    calls, streams = [fia.FiaCall(p) for p in ps], [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for c, s in zip(calls, streams):
+            c.run(s)
+    torch.cuda.synchronize()
+    for c, w in zip(calls, want):
+        assert torch.equal(c.out, w[0]) and torch.equal(c.lse, w[1]) and c.error_word() == 0
+
+
+def test_the_queue_of_a_plan_of_other_lengths():
+    """A plan made for longer sequences: entries past the cache run as empty, nothing outside
+    is read or written."""
+    p = serving.make_mx(B=20, QN=8, KVN=2, q_lens=[1] * 20, kv_lens=[700 + i for i in range(20)],
+                        block_size=32, seed=52, mask_mode=3).to(DEV)
+    call = fia.FiaCall(p)
+    call.plan()
+    short = copy.copy(p)
+    short.block_table = p.block_table[:, :5].contiguous()
+    other = fia.FiaCall(short, out=torch.full_like(call.out, 3.0))
+    n = min(call.ws.numel(), other.ws.numel())
+    other.ws[:n].copy_(call.ws[:n])
+    other.execute()
+    torch.cuda.synchronize()
+    assert other.error_word() == 2
 
 
 def test_python_calls_refuse_tensors_that_do_not_fit():

@@ -1,13 +1,15 @@
 """The calls of a serving step without a GPU: what they refuse, and the test suite's own
 statements of their definitions."""
+import contextlib
 import ctypes
+from types import SimpleNamespace
 
 import numpy as np
 import pytest
 import torch
 
 import decode_tile_scheduler_gb300 as fia
-from decode_tile_scheduler_gb300 import _abi
+from decode_tile_scheduler_gb300 import _abi, api
 from tests import serving
 from tests.test_bounded_cache_cpu import FAKE, _append, _cache, _evict, _fia_params
 
@@ -152,6 +154,32 @@ def test_python_calls_refuse_tensors_that_do_not_fit():
         a.update(kw)
         with pytest.raises(ValueError):
             fia.AssignPagesCall(**a, block_size=16)
+
+
+@pytest.mark.parametrize("kind,name", [(fia.AssignPagesCall, "fia_assign_pages"),
+                                       (fia.NormRopeAppendCall, "fia_norm_rope_append")])
+def test_calls_launch_on_their_tensors_device(kind, name, monkeypatch):
+    seen, current = [], [0]
+
+    @contextlib.contextmanager
+    def device(d):
+        before, current[0] = current[0], torch.device(d).index
+        yield
+        current[0] = before
+
+    monkeypatch.setattr(api, "_current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(api, "_current_stream", lambda index: 1000 + index)
+    monkeypatch.setattr(_abi, name, lambda params, stream: seen.append((current[0], stream)))
+    call, far = object.__new__(kind), torch.device("cuda", 1)
+    for k, v in dict(device=far, cache=SimpleNamespace(device=far), params=None, slots=None,
+                     positions=None, q_out=None).items():
+        setattr(call, k, v)
+    call.run()
+    call.run(77)
+    assert seen == [(1, 1001), (1, 77)] and current[0] == 0
+    with pytest.raises(ValueError, match="cuda:0"):
+        call.run(SimpleNamespace(device=torch.device("cuda", 0), cuda_stream=5))
 
 
 def test_mxfp4_statement():
