@@ -13,7 +13,9 @@
 // writes the rows.  (A search and a page per row bound the call by instructions: 1024
 // sequences with 52 k rows 22.5 us.)
 //
-// Latency-bound: lengths, a scan, then pages.  One CTA, or eight for many rows, each of
+// Latency-bound: lengths, a scan, then pages (64 sequences of a token 6.1 us a call, 3.4 of
+// them in the kernel: scan 0.9, pages 0.8, rows 1.1; 1024 sequences with 1 to 256 rows and
+// pages that go back 13.7).  One CTA, or eight for many rows, each of
 // which makes the prefix sums of all sequences for itself; past kWhole sequences each
 // makes a slice, and they look into each other's shared memory as a cluster.
 #include <atomic>
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(kThreads) assign_pages_kernel(const PagesArgs 
         t += (int)(ja - r.j);
         position = a.seen ? __ldg(a.seen + b) - (int)(len - ja) : (int)ja;
         int page = -1;
-        if (pg < a.W) {
+        if ((uint32_t)pg < (uint32_t)a.W) {  // (cu_seqlens_q that does not ascend: anything)
           const int held = seq.at(kHeld, b);
           page = pg < held ? __ldg(a.table + (int64_t)b * a.W + pg)
                            : listed(top - 1 - seq.at(kTake, b) - (pg - held));

@@ -29,6 +29,50 @@
 namespace fia {
 namespace {
 
+// A row's V scales v (bf16, a lane each) against the references: where one is past its
+// group's (a NaN is past nothing), the warp's new references, and the exact powers of two
+// that O's groups move by in f.  Returns whether they moved.
+__device__ __forceinline__ bool mx_references(const __nv_bfloat162 (&v)[2], __nv_bfloat162 (&vref)[2],
+                                              __nv_bfloat162 (&vinv)[2], float (&f)[4]) {
+  const auto bits = [](const __nv_bfloat162& x) { return *reinterpret_cast<const uint32_t*>(&x); };
+  // (the larger of two drops a NaN)
+  const bool past = bits(__hmax2(v[0], vref[0])) != bits(vref[0]) || bits(__hmax2(v[1], vref[1])) != bits(vref[1]);
+  if (!__any_sync(0xffffffffu, past)) return false;
+  uint32_t en[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t c = (bits(v[j >> 1]) >> (16 * (j & 1)) & 0xffffu) >> 7;
+    const uint32_t old = (bits(vref[j >> 1]) >> (16 * (j & 1)) & 0xffffu) >> 7;
+    en[j] = max(old, min(__reduce_max_sync(0xffffffffu, c == 255u ? 0u : c), (uint32_t)kMxRefMax));
+    // (a jump past 2^-126 leaves a negligible old sum and gives 0)
+    f[j] = __int_as_float(max(127 + (int)old - (int)en[j], 0) << 23);
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    vref[k] = mx_pair(en[2 * k] << 7, en[2 * k + 1] << 7);
+    vinv[k] = mx_pair((254 - en[2 * k]) << 7, (254 - en[2 * k + 1]) << 7);
+  }
+  return true;
+}
+// V scales over their references as fp16 pairs of rows 2k, 2k + 1 (lanes): groups 0 and 1
+// from the even lane, 2 and 3 from the odd one.
+__device__ __forceinline__ uint2 mx_scale_pairs(const __nv_bfloat162 (&v)[2], const __nv_bfloat162 (&vinv)[2],
+                                                int lane) {
+  float vf[4];
+  bf16x2x2_to_f32x4(__hmul2(v[0], vinv[0]), __hmul2(v[1], vinv[1]), vf);
+  const uint32_t h01 = pack_f16(vf[0], vf[1]), h23 = pack_f16(vf[2], vf[3]);
+  const uint32_t theirs = __shfl_xor_sync(0xffffffffu, lane & 1 ? h01 : h23, 1);
+  const uint32_t even = lane & 1 ? theirs : h01, odd = lane & 1 ? h23 : theirs;
+  return make_uint2(__byte_perm(even, odd, 0x5410), __byte_perm(even, odd, 0x7632));
+}
+// The row of a block of 16 whose address this lane gives the transposing ldmatrix of V:
+// matrices (keys 0, 8, 2, 10, 4, ..., even group), (1, 9, 3, 11, ..., even), and of the odd
+// group.  A lane's first register then holds keys 2q and 2q + 8, its second 2q + 1 and
+// 2q + 9, and one mask pairs the neighbours of both.
+__device__ __forceinline__ int mx_v_row(int lane) {
+  return 2 * ((lane & 7) >> 1) + 8 * (lane & 1) + ((lane >> 3) & 1);
+}
+
 constexpr int kFewCtas = 8, kFewWarps = 8, kFewThreads = 32 * kFewWarps;
 constexpr int kFewKeys = 16;                               // keys of a warp's step
 constexpr int kFewSpan = kFewCtas * kFewWarps;             // steps side by side
@@ -606,8 +650,10 @@ cudaError_t launch_few_t(const DecodeArgs& a, const CacheView& c, const KeyWeigh
 // window 1000 7.3 / 12.4, 8000 14.4 / 16.8; 32 units, 1000 9.5 / 15.7, 8000 27.0 /
 // 32.4; 48 units, 1000 16.8 / 16.8.  With key weights 4 units of 1000 keys 8.3 / 13.9,
 // of 4000 14.1 / 14.5, of 8000 22.3 / 17.5; 32 units 10.8 / 17.6, 18.8 / 26.3, 37.3 /
-// 36.1; 48 units of 2000 keys 24.1 / 23.3.  FP8 gains more.  (With FIA_DEBUG the other
-// kernels run: they report pages outside the pool.)
+// 36.1; 48 units of 2000 keys 24.1 / 23.3.  FP8 gains more.  MXFP4 takes it for calls
+// without a window too: 8 units, 300 keys 9.7 / 14.5, 2000 10.8 / 16.4, 4000 14.2 / 16.8,
+// 8000 18.5 / 21.8; 32 units, 300 10.3 / 14.8, 4000 16.5 / 24.0, 8000 24.6 / 26.8.  (With
+// FIA_DEBUG the other kernels run: they report pages outside the pool.)
 bool decode_is_few(const DecodeArgs& a, bool mx, bool weights) {
   const int sms = mx ? a.num_ctas / decode_mx_ctas() : a.num_ctas;
   if ((a.first_tokens == 0 && !weights && !mx) || a.mask || a.debug || sms < kFewCtas) return false;

@@ -4,11 +4,14 @@
 // A key is 68 bytes of K and of V where FP8 has 136, for the same number of elements to
 // widen, so the kernel is bound by the instructions of an element, not by memory.  What
 // it does about that:
-//  - Three CTAs to an SM, each with one producer warp and four consumer warps of 32 rows
-//    of a tile, so that a chunk's set-up, waits and merge run beside the others' products,
-//    and twelve consumer warps hide each other's latencies.  Units have 8 columns: 16, in
-//    two CTAs to an SM with the blocks of 16 rows one after the other, widen the codes once
-//    for both halves, but took 52 us where 8 take 45 (16 sequences, 1 to 4 rows of 4 heads).
+//  - Three CTAs to an SM, each with one producer warp and four consumer warps, so that a
+//    chunk's set-up and waits run beside the others' products.  Units have 8 columns: 16
+//    widen the codes once for both halves, but took 52 us where 8 took 45 (16 sequences,
+//    1 to 4 rows of 4 heads).
+//  - S^T = K Q^T: a warp has 32 of a tile's rows.  O^T = V^T P^T: it has 32 of the 128
+//    elements, the ones under one scale, and all rows; P goes through shared memory, twice
+//    (one barrier a tile).  So O is 8 registers a lane and needs no merge behind a chunk
+//    (560 cycles where adding up four warps' O took 4500), and P meets one scale a key.
 //  - Codes go from shared memory to mma fragments by ldmatrix.  K: 32 bits of a row are
 //    eight elements of one scale group, two k-steps of m16n8k16 (the order of a
 //    contraction is free).  V: to the transposing ldmatrix four elements of a key are
@@ -16,11 +19,17 @@
 //    pair the keys' codes in bytes, and cvt makes an fp16 pair of a byte.
 //  - E2M1 codes are fp16 values as they are.  K scales multiply the partial scores of
 //    their 32 elements in fp32; V scales multiply P, already in fp16 and transposed, as
-//    fp16 pairs (a P^T for each of the four groups of 32 elements).  A lane makes both
-//    from the bytes of one row, through shared memory, for the four lanes that use them.
+//    fp16 pairs.
 //
-// Measured issue costs (clocks per warp instruction and scheduler): cvt of a byte, prmt,
-// lop3 2, movmatrix and ex2 4.
+// Measured (one GB300; the call with plan and combine): 4 sequences of 32 to 128 k keys,
+// 64 / 8 heads (364 MB) 86.5 us, of which this kernel 79; its loads alone 65.6, its work
+// alone 76.8.  32 sequences of 512 to 4096 keys 34.9 us.  A warp issues 520 instructions
+// for 32 rows (128 of them cvt of a byte, 2 clocks each), in 950 clocks of its scheduler:
+// the ALU pipe is 53 % and mma 27 % busy, and these two do not run wholly side by side (4
+// cvt 8.1 clocks, 1 mma 8.1, both together 10.8; with 2 lop3 14.8 where 12 were due).  So
+// more warps do not help: four CTAs to an SM took 87.6 us, stages 2 to 4 the same, five
+// CTAs (72 registers) 105; nor do finer chunks (the end times of CTAs draw together, the
+// mean moves up).
 #pragma once
 
 namespace fia {
@@ -36,17 +45,18 @@ struct MxCfg {
   static constexpr int kScaleBytes = kKvTile * 4;
   static constexpr int kOffScale = 2 * kTileBytes, kOffMask = kOffScale + 2 * kScaleBytes;
   static constexpr int kStageBytes = kOffMask + (MR ? kDecodeMaxRows * kKvTile : 0);
-  static constexpr int kStages = MR ? 3 : 4;
+  static constexpr int kStages = 3;
   static constexpr int kQBytes = 8 * D * 2;
   static constexpr int kOffQ = kStages * kStageBytes;
-  static constexpr int kOffRedMl = kOffQ + kQBytes;
-  // (the merge's [4][warps][32] float4 lie in the chunk's last stage)
-  static_assert(4 * kWarps * 32 * 16 <= 2 * kTileBytes, "merge");
-  // a tile's scales as the products take them: K's of a row as four floats, V's of two
-  // rows as four fp16 pairs
-  static constexpr int kOffKs = kOffRedMl + kWarps * 8 * 8;
+  // P^T of a tile for everyone, twice: the B fragments of a warp's rows, 16 bytes a lane
+  static constexpr int kOffP = kOffQ + kQBytes;
+  // a tile's scales as the products take them: K's of a row as four floats; V's, a copy of
+  // 128 rows for each warp and its group, as fp16 pairs
+  static constexpr int kOffKs = kOffP + 2 * kWarps * 32 * 16;
   static constexpr int kOffVs = kOffKs + kKvTile * 16;
-  static constexpr int kOffBar = kOffVs + kKvTile / 2 * 16;
+  // the warps' largest scores and sums of 8 columns
+  static constexpr int kOffRed = kOffVs + kWarps * kKvTile * 2;
+  static constexpr int kOffBar = kOffRed + 2 * kWarps * 8 * 4;
   static constexpr int kOffMsg = (kOffBar + 8 * (2 * kStages + 2) + 15) / 16 * 16;
   static constexpr int kOffMisc = kOffMsg + 128;
   static constexpr int kSmem = kOffMisc + 16 + 512;           // + alignment slack (a swizzle's 512 bytes)
@@ -85,62 +95,29 @@ __device__ __forceinline__ void e8m0x4_to_f32x4(uint32_t w, float (&f)[4]) {
   e8m0x4_to_bf16x2x2(w, v);
   bf16x2x2_to_f32x4(v[0], v[1], f);
 }
-// The V scale references: codes from kMxRefMin to kMxRefMax, as bf16 values, and what a
-// scale is multiplied by.
+// The V scale reference of a group: codes from kMxRefMin to kMxRefMax, as bf16 values.
 constexpr int kMxRefMin = 27, kMxRefMax = 253;
 __device__ __forceinline__ __nv_bfloat162 mx_pair(uint32_t lo, uint32_t hi) {
   const uint32_t w = lo | hi << 16;
   return *reinterpret_cast<const __nv_bfloat162*>(&w);
 }
-
-// A row's V scales v (bf16, a lane each) against the references: where one is past its
-// group's (a NaN is past nothing), the warp's new references, and the exact powers of two
-// that O's groups move by in f.  Returns whether they moved.
-__device__ __forceinline__ bool mx_references(const __nv_bfloat162 (&v)[2], __nv_bfloat162 (&vref)[2],
-                                              __nv_bfloat162 (&vinv)[2], float (&f)[4]) {
-  const auto bits = [](const __nv_bfloat162& x) { return *reinterpret_cast<const uint32_t*>(&x); };
-  // (the larger of two drops a NaN)
-  const bool past = bits(__hmax2(v[0], vref[0])) != bits(vref[0]) || bits(__hmax2(v[1], vref[1])) != bits(vref[1]);
-  if (!__any_sync(0xffffffffu, past)) return false;
-  uint32_t en[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t c = (bits(v[j >> 1]) >> (16 * (j & 1)) & 0xffffu) >> 7;
-    const uint32_t old = (bits(vref[j >> 1]) >> (16 * (j & 1)) & 0xffffu) >> 7;
-    en[j] = max(old, min(__reduce_max_sync(0xffffffffu, c == 255u ? 0u : c), (uint32_t)kMxRefMax));
-    // (a jump past 2^-126 leaves a negligible old sum and gives 0)
-    f[j] = __int_as_float(max(127 + (int)old - (int)en[j], 0) << 23);
-  }
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    vref[k] = mx_pair(en[2 * k] << 7, en[2 * k + 1] << 7);
-    vinv[k] = mx_pair((254 - en[2 * k]) << 7, (254 - en[2 * k + 1]) << 7);
-  }
-  return true;
+// Keys of a block of 16.  The transposing ldmatrix gives a lane keys a, b of its first
+// matrix and c, d of its second, whose codes pair as (a, c) and (b, d); movmatrix gives it
+// neighbours of the score fragment.  With (a, b, c, d) = (q, 4 + q, 12 + q, 8 + q) every
+// one of these sets of eight rows differs modulo 8, so no ldmatrix meets a bank twice.
+__device__ __forceinline__ int mx_v_key(int lane) {  // whose address a lane gives: V
+  const int q = (lane & 7) >> 1, kind = (lane & 1) | ((lane >> 2) & 2);
+  return q + (kind == 0 ? 0 : kind == 1 ? 4 : kind == 2 ? 12 : 8);
 }
-// V scales over their references as fp16 pairs of rows 2k, 2k + 1 (lanes): groups 0 and 1
-// from the even lane, 2 and 3 from the odd one.
-__device__ __forceinline__ uint2 mx_scale_pairs(const __nv_bfloat162 (&v)[2], const __nv_bfloat162 (&vinv)[2],
-                                                int lane) {
-  float vf[4];
-  bf16x2x2_to_f32x4(__hmul2(v[0], vinv[0]), __hmul2(v[1], vinv[1]), vf);
-  const uint32_t h01 = pack_f16(vf[0], vf[1]), h23 = pack_f16(vf[2], vf[3]);
-  const uint32_t theirs = __shfl_xor_sync(0xffffffffu, lane & 1 ? h01 : h23, 1);
-  const uint32_t even = lane & 1 ? theirs : h01, odd = lane & 1 ? h23 : theirs;
-  return make_uint2(__byte_perm(even, odd, 0x5410), __byte_perm(even, odd, 0x7632));
-}
-// The row of a block of 16 whose address this lane gives the transposing ldmatrix of V:
-// matrices (keys 0, 8, 2, 10, 4, ..., even group), (1, 9, 3, 11, ..., even), and of the odd
-// group.  A lane's first register then holds keys 2q and 2q + 8, its second 2q + 1 and
-// 2q + 9, and one mask pairs the neighbours of both.
-__device__ __forceinline__ int mx_v_row(int lane) {
-  return 2 * ((lane & 7) >> 1) + 8 * (lane & 1) + ((lane >> 3) & 1);
+__device__ __forceinline__ int mx_k_key(int row) {  // the key in row 0..15 of a score fragment
+  const int q = (row & 7) >> 1, kind = (row & 1) | ((row >> 2) & 2);
+  return q + (kind == 0 ? 0 : kind == 1 ? 12 : kind == 2 ? 4 : 8);
 }
 // The fragments of a group's two m-tiles.  A lane has four elements d = 4g .. +3 of the
 // group of its four keys; m-tile h holds the elements 2h in its fragment rows 0-7, 2h + 1
 // in rows 8-15.
 __device__ __forceinline__ void mx_v_fragments(uint32_t lo, uint32_t hi, uint32_t (&va)[2][4]) {
-  // bytes of two keys' codes of one element: 0, 2 (keys 2q, 2q+1), 0, 2 (2q+8, 2q+9)
+  // bytes of two keys' codes of one element: 0, 2 (keys a, c), 0, 2 (b, d)
   const uint32_t ev = (lo & 0x0f0f0f0fu) | ((hi << 4) & 0xf0f0f0f0u);
   const uint32_t od = ((lo >> 4) & 0x0f0f0f0fu) | (hi & 0xf0f0f0f0u);  // and 1, 3
   e2m1x8_to_f16x2x4(ev, va[0][0], va[1][0], va[0][2], va[1][2]);
@@ -364,14 +341,20 @@ __global__ void __launch_bounds__(MxCfg<MR>::kThreads, MxCfg<MR>::kCtas)
   const int g = lane >> 2, q4 = lane & 3;
   const int R0 = warp * Cfg::kRows;
   const uint32_t smem_base = smem_u32(smem);
-  constexpr int KS = D / 16, MT = D / 16;  // k-steps, m-tiles
-  constexpr int NB = Cfg::kRows / 16;      // blocks of 16 rows, side by side
+  constexpr int KS = D / 16;           // k-steps of the scores
+  constexpr int NB = Cfg::kRows / 16;  // blocks of 16 rows, side by side
   // This lane's row in the ldmatrix of groups 0, 1 and of groups 2, 3 of a block of 16
-  // rows: matrices (rows 0-7, even group), (8-15, even), (0-7, odd), (8-15, odd).  And in
-  // the transposing one of V.
-  const uint32_t off[2] = {sw64(R0 + (lane & 15), lane >> 4), sw64(R0 + (lane & 15), 2 + (lane >> 4))};
-  const uint32_t voff[2] = {sw64(R0 + mx_v_row(lane), lane >> 4), sw64(R0 + mx_v_row(lane), 2 + (lane >> 4))};
-  float* red_ml = reinterpret_cast<float*>(smem + Cfg::kOffRedMl);
+  // rows: matrices (fragment rows 0-7, even group), (8-15, even), (0-7, odd), (8-15, odd);
+  // and in the transposing one of two blocks of V, this warp's group.
+  const int krow = R0 + mx_k_key(lane & 15);
+  const uint32_t off[2] = {sw64(krow, lane >> 4), sw64(krow, 2 + (lane >> 4))};
+  const uint32_t voff = Cfg::kTileBytes + sw64(16 * (lane >> 4) + mx_v_key(lane), warp);
+  const int key[2] = {mx_k_key(g), mx_k_key(g + 8)};  // of this lane's two score rows
+  float* red = reinterpret_cast<float*>(smem + Cfg::kOffRed);
+  // V scales: this lane makes the pairs of keys (q, 12 + q), (4 + q, 8 + q) of block lane / 4
+  const int vrow = 16 * g + q4;
+  uint8_t* vs_mine = smem + Cfg::kOffVs + warp * (2 * kKvTile) + ((g >> 1) * 4 + q4) * 16 + (g & 1) * 8;
+  const uint4* vs = reinterpret_cast<const uint4*>(smem + Cfg::kOffVs + warp * (2 * kKvTile)) + q4;
 
   int it = 0, ucount = 0;
   while (true) {
@@ -429,24 +412,20 @@ __global__ void __launch_bounds__(MxCfg<MR>::kThreads, MxCfg<MR>::kCtas)
       if (lane == 0) mbar_arrive(qempty);
       ++ucount;
     }
-    // O^T: m-tiles 2j and 2j + 1 are the elements of group j (mx_v_fragments)
-    float acc[MT][4];
+    // O^T of this warp's group of 32 elements (mx_v_fragments)
+    float acc[2][4];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    // Softmax references m_r (-inf: none yet; mu is 0 then), lazy: a score may pass its
+    for (int i = 0; i < 2; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    // Softmax references m_r, the warps' own copies of one (-inf: none yet; mu is 0 then), lazy: a score may pass its
     // column's by kOver.  They are kept kLift below the scores that set them, so that P,
     // at most 2^kOver, has fp16's bits down to 2^-(14 + kLift) of the largest.
     constexpr float kLift = 5.f, kOver = 13.f;
     float m_r[2] = {-INFINITY, -INFINITY}, mu[2] = {0.f, 0.f}, l_r[2] = {0.f, 0.f};
-    // V scale references, one for each group of 32 elements (0, 1 and 2, 3): the largest
-    // scale that the warp's tiles had so far.  V scales over them, at most 1, multiply P
-    // in fp16 (exact powers of two, down to 2^-24); O is kept over them.
-    __nv_bfloat162 vref[2], vinv[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      vref[k] = mx_pair(kMxRefMin << 7, kMxRefMin << 7);
-      vinv[k] = mx_pair((254 - kMxRefMin) << 7, (254 - kMxRefMin) << 7);
-    }
+    // The V scale reference: the largest scale of the group that the tiles had so far.  V
+    // scales over it, at most 1, multiply P in fp16 (exact powers of two, down to 2^-24); O
+    // is kept over it.
+    __nv_bfloat162 vref = mx_pair(kMxRefMin << 7, kMxRefMin << 7);
+    __nv_bfloat162 vinv = mx_pair((254 - kMxRefMin) << 7, (254 - kMxRefMin) << 7);
     // Keys that count as zeros in O whatever they hold: past kv_len, and between a band's
     // first tokens and its window.  (Codes are numbers all: a scale of 0 is enough.)
     const auto gone = [&](int j) {
@@ -459,39 +438,56 @@ __global__ void __launch_bounds__(MxCfg<MR>::kThreads, MxCfg<MR>::kCtas)
       wait_or_abort(&full[s], (it / S) & 1, a.err, misc);
       const uint32_t st = smem_base + s * Cfg::kStageBytes;
       const uint8_t* stp = smem + s * Cfg::kStageBytes;
-      const int jw = tile_at<X>(r, t_begin + tt) * kKvTile + R0;  // first KV row of this warp
+      const int jt = tile_at<X>(r, t_begin + tt) * kKvTile;
+      const int jw = jt + R0;  // first KV row of this warp
       const bool edge = (jw < r.lo_last) || (jw + Cfg::kRows - 1 > r.hi_first) || (MR && a.mask != nullptr);
-      if (X && !a.scores && (jw > r.hi || (jw >= a.first_tokens && jw + Cfg::kRows <= r.lo))) {
-        __syncwarp();  // no row sees any of them
-        if (lane == 0 && tt + 1 < ntile_here) mbar_arrive(&empty[s]);
-        continue;
-      }
-      // ---------------- scales: a lane takes those of one row ----------------
-      float vfct[4] = {1.f, 1.f, 1.f, 1.f};  // what O's groups are multiplied by
-      bool vmove;
+      // ---------------- scales ----------------
+      float vfct = 1.f;  // what O is multiplied by
       {
         const uint32_t* sc = reinterpret_cast<const uint32_t*>(stp + Cfg::kOffScale) + R0 + lane;
-        const uint32_t vw = gone(jw + lane) ? 0u : sc[kKvTile];
-        float kf[4];  // (NaN: the row's scores are NaN)
+        float kf[4];  // (K: a lane takes a row; NaN: the row's scores are NaN)
         e8m0x4_to_f32x4(sc[0], kf);
         *reinterpret_cast<float4*>(smem + Cfg::kOffKs + (R0 + lane) * 16) = make_float4(kf[0], kf[1], kf[2], kf[3]);
+        const uint8_t* sv = stp + Cfg::kOffScale + Cfg::kScaleBytes + vrow * 4 + warp;
+        uint32_t c[4] = {sv[0], sv[48], sv[16], sv[32]};  // keys q, 12 + q, 4 + q, 8 + q
+        if (jt + kKvTile > kvl || (X && jt + kKvTile > a.first_tokens))
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (gone(jt + vrow + (k == 0 ? 0 : k == 1 ? 12 : 4 * k - 4))) c[k] = 0u;
         __nv_bfloat162 v[2];
-        e8m0x4_to_bf16x2x2(vw, v);
-        vmove = mx_references(v, vref, vinv, vfct);
-        *reinterpret_cast<uint2*>(smem + Cfg::kOffVs + (R0 + lane) * 8) = mx_scale_pairs(v, vinv, lane);
+        e8m0x4_to_bf16x2x2(__byte_perm(c[0], c[1], 0x1140) | __byte_perm(c[2], c[3], 0x4011), v);
+        const auto bits = [](const __nv_bfloat162& x) { return *reinterpret_cast<const uint32_t*>(&x); };
+        // (the larger of two drops a NaN)
+        const __nv_bfloat162 most = __hmax2(__hmax2(v[0], v[1]), vref);
+        if (__any_sync(0xffffffffu, bits(most) != bits(vref))) {
+          const uint32_t old = (bits(vref) & 0xffffu) >> 7;
+          const uint32_t mine = max(bits(most) >> 23, (bits(most) & 0xffffu) >> 7);
+          const uint32_t now = min(__reduce_max_sync(0xffffffffu, mine), (uint32_t)kMxRefMax);
+          // (a jump past 2^-126 leaves a negligible old sum and gives 0)
+          vfct = __int_as_float(max(127 + (int)old - (int)now, 0) << 23);
+          vref = mx_pair(now << 7, now << 7);
+          vinv = mx_pair((254 - now) << 7, (254 - now) << 7);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[i][k] *= vfct;
+        }
+        float f[4];
+        bf16x2x2_to_f32x4(__hmul2(v[0], vinv), __hmul2(v[1], vinv), f);
+        *reinterpret_cast<uint2*>(vs_mine) = make_uint2(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]));
         __syncwarp();
       }
       // ---------------- S^T = K Q^T ----------------
-      const float4* ks = reinterpret_cast<const float4*>(smem + Cfg::kOffKs) + R0 + g;
-      float x[NB][4];  // keys g, g, g + 8, g + 8; columns 2q, 2q + 1, ...
+      const float4* ks = reinterpret_cast<const float4*>(smem + Cfg::kOffKs) + R0;
+      float x[NB][4];  // keys key[0], key[0], key[1], key[1]; columns 2q, 2q + 1, ...
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const float4 f0 = ks[16 * b], f1 = ks[16 * b + 8];
+        const float4 f0 = ks[16 * b + key[0]], f1 = ks[16 * b + key[1]];
         const float fa[4] = {f0.x, f0.y, f0.z, f0.w}, fb[4] = {f1.x, f1.y, f1.z, f1.w};
         x[b][0] = x[b][1] = x[b][2] = x[b][3] = 0.f;
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj) {  // groups 2*jj, 2*jj + 1
-          uint32_t w[4];  // (group 2*jj: rows g, g + 8), (group 2*jj + 1: ...), d = 8*q .. +7 of each
+          uint32_t w[4];  // (group 2*jj: both rows), (group 2*jj + 1: both), d = 8*q .. +7 of each
           ldsm_x4(st + off[jj] + 1024 * b, w[0], w[1], w[2], w[3]);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -511,12 +507,12 @@ __global__ void __launch_bounds__(MxCfg<MR>::kThreads, MxCfg<MR>::kCtas)
       }
       // ---------------- mask ----------------
       if (edge) {
-        const uint8_t* mk = stp + Cfg::kOffMask + R0 + g;
+        const uint8_t* mk = stp + Cfg::kOffMask + R0;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int e = k & 1, row = 16 * b + 8 * (k >> 1), j = jw + row + g;
+            const int e = k & 1, row = 16 * b + key[k >> 1], j = jw + row;
             bool ok = j >= loc[e];
             if (X) ok = ok || j < a.first_tokens;
             ok = ok && j <= hic[e];
@@ -531,7 +527,7 @@ __global__ void __launch_bounds__(MxCfg<MR>::kThreads, MxCfg<MR>::kCtas)
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int k = 0; k < 4; k += 2) {
-            const int j = jw + 16 * b + 4 * k + g;
+            const int j = jw + 16 * b + key[k >> 1];
             if (2 * q4 < r.ncols && j < end)
               *reinterpret_cast<float2*>(a.scores + (base + j) * a.score_cols + r.c0 + 2 * q4) =
                   make_float2(x[b][k] * slc, x[b][k + 1] * slc);
@@ -548,145 +544,114 @@ __global__ void __launch_bounds__(MxCfg<MR>::kThreads, MxCfg<MR>::kCtas)
         top[e] = mx * slc;
         over |= top[e] > m_r[e] + kOver;
       }
-      if (__any_sync(0xffffffffu, over) || vmove) {
-        float fct[2] = {1.f, 1.f};
+      // P^T in fp16, transposed (keys q, 12 + q and 4 + q, 8 + q of column g), to everyone
+      uint4* pm = reinterpret_cast<uint4*>(smem + Cfg::kOffP) + (it & 1) * (32 * W);
+      float sum[2];
+      const auto store_p = [&]() {
+        uint32_t pt[NB][2];
+        sum[0] = sum[1] = 0.f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          float pr[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            pr[k] = fast_exp2(fmaf(x[b][k], slc, -mu[k & 1]));
+            sum[k & 1] += pr[k];
+          }
+          pt[b][0] = movmatrix_t(pack_f16(pr[0], pr[1]));
+          pt[b][1] = movmatrix_t(pack_f16(pr[2], pr[3]));
+        }
+        pm[32 * warp + lane] = make_uint4(pt[0][0], pt[0][1], pt[1][0], pt[1][1]);
+      };
+      static_assert(NB == 2, "P's words");
+      store_p();
+      // (the other copy of P has been read by all when they are here)
+      if (named_bar_or(1, 32 * W, over)) {  // new references, and P again
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float mx = top[e];
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          if (g == 0) red[warp * 8 + 2 * q4 + e] = mx;
+        }
+        named_bar_sync(1, 32 * W);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = red[2 * q4 + e];
+#pragma unroll
+          for (int w2 = 1; w2 < W; ++w2) mx = fmaxf(mx, red[w2 * 8 + 2 * q4 + e]);
           const float mold = m_r[e];
           if (mx > mold + kOver) {
             m_r[e] = mu[e] = mx - kLift;
-            fct[e] = mold == -INFINITY ? 0.f : fast_exp2(mold - mu[e]);
-            l_r[e] *= fct[e];
+            const float f = mold == -INFINITY ? 0.f : fast_exp2(mold - mu[e]);
+            l_r[e] *= f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              acc[i][e] *= f;
+              acc[i][2 + e] *= f;
+            }
           }
         }
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[i][k] *= fct[k & 1] * vfct[i >> 1];
+        store_p();
+        named_bar_sync(1, 32 * W);
       }
-      // P^T in fp16, transposed: keys 2q, 2q+1 and 2q+8, 2q+9 of column g
-      uint32_t pt[NB][2];
+      l_r[0] += sum[0];
+      l_r[1] += sum[1];
+      // ---------------- O^T += V^T P^T, this warp's group, every row of the tile ----------------
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        float pr[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          pr[k] = fast_exp2(fmaf(x[b][k], slc, -mu[k & 1]));
-          l_r[k & 1] += pr[k];
-        }
-        pt[b][0] = movmatrix_t(pack_f16(pr[0], pr[1]));
-        pt[b][1] = movmatrix_t(pack_f16(pr[2], pr[3]));
-      }
-      // ---------------- O^T += V^T P^T ----------------
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        // the V scales of those keys, a pair for each group
-        const uint4* vp = reinterpret_cast<const uint4*>(smem + Cfg::kOffVs) + R0 / 2 + 8 * b + q4;
-        const uint4 s0 = vp[0], s1 = vp[4];
-        const uint32_t sa[4] = {s0.x, s0.y, s0.z, s0.w}, sb[4] = {s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-        for (int jj = 0; jj < 2; ++jj) {
-          uint32_t w[4];  // (group 2*jj: keys 2q, 2q+8), (keys 2q+1, 2q+9), (group 2*jj + 1: ...)
-          ldsm_x4_t(st + Cfg::kTileBytes + voff[jj] + 1024 * b, w[0], w[1], w[2], w[3]);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int j = 2 * jj + k;
-            uint32_t va[2][4];
-            mx_v_fragments(w[2 * k], w[2 * k + 1], va);
-            const uint32_t b0 = mul_f16x2(pt[b][0], sa[j]), b1 = mul_f16x2(pt[b][1], sb[j]);
-            mma_f16(acc[2 * j], va[0], b0, b1);
-            mma_f16(acc[2 * j + 1], va[1], b0, b1);
-          }
-        }
+      for (int b2 = 0; b2 < W; ++b2) {  // two blocks of 16
+        const uint4 pv = pm[32 * b2 + lane], sv = vs[4 * b2];
+        uint32_t w[4];  // (keys a, b), (c, d) of the first block, of the second
+        ldsm_x4_t(st + voff + 2048 * b2, w[0], w[1], w[2], w[3]);
+        uint32_t va[2][4];
+        mx_v_fragments(w[0], w[1], va);
+        uint32_t b0 = mul_f16x2(pv.x, sv.x), b1 = mul_f16x2(pv.y, sv.y);
+        mma_f16(acc[0], va[0], b0, b1);
+        mma_f16(acc[1], va[1], b0, b1);
+        mx_v_fragments(w[2], w[3], va);
+        b0 = mul_f16x2(pv.z, sv.z);
+        b1 = mul_f16x2(pv.w, sv.w);
+        mma_f16(acc[0], va[0], b0, b1);
+        mma_f16(acc[1], va[1], b0, b1);
       }
       __syncwarp();
-      if (lane == 0 && tt + 1 < ntile_here) mbar_arrive(&empty[s]);  // (the last: behind the merge)
+      if (lane == 0) mbar_arrive(&empty[s]);
     }
 
-    // ---------------- merge the warps' states ----------------
+    // ---------------- the columns' sums over the warps ----------------
+    float L[2] = {0.f, 0.f};
+    float* red_l = red + W * 8;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       l_r[e] += __shfl_xor_sync(0xffffffffu, l_r[e], 4);
       l_r[e] += __shfl_xor_sync(0xffffffffu, l_r[e], 8);
       l_r[e] += __shfl_xor_sync(0xffffffffu, l_r[e], 16);
+      if (g == 0) red_l[warp * 8 + 2 * q4 + e] = l_r[e];
     }
-    if (g == 0)
-      *reinterpret_cast<float4*>(red_ml + (warp * 8 + 2 * q4) * 2) = make_float4(m_r[0], l_r[0], m_r[1], l_r[1]);
     named_bar_sync(1, 32 * W);
-    float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f};
-    {
-      float4 ml[W];  // (m, l) of this lane's two columns
 #pragma unroll
-      for (int w2 = 0; w2 < W; ++w2) {
-        ml[w2] = *reinterpret_cast<const float4*>(red_ml + (w2 * 8 + 2 * q4) * 2);
-        M[0] = fmaxf(M[0], ml[w2].x);
-        M[1] = fmaxf(M[1], ml[w2].z);
-      }
+    for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int w2 = 0; w2 < W; ++w2) {
-        L[0] += ml[w2].x == -INFINITY ? 0.f : ml[w2].y * fast_exp2(ml[w2].x - M[0]);
-        L[1] += ml[w2].z == -INFINITY ? 0.f : ml[w2].w * fast_exp2(ml[w2].z - M[1]);
-      }
-      float back[4];
-      bf16x2x2_to_f32x4(vref[0], vref[1], back);
+      for (int w2 = 0; w2 < W; ++w2) L[e] += red_l[w2 * 8 + 2 * q4 + e];
+    const float back = __uint_as_float(*reinterpret_cast<const uint32_t*>(&vref) << 16);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float f = m_r[e] == -INFINITY ? 0.f : fast_exp2(m_r[e] - M[e]);
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          acc[i][e] *= f * back[i >> 1];
-          acc[i][2 + e] *= f * back[i >> 1];
-        }
-      }
-    }
-    // Warp w ends with m-tiles 2w and 2w + 1 (the elements of group w) summed over the
-    // warps: in each of two rounds every warp stores the four m-tiles 2k + round but its
-    // own, in the chunk's last stage, then adds the others' copies to its own.
-    float4 own[2];  // (d, column 2q), (d, 2q+1), (d+1, 2q), (d+1, 2q+1), d = 32 warp + 4 g + 2 round
-    own[0] = own[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (ntile_here > 0) {  // (else no stage, and nothing to add up)
-      const int s = (it + S - 1) % S;
-      float4* red4 = reinterpret_cast<float4*>(smem + s * Cfg::kStageBytes);
-#pragma unroll
-      for (int rnd = 0; rnd < 2; ++rnd) {
-        if (rnd > 0) named_bar_sync(1, 32 * W);  // the round before has been read
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float (&c)[4] = acc[2 * k + rnd];
-          const float4 mine = make_float4(c[0], c[1], c[2], c[3]);
-          if (k == warp) own[rnd] = mine;
-          else red4[(k * W + warp) * 32 + lane] = mine;
-        }
-        named_bar_sync(1, 32 * W);
-#pragma unroll
-        for (int w2 = 0; w2 < W; ++w2) {
-          if (w2 == warp) continue;
-          const float4 o = red4[(warp * W + w2) * 32 + lane];
-          own[rnd].x += o.x; own[rnd].y += o.y; own[rnd].z += o.z; own[rnd].w += o.w;
-        }
-      }
-      fence_proxy_async_smem();  // (the stage was written here; a copy will write it next)
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[s]);
-    }
+      for (int k = 0; k < 4; ++k) acc[i][k] *= back;
     const int64_t slot = min(max(slot0, (int64_t)0), a.max_chunks - 1);
     const int d = 32 * warp + 4 * g;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int hh = 2 * q4 + e;  // the unit's column
       if (hh >= r.ncols) continue;
-      const float4 o = e ? make_float4(own[0].y, own[0].w, own[1].y, own[1].w)
-                         : make_float4(own[0].x, own[0].z, own[1].x, own[1].z);
+      const float4 o = make_float4(acc[0][e], acc[0][2 + e], acc[1][e], acc[1][2 + e]);
       if (!split) {
         const int c = r.c0 + hh;
         const int i = c / a.G, h = r.hk * a.G + (c - i * a.G);
         const int64_t tok = (int64_t)r.qrow0 + i;
         float scl, lse;
-        finish_head(a, h, M[e], L[e], &scl, &lse);
+        finish_head(a, h, m_r[e], L[e], &scl, &lse);
         *reinterpret_cast<uint2*>(a.out + tok * a.out_stride + (int64_t)h * D + d) =
             make_uint2(pack_bf16(o.x * scl, o.y * scl), pack_bf16(o.z * scl, o.w * scl));
         if (a.lse && warp == 0 && g == 0)
@@ -696,7 +661,7 @@ __global__ void __launch_bounds__(MxCfg<MR>::kThreads, MxCfg<MR>::kCtas)
         float* col = a.partials + slot * (int64_t)a.GH * (D + 2) + (int64_t)hh * (D + 2);
         *reinterpret_cast<float2*>(col + d) = make_float2(o.x, o.y);
         *reinterpret_cast<float2*>(col + d + 2) = make_float2(o.z, o.w);
-        if (warp == 0 && g == 0) *reinterpret_cast<float2*>(col + D) = make_float2(M[e], L[e]);
+        if (warp == 0 && g == 0) *reinterpret_cast<float2*>(col + D) = make_float2(m_r[e], L[e]);
       }
     }
   }

@@ -9,6 +9,12 @@
 // whose loads are in flight together: weights times cosines and weights times sines are
 // made once for all of them, which leaves an element a product, a product and sum, and
 // the head's factor, in packed pairs of fp32.
+//
+// Measured: 8 prompts of 256 to 4096 tokens, 32 + 8 + 8 heads (375 MB) 70.2 us, 5.3 TB/s,
+// 0.79 of the measured copy rate; 4 of 256 to 2048 with 64 query heads into an FP8 cache
+// (122 MB) 29.1 us; 32 tokens 4.1 us, a launch.  Four rounds in blocks of 128 threads, at
+// least eight to an SM: blocks of 256 threads 73.5 us, of 64 71.6; with five or six blocks
+// of 256 to an SM for fewer registers 79.5 and 90.3; eight rounds 80, two 96.
 #include <cmath>
 
 #include "kv_cache.cuh"
