@@ -1,6 +1,8 @@
 """Pages assigned on the GPU, head norms with the rotation and the append in one pass, and
 whole serving steps."""
 import itertools
+import os
+import re
 
 import numpy as np
 import pytest
@@ -491,3 +493,31 @@ def test_a_captured_serving_step_replays():
     for a, b in zip(*outs):
         assert torch.equal(a, b)
     assert int(outs[0][2]) == nb - 6
+
+
+def test_the_readme_step():
+    """The README's step as it stands, against the calls' definitions."""
+    text = open(os.path.join(os.path.dirname(__file__), "..", "README.md")).read()
+    code = re.search(r"A serving step.*?```python\n(.*?)```", text, re.S).group(1)
+    B, QN, KVN, D, page, cap_pages = 2, 4, 2, 128, 32, 2
+    _, t = _serving_state("mx", B, KVN, D, page, cap_pages, 5, 0)
+    g = torch.Generator().manual_seed(72)
+    names = dict(fia=fia, k_codes=t[0], v_codes=t[1], k_scales=t[2], v_scales=t[3], block_table=t[4],
+                 lens=_i32([0] * B), held=_i32([0] * B), free_pages=_i32(range(5)), free_count=_i32([5]),
+                 page=page, cos_sin=serving.cos_sin(page * cap_pages, D).to(DEV),
+                 q_norm=torch.ones(D, dtype=torch.bfloat16, device=DEV), k_norm=None)
+    for n in range(1, 36):
+        x = torch.randn(B, 1, QN + 2 * KVN, D, generator=g).to(torch.bfloat16)
+        names["q_new"], names["k_new"], names["v_new"] = x.to(DEV).split((QN, KVN, KVN), 2)
+        exec(code, names)
+        assert names["lens"].tolist() == [n] * B and names["q"].shape == (B, 1, QN, D)
+        want, _ = serving.turned(x[:, 0, :QN], names["q_norm"], 1e-6, names["cos_sin"],
+                                 torch.full((B,), n - 1), False)
+        got = names["q"].cpu().double()[:, 0]
+        assert torch.all((got - want).abs() <= 2.0 ** -8 * want.abs() + 1e-5 * want.abs().max())
+        v = x[:, 0, QN + KVN:]
+        codes, scales = serving.mx_quantised(v)
+        at = names["slots"].long().cpu()
+        assert torch.equal(t[1].view(-1, KVN, D // 2).cpu()[at], torch.from_numpy(codes))
+        assert torch.equal(t[3].permute(0, 2, 1, 3).reshape(-1, KVN, D // 32).cpu()[at], torch.from_numpy(scales))
+    assert int(names["free_count"]) == 1
