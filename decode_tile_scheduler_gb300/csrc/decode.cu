@@ -383,14 +383,31 @@ __device__ __forceinline__ uint32_t pack_cost(int64_t cost, int ha) {
 // 63 of 512 204 -> 98 us, 64 of 512 to 32,768 FP8 keys 355 -> 182 us; with the
 // other rule for all unequal units the calls of shorter chunks lose up to a factor
 // of two (FP8, one of 65,536 keys among 15, window 8192: 18.5 -> 38 us).
+//
+// MXFP4, three CTAs to an SM, which a tile keeps busy by its instructions: a round of
+// chunks takes 7 units of 0.2 us a tile, the last one 6 or 5 where it leaves an SM two
+// CTAs or one; a chunk has a tile's time of its own, a split call 12 units.  Measured
+// (us): 16 sequences of a row, window 4096, by the rule above 41.0, so 32.8; of four rows
+// 55.9, 49.6; of 1 to 4 43.2, 43.0; window 1024 24.8, 24.7; 8 sequences, window 8192 41.3,
+// 41.6; 64 of a row 79.8, 78.4.  The other calls' rule: 32.8, 49.2, 48.8, 28.3, 45.4, 77.8.
 __device__ __forceinline__ int64_t window_chunk(const DecodeArgs& a, int64_t T, int cmax) {
   if (cmax < 1) return 1;
-  if (T > 0x7fffffffLL) return 0;  // (the other calls' rule counts in 64 bits)
+  // (the other calls' rule counts in 64 bits)
+  if (T > (a.ctas_per_sm > 1 ? 0x7ffffffLL : 0x7fffffffLL)) return 0;
   // (32-bit divisions: 64-bit ones cost the step half a microsecond)
   const uint32_t s = (threadIdx.x & 31) + 1, n = (uint32_t)a.num_ctas;
   const uint32_t z = ((uint32_t)cmax + s - 1) / s;
-  const uint32_t rounds = (((uint32_t)T + z - 1) / z + n - 1) / n;
-  const uint64_t time = (uint64_t)rounds * (5 * z + 13) + (s > 1 ? 13 : 0);  // fifths of a tile
+  uint64_t time;
+  if (a.ctas_per_sm > 1) {
+    const uint32_t parts = min(((uint32_t)cmax + z - 1) / z, 16u);  // chunks to a unit of cmax
+    const uint32_t chunks = ((uint32_t)T * parts + cmax - 1) / (uint32_t)cmax;
+    const uint32_t rounds = chunks / n, rest = 3 * (chunks - rounds * n);
+    const uint32_t per = 7 * rounds + (rest == 0 ? 0 : 5 + (rest > n) + (rest > 2 * n));
+    time = (uint64_t)per * (z + 1) + (s > 1 ? 12 : 0);
+  } else {
+    const uint32_t rounds = (((uint32_t)T + z - 1) / z + n - 1) / n;
+    time = (uint64_t)rounds * (5 * z + 13) + (s > 1 ? 13 : 0);  // fifths of a tile
+  }
   uint32_t key = 0xffffffffu;
   if (s <= 16 && s <= (uint32_t)cmax && (s == 1 || a.num_units * s <= a.max_chunks))
     key = (uint32_t)min(time, (uint64_t)0x3ffffff) * 32 + s;

@@ -5,9 +5,13 @@
 // widen, so the kernel is bound by the instructions of an element, not by memory.  What
 // it does about that:
 //  - Three CTAs to an SM, each with one producer warp and four consumer warps, so that a
-//    chunk's set-up and waits run beside the others' products.  Units have 8 columns: 16
-//    widen the codes once for both halves, but took 52 us where 8 took 45 (16 sequences,
-//    1 to 4 rows of 4 heads).
+//    chunk's set-up and waits run beside the others' products.
+//  - Units of 16 columns (NG = 2) where a KV head has more than 8 widen the codes once for
+//    both halves: 32 sequences of 512 to 4096 keys, 16 columns 51.6 us for 58.6, 128 query
+//    heads 49.2 for 58.3; 16 sequences of 2 to 16 k keys with 1 to 4 rows of 4 heads 63.6
+//    for 71.7.  Window calls keep 8: of few tiles a unit, many of them edges, 64 sequences,
+//    window 1024, 1 to 4 rows 54.4 us where 16 columns took 66.1 (window 4096, four rows:
+//    49.6 where 16 take 45.1).
 //  - S^T = K Q^T: a warp has 32 of a tile's rows.  O^T = V^T P^T: it has 32 of the 128
 //    elements, the ones under one scale, and all rows; P goes through shared memory, twice
 //    (one barrier a tile).  So O is 8 registers a lane and needs no merge behind a chunk
@@ -35,7 +39,7 @@
 namespace fia {
 namespace {
 
-template <bool MR>
+template <bool MR, int NG>
 struct MxCfg {
   static constexpr int D = 128, kRowBytes = D / 2;
   static constexpr int kWarps = 4, kRows = kKvTile / kWarps;  // consumers, rows of a tile each
@@ -45,18 +49,20 @@ struct MxCfg {
   static constexpr int kScaleBytes = kKvTile * 4;
   static constexpr int kOffScale = 2 * kTileBytes, kOffMask = kOffScale + 2 * kScaleBytes;
   static constexpr int kStageBytes = kOffMask + (MR ? kDecodeMaxRows * kKvTile : 0);
-  static constexpr int kStages = 3;
-  static constexpr int kQBytes = 8 * D * 2;
+  static constexpr int kStages = NG == 2 ? 2 : 3;
+  static constexpr int kQBytes = 8 * NG * D * 2;
   static constexpr int kOffQ = kStages * kStageBytes;
-  // P^T of a tile for everyone, twice: the B fragments of a warp's rows, 16 bytes a lane
-  static constexpr int kOffP = kOffQ + kQBytes;
+  // P^T of a tile for everyone, twice: the B fragments of a warp's rows, 16 bytes a lane and
+  // half of the columns
+  static constexpr int kOffQs = kOffQ + kQBytes;  // NG 2: the fragments of Q, in fp16
+  static constexpr int kOffP = kOffQs + (NG == 2 ? kQBytes : 0);
   // a tile's scales as the products take them: K's of a row as four floats; V's, a copy of
   // 128 rows for each warp and its group, as fp16 pairs
-  static constexpr int kOffKs = kOffP + 2 * kWarps * 32 * 16;
+  static constexpr int kOffKs = kOffP + 2 * NG * kWarps * 32 * 16;
   static constexpr int kOffVs = kOffKs + kKvTile * 16;
-  // the warps' largest scores and sums of 8 columns
+  // the warps' largest scores and sums of the columns
   static constexpr int kOffRed = kOffVs + kWarps * kKvTile * 2;
-  static constexpr int kOffBar = kOffRed + 2 * kWarps * 8 * 4;
+  static constexpr int kOffBar = kOffRed + 2 * kWarps * 8 * NG * 4;
   static constexpr int kOffMsg = (kOffBar + 8 * (2 * kStages + 2) + 15) / 16 * 16;
   static constexpr int kOffMisc = kOffMsg + 128;
   static constexpr int kSmem = kOffMisc + 16 + 512;           // + alignment slack (a swizzle's 512 bytes)
@@ -124,12 +130,12 @@ __device__ __forceinline__ void mx_v_fragments(uint32_t lo, uint32_t hi, uint32_
   e2m1x8_to_f16x2x4(od, va[0][1], va[1][1], va[0][3], va[1][3]);
 }
 
-// MR, X: as decode_kernel's.
-template <bool MR, bool X>
-__global__ void __launch_bounds__(MxCfg<MR>::kThreads, MxCfg<MR>::kCtas)
+// NG: halves of 8 columns; MR, X: as decode_kernel's.
+template <int NG, bool MR, bool X>
+__global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
     decode_mx_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tk,
                      const __grid_constant__ CUtensorMap tv) {
-  using Cfg = MxCfg<MR>;
+  using Cfg = MxCfg<MR, NG>;
   constexpr int D = Cfg::D, S = Cfg::kStages, W = Cfg::kWarps;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 511) &
@@ -366,61 +372,73 @@ __global__ void __launch_bounds__(MxCfg<MR>::kThreads, MxCfg<MR>::kCtas)
     const int64_t slot0 = msg.slot;
     const int t_begin = msg.t_begin, t_end = msg.t_end;
     const bool split = msg.nch > 1;
-    // keys seen by this lane's two columns, and their mask rows
-    int loc[2], hic[2], mrow[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if constexpr (MR) {
-        const int i = (r.c0 + min(2 * q4 + e, max(r.ncols, 1) - 1)) / a.G;
-        row_bounds(a, r.q_len, kvl, i, &loc[e], &hic[e]);
-        mrow[e] = (i - r.c0 / a.G) * kKvTile;
-      } else {
-        loc[e] = r.lo;
-        hic[e] = r.hi;
-        mrow[e] = 0;
-      }
-    }
+    const bool two = NG == 2 && r.ncols > 8;  // (columns in the second half)
     // Q^T fragments in fp16, times a power of two that puts the unit's largest element at
     // exponent 15 (decode_kernel tells why); k-step kk = 2*group + j covers
     // d = 32*group + 8*q + 4*j + {0..3}
-    uint32_t qb[KS][2];
+    uint32_t qb[NG][KS][2];
     float slc;
     {
       const uint16_t* qsm = reinterpret_cast<const uint16_t*>(smem + Cfg::kOffQ) + g * D + 8 * q4;
       uint32_t top = 0;  // (bf16 magnitudes order as integers)
 #pragma unroll
-      for (int kk = 0; kk < KS; ++kk) {
-        uint2 v = make_uint2(0u, 0u);
-        if (g < r.ncols) v = *reinterpret_cast<const uint2*>(qsm + (kk >> 1) * 32 + 4 * (kk & 1));
-        qb[kk][0] = v.x;
-        qb[kk][1] = v.y;
-        top = __vmaxu2(top, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu));
-      }
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int kk = 0; kk < KS; ++kk) {
+          uint2 v = make_uint2(0u, 0u);
+          if (8 * n + g < r.ncols)
+            v = *reinterpret_cast<const uint2*>(qsm + 8 * n * D + (kk >> 1) * 32 + 4 * (kk & 1));
+          qb[n][kk][0] = v.x;
+          qb[n][kk][1] = v.y;
+          top = __vmaxu2(top, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu));
+        }
       const uint32_t emax = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu)) >> 7;
       const int sh = min(max(142 - (int)emax, -100), 100);  // 15 - (emax - 127)
       // (the score factor is positive, its sign in the queries: hidden scores stay -inf)
       const float up = copysignf(__int_as_float((127 + sh) << 23), a.scale_log2);
       slc = fmaxf(fabsf(a.scale_log2) * __int_as_float((127 - sh) << 23), 1e-36f);
 #pragma unroll
-      for (int kk = 0; kk < KS; ++kk)
+      for (int n = 0; n < NG; ++n)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t v = qb[kk][k];
-          qb[kk][k] = pack_f16(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up);
-        }
+        for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t v = qb[n][kk][k];
+            qb[n][kk][k] = pack_f16(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up);
+          }
+      if constexpr (NG == 2) {  // (the four warps' fragments are the same: each keeps a quarter)
+        uint4* qs = reinterpret_cast<uint4*>(smem + Cfg::kOffQs) + lane;
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int j = 0; j < KS / 2; ++j)
+            if (j == warp)
+              qs[32 * (n * (KS / 2) + j)] =
+                  make_uint4(qb[n][2 * j][0], qb[n][2 * j][1], qb[n][2 * j + 1][0], qb[n][2 * j + 1][1]);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(qempty);
       ++ucount;
+      if constexpr (NG == 2) named_bar_sync(1, 32 * W);
     }
     // O^T of this warp's group of 32 elements (mx_v_fragments)
-    float acc[2][4];
+    float acc[NG][2][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    for (int n = 0; n < NG; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) acc[n][i][0] = acc[n][i][1] = acc[n][i][2] = acc[n][i][3] = 0.f;
     // Softmax references m_r, the warps' own copies of one (-inf: none yet; mu is 0 then), lazy: a score may pass its
     // column's by kOver.  They are kept kLift below the scores that set them, so that P,
     // at most 2^kOver, has fp16's bits down to 2^-(14 + kLift) of the largest.
     constexpr float kLift = 5.f, kOver = 13.f;
-    float m_r[2] = {-INFINITY, -INFINITY}, mu[2] = {0.f, 0.f}, l_r[2] = {0.f, 0.f};
+    float m_r[NG][2], mu[NG][2], l_r[NG][2];
+#pragma unroll
+    for (int n = 0; n < NG; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m_r[n][e] = -INFINITY;
+        mu[n][e] = l_r[n][e] = 0.f;
+      }
     // The V scale reference: the largest scale of the group that the tiles had so far.  V
     // scales over it, at most 1, multiply P in fp16 (exact powers of two, down to 2^-24); O
     // is kept over it.
@@ -468,9 +486,11 @@ __global__ void __launch_bounds__(MxCfg<MR>::kThreads, MxCfg<MR>::kCtas)
           vref = mx_pair(now << 7, now << 7);
           vinv = mx_pair((254 - now) << 7, (254 - now) << 7);
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int n = 0; n < NG; ++n)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) acc[i][k] *= vfct;
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) acc[n][i][k] *= vfct;
         }
         float f[4];
         bf16x2x2_to_f32x4(__hmul2(v[0], vinv), __hmul2(v[1], vinv), f);
@@ -479,12 +499,13 @@ __global__ void __launch_bounds__(MxCfg<MR>::kThreads, MxCfg<MR>::kCtas)
       }
       // ---------------- S^T = K Q^T ----------------
       const float4* ks = reinterpret_cast<const float4*>(smem + Cfg::kOffKs) + R0;
-      float x[NB][4];  // keys key[0], key[0], key[1], key[1]; columns 2q, 2q + 1, ...
+      float x[NG][NB][4];  // keys key[0], key[0], key[1], key[1]; columns 2q, 2q + 1, ...
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const float4 f0 = ks[16 * b + key[0]], f1 = ks[16 * b + key[1]];
         const float fa[4] = {f0.x, f0.y, f0.z, f0.w}, fb[4] = {f1.x, f1.y, f1.z, f1.w};
-        x[b][0] = x[b][1] = x[b][2] = x[b][3] = 0.f;
+#pragma unroll
+        for (int n = 0; n < NG; ++n) x[n][b][0] = x[n][b][1] = x[n][b][2] = x[n][b][3] = 0.f;
 #pragma unroll
         for (int jj = 0; jj < 2; ++jj) {  // groups 2*jj, 2*jj + 1
           uint32_t w[4];  // (group 2*jj: both rows), (group 2*jj + 1: both), d = 8*q .. +7 of each
@@ -495,13 +516,23 @@ __global__ void __launch_bounds__(MxCfg<MR>::kThreads, MxCfg<MR>::kCtas)
             uint32_t ka[2][4];
             e2m1x8_to_f16x2x4(w[2 * k], ka[0][0], ka[0][2], ka[1][0], ka[1][2]);
             e2m1x8_to_f16x2x4(w[2 * k + 1], ka[0][1], ka[0][3], ka[1][1], ka[1][3]);
-            float s4[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(s4, ka[0], qb[2 * j][0], qb[2 * j][1]);
-            mma_f16(s4, ka[1], qb[2 * j + 1][0], qb[2 * j + 1][1]);
-            x[b][0] += s4[0] * fa[j];
-            x[b][1] += s4[1] * fa[j];
-            x[b][2] += s4[2] * fb[j];
-            x[b][3] += s4[3] * fb[j];
+#pragma unroll
+            for (int n = 0; n < NG; ++n) {
+              if (n && !two) break;
+              float s4[4] = {0.f, 0.f, 0.f, 0.f};
+              if constexpr (NG == 2) {
+                const uint4 qv = reinterpret_cast<const uint4*>(smem + Cfg::kOffQs)[32 * (n * (KS / 2) + j) + lane];
+                mma_f16(s4, ka[0], qv.x, qv.y);
+                mma_f16(s4, ka[1], qv.z, qv.w);
+              } else {
+                mma_f16(s4, ka[0], qb[n][2 * j][0], qb[n][2 * j][1]);
+                mma_f16(s4, ka[1], qb[n][2 * j + 1][0], qb[n][2 * j + 1][1]);
+              }
+              x[n][b][0] += s4[0] * fa[j];
+              x[n][b][1] += s4[1] * fa[j];
+              x[n][b][2] += s4[2] * fb[j];
+              x[n][b][3] += s4[3] * fb[j];
+            }
           }
         }
       }
@@ -509,149 +540,187 @@ __global__ void __launch_bounds__(MxCfg<MR>::kThreads, MxCfg<MR>::kCtas)
       if (edge) {
         const uint8_t* mk = stp + Cfg::kOffMask + R0;
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int n = 0; n < NG; ++n)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int e = k & 1, row = 16 * b + key[k >> 1], j = jw + row;
-            bool ok = j >= loc[e];
-            if (X) ok = ok || j < a.first_tokens;
-            ok = ok && j <= hic[e];
-            if (MR && a.mask) ok = ok && mk[mrow[e] + row] == 0;
-            if (!ok) x[b][k] = -INFINITY;
+          for (int e = 0; e < 2; ++e) {  // column 2q + e of the half
+            int lo = r.lo, hi = r.hi, mrow = 0;  // the keys it sees, its mask row
+            if constexpr (MR) {
+              const int i = (r.c0 + min(8 * n + 2 * q4 + e, max(r.ncols, 1) - 1)) / a.G;
+              row_bounds(a, r.q_len, kvl, i, &lo, &hi);
+              mrow = (i - r.c0 / a.G) * kKvTile;
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int k = e; k < 4; k += 2) {
+                const int row = 16 * b + key[k >> 1], j = jw + row;
+                bool ok = j >= lo;
+                if (X) ok = ok || j < a.first_tokens;
+                ok = ok && j <= hi;
+                if (MR && a.mask) ok = ok && mk[mrow + row] == 0;
+                if (!ok) x[n][b][k] = -INFINITY;
+              }
           }
       }
       if (X && a.scores) {  // (decode_kernel: key weights)
         const int64_t base = ((int64_t)r.b * a.KVN + r.hk) * a.S_kv;
         const int end = min(kvl, a.S_kv);
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int n = 0; n < NG; ++n)
 #pragma unroll
-          for (int k = 0; k < 4; k += 2) {
-            const int j = jw + 16 * b + key[k >> 1];
-            if (2 * q4 < r.ncols && j < end)
-              *reinterpret_cast<float2*>(a.scores + (base + j) * a.score_cols + r.c0 + 2 * q4) =
-                  make_float2(x[b][k] * slc, x[b][k + 1] * slc);
-          }
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+              const int j = jw + 16 * b + key[k >> 1], c = 8 * n + 2 * q4;
+              if (c < r.ncols && j < end)
+                *reinterpret_cast<float2*>(a.scores + (base + j) * a.score_cols + r.c0 + c) =
+                    make_float2(x[n][b][k] * slc, x[n][b][k + 1] * slc);
+            }
       }
       // ---------------- online softmax per column ----------------
-      float top[2];
+      float top[NG][2];
       bool over = false;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float mx = fmaxf(x[0][e], x[0][2 + e]);
+      for (int n = 0; n < NG; ++n)
 #pragma unroll
-        for (int b = 1; b < NB; ++b) mx = fmaxf(mx, fmaxf(x[b][e], x[b][2 + e]));
-        top[e] = mx * slc;
-        over |= top[e] > m_r[e] + kOver;
-      }
-      // P^T in fp16, transposed (keys q, 12 + q and 4 + q, 8 + q of column g), to everyone
-      uint4* pm = reinterpret_cast<uint4*>(smem + Cfg::kOffP) + (it & 1) * (32 * W);
-      float sum[2];
-      const auto store_p = [&]() {
-        uint32_t pt[NB][2];
-        sum[0] = sum[1] = 0.f;
+        for (int e = 0; e < 2; ++e) {
+          float mx = fmaxf(x[n][0][e], x[n][0][2 + e]);
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          float pr[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            pr[k] = fast_exp2(fmaf(x[b][k], slc, -mu[k & 1]));
-            sum[k & 1] += pr[k];
-          }
-          pt[b][0] = movmatrix_t(pack_f16(pr[0], pr[1]));
-          pt[b][1] = movmatrix_t(pack_f16(pr[2], pr[3]));
+          for (int b = 1; b < NB; ++b) mx = fmaxf(mx, fmaxf(x[n][b][e], x[n][b][2 + e]));
+          top[n][e] = mx * slc;
+          over |= top[n][e] > m_r[n][e] + kOver;
         }
-        pm[32 * warp + lane] = make_uint4(pt[0][0], pt[0][1], pt[1][0], pt[1][1]);
+      // P^T in fp16, transposed (keys q, 12 + q and 4 + q, 8 + q of column g), to everyone
+      uint4* pm = reinterpret_cast<uint4*>(smem + Cfg::kOffP) + (it & 1) * (NG * 32 * W);
+      float sum[NG][2];
+      const auto store_p = [&]() {
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          sum[n][0] = sum[n][1] = 0.f;
+          if (n && !two) break;
+          uint32_t pt[NB][2];
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            float pr[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              pr[k] = fast_exp2(fmaf(x[n][b][k], slc, -mu[n][k & 1]));
+              sum[n][k & 1] += pr[k];
+            }
+            pt[b][0] = movmatrix_t(pack_f16(pr[0], pr[1]));
+            pt[b][1] = movmatrix_t(pack_f16(pr[2], pr[3]));
+          }
+          pm[32 * (W * n + warp) + lane] = make_uint4(pt[0][0], pt[0][1], pt[1][0], pt[1][1]);
+        }
       };
       static_assert(NB == 2, "P's words");
       store_p();
       // (the other copy of P has been read by all when they are here)
       if (named_bar_or(1, 32 * W, over)) {  // new references, and P again
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float mx = top[e];
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          if (g == 0) red[warp * 8 + 2 * q4 + e] = mx;
-        }
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float mx = top[n][e];
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            if (g == 0) red[(warp * NG + n) * 8 + 2 * q4 + e] = mx;
+          }
         named_bar_sync(1, 32 * W);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float mx = red[2 * q4 + e];
+        for (int n = 0; n < NG; ++n)
 #pragma unroll
-          for (int w2 = 1; w2 < W; ++w2) mx = fmaxf(mx, red[w2 * 8 + 2 * q4 + e]);
-          const float mold = m_r[e];
-          if (mx > mold + kOver) {
-            m_r[e] = mu[e] = mx - kLift;
-            const float f = mold == -INFINITY ? 0.f : fast_exp2(mold - mu[e]);
-            l_r[e] *= f;
+          for (int e = 0; e < 2; ++e) {
+            float mx = red[n * 8 + 2 * q4 + e];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              acc[i][e] *= f;
-              acc[i][2 + e] *= f;
+            for (int w2 = 1; w2 < W; ++w2) mx = fmaxf(mx, red[(w2 * NG + n) * 8 + 2 * q4 + e]);
+            const float mold = m_r[n][e];
+            if (mx > mold + kOver) {
+              m_r[n][e] = mu[n][e] = mx - kLift;
+              const float f = mold == -INFINITY ? 0.f : fast_exp2(mold - mu[n][e]);
+              l_r[n][e] *= f;
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                acc[n][i][e] *= f;
+                acc[n][i][2 + e] *= f;
+              }
             }
           }
-        }
         store_p();
         named_bar_sync(1, 32 * W);
       }
-      l_r[0] += sum[0];
-      l_r[1] += sum[1];
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) l_r[n][e] += sum[n][e];
       // ---------------- O^T += V^T P^T, this warp's group, every row of the tile ----------------
 #pragma unroll
       for (int b2 = 0; b2 < W; ++b2) {  // two blocks of 16
-        const uint4 pv = pm[32 * b2 + lane], sv = vs[4 * b2];
+        const uint4 sv = vs[4 * b2];
         uint32_t w[4];  // (keys a, b), (c, d) of the first block, of the second
         ldsm_x4_t(st + voff + 2048 * b2, w[0], w[1], w[2], w[3]);
-        uint32_t va[2][4];
-        mx_v_fragments(w[0], w[1], va);
-        uint32_t b0 = mul_f16x2(pv.x, sv.x), b1 = mul_f16x2(pv.y, sv.y);
-        mma_f16(acc[0], va[0], b0, b1);
-        mma_f16(acc[1], va[1], b0, b1);
-        mx_v_fragments(w[2], w[3], va);
-        b0 = mul_f16x2(pv.z, sv.z);
-        b1 = mul_f16x2(pv.w, sv.w);
-        mma_f16(acc[0], va[0], b0, b1);
-        mma_f16(acc[1], va[1], b0, b1);
+        uint32_t va[2][2][4];
+        mx_v_fragments(w[0], w[1], va[0]);
+        mx_v_fragments(w[2], w[3], va[1]);
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          if (n && !two) break;
+          const uint4 pv = pm[32 * (W * n + b2) + lane];
+          uint32_t b0 = mul_f16x2(pv.x, sv.x), b1 = mul_f16x2(pv.y, sv.y);
+          mma_f16(acc[n][0], va[0][0], b0, b1);
+          mma_f16(acc[n][1], va[0][1], b0, b1);
+          b0 = mul_f16x2(pv.z, sv.z);
+          b1 = mul_f16x2(pv.w, sv.w);
+          mma_f16(acc[n][0], va[1][0], b0, b1);
+          mma_f16(acc[n][1], va[1][1], b0, b1);
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
     }
 
     // ---------------- the columns' sums over the warps ----------------
-    float L[2] = {0.f, 0.f};
-    float* red_l = red + W * 8;
+    float L[NG][2];
+    float* red_l = red + W * NG * 8;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      l_r[e] += __shfl_xor_sync(0xffffffffu, l_r[e], 4);
-      l_r[e] += __shfl_xor_sync(0xffffffffu, l_r[e], 8);
-      l_r[e] += __shfl_xor_sync(0xffffffffu, l_r[e], 16);
-      if (g == 0) red_l[warp * 8 + 2 * q4 + e] = l_r[e];
-    }
+    for (int n = 0; n < NG; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float l = l_r[n][e];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (g == 0) red_l[(warp * NG + n) * 8 + 2 * q4 + e] = l;
+      }
     named_bar_sync(1, 32 * W);
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-#pragma unroll
-      for (int w2 = 0; w2 < W; ++w2) L[e] += red_l[w2 * 8 + 2 * q4 + e];
     const float back = __uint_as_float(*reinterpret_cast<const uint32_t*>(&vref) << 16);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int n = 0; n < NG; ++n) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) acc[i][k] *= back;
+      for (int e = 0; e < 2; ++e) {
+        L[n][e] = 0.f;
+#pragma unroll
+        for (int w2 = 0; w2 < W; ++w2) L[n][e] += red_l[(w2 * NG + n) * 8 + 2 * q4 + e];
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[n][i][k] *= back;
+    }
     const int64_t slot = min(max(slot0, (int64_t)0), a.max_chunks - 1);
     const int d = 32 * warp + 4 * g;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int hh = 2 * q4 + e;  // the unit's column
+    for (int k = 0; k < 2 * NG; ++k) {
+      const int n = k >> 1, e = k & 1, hh = 8 * n + 2 * q4 + e;  // the unit's column
       if (hh >= r.ncols) continue;
-      const float4 o = make_float4(acc[0][e], acc[0][2 + e], acc[1][e], acc[1][2 + e]);
+      const float4 o = make_float4(acc[n][0][e], acc[n][0][2 + e], acc[n][1][e], acc[n][1][2 + e]);
       if (!split) {
         const int c = r.c0 + hh;
         const int i = c / a.G, h = r.hk * a.G + (c - i * a.G);
         const int64_t tok = (int64_t)r.qrow0 + i;
         float scl, lse;
-        finish_head(a, h, m_r[e], L[e], &scl, &lse);
+        finish_head(a, h, m_r[n][e], L[n][e], &scl, &lse);
         *reinterpret_cast<uint2*>(a.out + tok * a.out_stride + (int64_t)h * D + d) =
             make_uint2(pack_bf16(o.x * scl, o.y * scl), pack_bf16(o.z * scl, o.w * scl));
         if (a.lse && warp == 0 && g == 0)
@@ -661,16 +730,16 @@ __global__ void __launch_bounds__(MxCfg<MR>::kThreads, MxCfg<MR>::kCtas)
         float* col = a.partials + slot * (int64_t)a.GH * (D + 2) + (int64_t)hh * (D + 2);
         *reinterpret_cast<float2*>(col + d) = make_float2(o.x, o.y);
         *reinterpret_cast<float2*>(col + d + 2) = make_float2(o.z, o.w);
-        if (warp == 0 && g == 0) *reinterpret_cast<float2*>(col + D) = make_float2(m_r[e], L[e]);
+        if (warp == 0 && g == 0) *reinterpret_cast<float2*>(col + D) = make_float2(m_r[n][e], L[n][e]);
       }
     }
   }
 }
 
-template <bool MR, bool X>
+template <int NG, bool MR, bool X>
 cudaError_t launch_mx_t(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
-  using Cfg = MxCfg<MR>;
-  auto kern = decode_mx_kernel<MR, X>;
+  using Cfg = MxCfg<MR, NG>;
+  auto kern = decode_mx_kernel<NG, MR, X>;
   static std::atomic<uint64_t> done_mask[4];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -684,16 +753,21 @@ cudaError_t launch_mx_t(const DecodeArgs& a, const CUtensorMap& tk, const CUtens
   return launch_pdl(kern, dim3(a.num_ctas), dim3(Cfg::kThreads), Cfg::kSmem, s, a, tk, tv);
 }
 
+template <int NG>
+cudaError_t launch_mx(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  const bool mr = a.S_max > 1 || a.mask != nullptr;
+  if (a.first_tokens > 0 || a.scores)
+    return mr ? launch_mx_t<NG, true, true>(a, tk, tv, s) : launch_mx_t<NG, false, true>(a, tk, tv, s);
+  return mr ? launch_mx_t<NG, true, false>(a, tk, tv, s) : launch_mx_t<NG, false, false>(a, tk, tv, s);
+}
+
 }  // namespace
 
-int decode_mx_ctas() { return MxCfg<false>::kCtas; }
+int decode_mx_ctas() { return MxCfg<false, 1>::kCtas; }
 
 static cudaError_t launch_decode_mx(const DecodeArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
                                     cudaStream_t s) {
-  const bool mr = a.S_max > 1 || a.mask != nullptr;
-  if (a.first_tokens > 0 || a.scores)
-    return mr ? launch_mx_t<true, true>(a, tk, tv, s) : launch_mx_t<false, true>(a, tk, tv, s);
-  return mr ? launch_mx_t<true, false>(a, tk, tv, s) : launch_mx_t<false, false>(a, tk, tv, s);
+  return a.GH == 16 ? launch_mx<2>(a, tk, tv, s) : launch_mx<1>(a, tk, tv, s);
 }
 
 }  // namespace fia

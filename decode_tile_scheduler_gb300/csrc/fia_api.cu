@@ -249,7 +249,7 @@ fia_status decode_plan(const fia_params* p, DecodePlan* pl) {
   if (st != FIA_OK) return st;
   const int G = p->num_q_heads / p->num_kv_heads;
   const int cols = p->max_seqlen_q * G;  // (query row, head) columns of a KV head
-  const int GH = decode_group_heads(p->max_seqlen_q, cols, p->kv_dtype == FIA_KV_MXFP4);
+  const int GH = decode_group_heads(p->max_seqlen_q, cols, p->kv_dtype == FIA_KV_MXFP4, p->first_tokens > 0);
   const int HG = (int)ceil_div(cols, GH);
   if (p->kv_dtype == FIA_KV_MXFP4) n *= decode_mx_ctas();  // (several CTAs to an SM)
   pl->n = n;
@@ -278,7 +278,8 @@ DecodeArgs decode_args(const fia_params* p, const DecodePlan& pl, void* ws) {
   a.KVN = p->num_kv_heads;
   a.D = p->head_dim;
   a.G = G;
-  a.GH = decode_group_heads(p->max_seqlen_q, p->max_seqlen_q * G, p->kv_dtype == FIA_KV_MXFP4);
+  a.GH = decode_group_heads(p->max_seqlen_q, p->max_seqlen_q * G, p->kv_dtype == FIA_KV_MXFP4,
+                            p->first_tokens > 0);
   a.HG = (int)ceil_div(p->max_seqlen_q * G, a.GH);
   a.layout = p->layout;
   a.S_q = p->layout == FIA_LAYOUT_BSND ? p->max_seqlen_q : 1;
@@ -315,6 +316,7 @@ DecodeArgs decode_args(const fia_params* p, const DecodePlan& pl, void* ws) {
   a.num_units = pl.U;
   a.chunks_per_cta = pl.W;
   a.small_div = decode_small_div(p);
+  a.ctas_per_sm = p->kv_dtype == FIA_KV_MXFP4 ? decode_mx_ctas() : 1;
   a.small_min = p->kv_dtype == FIA_KV_MXFP4 ? 6 : 1;
   a.max_chunks = pl.max_chunks;
   char* w = static_cast<char*>(ws);

@@ -35,9 +35,10 @@ constexpr int kDecodeMaxRows = 16; // query rows per sequence the decode kernel 
 // 4-row GQA-4 decode: 92.2 against 100.4 us per execute while 16-column
 // units spilled registers; the same, 88.0 against 88.2 us, once the
 // consumers had 208 registers).
-// (MXFP4: always 8; decode_mx.cuh tells why.)
-inline int decode_group_heads(int rows, int cols, bool mx) {
-  return rows == 1 && cols > 8 && !mx ? 16 : 8;
+// (MXFP4: 16 for more than 8 columns, whose codes are then widened once, except in a
+// window call; decode_mx.cuh has both sides' times.)
+inline int decode_group_heads(int rows, int cols, bool mx, bool window) {
+  return cols > 8 && (mx ? !window : rows == 1) ? 16 : 8;
 }
 
 // Whether two arrays of `rows` rows, `stride` 4-byte elements apart, share an element
@@ -86,6 +87,7 @@ struct DecodeArgs {
   int num_ctas;
   int chunks_per_cta;          // W: the chunk size aims at W chunks per CTA
   int small_div;               // small chunks of ceil(C / small_div) tiles (2; 1 for FP8 or rows > 1)
+  int ctas_per_sm;             // 3 for MXFP4, else 1 (window_chunk)
   int small_min;               // tiles of a small chunk at least, where C has them (MXFP4: 6, else 1)
   int64_t num_units;           // B * KVN * HG
   int64_t max_chunks;          // partial slots: a bound on the number of chunks

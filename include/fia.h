@@ -607,8 +607,8 @@ fia_status fia_selftest_bounded_wait(int32_t *status, uint64_t limit_ns, void *s
  *
  * Decode schedule (written by fia_plan): the columns of a KV head are its
  * (query row, query head) pairs, S*G of them (S = max_seqlen_q <= 16), taken
- * in groups of GH = 16 (S = 1 and G > 8, not MXFP4), else 8; work unit
- * u = (b, kv head, group),
+ * in groups of GH = 16 (more than 8 columns with S = 1, or over MXFP4 without
+ * first_tokens), else 8; work unit u = (b, kv head, group),
  * UPB = KV_N * ceil(S*G/GH) units per batch, of which the first
  * A(b) = KV_N * ceil(q_len(b)*G/GH) hold columns of batch b ("active", active
  * index a).  Cost of an active unit = KV tiles (128 positions) its rows see
@@ -621,7 +621,9 @@ fia_status fia_selftest_bounded_wait(int32_t *status, uint64_t limit_ns, void *s
  * units.  (A band with first_tokens and U >= n / 8: units of c_max tiles at most, cut in s
  * chunks of C = c2 = ceil(c_max / s), the s of 1 .. 16 with the least
  * ceil(ceil(T / C) / n) (5 C + 13) + (13 if s > 1), where n W + 2k U chunks
- * suffice; but as above where that C is over 24 and T < 3/4 U c_max.)
+ * suffice; MXFP4: (7 f + (0, 5, 6, 7 for r = 0, to n / 3, to 2n / 3, above)) (C + 1) +
+ * (12 if s > 1) with ceil(T ceil(c_max / C) / c_max) = f n + r; but as above where that
+ * C is over 24 and T < 3/4 U c_max.)
  * sched holds int64 {C, c2, chunks N, big chunks F, split batches M, plan
  * mark 0x4649414445434F44, B, CTA count}, then Q[B+1] (partial slots before
  * batch b: chunk i of active unit a of batch b owns slot Q[b] + i*A(b) + a),

@@ -387,6 +387,37 @@ def test_pools_past_two_to_the_31_bytes():
     assert torch.equal(d.v_scale[nb - 1, :, 122].cpu(), torch.from_numpy(scale))
 
 
+@pytest.mark.parametrize("B,kv,window,rows", [(40, 3000, None, 1), (7, 20000, None, 3), (1, 100, None, 1),
+                                              (40, 9000, 4096, 1), (60, 5000, 1024, 1), (24, 2500, 2048, 1)])
+def test_the_plan(B, kv, window, rows):
+    """The chunk sizes and counts that fia.h states."""
+    kw = dict(mask_mode=4, pre_tokens=window - 1, next_tokens=0, first_tokens=4) if window else dict(mask_mode=3)
+    p = serving.make_mx(B=B, QN=8, KVN=2, q_lens=[rows] * B, kv_lens=[kv] * B, block_size=128, seed=60, **kw).to(DEV)
+    call = fia.FiaCall(p, num_sms=50)
+    call.plan()
+    torch.cuda.synchronize()
+    lay = fia.fia_get_plan_layout(call.params)
+    C, c2, N = call.ws[lay.sched_off:lay.sched_off + 24].view(torch.int64).tolist()
+    n, U = 150, 2 * B * (2 if rows * 4 > 16 else 1)
+    cost = -(-kv // 128)
+    if window and kv > window + 4:
+        t0 = (kv - window) // 128
+        cost = cost - t0 + min(t0, 1)
+    T = U * cost
+    want = max(1, -(-T // (2 * n)))
+    want = want, max(-(-want // 2), min(want, 6))
+    if window and 8 * U >= n:
+        def time(s):
+            z = -(-cost // s)
+            f, r = divmod(-(-T * -(-cost // z) // cost), n)
+            return (7 * f + (0 if r == 0 else 5 + (3 * r > n) + (3 * r > 2 * n))) * (z + 1) + 12 * (s > 1), s
+        s = min(time(s) for s in range(1, min(16, cost) + 1) if s == 1 or U * s <= 2 * n + 4 * U)[1]
+        want = (-(-cost // s),) * 2
+    assert (C, c2) == want
+    n1 = max(0, cost // C - 1)
+    assert N == U * (n1 + -(-(cost - n1 * C) // c2))
+
+
 def test_calls_side_by_side():
     """Two calls on two streams, each with its workspace, many times: the same bits as alone."""
     ps = [serving.make_mx(B=12, QN=16, KVN=2, q_lens=[2] * 12, kv_lens=[900 + 70 * i for i in range(12)],

@@ -43,12 +43,22 @@ def test_a_bad_mxfp4_cache_is_refused(fields, status):
 
 @pytest.mark.parametrize("rows", [1, 16, 40])
 def test_mxfp4_workspaces(rows):
-    """Decode takes what an FP8 cache takes; a prompt its 16-bit copies of K and V."""
-    st, n = _size(_fia_params(max_seqlen_q=rows, **MX))
+    """Decode: the slots of its plan, of three CTAs to each of num_sms; a prompt its 16-bit
+    copies of K and V."""
+    p = _fia_params(max_seqlen_q=rows, **MX)
+    st, n = _size(p)
     st8, n8 = _size(_fia_params(max_seqlen_q=rows, kv_dtype=1, quant_tile=64, k_scale=FAKE,
                                 v_scale=FAKE))
     assert st == st8 == fia.FIA_OK
-    assert n == n8 if rows <= 16 else 4 * 4 * 1024 * 2 * 128 < n <= n8
+    if rows <= 16:
+        GH = 8 if rows * 4 <= 8 else 16
+        lay = _abi.fia_get_plan_layout(p)
+        assert lay.num_ctas == 3 * 152 and lay.num_units == 4 * 2 * -(-rows * 4 // GH)
+        assert lay.max_chunks == 2 * lay.num_ctas + 4 * lay.num_units
+        slots = lay.max_chunks * (16 + 4 * GH * (128 + 2))  # queue entries and partial sums
+        assert slots <= n <= slots + 8192 and n == lay.total_bytes
+    else:
+        assert 4 * 4 * 1024 * 2 * 128 < n <= n8
     assert _size(_fia_params(max_seqlen_q=rows, block_table=0, max_seqlen_kv=1024, **MX))[0] == 0
 
 
