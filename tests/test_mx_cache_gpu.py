@@ -178,6 +178,16 @@ def test_decode_weights(QN, rows):
                            block_size=32, mask_mode=3), weights=True)
 
 
+@pytest.mark.parametrize("QN,rows", [(12, 2), (4, 9), (24, 1), (4, 16)])
+def test_decode_of_sixteen_columns(QN, rows):
+    """Units of more than 8 columns, the last one in part: explicit masks with rows that see
+    nothing, key weights, a top-left mask."""
+    kw = dict(B=2, QN=QN, KVN=2, q_lens=[rows] * 2, kv_lens=[401, 130], block_size=64, seed=10)
+    _check(serving.make_mx(mask_mode=1, mask_density=0.4, mask_full_rows=1, **kw))
+    _check(serving.make_mx(mask_mode=2, **kw))
+    _check(serving.make_mx(mask_mode=3, **kw), weights=True)
+
+
 def test_decode_of_a_large_batch():
     g = torch.Generator().manual_seed(1)
     lens = torch.randint(0, 300, (200,), generator=g).tolist()
