@@ -390,15 +390,16 @@ __device__ __forceinline__ uint32_t pack_cost(int64_t cost, int ha) {
 // (us): 16 sequences of a row, window 4096, by the rule above 41.0, so 32.8; of four rows
 // 55.9, 49.6; of 1 to 4 43.2, 43.0; window 1024 24.8, 24.7; 8 sequences, window 8192 41.3,
 // 41.6; 64 of a row 79.8, 78.4.  The other calls' rule: 32.8, 49.2, 48.8, 28.3, 45.4, 77.8.
+template <bool MX>
 __device__ __forceinline__ int64_t window_chunk(const DecodeArgs& a, int64_t T, int cmax) {
   if (cmax < 1) return 1;
   // (the other calls' rule counts in 64 bits)
-  if (T > (a.ctas_per_sm > 1 ? 0x7ffffffLL : 0x7fffffffLL)) return 0;
+  if (T > (MX ? 0x7ffffffLL : 0x7fffffffLL)) return 0;
   // (32-bit divisions: 64-bit ones cost the step half a microsecond)
   const uint32_t s = (threadIdx.x & 31) + 1, n = (uint32_t)a.num_ctas;
   const uint32_t z = ((uint32_t)cmax + s - 1) / s;
   uint64_t time;
-  if (a.ctas_per_sm > 1) {
+  if constexpr (MX) {
     const uint32_t parts = min(((uint32_t)cmax + z - 1) / z, 16u);  // chunks to a unit of cmax
     const uint32_t chunks = ((uint32_t)T * parts + cmax - 1) / (uint32_t)cmax;
     const uint32_t rounds = chunks / n, rest = 3 * (chunks - rounds * n);
@@ -416,6 +417,8 @@ __device__ __forceinline__ int64_t window_chunk(const DecodeArgs& a, int64_t T, 
   return best > 24 && 4 * T < 3 * a.num_units * cmax ? 0 : best;
 }
 
+// MX: over an MXFP4 cache (chunks of its own; apart, since the code is fetched cold).
+template <bool MX>
 __global__ void __launch_bounds__(1024) decode_schedule_kernel(const DecodeArgs a) {
   __shared__ uint32_t ws[32][3];
   __shared__ int64_t ws_total[32];
@@ -485,7 +488,7 @@ __global__ void __launch_bounds__(1024) decode_schedule_kernel(const DecodeArgs 
   int64_t C = 0, c2;
   if (window) {
     cmax = __reduce_max_sync(0xffffffffu, lane < (int)(blockDim.x >> 5) ? ws_cost[lane] : 0);
-    c2 = C = window_chunk(a, T, cmax);
+    c2 = C = window_chunk<MX>(a, T, cmax);
   }
   if (C == 0) {
     C = 1;
@@ -497,7 +500,7 @@ __global__ void __launch_bounds__(1024) decode_schedule_kernel(const DecodeArgs 
               : (T - 1) / per + 1;
     c2 = C <= 0x7fffffffLL ? (int64_t)((uint32_t)(C + a.small_div - 1) / (uint32_t)a.small_div)
                            : (C + a.small_div - 1) / a.small_div;
-    c2 = max(c2, min(C, (int64_t)a.small_min));
+    if constexpr (MX) c2 = max(c2, min(C, (int64_t)kMxSmallChunk));
   }
 
   // per batch: big and small chunks of its active units and whether it is
@@ -2030,7 +2033,8 @@ size_t decode_smem_bytes(int D, int fp8) {
 }
 
 cudaError_t launch_decode_schedule(const DecodeArgs& a, cudaStream_t s) {
-  decode_schedule_kernel<<<1, 1024, 0, s>>>(a);
+  if (a.mx) decode_schedule_kernel<true><<<1, 1024, 0, s>>>(a);
+  else decode_schedule_kernel<false><<<1, 1024, 0, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -654,9 +654,9 @@ cudaError_t launch_few_t(const DecodeArgs& a, const CacheView& c, const KeyWeigh
 // without a window too: 8 units, 300 keys 9.7 / 14.5, 2000 10.8 / 16.4, 4000 14.2 / 16.8,
 // 8000 18.5 / 21.8; 32 units, 300 10.3 / 14.8, 4000 16.5 / 24.0, 8000 24.6 / 26.8.  (With
 // FIA_DEBUG the other kernels run: they report pages outside the pool.)
-bool decode_is_few(const DecodeArgs& a, bool mx, bool weights) {
-  const int sms = mx ? a.num_ctas / decode_mx_ctas() : a.num_ctas;
-  if ((a.first_tokens == 0 && !weights && !mx) || a.mask || a.debug || sms < kFewCtas) return false;
+bool decode_is_few(const DecodeArgs& a, bool weights) {
+  const int sms = a.mx ? a.num_ctas / decode_mx_ctas() : a.num_ctas;
+  if ((a.first_tokens == 0 && !weights && !a.mx) || a.mask || a.debug || sms < kFewCtas) return false;
   const int64_t groups = (a.S_max * a.G + 7) / 8;
   if (weights && groups > 1) return false;  // (a key's weight is a sum within one unit)
   return (int64_t)a.B * a.KVN * groups * 9 <= 2 * sms &&

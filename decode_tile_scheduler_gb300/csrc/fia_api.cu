@@ -316,8 +316,7 @@ DecodeArgs decode_args(const fia_params* p, const DecodePlan& pl, void* ws) {
   a.num_units = pl.U;
   a.chunks_per_cta = pl.W;
   a.small_div = decode_small_div(p);
-  a.ctas_per_sm = p->kv_dtype == FIA_KV_MXFP4 ? decode_mx_ctas() : 1;
-  a.small_min = p->kv_dtype == FIA_KV_MXFP4 ? 6 : 1;
+  a.mx = p->kv_dtype == FIA_KV_MXFP4;
   a.max_chunks = pl.max_chunks;
   char* w = static_cast<char*>(ws);
   a.sched = reinterpret_cast<int64_t*>(w + pl.off_sched);
@@ -760,7 +759,7 @@ fia_status execute_decode(const fia_params* p, void* ws, cudaStream_t s, bool pl
   fia_status st = decode_plan(p, &pl);
   if (st != FIA_OK) return st;
   DecodeArgs a = decode_args(p, pl, ws);
-  if (decode_is_few(a, p->kv_dtype == FIA_KV_MXFP4, w != nullptr))
+  if (decode_is_few(a, w != nullptr))
     return launch_decode_few(a, cache_of(p), w, planned, s) == cudaSuccess ? FIA_OK : FIA_ERR_CUDA;
   a.scores = scores;
   a.score_cols = cols;

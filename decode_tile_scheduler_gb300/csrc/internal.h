@@ -25,6 +25,7 @@ struct NvtxRange {
 constexpr int kKvTile = 128;   // KV positions per tile (one split granule)
 constexpr int kQTile = 128;    // query rows per prefill tile
 constexpr int kMaxHeadGroup = 16;  // query columns packed per decode unit, at most
+constexpr int kMxSmallChunk = 6;   // MXFP4 decode: tiles of a small chunk at least, where C has them
 constexpr int kDecodeMaxRows = 16; // query rows per sequence the decode kernel takes
 
 // Columns per decode unit: the (query row, query head) pairs of a KV head,
@@ -87,8 +88,7 @@ struct DecodeArgs {
   int num_ctas;
   int chunks_per_cta;          // W: the chunk size aims at W chunks per CTA
   int small_div;               // small chunks of ceil(C / small_div) tiles (2; 1 for FP8 or rows > 1)
-  int ctas_per_sm;             // 3 for MXFP4, else 1 (window_chunk)
-  int small_min;               // tiles of a small chunk at least, where C has them (MXFP4: 6, else 1)
+  int mx;                      // the cache is MXFP4
   int64_t num_units;           // B * KVN * HG
   int64_t max_chunks;          // partial slots: a bound on the number of chunks
   int64_t* sched;              // [8 + 3(B+1) + B]: C, c2, chunks, big chunks, split
@@ -209,7 +209,7 @@ cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& tk, const CUte
 // Whether a call has few units and few keys (a rule on sizes), and its one kernel:
 // `planned` if it has to find a plan in the workspace, else the plan's launch goes
 // before it and need not be done.
-bool decode_is_few(const DecodeArgs& a, bool mx, bool weights);
+bool decode_is_few(const DecodeArgs& a, bool weights);
 // CTAs of the MXFP4 decode kernel to an SM.
 int decode_mx_ctas();
 cudaError_t launch_decode_few(const DecodeArgs& a, const fia_kv_cache& cache, const KeyWeightsOut* w,
