@@ -7,7 +7,7 @@
 // Columns and units: the query side of KV head hk of a sequence is its
 // (query row i, query head h of the GQA group) pairs, column c = i*G + h%G,
 // S_max*G of them.  A work unit (batch b, KV head hk, column group hg) holds up
-// to GH consecutive columns (16 for one query row with G > 8, else 8): they
+// to GH consecutive columns (8 or 16: decode_group_heads): they
 // form the N columns of every mma.sync, so each KV page is read once for all
 // of them (the GQA heads and, for multi-token decode, the query rows too; the
 // units of one KV head sit next to each other in the queue and share its
@@ -23,7 +23,8 @@
 // r = c - n1*C tiles (C <= r < 2C unless c < C) in small chunks of
 // c2 = ceil(C/k) tiles, k = 2 for a bf16 cache and one query row, else 1
 // (every chunk has a fixed cost, and the FP8 and multi-row units' tiles
-// cost the consumers more).  A window call takes another C, and c2 = C, where
+// cost the consumers more; MXFP4: W = 2 with three CTAs to an SM, k = 2, c2 six
+// tiles at least).  A window call takes another C, and c2 = C, where
 // its units are about of one size or short (window_chunk).  The claim queue lists every big chunk
 // (batch-major, then chunk, then active unit of the batch) before every small
 // chunk (same order), so the work left at the end is always small pieces.  CTAs claim
