@@ -15,9 +15,10 @@
 //
 // Latency-bound: lengths, a scan, then pages (64 sequences of a token 6.1 us a call, 3.4 of
 // them in the kernel: scan 0.9, pages 0.8, rows 1.1; 1024 sequences with 1 to 256 rows and
-// pages that go back 13.7).  One CTA, or eight for many rows, each of
-// which makes the prefix sums of all sequences for itself; past kWhole sequences each
-// makes a slice, and they look into each other's shared memory as a cluster.
+// pages that go back 10.4).  One CTA, or a cluster of sixteen for many rows (eight took
+// 12.7 us, half of it the rows: few SMs issue their stores), each of which makes the prefix
+// sums of all sequences for itself; past kWhole sequences each makes a slice, and they
+// look into each other's shared memory.
 #include <atomic>
 #include <cstring>
 
@@ -29,8 +30,8 @@ namespace fia {
 namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kMaxCtas = 8;
-constexpr int kWhole = 4096;  // sequences whose prefix sums every CTA holds
+constexpr int kMaxCtas = 16, kPortable = 8;  // of a cluster: at most, on every device
+constexpr int kWhole = 8192;  // sequences whose prefix sums every CTA holds (5000: 25 us, in slices 41)
 constexpr int kPieceRows = 128;
 
 struct PagesArgs {
@@ -292,6 +293,36 @@ __global__ void __launch_bounds__(kThreads) assign_pages_kernel(const PagesArgs 
   }
 }
 
+// CTAs of a large call's cluster, and the kernel made ready for them, once a device.
+cudaError_t pages_ctas(int dev, int* n) {
+  static std::atomic<int> known[256];
+  std::atomic<int>& mine = known[dev & 255];
+  *n = mine.load();
+  if (*n) return cudaSuccess;
+  constexpr int smem = 4 * (kArrays * kWhole + kWhole + 1);
+  static_assert(smem >= 4 * kArrays * (65536 / kPortable), "a slice of the largest batch");
+  cudaError_t e = cudaFuncSetAttribute(assign_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  *n = kPortable;
+  if (cudaFuncSetAttribute(assign_pages_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kMaxCtas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kMaxCtas;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int fit = 0;
+    if (cudaOccupancyMaxActiveClusters(&fit, assign_pages_kernel, &cfg) == cudaSuccess && fit > 0) *n = kMaxCtas;
+  }
+  cudaGetLastError();  // (a device without such clusters is no error)
+  mine.store(*n);
+  return cudaSuccess;
+}
+
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace
@@ -329,7 +360,8 @@ extern "C" fia_status fia_assign_pages(const fia_pages_params* p, void* stream) 
   // (counts that overlap in part: a sequence's would be read after another's was written)
   if (rows_overlap(p->pages_held, p->pages_held_out, 1, p->batch, p->batch)) return FIA_ERR_BAD_SHAPE;
   const int64_t rows = tnd ? p->total_q : (int64_t)p->batch * p->seqlen_q;
-  if (rows > INT32_MAX - 8192) return FIA_ERR_BAD_SHAPE;  // (counted in 32 bits, in strides of 8192)
+  // (counted in 32 bits, in strides of all threads)
+  if (rows > INT32_MAX - kMaxCtas * kThreads) return FIA_ERR_BAD_SHAPE;
   PagesArgs a;
   memset(&a, 0, sizeof a);
   a.B = p->batch;
@@ -356,20 +388,12 @@ extern "C" fia_status fia_assign_pages(const fia_pages_params* p, void* stream) 
   a.slots = p->slots;
   a.positions = p->positions;
   a.status = p->status;
+  int dev = 0, most = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || pages_ctas(dev, &most) != cudaSuccess) return FIA_ERR_CUDA;
   // (1024 sequences, 6.5 k pages back: eight CTAs 13.1 us with 49 k rows; one 14.5 with 800)
-  const int nc = a.B > kThreads / 2 || a.T > 2 * kThreads ? kMaxCtas : 1;
+  const int nc = a.B > kThreads / 2 || a.T > 2 * kThreads ? most : 1;
   a.per = a.B <= kWhole ? a.B : (a.B + nc - 1) / nc;
   const size_t smem = 4 * (kArrays * (size_t)a.per + (a.cu && a.B <= kWhole ? a.B + 1 : 0));
-  static std::atomic<uint64_t> done_mask[4];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return FIA_ERR_CUDA;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (!(done_mask[(dev >> 6) & 3].load() & bit)) {
-    if (cudaFuncSetAttribute(assign_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             4 * kArrays * (65536 / kMaxCtas)) != cudaSuccess)
-      return FIA_ERR_CUDA;
-    done_mask[(dev >> 6) & 3].fetch_or(bit);
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(nc);
   // (a small call's barriers and launch are shorter with fewer warps)

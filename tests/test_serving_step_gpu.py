@@ -80,7 +80,7 @@ def _pages_case(B, block, cap_pages, seed, *, q_max=3, tnd=False, spare=8, seen=
 
 
 @pytest.mark.parametrize("B,block,cap_pages", [(1, 16, 1), (3, 32, 4), (64, 128, 32), (1023, 48, 3),
-                                               (1024, 16, 2), (1025, 64, 5), (5000, 16, 4)])
+                                               (1024, 16, 2), (1025, 64, 5), (5000, 16, 4), (8192, 16, 2), (9001, 32, 3)])
 @pytest.mark.parametrize("tnd,in_place", [(False, True), (True, False)])
 def test_assign_pages(B, block, cap_pages, tnd, in_place):
     _pages_case(B, block, cap_pages, seed=B, tnd=tnd, in_place=in_place, q_max=2 if B > 100 else 7,
