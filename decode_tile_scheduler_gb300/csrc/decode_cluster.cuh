@@ -15,7 +15,7 @@
 // memory until the columns' lse is known.
 //
 // MXFP4: a warp's 16 rows go through its part of shared memory, and from there as in
-// decode_mx.cuh.
+// decode_mx.cuh, windows of V scales and far groups too (a warp's own, of all four groups).
 //
 // Bound by latency: lengths and page table, then K and V, then two folds.  One sequence,
 // 8 KV heads, a window of 1024 and 4 first tokens: 7.7 us a call in a graph (plan, decode
@@ -29,38 +29,9 @@
 namespace fia {
 namespace {
 
-// A row's V scales v (bf16, a lane each) against the references: where one is past its
-// group's (a NaN is past nothing), the warp's new references, and the exact powers of two
-// that O's groups move by in f.  Returns whether they moved.
-__device__ __forceinline__ bool mx_references(const __nv_bfloat162 (&v)[2], __nv_bfloat162 (&vref)[2],
-                                              __nv_bfloat162 (&vinv)[2], float (&f)[4]) {
-  const auto bits = [](const __nv_bfloat162& x) { return *reinterpret_cast<const uint32_t*>(&x); };
-  // (the larger of two drops a NaN)
-  const bool past = bits(__hmax2(v[0], vref[0])) != bits(vref[0]) || bits(__hmax2(v[1], vref[1])) != bits(vref[1]);
-  if (!__any_sync(0xffffffffu, past)) return false;
-  uint32_t en[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t c = (bits(v[j >> 1]) >> (16 * (j & 1)) & 0xffffu) >> 7;
-    const uint32_t old = (bits(vref[j >> 1]) >> (16 * (j & 1)) & 0xffffu) >> 7;
-    en[j] = max(old, min(__reduce_max_sync(0xffffffffu, c == 255u ? 0u : c), (uint32_t)kMxRefMax));
-    // (a jump past 2^-126 leaves a negligible old sum and gives 0)
-    f[j] = __int_as_float(max(127 + (int)old - (int)en[j], 0) << 23);
-  }
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    vref[k] = mx_pair(en[2 * k] << 7, en[2 * k + 1] << 7);
-    vinv[k] = mx_pair((254 - en[2 * k]) << 7, (254 - en[2 * k + 1]) << 7);
-  }
-  return true;
-}
-// V scales over their references as fp16 pairs of rows 2k, 2k + 1 (lanes): groups 0 and 1
-// from the even lane, 2 and 3 from the odd one.
-__device__ __forceinline__ uint2 mx_scale_pairs(const __nv_bfloat162 (&v)[2], const __nv_bfloat162 (&vinv)[2],
-                                                int lane) {
-  float vf[4];
-  bf16x2x2_to_f32x4(__hmul2(v[0], vinv[0]), __hmul2(v[1], vinv[1]), vf);
-  const uint32_t h01 = pack_f16(vf[0], vf[1]), h23 = pack_f16(vf[2], vf[3]);
+// V scale factors (fp16) of rows 2k, 2k + 1 (lanes) as pairs: groups 0 and 1 from the even
+// lane, 2 and 3 from the odd one.
+__device__ __forceinline__ uint2 mx_scale_pairs(uint32_t h01, uint32_t h23, int lane) {
   const uint32_t theirs = __shfl_xor_sync(0xffffffffu, lane & 1 ? h01 : h23, 1);
   const uint32_t even = lane & 1 ? theirs : h01, odd = lane & 1 ? h23 : theirs;
   return make_uint2(__byte_perm(even, odd, 0x5410), __byte_perm(even, odd, 0x7632));
@@ -169,7 +140,7 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
   // MXFP4: Q in fp16 times a power of two, K's 2 k-steps a group, the score factor (all
   // as in decode_mx_kernel)
   float slc = a.scale_log2;
-  __nv_bfloat162 vref[2], vinv[2];
+  uint32_t win = kMxWindow * 0x1010101u, far = 0u;  // a byte a group: its window's top; 0x80: far
   if constexpr (MX) {
     uint32_t emax = 0;
 #pragma unroll
@@ -187,11 +158,6 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
     };
 #pragma unroll
     for (int i = 0; i < NK; ++i) q[i] = make_uint4(half(q[i].x), half(q[i].y), half(q[i].z), half(q[i].w));
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      vref[k] = mx_pair(kMxRefMin << 7, kMxRefMin << 7);
-      vinv[k] = mx_pair((254 - kMxRefMin) << 7, (254 - kMxRefMin) << 7);
-    }
   }
   // the bounds of this lane's two columns
   int lo[2], hi[2];
@@ -298,7 +264,6 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
 
     // ---- scores ----
     float x[4];  // keys g, g, g + 8, g + 8; columns 2 q4, 2 q4 + 1, ...
-    float vfct[4] = {1.f, 1.f, 1.f, 1.f};  // MXFP4: what O's groups are multiplied by
     if constexpr (MX) {
       __syncwarp();  // (the step before has read its rows)
 #pragma unroll
@@ -308,13 +273,41 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
       }
       float kf[4];
       e8m0x4_to_f32x4(ksw, kf);
-      __nv_bfloat162 v[2];
-      e8m0x4_to_bf16x2x2(vsw, v);
-      mx_references(v, vref, vinv, vfct);
-      const uint2 pairs = mx_scale_pairs(v, vinv, lane);
+      if (!(lane < kFewKeys && seen(lane))) vsw = win - 0x04040404u;  // (in the windows)
+      const uint32_t fct = vsw + (0x10101010u - win);  // 2^(1 - d): fp16 exponents 16 - d
+      uint32_t h01 = __byte_perm(fct, 0u, 0x4140) << 10, h23 = __byte_perm(fct, 0u, 0x4342) << 10;
+      const uint32_t out = n == 0 ? __vsub4(win - 0x04040404u, vsw) & 0xf8f8f8f8u : __vsub4(win, vsw) & 0xf0f0f0f0u;
+      if (__any_sync(0xffffffffu, (out | far) != 0u)) {
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t code = vsw >> (8 * j) & 255u;
+          const bool was = far >> (8 * j + 7) & 1u;
+          const uint32_t most = __reduce_max_sync(0xffffffffu, code == 255u ? 0u : code);
+          const uint32_t least = __reduce_min_sync(0xffffffffu, code == 0u ? 255u : code);
+          const uint32_t top = n == 0 ? mx_window(least, most) : win >> (8 * j) & 255u;
+          const bool is = was || most > top || least + 15 < top;
+          const uint32_t now = is ? max(top, most) : top;
+          if (is) {
+            const int e = (int)(top - now) - (was ? kMxFar : 1) + kMxFar;
+            const float f0 = mx_pow2(e / 2), f1 = mx_pow2(e - e / 2);
+#pragma unroll
+            for (int i = 2 * (j & 1); i < 2 * (j & 1) + 2; ++i)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) O[j >> 1][i][k] = O[j >> 1][i][k] * f0 * f1;
+            far |= 0x80u << (8 * j);
+          }
+          win = (win & ~(255u << (8 * j))) | now << (8 * j);
+          h[j] = is ? 0u : code == 255u ? 0x7e00u : (uint32_t)max((int)(code + 16u - now), 0) << 10;
+        }
+        h01 = h[0] | h[1] << 16;
+        h23 = h[2] | h[3] << 16;
+      }
+      const uint2 pairs = mx_scale_pairs(h01, h23, lane);
       if (lane < kFewKeys) {
         *reinterpret_cast<float4*>(rows + 2048 + lane * 16) = make_float4(kf[0], kf[1], kf[2], kf[3]);
         *reinterpret_cast<uint2*>(rows + 2304 + lane * 8) = pairs;
+        *reinterpret_cast<uint32_t*>(rows + 2432 + lane * 4) = vsw;
       }
       __syncwarp();
       const float4 f0 = *reinterpret_cast<const float4*>(rows + 2048 + g * 16);
@@ -402,7 +395,7 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
         vexp[i] = en;
       }
     }
-    float p[4];
+    float p[4], mus[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       // (MXFP4: the reference lies 13 lower, which keeps P's bits in fp16)
@@ -410,6 +403,7 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
       const float mu = mx == -INFINITY ? 0.f : mx;
+      mus[e] = mu;
       const float corr = fast_exp2(m[e] - mu);  // (m = -inf: 0)
       m[e] = mx;
       p[e] = fast_exp2(x[e] - mu);
@@ -419,7 +413,7 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float f = MX ? corr * vfct[2 * i + (k >> 1)] : FP8 ? corr * ratio[i] : corr;
+          const float f = FP8 ? corr * ratio[i] : corr;
           O[i][k][e] *= f;
           O[i][k][2 + e] *= f;
         }
@@ -444,6 +438,32 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
           b1 = mul_f16x2(p1, sb[2 * jj + k]);
           mma_f16(O[jj][2 * k], va[0], b0, b1);
           mma_f16(O[jj][2 * k + 1], va[1], b0, b1);
+        }
+      }
+      if (far) {  // P times its scale from the scores, as two terms in bf16
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (!(far >> (8 * j + 7) & 1u)) continue;
+          const int top = (int)(win >> (8 * j) & 255u) - kMxFar;
+          const int c0 = rows[2432 + g * 4 + j], c1 = rows[2432 + (g + 8) * 4 + j];
+          const float s0 = c0 == 255 ? __int_as_float(0x7fffffff) : (float)(c0 - top);
+          const float s1 = c1 == 255 ? __int_as_float(0x7fffffff) : (float)(c1 - top);
+          const float t0 = fast_exp2(x[0] - mus[0] + s0), t1 = fast_exp2(x[1] - mus[1] + s0);
+          const float t2 = fast_exp2(x[2] - mus[0] + s1), t3 = fast_exp2(x[3] - mus[1] + s1);
+          uint32_t w[4], va[2][4];
+          ldsm_x4_t(smem_u32(rows) + 1024 + sw64(mx_v_row(lane), 2 * (j >> 1) + (lane >> 4)), w[0], w[1], w[2], w[3]);
+          mx_v_fragments(w[2 * (j & 1)], w[2 * (j & 1) + 1], va);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) va[i][y] = f16x2_to_bf16x2(va[i][y]);
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            b0 = movmatrix_t(mx_halves(t0, t1, y));
+            b1 = movmatrix_t(mx_halves(t2, t3, y));
+            mma_bf16(O[j >> 1][2 * (j & 1)], va[0], b0, b1);
+            mma_bf16(O[j >> 1][2 * (j & 1) + 1], va[1], b0, b1);
+          }
         }
       }
     } else if constexpr (!FP8) {
@@ -484,15 +504,18 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
   for (int e = 0; e < 2; ++e) {
 #pragma unroll
     for (int d = 4; d < 32; d <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
+    const int lower = MX ? mx_lower(m[e], l[e]) : 0;
     if (g == 0) ml_warp[wid][2 * q4 + e] = make_float2(m[e], l[e]);
     if constexpr (MX) {
       if (e == 0) __syncwarp();  // (o_warp held the last step's rows)
-      float back[4];
-      bf16x2x2_to_f32x4(vref[0], vref[1], back);
 #pragma unroll
-      for (int t = 0; t < 8; ++t)  // group t / 2, elements 4g + 2 (t % 2) and the next
+      for (int t = 0; t < 8; ++t) {  // group t / 2, elements 4g + 2 (t % 2) and the next
+        const int back = (int)(win >> (4 * (t & 6)) & 255u) - lower -
+                         (far >> (4 * (t & 6) + 7) & 1u ? 127 + kMxFar : 128);
+        const float back0 = mx_pow2(back / 2), back1 = mx_pow2(back - back / 2);
         *reinterpret_cast<float2*>(&o_warp[wid][2 * q4 + e][32 * (t >> 1) + 4 * g + 2 * (t & 1)]) =
-            make_float2(back[t >> 1] * O[t >> 2][t & 3][e], back[t >> 1] * O[t >> 2][t & 3][2 + e]);
+            make_float2(O[t >> 2][t & 3][e] * back0 * back1, O[t >> 2][t & 3][2 + e] * back0 * back1);
+      }
     }
 #pragma unroll
     for (int i = 0; i < NV && !MX; ++i) {

@@ -23,7 +23,10 @@
 //    pair the keys' codes in bytes, and cvt makes an fp16 pair of a byte.
 //  - E2M1 codes are fp16 values as they are.  K scales multiply the partial scores of
 //    their 32 elements in fp32; V scales multiply P, already in fp16 and transposed, as
-//    fp16 pairs.
+//    fp16 pairs, where a chunk's scales of a group lie within 16 binades.  A group whose
+//    scales do not has its P times scale made of the scores, as two terms in bf16, whose
+//    exponents reach (kMxFar): a key of little weight, or none, takes no bit from the
+//    others however large its V is.
 //
 // Measured (one GB300; the call with plan and combine): 4 sequences of 32 to 128 k keys,
 // 64 / 8 heads (364 MB) 86.5 us, of which this kernel 79; its loads alone 65.6, its work
@@ -65,7 +68,8 @@ struct MxCfg {
   static constexpr int kOffBar = kOffRed + 2 * kWarps * 8 * NG * 4;
   static constexpr int kOffMsg = (kOffBar + 8 * (2 * kStages + 2) + 15) / 16 * 16;
   static constexpr int kOffMisc = kOffMsg + 128;
-  static constexpr int kSmem = kOffMisc + 16 + 512;           // + alignment slack (a swizzle's 512 bytes)
+  static constexpr int kOffGroups = kOffMisc + 16;            // the far groups' references
+  static constexpr int kSmem = kOffGroups + 4 * kWarps + 512;  // + alignment slack (a swizzle's 512 bytes)
   static_assert(kStageBytes % 512 == 0, "alignment");
   static_assert(kCtas * (kSmem + 1024) <= 233472, "shared memory");
 };
@@ -101,11 +105,37 @@ __device__ __forceinline__ void e8m0x4_to_f32x4(uint32_t w, float (&f)[4]) {
   e8m0x4_to_bf16x2x2(w, v);
   bf16x2x2_to_f32x4(v[0], v[1], f);
 }
-// The V scale reference of a group: codes from kMxRefMin to kMxRefMax, as bf16 values.
-constexpr int kMxRefMin = 27, kMxRefMax = 253;
-__device__ __forceinline__ __nv_bfloat162 mx_pair(uint32_t lo, uint32_t hi) {
-  const uint32_t w = lo | hi << 16;
-  return *reinterpret_cast<const __nv_bfloat162*>(&w);
+// A far group's O lies this much lower against the largest scale: products up to 2^14 with
+// 2^kMxFar, and sums of them, stay in fp32, and scales down to 2^-195 of the largest keep
+// the bits of bf16.
+constexpr int kMxFar = 60;
+// Where a window of V scales starts: its inner codes, 2^-7 to 1, are those of 32 values whose
+// largest is 2^-6 to 6 (at 0 a chunk's first tile took its way to a window always: 32
+// sequences of 512 to 4096 keys 35.7 us for 35.3, two of 300 and 777 9.5 for 9.0).
+constexpr uint32_t kMxWindow = 131;
+// The window for codes of least .. most (0: none), the largest of which it may not reach.
+__device__ __forceinline__ uint32_t mx_window(uint32_t least, uint32_t most) {
+  return most == 0u ? kMxWindow : min(max(most + 4u, 15u), min(least + 15u, 254u));
+}
+// 2^e as a float, 0 below its normal numbers.
+__device__ __forceinline__ float mx_pow2(int e) { return __int_as_float(max(min(e, 127) + 127, 0) << 23); }
+// A column's sum l as l * 2^-k below 2^-7, k returned and its exponent moved by it: O, moved
+// as far, is then a 128th of an average of V, and 128 such do not leave fp32 together.
+__device__ __forceinline__ int mx_lower(float& m, float& l) {
+  const int k = l > 0.f ? (int)(__float_as_uint(l) >> 23) - 119 : 0;
+  m += (float)k;
+  l *= mx_pow2(-k);
+  return k;
+}
+// Two values as a pair of bf16, or (`rest`) what such a pair leaves of them.
+__device__ __forceinline__ uint32_t mx_halves(float a, float b, bool rest) {
+  const uint32_t w = pack_bf16(a, b);
+  return rest ? pack_bf16(a - __uint_as_float(w << 16), b - __uint_as_float(w & 0xffff0000u)) : w;
+}
+// A pair of fp16 codes' values as bf16 (exact).
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t w) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return pack_bf16(f.x, f.y);
 }
 // Keys of a block of 16.  The transposing ldmatrix gives a lane keys a, b of its first
 // matrix and c, d of its second, whose codes pair as (a, c) and (b, d); movmatrix gives it
@@ -430,7 +460,7 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
     // Softmax references m_r, the warps' own copies of one (-inf: none yet; mu is 0 then), lazy: a score may pass its
     // column's by kOver.  They are kept kLift below the scores that set them, so that P,
     // at most 2^kOver, has fp16's bits down to 2^-(14 + kLift) of the largest.
-    constexpr float kLift = 5.f, kOver = 13.f;
+    constexpr float kLift = 8.f, kOver = 14.f;
     float m_r[NG][2], mu[NG][2], l_r[NG][2];
 #pragma unroll
     for (int n = 0; n < NG; ++n)
@@ -439,11 +469,16 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
         m_r[n][e] = -INFINITY;
         mu[n][e] = l_r[n][e] = 0.f;
       }
-    // The V scale reference: the largest scale of the group that the tiles had so far.  V
-    // scales over it, at most 1, multiply P in fp16 (exact powers of two, down to 2^-24); O
-    // is kept over it.
-    __nv_bfloat162 vref = mx_pair(kMxRefMin << 7, kMxRefMin << 7);
-    __nv_bfloat162 vinv = mx_pair((254 - kMxRefMin) << 7, (254 - kMxRefMin) << 7);
+    // The window of this warp's V scales: codes win - 15 .. win, over whose 2^(win - 128) O is
+    // kept; P meets factors of 2^-14 to 2.  So no product of a key within 2^-8 of its
+    // column's largest weight falls below fp16's normal numbers, and what smaller ones lose
+    // is below 2^-18 of O's terms.  It stays where it is unless a scale of the chunk's first
+    // tile lies outside its inner eight codes.  A later code outside it, NaN (255) and 0
+    // (values below bf16's normal numbers) apart, makes the group far for the rest of the
+    // chunk: O is then over 2^(win - 127 - kMxFar), win the largest code so far.  Both halves
+    // of `win` hold the code; far: the upper one 0xffff.
+    uint32_t win = kMxWindow * 0x10001u;
+    if (lane == 0) reinterpret_cast<int*>(smem + Cfg::kOffGroups)[warp] = 0;
     // Keys that count as zeros in O whatever they hold: past kv_len, and between a band's
     // first tokens and its window.  (Codes are numbers all: a scale of 0 is enough.)
     const auto gone = [&](int j) {
@@ -460,7 +495,6 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
       const int jw = jt + R0;  // first KV row of this warp
       const bool edge = (jw < r.lo_last) || (jw + Cfg::kRows - 1 > r.hi_first) || (MR && a.mask != nullptr);
       // ---------------- scales ----------------
-      float vfct = 1.f;  // what O is multiplied by
       {
         const uint32_t* sc = reinterpret_cast<const uint32_t*>(stp + Cfg::kOffScale) + R0 + lane;
         float kf[4];  // (K: a lane takes a row; NaN: the row's scores are NaN)
@@ -471,30 +505,43 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
         if (jt + kKvTile > kvl || (X && jt + kKvTile > a.first_tokens))
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (gone(jt + vrow + (k == 0 ? 0 : k == 1 ? 12 : 4 * k - 4))) c[k] = 0u;
-        __nv_bfloat162 v[2];
-        e8m0x4_to_bf16x2x2(__byte_perm(c[0], c[1], 0x1140) | __byte_perm(c[2], c[3], 0x4011), v);
-        const auto bits = [](const __nv_bfloat162& x) { return *reinterpret_cast<const uint32_t*>(&x); };
-        // (the larger of two drops a NaN)
-        const __nv_bfloat162 most = __hmax2(__hmax2(v[0], v[1]), vref);
-        if (__any_sync(0xffffffffu, bits(most) != bits(vref))) {
-          const uint32_t old = (bits(vref) & 0xffffu) >> 7;
-          const uint32_t mine = max(bits(most) >> 23, (bits(most) & 0xffffu) >> 7);
-          const uint32_t now = min(__reduce_max_sync(0xffffffffu, mine), (uint32_t)kMxRefMax);
-          // (a jump past 2^-126 leaves a negligible old sum and gives 0)
-          vfct = __int_as_float(max(127 + (int)old - (int)now, 0) << 23);
-          vref = mx_pair(now << 7, now << 7);
-          vinv = mx_pair((254 - now) << 7, (254 - now) << 7);
+            if (gone(jt + vrow + (k == 0 ? 0 : k == 1 ? 12 : 4 * k - 4))) c[k] = (win - 4u) & 0xffffu;
+        // factor 2^(1 - d) of a code d below the window's top: fp16 exponent 16 - d
+        const uint32_t c01 = c[0] | c[1] << 16, c23 = c[2] | c[3] << 16;
+        const uint32_t high = tt == 0 ? win - 0x40004u : win, out = tt == 0 ? 0xfff8fff8u : 0xfff0fff0u;
+        uint2 f = make_uint2((c01 + 0x100010u - win) << 10, (c23 + 0x100010u - win) << 10);
+        if (__any_sync(0xffffffffu, (((high - c01) | (high - c23)) & out) != 0u)) {
+          uint32_t most = 0u, least = 255u;
 #pragma unroll
-          for (int n = 0; n < NG; ++n)
+          for (int k = 0; k < 4; ++k)
+            if (c[k] != 0u && c[k] != 255u) {
+              most = max(most, c[k]);
+              least = min(least, c[k]);
+            }
+          most = __reduce_max_sync(0xffffffffu, most);
+          least = __reduce_min_sync(0xffffffffu, least);
+          const uint32_t top = tt == 0 ? mx_window(least, most) : win & 0xffffu;
+          const bool was = win >> 31, far = was || most > top || least + 15 < top;
+          const uint32_t now = far ? max(top, most) : top;
+          if (far) {
+            const int e = (int)(top - now) - (was ? kMxFar : 1) + kMxFar;  // O moves by 2^e
+            const float f0 = mx_pow2(e / 2), f1 = mx_pow2(e - e / 2);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int n = 0; n < NG; ++n)
 #pragma unroll
-              for (int k = 0; k < 4; ++k) acc[n][i][k] *= vfct;
+              for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[n][i][k] = acc[n][i][k] * f0 * f1;
+            if (lane == 0) reinterpret_cast<int*>(smem + Cfg::kOffGroups)[warp] = (int)now;
+          }
+          win = now | (far ? 0xffffu : now) << 16;
+          uint32_t h[4];  // (far: O's products are made apart)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            h[k] = far ? 0u : c[k] == 255u ? 0x7e00u : (uint32_t)max((int)(c[k] + 16u - now), 0) << 10;
+          f = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
         }
-        float f[4];
-        bf16x2x2_to_f32x4(__hmul2(v[0], vinv), __hmul2(v[1], vinv), f);
-        *reinterpret_cast<uint2*>(vs_mine) = make_uint2(pack_f16(f[0], f[1]), pack_f16(f[2], f[3]));
+        *reinterpret_cast<uint2*>(vs_mine) = f;
         __syncwarp();
       }
       // ---------------- S^T = K Q^T ----------------
@@ -615,8 +662,10 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
       };
       static_assert(NB == 2, "P's words");
       store_p();
+      bool any_far = false;
       // (the other copy of P has been read by all when they are here)
-      if (named_bar_or(1, 32 * W, over)) {  // new references, and P again
+      if (named_bar_or(1, 32 * W, over || win >> 31)) {  // new references, and P again; far groups
+        const int4 far = *reinterpret_cast<const int4*>(smem + Cfg::kOffGroups);
 #pragma unroll
         for (int n = 0; n < NG; ++n)
 #pragma unroll
@@ -649,6 +698,15 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
           }
         store_p();
         named_bar_sync(1, 32 * W);
+        any_far = (far.x | far.y | far.z | far.w) != 0;
+        if (any_far) {  // the scores in the place of this warp's K rows
+          float4* xs = reinterpret_cast<float4*>(smem + s * Cfg::kStageBytes + R0 * Cfg::kRowBytes) + lane;
+#pragma unroll
+          for (int n = 0; n < NG; ++n)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+              xs[32 * (n * NB + b)] = make_float4(x[n][b][0], x[n][b][1], x[n][b][2], x[n][b][3]);
+        }
       }
 #pragma unroll
       for (int n = 0; n < NG; ++n)
@@ -676,6 +734,61 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
           mma_f16(acc[n][1], va[1][1], b0, b1);
         }
       }
+      if (any_far) {
+        // A far group's P times its scale over 2^(its reference - kMxFar), as two terms in bf16
+        // one after the other, goes through the other copy of P, which nobody reads now.
+        const float4* xs = reinterpret_cast<const float4*>(stp + R0 * Cfg::kRowBytes) + lane;
+        uint4* pf = reinterpret_cast<uint4*>(smem + Cfg::kOffP) + (~it & 1) * (NG * 32 * W);
+#pragma unroll 1
+        for (int term = 0; term < 2 * W; ++term) {
+          const int j = term >> 1, ref = reinterpret_cast<const volatile int*>(smem + Cfg::kOffGroups)[j];
+          if (ref == 0) continue;
+          const uint8_t* sv = stp + Cfg::kOffScale + Cfg::kScaleBytes + R0 * 4 + j;
+#pragma unroll
+          for (int n = 0; n < NG; ++n) {
+            if (n && !two) break;
+            uint32_t pt[NB][2];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              const float4 v = xs[32 * (n * NB + b)];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int row = 16 * b + key[h], c = gone(jw + row) ? 0 : sv[4 * row];
+                const float e = c == 255 ? __int_as_float(0x7fffffff) : (float)(c + kMxFar - ref);
+                pt[b][h] = movmatrix_t(mx_halves(fast_exp2(fmaf(h ? v.z : v.x, slc, -mu[n][0]) + e),
+                                                 fast_exp2(fmaf(h ? v.w : v.y, slc, -mu[n][1]) + e), term & 1));
+              }
+            }
+            pf[32 * (W * n + warp) + lane] = make_uint4(pt[0][0], pt[0][1], pt[1][0], pt[1][1]);
+          }
+          named_bar_sync(1, 32 * W);
+          if (warp == j) {
+#pragma unroll 1
+            for (int b2 = 0; b2 < W; ++b2) {
+              uint32_t w[4];
+              ldsm_x4_t(st + voff + 2048 * b2, w[0], w[1], w[2], w[3]);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t va[2][4];
+                mx_v_fragments(w[2 * h], w[2 * h + 1], va);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) va[i][k] = f16x2_to_bf16x2(va[i][k]);
+#pragma unroll
+                for (int n = 0; n < NG; ++n) {
+                  if (n && !two) break;
+                  const uint4 pv = pf[32 * (W * n + b2) + lane];
+                  mma_bf16(acc[n][0], va[0], h ? pv.z : pv.x, h ? pv.w : pv.y);
+                  mma_bf16(acc[n][1], va[1], h ? pv.z : pv.x, h ? pv.w : pv.y);
+                }
+              }
+            }
+          }
+          named_bar_sync(1, 32 * W);
+        }
+        fence_proxy_async_smem();  // (before the copy that overwrites the scores)
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
     }
@@ -694,7 +807,7 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
         if (g == 0) red_l[(warp * NG + n) * 8 + 2 * q4 + e] = l;
       }
     named_bar_sync(1, 32 * W);
-    const float back = __uint_as_float(*reinterpret_cast<const uint32_t*>(&vref) << 16);
+    const int back = (int)(win & 0xffffu) - (win >> 31 ? 127 + kMxFar : 128);
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
 #pragma unroll
@@ -702,11 +815,14 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
         L[n][e] = 0.f;
 #pragma unroll
         for (int w2 = 0; w2 < W; ++w2) L[n][e] += red_l[(w2 * NG + n) * 8 + 2 * q4 + e];
+        const int by = back - mx_lower(m_r[n][e], L[n][e]);
+        const float f0 = mx_pow2(by / 2), f1 = mx_pow2(by - by / 2);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          acc[n][i][e] = acc[n][i][e] * f0 * f1;
+          acc[n][i][2 + e] = acc[n][i][2 + e] * f0 * f1;
+        }
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[n][i][k] *= back;
     }
     const int64_t slot = min(max(slot0, (int64_t)0), a.max_chunks - 1);
     const int d = 32 * warp + 4 * g;
