@@ -583,6 +583,14 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
           }
         }
       }
+      // (rounded here, once: with the factor in the exponent's fma, the largest score and its
+      // reference would differ by the product's rounding, thousands for scores of 2^40)
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[n][b][k] *= slc;
       // ---------------- mask ----------------
       if (edge) {
         const uint8_t* mk = stp + Cfg::kOffMask + R0;
@@ -621,7 +629,7 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
               const int j = jw + 16 * b + key[k >> 1], c = 8 * n + 2 * q4;
               if (c < r.ncols && j < end)
                 *reinterpret_cast<float2*>(a.scores + (base + j) * a.score_cols + r.c0 + c) =
-                    make_float2(x[n][b][k] * slc, x[n][b][k + 1] * slc);
+                    make_float2(x[n][b][k], x[n][b][k + 1]);
             }
       }
       // ---------------- online softmax per column ----------------
@@ -634,8 +642,8 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
           float mx = fmaxf(x[n][0][e], x[n][0][2 + e]);
 #pragma unroll
           for (int b = 1; b < NB; ++b) mx = fmaxf(mx, fmaxf(x[n][b][e], x[n][b][2 + e]));
-          top[n][e] = mx * slc;
-          over |= top[n][e] > m_r[n][e] + kOver;
+          top[n][e] = mx;
+          over |= mx > m_r[n][e] + kOver;
         }
       // P^T in fp16, transposed (keys q, 12 + q and 4 + q, 8 + q of column g), to everyone
       uint4* pm = reinterpret_cast<uint4*>(smem + Cfg::kOffP) + (it & 1) * (NG * 32 * W);
@@ -651,7 +659,7 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
             float pr[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              pr[k] = fast_exp2(fmaf(x[n][b][k], slc, -mu[n][k & 1]));
+              pr[k] = fast_exp2(x[n][b][k] - mu[n][k & 1]);
               sum[n][k & 1] += pr[k];
             }
             pt[b][0] = movmatrix_t(pack_f16(pr[0], pr[1]));
@@ -755,8 +763,8 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
               for (int h = 0; h < 2; ++h) {
                 const int row = 16 * b + key[h], c = gone(jw + row) ? 0 : sv[4 * row];
                 const float e = c == 255 ? __int_as_float(0x7fffffff) : (float)(c + kMxFar - ref);
-                pt[b][h] = movmatrix_t(mx_halves(fast_exp2(fmaf(h ? v.z : v.x, slc, -mu[n][0]) + e),
-                                                 fast_exp2(fmaf(h ? v.w : v.y, slc, -mu[n][1]) + e), term & 1));
+                pt[b][h] = movmatrix_t(mx_halves(fast_exp2((h ? v.z : v.x) - mu[n][0] + e),
+                                                 fast_exp2((h ? v.w : v.y) - mu[n][1] + e), term & 1));
               }
             }
             pf[32 * (W * n + warp) + lane] = make_uint4(pt[0][0], pt[0][1], pt[1][0], pt[1][1]);
