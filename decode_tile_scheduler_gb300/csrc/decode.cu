@@ -664,6 +664,14 @@ __device__ __forceinline__ void combine_store(const DecodeArgs& a, int b, int64_
   }
 }
 
+// The power of two for a column's query in fp16, from the largest exponent among this lane's
+// elements; the four lanes of a column hold them all.
+__device__ __forceinline__ int column_shift(uint32_t emax) {
+  emax = max(emax, __shfl_xor_sync(0xffffffffu, emax, 1));
+  emax = max(emax, __shfl_xor_sync(0xffffffffu, emax, 2));
+  return min(max(142 - (int)emax, -100), 100);  // 15 - (emax - 127)
+}
+
 // ---------------------------------------------------------------------------
 // decode kernel
 // ---------------------------------------------------------------------------
@@ -1093,8 +1101,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // ---- Q^T fragments (mma B operand: k = d, n = column) ----
     uint32_t qb[NG][KS][2];
-    // score factor: scale * log2(e), times 2^-sh on the FP8 path (below)
-    float slc = a.scale_log2;
+    // score factors of columns 2q, 2q + 1: scale * log2(e), times 2^-sh on the FP8 path (below)
+    float slc[NG][2];
+#pragma unroll
+    for (int ng = 0; ng < NG; ++ng) slc[ng][0] = slc[ng][1] = a.scale_log2;
     {
       const uint16_t* qsm = reinterpret_cast<const uint16_t*>(smem + Cfg::kOffQ + qs * Cfg::kQBytes);
       if constexpr (!FP8) {
@@ -1111,20 +1121,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       } else {
         // The FP8 products run in fp16, whose range is far narrower than
-        // bf16's.  The unit's queries are multiplied by 2^sh, a power of two
-        // chosen from the largest exponent E among them so that the largest
-        // element lands at exponent 15 (sh = 15 - E, kept in [-100, 100]):
+        // bf16's.  A column's query is multiplied by 2^sh, a power of two
+        // chosen from the largest exponent E among its elements so that the
+        // largest lands at exponent 15 (sh = 15 - E, kept in [-100, 100]):
         // nothing overflows, every element within 2^-29 of the largest
         // converts exactly (smaller ones round to multiples of 2^(E-39),
         // far below the scores' tolerance), and the scores take 2^-sh back
-        // in their scale factor.  Powers of two scale exactly.
+        // in their scale factor.  Powers of two scale exactly.  (One power for
+        // all columns let an infinite or NaN query set the others to 0.)
         // k-step kk = 4*tile + j covers d = 64*tile + 16*q + 4*j + {0..3}:
         // slots 2q,2q+1 <- the first two, slots 2q+8,2q+9 <- the last two
-        uint32_t emax = 0;
 #pragma unroll
         for (int ng = 0; ng < NG; ++ng) {
           const int head = ng * 8 + g;
-          if (head < r.ncols) {
+          const bool ok = head < r.ncols;
+          uint32_t emax = 0;
+          if (ok) {
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
               const int d0 = (kk >> 2) * 64 + 16 * q4 + 4 * (kk & 3);
@@ -1133,15 +1145,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    max((v.y >> 7) & 0xffu, (v.y >> 23) & 0xffu)));
             }
           }
-        }
-        emax = __reduce_max_sync(0xffffffffu, emax);  // over the unit's columns
-        const int sh = min(max(142 - (int)emax, -100), 100);  // 15 - (emax - 127)
-        const float up = __int_as_float((127 + sh) << 23);
-        slc = a.scale_log2 * __int_as_float((127 - sh) << 23);
-#pragma unroll
-        for (int ng = 0; ng < NG; ++ng) {
-          const int head = ng * 8 + g;
-          const bool ok = head < r.ncols;
+          const int sh = column_shift(emax);
+          const float up = __int_as_float((127 + sh) << 23);
+          const float down = a.scale_log2 * __int_as_float((127 - sh) << 23);
+          slc[ng][0] = __shfl_sync(0xffffffffu, down, 8 * q4);
+          slc[ng][1] = __shfl_sync(0xffffffffu, down, 8 * q4 + 4);
 #pragma unroll
           for (int kk = 0; kk < KS; ++kk) {
             const int d0 = (kk >> 2) * 64 + 16 * q4 + 4 * (kk & 3);
@@ -1374,8 +1382,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            xs[ng][e] = sc[ng][e] * slc;
-            xs[ng][2 + e] = sc[ng][2 + e] * slc;
+            xs[ng][e] = sc[ng][e] * slc[ng][e];
+            xs[ng][2 + e] = sc[ng][2 + e] * slc[ng][e];
           }
       } else {
         // each column against its own row's bounds, and the explicit mask's
@@ -1397,8 +1405,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               okA = okA && mk[mrow[ng][e] + ta] == 0;
               okB = okB && mk[mrow[ng][e] + tb] == 0;
             }
-            xs[ng][e] = okA ? sc[ng][e] * slc : -INFINITY;
-            xs[ng][2 + e] = okB ? sc[ng][2 + e] * slc : -INFINITY;
+            xs[ng][e] = okA ? sc[ng][e] * slc[ng][e] : -INFINITY;
+            xs[ng][2 + e] = okB ? sc[ng][2 + e] * slc[ng][e] : -INFINITY;
           }
       }
       if (X && a.scores) {

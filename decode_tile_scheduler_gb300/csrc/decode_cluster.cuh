@@ -137,9 +137,9 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
       q[i] = __ldg(src + (FP8 ? 2 * (q4 + 4 * (i >> 1)) + (i & 1) : q4 + 4 * i));
     }
   }
-  // MXFP4: Q in fp16 times a power of two, K's 2 k-steps a group, the score factor (all
-  // as in decode_mx_kernel)
-  float slc = a.scale_log2;
+  // MXFP4: Q in fp16, each column times a power of two, K's 2 k-steps a group, the score
+  // factors (all as in decode_mx_kernel)
+  float slc[2];
   uint32_t win = kMxWindow * 0x1010101u, far = 0u;  // a byte a group: its window's top; 0x80: far
   if constexpr (MX) {
     uint32_t emax = 0;
@@ -149,10 +149,11 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
 #pragma unroll
       for (int k = 0; k < 4; ++k) emax = max(emax, max((w[k] >> 7) & 0xffu, (w[k] >> 23) & 0xffu));
     }
-    emax = __reduce_max_sync(0xffffffffu, emax);
-    const int sh = min(max(142 - (int)emax, -100), 100);
+    const int sh = column_shift(emax);
     const float up = __int_as_float((127 + sh) << 23);
-    slc = a.scale_log2 * __int_as_float((127 - sh) << 23);
+    const float down = a.scale_log2 * __int_as_float((127 - sh) << 23);
+    slc[0] = __shfl_sync(0xffffffffu, down, 8 * q4);
+    slc[1] = __shfl_sync(0xffffffffu, down, 8 * q4 + 4);
     const auto half = [&](uint32_t w) {
       return pack_f16(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up);
     };
@@ -334,7 +335,7 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
         }
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] *= slc;
+      for (int k = 0; k < 4; ++k) x[k] *= slc[k & 1];
     } else if constexpr (FP8) {
       float h[2][4];
 #pragma unroll

@@ -69,7 +69,8 @@ struct MxCfg {
   static constexpr int kOffMsg = (kOffBar + 8 * (2 * kStages + 2) + 15) / 16 * 16;
   static constexpr int kOffMisc = kOffMsg + 128;
   static constexpr int kOffGroups = kOffMisc + 16;            // the far groups' references
-  static constexpr int kSmem = kOffGroups + 4 * kWarps + 512;  // + alignment slack (a swizzle's 512 bytes)
+  static constexpr int kOffFactors = kOffGroups + 4 * kWarps;  // NG 2: the columns' score factors
+  static constexpr int kSmem = kOffFactors + (NG == 2 ? 64 : 0) + 512;  // + alignment slack (a swizzle's 512 bytes)
   static_assert(kStageBytes % 512 == 0, "alignment");
   static_assert(kCtas * (kSmem + 1024) <= 233472, "shared memory");
 };
@@ -403,16 +404,18 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
     const int t_begin = msg.t_begin, t_end = msg.t_end;
     const bool split = msg.nch > 1;
     const bool two = NG == 2 && r.ncols > 8;  // (columns in the second half)
-    // Q^T fragments in fp16, times a power of two that puts the unit's largest element at
-    // exponent 15 (decode_kernel tells why); k-step kk = 2*group + j covers
+    // Q^T fragments in fp16, each column times a power of two that puts its largest element
+    // at exponent 15 (decode_kernel tells why); k-step kk = 2*group + j covers
     // d = 32*group + 8*q + 4*j + {0..3}
     uint32_t qb[NG][KS][2];
-    float slc;
+    // the score factors of columns 2q, 2q + 1 (NG 2: in shared memory, for their registers)
+    float slc[2];
+    float* factors = reinterpret_cast<float*>(smem + Cfg::kOffFactors);
     {
       const uint16_t* qsm = reinterpret_cast<const uint16_t*>(smem + Cfg::kOffQ) + g * D + 8 * q4;
-      uint32_t top = 0;  // (bf16 magnitudes order as integers)
 #pragma unroll
-      for (int n = 0; n < NG; ++n)
+      for (int n = 0; n < NG; ++n) {
+        uint32_t top = 0;  // (bf16 magnitudes order as integers)
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
           uint2 v = make_uint2(0u, 0u);
@@ -422,13 +425,16 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
           qb[n][kk][1] = v.y;
           top = __vmaxu2(top, __vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu));
         }
-      const uint32_t emax = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu)) >> 7;
-      const int sh = min(max(142 - (int)emax, -100), 100);  // 15 - (emax - 127)
-      // (the score factor is positive, its sign in the queries: hidden scores stay -inf)
-      const float up = copysignf(__int_as_float((127 + sh) << 23), a.scale_log2);
-      slc = fmaxf(fabsf(a.scale_log2) * __int_as_float((127 - sh) << 23), 1e-36f);
-#pragma unroll
-      for (int n = 0; n < NG; ++n)
+        const int sh = column_shift(max(top >> 16, top & 0xffffu) >> 7);
+        // (the score factor is positive, its sign in the queries: hidden scores stay -inf)
+        const float up = copysignf(__int_as_float((127 + sh) << 23), a.scale_log2);
+        const float down = fmaxf(fabsf(a.scale_log2) * __int_as_float((127 - sh) << 23), 1e-36f);
+        if constexpr (NG == 2) {
+          if (warp == 0 && q4 == 0) factors[8 * n + g] = down;
+        } else {
+          slc[0] = __shfl_sync(0xffffffffu, down, 8 * q4);
+          slc[1] = __shfl_sync(0xffffffffu, down, 8 * q4 + 4);
+        }
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk)
 #pragma unroll
@@ -436,6 +442,7 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
             const uint32_t v = qb[n][kk][k];
             qb[n][kk][k] = pack_f16(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up);
           }
+      }
       if constexpr (NG == 2) {  // (the four warps' fragments are the same: each keeps a quarter)
         uint4* qs = reinterpret_cast<uint4*>(smem + Cfg::kOffQs) + lane;
 #pragma unroll
@@ -586,11 +593,17 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
       // (rounded here, once: with the factor in the exponent's fma, the largest score and its
       // reference would differ by the product's rounding, thousands for scores of 2^40)
 #pragma unroll
-      for (int n = 0; n < NG; ++n)
+      for (int n = 0; n < NG; ++n) {
+        float f[2] = {slc[0], slc[1]};
+        if constexpr (NG == 2) {
+          f[0] = factors[8 * n + 2 * q4];
+          f[1] = factors[8 * n + 2 * q4 + 1];
+        }
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[n][b][k] *= slc;
+          for (int k = 0; k < 4; ++k) x[n][b][k] *= f[k & 1];
+      }
       // ---------------- mask ----------------
       if (edge) {
         const uint8_t* mk = stp + Cfg::kOffMask + R0;
