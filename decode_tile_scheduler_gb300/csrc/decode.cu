@@ -664,6 +664,10 @@ __device__ __forceinline__ void combine_store(const DecodeArgs& a, int b, int64_
   }
 }
 
+// A column's reference where its sum is no number: 0.  (Scores that are all NaN leave -inf, the
+// mark of a column without keys, which the folds pass by.)
+__device__ __forceinline__ float number_of(float m, float l) { return l != l ? 0.f : m; }
+
 // The power of two for a column's query in fp16, from the largest exponent among this lane's
 // elements; the four lanes of a column hold them all.
 __device__ __forceinline__ int column_shift(uint32_t emax) {
@@ -1604,6 +1608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += __shfl_xor_sync(0xffffffffu, l, 8);
         l += __shfl_xor_sync(0xffffffffu, l, 16);
         l_r[ng][e] = l;
+        m_r[ng][e] = number_of(m_r[ng][e], l);
       }
       if (g == 0) {
         red_ml[(cw * kMaxGH + ng * 8 + 2 * q4) * 2 + 0] = m_r[ng][0];

@@ -836,6 +836,7 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
         L[n][e] = 0.f;
 #pragma unroll
         for (int w2 = 0; w2 < W; ++w2) L[n][e] += red_l[(w2 * NG + n) * 8 + 2 * q4 + e];
+        m_r[n][e] = number_of(m_r[n][e], L[n][e]);
         const int by = back - mx_lower(m_r[n][e], L[n][e]);
         const float f0 = mx_pow2(by / 2), f1 = mx_pow2(by - by / 2);
 #pragma unroll

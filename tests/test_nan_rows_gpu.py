@@ -1,0 +1,77 @@
+"""Rows whose scores are NaN give NaN, in one chunk or in many, and rows without keys zeros."""
+import pytest
+import torch
+
+import decode_tile_scheduler_gb300 as fia
+import fia_inputs as fi
+from tests import serving
+from tests.test_mx_cache_gpu import NO_CLUSTER
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+LENS = [2049, 1025, 0, 129, 1]
+
+
+def _problem(fmt, rows=1, QN=4, **kw):
+    args = dict(B=len(LENS), QN=QN, KVN=2, q_lens=[rows] * len(LENS), kv_lens=LENS, block_size=32, seed=71,
+                poison=False, mask_mode=3)
+    args.update(kw)
+    if fmt == "mx":
+        return serving.make_mx(**args)
+    return fi.make_fia(D=128, kv_dtype=fi.KV_FP8_E4M3 if fmt == "fp8" else fi.KV_BF16, **args)
+
+
+def _poison_key(p, fmt, b, j):
+    page, row = int(p.block_table[b, j // p.block_size]), j % p.block_size
+    if fmt == "mx":
+        p.k_scale[page, :, row, 1] = 255
+    elif fmt == "fp8":
+        p.k_cache[page, row, :, 40] = 0x7F
+    else:
+        p.k_cache[page, row, :, 40] = float("nan")
+
+
+def _out(p, num_sms, weights=False):
+    call = (fia.KeyWeightsCall if weights else fia.FiaCall)(p.to(DEV), num_sms=num_sms)
+    got = call.run()
+    torch.cuda.synchronize()
+    assert call.error_word() == 0
+    return [x.cpu() for x in got]
+
+
+def _check(got, clean, bad):
+    """bad [B, S, QN]: the rows that are NaN; the others' bits stay."""
+    assert torch.equal(torch.isnan(got[0]), bad[..., None].expand(got[0].shape))
+    assert torch.equal(got[0][~bad], clean[0][~bad])
+    lse, was = (x[1][..., 0].transpose(1, 2) for x in (got, clean))
+    assert torch.equal(torch.isnan(lse), bad) and torch.equal(lse[~bad], was[~bad])
+
+
+@pytest.mark.parametrize("num_sms", [0, 1, NO_CLUSTER])
+@pytest.mark.parametrize("kind", ["plain", "sinks", "window", "weights", "columns"])
+@pytest.mark.parametrize("fmt", ["mx", "fp8", "bf16"])
+def test_a_nan_key_alone_in_the_last_chunk(fmt, kind, num_sms):
+    kw = {"window": dict(mask_mode=4, pre_tokens=5000, first_tokens=4), "sinks": dict(with_sinks=True),
+          "columns": dict(QN=32)}.get(kind, {})
+    p = _problem(fmt, **kw)
+    clean = _out(p, num_sms, kind == "weights")
+    bad = torch.zeros(clean[0].shape[:3], dtype=torch.bool)
+    for b, n in enumerate(LENS):
+        if n:
+            _poison_key(p, fmt, b, n - 1)
+            bad[b] = True
+    _check(_out(p, num_sms, kind == "weights"), clean, bad)
+
+
+@pytest.mark.parametrize("num_sms", [0, 1, NO_CLUSTER])
+@pytest.mark.parametrize("rows", [1, 3])
+@pytest.mark.parametrize("fmt", ["mx", "fp8", "bf16"])
+def test_a_nan_query_over_many_chunks(fmt, rows, num_sms):
+    p = _problem(fmt, rows)
+    clean = _out(p, num_sms)
+    bad = torch.zeros(clean[0].shape[:3], dtype=torch.bool)
+    for b, n in enumerate(LENS):
+        p.q[b, rows - 1, 1, 9] = float("nan")
+        bad[b, rows - 1, 1] = n > 0
+    _check(_out(p, num_sms), clean, bad)
