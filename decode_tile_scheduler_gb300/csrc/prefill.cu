@@ -932,7 +932,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
       }
       // ---- epilogue ----
       float scl = 0.f, lse = INFINITY;
-      if (m_used != -INFINITY && l > 0.f) {  // l == 0: the row saw no key
+      if (l != l) {  // NaN among its scores
+        scl = lse = l;
+      } else if (m_used != -INFINITY && l > 0.f) {  // l == 0: the row saw no key
         float Mp = m_used, L = l;
         if (a.sinks) {
           const float sk = a.sinks[h] * 1.4426950408889634f;

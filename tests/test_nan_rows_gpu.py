@@ -75,3 +75,14 @@ def test_a_nan_query_over_many_chunks(fmt, rows, num_sms):
         p.q[b, rows - 1, 1, 9] = float("nan")
         bad[b, rows - 1, 1] = n > 0
     _check(_out(p, num_sms), clean, bad)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "fp8", "bf16"])
+def test_prompts(fmt):
+    p = _problem(fmt, 30, kv_lens=[2049, 1025, 0, 129, 1])
+    clean = _out(p, 0)
+    bad = torch.zeros(clean[0].shape[:3], dtype=torch.bool)
+    for b, n in enumerate(LENS):
+        p.q[b, 29, 1, 9] = float("nan")
+        bad[b, 29, 1] = n > 0
+    _check(_out(p, 0), clean, bad)
