@@ -181,7 +181,8 @@ __global__ void __launch_bounds__(256) kv_dequant_kernel(const DequantArgs a) {
 __global__ void __launch_bounds__(256, 6) mx_dequant_kernel(const DequantArgs a, int rows, int blocks) {
   constexpr int U = 2;
   const int b = blockIdx.x / blocks, j0 = (blockIdx.x - b * blocks) * rows;
-  const int kv_len = min(a.seqused_kv ? a.seqused_kv[b] : a.cap, a.cap);
+  // (never below 0: kv_len - j0 would leave 32 bits for a length near their lower end)
+  const int kv_len = max(min(a.seqused_kv ? a.seqused_kv[b] : a.cap, a.cap), 0);
   const int vectors = min(rows, kv_len - j0) * a.KVN, piece = threadIdx.x & 15;
   for (int v0 = threadIdx.x >> 4; v0 < vectors; v0 += 16 * U) {
     uint32_t code[2][U], scale[2][U];
