@@ -38,6 +38,29 @@ fia_status scratch_address(void** out) {
   return FIA_OK;
 }
 
+// Persistent CTAs of an MXFP4 plan, as fia_params' num_sms counts them, whose partial slots
+// fit the array: its three to an SM have slots for 24 units of 16 columns beside their own,
+// one to an SM for 175.  The most that fit, down to one to an SM; `lay` becomes their plan's.
+fia_status fit_ctas(fia_params* p, fia_plan_layout* lay) {
+  const int per = fia::decode_mx_ctas(), all = lay->num_ctas / per;
+  int lo = (all + per - 1) / per, hi = all;  // (the plan grows with their number; hi's does not fit)
+  fia_plan_layout l;
+  fia_status st;
+  auto fits = [&](int n) {
+    p->num_sms = n;
+    st = fia_get_plan_layout(p, &l);
+    return st == FIA_OK && l.total_bytes <= (int64_t)FIA_NOALLOC_SCRATCH_BYTES;
+  };
+  if (!fits(lo)) return st == FIA_OK ? FIA_ERR_WORKSPACE_TOO_SMALL : st;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (fits(mid)) lo = mid; else hi = mid;
+  }
+  fits(lo);
+  *lay = l;
+  return FIA_OK;
+}
+
 }  // namespace
 
 extern "C" fia_status fia_decode_run_noalloc(const fia_params* p, int32_t* status, void* stream) {
@@ -46,7 +69,14 @@ extern "C" fia_status fia_decode_run_noalloc(const fia_params* p, int32_t* statu
   fia_status st = fia_get_plan_layout(p, &lay);
   if (st != FIA_OK) return st;
   if (lay.branch == 2) return FIA_ERR_UNSUPPORTED;  // decode only
-  if (lay.total_bytes > (int64_t)FIA_NOALLOC_SCRATCH_BYTES) return FIA_ERR_WORKSPACE_TOO_SMALL;
+  fia_params fewer;
+  if (lay.total_bytes > (int64_t)FIA_NOALLOC_SCRATCH_BYTES) {
+    if (lay.branch != 1 || p->kv_dtype != FIA_KV_MXFP4) return FIA_ERR_WORKSPACE_TOO_SMALL;
+    fewer = *p;
+    st = fit_ctas(&fewer, &lay);
+    if (st != FIA_OK) return st;
+    p = &fewer;
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (lay.branch == 0) {  // no query row: nothing runs, and nothing failed
     if (status && cudaMemsetAsync(status, 0, sizeof(int32_t), s) != cudaSuccess)

@@ -271,8 +271,10 @@ fia_status fia_run(const fia_params *p, void *workspace, size_t workspace_bytes,
  *    word lives in the library's array.
  *  - Returns FIA_ERR_WORKSPACE_TOO_SMALL, before launching anything, when the
  *    decode plan needs more than FIA_NOALLOC_SCRATCH_BYTES (what fia_get_
- *    workspace_size reports for the same params), FIA_ERR_UNSUPPORTED for the
- *    prefill branch, and any status fia_run returns.
+ *    workspace_size reports for the same params; over an MXFP4 cache, whose
+ *    plans have three persistent CTAs to an SM, with as many of them as fit, but
+ *    one to an SM at least), FIA_ERR_UNSUPPORTED for the prefill branch, and any
+ *    status fia_run returns.
  *  - Every call looks up the array's device address in the current context;
  *    the first call on a device loads the library's device code there, so
  *    make that first call before any stream capture.
