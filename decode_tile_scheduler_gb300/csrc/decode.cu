@@ -668,6 +668,50 @@ __device__ __forceinline__ void combine_store(const DecodeArgs& a, int b, int64_
 // mark of a column without keys, which the folds pass by.)
 __device__ __forceinline__ float number_of(float m, float l) { return l != l ? 0.f : m; }
 
+// V scales of a coded cache against P, which is multiplied in fp16 (MXFP4, and FP8 in
+// decode_few_kernel).  While the scales of a warp's keys lie within 16 binades, a window of
+// exponents set by the first of them, P times its scale over the window's top has fp16's bits
+// for every key that counts.  A scale outside the window makes the elements under such scales
+// far for the rest of the chunk: their products are made of the scores with the exponents
+// added, as two terms in bf16.  (Over the largest scale alone, hidden keys' too, a key of
+// large V and no weight set all others to 0.)
+//
+// A far sum lies 2^kFar lower against the largest scale: products up to 2^15 times 2^kFar,
+// and sums of them, stay in fp32, and scales down to 2^-190 of the largest keep their bits.
+constexpr int kFar = 60;
+// The window's top for exponents of least .. most (0: none, the window `start` stays); it is
+// below `most` where they do not fit.
+__device__ __forceinline__ uint32_t scale_window(uint32_t least, uint32_t most, uint32_t start) {
+  return most == 0u ? start : min(max(most + 4u, 15u), min(least + 15u, 254u));
+}
+// 2^e as a float, 0 below its normal numbers.
+__device__ __forceinline__ float pow2_of(int e) { return __int_as_float(max(min(e, 127) + 127, 0) << 23); }
+// Two values as a pair of bf16, or (`rest`) what such a pair leaves of them.
+__device__ __forceinline__ uint32_t bf16_term(float a, float b, bool rest) {
+  const uint32_t w = pack_bf16(a, b);
+  return rest ? pack_bf16(a - __uint_as_float(w << 16), b - __uint_as_float(w & 0xffff0000u)) : w;
+}
+// A pair of fp16 codes' values as bf16 (exact).
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t w) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return pack_bf16(f.x, f.y);
+}
+// FP8: the exponents of a key's two scales in 16 bits each; where a window starts (its inner
+// eight are those of 64 values whose largest is 2^-4 to 14); and a far product of score x
+// less its reference and scale v, over 2^(top - 127 - kFar).
+constexpr uint32_t kFp8Window = 125;
+constexpr int kFp8Least = 7;  // decode_kernel's least reference: 2^-120
+__device__ __forceinline__ uint32_t exponents2(const float2& v) {
+  return (__float_as_uint(v.x) >> 23 & 0xffu) | (__float_as_uint(v.y) >> 7 & 0xff0000u);
+}
+__device__ __forceinline__ float far_product(float x, float v, int top) {
+  const uint32_t bits = __float_as_uint(v);
+  const int e = (int)(bits >> 23 & 0xffu);
+  if (e == 0) return 0.f;
+  const float mant = e == 255 ? v : __uint_as_float((bits & 0x807fffffu) | 0x3f800000u);
+  return fast_exp2(x + (float)(e - top + kFar)) * mant;
+}
+
 // The power of two for a column's query in fp16, from the largest exponent among this lane's
 // elements; the four lanes of a column hold them all.
 __device__ __forceinline__ int column_shift(uint32_t emax) {
@@ -1186,7 +1230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       m_r[ng][0] = m_r[ng][1] = -INFINITY;
       l_r[ng][0] = l_r[ng][1] = 0.f;
     }
-    int vexp[2] = {0, 0};  // FP8: exponent of the V scale reference per d-tile (0: none yet)
+    int vexp[2] = {kFp8Least, kFp8Least};  // FP8: the V scale reference's exponent per d-tile
 
     // FP8: the P V of each tile runs one tile late, beside the next tile's
     // Q K^T and softmax (two independent instruction streams per warp)
@@ -1381,6 +1425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // any column needs that; only then are the row maxima reduced.
       float xs[NG][4];
       bool over = false;
+      bool seen0 = true, seen1 = true;  // FP8: this lane's two keys, by one of its columns
       if (!edge) {
 #pragma unroll
         for (int ng = 0; ng < NG; ++ng)
@@ -1394,6 +1439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // bytes of that row (staged with the tile) where there is one
         const uint8_t* mk = stp + Cfg::kOffMask;
         const int ta = R0 + rho16(g), tb = R0 + rho16(g + 8);  // rows within the tile
+        seen0 = seen1 = false;
 #pragma unroll
         for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
@@ -1409,6 +1455,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               okA = okA && mk[mrow[ng][e] + ta] == 0;
               okB = okB && mk[mrow[ng][e] + tb] == 0;
             }
+            seen0 |= okA;
+            seen1 |= okB;
             xs[ng][e] = okA ? sc[ng][e] * slc[ng][e] : -INFINITY;
             xs[ng][2 + e] = okB ? sc[ng][2 + e] * slc[ng][e] : -INFINITY;
           }
@@ -1517,31 +1565,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         static_assert(NT == 2, "FP8 decode is built for D = 128");
         const float* vs = reinterpret_cast<const float*>(stp + 2 * Cfg::kTileBytes + Cfg::kScaleBytes);
         const int rowa = R0 + pi8(g), rowb = R0 + 8 + pi8(g);
-        // V scales of fragment rows g, g+8 (zero where the row is gone)
+        // V scales of fragment rows g, g+8; zero where none of this lane's columns sees the
+        // key, whose V may then be of any size and takes nothing from the others
         float2 v0 = *reinterpret_cast<const float2*>(vs + rowa * NT);
         float2 v1 = *reinterpret_cast<const float2*>(vs + rowb * NT);
-        if (cut) {
-          if (gone(jg0)) v0 = make_float2(0.f, 0.f);
-          if (gone(jg1)) v1 = make_float2(0.f, 0.f);
-        }
+        if (!seen0) v0 = make_float2(0.f, 0.f);
+        if (!seen1) v1 = make_float2(0.f, 0.f);
         // Warp-wide power-of-two reference per d-tile: 2^(e-127) with e the
         // largest exponent of a V scale seen so far (positive floats order
         // like their bit patterns, so one warp max over the bits finds it).
-        // P^T * scale / ref then stays below 2^9 in fp16, and moving the
+        // P^T * scale * 2^6 / ref then stays below 2^15 in fp16, and moving the
         // reference rescales the accumulators by an exact power of two.
         float ratio[2], iv[2];
 #pragma unroll
         for (int t2 = 0; t2 < 2; ++t2) {
           const uint32_t bits = max(__float_as_uint(t2 ? v0.y : v0.x), __float_as_uint(t2 ? v1.y : v1.x));
-          const int e = (int)(__reduce_max_sync(0xffffffffu, bits) >> 23);
+          const int e = min((int)(__reduce_max_sync(0xffffffffu, bits) >> 23), 253);
           const int en = max(vexp[t2], e);
-          // 2^(old - new) and 2^(127 - new) built from their exponent bits
+          // 2^(old - new) and 2^(133 - new) built from their exponent bits
           // (a jump past 2^-126 leaves a negligible old sum and gives 0)
-          ratio[t2] = (en == vexp[t2] || vexp[t2] == 0)
-                          ? 1.f
-                          : __int_as_float(max(127 + vexp[t2] - en, 0) << 23);
+          ratio[t2] = en == vexp[t2] ? 1.f : __int_as_float(max(127 + vexp[t2] - en, 0) << 23);
           vexp[t2] = en;
-          iv[t2] = (en > 0 && en < 254) ? __int_as_float((254 - en) << 23) : 1.f;
+          iv[t2] = __int_as_float((260 - en) << 23);
         }
         // P^T of this tile with the V scales folded in, and the factors the
         // accumulators take before its P V is added
@@ -1587,7 +1632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (FP8) {
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        const float f = vexp[i >> 2] > 0 ? __int_as_float(vexp[i >> 2] << 23) : 1.f;  // 2^(e-127)
+        const float f = __int_as_float((vexp[i >> 2] - 6) << 23);  // 2^(e-133)
 #pragma unroll
         for (int ng = 0; ng < NG; ++ng) {
           acc[i][ng][0] *= f; acc[i][ng][1] *= f; acc[i][ng][2] *= f; acc[i][ng][3] *= f;

@@ -175,7 +175,8 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
   __syncthreads();
 
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  int vexp[2] = {1, 1};  // FP8: O is kept over 2^(vexp - 127), per half of D
+  // FP8: the windows of the halves' V scales as in decode_kernel; O over 2^(top - 140)
+  uint32_t win8 = kFp8Window * 0x10001u;
   float O[NV][4][4];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
@@ -286,12 +287,12 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
           const bool was = far >> (8 * j + 7) & 1u;
           const uint32_t most = __reduce_max_sync(0xffffffffu, code == 255u ? 0u : code);
           const uint32_t least = __reduce_min_sync(0xffffffffu, code == 0u ? 255u : code);
-          const uint32_t top = n == 0 ? mx_window(least, most) : win >> (8 * j) & 255u;
+          const uint32_t top = n == 0 ? scale_window(least, most, kMxWindow) : win >> (8 * j) & 255u;
           const bool is = was || most > top || least + 15 < top;
           const uint32_t now = is ? max(top, most) : top;
           if (is) {
-            const int e = (int)(top - now) - (was ? kMxFar : 1) + kMxFar;
-            const float f0 = mx_pow2(e / 2), f1 = mx_pow2(e - e / 2);
+            const int e = (int)(top - now) - (was ? kFar : 1) + kFar;
+            const float f0 = pow2_of(e / 2), f1 = pow2_of(e - e / 2);
 #pragma unroll
             for (int i = 2 * (j & 1); i < 2 * (j & 1) + 2; ++i)
 #pragma unroll
@@ -381,20 +382,38 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
 
     // ---- softmax: this warp's running maximum and sum ----
     // FP8: P times its V scale is multiplied in fp16 (the codes are fp16 values, and
-    // bf16 would drop three bits of P), over a power of two near the largest scale so
-    // far, which keeps it below 4; a new one moves O by an exact factor.
-    float ratio[2], over[2];
+    // bf16 would drop three bits of P), as in decode_kernel.
+    float over[2];
     if constexpr (FP8) {
+      uint32_t e[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t bits = max(__float_as_uint(fabsf(i ? vsc[0].y : vsc[0].x)),
-                                  __float_as_uint(fabsf(i ? vsc[1].y : vsc[1].x)));
-        const int en = max(vexp[i], min((int)(__reduce_max_sync(0xffffffffu, bits) >> 23), 253));
-        // (a jump past 2^-126 leaves a negligible old sum and gives 0)
-        ratio[i] = __int_as_float(max(127 + vexp[i] - en, 0) << 23);
-        over[i] = __int_as_float((254 - en) << 23);
-        vexp[i] = en;
+      for (int k = 0; k < 2; ++k) e[k] = seen(g + 8 * k) ? exponents2(vsc[k]) : win8 - 0x40004u;
+      const uint32_t high = n == 0 ? win8 - 0x40004u : win8, out = n == 0 ? 0xfff8fff8u : 0xfff0fff0u;
+      if (__any_sync(0xffffffffu, (((high - e[0]) | (high - e[1])) & out) != 0u)) {
+        uint32_t next = 0u;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t u = e[0] >> (16 * i) & 0xffu, v = e[1] >> (16 * i) & 0xffu;
+          const uint32_t most = __reduce_max_sync(0xffffffffu, max(u == 255u ? 0u : u, v == 255u ? 0u : v));
+          const uint32_t least = __reduce_min_sync(0xffffffffu, min(u == 0u ? 255u : u, v == 0u ? 255u : v));
+          const uint32_t top = n == 0 ? scale_window(least, most, kFp8Window) : win8 >> (16 * i) & 0xffu;
+          const bool was = win8 >> (16 * i + 15) & 1u, is = was || most > top || least + 15 < top;
+          const uint32_t now = is ? max(top, most) : top;
+          if (is) {
+            const int by = (int)(top - now) - (was ? kFar : 13) + kFar;
+            const float f0 = pow2_of(by / 2), f1 = pow2_of(by - by / 2);
+#pragma unroll
+            for (int t4 = 0; t4 < 4; ++t4)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) O[i][t4][k] = O[i][t4][k] * f0 * f1;
+          }
+          next |= (now | (is ? 0x8000u : 0u)) << (16 * i);
+        }
+        win8 = next;
       }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)  // (far: O's products are made apart)
+        over[i] = win8 >> (16 * i + 15) & 1u ? 0.f : pow2_of(140 - (int)(win8 >> (16 * i) & 0xffu));
     }
     float p[4], mus[2];
 #pragma unroll
@@ -414,9 +433,8 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float f = FP8 ? corr * ratio[i] : corr;
-          O[i][k][e] *= f;
-          O[i][k][2 + e] *= f;
+          O[i][k][e] *= corr;
+          O[i][k][2 + e] *= corr;
         }
     }
 
@@ -445,7 +463,7 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (!(far >> (8 * j + 7) & 1u)) continue;
-          const int top = (int)(win >> (8 * j) & 255u) - kMxFar;
+          const int top = (int)(win >> (8 * j) & 255u) - kFar;
           const int c0 = rows[2432 + g * 4 + j], c1 = rows[2432 + (g + 8) * 4 + j];
           const float s0 = c0 == 255 ? __int_as_float(0x7fffffff) : (float)(c0 - top);
           const float s1 = c1 == 255 ? __int_as_float(0x7fffffff) : (float)(c1 - top);
@@ -460,8 +478,8 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
             for (int y = 0; y < 4; ++y) va[i][y] = f16x2_to_bf16x2(va[i][y]);
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            b0 = movmatrix_t(mx_halves(t0, t1, y));
-            b1 = movmatrix_t(mx_halves(t2, t3, y));
+            b0 = movmatrix_t(bf16_term(t0, t1, y));
+            b1 = movmatrix_t(bf16_term(t2, t3, y));
             mma_bf16(O[j >> 1][2 * (j & 1)], va[0], b0, b1);
             mma_bf16(O[j >> 1][2 * (j & 1) + 1], va[1], b0, b1);
           }
@@ -498,6 +516,32 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
         }
       }
     }
+    if (FP8 && (win8 & 0x80008000u)) {  // P times its scale from the scores, as two terms in bf16
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (!(win8 >> (16 * i + 15) & 1u)) continue;
+        const int top = (int)(win8 >> (16 * i) & 0xffu);
+        float t4[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          t4[k] = far_product(x[k] - mus[k & 1], i ? vsc[k >> 1].y : vsc[k >> 1].x, top);
+#pragma unroll
+        for (int term = 0; term < 2; ++term) {
+          b0 = movmatrix_t(bf16_term(t4[0], t4[1], term));
+          b1 = movmatrix_t(bf16_term(t4[2], t4[3], term));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t f[4];
+            const uint32_t sel = k & 1 ? 0x7362u : 0x5140u;
+            const uint32_t y0 = k < 2 ? vx[0][i].x : vx[0][i].y, y1 = k < 2 ? vx[1][i].x : vx[1][i].y;
+            const uint32_t y2 = k < 2 ? vx[2][i].x : vx[2][i].y, y3 = k < 2 ? vx[3][i].x : vx[3][i].y;
+            codes_bf16(__byte_perm(y0, y1, sel), f[0], f[1]);
+            codes_bf16(__byte_perm(y2, y3, sel), f[2], f[3]);
+            mma_bf16(O[i][k], f, b0, b1);
+          }
+        }
+      }
+    }
   }
 
   // ---- the CTA's warps ----
@@ -512,19 +556,20 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
 #pragma unroll
       for (int t = 0; t < 8; ++t) {  // group t / 2, elements 4g + 2 (t % 2) and the next
         const int back = (int)(win >> (4 * (t & 6)) & 255u) - lower -
-                         (far >> (4 * (t & 6) + 7) & 1u ? 127 + kMxFar : 128);
-        const float back0 = mx_pow2(back / 2), back1 = mx_pow2(back - back / 2);
+                         (far >> (4 * (t & 6) + 7) & 1u ? 127 + kFar : 128);
+        const float back0 = pow2_of(back / 2), back1 = pow2_of(back - back / 2);
         *reinterpret_cast<float2*>(&o_warp[wid][2 * q4 + e][32 * (t >> 1) + 4 * g + 2 * (t & 1)]) =
             make_float2(O[t >> 2][t & 3][e] * back0 * back1, O[t >> 2][t & 3][2 + e] * back0 * back1);
       }
     }
 #pragma unroll
     for (int i = 0; i < NV && !MX; ++i) {
-      const float back = FP8 ? __int_as_float(vexp[i] << 23) : 1.f;
+      const int by = FP8 ? (int)(win8 >> (16 * i) & 0xffu) - (win8 >> (16 * i + 15) & 1u ? 127 + kFar : 140) : 0;
+      const float back0 = FP8 ? pow2_of(by / 2) : 1.f, back1 = FP8 ? pow2_of(by - by / 2) : 1.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k)  // elements 2k and 2k + 1 of piece g + 8i
         *reinterpret_cast<float2*>(&o_warp[wid][2 * q4 + e][(g + 8 * i) * 8 + 2 * k]) =
-            make_float2(back * O[i][k][e], back * O[i][k][2 + e]);
+            make_float2(back0 * O[i][k][e] * back1, back0 * O[i][k][2 + e] * back1);
     }
   }
   __syncthreads();

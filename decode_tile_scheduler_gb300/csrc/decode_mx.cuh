@@ -25,7 +25,7 @@
 //    their 32 elements in fp32; V scales multiply P, already in fp16 and transposed, as
 //    fp16 pairs, where a chunk's scales of a group lie within 16 binades.  A group whose
 //    scales do not has its P times scale made of the scores, as two terms in bf16, whose
-//    exponents reach (kMxFar): a key of little weight, or none, takes no bit from the
+//    exponents reach (kFar): a key of little weight, or none, takes no bit from the
 //    others however large its V is.
 //
 // Measured (one GB300; the call with plan and combine): 4 sequences of 32 to 128 k keys,
@@ -106,37 +106,17 @@ __device__ __forceinline__ void e8m0x4_to_f32x4(uint32_t w, float (&f)[4]) {
   e8m0x4_to_bf16x2x2(w, v);
   bf16x2x2_to_f32x4(v[0], v[1], f);
 }
-// A far group's O lies this much lower against the largest scale: products up to 2^14 with
-// 2^kMxFar, and sums of them, stay in fp32, and scales down to 2^-195 of the largest keep
-// the bits of bf16.
-constexpr int kMxFar = 60;
 // Where a window of V scales starts: its inner codes, 2^-7 to 1, are those of 32 values whose
 // largest is 2^-6 to 6 (at 0 a chunk's first tile took its way to a window always: 32
 // sequences of 512 to 4096 keys 35.7 us for 35.3, two of 300 and 777 9.5 for 9.0).
 constexpr uint32_t kMxWindow = 131;
-// The window for codes of least .. most (0: none), the largest of which it may not reach.
-__device__ __forceinline__ uint32_t mx_window(uint32_t least, uint32_t most) {
-  return most == 0u ? kMxWindow : min(max(most + 4u, 15u), min(least + 15u, 254u));
-}
-// 2^e as a float, 0 below its normal numbers.
-__device__ __forceinline__ float mx_pow2(int e) { return __int_as_float(max(min(e, 127) + 127, 0) << 23); }
 // A column's sum l as l * 2^-k below 2^-7, k returned and its exponent moved by it: O, moved
 // as far, is then a 128th of an average of V, and 128 such do not leave fp32 together.
 __device__ __forceinline__ int mx_lower(float& m, float& l) {
   const int k = l > 0.f ? (int)(__float_as_uint(l) >> 23) - 119 : 0;
   m += (float)k;
-  l *= mx_pow2(-k);
+  l *= pow2_of(-k);
   return k;
-}
-// Two values as a pair of bf16, or (`rest`) what such a pair leaves of them.
-__device__ __forceinline__ uint32_t mx_halves(float a, float b, bool rest) {
-  const uint32_t w = pack_bf16(a, b);
-  return rest ? pack_bf16(a - __uint_as_float(w << 16), b - __uint_as_float(w & 0xffff0000u)) : w;
-}
-// A pair of fp16 codes' values as bf16 (exact).
-__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t w) {
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-  return pack_bf16(f.x, f.y);
 }
 // Keys of a block of 16.  The transposing ldmatrix gives a lane keys a, b of its first
 // matrix and c, d of its second, whose codes pair as (a, c) and (b, d); movmatrix gives it
@@ -482,7 +462,7 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
     // is below 2^-18 of O's terms.  It stays where it is unless a scale of the chunk's first
     // tile lies outside its inner eight codes.  A later code outside it, NaN (255) and 0
     // (values below bf16's normal numbers) apart, makes the group far for the rest of the
-    // chunk: O is then over 2^(win - 127 - kMxFar), win the largest code so far.  Both halves
+    // chunk: O is then over 2^(win - 127 - kFar), win the largest code so far.  Both halves
     // of `win` hold the code; far: the upper one 0xffff.
     uint32_t win = kMxWindow * 0x10001u;
     if (lane == 0) reinterpret_cast<int*>(smem + Cfg::kOffGroups)[warp] = 0;
@@ -527,12 +507,12 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
             }
           most = __reduce_max_sync(0xffffffffu, most);
           least = __reduce_min_sync(0xffffffffu, least);
-          const uint32_t top = tt == 0 ? mx_window(least, most) : win & 0xffffu;
+          const uint32_t top = tt == 0 ? scale_window(least, most, kMxWindow) : win & 0xffffu;
           const bool was = win >> 31, far = was || most > top || least + 15 < top;
           const uint32_t now = far ? max(top, most) : top;
           if (far) {
-            const int e = (int)(top - now) - (was ? kMxFar : 1) + kMxFar;  // O moves by 2^e
-            const float f0 = mx_pow2(e / 2), f1 = mx_pow2(e - e / 2);
+            const int e = (int)(top - now) - (was ? kFar : 1) + kFar;  // O moves by 2^e
+            const float f0 = pow2_of(e / 2), f1 = pow2_of(e - e / 2);
 #pragma unroll
             for (int n = 0; n < NG; ++n)
 #pragma unroll
@@ -756,7 +736,7 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
         }
       }
       if (any_far) {
-        // A far group's P times its scale over 2^(its reference - kMxFar), as two terms in bf16
+        // A far group's P times its scale over 2^(its reference - kFar), as two terms in bf16
         // one after the other, goes through the other copy of P, which nobody reads now.
         const float4* xs = reinterpret_cast<const float4*>(stp + R0 * Cfg::kRowBytes) + lane;
         uint4* pf = reinterpret_cast<uint4*>(smem + Cfg::kOffP) + (~it & 1) * (NG * 32 * W);
@@ -775,8 +755,8 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const int row = 16 * b + key[h], c = gone(jw + row) ? 0 : sv[4 * row];
-                const float e = c == 255 ? __int_as_float(0x7fffffff) : (float)(c + kMxFar - ref);
-                pt[b][h] = movmatrix_t(mx_halves(fast_exp2((h ? v.z : v.x) - mu[n][0] + e),
+                const float e = c == 255 ? __int_as_float(0x7fffffff) : (float)(c + kFar - ref);
+                pt[b][h] = movmatrix_t(bf16_term(fast_exp2((h ? v.z : v.x) - mu[n][0] + e),
                                                  fast_exp2((h ? v.w : v.y) - mu[n][1] + e), term & 1));
               }
             }
@@ -828,7 +808,7 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
         if (g == 0) red_l[(warp * NG + n) * 8 + 2 * q4 + e] = l;
       }
     named_bar_sync(1, 32 * W);
-    const int back = (int)(win & 0xffffu) - (win >> 31 ? 127 + kMxFar : 128);
+    const int back = (int)(win & 0xffffu) - (win >> 31 ? 127 + kFar : 128);
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
 #pragma unroll
@@ -838,7 +818,7 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
         for (int w2 = 0; w2 < W; ++w2) L[n][e] += red_l[(w2 * NG + n) * 8 + 2 * q4 + e];
         m_r[n][e] = number_of(m_r[n][e], L[n][e]);
         const int by = back - mx_lower(m_r[n][e], L[n][e]);
-        const float f0 = mx_pow2(by / 2), f1 = mx_pow2(by - by / 2);
+        const float f0 = pow2_of(by / 2), f1 = pow2_of(by - by / 2);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           acc[n][i][e] = acc[n][i][e] * f0 * f1;

@@ -56,7 +56,11 @@
  *    lse = +inf, with or without a sink ("...V4" empty-tensor rule; "...V2"
  *    invalid-row correction);
  *  - FP8 KV: E4M3 codes with one fp32 scale per 64 consecutive elements of D,
- *    value = code * scale; sparse packed FP8 rows carry E8M0 tile scales;
+ *    value = code * scale; sparse packed FP8 rows carry E8M0 tile scales.
+ *    Products with V are held in fp16 against the largest V scale: decode, of the
+ *    keys that a row sees, where scales down to 2^-20 of it keep their bits (calls of
+ *    few units with first_tokens or key weights: any); prompts, of a sequence's KV
+ *    head, down to 2^-14;
  *  - MXFP4 KV: E2M1 codes (sign, two exponent bits, one of mantissa: 0, 0.5, 1,
  *    1.5, 2, 3, 4, 6) with one E8M0 scale byte s per 32 consecutive elements of
  *    D, value = code * 2^(s - 127); s = 255 makes the 32 values NaN.
