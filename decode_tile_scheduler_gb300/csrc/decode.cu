@@ -1579,9 +1579,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         float ratio[2], iv[2];
 #pragma unroll
         for (int t2 = 0; t2 < 2; ++t2) {
-          const uint32_t bits = max(__float_as_uint(t2 ? v0.y : v0.x), __float_as_uint(t2 ? v1.y : v1.x));
-          const int e = min((int)(__reduce_max_sync(0xffffffffu, bits) >> 23), 253);
-          const int en = max(vexp[t2], e);
+          const uint32_t b0 = __float_as_uint(t2 ? v0.y : v0.x), b1 = __float_as_uint(t2 ? v1.y : v1.x);
+          // (infinite or NaN ones are no reference for the rows that see none)
+          const uint32_t most =
+              __reduce_max_sync(0xffffffffu, max(b0 < 0x7f800000u ? b0 : 0u, b1 < 0x7f800000u ? b1 : 0u));
+          const int en = max(vexp[t2], min((int)(most >> 23), 253));
           // 2^(old - new) and 2^(133 - new) built from their exponent bits
           // (a jump past 2^-126 leaves a negligible old sum and gives 0)
           ratio[t2] = en == vexp[t2] ? 1.f : __int_as_float(max(127 + vexp[t2] - en, 0) << 23);

@@ -145,3 +145,20 @@ def test_a_nan_scale_beside_far_ones(num_sms):
     assert torch.equal(torch.isnan(got[0]), ~same)
     assert torch.all(((got[0][0].cpu().double() - o).abs() <= to)[same[0].cpu()])
     assert torch.all((got[1][0, :, :, 0].T.cpu().double() - l).abs() <= bounded.lse_tolerance(p, A, 300))
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("num_sms", [0, 1, NO_CLUSTER])
+@pytest.mark.parametrize("QN,kw", [(4, dict(mask_mode=3)), (16, dict(mask_mode=3)), (4, FEW)])
+def test_rows_that_do_not_see_an_infinite_scale(QN, kw, num_sms, value):
+    """The newest key's scale is no number: the row that sees it gives NaN, and the others give
+    NaN or what they are, nothing between."""
+    p = _problem(B=1, QN=QN, KVN=2, q_lens=[4], kv_lens=[700], seed=50, **kw)
+    o, _, _, mag, A = bounded.attention(p)[0]
+    page, row = _at(p, 699)
+    p.v_scale[page, :, row] = value
+    got = _run(p, num_sms=num_sms)[0][0].cpu().double()
+    # (infinities times codes of either sign, or of 0)
+    assert not torch.isfinite(got[3]).any()
+    to = 1.01 * bounded.HALF_BF16 * (mag + o.abs()) + 2 * (bounded.lse_tolerance(p, A, 700) + bounded.HALF_FP16) * mag
+    assert torch.all(((got - o).abs() <= to)[:3] | torch.isnan(got[:3]))
