@@ -1179,25 +1179,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         // all columns let an infinite or NaN query set the others to 0.)
         // k-step kk = 4*tile + j covers d = 64*tile + 16*q + 4*j + {0..3}:
         // slots 2q,2q+1 <- the first two, slots 2q+8,2q+9 <- the last two
+        uint32_t emax[NG];
 #pragma unroll
         for (int ng = 0; ng < NG; ++ng) {
           const int head = ng * 8 + g;
-          const bool ok = head < r.ncols;
-          uint32_t emax = 0;
-          if (ok) {
+          emax[ng] = 0;
+          if (head < r.ncols) {
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
               const int d0 = (kk >> 2) * 64 + 16 * q4 + 4 * (kk & 3);
               const uint2 v = *reinterpret_cast<const uint2*>(qsm + head * D + d0);
-              emax = max(emax, max(max((v.x >> 7) & 0xffu, (v.x >> 23) & 0xffu),
-                                   max((v.y >> 7) & 0xffu, (v.y >> 23) & 0xffu)));
+              emax[ng] = max(emax[ng], max(max((v.x >> 7) & 0xffu, (v.x >> 23) & 0xffu),
+                                           max((v.y >> 7) & 0xffu, (v.y >> 23) & 0xffu)));
             }
           }
-          const int sh = column_shift(emax);
-          const float up = __int_as_float((127 + sh) << 23);
+        }
+        float up[NG];
+#pragma unroll
+        for (int ng = 0; ng < NG; ++ng) {
+          const int sh = column_shift(emax[ng]);
+          up[ng] = __int_as_float((127 + sh) << 23);
           const float down = a.scale_log2 * __int_as_float((127 - sh) << 23);
           slc[ng][0] = __shfl_sync(0xffffffffu, down, 8 * q4);
           slc[ng][1] = __shfl_sync(0xffffffffu, down, 8 * q4 + 4);
+        }
+#pragma unroll
+        for (int ng = 0; ng < NG; ++ng) {
+          const int head = ng * 8 + g;
+          const bool ok = head < r.ncols;
 #pragma unroll
           for (int kk = 0; kk < KS; ++kk) {
             const int d0 = (kk >> 2) * 64 + 16 * q4 + 4 * (kk & 3);
@@ -1205,8 +1214,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint2 v = *reinterpret_cast<const uint2*>(qsm + head * D + d0);
               const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
               const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.y));
-              qb[ng][kk][0] = pack_f16(lo.x * up, lo.y * up);
-              qb[ng][kk][1] = pack_f16(hi.x * up, hi.y * up);
+              qb[ng][kk][0] = pack_f16(lo.x * up[ng], lo.y * up[ng]);
+              qb[ng][kk][1] = pack_f16(hi.x * up[ng], hi.y * up[ng]);
             } else {
               qb[ng][kk][0] = qb[ng][kk][1] = 0u;
             }
