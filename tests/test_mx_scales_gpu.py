@@ -143,3 +143,14 @@ def test_many_rows_of_far_scales():
     p.v_scale = _spread(p, 100, 150, 51)
     _check(p)
     assert all(torch.equal(x, y) for x, y in zip(_run(p), _run(p)))
+
+
+@pytest.mark.parametrize("lo,hi", [(120, 134), (107, 147), (30, 220)])
+@pytest.mark.parametrize("QN,rows,weights", [(32, 1, True), (4, 9, True), (4, 3, True), (8, 1, True), (4, 3, False),
+                                             (8, 1, False), (32, 1, False), (4, 16, False)])
+def test_every_kernel_with_far_scales(QN, rows, weights, lo, hi):
+    """8 and 16 columns, one row and several, with and without key weights."""
+    p = serving.make_mx(B=2, QN=QN, KVN=2, q_lens=[rows] * 2, kv_lens=[1500, 333], block_size=64, seed=52,
+                        mask_mode=3, poison=False)
+    p.v_scale = _spread(p, lo, hi, 53)
+    _check(p, weights=weights, num_sms=NO_CLUSTER)
