@@ -292,8 +292,8 @@ class KvCache:
     with an int32 block table [B, max pages], or contiguous tensors [B, S, KV
     heads, D]; bf16, or E4M3 codes (uint8 or float8_e4m3fn) with fp32 scales
     [pages or B, KV heads, rows, D/64], or MXFP4: bytes of two E2M1 codes (uint8,
-    D/2 in the place of D) with E8M0 scales (uint8 or float8_e8m0fnu) [pages or B,
-    KV heads, rows, D/32]."""
+    D/2 in the place of D; a tensor of float4_e2m1fn_x2 as .view(torch.uint8)) with E8M0
+    scales (uint8 or float8_e8m0fnu) [pages or B, KV heads, rows, D/32]."""
 
     def __init__(self, k_cache: torch.Tensor, v_cache: torch.Tensor,
                  block_table: Optional[torch.Tensor] = None, *,
@@ -517,7 +517,9 @@ class NormRopeAppendCall:
     and v_new to `slots` (int32 [T]) of the cache.  q, k_new, v_new are bf16 [T, heads,
     D] or [B, S, heads, D], and tokens may be strided (slices of a fused projection).
     Rows with a position below 0 are left out; `status` (int32 [1]) becomes 3 where a
-    slot or a position lies outside.  run() returns q_out."""
+    slot or a position lies outside.  Slots differ from each other.  Weights and positions
+    of a bounded cache are not set: there KvAppendCall takes the new rows.  run() returns
+    q_out."""
 
     def __init__(self, cache: KvCache, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
                  slots: torch.Tensor, positions: torch.Tensor,

@@ -18,7 +18,8 @@
 // pages that go back 10.4).  One CTA, or a cluster of sixteen for many rows (eight took
 // 12.7 us, half of it the rows: few SMs issue their stores), each of which makes the prefix
 // sums of all sequences for itself; past kWhole sequences each makes a slice, and they
-// look into each other's shared memory.
+// look into each other's shared memory.  (Its CTAs start together, on sixteen free SMs of one
+// GPC: beside a kernel on another stream that holds the SMs, the call waits for them.)
 #include <atomic>
 #include <cstring>
 

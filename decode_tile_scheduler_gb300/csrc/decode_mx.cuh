@@ -9,9 +9,10 @@
 //  - Units of 16 columns (NG = 2) where a KV head has more than 8 widen the codes once for
 //    both halves: 32 sequences of 512 to 4096 keys, 16 columns 51.6 us for 58.6, 128 query
 //    heads 49.2 for 58.3; 16 sequences of 2 to 16 k keys with 1 to 4 rows of 4 heads 63.6
-//    for 71.7.  Window calls keep 8: of few tiles a unit, many of them edges, 64 sequences,
-//    window 1024, 1 to 4 rows 54.4 us where 16 columns took 66.1 (window 4096, four rows:
-//    49.6 where 16 take 45.1).
+//    for 71.7 (when it was chosen; the columns' own factors and the windows of V scales
+//    have cost these units 2 to 3 % since).  Window calls keep 8: of few tiles a unit, many
+//    of them edges, 64 sequences, window 1024, 1 to 4 rows 54.4 us where 16 columns took
+//    66.1; long windows lose by it (window 4096, four rows: 49.6 where 16 took 45.1).
 //  - S^T = K Q^T: a warp has 32 of a tile's rows.  O^T = V^T P^T: it has 32 of the 128
 //    elements, the ones under one scale, and all rows; P goes through shared memory, twice
 //    (one barrier a tile).  So O is 8 registers a lane and needs no merge behind a chunk
@@ -26,17 +27,19 @@
 //    fp16 pairs, where a chunk's scales of a group lie within 16 binades.  A group whose
 //    scales do not has its P times scale made of the scores, as two terms in bf16, whose
 //    exponents reach (kFar): a key of little weight, or none, takes no bit from the
-//    others however large its V is.
+//    others however large its V is.  (A batch whose every group is far 139 us for 35.)
+//  - Each column's query is multiplied by a power of two of its own, so that no head or row
+//    meets another's size.
 //
 // Measured (one GB300; the call with plan and combine): 4 sequences of 32 to 128 k keys,
-// 64 / 8 heads (364 MB) 86.5 us, of which this kernel 79; its loads alone 65.6, its work
-// alone 76.8.  32 sequences of 512 to 4096 keys 34.9 us.  A warp issues 520 instructions
-// for 32 rows (128 of them cvt of a byte, 2 clocks each), in 950 clocks of its scheduler:
-// the ALU pipe is 53 % and mma 27 % busy, and these two do not run wholly side by side (4
-// cvt 8.1 clocks, 1 mma 8.1, both together 10.8; with 2 lop3 14.8 where 12 were due).  So
-// more warps do not help: four CTAs to an SM took 87.6 us, stages 2 to 4 the same, five
-// CTAs (72 registers) 105; nor do finer chunks (the end times of CTAs draw together, the
-// mean moves up).
+// 64 / 8 heads (364 MB) 86.0 us, of which this kernel 79; its loads alone 65.6, its work
+// alone 76.8.  32 sequences of 512 to 4096 keys 34.8 us.  A warp issues 518 instructions
+// for 32 rows (139 of them conversions of 2 clocks, of which 128 of a byte of codes), in 950
+// clocks of its scheduler: the ALU pipe is 50 % and mma 26 % busy, and these two do not run
+// wholly side by side (4 cvt 8.1 clocks, 1 mma 8.1, both together 10.8; with 2 lop3 14.8
+// where 12 were due).  So more warps do not help: four CTAs to an SM took 87.6 us, stages
+// 2 to 4 the same, five CTAs (72 registers) 105; nor do finer chunks (the end times of
+// CTAs draw together, the mean moves up).
 #pragma once
 
 namespace fia {

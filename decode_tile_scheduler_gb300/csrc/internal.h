@@ -37,7 +37,8 @@ constexpr int kDecodeMaxRows = 16; // query rows per sequence the decode kernel 
 // units spilled registers; the same, 88.0 against 88.2 us, once the
 // consumers had 208 registers).
 // (MXFP4: 16 for more than 8 columns, whose codes are then widened once, except in a
-// window call; decode_mx.cuh has both sides' times.)
+// window call, which gains by 8 where a unit has few tiles and loses by them where it has
+// many; decode_mx.cuh has both sides' times.)
 inline int decode_group_heads(int rows, int cols, bool mx, bool window) {
   return cols > 8 && (mx ? !window : rows == 1) ? 16 : 8;
 }

@@ -473,8 +473,13 @@ fia_status fia_assign_pages(const fia_pages_params *p, void *stream);
  *    int32 that the caller has cleared) becomes 3.  A slot outside the cache: K and V
  *    are left out, and *status becomes 3.
  *  - q_out may be q itself (of the same token stride); otherwise the outputs share no
- *    memory with the inputs.  Two rows with the same slot leave either's values.
- *  - Nothing else is written.  One launch, no workspace, deterministic. */
+ *    memory with the inputs.  Slots differ: two rows with the same one leave pieces of
+ *    both there, of a quantised row also one's codes under the other's scale.
+ *  - Nothing else is written: not the per-key state of a bounded cache, weights and
+ *    positions, which fia_kv_append sets for its new slots.  A cache with such state takes
+ *    its new rows by fia_kv_append (or its caller sets the state of the new slots), or a
+ *    slot used again goes on with what was counted for the key it held before.
+ *  - One launch, no workspace; deterministic, the slots being different. */
 typedef struct fia_norm_rope_params {
     fia_kv_cache cache;       /* its D is the heads' D; block_table as elsewhere  */
                               /* (non-NULL for a paged cache)                   */
