@@ -275,7 +275,8 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
       }
       float kf[4];
       e8m0x4_to_f32x4(ksw, kf);
-      if (!(lane < kFewKeys && seen(lane))) vsw = win - 0x04040404u;  // (in the windows)
+      const bool counts = lane < kFewKeys && seen(lane);
+      if (!counts) vsw = win - 0x04040404u;            // (in the windows)
       const uint32_t fct = vsw + (0x10101010u - win);  // 2^(1 - d): fp16 exponents 16 - d
       uint32_t h01 = __byte_perm(fct, 0u, 0x4140) << 10, h23 = __byte_perm(fct, 0u, 0x4342) << 10;
       const uint32_t out = n == 0 ? __vsub4(win - 0x04040404u, vsw) & 0xf8f8f8f8u : __vsub4(win, vsw) & 0xf0f0f0f0u;
@@ -285,8 +286,8 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
         for (int j = 0; j < 4; ++j) {
           const uint32_t code = vsw >> (8 * j) & 255u;
           const bool was = far >> (8 * j + 7) & 1u;
-          const uint32_t most = __reduce_max_sync(0xffffffffu, code == 255u ? 0u : code);
-          const uint32_t least = __reduce_min_sync(0xffffffffu, code == 0u ? 255u : code);
+          const uint32_t most = __reduce_max_sync(0xffffffffu, !counts || code == 255u ? 0u : code);
+          const uint32_t least = __reduce_min_sync(0xffffffffu, !counts || code == 0u ? 255u : code);
           const uint32_t top = n == 0 ? scale_window(least, most, kMxWindow) : win >> (8 * j) & 255u;
           const bool is = was || most > top || least + 15 < top;
           const uint32_t now = is ? max(top, most) : top;
@@ -387,13 +388,13 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
     if constexpr (FP8) {
       uint32_t e[2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) e[k] = seen(g + 8 * k) ? exponents2(vsc[k]) : win8 - 0x40004u;
+      for (int k = 0; k < 2; ++k) e[k] = seen(g + 8 * k) ? exponents2(vsc[k]) : win8 - 0x40004u;  // (inside)
       const uint32_t high = n == 0 ? win8 - 0x40004u : win8, out = n == 0 ? 0xfff8fff8u : 0xfff0fff0u;
       if (__any_sync(0xffffffffu, (((high - e[0]) | (high - e[1])) & out) != 0u)) {
         uint32_t next = 0u;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint32_t u = e[0] >> (16 * i) & 0xffu, v = e[1] >> (16 * i) & 0xffu;
+          const uint32_t u = seen(g) ? e[0] >> (16 * i) & 0xffu : 0u, v = seen(g + 8) ? e[1] >> (16 * i) & 0xffu : 0u;
           const uint32_t most = __reduce_max_sync(0xffffffffu, max(u == 255u ? 0u : u, v == 255u ? 0u : v));
           const uint32_t least = __reduce_min_sync(0xffffffffu, min(u == 0u ? 255u : u, v == 0u ? 255u : v));
           const uint32_t top = n == 0 ? scale_window(least, most, kFp8Window) : win8 >> (16 * i) & 0xffu;

@@ -492,10 +492,12 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
         *reinterpret_cast<float4*>(smem + Cfg::kOffKs + (R0 + lane) * 16) = make_float4(kf[0], kf[1], kf[2], kf[3]);
         const uint8_t* sv = stp + Cfg::kOffScale + Cfg::kScaleBytes + vrow * 4 + warp;
         uint32_t c[4] = {sv[0], sv[48], sv[16], sv[32]};  // keys q, 12 + q, 4 + q, 8 + q
-        if (jt + kKvTile > kvl || (X && jt + kKvTile > a.first_tokens))
+        const bool some_gone = jt + kKvTile > kvl || (X && jt + kKvTile > a.first_tokens);
+        const auto key_gone = [&](int k) { return gone(jt + vrow + (k == 0 ? 0 : k == 1 ? 12 : 4 * k - 4)); };
+        if (some_gone)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (gone(jt + vrow + (k == 0 ? 0 : k == 1 ? 12 : 4 * k - 4))) c[k] = (win - 4u) & 0xffffu;
+            if (key_gone(k)) c[k] = (win - 4u) & 0xffffu;
         // factor 2^(1 - d) of a code d below the window's top: fp16 exponent 16 - d
         const uint32_t c01 = c[0] | c[1] << 16, c23 = c[2] | c[3] << 16;
         const uint32_t high = tt == 0 ? win - 0x40004u : win, out = tt == 0 ? 0xfff8fff8u : 0xfff0fff0u;
@@ -504,7 +506,7 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
           uint32_t most = 0u, least = 255u;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (c[k] != 0u && c[k] != 255u) {
+            if (c[k] != 0u && c[k] != 255u && !(some_gone && key_gone(k))) {
               most = max(most, c[k]);
               least = min(least, c[k]);
             }
