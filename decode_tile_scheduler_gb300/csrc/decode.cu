@@ -1581,14 +1581,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!seen0) v0 = make_float2(0.f, 0.f);
         if (!seen1) v1 = make_float2(0.f, 0.f);
         // Warp-wide power-of-two reference per d-tile: 2^(e-127) with e the
-        // largest exponent of a V scale seen so far (positive floats order
+        // largest exponent of a V scale seen so far (magnitudes order
         // like their bit patterns, so one warp max over the bits finds it).
         // P^T * scale * 2^6 / ref then stays below 2^15 in fp16, and moving the
         // reference rescales the accumulators by an exact power of two.
         float ratio[2], iv[2];
 #pragma unroll
         for (int t2 = 0; t2 < 2; ++t2) {
-          const uint32_t b0 = __float_as_uint(t2 ? v0.y : v0.x), b1 = __float_as_uint(t2 ? v1.y : v1.x);
+          const uint32_t b0 = __float_as_uint(fabsf(t2 ? v0.y : v0.x));
+          const uint32_t b1 = __float_as_uint(fabsf(t2 ? v1.y : v1.x));
           // (infinite or NaN ones are no reference for the rows that see none)
           const uint32_t most =
               __reduce_max_sync(0xffffffffu, max(b0 < 0x7f800000u ? b0 : 0u, b1 < 0x7f800000u ? b1 : 0u));

@@ -162,3 +162,14 @@ def test_rows_that_do_not_see_an_infinite_scale(QN, kw, num_sms, value):
     assert not torch.isfinite(got[3]).any()
     to = 1.01 * bounded.HALF_BF16 * (mag + o.abs()) + 2 * (bounded.lse_tolerance(p, A, 700) + bounded.HALF_FP16) * mag
     assert torch.all(((got - o).abs() <= to)[:3] | torch.isnan(got[:3]))
+
+
+@pytest.mark.parametrize("num_sms", [0, 1, NO_CLUSTER])
+@pytest.mark.parametrize("QN,rows,kw", [(8, 1, {}), (32, 1, {}), (4, 3, {}), (4, 3, FEW)])
+def test_scales_of_either_sign(QN, rows, kw, num_sms):
+    """A value is its code times its scale, whatever the scale's sign."""
+    p = _problem(**{**dict(B=2, QN=QN, KVN=2, q_lens=[rows] * 2, kv_lens=[900, 333], seed=51, mask_mode=3), **kw})
+    g = torch.Generator().manual_seed(52)
+    for s in (p.k_scale, p.v_scale):
+        s *= torch.where(torch.rand(s.shape, generator=g) < 0.5, -1.0, 1.0)
+    _check(p, num_sms=num_sms)
