@@ -52,14 +52,16 @@ __global__ void __launch_bounds__(256) lse_combine_kernel(const CombineArgs a) {
     // the total: largest finite lse, then the sum of e^{lse_k - max}
     float lk[FIA_COMBINE_MAX_PARTS];
     float M = -INFINITY;
+    bool nan = false;  // (a part whose row is NaN: so is the total)
 #pragma unroll
     for (int k = 0; k < FIA_COMBINE_MAX_PARTS; ++k) {
       lk[k] = k < a.n ? __ldg(a.l[k] + li) : INFINITY;
       if (lk[k] != INFINITY) M = fmaxf(M, lk[k]);
+      nan |= lk[k] != lk[k];
     }
     // a sink is one more logit with no value, counted once when some part
     // saw a key (a row that sees no key stays 0 / +inf, with a sink too)
-    const bool any = M != -INFINITY;
+    const bool any = M != -INFINITY || nan;
     const float sk = (a.sinks && any) ? __ldg(a.sinks + h) : -INFINITY;
     const float Mx = fmaxf(M, sk);
     float S = 0.f;
@@ -69,7 +71,7 @@ __global__ void __launch_bounds__(256) lse_combine_kernel(const CombineArgs a) {
         if (lk[k] != INFINITY) S += expf(lk[k] - Mx);
       if (sk != -INFINITY) S += expf(sk - Mx);
     }
-    const bool empty = !any || !(S > 0.f);
+    const bool empty = !any || S <= 0.f;
     const float L = empty ? INFINITY : Mx + logf(S);
     uint16_t* orow = a.out + r * a.D;
     for (int d0 = 8 * lane; d0 < a.D; d0 += 256) {

@@ -86,3 +86,27 @@ def test_prompts(fmt):
         p.q[b, 29, 1, 9] = float("nan")
         bad[b, 29, 1] = n > 0
     _check(_out(p, 0), clean, bad)
+
+
+@pytest.mark.parametrize("sinks", [False, True])
+@pytest.mark.parametrize("parts", [[1], [0, 1, 2], [2]])
+def test_a_part_that_is_nan(parts, sinks):
+    """Rows of which some parts are NaN, or all, and rows that no part sees."""
+    T, N, D, n = 5, 3, 128, 3
+    g = torch.Generator().manual_seed(72)
+    outs = [torch.randn(T, N, D, generator=g).to(torch.bfloat16).to(DEV) for _ in range(n)]
+    lses = [torch.randn(T, N, 1, generator=g).to(DEV) for _ in range(n)]
+    for l in lses:
+        l[4] = float("inf")
+    kw = dict(layout=fi.LAYOUT_TND, num_heads=N, total_q=T,
+              sinks=torch.randn(N, generator=g).to(DEV) if sinks else None)
+    clean = [x.clone() for x in fia.lse_combine(outs, lses, **kw)]
+    for k in parts:
+        outs[k][2, 1] = float("nan")
+        lses[k][2, 1] = float("nan")
+    out, lse = fia.lse_combine(outs, lses, **kw)
+    bad = torch.zeros(T, N, dtype=torch.bool, device=DEV)
+    bad[2, 1] = True
+    assert torch.equal(torch.isnan(out), bad[..., None].expand(out.shape)) and torch.equal(torch.isnan(lse)[..., 0], bad)
+    assert torch.equal(out[~bad], clean[0][~bad]) and torch.equal(lse[~bad], clean[1][~bad])
+    assert torch.all(out[4] == 0) and torch.all(lse[4] == float("inf"))
