@@ -71,8 +71,8 @@ struct MxCfg {
   static constexpr int kOffBar = kOffRed + 2 * kWarps * 8 * NG * 4;
   static constexpr int kOffMsg = (kOffBar + 8 * (2 * kStages + 2) + 15) / 16 * 16;
   static constexpr int kOffMisc = kOffMsg + 128;
-  static constexpr int kOffGroups = kOffMisc + 16;            // the far groups' references
-  static constexpr int kOffFactors = kOffGroups + 4 * kWarps;  // NG 2: the columns' score factors
+  static constexpr int kOffGroups = kOffMisc + 16;            // the far groups' references, twice
+  static constexpr int kOffFactors = kOffGroups + 8 * kWarps;  // NG 2: the columns' score factors
   static constexpr int kSmem = kOffFactors + (NG == 2 ? 64 : 0) + 512;  // + alignment slack (a swizzle's 512 bytes)
   static_assert(kStageBytes % 512 == 0, "alignment");
   static_assert(kCtas * (kSmem + 1024) <= 233472, "shared memory");
@@ -447,9 +447,10 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
     for (int n = 0; n < NG; ++n)
 #pragma unroll
       for (int i = 0; i < 2; ++i) acc[n][i][0] = acc[n][i][1] = acc[n][i][2] = acc[n][i][3] = 0.f;
-    // Softmax references m_r, the warps' own copies of one (-inf: none yet; mu is 0 then), lazy: a score may pass its
-    // column's by kOver.  They are kept kLift below the scores that set them, so that P,
-    // at most 2^kOver, has fp16's bits down to 2^-(14 + kLift) of the largest.
+    // Softmax references m_r, the warps' own copies of one (-inf: none yet; mu is 0 then),
+    // lazy: a score may pass its column's by kOver.  They are kept kLift below the scores that
+    // set them, so that P, at most 2^kOver, has fp16's bits down to 2^-(14 + kLift) of the
+    // largest.
     constexpr float kLift = 8.f, kOver = 14.f;
     float m_r[NG][2], mu[NG][2], l_r[NG][2];
 #pragma unroll
@@ -468,7 +469,9 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
     // chunk: O is then over 2^(win - 127 - kFar), win the largest code so far.  Both halves
     // of `win` hold the code; far: the upper one 0xffff.
     uint32_t win = kMxWindow * 0x10001u;
-    if (lane == 0) reinterpret_cast<int*>(smem + Cfg::kOffGroups)[warp] = 0;
+    // The far groups' references, 0 where a group is not far: a copy for a tile and one for the
+    // next, whose warps may write theirs while others still go by this tile's.
+    if (lane < 2) reinterpret_cast<int*>(smem + Cfg::kOffGroups)[W * lane + warp] = 0;
     // Keys that count as zeros in O whatever they hold: past kv_len, and between a band's
     // first tokens and its window.  (Codes are numbers all: a scale of 0 is enough.)
     const auto gone = [&](int j) {
@@ -524,7 +527,7 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
               for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[n][i][k] = acc[n][i][k] * f0 * f1;
-            if (lane == 0) reinterpret_cast<int*>(smem + Cfg::kOffGroups)[warp] = (int)now;
+            if (lane == 0) reinterpret_cast<int*>(smem + Cfg::kOffGroups)[W * (it & 1) + warp] = (int)now;
           }
           win = now | (far ? 0xffffu : now) << 16;
           uint32_t h[4];  // (far: O's products are made apart)
@@ -671,7 +674,7 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
       bool any_far = false;
       // (the other copy of P has been read by all when they are here)
       if (named_bar_or(1, 32 * W, over || win >> 31)) {  // new references, and P again; far groups
-        const int4 far = *reinterpret_cast<const int4*>(smem + Cfg::kOffGroups);
+        const int4 far = reinterpret_cast<const int4*>(smem + Cfg::kOffGroups)[it & 1];
 #pragma unroll
         for (int n = 0; n < NG; ++n)
 #pragma unroll
@@ -747,7 +750,8 @@ __global__ void __launch_bounds__(MxCfg<MR, NG>::kThreads, MxCfg<MR, NG>::kCtas)
         uint4* pf = reinterpret_cast<uint4*>(smem + Cfg::kOffP) + (~it & 1) * (NG * 32 * W);
 #pragma unroll 1
         for (int term = 0; term < 2 * W; ++term) {
-          const int j = term >> 1, ref = reinterpret_cast<const volatile int*>(smem + Cfg::kOffGroups)[j];
+          const int j = term >> 1;
+          const int ref = reinterpret_cast<const int*>(smem + Cfg::kOffGroups)[W * (it & 1) + j];
           if (ref == 0) continue;
           const uint8_t* sv = stp + Cfg::kOffScale + Cfg::kScaleBytes + R0 * 4 + j;
 #pragma unroll
