@@ -175,7 +175,8 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
   __syncthreads();
 
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  // FP8: the windows of the halves' V scales as in decode_kernel; O over 2^(top - 140)
+  // FP8: the windows of the halves' V scales, 16 bits apart (0x8000 beside: far); O over
+  // 2^(top - 140), far over 2^(top - 127 - kFar)
   uint32_t win8 = kFp8Window * 0x10001u;
   float O[NV][4][4];
 #pragma unroll
@@ -383,7 +384,7 @@ __global__ void __cluster_dims__(kFewCtas, 1, 1) __launch_bounds__(kFewThreads, 
 
     // ---- softmax: this warp's running maximum and sum ----
     // FP8: P times its V scale is multiplied in fp16 (the codes are fp16 values, and
-    // bf16 would drop three bits of P), as in decode_kernel.
+    // bf16 would drop three bits of P) over the top of a window of scales, or in two terms.
     float over[2];
     if constexpr (FP8) {
       uint32_t e[2];

@@ -10,7 +10,7 @@
 //    both halves: 32 sequences of 512 to 4096 keys, 16 columns 51.6 us for 58.6, 128 query
 //    heads 49.2 for 58.3; 16 sequences of 2 to 16 k keys with 1 to 4 rows of 4 heads 63.6
 //    for 71.7 (when it was chosen; the columns' own factors and the windows of V scales
-//    have cost these units 2 to 3 % since).  Window calls keep 8: of few tiles a unit, many
+//    have cost these units 3 to 5 % since).  Window calls keep 8: of few tiles a unit, many
 //    of them edges, 64 sequences, window 1024, 1 to 4 rows 54.4 us where 16 columns took
 //    66.1; long windows lose by it (window 4096, four rows: 49.6 where 16 took 45.1).
 //  - S^T = K Q^T: a warp has 32 of a tile's rows.  O^T = V^T P^T: it has 32 of the 128
