@@ -28,11 +28,12 @@
 //
 // MXFP4 caches take one pass (mx_dequant_kernel): an E2M1 code times its E8M0 scale
 // is a bf16 value as it is, so the copies are exact and the prompt runs as over a
-// bf16 cache.
+// bf16 cache.  (Products past bf16's largest number, scales of 2^126 and 2^127, count as it.)
 #include <algorithm>
 
 #include "common.cuh"
 #include "internal.h"
+#include "kv_quant.cuh"
 
 namespace fia {
 
@@ -214,8 +215,11 @@ __global__ void __launch_bounds__(256, 6) mx_dequant_kernel(const DequantArgs a,
         e2m1x8_to_f16x2x4(code[kv][u], p[0], p[1], p[2], p[3]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[k]));
-          o[k] = pack_bf16(f.x * sc, f.y * sc);
+          float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[k]));
+          f = make_float2(f.x * sc, f.y * sc);
+          if (e - 253u < 2u)  // past bf16's numbers: its largest (a row that does not see the key: 0 * inf)
+            f = make_float2(fminf(fmaxf(f.x, -kBf16Max), kBf16Max), fminf(fmaxf(f.y, -kBf16Max), kBf16Max));
+          o[k] = pack_bf16(f.x, f.y);
         }
         *reinterpret_cast<uint4*>((kv ? a.v_out : a.k_out) + to[u]) = make_uint4(o[0], o[1], o[2], o[3]);
       }

@@ -63,7 +63,8 @@
  *    head, down to 2^-14;
  *  - MXFP4 KV: E2M1 codes (sign, two exponent bits, one of mantissa: 0, 0.5, 1,
  *    1.5, 2, 3, 4, 6) with one E8M0 scale byte s per 32 consecutive elements of
- *    D, value = code * 2^(s - 127); s = 255 makes the 32 values NaN.
+ *    D, value = code * 2^(s - 127); s = 255 makes the 32 values NaN.  (Prompts take
+ *    values past bf16's largest number as that number.)
  */
 #ifndef FIA_H_
 #define FIA_H_

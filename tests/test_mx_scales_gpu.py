@@ -154,3 +154,27 @@ def test_every_kernel_with_far_scales(QN, rows, weights, lo, hi):
                         mask_mode=3, poison=False)
     p.v_scale = _spread(p, lo, hi, 53)
     _check(p, weights=weights, num_sms=NO_CLUSTER)
+
+
+@pytest.mark.parametrize("code", [252, 253, 254])
+@pytest.mark.parametrize("rows,num_sms", [(40, 0), (3, 0), (3, NO_CLUSTER)])
+@pytest.mark.parametrize("name", ["k_scale", "v_scale"])
+def test_the_largest_scales_reach_their_rows_alone(name, rows, num_sms, code):
+    """The newest key's values lie at bf16's end and past it: the rows that do not see it keep
+    their bits."""
+    p = serving.make_mx(B=1, QN=4, KVN=2, q_lens=[rows], kv_lens=[300], block_size=32, seed=54, mask_mode=3,
+                        poison=False)
+    clean = [x.cpu().clone() for x in _run(p, num_sms=num_sms)]
+    page, row = _at(p, 299)
+    getattr(p, name)[page, :, row] = code
+    got = [x.cpu() for x in _run(p, num_sms=num_sms)]
+    before = slice(0, rows - 1)
+    assert torch.isfinite(got[0][:, before]).all()
+    if rows > 16:
+        assert torch.equal(got[0][:, before], clean[0][:, before])
+    else:  # (a far group's products are made in other roundings)
+        o, _, _, mag, A = bounded.attention(serving.decoded(p))[0]
+        tl = bounded.lse_tolerance(p, min(A, 100.0), 300)
+        to = 1.01 * bounded.HALF_BF16 * (mag + o.abs()) + 2 * tl * mag
+        assert torch.all(((got[0][0].double() - o).abs() <= to)[before])
+    assert torch.equal(got[1][:, :, before], clean[1][:, :, before])
